@@ -314,6 +314,178 @@ la_status la_forward_delta(const void *q, const void *k, const void *v, void *ou
                            const float *beta, const float *alpha, float *S, int B,
                            int H, int N, int d, la_dtype dtype, la_stream_t stream);
 
+/*
+ * Strides in elements of a [B][H][N][d] tensor whose last dimension is
+ * contiguous.  Every row starts at data + i_b*b + i_h*h + i_n*n.  A
+ * dimension of an input may have stride 0 (a broadcast input); the rows of a
+ * written tensor may not overlap.
+ */
+typedef struct {
+    long long b, h, n;
+} la_strides;
+
+/*
+ * The position rotation of la_qk_norm_rope.  Pair i < rotary_dim / 2 of a
+ * row at position p is turned by the angle p * frequencies[i] (radians).
+ */
+typedef struct {
+    const double *frequencies; /* HOST array of rotary_dim / 2 values in
+                                  [-1e9, 1e9], read during the call         */
+    int rotary_dim;            /* even, 0..d; 0: no rotation                 */
+    int interleaved;           /* 0: pair i is (x[i], x[i + rotary_dim / 2]);
+                                  1: pair i is (x[2i], x[2i + 1])            */
+    const void *positions;     /* DEVICE integers, one per batch entry and
+                                  token, or NULL: token n is at position n   */
+    int position_bytes;        /* 4 or 8 (signed); ignored without positions */
+    long long position_stride_b, position_stride_n; /* in elements, >= 0     */
+    long long offset;          /* added to every position                    */
+} la_rope;
+
+/*
+ * la_qk_norm_rope -- queries and keys as the forward and decode entry points
+ * take them, out of a projection's output, in one pass: each row (one token
+ * of one head, d values) is divided by its root mean square, scaled by a
+ * weight per feature and rotated by its position,
+ *   n = x / sqrt(mean(x^2) + eps),  u = w (.) n,
+ *   (y1, y2) = (u1 cos t - u2 sin t, u2 cos t + u1 sin t)  for each pair,
+ * features from rotary_dim on pass without rotation.  The pages normalise k
+ * for the delta rule and rotate q and k in retention models without giving
+ * the formulas; these are the usual ones.  With the identity feature map and
+ * no normaliser, <y_q, y_k> then depends on positions by their difference.
+ *
+ *   q, k       [B][Hq][N][d] and [B][Hk][N][d] device, dtype `dtype`, read only.
+ *   q_out, k_out   like q and k, written; may be q and k themselves with the
+ *              same strides, otherwise may not alias an input or each other.
+ *   strides    4 strides, of q, k, q_out, k_out, or NULL: all contiguous
+ *              [B][H][N][d].  A token-major projection [B][N][H*d] is
+ *              {N*H*d, d, H*d}: the call then turns the layout as well.
+ *   q_weight, k_weight   [d] device, dtype `weight_dtype`, or NULL for ones.
+ *   norm       1, or 0: no normalisation (u = x; the weights must be NULL).
+ *   eps        > 0 and finite (ignored without norm).
+ *   rope       the rotation, or NULL for none.
+ *   B, N, Hq, Hk >= 0 (Hq == 0 or Hk == 0 leaves that side out; its pointers
+ *              may be NULL), d in 1..LA_MAX_D.
+ * A decode step is N == 1 with one position per sequence.  Sums of squares
+ * are fp32; the angle is exact in the position (64-bit fixed-point turns), so
+ * far positions lose nothing.  One kernel, no workspace.
+ */
+la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                          const la_strides *strides, const void *q_weight,
+                          const void *k_weight, int norm, float eps,
+                          const la_rope *rope, int B, int Hq, int Hk, int N, int d,
+                          la_dtype dtype, la_dtype weight_dtype, la_stream_t stream);
+
+/*
+ * la_backward_qk_norm_rope -- gradients of la_qk_norm_rope: with g the
+ * gradient of a row's output turned back by its angle,
+ *   dw = sum over rows of g (.) n,
+ *   dx = (w (.) g - n mean(n (.) w (.) g)) / sqrt(mean(x^2) + eps).
+ *   dq_out, dk_out   gradients of the outputs, like q and k, read only.
+ *   q, k       the forward's inputs (may be NULL with norm == 0, whose
+ *              gradient does not need them).
+ *   dq, dk     gradients of the inputs, written; may be dq_out and dk_out
+ *              themselves with the same strides, otherwise no aliasing.
+ *   dq_weight, dk_weight   [d] fp32 device, written, or NULL: not computed.
+ *              Summed in a fixed order: repeated calls are bit-identical.
+ *   strides    6 strides, of dq_out, dk_out, q, k, dq, dk, or NULL: contiguous.
+ * Other arguments as la_qk_norm_rope (the same values as in the forward).
+ * B*N == 0 writes zero weight gradients.  With a weight gradient the call
+ * takes a stream-ordered workspace (LA_ERR_NO_MEMORY if that fails).
+ */
+la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const void *q,
+                                   const void *k, void *dq, void *dk, float *dq_weight,
+                                   float *dk_weight, const la_strides *strides,
+                                   const void *q_weight, const void *k_weight, int norm,
+                                   float eps, const la_rope *rope, int B, int Hq, int Hk,
+                                   int N, int d, la_dtype dtype, la_dtype weight_dtype,
+                                   la_stream_t stream);
+
+/* What a gate tensor of the per-channel recurrence holds: the gate a itself,
+ * its logarithm (a = exp(g)) or its logit (a = 1 / (1 + exp(-g))). */
+typedef enum { LA_GATE_VALUE = 0, LA_GATE_LOG = 1, LA_GATE_LOGIT = 2 } la_gate;
+
+/* Strides in elements of a [B][N][C] tensor whose last dimension is
+ * contiguous; a dimension of an input may have stride 0. */
+typedef struct {
+    long long b, n;
+} la_seq_strides;
+
+/*
+ * la_forward_recurrence -- the gated linear recurrence with a gate per
+ * channel ("Linear Attention", GLA's S_t = G_t (.) S_{t-1} + ..., on a vector
+ * state; the z_t of the running statistics under vector gates):
+ *   h_t = a_t (.) h_{t-1} + x_t                 (complement == 0)
+ *   h_t = a_t (.) h_{t-1} + (1 - a_t) (.) x_t   (complement == 1)
+ * for t = 1..N, with out_t = h_t.
+ *   x          [B][N][C] device, dtype `dtype`, read only.
+ *   gates      [B][N][C] device, dtype `gate_dtype` (LA_F32, or `dtype`),
+ *              holding a_t as `gate` says.  Not checked; values outside
+ *              [0, 1] (positive logarithms) follow the formula while the
+ *              products of gates stay finite.  A gate of 0 (logarithm or
+ *              logit -inf) starts a new sequence; a gate of 1 (0, +inf) with
+ *              x = 0, or with complement any finite x, keeps the state.
+ *   h0         [B][C] fp32 device, the state before the first token, or NULL
+ *              for zero.
+ *   out        [B][N][C] device, dtype `dtype`, written; may be x itself with
+ *              the same strides, otherwise no aliasing.
+ *   h_last     [B][C] fp32 device, written with the state after the last
+ *              token (unrounded), or NULL; may be h0 itself.
+ *   strides    3 strides, of x, gates, out, or NULL: contiguous.
+ *   B, N, C >= 0 (B*C == 0 is a no-op; N == 0 copies h0 to h_last).
+ * States and gate products are fp32.  Sequences are cut along N (the pieces
+ * are joined in a fixed order: repeated calls are bit-identical).
+ * A non-finite value stays within its sequence and channel.
+ */
+la_status la_forward_recurrence(const void *x, const void *gates, const float *h0,
+                                void *out, float *h_last, const la_seq_strides *strides,
+                                int B, int N, int C, la_gate gate, int complement,
+                                la_dtype dtype, la_dtype gate_dtype, la_stream_t stream);
+
+/*
+ * la_backward_recurrence -- gradients of la_forward_recurrence.  With c_t the
+ * factor of x_t (1, or 1 - a_t) and, from the last token backwards,
+ *   g_t = dout_t + a_{t+1} (.) g_{t+1}   (g_N = dout_N + dh_last),
+ *   dx_t = c_t (.) g_t,   dh0 = a_1 (.) g_1,
+ *   dgates_t = s_t (.) g_t (.) (h_{t-1} - x_t [complement]),
+ * s_t = 1, a_t or a_t (1 - a_t) for a gate given as value, logarithm, logit.
+ *   dout       [B][N][C] device, dtype `dtype`: the gradient of out.
+ *   gates, h0  as in the forward.
+ *   out        [B][N][C] device, dtype `dtype`: what the forward wrote (the
+ *              states h_t, rounded to dtype, that dgates reads).
+ *   x          the forward's input; needed with complement only, else NULL.
+ *   dh_last    [B][C] fp32 device: gradient of h_last, or NULL for zero.
+ *   dx         [B][N][C] device, dtype `dtype`, written; may be dout itself
+ *              with the same strides.
+ *   dgates     [B][N][C] device, dtype `gate_dtype`, written: the gradient of
+ *              the gate tensor as given (value, logarithm or logit).
+ *   dh0        [B][C] fp32 device, written, or NULL; may be dh_last itself.
+ *   strides    6 strides, of dout, gates, out, x, dx, dgates, or NULL:
+ *              contiguous.
+ * Other arguments as la_forward_recurrence.  N == 0 copies dh_last to dh0.
+ */
+la_status la_backward_recurrence(const void *dout, const void *gates, const void *out,
+                                 const void *x, const float *h0, const float *dh_last,
+                                 void *dx, void *dgates, float *dh0,
+                                 const la_seq_strides *strides, int B, int N, int C,
+                                 la_gate gate, int complement, la_dtype dtype,
+                                 la_dtype gate_dtype, la_stream_t stream);
+
+/*
+ * la_decode_step_recurrence -- one token of la_forward_recurrence.
+ *   h          [B][C] fp32 device, the state, read.
+ *   h_out      [B][C] fp32 device, the new state, written; h itself for an
+ *              update in place.
+ *   x, gates   [B][C] device; out [B][C] device, dtype `dtype`, written (h_out
+ *              rounded); may be x itself with the same stride.
+ *   strides    3 strides between batch entries, of x, gates, out, or NULL: C.
+ * Other arguments as la_forward_recurrence.
+ */
+la_status la_decode_step_recurrence(const float *h, float *h_out, const void *x,
+                                    const void *gates, void *out, const long long *strides,
+                                    int B, int C, la_gate gate, int complement,
+                                    la_dtype dtype, la_dtype gate_dtype,
+                                    la_stream_t stream);
+
 /* Size of the fixed device scratch used by la_forward_causal_noalloc. */
 #define LA_NOALLOC_SCRATCH_BYTES (16u << 20)
 

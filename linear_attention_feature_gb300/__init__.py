@@ -9,6 +9,7 @@ on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -18,6 +19,8 @@ __all__ = ["forward", "forward_variant", "forward_gated", "decode_step_gated",
            "decode_step_delta",
            "forward_causal_state", "forward_host",
            "host_workspace_bytes", "decode_step",
+           "rope_frequencies", "qk_norm_rope", "backward_qk_norm_rope",
+           "forward_recurrence", "backward_recurrence", "decode_step_recurrence",
            "check_device_status",
            "kernel_launch_count", "LinAttnError",
            "load_library", "LA_F32", "LA_BF16", "STATUS", "EXPORTED"]
@@ -34,13 +37,24 @@ EXPORTED = ("la_forward", "la_forward_ex", "la_decode_step",
             "la_forward_host_workspace_bytes", "la_forward_causal_state",
             "la_decode_step_ex", "la_forward_variant", "la_decode_step_variant",
             "la_forward_gated", "la_decode_step_gated", "la_decode_step_delta",
-            "la_debug_inject_timeout", "la_debug_fail_next_allocs", "la_forward_delta")
+            "la_debug_inject_timeout", "la_debug_fail_next_allocs", "la_forward_delta",
+            "la_qk_norm_rope", "la_backward_qk_norm_rope", "la_forward_recurrence",
+            "la_backward_recurrence", "la_decode_step_recurrence")
 
 FEATURE_MAPS = {"elu1": 0, "identity": 1}
+GATES = {"value": 0, "log": 1, "logit": 2}
 
 
 class _Variant(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("normalise", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("frequencies", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("position_bytes", ctypes.c_int),
+                ("position_stride_b", ctypes.c_longlong),
+                ("position_stride_n", ctypes.c_longlong), ("offset", ctypes.c_longlong)]
 
 
 def _variant(feature_map, normalise):
@@ -85,6 +99,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.la_forward_host_workspace_bytes.argtypes = [I, I, I, I, I]
     lib.la_forward_host_workspace_bytes.restype = ctypes.c_size_t
     lib.la_forward_delta.argtypes = [V, V, V, V, V, V, V, I, I, I, I, I, V]
+    lib.la_qk_norm_rope.argtypes = [V, V, V, V, V, V, V, I, ctypes.c_float, V,
+                                    I, I, I, I, I, I, I, V]
+    lib.la_backward_qk_norm_rope.argtypes = [V, V, V, V, V, V, V, V, V, V, V, I,
+                                             ctypes.c_float, V, I, I, I, I, I, I, I, V]
+    lib.la_forward_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, I, V]
+    lib.la_backward_recurrence.argtypes = [V, V, V, V, V, V, V, V, V, V,
+                                           I, I, I, I, I, I, I, V]
+    lib.la_decode_step_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, V]
     lib.la_debug_inject_timeout.argtypes = [ctypes.c_longlong, I]
     lib.la_debug_fail_next_allocs.argtypes = [I]
     lib.la_check_device_status.argtypes = [V]
@@ -100,7 +122,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
               "la_forward_variant", "la_decode_step_variant",
               "la_forward_gated", "la_decode_step_gated", "la_decode_step_delta",
               "la_debug_inject_timeout", "la_debug_fail_next_allocs",
-              "la_forward_delta", "la_check_device_status", "la_abi_version"):
+              "la_forward_delta", "la_check_device_status", "la_abi_version",
+              "la_qk_norm_rope", "la_backward_qk_norm_rope", "la_forward_recurrence",
+              "la_backward_recurrence", "la_decode_step_recurrence"):
         getattr(lib, n).restype = I
     if path is None:
         _lib = lib
@@ -139,6 +163,11 @@ def _stream_ptr(stream, device):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(device):
+    """`device` as the current CUDA device while the library is called."""
+    return _torch().cuda.device(device)
 
 
 def _decay_arg(decay, H):
@@ -383,6 +412,328 @@ def decode_step(S, z, q, k, v, out=None, *, decay=None, feature_map="elu1",
             ctypes.c_void_p(v.data_ptr()), ctypes.c_void_p(out.data_ptr()),
             B, H, d, _decay_arg(decay, H), _dtype_code(q),
             _variant(feature_map, normalise), _stream_ptr(stream, q.device))
+    _raise_if(st)
+    return out
+
+
+# ------------------------------------------------------------------ queries
+# and keys out of a projection
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0):
+    """The usual rotation frequencies base^(-2i / rotary_dim), i < rotary_dim
+    / 2, in radians per position, as qk_norm_rope takes them."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    return array.array("d", [float(base) ** (-2.0 * i / rotary_dim)
+                             for i in range(rotary_dim // 2)])
+
+
+def _rope(frequencies, positions, offset, interleaved, q):
+    """The rotation's descriptor and what has to outlive the call."""
+    if frequencies is None or len(frequencies) == 0:
+        return None, None
+    f = frequencies
+    if not (isinstance(f, array.array) and f.typecode == "d"):
+        f = array.array("d", [float(x) for x in f])
+    r = _Rope(f.buffer_info()[0], 2 * len(f), int(bool(interleaved)), None, 0, 0, 0, int(offset))
+    if positions is not None:
+        torch = _torch()
+        shape = (q.shape[0],) if q.dim() == 3 else (q.shape[0], q.shape[2])
+        if tuple(positions.shape) != shape and tuple(positions.shape) != shape[1:]:
+            raise ValueError(f"positions must have the shape {list(shape)}"
+                             + (f" or {list(shape[1:])}" if q.dim() == 4 else ""))
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be int32 or int64")
+        if positions.device != q.device:
+            raise ValueError("positions must be on q's CUDA device")
+        st = positions.stride()
+        r.positions = positions.data_ptr()
+        r.position_bytes = positions.element_size()
+        if q.dim() == 3:
+            r.position_stride_b = st[0]
+        else:
+            r.position_stride_b = st[0] if positions.dim() == 2 else 0
+            r.position_stride_n = st[-1]
+    return r, f
+
+
+def _check_rows(like, *ts):
+    """Tensors of rows: `like`'s dtype and device, the last dimension contiguous."""
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on a CUDA device")
+        if t.device != like.device:
+            raise ValueError("all tensors must be on one CUDA device")
+        if t.dtype != like.dtype:
+            raise TypeError("q, k, their outputs and gradients must share one dtype")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
+
+
+def _row_strides(*ts):
+    """la_strides of [B, H, N, d] or [B, H, d] tensors (None: zeros)."""
+    v = []
+    for t in ts:
+        if t is None:
+            v += (0, 0, 0)
+            continue
+        s = t.stride()
+        v += (s[0], s[1], s[2] if len(s) == 4 else 0)
+    return (ctypes.c_longlong * len(v))(*v)
+
+
+def _weight(w, d, like):
+    """(pointer or None, its dtype code) of a [d] weight."""
+    if w is None:
+        return None, LA_F32
+    if tuple(w.shape) != (d,):
+        raise ValueError(f"a weight must have the shape [{d}]")
+    if w.device != like.device:
+        raise ValueError("the weights must be on q's CUDA device")
+    if not w.is_contiguous():
+        raise ValueError("a weight must be contiguous")
+    return w.data_ptr(), _dtype_code(w)
+
+
+def _weights(q_weight, k_weight, d, like):
+    wq, cq = _weight(q_weight, d, like)
+    wk, ck = _weight(k_weight, d, like)
+    if wq is not None and wk is not None and cq != ck:
+        raise TypeError("q_weight and k_weight must share one dtype")
+    return wq, wk, cq if wq is not None else ck
+
+
+def _check_qk(q, k):
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
+    if k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:]:
+        raise ValueError("q and k may differ in the number of heads only")
+
+
+def _head_major(t):
+    torch = _torch()
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions=None, *,
+                 offset: int = 0, norm: bool = True, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Queries and keys as forward() and decode_step() take them, in one pass:
+    RMS norm over each head's d values, times a weight per feature, then the
+    position rotation.  q [B, Hq, N, d] and k [B, Hk, N, d] (or [B, H, d]: one
+    token each) may have any strides with a contiguous last dimension, such as
+    views of a fused projection; the results are contiguous unless q_out and
+    k_out say otherwise (q_out=q, k_out=k: in place).
+
+    q_weight, k_weight [d]: float32 or q's dtype, or None.  frequencies:
+    radians per position of each pair (rope_frequencies()), None for no
+    rotation; features beyond 2 len(frequencies) are not rotated.  positions:
+    int32 or int64 [B, N] or [N] ([B] for one token), or None for 0..N-1;
+    `offset` is added.  interleaved: pairs (2i, 2i+1) instead of (i, i + R/2).
+    Returns (q_out, k_out)."""
+    _check_qk(q, k)
+    if q_out is None:
+        q_out = _head_major(q)
+    if k_out is None:
+        k_out = _head_major(k)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    _check_rows(q, q, k, q_out, k_out)
+    d = q.shape[-1]
+    wq, wk, wcode = _weights(q_weight, k_weight, d, q)
+    rope, keep = _rope(frequencies, positions, offset, interleaved, q)
+    N = q.shape[2] if q.dim() == 4 else 1
+    lib = load_library()
+    with _on(q.device):
+        st = lib.la_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+            _row_strides(q, k, q_out, k_out), wq, wk, int(bool(norm)), float(eps),
+            ctypes.byref(rope) if rope is not None else None, q.shape[0], q.shape[1],
+            k.shape[1], N, d, _dtype_code(q), wcode, _stream_ptr(stream, q.device))
+    _raise_if(st)
+    return q_out, k_out
+
+
+def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
+                          frequencies=None, positions=None, *, offset: int = 0,
+                          norm: bool = True, eps: float = 1e-6, interleaved: bool = False,
+                          dq=None, dk=None, stream=None):
+    """Gradients of qk_norm_rope (same arguments as the forward call): returns
+    (dq, dk, dq_weight, dk_weight), the weights' in float32 and None where
+    there is no weight.  dq and dk take any strides, such as views of a fused
+    projection's gradient (default: laid out like q and k)."""
+    torch = _torch()
+    _check_qk(q, k)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError("dq_out and dk_out must have the shapes of q and k")
+    if dq is None:
+        dq = torch.empty_like(q)
+    if dk is None:
+        dk = torch.empty_like(k)
+    if dq.shape != q.shape or dk.shape != k.shape:
+        raise ValueError("dq and dk must have the shapes of q and k")
+    _check_rows(q, dq_out, dk_out, q, k, dq, dk)
+    d = q.shape[-1]
+    wq, wk, wcode = _weights(q_weight, k_weight, d, q)
+    dwq = torch.empty(d, dtype=torch.float32, device=q.device) if wq is not None else None
+    dwk = torch.empty(d, dtype=torch.float32, device=q.device) if wk is not None else None
+    rope, keep = _rope(frequencies, positions, offset, interleaved, q)
+    N = q.shape[2] if q.dim() == 4 else 1
+    lib = load_library()
+    with _on(q.device):
+        st = lib.la_backward_qk_norm_rope(
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if dwq is not None else None,
+            dwk.data_ptr() if dwk is not None else None,
+            _row_strides(dq_out, dk_out, q, k, dq, dk), wq, wk, int(bool(norm)), float(eps),
+            ctypes.byref(rope) if rope is not None else None, q.shape[0], q.shape[1],
+            k.shape[1], N, d, _dtype_code(q), wcode, _stream_ptr(stream, q.device))
+    _raise_if(st)
+    return dq, dk, dwq, dwk
+
+
+# ------------------------------------------------------------------ the
+# recurrence with a gate per channel
+
+def _gate(gate) -> int:
+    code = GATES.get(gate)
+    if code is None:
+        raise ValueError(f"gate must be one of {sorted(GATES)}")
+    return code
+
+
+def _check_seq(x, gates, *ts):
+    """[B, N, C] (or [B, C]) tensors of x's shape, dtype and device, and gates."""
+    torch = _torch()
+    if any(t.shape != x.shape for t in (gates, *ts)):
+        raise ValueError("x, gates, out and the gradients must share one shape")
+    for t in (x, gates, *ts):
+        if not t.is_cuda or t.device != x.device:
+            raise ValueError("all tensors must be on one CUDA device")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
+        if t is not gates and t.dtype != x.dtype:
+            raise TypeError("x, out and the gradients must share one dtype")
+    if gates.dtype != x.dtype and gates.dtype != torch.float32:
+        raise TypeError("gates must be float32 or of x's dtype")
+
+
+def _check_state(B, C, like, *hs):
+    torch = _torch()
+    for h in hs:
+        if h is None:
+            continue
+        if tuple(h.shape) != (B, C) or h.dtype != torch.float32:
+            raise ValueError("a state must be float32 [B, C]")
+        if h.device != like.device:
+            raise ValueError("all tensors must be on one CUDA device")
+        if not h.is_contiguous():
+            raise ValueError("a state must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _seq_strides(*ts):
+    v = []
+    for t in ts:
+        v += (0, 0) if t is None else t.stride()[:2]
+    return (ctypes.c_longlong * len(v))(*v)
+
+
+def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = "value",
+                       complement: bool = False, stream=None):
+    """The gated linear recurrence with a gate per channel over sequences
+    x, gates [B, N, C]: h_t = a_t h_{t-1} + x_t, or + (1 - a_t) x_t with
+    `complement`.  gates (float32 or x's dtype) hold a_t ("value"), log a_t
+    ("log") or its logit ("logit").  h0 [B, C] float32: the state before the
+    first token (None: zero).  Any strides with contiguous channels.  Returns
+    (out [B, N, C], h_last [B, C] float32); h_last=h0 updates in place, and
+    decode_step_recurrence continues from it."""
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must be [B, N, C]")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B, N, C = x.shape
+    if h_last is None:
+        h_last = torch.empty(B, C, dtype=torch.float32, device=x.device)
+    code = _gate(gate)
+    _check_seq(x, gates, out)
+    _check_state(B, C, x, h0, h_last)
+    lib = load_library()
+    with _on(x.device):
+        st = lib.la_forward_recurrence(
+            x.data_ptr(), gates.data_ptr(), _ptr(h0), out.data_ptr(), h_last.data_ptr(),
+            _seq_strides(x, gates, out), B, N, C, code, int(bool(complement)),
+            _dtype_code(x), _dtype_code(gates), _stream_ptr(stream, x.device))
+    _raise_if(st)
+    return out, h_last
+
+
+def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=None,
+                        dgates=None, dh0=None, gate: str = "value",
+                        complement: bool = False, stream=None):
+    """Gradients of forward_recurrence: dout and dh_last (None: zero) are those
+    of its two results, `out` is what it returned; x is needed with
+    `complement` only.  Returns (dx, dgates, dh0), dgates with respect to the
+    gates as given (value, logarithm or logit)."""
+    torch = _torch()
+    if dout.dim() != 3:
+        raise ValueError("dout must be [B, N, C]")
+    if complement and x is None:
+        raise ValueError("x is needed with complement")
+    B, N, C = dout.shape
+    if dx is None:
+        dx = torch.empty(dout.shape, dtype=dout.dtype, device=dout.device)
+    if dgates is None:
+        dgates = torch.empty(gates.shape, dtype=gates.dtype, device=gates.device)
+    if dh0 is None:
+        dh0 = torch.empty(B, C, dtype=torch.float32, device=dout.device)
+    code = _gate(gate)
+    if not complement:
+        x = None
+    _check_seq(dout, gates, out, dx, *([x] if x is not None else []))
+    if dgates.dtype != gates.dtype:
+        raise TypeError("dgates must have the dtype of gates")
+    _check_seq(dout, dgates)
+    _check_state(B, C, dout, h0, dh_last, dh0)
+    lib = load_library()
+    with _on(dout.device):
+        st = lib.la_backward_recurrence(
+            dout.data_ptr(), gates.data_ptr(), out.data_ptr(), _ptr(x), _ptr(h0),
+            _ptr(dh_last), dx.data_ptr(), dgates.data_ptr(), dh0.data_ptr(),
+            _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, code,
+            int(bool(complement)), _dtype_code(dout), _dtype_code(gates),
+            _stream_ptr(stream, dout.device))
+    _raise_if(st)
+    return dx, dgates, dh0
+
+
+def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "value",
+                           complement: bool = False, stream=None):
+    """One token of forward_recurrence: h [B, C] float32 is updated in place
+    (or read, and the new state written to h_out); x, gates [B, C].  Returns
+    out [B, C], the new state in x's dtype."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if h_out is None:
+        h_out = h
+    B, C = x.shape
+    code = _gate(gate)
+    _check_seq(x, gates, out)
+    _check_state(B, C, x, h, h_out)
+    lib = load_library()
+    with _on(x.device):
+        st = lib.la_decode_step_recurrence(
+            h.data_ptr(), h_out.data_ptr(), x.data_ptr(), gates.data_ptr(), out.data_ptr(),
+            (ctypes.c_longlong * 3)(x.stride(0), gates.stride(0), out.stride(0)), B, C, code,
+            int(bool(complement)), _dtype_code(x), _dtype_code(gates),
+            _stream_ptr(stream, x.device))
     _raise_if(st)
     return out
 
