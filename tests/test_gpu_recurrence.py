@@ -268,7 +268,13 @@ def test_padding_keeps_and_zero_gates_reset():
     z[:, 250:] = 1.0
     x[:, 250:] = 0.0
     out, hl = la.forward_recurrence(x.cuda(), z.cuda(), h0.cuda())
-    assert torch.equal(hl, out[:, 249]) and torch.equal(out[:, 300], out[:, 249])
+    assert torch.equal(hl, out[:, -1])
+    # the state is kept up to rounding: out[249] and each later state are the
+    # same exact number, reached by pieces joined differently, each within 16 u E
+    E = bound(x, z, h0, "value", False)
+    for t in (250, 300, 399):
+        err = (out[:, t] - out[:, 249]).abs().cpu().double()
+        assert torch.all(err <= 16 * U * (E[:, t] + E[:, 249]))
     z[:, 100] = 0.0
     a, _ = la.forward_recurrence(x.cuda(), z.cuda(), h0.cuda())
     b, _ = la.forward_recurrence(x.cuda(), z.cuda(), 5 + h0.cuda())
