@@ -10,19 +10,22 @@
 // walked in scan order: tokens ascending, or descending for the gradient.
 //
 // The data is read once.  A block of 8 warps takes a strip of 32 lanes x V
-// channels (one 128-byte row per token and warp) and walks the sequence in
-// rounds of 8 x L tokens, L consecutive ones per warp: each thread copies its own
-// tokens of its own channels into shared memory with cp.async, three rounds deep
-// (the slots are private to the thread, so the copies need no barrier), forms
-// the affine map (A, H) of its L tokens, and one block barrier later applies
-// the maps of the warps before it to the state that the block carries from
-// round to round, then walks its L tokens again from there and stores.
+// channels (one 128-byte row per token) and walks the sequence in rounds of
+// 8 x L tokens, L consecutive ones per warp.  TMA brings a round's tiles into
+// shared memory, three rounds deep.  Each thread forms the affine map (A, H) of
+// its L tokens in registers, and one block barrier later applies the maps of
+// the warps before it to the state that the block carries from round to round,
+// walks its L tokens again from there and stores.
 //
 // Where there are fewer strips than the GPU holds blocks, a cluster of S blocks
 // shares a strip: a round is then S x 8 x L tokens, each block leaves its map in
 // the shared memory of the others, and one cluster barrier replaces the
 // sequence's serial chain.  Maps are joined in scan order, the same for every
-// alignment and type, so repeated calls are bit-identical.
+// alignment, so repeated calls are bit-identical.
+//
+// Rows that TMA cannot take (strides or bases that are not multiples of 16
+// bytes) are read by the threads themselves, each its own tokens and channels
+// into the same places; 4-byte values with cp.async.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -31,33 +34,139 @@
 
 #include "la_internal.h"
 #include "la_tc_host.h"
+#include "la_tc_ptx.cuh"
 
 namespace la {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;        // rounds of copies in flight
+constexpr int kStages = 3;  // rounds of copies in flight
 constexpr int kMaxCluster = 8;
+constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait for a copy, about 2 s
 
-__device__ __forceinline__ float ld(const float *p) { return *p; }
-__device__ __forceinline__ float ld(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st(float *p, float x) { *p = x; }
-__device__ __forceinline__ void st(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+// V channels of one thread; two go through the packed fp32 instructions, which
+// round like the single ones.
+template <int V>
+struct alignas(4 * V) Vec {
+    float v[V];
+};
+__device__ __forceinline__ float2 f2(const Vec<2> &a) { return make_float2(a.v[0], a.v[1]); }
+__device__ __forceinline__ Vec<2> vec(float2 a) { return {{a.x, a.y}}; }
+template <int V>
+__device__ __forceinline__ Vec<V> fma_v(Vec<V> a, Vec<V> b, Vec<V> c) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.v[e] = fmaf(a.v[e], b.v[e], c.v[e]);
+    return a;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> mul_v(Vec<V> a, Vec<V> b) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.v[e] = __fmul_rn(a.v[e], b.v[e]);
+    return a;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> add_v(Vec<V> a, Vec<V> b) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.v[e] = __fadd_rn(a.v[e], b.v[e]);
+    return a;
+}
+__device__ __forceinline__ Vec<2> fma_v(Vec<2> a, Vec<2> b, Vec<2> c) {
+    return vec(__ffma2_rn(f2(a), f2(b), f2(c)));
+}
+__device__ __forceinline__ Vec<2> mul_v(Vec<2> a, Vec<2> b) { return vec(__fmul2_rn(f2(a), f2(b))); }
+__device__ __forceinline__ Vec<2> add_v(Vec<2> a, Vec<2> b) { return vec(__fadd2_rn(f2(a), f2(b))); }
+template <int V>
+__device__ __forceinline__ Vec<V> all_v(float x) {
+    Vec<V> r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = x;
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> neg_v(Vec<V> a) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a.v[e] = -a.v[e];
+    return a;
+}
+
+// V adjacent values in memory.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Mem {
+    T v[V];
+};
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float &d, float x) { d = x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
+template <typename T, int V>
+__device__ __forceinline__ Vec<V> widen(Mem<T, V> m) {
+    Vec<V> r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = to_f(m.v[e]);
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Mem<T, V> narrow(Vec<V> x) {
+    Mem<T, V> m;
+#pragma unroll
+    for (int e = 0; e < V; ++e) from_f(m.v[e], x.v[e]);
+    return m;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // The gate a and 1 - a, without cancellation in either.
-template <int kGate>
-__device__ __forceinline__ void gate_of(float z, float *a, float *rest) {
+template <int kGate, int V>
+__device__ __forceinline__ void gate_of(Vec<V> z, bool need_rest, Vec<V> &a, Vec<V> &rest) {
     if (kGate == LA_GATE_VALUE) {
-        *a = z;
-        *rest = __fsub_rn(1.f, z);
+        a = z;
+        rest = add_v(all_v<V>(1.f), neg_v(z));
     } else if (kGate == LA_GATE_LOG) {
-        *a = expf(z);
-        *rest = -expm1f(z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) a.v[e] = expf(z.v[e]);
+        rest = add_v(all_v<V>(1.f), neg_v(a));
+        if (need_rest) {
+            // 1 - e^z = -z (1 + z/2 (1 + z/3 (...))) near 0, to 2^-24 for |z| <= 1/4
+            Vec<V> s = fma_v(z, all_v<V>(1.f / 720.f), all_v<V>(1.f / 120.f));
+            s = fma_v(s, z, all_v<V>(1.f / 24.f));
+            s = fma_v(s, z, all_v<V>(1.f / 6.f));
+            s = fma_v(s, z, all_v<V>(0.5f));
+            s = fma_v(s, z, all_v<V>(1.f));
+            s = mul_v(s, neg_v(z));
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (fabsf(z.v[e]) <= 0.25f) rest.v[e] = s.v[e];
+        }
     } else {
-        const float t = expf(-fabsf(z)), s = __fdividef(1.f, 1.f + t), u = __fmul_rn(t, s);
-        *a = z < 0.f ? u : s;
-        *rest = z < 0.f ? s : u;
+        // t = e^-z; the smaller of a and 1 - a first, the other as its
+        // complement.  The product with log2(e) is off by 2^-24 |z| in t, but
+        // a is off by only (1 - a) of that.
+        const Vec<V> q = mul_v(z, all_v<V>(-1.4426950408889634f));
+        Vec<V> t, r, small;
+#pragma unroll
+        for (int e = 0; e < V; ++e) t.v[e] = exp2_approx(q.v[e]);
+        const Vec<V> d = add_v(t, all_v<V>(1.f));
+#pragma unroll
+        for (int e = 0; e < V; ++e) r.v[e] = rcp_approx(d.v[e]);
+        const Vec<V> tr = mul_v(t, r);
+#pragma unroll
+        for (int e = 0; e < V; ++e) small.v[e] = z.v[e] < 0.f ? r.v[e] : tr.v[e];
+        const Vec<V> other = add_v(all_v<V>(1.f), neg_v(small));
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            a.v[e] = z.v[e] < 0.f ? small.v[e] : other.v[e];
+            rest.v[e] = z.v[e] < 0.f ? other.v[e] : small.v[e];
+        }
     }
 }
 
@@ -73,237 +182,263 @@ struct SeqOut {
 // Forward: in = {x, gates}, out = {out}.  Backward: in = {dout, gates, out, x},
 // out = {dx, dgates}.
 struct Params {
+    CUtensorMap map[4];  // of in, where TMA reads it
     Seq in[4];
     SeqOut out[2];
     const float *first;  // h0; backward dh_last: the carried state at the start
     float *last;         // h_last; backward dh0
     const float *h0;     // backward: h_0, for the first token's gate
+    int *status;
     int B, N, C, complement, strips;
 };
 
-__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes, int valid) {
-    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-    if (bytes == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(valid)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(valid)
-                     : "memory");
-}
-
-// V adjacent values in a thread's slot.
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Slot {
-    T v[V];
-};
-
-// Slots of one tensor in one stage: [L][kThreads].
-template <typename T, int V, int L>
-constexpr int slots_bytes() {
-    return (int)sizeof(T) * V * L * kThreads;
-}
+// Bytes of one stage: a tile [kWarps L][32 V] of the gates, then of each other
+// input.
 template <typename T, typename G, int V, int L, bool kBack>
 constexpr int stage_bytes(int complement) {
-    return slots_bytes<T, V, L>() * (kBack ? 2 + complement : 1) + slots_bytes<G, V, L>();
+    return kWarps * L * 32 * V *
+           ((int)sizeof(G) + (int)sizeof(T) * (kBack ? 2 + complement : 1));
 }
 
-// kFast: every row of every tensor is aligned to V values.
-template <typename T, typename G, int V, int L, int kGate, bool kFast, bool kBack>
+// Waits for a stage's copies, with a limit: afterwards the launch is marked as
+// failed in the status word and goes on without waiting.
+__device__ __forceinline__ void wait_stage(uint64_t *bar, unsigned parity, bool &dead, int *status) {
+    if (dead || tc::mbar_try_wait(bar, parity)) return;
+    if (!tc::mbar_wait(bar, parity, clock64() + kWaitCycles, nullptr)) {
+        dead = true;
+        if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
+            atomicExch(status + 1, (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
+    }
+}
+
+template <bool k>
+struct Flag {
+    static constexpr bool value = k;
+};
+
+template <typename T, typename G, int V, int L, int kGate, bool kTma, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_constant__ Params p) {
     namespace cg = cooperative_groups;
     constexpr int kTile = kWarps * L;  // tokens per block and round
-    extern __shared__ char stages[];
-    __shared__ float warp_map[2][kWarps][2][32 * V];
-    __shared__ float block_map[2][kMaxCluster][2][32 * V];
+    constexpr int kRow = 32 * V;
+    extern __shared__ __align__(128) char stages[];
+    __shared__ float warp_map[2][kWarps][2][kRow];
+    __shared__ float block_map[2][kMaxCluster][2][kRow];
+    __shared__ uint64_t full[kStages];
 
     const cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int strip = (int)(blockIdx.x / S) % p.strips, b = (int)(blockIdx.x / S) / p.strips;
-    const int c = (strip * 32 + lane) * V;          // first channel
-    const int here = min(max(p.C - c, 0), V);       // channels that exist
+    const int c0 = strip * kRow, c = c0 + lane * V;  // first channel
+    const int here = min(max(p.C - c, 0), V);        // channels that exist
     const int rounds = (int)(((long long)p.N + (long long)S * kTile - 1) / ((long long)S * kTile));
     const int bytes = stage_bytes<T, G, V, L, kBack>(p.complement);
 
-    // token of this thread's i-th step in scan order in round r, or outside
-    // [0, N) behind the sequence's end
-    auto first_step = [&](int r) { return ((long long)r * S + rank) * kTile + warp * L; };
-    auto token = [&](long long step) { return kBack ? p.N - 1 - step : step; };
-
-    auto slot_x = [&](int stage, int which) {
-        return reinterpret_cast<Slot<T, V> *>(stages + (size_t)stage * bytes +
-                                              slots_bytes<G, V, L>() +
-                                              which * slots_bytes<T, V, L>()) + tid;
-    };
-    auto slot_z = [&](int stage) {
-        return reinterpret_cast<Slot<G, V> *>(stages + (size_t)stage * bytes) + tid;
-    };
-    auto fetch_one = [&](auto *slot, const Seq &q, long long t, bool ok) {
-        using E = std::remove_reference_t<decltype(slot->v[0])>;
-        const E *src = static_cast<const E *>(q.p) + (ok ? b * q.b + t * q.n + c : 0);
-        if (kFast) {
-            copy_async(slot, src, (int)sizeof(E) * V, ok ? here * (int)sizeof(E) : 0);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) slot->v[e] = ok && e < here ? src[e] : E(0.f);
-        }
+    // A tile holds the tokens from `low` up; step j of the block in scan order
+    // is its row j, or from the other end backwards.
+    auto first_step = [&](int r) { return ((long long)r * S + rank) * kTile; };
+    auto low = [&](int r) { return kBack ? p.N - first_step(r) - kTile : first_step(r); };
+    auto row = [&](int i) { return kBack ? kTile - 1 - (warp * L + i) : warp * L + i; };
+    auto tile_z = [&](int stage) { return reinterpret_cast<G *>(stages + stage * bytes); };
+    auto tile_x = [&](int stage, int which) {
+        return reinterpret_cast<T *>(stages + stage * bytes + kTile * kRow * (int)sizeof(G)) +
+               which * kTile * kRow;
     };
     auto fetch = [&](int r) {
         const int stage = r % kStages;
-        const long long s0 = first_step(r);
+        if (kTma) {
+            if (tid != 0 || r >= rounds) return;
+            const int t = (int)low(r);
+            const uint64_t policy = tc::policy_evict_first();
+            tc::mbar_arrive_expect_tx(&full[stage], bytes);
+            tc::tma_load_3d(tile_z(stage), &p.map[1], &full[stage], c0, t, b, policy);
+            tc::tma_load_3d(tile_x(stage, 0), &p.map[0], &full[stage], c0, t, b, policy);
+            if (kBack) {
+                tc::tma_load_3d(tile_x(stage, 1), &p.map[2], &full[stage], c0, t - 1, b, policy);
+                if (p.complement)
+                    tc::tma_load_3d(tile_x(stage, 2), &p.map[3], &full[stage], c0, t, b, policy);
+            }
+            return;
+        }
+        auto mine = [&](auto *tile, const Seq &q, int shift) {
+            using E = std::remove_reference_t<decltype(*tile)>;
+            const E *src = static_cast<const E *>(q.p) + b * q.b + c;
+            for (int i = 0; i < L; ++i) {
+                const long long t = low(r) + row(i) - shift;
+                const bool ok = r < rounds && t >= 0 && t < p.N;
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const long long t = token(s0 + i);
-            const bool ok = r < rounds && s0 + i < p.N && here > 0;
-            if (ok || kFast) {
-                fetch_one(slot_x(stage, 0) + i * kThreads, p.in[0], t, ok);
-                fetch_one(slot_z(stage) + i * kThreads, p.in[1], t, ok);
-                if (kBack) {
-                    fetch_one(slot_x(stage, 1) + i * kThreads, p.in[2], t - 1, ok && t > 0);
-                    if (p.complement) fetch_one(slot_x(stage, 2) + i * kThreads, p.in[3], t, ok);
+                for (int e = 0; e < V; ++e) {
+                    E *dst = tile + row(i) * kRow + lane * V + e;
+                    if (!ok || e >= here)
+                        *dst = E(0.f);
+                    else if (sizeof(E) == 4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         tc::smem_u32(dst)), "l"(src + t * q.n + e) : "memory");
+                    else
+                        *dst = src[t * q.n + e];
                 }
             }
+        };
+        mine(tile_z(stage), p.in[1], 0);
+        mine(tile_x(stage, 0), p.in[0], 0);
+        if (kBack) {
+            mine(tile_x(stage, 1), p.in[2], 1);
+            if (p.complement) mine(tile_x(stage, 2), p.in[3], 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-#pragma unroll
+    if (kTma) {
+        if (tid == 0) {
+            for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
+            tc::fence_mbar_init();
+        }
+        __syncthreads();
+    }
     for (int r = 0; r < kStages; ++r) fetch(r);
 
-    float carry[V], h0[V];
+    Vec<V> carry = all_v<V>(0.f), h0 = all_v<V>(0.f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const long long at = (long long)b * p.C + c + e;
-        carry[e] = p.first && e < here ? p.first[at] : 0.f;
-        h0[e] = kBack && p.h0 && e < here ? p.h0[at] : 0.f;
+        if (p.first && e < here) carry.v[e] = p.first[at];
+        if (kBack && p.h0 && e < here) h0.v[e] = p.h0[at];
     }
-
+    bool dead = false;
     // the others' shared memory is written from here on
     if (S > 1) cluster.sync();
     for (int r = 0; r < rounds; ++r) {
         const int stage = r % kStages, par = r & 1;
-        const long long s0 = first_step(r);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const long long s0 = first_step(r) + warp * L;  // this thread's first step
+        const bool behind = s0 + L >= p.N;              // the sequence's end is in or before it
+        const bool edge = behind || c0 + kRow > p.C;
+        if (kTma)
+            wait_stage(&full[stage], (unsigned)(r / kStages) & 1u, dead, p.status);
+        else
+            asm volatile("cp.async.wait_group %0;" ::"n"(kBack ? kStages - 2 : kStages - 1)
+                         : "memory");
+        const G *zt = tile_z(stage) + lane * V;
+        const T *xt = tile_x(stage, 0) + lane * V;
         // a and y (backward: a and 1 - a) of the L tokens, and their map
-        float a[L][V], y[L][V], A[V], H[V];
+        Vec<V> a[L], y[L], A = all_v<V>(1.f), H = all_v<V>(0.f);
+        auto form = [&](auto at_edge) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) A[e] = 1.f, H[e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const Slot<T, V> in = slot_x(stage, 0)[i * kThreads];
-            const Slot<G, V> z = slot_z(stage)[i * kThreads];
-            const bool ok = s0 + i < p.N;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float rest;
-                const float v = ld(&in.v[e]);
-                gate_of<kGate>(ld(&z.v[e]), &a[i][e], &rest);
-                if (!kBack) y[i][e] = p.complement ? __fmul_rn(rest, v) : v;
-                if (kBack) y[i][e] = rest;
-                if (!ok) a[i][e] = 1.f, y[i][e] = 0.f;
-                H[e] = kBack ? __fmul_rn(a[i][e], __fadd_rn(ok ? v : 0.f, H[e]))
-                             : fmaf(a[i][e], H[e], y[i][e]);
-                A[e] = __fmul_rn(A[e], a[i][e]);
+            for (int i = 0; i < L; ++i) {
+                const Vec<V> z = widen<G, V>(*reinterpret_cast<const Mem<G, V> *>(zt + row(i) * kRow));
+                Vec<V> x = widen<T, V>(*reinterpret_cast<const Mem<T, V> *>(xt + row(i) * kRow));
+                Vec<V> rest;
+                gate_of<kGate, V>(z, p.complement || kBack, a[i], rest);
+                y[i] = kBack ? rest : p.complement ? mul_v(rest, x) : x;
+                if (at_edge.value && s0 + i >= p.N) {
+                    a[i] = all_v<V>(1.f);
+                    x = y[i] = all_v<V>(0.f);
+                }
+                H = kBack ? mul_v(a[i], add_v(x, H)) : fma_v(a[i], H, y[i]);
+                A = mul_v(A, a[i]);
             }
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            warp_map[par][warp][0][lane * V + e] = A[e];
-            warp_map[par][warp][1][lane * V + e] = H[e];
-        }
+        };
+        if (edge)
+            form(Flag<true>());
+        else
+            form(Flag<false>());
+        *reinterpret_cast<Vec<V> *>(&warp_map[par][warp][0][lane * V]) = A;
+        *reinterpret_cast<Vec<V> *>(&warp_map[par][warp][1][lane * V]) = H;
         __syncthreads();
+        // forward, everything of this round is in registers now; backward, the
+        // round before is done with its tiles
+        if (!kBack) fetch(r + kStages);
+        if (kBack && r > 0) fetch(r - 1 + kStages);
         // the map of the warps before this one, and of the whole block
-        float Ab[V], Hb[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) Ab[e] = 1.f, Hb[e] = 0.f;
+        Vec<V> Ab = all_v<V>(1.f), Hb = all_v<V>(0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (w == warp) A[e] = Ab[e], H[e] = Hb[e];
-                const float Aw = warp_map[par][w][0][lane * V + e];
-                Hb[e] = fmaf(Aw, Hb[e], warp_map[par][w][1][lane * V + e]);
-                Ab[e] = __fmul_rn(Ab[e], Aw);
-            }
+            if (w == warp) A = Ab, H = Hb;
+            const Vec<V> Aw = *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][0][lane * V]);
+            const Vec<V> Hw = *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][1][lane * V]);
+            Hb = fma_v(Aw, Hb, Hw);
+            Ab = mul_v(Ab, Aw);
         }
-        float state[V];
+        Vec<V> state = all_v<V>(0.f);
         if (S == 1) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                state[e] = fmaf(A[e], carry[e], H[e]);
-                carry[e] = fmaf(Ab[e], carry[e], Hb[e]);
-            }
+            state = fma_v(A, carry, H);
+            carry = fma_v(Ab, carry, Hb);
         } else {
-            for (int to = warp; to < S; to += kWarps) {
-                float *there = cluster.map_shared_rank(&block_map[par][rank][0][0], to);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    there[lane * V + e] = Ab[e];
-                    there[32 * V + lane * V + e] = Hb[e];
-                }
+            if (warp < S) {
+                float *there = cluster.map_shared_rank(&block_map[par][rank][0][lane * V], warp);
+                *reinterpret_cast<Vec<V> *>(there) = Ab;
+                *reinterpret_cast<Vec<V> *>(there + kRow) = Hb;
             }
             cluster.sync();
-            for (int k = 0; k < S; ++k)
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (k == rank) state[e] = fmaf(A[e], carry[e], H[e]);
-                    carry[e] = fmaf(block_map[par][k][0][lane * V + e], carry[e],
-                                    block_map[par][k][1][lane * V + e]);
-                }
+            for (int k = 0; k < S; ++k) {
+                if (k == rank) state = fma_v(A, carry, H);
+                carry = fma_v(*reinterpret_cast<const Vec<V> *>(&block_map[par][k][0][lane * V]),
+                              carry,
+                              *reinterpret_cast<const Vec<V> *>(&block_map[par][k][1][lane * V]));
+            }
         }
         // the L tokens again, from the state that reaches them
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const bool ok = s0 + i < p.N && here > 0;
-            const long long t = token(s0 + i);
-            float o[V], oz[V];
-            if (!kBack) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) o[e] = state[e] = fmaf(a[i][e], state[e], y[i][e]);
-            } else {
-                const Slot<T, V> in = slot_x(stage, 0)[i * kThreads];
-                const Slot<T, V> h = slot_x(stage, 1)[i * kThreads];
-                const Slot<T, V> x = slot_x(stage, p.complement ? 2 : 0)[i * kThreads];
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float g = __fadd_rn(ok ? ld(&in.v[e]) : 0.f, state[e]);
-                    float before = t > 0 ? ld(&h.v[e]) : h0[e];
-                    if (p.complement) before = __fsub_rn(before, ld(&x.v[e]));
-                    const float slope = kGate == LA_GATE_VALUE ? 1.f
-                                        : kGate == LA_GATE_LOG ? a[i][e]
-                                                               : __fmul_rn(a[i][e], y[i][e]);
-                    o[e] = p.complement ? __fmul_rn(y[i][e], g) : g;
-                    oz[e] = __fmul_rn(__fmul_rn(slope, g), before);
-                    state[e] = __fmul_rn(a[i][e], g);
-                }
-            }
-            if (!ok) continue;
-            auto put = [&](auto *base, const SeqOut &q, const float (&v)[V]) {
-                using E = std::remove_pointer_t<decltype(base)>;
-                E *dst = base + b * q.b + t * q.n + c;
-                if (kFast && here == V) {
-                    Slot<E, V> w;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) st(&w.v[e], v[e]);
-                    *reinterpret_cast<Slot<E, V> *>(dst) = w;
+        const long long t0 = kBack ? p.N - 1 - s0 : s0;
+        auto walk = [&](auto at_edge) {
+            T *o = static_cast<T *>(p.out[0].p) + b * p.out[0].b + t0 * p.out[0].n + c;
+            G *oz = static_cast<G *>(p.out[1].p) + b * p.out[1].b + t0 * p.out[1].n + c;
+            auto put = [&](auto *dst, const Vec<V> &v) {
+                using E = std::remove_reference_t<decltype(*dst)>;
+                const Mem<E, V> m = narrow<E, V>(v);
+                if (kTma && (!at_edge.value || here == V)) {
+                    *reinterpret_cast<Mem<E, V> *>(dst) = m;
                 } else {
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        if (e < here) st(dst + e, v[e]);
+                        if (e < here) dst[e] = m.v[e];
                 }
             };
-            put(static_cast<T *>(p.out[0].p), p.out[0], o);
-            if (kBack) put(static_cast<G *>(p.out[1].p), p.out[1], oz);
-        }
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const bool ok = !at_edge.value || s0 + i < p.N;
+                if (!kBack) {
+                    state = fma_v(a[i], state, y[i]);
+                    if (ok) put(o, state);
+                    o += p.out[0].n;
+                    continue;
+                }
+                auto tile = [&](int which) {
+                    return widen<T, V>(*reinterpret_cast<const Mem<T, V> *>(
+                        tile_x(stage, which) + lane * V + row(i) * kRow));
+                };
+                Vec<V> g = tile(0), h = tile(1);
+                if (at_edge.value && !ok) g = all_v<V>(0.f);
+                if (at_edge.value && s0 + i == p.N - 1) h = h0;
+                g = add_v(g, state);
+                if (p.complement) h = add_v(h, neg_v(tile(2)));
+                if (ok) {
+                    put(o, p.complement ? mul_v(y[i], g) : g);
+                    Vec<V> dz = mul_v(g, h);
+                    if (kGate != LA_GATE_VALUE) dz = mul_v(dz, a[i]);
+                    if (kGate == LA_GATE_LOGIT) dz = mul_v(dz, y[i]);
+                    put(oz, dz);
+                }
+                state = mul_v(a[i], g);
+                o -= p.out[0].n;
+                oz -= p.out[1].n;
+            }
+        };
+        if (edge)
+            walk(Flag<true>());
+        else
+            walk(Flag<false>());
         // the state behind the last token, as its warp has it: forward, these
         // are the bits that `out` was rounded from
-        if (p.last && s0 < p.N && s0 + L >= p.N)
+        if (p.last && behind && s0 < p.N)
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (e < here) p.last[(long long)b * p.C + c + e] = state[e];
-        fetch(r + kStages);
+                if (e < here) p.last[(long long)b * p.C + c + e] = state.v[e];
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (kTma && dead)  // copies may still be under way: leave after them
+        for (int r = max(0, rounds - kStages); r < rounds; ++r)
+            tc::mbar_wait(&full[r % kStages], (unsigned)(r / kStages) & 1u,
+                          clock64() + kWaitCycles, nullptr);
 }
 
 // One token: V adjacent channels per thread.
@@ -321,21 +456,20 @@ __global__ void __launch_bounds__(kThreads) rec_step_kernel(const StepParams p) 
     const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
     if (i >= (long long)p.B * p.C) return;
     const int b = (int)(i / p.C), c = (int)(i % p.C);
-    const Slot<T, V> x = *reinterpret_cast<const Slot<T, V> *>(static_cast<const T *>(p.x) + b * p.sx + c);
-    const Slot<G, V> z = *reinterpret_cast<const Slot<G, V> *>(static_cast<const G *>(p.gates) + b * p.sg + c);
-    const Slot<float, V> h = *reinterpret_cast<const Slot<float, V> *>(p.h + i);
-    Slot<float, V> s;
-    Slot<T, V> o;
+    auto get = [](const auto *q) {
+        using E = std::remove_const_t<std::remove_reference_t<decltype(*q)>>;
+        return widen<E, V>(*reinterpret_cast<const Mem<E, V> *>(q));
+    };
+    const Vec<V> x = get(static_cast<const T *>(p.x) + b * p.sx + c);
+    const Vec<V> z = get(static_cast<const G *>(p.gates) + b * p.sg + c);
+    const Vec<V> h = get(p.h + i);
+    Vec<V> a, rest, s;
+    gate_of<kGate, V>(z, p.complement, a, rest);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float a, rest;
-        const float v = ld(&x.v[e]);
-        gate_of<kGate>(ld(&z.v[e]), &a, &rest);
-        s.v[e] = fmaf(a, h.v[e], p.complement ? __fmul_rn(rest, v) : v);
-        st(&o.v[e], s.v[e]);
-    }
-    *reinterpret_cast<Slot<float, V> *>(p.h_out + i) = s;
-    *reinterpret_cast<Slot<T, V> *>(static_cast<T *>(p.out) + b * p.so + c) = o;
+    for (int e = 0; e < V; ++e)
+        s.v[e] = fmaf(a.v[e], h.v[e], p.complement ? __fmul_rn(rest.v[e], x.v[e]) : x.v[e]);
+    *reinterpret_cast<Mem<float, V> *>(p.h_out + i) = narrow<float, V>(s);
+    *reinterpret_cast<Mem<T, V> *>(static_cast<T *>(p.out) + b * p.so + c) = narrow<T, V>(s);
 }
 
 la_status rec_fail(la_status s, const char *who, const char *msg) {
@@ -391,22 +525,55 @@ bool aligned(const void *p, long long b, long long n, int B, int N, int v, int e
            (N <= 1 || n % v == 0);
 }
 
-template <typename T, typename G, int V, int kGate, bool kFast, bool kBack>
-cudaError_t launch_scan(Params p, cudaStream_t stream) {
+// Whether TMA can read the tensor: 16-byte aligned rows that do not overlap.
+bool tma_ok(const Seq &q, int B, int N, int C, int elem) {
+    const long long most = 1LL << 40;
+    return (uintptr_t)q.p % 16 == 0 && N < 0x7fff0000 &&
+           (N <= 1 || (q.n >= C && q.n * elem % 16 == 0 && q.n < most / elem)) &&
+           (B <= 1 || (q.b >= C && q.b * elem % 16 == 0 && q.b < most / elem));
+}
+
+// Map of a tensor as [B][N][C], box [1][rows][columns].
+bool make_map(CUtensorMap *map, const Seq &q, int B, int N, int C, int elem, int columns, int rows) {
+    cudaError_t err;
+    auto enc = tchost::encode_fn(&err);
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)C, (cuuint64_t)N, (cuuint64_t)B};
+    const cuuint64_t any = ((cuuint64_t)C * elem + 15) / 16 * 16;  // of a dimension of one
+    const cuuint64_t strides[2] = {N <= 1 ? any : (cuuint64_t)q.n * elem,
+                                   B <= 1 ? any : (cuuint64_t)q.b * elem};
+    const cuuint32_t box[3] = {(cuuint32_t)columns, (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
+    return enc(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+               3, const_cast<void *>(q.p), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <typename T, typename G, int V, int kGate, bool kBack>
+cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
     constexpr int L = kBack ? 8 : 16;
-    auto kern = rec_scan_kernel<T, G, V, L, kGate, kFast, kBack>;
+    if (tma)
+        for (int i = 0; i < (kBack ? 3 + p.complement : 2); ++i)
+            if (!make_map(&p.map[i], p.in[i], p.B, p.N, p.C,
+                          i == 1 ? (int)sizeof(G) : (int)sizeof(T), 32 * V, kWarps * L))
+                return cudaErrorInvalidValue;
+    auto kern = tma ? rec_scan_kernel<T, G, V, L, kGate, true, kBack>
+                    : rec_scan_kernel<T, G, V, L, kGate, false, kBack>;
     const size_t smem = (size_t)kStages * stage_bytes<T, G, V, L, kBack>(p.complement);
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) p.status = device_status_word(&e);
     if (e != cudaSuccess) return e;
     p.strips = (p.C + 32 * V - 1) / (32 * V);
     const long long strips = (long long)p.B * p.strips;
     // as many blocks per strip as the GPU holds at once (two per SM) and the
     // sequence has work for
     int S = 1;
-    while (S < kMaxCluster && strips * S * 2 <= 2LL * sms && (long long)S * kWarps * L < p.N) S *= 2;
+    while (S < kMaxCluster && strips * S * 2 <= 2LL * sms && (long long)S * kWarps * L < p.N)
+        S *= 2;
     if (strips * S > 2147483647LL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(strips * S));
@@ -421,34 +588,32 @@ cudaError_t launch_scan(Params p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <typename T, typename G, int V, bool kFast, bool kBack>
-cudaError_t launch_gate(const Params &p, la_gate gate, cudaStream_t s) {
-    if (gate == LA_GATE_VALUE) return launch_scan<T, G, V, LA_GATE_VALUE, kFast, kBack>(p, s);
-    if (gate == LA_GATE_LOG) return launch_scan<T, G, V, LA_GATE_LOG, kFast, kBack>(p, s);
-    return launch_scan<T, G, V, LA_GATE_LOGIT, kFast, kBack>(p, s);
+template <typename T, typename G, int V, bool kBack>
+cudaError_t launch_gate(Params &p, la_gate gate, bool tma, cudaStream_t s) {
+    if (gate == LA_GATE_VALUE) return launch_scan<T, G, V, LA_GATE_VALUE, kBack>(p, tma, s);
+    if (gate == LA_GATE_LOG) return launch_scan<T, G, V, LA_GATE_LOG, kBack>(p, tma, s);
+    return launch_scan<T, G, V, LA_GATE_LOGIT, kBack>(p, tma, s);
 }
 
 template <bool kBack>
-la_status launch(const char *who, const Params &p, la_gate gate, la_dtype dtype,
-                 la_dtype gate_dtype, cudaStream_t s) {
-    // the kernel takes 4 bytes of x per thread and token: two bf16 channels
+la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dtype gate_dtype,
+                 cudaStream_t s) {
+    // a thread takes 4 bytes of x per token: two bf16 channels
     const int v = dtype == LA_F32 ? 1 : 2;
     const int ex = dtype == LA_F32 ? 4 : 2, ez = gate_dtype == LA_F32 ? 4 : 2;
-    bool fast = true;
-    for (int i = 0; i < 4; ++i)
-        fast = fast && aligned(p.in[i].p, p.in[i].b, p.in[i].n, p.B, p.N, v, i == 1 ? ez : ex);
+    bool tma = true;
+    for (int i = 0; i < (kBack ? 3 + p.complement : 2); ++i)
+        tma = tma && tma_ok(p.in[i], p.B, p.N, p.C, i == 1 ? ez : ex);
     for (int i = 0; i < 2; ++i)
-        fast = fast && aligned(p.out[i].p, p.out[i].b, p.out[i].n, p.B, p.N, v, i == 1 ? ez : ex);
+        tma = tma && aligned(p.out[i].p, p.out[i].b, p.out[i].n, p.B, p.N, v, i == 1 ? ez : ex);
     using bf16 = __nv_bfloat16;
     cudaError_t e;
     if (dtype == LA_F32)
-        e = launch_gate<float, float, 1, true, kBack>(p, gate, s);
+        e = launch_gate<float, float, 1, kBack>(p, gate, tma, s);
     else if (gate_dtype == LA_F32)
-        e = fast ? launch_gate<bf16, float, 2, true, kBack>(p, gate, s)
-                 : launch_gate<bf16, float, 2, false, kBack>(p, gate, s);
+        e = launch_gate<bf16, float, 2, kBack>(p, gate, tma, s);
     else
-        e = fast ? launch_gate<bf16, bf16, 2, true, kBack>(p, gate, s)
-                 : launch_gate<bf16, bf16, 2, false, kBack>(p, gate, s);
+        e = launch_gate<bf16, bf16, 2, kBack>(p, gate, tma, s);
     return done(who, e);
 }
 
