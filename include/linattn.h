@@ -367,7 +367,8 @@ typedef struct {
  *              may be NULL), d in 1..LA_MAX_D.
  * A decode step is N == 1 with one position per sequence.  Sums of squares
  * are fp32; the angle is exact in the position (64-bit fixed-point turns), so
- * far positions lose nothing.  One kernel, no workspace.
+ * far positions lose nothing.  A row's result does not depend on strides or
+ * alignment.  One kernel, no workspace.
  */
 la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
                           const la_strides *strides, const void *q_weight,
@@ -389,8 +390,12 @@ la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out
  *              Summed in a fixed order: repeated calls are bit-identical.
  *   strides    6 strides, of dq_out, dk_out, q, k, dq, dk, or NULL: contiguous.
  * Other arguments as la_qk_norm_rope (the same values as in the forward).
- * B*N == 0 writes zero weight gradients.  With a weight gradient the call
- * takes a stream-ordered workspace (LA_ERR_NO_MEMORY if that fails).
+ *   workspace  device buffer for the weight gradients' partial sums, 16-byte
+ *              aligned, of la_backward_qk_norm_rope_workspace_bytes(d) bytes, not
+ *              used by anything else until `stream` has passed the call; or
+ *              NULL: allocated stream-ordered (LA_ERR_NO_MEMORY if that fails).
+ *              Without weight gradients none is needed.
+ * B*N == 0 writes zero weight gradients.
  */
 la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const void *q,
                                    const void *k, void *dq, void *dk, float *dq_weight,
@@ -398,7 +403,12 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
                                    const void *q_weight, const void *k_weight, int norm,
                                    float eps, const la_rope *rope, int B, int Hq, int Hk,
                                    int N, int d, la_dtype dtype, la_dtype weight_dtype,
+                                   void *workspace, size_t workspace_bytes,
                                    la_stream_t stream);
+
+/* Workspace bytes that la_backward_qk_norm_rope needs at most on the current
+ * device for head dimension d (0 for an invalid d). */
+size_t la_backward_qk_norm_rope_workspace_bytes(int d);
 
 /* What a gate tensor of the per-channel recurrence holds: the gate a itself,
  * its logarithm (a = exp(g)) or its logit (a = 1 / (1 + exp(-g))). */

@@ -10,8 +10,10 @@ on a CUDA device, the call raises.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -38,7 +40,8 @@ EXPORTED = ("la_forward", "la_forward_ex", "la_decode_step",
             "la_decode_step_ex", "la_forward_variant", "la_decode_step_variant",
             "la_forward_gated", "la_decode_step_gated", "la_decode_step_delta",
             "la_debug_inject_timeout", "la_debug_fail_next_allocs", "la_forward_delta",
-            "la_qk_norm_rope", "la_backward_qk_norm_rope", "la_forward_recurrence",
+            "la_qk_norm_rope", "la_backward_qk_norm_rope",
+            "la_backward_qk_norm_rope_workspace_bytes", "la_forward_recurrence",
             "la_backward_recurrence", "la_decode_step_recurrence")
 
 FEATURE_MAPS = {"elu1": 0, "identity": 1}
@@ -47,14 +50,6 @@ GATES = {"value": 0, "log": 1, "logit": 2}
 
 class _Variant(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("normalise", ctypes.c_int)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("frequencies", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p),
-                ("position_bytes", ctypes.c_int),
-                ("position_stride_b", ctypes.c_longlong),
-                ("position_stride_n", ctypes.c_longlong), ("offset", ctypes.c_longlong)]
 
 
 def _variant(feature_map, normalise):
@@ -102,7 +97,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.la_qk_norm_rope.argtypes = [V, V, V, V, V, V, V, I, ctypes.c_float, V,
                                     I, I, I, I, I, I, I, V]
     lib.la_backward_qk_norm_rope.argtypes = [V, V, V, V, V, V, V, V, V, V, V, I,
-                                             ctypes.c_float, V, I, I, I, I, I, I, I, V]
+                                             ctypes.c_float, V, I, I, I, I, I, I, I,
+                                             V, ctypes.c_size_t, V]
+    lib.la_backward_qk_norm_rope_workspace_bytes.argtypes = [I]
+    lib.la_backward_qk_norm_rope_workspace_bytes.restype = ctypes.c_size_t
     lib.la_forward_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, I, V]
     lib.la_backward_recurrence.argtypes = [V, V, V, V, V, V, V, V, V, V,
                                            I, I, I, I, I, I, I, V]
@@ -165,9 +163,19 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_AS_IS = contextlib.nullcontext()
+
+
 def _on(device):
     """`device` as the current CUDA device while the library is called."""
-    return _torch().cuda.device(device)
+    torch = _torch()
+    return _AS_IS if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _decay_arg(decay, H):
@@ -428,91 +436,96 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0):
                              for i in range(rotary_dim // 2)])
 
 
+# la_rope: frequencies, rotary_dim, interleaved, positions, position_bytes,
+# position_stride_b, position_stride_n, offset
+_ROPE = struct.Struct("@PiiPiqqq")
+
+
 def _rope(frequencies, positions, offset, interleaved, q):
-    """The rotation's descriptor and what has to outlive the call."""
+    """The packed la_rope (None: no rotation) and what has to outlive the call."""
     if frequencies is None or len(frequencies) == 0:
         return None, None
     f = frequencies
     if not (isinstance(f, array.array) and f.typecode == "d"):
         f = array.array("d", [float(x) for x in f])
-    r = _Rope(f.buffer_info()[0], 2 * len(f), int(bool(interleaved)), None, 0, 0, 0, int(offset))
+    ptr, nbytes, sb, sn = 0, 0, 0, 0
     if positions is not None:
         torch = _torch()
-        shape = (q.shape[0],) if q.dim() == 3 else (q.shape[0], q.shape[2])
-        if tuple(positions.shape) != shape and tuple(positions.shape) != shape[1:]:
-            raise ValueError(f"positions must have the shape {list(shape)}"
-                             + (f" or {list(shape[1:])}" if q.dim() == 4 else ""))
-        if positions.dtype not in (torch.int32, torch.int64):
+        shape, st = positions.shape, positions.stride()
+        want = q.shape[:1] if q.dim() == 3 else (q.shape[0], q.shape[2])
+        if shape == want:
+            sb, sn = (st[0], 0) if q.dim() == 3 else st
+        elif q.dim() == 4 and shape == want[1:]:
+            sn = st[0]
+        else:
+            raise ValueError(f"positions must have the shape {list(want)}"
+                             + (f" or {list(want[1:])}" if q.dim() == 4 else ""))
+        if positions.dtype == torch.int64:
+            nbytes = 8
+        elif positions.dtype == torch.int32:
+            nbytes = 4
+        else:
             raise TypeError("positions must be int32 or int64")
         if positions.device != q.device:
             raise ValueError("positions must be on q's CUDA device")
-        st = positions.stride()
-        r.positions = positions.data_ptr()
-        r.position_bytes = positions.element_size()
-        if q.dim() == 3:
-            r.position_stride_b = st[0]
-        else:
-            r.position_stride_b = st[0] if positions.dim() == 2 else 0
-            r.position_stride_n = st[-1]
-    return r, f
+        ptr = positions.data_ptr()
+    return _ROPE.pack(f.buffer_info()[0], 2 * len(f), bool(interleaved), ptr, nbytes, sb, sn,
+                      offset), f
 
 
 def _check_rows(like, *ts):
-    """Tensors of rows: `like`'s dtype and device, the last dimension contiguous."""
+    """Tensors of rows: one dtype, one CUDA device, the last dimension contiguous."""
+    device, dtype = like.device, like.dtype
+    if not like.is_cuda:
+        raise ValueError("all tensors must be on a CUDA device")
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("all tensors must be on a CUDA device")
-        if t.device != like.device:
+        if t.device != device:
             raise ValueError("all tensors must be on one CUDA device")
-        if t.dtype != like.dtype:
+        if t.dtype != dtype:
             raise TypeError("q, k, their outputs and gradients must share one dtype")
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("the last dimension must be contiguous")
 
 
 def _row_strides(*ts):
-    """la_strides of [B, H, N, d] or [B, H, d] tensors (None: zeros)."""
+    """la_strides of [B, H, N, d] or [B, H, d] tensors."""
     v = []
     for t in ts:
-        if t is None:
-            v += (0, 0, 0)
-            continue
         s = t.stride()
-        v += (s[0], s[1], s[2] if len(s) == 4 else 0)
-    return (ctypes.c_longlong * len(v))(*v)
-
-
-def _weight(w, d, like):
-    """(pointer or None, its dtype code) of a [d] weight."""
-    if w is None:
-        return None, LA_F32
-    if tuple(w.shape) != (d,):
-        raise ValueError(f"a weight must have the shape [{d}]")
-    if w.device != like.device:
-        raise ValueError("the weights must be on q's CUDA device")
-    if not w.is_contiguous():
-        raise ValueError("a weight must be contiguous")
-    return w.data_ptr(), _dtype_code(w)
+        v += s[:3] if len(s) == 4 else (s[0], s[1], 0)
+    return struct.pack(f"@{len(v)}q", *v)
 
 
 def _weights(q_weight, k_weight, d, like):
-    wq, cq = _weight(q_weight, d, like)
-    wk, ck = _weight(k_weight, d, like)
-    if wq is not None and wk is not None and cq != ck:
-        raise TypeError("q_weight and k_weight must share one dtype")
-    return wq, wk, cq if wq is not None else ck
+    """(q_weight's and k_weight's pointers or None, their dtype code)."""
+    ptr, code = [None, None], None
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is None:
+            continue
+        if w.dim() != 1 or w.shape[0] != d:
+            raise ValueError(f"a weight must have the shape [{d}]")
+        if w.device != like.device:
+            raise ValueError("the weights must be on q's CUDA device")
+        if not w.is_contiguous():
+            raise ValueError("a weight must be contiguous")
+        if code is not None and w.dtype != q_weight.dtype:
+            raise TypeError("q_weight and k_weight must share one dtype")
+        ptr[i], code = w.data_ptr(), _dtype_code(w)
+    return ptr[0], ptr[1], code or LA_F32
 
 
 def _check_qk(q, k):
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    qs, ks = q.shape, k.shape
+    if len(qs) not in (3, 4) or len(ks) != len(qs):
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
-    if k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:]:
+    if ks[0] != qs[0] or ks[2:] != qs[2:]:
         raise ValueError("q and k may differ in the number of heads only")
+    return qs[0], qs[1], ks[1], qs[2] if len(qs) == 4 else 1, qs[-1]
 
 
-def _head_major(t):
+def _contiguous_like(t):
     torch = _torch()
-    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions=None, *,
@@ -525,31 +538,28 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     views of a fused projection; the results are contiguous unless q_out and
     k_out say otherwise (q_out=q, k_out=k: in place).
 
-    q_weight, k_weight [d]: float32 or q's dtype, or None.  frequencies:
+    q_weight, k_weight [d]: float32 or bfloat16, or None.  frequencies:
     radians per position of each pair (rope_frequencies()), None for no
     rotation; features beyond 2 len(frequencies) are not rotated.  positions:
     int32 or int64 [B, N] or [N] ([B] for one token), or None for 0..N-1;
     `offset` is added.  interleaved: pairs (2i, 2i+1) instead of (i, i + R/2).
     Returns (q_out, k_out)."""
-    _check_qk(q, k)
+    B, Hq, Hk, N, d = _check_qk(q, k)
     if q_out is None:
-        q_out = _head_major(q)
+        q_out = _contiguous_like(q)
     if k_out is None:
-        k_out = _head_major(k)
+        k_out = _contiguous_like(k)
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out and k_out must have the shapes of q and k")
     _check_rows(q, q, k, q_out, k_out)
-    d = q.shape[-1]
     wq, wk, wcode = _weights(q_weight, k_weight, d, q)
     rope, keep = _rope(frequencies, positions, offset, interleaved, q)
-    N = q.shape[2] if q.dim() == 4 else 1
-    lib = load_library()
-    with _on(q.device):
-        st = lib.la_qk_norm_rope(
+    device = q.device
+    with _on(device):
+        st = load_library().la_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            _row_strides(q, k, q_out, k_out), wq, wk, int(bool(norm)), float(eps),
-            ctypes.byref(rope) if rope is not None else None, q.shape[0], q.shape[1],
-            k.shape[1], N, d, _dtype_code(q), wcode, _stream_ptr(stream, q.device))
+            _row_strides(q, k, q_out, k_out), wq, wk, bool(norm), eps, rope, B, Hq, Hk, N, d,
+            _dtype_code(q), wcode, _raw_stream(stream, device))
     _raise_if(st)
     return q_out, k_out
 
@@ -563,7 +573,7 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     there is no weight.  dq and dk take any strides, such as views of a fused
     projection's gradient (default: laid out like q and k)."""
     torch = _torch()
-    _check_qk(q, k)
+    B, Hq, Hk, N, d = _check_qk(q, k)
     if dq_out.shape != q.shape or dk_out.shape != k.shape:
         raise ValueError("dq_out and dk_out must have the shapes of q and k")
     if dq is None:
@@ -573,21 +583,26 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     if dq.shape != q.shape or dk.shape != k.shape:
         raise ValueError("dq and dk must have the shapes of q and k")
     _check_rows(q, dq_out, dk_out, q, k, dq, dk)
-    d = q.shape[-1]
     wq, wk, wcode = _weights(q_weight, k_weight, d, q)
-    dwq = torch.empty(d, dtype=torch.float32, device=q.device) if wq is not None else None
-    dwk = torch.empty(d, dtype=torch.float32, device=q.device) if wk is not None else None
+    device, lib = q.device, load_library()
     rope, keep = _rope(frequencies, positions, offset, interleaved, q)
-    N = q.shape[2] if q.dim() == 4 else 1
-    lib = load_library()
-    with _on(q.device):
+    with _on(device):
+        dwq = dwk = ws = None
+        ws_bytes = 0
+        if wq is not None:
+            dwq = torch.empty(d, dtype=torch.float32, device=device)
+        if wk is not None:
+            dwk = torch.empty(d, dtype=torch.float32, device=device)
+        # on the current stream torch's allocator gives the workspace; the
+        # library allocates on another one
+        if stream is None and (wq is not None or wk is not None):
+            ws_bytes = lib.la_backward_qk_norm_rope_workspace_bytes(d)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         st = lib.la_backward_qk_norm_rope(
-            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if dwq is not None else None,
-            dwk.data_ptr() if dwk is not None else None,
-            _row_strides(dq_out, dk_out, q, k, dq, dk), wq, wk, int(bool(norm)), float(eps),
-            ctypes.byref(rope) if rope is not None else None, q.shape[0], q.shape[1],
-            k.shape[1], N, d, _dtype_code(q), wcode, _stream_ptr(stream, q.device))
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), _ptr(dwq), _ptr(dwk), _row_strides(dq_out, dk_out, q, k, dq, dk), wq,
+            wk, bool(norm), eps, rope, B, Hq, Hk, N, d, _dtype_code(q), wcode, _ptr(ws), ws_bytes,
+            _raw_stream(stream, device))
     _raise_if(st)
     return dq, dk, dwq, dwk
 
@@ -604,26 +619,31 @@ def _gate(gate) -> int:
 
 def _check_seq(x, gates, *ts):
     """[B, N, C] (or [B, C]) tensors of x's shape, dtype and device, and gates."""
-    torch = _torch()
-    if any(t.shape != x.shape for t in (gates, *ts)):
-        raise ValueError("x, gates, out and the gradients must share one shape")
-    for t in (x, gates, *ts):
-        if not t.is_cuda or t.device != x.device:
-            raise ValueError("all tensors must be on one CUDA device")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("the last dimension must be contiguous")
-        if t is not gates and t.dtype != x.dtype:
+    shape, dtype, device = x.shape, x.dtype, x.device
+    for t in ts:
+        if t.shape != shape:
+            raise ValueError("x, gates, out and the gradients must share one shape")
+        if t.dtype != dtype:
             raise TypeError("x, out and the gradients must share one dtype")
-    if gates.dtype != x.dtype and gates.dtype != torch.float32:
+    if gates.shape != shape:
+        raise ValueError("x, gates, out and the gradients must share one shape")
+    if gates.dtype != dtype and gates.dtype != _torch().float32:
         raise TypeError("gates must be float32 or of x's dtype")
+    if not x.is_cuda:
+        raise ValueError("all tensors must be on one CUDA device")
+    for t in (x, gates, *ts):
+        if t.device != device:
+            raise ValueError("all tensors must be on one CUDA device")
+        if t.stride(-1) != 1 and shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
 
 
 def _check_state(B, C, like, *hs):
-    torch = _torch()
+    float32 = _torch().float32
     for h in hs:
         if h is None:
             continue
-        if tuple(h.shape) != (B, C) or h.dtype != torch.float32:
+        if h.dim() != 2 or h.shape[0] != B or h.shape[1] != C or h.dtype != float32:
             raise ValueError("a state must be float32 [B, C]")
         if h.device != like.device:
             raise ValueError("all tensors must be on one CUDA device")
@@ -639,7 +659,7 @@ def _seq_strides(*ts):
     v = []
     for t in ts:
         v += (0, 0) if t is None else t.stride()[:2]
-    return (ctypes.c_longlong * len(v))(*v)
+    return struct.pack(f"@{len(v)}q", *v)
 
 
 def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = "value",
@@ -655,19 +675,18 @@ def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = 
     if x.dim() != 3:
         raise ValueError("x must be [B, N, C]")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _contiguous_like(x)
     B, N, C = x.shape
     if h_last is None:
         h_last = torch.empty(B, C, dtype=torch.float32, device=x.device)
     code = _gate(gate)
     _check_seq(x, gates, out)
     _check_state(B, C, x, h0, h_last)
-    lib = load_library()
     with _on(x.device):
-        st = lib.la_forward_recurrence(
+        st = load_library().la_forward_recurrence(
             x.data_ptr(), gates.data_ptr(), _ptr(h0), out.data_ptr(), h_last.data_ptr(),
-            _seq_strides(x, gates, out), B, N, C, code, int(bool(complement)),
-            _dtype_code(x), _dtype_code(gates), _stream_ptr(stream, x.device))
+            _seq_strides(x, gates, out), B, N, C, code, bool(complement), _dtype_code(x),
+            _dtype_code(gates), _raw_stream(stream, x.device))
     _raise_if(st)
     return out, h_last
 
@@ -686,9 +705,9 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
         raise ValueError("x is needed with complement")
     B, N, C = dout.shape
     if dx is None:
-        dx = torch.empty(dout.shape, dtype=dout.dtype, device=dout.device)
+        dx = _contiguous_like(dout)
     if dgates is None:
-        dgates = torch.empty(gates.shape, dtype=gates.dtype, device=gates.device)
+        dgates = _contiguous_like(gates)
     if dh0 is None:
         dh0 = torch.empty(B, C, dtype=torch.float32, device=dout.device)
     code = _gate(gate)
@@ -699,14 +718,12 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
         raise TypeError("dgates must have the dtype of gates")
     _check_seq(dout, dgates)
     _check_state(B, C, dout, h0, dh_last, dh0)
-    lib = load_library()
     with _on(dout.device):
-        st = lib.la_backward_recurrence(
+        st = load_library().la_backward_recurrence(
             dout.data_ptr(), gates.data_ptr(), out.data_ptr(), _ptr(x), _ptr(h0),
             _ptr(dh_last), dx.data_ptr(), dgates.data_ptr(), dh0.data_ptr(),
-            _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, code,
-            int(bool(complement)), _dtype_code(dout), _dtype_code(gates),
-            _stream_ptr(stream, dout.device))
+            _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, code, bool(complement),
+            _dtype_code(dout), _dtype_code(gates), _raw_stream(stream, dout.device))
     _raise_if(st)
     return dx, dgates, dh0
 
@@ -716,24 +733,22 @@ def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "va
     """One token of forward_recurrence: h [B, C] float32 is updated in place
     (or read, and the new state written to h_out); x, gates [B, C].  Returns
     out [B, C], the new state in x's dtype."""
-    torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _contiguous_like(x)
     if h_out is None:
         h_out = h
     B, C = x.shape
     code = _gate(gate)
     _check_seq(x, gates, out)
     _check_state(B, C, x, h, h_out)
-    lib = load_library()
     with _on(x.device):
-        st = lib.la_decode_step_recurrence(
+        st = load_library().la_decode_step_recurrence(
             h.data_ptr(), h_out.data_ptr(), x.data_ptr(), gates.data_ptr(), out.data_ptr(),
-            (ctypes.c_longlong * 3)(x.stride(0), gates.stride(0), out.stride(0)), B, C, code,
-            int(bool(complement)), _dtype_code(x), _dtype_code(gates),
-            _stream_ptr(stream, x.device))
+            struct.pack("@3q", x.stride(0), gates.stride(0), out.stride(0)), B, C, code,
+            bool(complement), _dtype_code(x), _dtype_code(gates),
+            _raw_stream(stream, x.device))
     _raise_if(st)
     return out
 

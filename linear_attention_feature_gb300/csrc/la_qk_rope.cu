@@ -47,37 +47,37 @@ struct Params {
     float eps, inv_d;
     float *partial;  // backward: a row of d sums of g n for each block, or NULL
     // the split of the work, see qk_rows_kernel
-    int lane_bits, token_bits, heads_per_unit, chunks[2], blocks_q;
+    int lane_bits, token_bits, rows_per_unit, chunks[2], blocks_q;
     unsigned long long turns[kMaxPairs];  // frequency, 2^-64 turns per position
 };
 
 // V values of T as they lie in memory: one load or store of V * sizeof(T) bytes.
-template <int kBytes> struct Raw;
-template <> struct Raw<16> { using type = uint4; };
-template <> struct Raw<8> { using type = uint2; };
-template <> struct Raw<4> { using type = unsigned; };
-template <> struct Raw<2> { using type = unsigned short; };
-
 template <typename T, int V>
-struct Pack {
-    union {
-        typename Raw<sizeof(T) * V>::type raw;
-        T v[V];
-    };
-    __device__ Pack() {}
+struct alignas(sizeof(T) * V) Pack {
+    T v[V];
 };
-template <typename T, int V>
-__device__ __forceinline__ void load(Pack<T, V> &p, const T *src) {
-    p.raw = *reinterpret_cast<const typename Raw<sizeof(T) * V>::type *>(src);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store(T *dst, const Pack<T, V> &p) {
-    *reinterpret_cast<typename Raw<sizeof(T) * V>::type *>(dst) = p.raw;
-}
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float &d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
+
+// Global to shared memory, zeros where !ok; asynchronous from 4 bytes on.
+template <typename T, int V>
+__device__ __forceinline__ void fetch(Pack<T, V> *dst, const T *src, bool ok) {
+    constexpr int kBytes = (int)sizeof(T) * V;
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    if (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
+                     "r"(ok ? 16 : 0) : "memory");
+    else if (kBytes == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src),
+                     "r"(ok ? 8 : 0) : "memory");
+    else if (kBytes == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src),
+                     "r"(ok ? 4 : 0) : "memory");
+    else
+        for (int e = 0; e < V; ++e) dst->v[e] = ok ? src[e] : T(0.f);
+}
 
 __device__ __forceinline__ float weight_at(const void *w, int w_bf16, int i) {
     if (!w) return 1.f;
@@ -94,32 +94,60 @@ __device__ __forceinline__ long long position_of(const Params &p, int b, int n) 
 }
 
 // cos and sin of pos * turns (2^-64 turns).  The top 32 bits as a signed
-// number are the angle in 2^-31 half turns, in [-1, 1).
+// number are the angle in 2^-31 half turns, in [-1, 1).  For bf16 rows the
+// special function unit is exact enough: within [-pi, pi] it is off by 2^-21 at
+// most, 2^-12 of half a step of the result.
+template <bool kFine>
 __device__ __forceinline__ void turn_of(long long pos, unsigned long long turns, float *c,
                                         float *s) {
-    const unsigned long long phase = (unsigned long long)pos * turns;
-    sincospif((float)(int)(phase >> 32) * 0x1p-31f, s, c);
+    const float t = (float)(int)(((unsigned long long)pos * turns) >> 32);
+    if (kFine)
+        sincospif(t * 0x1p-31f, s, c);
+    else
+        __sincosf(t * 1.46291807926715968e-9f, s, c);  // pi 2^-31
 }
 
-// Sum over a row of K chunks of V terms in each of 2^bits lanes.  Term e of
-// chunk j in lane l stands for pair ((j << bits) + l) V + e; the sum is the
-// binary tree over the pair's bits from the lowest up, so that it does not
-// depend on V: a row gives the same bits whatever its alignment.
-template <int V, int K>
-__device__ __forceinline__ float row_sum(float (&t)[K][V], int bits) {
+// Sum over a row of K chunks of V terms in each of 2^bits lanes, N sums at
+// once.  Term e of chunk j in lane l stands for pair ((j << bits) + l) V + e; the
+// sum is the binary tree over the pair's bits from the lowest up, so that it
+// does not depend on V: a row gives the same bits whatever its alignment.
+template <int N, int K, int P>
+__device__ __forceinline__ void row_sum(float2 (&t)[N][K][P], int bits, float (&sum)[N]) {
+    float u[N][K];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
+    for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int o = 1; o < V; o *= 2)
+        for (int j = 0; j < K; ++j) {
+            float w[P];
 #pragma unroll
-            for (int e = 0; e < V; e += 2 * o) t[j][e] += t[j][e + o];
-        for (int o = 1; o >> bits == 0; o <<= 1) t[j][0] += __shfl_xor_sync(~0u, t[j][0], o);
+            for (int e = 0; e < P; ++e) w[e] = __fadd_rn(t[q][j][e].x, t[q][j][e].y);
+#pragma unroll
+            for (int o = 1; o < P; o *= 2)
+#pragma unroll
+                for (int e = 0; e < P; e += 2 * o) w[e] = __fadd_rn(w[e], w[e + o]);
+            u[q][j] = w[0];
+        }
+    for (int o = 1; o >> bits == 0; o <<= 1)
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+#pragma unroll
+            for (int j = 0; j < K; ++j) u[q][j] += __shfl_xor_sync(~0u, u[q][j], o);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+#pragma unroll
+        for (int o = 1; o < K; o *= 2)
+#pragma unroll
+            for (int j = 0; j < K; j += 2 * o) u[q][j] += u[q][j + o];
+        sum[q] = u[q][0];
     }
-#pragma unroll
-    for (int o = 1; o < K; o *= 2)
-#pragma unroll
-        for (int j = 0; j < K; j += 2 * o) t[j][0] += t[j + o][0];
-    return t[0][0];
+}
+
+// Rows in flight per thread.
+template <bool kBack>
+constexpr int ring_depth() { return kBack ? 3 : 4; }
+template <typename T, int V, int K, bool kBack>
+constexpr int ring_bytes() {
+    return ring_depth<kBack>() * (kBack ? 2 : 1) * K * 2 * kThreads * V * (int)sizeof(T);
 }
 
 // A row is shared by 2^lane_bits lanes of a warp.  A lane takes K chunks of V
@@ -127,17 +155,25 @@ __device__ __forceinline__ float row_sum(float (&t)[K][V], int bits) {
 // where pairs are neighbours (kInter, and where d is odd, which leaves the last
 // alone), else (i, i + half) in the rotated part and (i + half, i + d / 2) in
 // the rest: both values of a pair are always in one thread and every access is
-// one vector.  A block's groups of lanes are 2^token_bits tokens
-// times as many heads as are left; a unit of work is such a tile of tokens and
-// `heads_per_unit` heads of one side.  Angles (a 64-bit product, sincospi) are
-// formed once per token and lane and serve all heads of the unit.
+// one vector.
 //
-// Forward: one unit per block.  Backward: a block takes the units of one side
-// blockIdx, blockIdx + blocks, ..., and keeps its sums of g n in registers; they
-// leave once at its end.
+// A block's groups of lanes are 2^token_bits tokens times as many heads as are
+// left.  A unit of work is such a tile of tokens and rows_per_unit rows (heads)
+// per group; a block walks the units blockIdx, blockIdx + blocks, ...  Forward,
+// the heads of q and k are one list; backward, a block keeps to one side, and
+// the sums of g n stay in its registers until its end.  Angles are formed once per
+// token and lane and serve all rows of the unit.  Rows travel through a ring in
+// shared memory, filled by cp.async some rows ahead; every thread reads only
+// what it copied itself, so the ring needs no barrier.
 template <typename T, int V, int K, bool kInter, bool kBack>
-__global__ void __launch_bounds__(kThreads) qk_rows_kernel(const __grid_constant__ Params p) {
-    constexpr int U = kBack ? (V == 1 ? 1 : 2) : (V * K >= 8 ? 2 : 4);  // rows in flight
+__global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_constant__ Params p) {
+    constexpr int P = (V + 1) / 2;  // packed pairs per chunk (V = 1: half of one)
+    constexpr int kDepth = ring_depth<kBack>(), kSrc = kBack ? 2 : 1;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ unsigned long long turns[kMaxPairs];
+    __shared__ float weight[2][LA_MAX_D];
+    Pack<T, V> *ring = reinterpret_cast<Pack<T, V> *>(smem) + threadIdx.x;
+
     const int bits = p.lane_bits, lane = threadIdx.x & ((1 << bits) - 1);
     const int group = threadIdx.x >> bits;
     const int tok_in = group & ((1 << p.token_bits) - 1), head_in = group >> p.token_bits;
@@ -145,28 +181,23 @@ __global__ void __launch_bounds__(kThreads) qk_rows_kernel(const __grid_constant
     const int pairs = (p.d + 1) / 2;
     const long long tokens = (long long)p.B * p.N;
 
-    int which;
-    long long unit, unit_step;
-    if (kBack) {
-        which = (int)blockIdx.x >= p.blocks_q;
-        unit = which ? blockIdx.x - p.blocks_q : blockIdx.x;
-        unit_step = which ? gridDim.x - p.blocks_q : p.blocks_q;
-    } else {
-        const int all = p.chunks[0] + p.chunks[1];
-        const long long tile = blockIdx.x / all;
-        const int chunk = (int)(blockIdx.x - tile * all);
-        which = chunk >= p.chunks[0];
-        unit = tile * p.chunks[which] + (which ? chunk - p.chunks[0] : chunk);
-        unit_step = 0;
-    }
-    const Side &sd = p.side[which];
-    const int chunks = p.chunks[which], H = sd.H;
+    const int side0 = kBack && (int)blockIdx.x >= p.blocks_q;
+    const int Hq = p.side[0].H;
+    const int heads = kBack ? p.side[side0].H : Hq + p.side[1].H;
+    const int chunks = p.chunks[side0];
+    const unsigned first = side0 ? blockIdx.x - p.blocks_q : blockIdx.x;
+    const unsigned stride = !kBack ? gridDim.x : side0 ? gridDim.x - p.blocks_q : p.blocks_q;
     const long long units = ((tokens + (1 << p.token_bits) - 1) >> p.token_bits) * chunks;
 
-    // this lane's features and their weights
-    int lo[K], hi[K];
+    for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) turns[i] = i < p.half ? p.turns[i] : 0;
+    for (int i = threadIdx.x; i < p.d; i += kThreads) {
+        weight[0][i] = weight_at(p.side[0].w, p.w_bf16, i);
+        weight[1][i] = weight_at(p.side[1].w, p.w_bf16, i);
+    }
+    __syncthreads();
+
+    int lo[K], hi[K];  // this lane's features
     bool l_ok[K], h_ok[K];
-    float w[K][2 * V];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
         const int i = (lane + (j << bits)) * V;  // first pair of the chunk
@@ -175,137 +206,244 @@ __global__ void __launch_bounds__(kThreads) qk_rows_kernel(const __grid_constant
         hi[j] = next ? 2 * i + V : rot ? i + p.half : i + p.d / 2;
         l_ok[j] = i < pairs;
         h_ok[j] = l_ok[j] && hi[j] < p.d;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[j][e] = l_ok[j] ? weight_at(sd.w, p.w_bf16, lo[j] + e) : 0.f;
-            w[j][V + e] = h_ok[j] ? weight_at(sd.w, p.w_bf16, hi[j] + e) : 0.f;
-        }
     }
-    float dw[K][2 * V] = {};
 
-    do {
+    // Where a unit's rows of this group are.
+    struct Where {
+        const T *x[2], *dy[2];
+        T *y[2];
+        int head;  // the group's first
+        long long pos;
+        bool ok;
+    };
+    auto locate = [&](long long unit, bool compute) {
+        Where w;
         const long long tile = unit / chunks;
-        const int h0 = (int)(unit - tile * chunks) * p.heads_per_unit;
-        const int h1 = min(h0 + p.heads_per_unit, H);
         const long long tok = (tile << p.token_bits) + tok_in;
-        const bool t_ok = tok < tokens && (!kBack || unit < units);
-        const bool small = tokens <= 0x7fffffff;
-        const int b = !t_ok ? 0 : small ? (int)((unsigned)tok / (unsigned)p.N) : (int)(tok / p.N);
-        const int n = t_ok ? (int)(tok - (long long)b * p.N) : 0;
-        const T *x = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n;
-        const T *dy = static_cast<const T *>(sd.dy) + b * sd.sdy.b + n * sd.sdy.n;
-        T *y = static_cast<T *>(sd.y) + b * sd.sy.b + n * sd.sy.n;
+        w.head = (int)(unit - tile * chunks) * p.rows_per_unit * head_step + head_in;
+        w.ok = unit < units && tok < tokens;
+        const int b = !w.ok ? 0 : tokens <= 0x7fffffff ? (int)((unsigned)tok / (unsigned)p.N)
+                                                      : (int)(tok / p.N);
+        const int n = w.ok ? (int)(tok - (long long)b * p.N) : 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (kBack && s != side0) continue;
+            const Side &sd = p.side[s];
+            w.x[s] = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n;
+            w.dy[s] = static_cast<const T *>(sd.dy) + b * sd.sdy.b + n * sd.sdy.n;
+            w.y[s] = static_cast<T *>(sd.y) + b * sd.sy.b + n * sd.sy.n;
+        }
+        w.pos = compute && p.half && w.ok ? position_of(p, b, n) : 0;
+        return w;
+    };
+    auto side_of = [&](int head) { return kBack ? side0 : (int)(head >= Hq); };
+    auto slot = [&](int depth, int src, int j, int half) {
+        return ring + (((depth * kSrc + src) * K + j) * 2 + half) * kThreads;
+    };
 
-        float cs[K][V], sn[K][V];
-        const long long pos = p.half && t_ok ? position_of(p, b, n) : 0;
+    // the copying side of the ring
+    long long f_unit = first;
+    int f_row = 0, f_depth = 0;
+    Where f = locate(f_unit, false);
+    auto fetch_row = [&]() {
+        const int head = f.head + f_row * head_step;
+        const bool ok = f.ok && head < heads;
+        const int s = kBack || ok ? side_of(head) : Hq == 0;  // a side with rows
+        const int h = ok ? head - (!kBack && s ? Hq : 0) : 0;
+        const Side &sd = p.side[s];
+        const T *x = (s ? f.x[1] : f.x[0]) + h * sd.sx.h;
+        const T *dy = (s ? f.dy[1] : f.dy[0]) + h * sd.sdy.h;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool l = ok && l_ok[j], hh = ok && h_ok[j];
+            if (!kBack || p.norm) {
+                fetch<T, V>(slot(f_depth, 0, j, 0), l ? x + lo[j] : x, l);
+                fetch<T, V>(slot(f_depth, 0, j, 1), hh ? x + hi[j] : x, hh);
+            }
+            if (kBack) {
+                fetch<T, V>(slot(f_depth, 1, j, 0), l ? dy + lo[j] : dy, l);
+                fetch<T, V>(slot(f_depth, 1, j, 1), hh ? dy + hi[j] : dy, hh);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        f_depth = f_depth + 1 == kDepth ? 0 : f_depth + 1;
+        if (++f_row == p.rows_per_unit) {
+            f_row = 0;
+            f_unit += stride;
+            f = locate(f_unit, false);
+        }
+    };
+    for (int i = 0; i < kDepth - 1; ++i) fetch_row();
+
+    // one vector pair of a slot as the pairs' first and second values
+    auto open = [&](const Pack<T, V> *l, const Pack<T, V> *h, float2 (&m0)[P], float2 (&m1)[P]) {
+        const Pack<T, V> a = *l, c = *h;
+        float e[2 * V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = to_f(a.v[i]), e[V + i] = to_f(c.v[i]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (V == 1) {
+                m0[0] = make_float2(e[0], 0.f);
+                m1[0] = make_float2(e[1], 0.f);
+            } else if (kInter) {
+                m0[i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
+                m1[i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
+            } else {
+                m0[i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
+                m1[i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
+            }
+        }
+    };
+
+    float2 w0[K][P], w1[K][P], dw0[K][P], dw1[K][P];
+    auto load_weights = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            float e[2 * V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                e[i] = l_ok[j] ? weight[s][lo[j] + i] : 0.f;
+                e[V + i] = h_ok[j] ? weight[s][hi[j] + i] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                if (V == 1) {
+                    w0[j][0] = make_float2(e[0], 0.f);
+                    w1[j][0] = make_float2(e[1], 0.f);
+                } else if (kInter) {
+                    w0[j][i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
+                    w1[j][i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
+                } else {
+                    w0[j][i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
+                    w1[j][i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
+                }
+            }
+        }
+    };
+    int w_side = side0;
+    load_weights(w_side);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
+
+    int depth = 0;
+    for (long long unit = first; unit < units; unit += stride) {
+        const Where at = locate(unit, true);
+        float2 cs[K][P], sn[K][P];
 #pragma unroll
         for (int j = 0; j < K; ++j)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int e = 0; e < 2 * P; ++e) {
                 const int i = (lane + (j << bits)) * V + e;
-                cs[j][e] = 1.f;
-                sn[j][e] = 0.f;
-                if (i < p.half) turn_of(pos, p.turns[i], &cs[j][e], &sn[j][e]);
+                float c = 1.f, s = 0.f;
+                if (e < V && i < p.half) turn_of<sizeof(T) == 4>(at.pos, turns[i], &c, &s);
+                (e % 2 ? cs[j][e / 2].y : cs[j][e / 2].x) = c;
+                (e % 2 ? sn[j][e / 2].y : sn[j][e / 2].x) = s;
             }
+        for (int row = 0; row < p.rows_per_unit; ++row) {
+            fetch_row();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            const int head = at.head + row * head_step, s = side_of(head);
+            const bool ok = at.ok && head < heads;
+            if (!kBack && s != w_side) load_weights(w_side = s);
+            const Side &sd = p.side[s];
+            T *y = (s ? at.y[1] : at.y[0]) + (head - (!kBack && s ? Hq : 0)) * sd.sy.h;
 
-        for (int h = h0 + head_in; h - head_in < h1; h += U * head_step) {
-            Pack<T, V> rx[U][K][2], rg[U][K][2];
-            bool ok[U];
+            float2 v0[K][P], v1[K][P], g0[K][P], g1[K][P], t[kSrc][K][P];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int hu = h + u * head_step;
-                ok[u] = t_ok && hu < h1;
-                if (!ok[u]) continue;
+            for (int j = 0; j < K; ++j) {
+                if (!kBack || p.norm) {
+                    open(slot(depth, 0, j, 0), slot(depth, 0, j, 1), v0[j], v1[j]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    if (!kBack || p.norm) {
-                        if (l_ok[j]) load<T, V>(rx[u][j][0], x + hu * sd.sx.h + lo[j]);
-                        if (h_ok[j]) load<T, V>(rx[u][j][1], x + hu * sd.sx.h + hi[j]);
-                    }
-                    if (kBack) {
-                        if (l_ok[j]) load<T, V>(rg[u][j][0], dy + hu * sd.sdy.h + lo[j]);
-                        if (h_ok[j]) load<T, V>(rg[u][j][1], dy + hu * sd.sdy.h + hi[j]);
-                    }
+                    for (int i = 0; i < P; ++i) v0[j][i] = v1[j][i] = make_float2(0.f, 0.f);
+                }
+                if (kBack) open(slot(depth, kSrc - 1, j, 0), slot(depth, kSrc - 1, j, 1), g0[j], g1[j]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    t[0][j][i] = __ffma2_rn(v0[j][i], v0[j][i], __fmul2_rn(v1[j][i], v1[j][i]));
+                    if (!kBack) continue;
+                    // turned back, then times the weight for dx
+                    const float2 a = g0[j][i], c = g1[j][i];
+                    const float2 ns = make_float2(-sn[j][i].x, -sn[j][i].y);
+                    g0[j][i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(c, sn[j][i]));
+                    g1[j][i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, ns));
+                    t[kSrc - 1][j][i] =
+                        __ffma2_rn(v0[j][i], __fmul2_rn(w0[j][i], g0[j][i]),
+                                   __fmul2_rn(v1[j][i], __fmul2_rn(w1[j][i], g1[j][i])));
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[K][2 * V], g[K][2 * V];
-                float ss[K][V], dot[K][V];
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const bool have = ok[u] && (!kBack || p.norm);
-                        v[j][e] = have && l_ok[j] ? to_f(rx[u][j][0].v[e]) : 0.f;
-                        v[j][V + e] = have && h_ok[j] ? to_f(rx[u][j][1].v[e]) : 0.f;
-                        if (kBack) {
-                            g[j][e] = ok[u] && l_ok[j] ? to_f(rg[u][j][0].v[e]) : 0.f;
-                            g[j][V + e] = ok[u] && h_ok[j] ? to_f(rg[u][j][1].v[e]) : 0.f;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
-                        ss[j][e] = fmaf(v[j][i0], v[j][i0], __fmul_rn(v[j][i1], v[j][i1]));
-                        if (kBack) {
-                            const float a = g[j][i0], c = g[j][i1];
-                            g[j][i0] = fmaf(a, cs[j][e], __fmul_rn(c, sn[j][e]));
-                            g[j][i1] = fmaf(c, cs[j][e], -__fmul_rn(a, sn[j][e]));
-                            dot[j][e] = fmaf(__fmul_rn(v[j][i0], w[j][i0]), g[j][i0],
-                                             __fmul_rn(__fmul_rn(v[j][i1], w[j][i1]), g[j][i1]));
-                        }
-                    }
-                }
-                float r = 1.f, m = 0.f;
-                if (p.norm) {
-                    r = rsqrtf(fmaf(row_sum<V, K>(ss, bits), p.inv_d, p.eps));
-                    if (kBack)
-                        m = __fmul_rn(__fmul_rn(row_sum<V, K>(dot, bits), p.inv_d),
-                                      __fmul_rn(r, r));
-                }
-                const int hu = h + u * head_step;
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    Pack<T, V> o[2];
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
-                        float o0, o1;
-                        if (!kBack) {
-                            const float a = __fmul_rn(__fmul_rn(v[j][i0], r), w[j][i0]);
-                            const float c = __fmul_rn(__fmul_rn(v[j][i1], r), w[j][i1]);
-                            o0 = fmaf(a, cs[j][e], -__fmul_rn(c, sn[j][e]));
-                            o1 = fmaf(c, cs[j][e], __fmul_rn(a, sn[j][e]));
-                        } else {
-                            dw[j][i0] = fmaf(g[j][i0], __fmul_rn(v[j][i0], r), dw[j][i0]);
-                            dw[j][i1] = fmaf(g[j][i1], __fmul_rn(v[j][i1], r), dw[j][i1]);
-                            o0 = __fmul_rn(r, fmaf(w[j][i0], g[j][i0], -__fmul_rn(v[j][i0], m)));
-                            o1 = __fmul_rn(r, fmaf(w[j][i1], g[j][i1], -__fmul_rn(v[j][i1], m)));
-                        }
-                        from_f(i0 < V ? o[0].v[i0 % V] : o[1].v[i0 % V], o0);
-                        from_f(i1 < V ? o[0].v[i1 % V] : o[1].v[i1 % V], o1);
-                    }
-                    if (ok[u] && l_ok[j]) store<T, V>(y + hu * sd.sy.h + lo[j], o[0]);
-                    if (ok[u] && h_ok[j]) store<T, V>(y + hu * sd.sy.h + hi[j], o[1]);
-                }
+            float r = 1.f, m = 0.f;
+            if (p.norm) {
+                float sum[kSrc];
+                row_sum<kSrc, K, P>(t, bits, sum);
+                r = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
+                // n w g summed is r sum(v w g)
+                if (kBack) m = __fmul_rn(__fmul_rn(sum[kSrc - 1], p.inv_d), r);
             }
+            const float2 r2 = make_float2(r, r), m2 = make_float2(-m, -m);
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                float2 o0[P], o1[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float2 n0 = __fmul2_rn(v0[j][i], r2), n1 = __fmul2_rn(v1[j][i], r2);
+                    if (!kBack) {
+                        const float2 a = __fmul2_rn(n0, w0[j][i]), c = __fmul2_rn(n1, w1[j][i]);
+                        const float2 ns = make_float2(-sn[j][i].x, -sn[j][i].y);
+                        o0[i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(c, ns));
+                        o1[i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
+                    } else {
+                        dw0[j][i] = __ffma2_rn(g0[j][i], n0, dw0[j][i]);
+                        dw1[j][i] = __ffma2_rn(g1[j][i], n1, dw1[j][i]);
+                        o0[i] = __fmul2_rn(
+                            r2, __ffma2_rn(n0, m2, __fmul2_rn(w0[j][i], g0[j][i])));
+                        o1[i] = __fmul2_rn(
+                            r2, __ffma2_rn(n1, m2, __fmul2_rn(w1[j][i], g1[j][i])));
+                    }
+                }
+                Pack<T, V> l, h;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float a = e % 2 ? o0[e / 2].y : o0[e / 2].x;
+                    const float c = e % 2 ? o1[e / 2].y : o1[e / 2].x;
+                    const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
+                    from_f(i0 < V ? l.v[i0 % V] : h.v[i0 % V], a);
+                    from_f(i1 < V ? l.v[i1 % V] : h.v[i1 % V], c);
+                }
+                if (ok && l_ok[j]) *reinterpret_cast<Pack<T, V> *>(y + lo[j]) = l;
+                if (ok && h_ok[j]) *reinterpret_cast<Pack<T, V> *>(y + hi[j]) = h;
+            }
+            depth = depth + 1 == kDepth ? 0 : depth + 1;
         }
-        unit += unit_step;
-    } while (kBack && unit < units);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 
-    if (!kBack || !sd.dw) return;
-    // the block's sums: over the groups of each warp, then over the warps
-    __shared__ float sum[kThreads / 32][LA_MAX_D];
+    if (!kBack || !p.partial) return;
+    // the block's sums: over the groups of each warp, then over the warps, in
+    // the ring's memory
+    __syncthreads();
+    float(*sum)[LA_MAX_D] = reinterpret_cast<float(*)[LA_MAX_D]>(smem);
     const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) {
-            float t = dw[j][e];
-            for (int o = 1 << bits; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
-            const int f = e < V ? lo[j] + e : hi[j] + e - V;
-            if ((threadIdx.x & 31) == lane && (e < V ? l_ok[j] : h_ok[j])) sum[warp][f] = t;
+        for (int e = 0; e < V; ++e) {
+            float a = e % 2 ? dw0[j][e / 2].y : dw0[j][e / 2].x;
+            float c = e % 2 ? dw1[j][e / 2].y : dw1[j][e / 2].x;
+            for (int o = 1 << bits; o < 32; o <<= 1) {
+                a += __shfl_xor_sync(~0u, a, o);
+                c += __shfl_xor_sync(~0u, c, o);
+            }
+            const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
+            const int f0 = i0 < V ? lo[j] + i0 : hi[j] + i0 - V;
+            const int f1 = i1 < V ? lo[j] + i1 : hi[j] + i1 - V;
+            if ((threadIdx.x & 31) == lane) {
+                if (i0 < V ? l_ok[j] : h_ok[j]) sum[warp][f0] = a;
+                if (i1 < V ? l_ok[j] : h_ok[j]) sum[warp][f1] = c;
+            }
         }
     __syncthreads();
     for (int i = threadIdx.x; i < p.d; i += kThreads) {
@@ -398,22 +536,26 @@ int vector_of(const Params &p, int most, int elem) {
 
 template <typename T, int V, int K, bool kBack>
 cudaError_t launch_rows(const Params &p, unsigned blocks, cudaStream_t stream) {
-    if (p.interleaved)
-        qk_rows_kernel<T, V, K, true, kBack><<<blocks, kThreads, 0, stream>>>(p);
-    else
-        qk_rows_kernel<T, V, K, false, kBack><<<blocks, kThreads, 0, stream>>>(p);
+    auto kern = p.interleaved ? qk_rows_kernel<T, V, K, true, kBack>
+                              : qk_rows_kernel<T, V, K, false, kBack>;
+    // the sums of the weight gradient, 8 rows of LA_MAX_D, share the ring
+    const int smem = std::max(ring_bytes<T, V, K, kBack>(), kThreads / 32 * LA_MAX_D * 4);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<blocks, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
+// Blocks that a weight gradient's partial sums come from, at most.
+long long back_blocks(int sms) { return 2LL * sms; }
+
 template <typename T, bool kBack>
-la_status launch(const char *who, Params &p, cudaStream_t stream) {
+la_status launch(const char *who, Params &p, void *workspace, size_t workspace_bytes,
+                 cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
     if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
-    // 16-byte accesses forward; backward 4 values, so that the sums, weights
-    // and angles of a lane leave room for enough warps
-    const int most = kBack ? 4 : 16 / (int)sizeof(T);
-    const int v = vector_of(p, most, (int)sizeof(T));
+    const int v = vector_of(p, 16 / (int)sizeof(T), (int)sizeof(T));
     const int chunks = ((p.d + 1) / 2 + v - 1) / v;  // of a row
     while ((1 << p.lane_bits) < chunks && p.lane_bits < 5) ++p.lane_bits;
     const int groups = kThreads >> p.lane_bits;
@@ -421,44 +563,50 @@ la_status launch(const char *who, Params &p, cudaStream_t stream) {
     while ((1 << p.token_bits) < groups && (1 << p.token_bits) < tokens) ++p.token_bits;
     const int head_step = groups >> p.token_bits;
     const long long tiles = (tokens + (1 << p.token_bits) - 1) >> p.token_bits;
-    // 8 heads per angle, fewer where that leaves SMs without work
-    long long units = 0;
-    for (int reuse = 8;; reuse /= 2) {
-        p.heads_per_unit = head_step * reuse;
-        units = 0;
+    const int heads[2] = {kBack ? p.side[0].H : p.side[0].H + p.side[1].H,
+                          kBack ? p.side[1].H : 0};
+    const long long most = kBack ? back_blocks(sms) : 3LL * sms;
+    // all heads per angle, fewer where that leaves too few units to share out
+    // evenly
+    long long units[2];
+    for (p.rows_per_unit = (std::max(heads[0], heads[1]) + head_step - 1) / head_step;;
+         p.rows_per_unit = (p.rows_per_unit + 1) / 2) {
         for (int i = 0; i < 2; ++i) {
-            p.chunks[i] = (p.side[i].H + p.heads_per_unit - 1) / p.heads_per_unit;
-            units += tiles * p.chunks[i];
+            const int per_unit = p.rows_per_unit * head_step;
+            p.chunks[i] = (heads[i] + per_unit - 1) / per_unit;
+            units[i] = tiles * p.chunks[i];
         }
-        if (reuse == 1 || units >= 4LL * sms) break;
+        if (p.rows_per_unit == 1 || units[0] + units[1] >= 6 * most) break;
     }
-    long long blocks = units;
+    // as many blocks as run at once; backward shared by the sides as their units
+    const long long all = units[0] + units[1];
+    long long blocks = std::min(all, most);
     if (kBack) {
-        // as many blocks as run at once, shared by the sides as their units
-        const long long most_blocks = 3LL * sms;
-        const long long uq = tiles * p.chunks[0], uk = tiles * p.chunks[1];
-        long long bq = uq, bk = uk;
-        if (units > most_blocks) {
-            bq = uq ? std::max(1LL, most_blocks * uq / units) : 0;
-            bk = uk ? std::max(1LL, most_blocks - bq) : 0;
+        long long bq = units[0], bk = units[1];
+        if (all > most) {
+            bq = bq ? std::max(1LL, std::min(most - (bk ? 1 : 0), most * bq / all)) : 0;
+            bk = bk ? most - bq : 0;
         }
         p.blocks_q = (int)bq;
         blocks = bq + bk;
     }
-    if (blocks > 2147483647LL) return qk_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     void *ws = nullptr;
     const bool want_dw = kBack && (p.side[0].dw || p.side[1].dw);
-    if (want_dw) {
-        e = tc_workspace_alloc(&ws, sizeof(float) * (size_t)blocks * p.d, stream);
+    const size_t need = sizeof(float) * (size_t)blocks * p.d;
+    if (want_dw && workspace) {
+        if (workspace_bytes < need || (uintptr_t)workspace % 16)
+            return qk_fail(LA_ERR_INVALID_ARG, who, "workspace too small or not 16-byte aligned");
+        p.partial = static_cast<float *>(workspace);
+    } else if (want_dw) {
+        e = tc_workspace_alloc(&ws, need, stream);
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
             return qk_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
         }
         p.partial = static_cast<float *>(ws);
     }
-    constexpr int kV16 = 16 / (int)sizeof(T);
-    if (!kBack && v == kV16 && kV16 == 8)
-        e = launch_rows<T, kBack ? 4 : kV16, 1, kBack>(p, (unsigned)blocks, stream);
+    if (v == 8)
+        e = launch_rows<T, sizeof(T) == 2 ? 8 : 4, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 4)
         e = launch_rows<T, 4, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 2)
@@ -585,8 +733,8 @@ la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out
     if (Hq && Hk && (q_out == k || k_out == q || q_out == k_out))
         return qk_fail(LA_ERR_INVALID_ARG, who, "an output aliases the other side");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == LA_F32 ? launch<float, false>(who, p, s)
-                           : launch<__nv_bfloat16, false>(who, p, s);
+    return dtype == LA_F32 ? launch<float, false>(who, p, nullptr, 0, s)
+                           : launch<__nv_bfloat16, false>(who, p, nullptr, 0, s);
 }
 
 __attribute__((visibility("default")))
@@ -595,8 +743,8 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
                                    float *dk_weight, const la_strides *strides,
                                    const void *q_weight, const void *k_weight, int norm,
                                    float eps, const la_rope *rope, int B, int Hq, int Hk, int N,
-                                   int d, la_dtype dtype, la_dtype weight_dtype,
-                                   la_stream_t stream) {
+                                   int d, la_dtype dtype, la_dtype weight_dtype, void *workspace,
+                                   size_t workspace_bytes, la_stream_t stream) {
     const char *who = "la_backward_qk_norm_rope";
     Params p;
     la_status st = qk_common(who, p, q_weight, k_weight, norm, eps, rope, B, Hq, Hk, N, d, dtype,
@@ -640,8 +788,16 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
             if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
         }
     if (B == 0 || N == 0 || Hq + Hk == 0) return LA_OK;
-    return dtype == LA_F32 ? launch<float, true>(who, p, s)
-                           : launch<__nv_bfloat16, true>(who, p, s);
+    return dtype == LA_F32 ? launch<float, true>(who, p, workspace, workspace_bytes, s)
+                           : launch<__nv_bfloat16, true>(who, p, workspace, workspace_bytes, s);
+}
+
+__attribute__((visibility("default")))
+size_t la_backward_qk_norm_rope_workspace_bytes(int d) {
+    if (d < 1 || d > LA_MAX_D) return 0;
+    int sms = 0;
+    if (tchost::sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
+    return sizeof(float) * (size_t)back_blocks(sms) * d;
 }
 
 }  // extern "C"

@@ -2,14 +2,15 @@
 
 Tolerances, with u = 2^-24 (half a step of fp32) and half = half a step of the
 output's type, relative:
-- forward: r = 1/sqrt(mean + eps) carries the rounding of a sum of at most 32
-  terms per lane and 5 lane steps (37 u, halved by the root), the division and
-  the square root (4 u); w n adds 2 u; cos and sin are off by at most 4 u (the
-  angle's conversion to fp32 is 1.6 u, the function 2 u); the products and
-  their sum 3 u.  That is below 40 u (|u1| + |u2|), plus half |y|.
-- dx: the turned-back gradient is off by 8 u (|dy1| + |dy2|) =: 8 u G; dx is
-  r (w g - n m) with m = mean(n w g) off by at most 64 u mean(|n| |w| G), so
-  64 u r (|w| G + |n| mean(|n| |w| G)), plus half |dx|.
+- forward: r = 1/sqrt(mean + eps) carries the rounding of a sum of at most 128
+  pairs as a binary tree (9 u, halved by the root), the mean and the root (4 u);
+  w n adds 2 u; cos and sin are off by at most 4 u for fp32 rows (the angle's
+  conversion to fp32 is 1.6 u, the function 2 u) and 12 u for bf16 ones (2^-21.2
+  of the special function unit); the products and their sum 3 u.  That is below
+  40 u (|u1| + |u2|), plus half |y|.
+- dx: the turned-back gradient is off by 16 u (|dy1| + |dy2|) =: 16 u G; dx is
+  r (w g - n m) with m = mean(n w g) off by at most 38 u mean(|n| |w| G), n by
+  10 u and r by 9 u, so 64 u r (|w| G + |n| mean(|n| |w| G)), plus half |dx|.
 - dw: a sum over rows whose longest chain of additions is the rows of one
   thread, the threads of a block and the blocks, below 1500 at these sizes:
   (1500 + 64) u sum(G |n|)."""
@@ -457,18 +458,25 @@ def test_other_stream_and_captured_graph():
     check_forward(y[0], q, wq, pos, freq, False)
 
 
-def test_workspace_failure_is_reported():
+def test_workspaces():
+    # the binding brings one on the current stream; on a stream given by the
+    # caller the library allocates, and reports a failure
     q = rows(1, 2, 9, 64, "f32", 141, "head")
     w = torch.ones(64, device="cuda")
     lib = la.load_library()
+    here = torch.cuda.current_stream()
+    ref = la.backward_qk_norm_rope(q, q, q, q.clone(), w, w)
+    got = la.backward_qk_norm_rope(q, q, q, q.clone(), w, w, stream=here)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
     assert lib.la_debug_fail_next_allocs(1) == 0
     try:
+        la.backward_qk_norm_rope(q, q, q, q.clone(), w, w)  # allocates nothing
         with pytest.raises(la.LinAttnError) as e:
-            la.backward_qk_norm_rope(q, q, q, q.clone(), w, w)
+            la.backward_qk_norm_rope(q, q, q, q.clone(), w, w, stream=here)
         assert e.value.status == 4
     finally:
         lib.la_debug_fail_next_allocs(0)
-    la.backward_qk_norm_rope(q, q, q, q.clone(), w, w)
 
 
 def test_offsets_past_32_bits():

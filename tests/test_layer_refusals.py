@@ -23,11 +23,19 @@ def strides(*v):
     return (ctypes.c_longlong * len(v))(*v)
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("frequencies", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("position_bytes", ctypes.c_int),
+                ("position_stride_b", ctypes.c_longlong),
+                ("position_stride_n", ctypes.c_longlong), ("offset", ctypes.c_longlong)]
+
+
 def rope(n=32, rotary=None, interleaved=0, positions=None, nbytes=8, sb=0, sn=0, freq=None,
          values=None):
     f = array.array("d", values if values is not None else [0.5] * n)
-    r = la._Rope(f.buffer_info()[0] if freq is None else freq, 2 * n if rotary is None else rotary,
-                 interleaved, positions, nbytes, sb, sn, 0)
+    r = Rope(f.buffer_info()[0] if freq is None else freq, 2 * n if rotary is None else rotary,
+             interleaved, positions, nbytes, sb, sn, 0)
     r.keep = f
     return r
 
@@ -89,9 +97,9 @@ def test_qk_norm_rope_empty_problems(lib):
 
 
 def back(lib, gq=P[0], gk=P[1], q=P[2], k=P[3], dq=P[4], dk=P[5], dwq=None, dwk=None, st=None,
-         norm=1, B=1, Hq=2, Hk=2, N=3, d=64):
+         norm=1, B=1, Hq=2, Hk=2, N=3, d=64, ws=None, ws_bytes=0):
     return lib.la_backward_qk_norm_rope(gq, gk, q, k, dq, dk, dwq, dwk, st, None, None, norm, 1e-6,
-                                        None, B, Hq, Hk, N, d, 1, 0, None)
+                                        None, B, Hq, Hk, N, d, 1, 0, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw, msg", [
@@ -206,6 +214,18 @@ def step(lib, h=P[0], ho=P[1], x=P[2], z=P[3], out=P[4], st=None, B=2, C=8, gate
 def test_decode_step_recurrence_refuses(lib, kw, msg):
     assert step(lib, **kw) == INVALID
     assert msg in lib.la_last_error().decode()
+
+
+def test_the_packed_rotation_is_the_struct():
+    assert la._ROPE.size == ctypes.sizeof(Rope)
+    packed = la._ROPE.pack(1, 2, True, 3, 4, 5, 6, 7)
+    assert packed == bytes(Rope(1, 2, 1, 3, 4, 5, 6, 7))
+
+
+def test_workspace_query(lib):
+    f = lib.la_backward_qk_norm_rope_workspace_bytes
+    assert f(0) == 0 and f(257) == 0
+    assert f(128) == 2 * f(64) > 0
 
 
 def test_rope_frequencies():
