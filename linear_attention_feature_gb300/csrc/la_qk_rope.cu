@@ -540,8 +540,11 @@ cudaError_t launch_rows(const Params &p, unsigned blocks, cudaStream_t stream) {
                               : qk_rows_kernel<T, V, K, false, kBack>;
     // the sums of the weight gradient, 8 rows of LA_MAX_D, share the ring
     const int smem = std::max(ring_bytes<T, V, K, kBack>(), kThreads / 32 * LA_MAX_D * 4);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 40 * 1024) {  // 48 KB with the static arrays need no attribute
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     kern<<<blocks, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }

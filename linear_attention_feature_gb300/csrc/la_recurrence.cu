@@ -18,10 +18,11 @@
 // walks its L tokens again from there and stores.
 //
 // Where there are fewer strips than the GPU holds blocks, a cluster of S blocks
-// shares a strip: a round is then S x 8 x L tokens, each block leaves its map in
-// the shared memory of the others, and one cluster barrier replaces the
-// sequence's serial chain.  Maps are joined in scan order, the same for every
-// alignment, so repeated calls are bit-identical.
+// shares a strip: a round is then S x 8 x L tokens, and each block sends its map
+// into the shared memory of the others (st.async, counted by an mbarrier there:
+// a cluster barrier's release would wait for the round's global stores as
+// well, which took half of the time).  Maps are joined in scan order, the same
+// for every alignment, so repeated calls are bit-identical.
 //
 // Rows that TMA cannot take (strides or bases that are not multiples of 16
 // bytes) are read by the threads themselves, each its own tokens and channels
@@ -200,15 +201,32 @@ constexpr int stage_bytes(int complement) {
            ((int)sizeof(G) + (int)sizeof(T) * (kBack ? 2 + complement : 1));
 }
 
-// Waits for a stage's copies, with a limit: afterwards the launch is marked as
-// failed in the status word and goes on without waiting.
-__device__ __forceinline__ void wait_stage(uint64_t *bar, unsigned parity, bool &dead, int *status) {
+// Waits for a stage's copies or the cluster's maps, with a limit: afterwards the
+// launch is marked as failed in the status word and goes on without waiting.
+__device__ __forceinline__ void wait_for(uint64_t *bar, unsigned parity, bool &dead, int *status) {
     if (dead || tc::mbar_try_wait(bar, parity)) return;
     if (!tc::mbar_wait(bar, parity, clock64() + kWaitCycles, nullptr)) {
         dead = true;
         if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
             atomicExch(status + 1, (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
     }
+}
+
+// A thread's part (A, H) of a block's map to the same place in the block `to` of
+// the cluster, counted on the barrier at `bar`'s place there.
+template <int V>
+__device__ __forceinline__ void send_map(float *place, uint64_t *bar, int to, const Vec<V> &A,
+                                         const Vec<V> &H) {
+    unsigned dst, mb;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(tc::smem_u32(place)), "r"(to));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(mb) : "r"(tc::smem_u32(bar)), "r"(to));
+    if constexpr (V == 2)
+        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
+                     "{%1, %2, %3, %4}, [%5];" ::"r"(dst), "f"(A.v[0]), "f"(A.v[1]), "f"(H.v[0]),
+                     "f"(H.v[1]), "r"(mb) : "memory");
+    else
+        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], "
+                     "{%1, %2}, [%3];" ::"r"(dst), "f"(A.v[0]), "f"(H.v[0]), "r"(mb) : "memory");
 }
 
 template <bool k>
@@ -223,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
     constexpr int kRow = 32 * V;
     extern __shared__ __align__(128) char stages[];
     __shared__ float warp_map[2][kWarps][2][kRow];
-    __shared__ float block_map[2][kMaxCluster][2][kRow];
-    __shared__ uint64_t full[kStages];
+    __shared__ __align__(16) float block_map[2][kMaxCluster][32][2 * V];  // (A, H) per lane
+    __shared__ uint64_t full[kStages], maps_in[2];
 
     const cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -289,13 +307,12 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    if (kTma) {
-        if (tid == 0) {
-            for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
-            tc::fence_mbar_init();
-        }
-        __syncthreads();
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&maps_in[i], 1);
+        tc::fence_mbar_init();
     }
+    __syncthreads();
     for (int r = 0; r < kStages; ++r) fetch(r);
 
     Vec<V> carry = all_v<V>(0.f), h0 = all_v<V>(0.f);
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
         const bool behind = s0 + L >= p.N;              // the sequence's end is in or before it
         const bool edge = behind || c0 + kRow > p.C;
         if (kTma)
-            wait_stage(&full[stage], (unsigned)(r / kStages) & 1u, dead, p.status);
+            wait_for(&full[stage], (unsigned)(r / kStages) & 1u, dead, p.status);
         else
             asm volatile("cp.async.wait_group %0;" ::"n"(kBack ? kStages - 2 : kStages - 1)
                          : "memory");
@@ -364,17 +381,16 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
             state = fma_v(A, carry, H);
             carry = fma_v(Ab, carry, Hb);
         } else {
-            if (warp < S) {
-                float *there = cluster.map_shared_rank(&block_map[par][rank][0][lane * V], warp);
-                *reinterpret_cast<Vec<V> *>(there) = Ab;
-                *reinterpret_cast<Vec<V> *>(there + kRow) = Hb;
-            }
-            cluster.sync();
+            // A block sends its map of round r + 2, to the same place, only
+            // after it has those of round r + 1, and this block's goes out after
+            // it has read round r's: two places are enough.
+            if (tid == 0) tc::mbar_arrive_expect_tx(&maps_in[par], S * 32 * 2 * V * 4);
+            if (warp < S) send_map<V>(block_map[par][rank][lane], &maps_in[par], warp, Ab, Hb);
+            wait_for(&maps_in[par], (unsigned)(r >> 1) & 1u, dead, p.status);
             for (int k = 0; k < S; ++k) {
                 if (k == rank) state = fma_v(A, carry, H);
-                carry = fma_v(*reinterpret_cast<const Vec<V> *>(&block_map[par][k][0][lane * V]),
-                              carry,
-                              *reinterpret_cast<const Vec<V> *>(&block_map[par][k][1][lane * V]));
+                const Vec<V> *m = reinterpret_cast<const Vec<V> *>(block_map[par][k][lane]);
+                carry = fma_v(m[0], carry, m[1]);
             }
         }
         // the L tokens again, from the state that reaches them
@@ -439,6 +455,10 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
         for (int r = max(0, rounds - kStages); r < rounds; ++r)
             tc::mbar_wait(&full[r % kStages], (unsigned)(r / kStages) & 1u,
                           clock64() + kWaitCycles, nullptr);
+    if (S > 1) {  // no block leaves while another may still send to it
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+    }
 }
 
 // One token: V adjacent channels per thread.
