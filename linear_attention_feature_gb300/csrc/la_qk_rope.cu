@@ -47,7 +47,7 @@ struct Params {
     float eps, inv_d;
     float *partial;  // backward: a row of d sums of g n for each block, or NULL
     // the split of the work, see qk_rows_kernel
-    int lane_bits, token_bits, rows_per_unit, chunks[2], blocks_q;
+    int lane_bits, token_bits, blocks_q;
     unsigned long long turns[kMaxPairs];  // frequency, 2^-64 turns per position
 };
 
@@ -157,21 +157,20 @@ constexpr int ring_bytes() {
 // the rest: both values of a pair are always in one thread and every access is
 // one vector.
 //
-// A block's groups of lanes are 2^token_bits tokens times as many heads as are
-// left.  A unit of work is such a tile of tokens and rows_per_unit rows (heads)
-// per group; a block walks the units blockIdx, blockIdx + blocks, ...  Forward,
-// the heads of q and k are one list; backward, a block keeps to one side, and
-// the sums of g n stay in its registers until its end.  Angles are formed once per
-// token and lane and serve all rows of the unit.  Rows travel through a ring in
-// shared memory, filled by cp.async some rows ahead; every thread reads only
-// what it copied itself, so the ring needs no barrier.
+// A block keeps to one side.  Its groups of lanes are a tile of 2^token_bits
+// tokens times as many heads as are left, so a tile is H / heads rows per group;
+// the rows of all tiles form one list, of which every block takes an equal piece.
+// Angles are formed once per token and lane and serve the tile's rows.  Rows
+// travel through a ring in shared memory, filled by cp.async some rows ahead;
+// every thread reads only what it copied itself, so the ring needs no barrier.
+// Backward, the sums of g n stay in registers until the block's end.
 template <typename T, int V, int K, bool kInter, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_constant__ Params p) {
     constexpr int P = (V + 1) / 2;  // packed pairs per chunk (V = 1: half of one)
     constexpr int kDepth = ring_depth<kBack>(), kSrc = kBack ? 2 : 1;
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long turns[kMaxPairs];
-    __shared__ float weight[2][LA_MAX_D];
+    __shared__ float weight[LA_MAX_D];
     Pack<T, V> *ring = reinterpret_cast<Pack<T, V> *>(smem) + threadIdx.x;
 
     const int bits = p.lane_bits, lane = threadIdx.x & ((1 << bits) - 1);
@@ -181,19 +180,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     const int pairs = (p.d + 1) / 2;
     const long long tokens = (long long)p.B * p.N;
 
-    const int side0 = kBack && (int)blockIdx.x >= p.blocks_q;
-    const int Hq = p.side[0].H;
-    const int heads = kBack ? p.side[side0].H : Hq + p.side[1].H;
-    const int chunks = p.chunks[side0];
-    const unsigned first = side0 ? blockIdx.x - p.blocks_q : blockIdx.x;
-    const unsigned stride = !kBack ? gridDim.x : side0 ? gridDim.x - p.blocks_q : p.blocks_q;
-    const long long units = ((tokens + (1 << p.token_bits) - 1) >> p.token_bits) * chunks;
+    const int which = (int)blockIdx.x >= p.blocks_q;
+    const Side &sd = p.side[which];
+    const int H = sd.H, rows = (H + head_step - 1) / head_step;  // per tile
+    const long long total = ((tokens + (1 << p.token_bits) - 1) >> p.token_bits) * rows;
+    const int blocks = which ? gridDim.x - p.blocks_q : p.blocks_q;
+    const int block = which ? blockIdx.x - p.blocks_q : blockIdx.x;
+    const long long it0 = total * block / blocks, it1 = total * (block + 1) / blocks;
 
-    for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) turns[i] = i < p.half ? p.turns[i] : 0;
-    for (int i = threadIdx.x; i < p.d; i += kThreads) {
-        weight[0][i] = weight_at(p.side[0].w, p.w_bf16, i);
-        weight[1][i] = weight_at(p.side[1].w, p.w_bf16, i);
-    }
+    for (int i = threadIdx.x; i < p.half; i += kThreads) turns[i] = p.turns[i];
+    for (int i = threadIdx.x; i < p.d; i += kThreads) weight[i] = weight_at(sd.w, p.w_bf16, i);
     __syncthreads();
 
     int lo[K], hi[K];  // this lane's features
@@ -208,70 +204,61 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         h_ok[j] = l_ok[j] && hi[j] < p.d;
     }
 
-    // Where a unit's rows of this group are.
-    struct Where {
-        const T *x[2], *dy[2];
-        T *y[2];
-        int head;  // the group's first
-        long long pos;
-        bool ok;
-    };
-    auto locate = [&](long long unit, bool compute) {
-        Where w;
-        const long long tile = unit / chunks;
+    // the batch entry and token of this group in a tile
+    auto locate = [&](long long tile, int &b, int &n) {
         const long long tok = (tile << p.token_bits) + tok_in;
-        w.head = (int)(unit - tile * chunks) * p.rows_per_unit * head_step + head_in;
-        w.ok = unit < units && tok < tokens;
-        const int b = !w.ok ? 0 : tokens <= 0x7fffffff ? (int)((unsigned)tok / (unsigned)p.N)
-                                                      : (int)(tok / p.N);
-        const int n = w.ok ? (int)(tok - (long long)b * p.N) : 0;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (kBack && s != side0) continue;
-            const Side &sd = p.side[s];
-            w.x[s] = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n;
-            w.dy[s] = static_cast<const T *>(sd.dy) + b * sd.sdy.b + n * sd.sdy.n;
-            w.y[s] = static_cast<T *>(sd.y) + b * sd.sy.b + n * sd.sy.n;
-        }
-        w.pos = compute && p.half && w.ok ? position_of(p, b, n) : 0;
-        return w;
+        const bool ok = tok < tokens;
+        b = !ok ? 0 : tokens <= 0x7fffffff ? (int)((unsigned)tok / (unsigned)p.N) : (int)(tok / p.N);
+        n = ok ? (int)(tok - (long long)b * p.N) : 0;
+        return ok;
     };
-    auto side_of = [&](int head) { return kBack ? side0 : (int)(head >= Hq); };
     auto slot = [&](int depth, int src, int j, int half) {
         return ring + (((depth * kSrc + src) * K + j) * 2 + half) * kThreads;
     };
 
     // the copying side of the ring
-    long long f_unit = first;
-    int f_row = 0, f_depth = 0;
-    Where f = locate(f_unit, false);
+    long long f_it = it0, f_tile = it0 / rows;
+    int f_row = (int)(it0 - f_tile * rows), f_depth = 0;
+    bool f_ok = false;
+    const T *fx = nullptr, *fg = nullptr;  // the next row
+    const long long fx_step = head_step * sd.sx.h, fg_step = head_step * sd.sdy.h;
+    auto f_enter = [&]() {
+        int b, n;
+        f_ok = locate(f_tile, b, n);
+        const int h = head_in + f_row * head_step;
+        if (!kBack || p.norm)
+            fx = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n + h * sd.sx.h;
+        if (kBack) fg = static_cast<const T *>(sd.dy) + b * sd.sdy.b + n * sd.sdy.n + h * sd.sdy.h;
+    };
+    f_enter();
     auto fetch_row = [&]() {
-        const int head = f.head + f_row * head_step;
-        const bool ok = f.ok && head < heads;
-        const int s = kBack || ok ? side_of(head) : Hq == 0;  // a side with rows
-        const int h = ok ? head - (!kBack && s ? Hq : 0) : 0;
-        const Side &sd = p.side[s];
-        const T *x = (s ? f.x[1] : f.x[0]) + h * sd.sx.h;
-        const T *dy = (s ? f.dy[1] : f.dy[0]) + h * sd.sdy.h;
+        if (f_it < it1) {
+            const bool ok = f_ok && head_in + f_row * head_step < H;
+            const T *x = ok ? fx : static_cast<const T *>(sd.x);
+            const T *g = ok ? fg : static_cast<const T *>(sd.dy);
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const bool l = ok && l_ok[j], hh = ok && h_ok[j];
-            if (!kBack || p.norm) {
-                fetch<T, V>(slot(f_depth, 0, j, 0), l ? x + lo[j] : x, l);
-                fetch<T, V>(slot(f_depth, 0, j, 1), hh ? x + hi[j] : x, hh);
+            for (int j = 0; j < K; ++j) {
+                const bool l = ok && l_ok[j], h = ok && h_ok[j];
+                if (!kBack || p.norm) {
+                    fetch<T, V>(slot(f_depth, 0, j, 0), l ? x + lo[j] : x, l);
+                    fetch<T, V>(slot(f_depth, 0, j, 1), h ? x + hi[j] : x, h);
+                }
+                if (kBack) {
+                    fetch<T, V>(slot(f_depth, kSrc - 1, j, 0), l ? g + lo[j] : g, l);
+                    fetch<T, V>(slot(f_depth, kSrc - 1, j, 1), h ? g + hi[j] : g, h);
+                }
             }
-            if (kBack) {
-                fetch<T, V>(slot(f_depth, 1, j, 0), l ? dy + lo[j] : dy, l);
-                fetch<T, V>(slot(f_depth, 1, j, 1), hh ? dy + hi[j] : dy, hh);
+            f_depth = f_depth + 1 == kDepth ? 0 : f_depth + 1;
+            ++f_it;
+            fx += fx_step;
+            fg += fg_step;
+            if (++f_row == rows) {
+                f_row = 0;
+                ++f_tile;
+                f_enter();
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        f_depth = f_depth + 1 == kDepth ? 0 : f_depth + 1;
-        if (++f_row == p.rows_per_unit) {
-            f_row = 0;
-            f_unit += stride;
-            f = locate(f_unit, false);
-        }
     };
     for (int i = 0; i < kDepth - 1; ++i) fetch_row();
 
@@ -297,40 +284,40 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     };
 
     float2 w0[K][P], w1[K][P], dw0[K][P], dw1[K][P];
-    auto load_weights = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            float e[2 * V];
+    for (int j = 0; j < K; ++j) {
+        float e[2 * V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                e[i] = l_ok[j] ? weight[s][lo[j] + i] : 0.f;
-                e[V + i] = h_ok[j] ? weight[s][hi[j] + i] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (V == 1) {
-                    w0[j][0] = make_float2(e[0], 0.f);
-                    w1[j][0] = make_float2(e[1], 0.f);
-                } else if (kInter) {
-                    w0[j][i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
-                    w1[j][i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
-                } else {
-                    w0[j][i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
-                    w1[j][i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
-                }
-            }
+        for (int i = 0; i < V; ++i) {
+            e[i] = l_ok[j] ? weight[lo[j] + i] : 0.f;
+            e[V + i] = h_ok[j] ? weight[hi[j] + i] : 0.f;
         }
-    };
-    int w_side = side0;
-    load_weights(w_side);
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-#pragma unroll
-        for (int i = 0; i < P; ++i) dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < P; ++i) {
+            if (V == 1) {
+                w0[j][0] = make_float2(e[0], 0.f);
+                w1[j][0] = make_float2(e[1], 0.f);
+            } else if (kInter) {
+                w0[j][i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
+                w1[j][i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
+            } else {
+                w0[j][i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
+                w1[j][i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
+            }
+            dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
+        }
+    }
 
     int depth = 0;
-    for (long long unit = first; unit < units; unit += stride) {
-        const Where at = locate(unit, true);
+    long long tile = it0 / rows;
+    int row = (int)(it0 - tile * rows);
+    const long long y_step = head_step * sd.sy.h;
+    for (long long it = it0; it < it1;) {
+        int b, n;
+        const bool t_ok = locate(tile, b, n);
+        T *y = static_cast<T *>(sd.y) + b * sd.sy.b + n * sd.sy.n +
+               (head_in + row * head_step) * sd.sy.h;
+        const long long pos = p.half && t_ok ? position_of(p, b, n) : 0;
         float2 cs[K][P], sn[K][P];
 #pragma unroll
         for (int j = 0; j < K; ++j)
@@ -338,18 +325,14 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             for (int e = 0; e < 2 * P; ++e) {
                 const int i = (lane + (j << bits)) * V + e;
                 float c = 1.f, s = 0.f;
-                if (e < V && i < p.half) turn_of<sizeof(T) == 4>(at.pos, turns[i], &c, &s);
+                if (e < V && i < p.half) turn_of<sizeof(T) == 4>(pos, turns[i], &c, &s);
                 (e % 2 ? cs[j][e / 2].y : cs[j][e / 2].x) = c;
                 (e % 2 ? sn[j][e / 2].y : sn[j][e / 2].x) = s;
             }
-        for (int row = 0; row < p.rows_per_unit; ++row) {
+        for (; row < rows && it < it1; ++row, ++it, y += y_step) {
             fetch_row();
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-            const int head = at.head + row * head_step, s = side_of(head);
-            const bool ok = at.ok && head < heads;
-            if (!kBack && s != w_side) load_weights(w_side = s);
-            const Side &sd = p.side[s];
-            T *y = (s ? at.y[1] : at.y[0]) + (head - (!kBack && s ? Hq : 0)) * sd.sy.h;
+            const bool ok = t_ok && head_in + row * head_step < H;
 
             float2 v0[K][P], v1[K][P], g0[K][P], g1[K][P], t[kSrc][K][P];
 #pragma unroll
@@ -367,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                     if (!kBack) continue;
                     // turned back, then times the weight for dx
                     const float2 a = g0[j][i], c = g1[j][i];
-                    const float2 ns = make_float2(-sn[j][i].x, -sn[j][i].y);
+                    const float2 as = __fmul2_rn(a, sn[j][i]);
                     g0[j][i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(c, sn[j][i]));
-                    g1[j][i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, ns));
+                    g1[j][i] = make_float2(fmaf(c.x, cs[j][i].x, -as.x),
+                                           fmaf(c.y, cs[j][i].y, -as.y));
                     t[kSrc - 1][j][i] =
                         __ffma2_rn(v0[j][i], __fmul2_rn(w0[j][i], g0[j][i]),
                                    __fmul2_rn(v1[j][i], __fmul2_rn(w1[j][i], g1[j][i])));
@@ -392,8 +376,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                     const float2 n0 = __fmul2_rn(v0[j][i], r2), n1 = __fmul2_rn(v1[j][i], r2);
                     if (!kBack) {
                         const float2 a = __fmul2_rn(n0, w0[j][i]), c = __fmul2_rn(n1, w1[j][i]);
-                        const float2 ns = make_float2(-sn[j][i].x, -sn[j][i].y);
-                        o0[i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(c, ns));
+                        const float2 cn = __fmul2_rn(c, sn[j][i]);
+                        o0[i] = make_float2(fmaf(a.x, cs[j][i].x, -cn.x),
+                                            fmaf(a.y, cs[j][i].y, -cn.y));
                         o1[i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
                     } else {
                         dw0[j][i] = __ffma2_rn(g0[j][i], n0, dw0[j][i]);
@@ -418,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             }
             depth = depth + 1 == kDepth ? 0 : depth + 1;
         }
+        row = 0;
+        ++tile;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
@@ -549,8 +536,8 @@ cudaError_t launch_rows(const Params &p, unsigned blocks, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Blocks that a weight gradient's partial sums come from, at most.
-long long back_blocks(int sms) { return 2LL * sms; }
+// Blocks of one call at most: two run on an SM at once.
+long long resident_blocks(int sms) { return 2LL * sms; }
 
 template <typename T, bool kBack>
 la_status launch(const char *who, Params &p, void *workspace, size_t workspace_bytes,
@@ -566,33 +553,18 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     while ((1 << p.token_bits) < groups && (1 << p.token_bits) < tokens) ++p.token_bits;
     const int head_step = groups >> p.token_bits;
     const long long tiles = (tokens + (1 << p.token_bits) - 1) >> p.token_bits;
-    const int heads[2] = {kBack ? p.side[0].H : p.side[0].H + p.side[1].H,
-                          kBack ? p.side[1].H : 0};
-    const long long most = kBack ? back_blocks(sms) : 3LL * sms;
-    // all heads per angle, fewer where that leaves too few units to share out
-    // evenly
-    long long units[2];
-    for (p.rows_per_unit = (std::max(heads[0], heads[1]) + head_step - 1) / head_step;;
-         p.rows_per_unit = (p.rows_per_unit + 1) / 2) {
-        for (int i = 0; i < 2; ++i) {
-            const int per_unit = p.rows_per_unit * head_step;
-            p.chunks[i] = (heads[i] + per_unit - 1) / per_unit;
-            units[i] = tiles * p.chunks[i];
-        }
-        if (p.rows_per_unit == 1 || units[0] + units[1] >= 6 * most) break;
+    // as many blocks as run at once, shared by the sides as their rows
+    const long long most = resident_blocks(sms);
+    long long total[2];
+    for (int i = 0; i < 2; ++i) total[i] = tiles * ((p.side[i].H + head_step - 1) / head_step);
+    long long bq = total[0], bk = total[1];
+    if (bq + bk > most) {
+        const double share = (double)total[0] / (double)(total[0] + total[1]);
+        bq = bq ? std::max(1LL, std::min(most - (bk ? 1 : 0), std::llround(share * most))) : 0;
+        bk = bk ? most - bq : 0;
     }
-    // as many blocks as run at once; backward shared by the sides as their units
-    const long long all = units[0] + units[1];
-    long long blocks = std::min(all, most);
-    if (kBack) {
-        long long bq = units[0], bk = units[1];
-        if (all > most) {
-            bq = bq ? std::max(1LL, std::min(most - (bk ? 1 : 0), most * bq / all)) : 0;
-            bk = bk ? most - bq : 0;
-        }
-        p.blocks_q = (int)bq;
-        blocks = bq + bk;
-    }
+    p.blocks_q = (int)bq;
+    const long long blocks = bq + bk;
     void *ws = nullptr;
     const bool want_dw = kBack && (p.side[0].dw || p.side[1].dw);
     const size_t need = sizeof(float) * (size_t)blocks * p.d;
@@ -800,7 +772,7 @@ size_t la_backward_qk_norm_rope_workspace_bytes(int d) {
     if (d < 1 || d > LA_MAX_D) return 0;
     int sms = 0;
     if (tchost::sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
-    return sizeof(float) * (size_t)back_blocks(sms) * d;
+    return sizeof(float) * (size_t)resident_blocks(sms) * d;
 }
 
 }  // extern "C"

@@ -43,7 +43,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 3;  // rounds of copies in flight
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait for a copy, about 2 s
 
 // V channels of one thread; two go through the packed fp32 instructions, which
@@ -131,11 +131,11 @@ template <int kGate, int V>
 __device__ __forceinline__ void gate_of(Vec<V> z, bool need_rest, Vec<V> &a, Vec<V> &rest) {
     if (kGate == LA_GATE_VALUE) {
         a = z;
-        rest = add_v(all_v<V>(1.f), neg_v(z));
+        rest = fma_v(z, all_v<V>(-1.f), all_v<V>(1.f));
     } else if (kGate == LA_GATE_LOG) {
 #pragma unroll
         for (int e = 0; e < V; ++e) a.v[e] = expf(z.v[e]);
-        rest = add_v(all_v<V>(1.f), neg_v(a));
+        rest = fma_v(a, all_v<V>(-1.f), all_v<V>(1.f));
         if (need_rest) {
             // 1 - e^z = -z (1 + z/2 (1 + z/3 (...))) near 0, to 2^-24 for |z| <= 1/4
             Vec<V> s = fma_v(z, all_v<V>(1.f / 720.f), all_v<V>(1.f / 120.f));
@@ -162,7 +162,7 @@ __device__ __forceinline__ void gate_of(Vec<V> z, bool need_rest, Vec<V> &a, Vec
         const Vec<V> tr = mul_v(t, r);
 #pragma unroll
         for (int e = 0; e < V; ++e) small.v[e] = z.v[e] < 0.f ? r.v[e] : tr.v[e];
-        const Vec<V> other = add_v(all_v<V>(1.f), neg_v(small));
+        const Vec<V> other = fma_v(small, all_v<V>(-1.f), all_v<V>(1.f));
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             a.v[e] = z.v[e] < 0.f ? small.v[e] : other.v[e];
@@ -241,17 +241,23 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
     constexpr int kRow = 32 * V;
     extern __shared__ __align__(128) char stages[];
     __shared__ float warp_map[2][kWarps][2][kRow];
-    __shared__ __align__(16) float block_map[2][kMaxCluster][32][2 * V];  // (A, H) per lane
     __shared__ uint64_t full[kStages], maps_in[2];
 
     const cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // the same in all lanes, so that row addresses are formed once per warp
+    const int warp = __shfl_sync(~0u, tid >> 5, 0);
     const int strip = (int)(blockIdx.x / S) % p.strips, b = (int)(blockIdx.x / S) / p.strips;
     const int c0 = strip * kRow, c = c0 + lane * V;  // first channel
     const int here = min(max(p.C - c, 0), V);        // channels that exist
     const int rounds = (int)(((long long)p.N + (long long)S * kTile - 1) / ((long long)S * kTile));
     const int bytes = stage_bytes<T, G, V, L, kBack>(p.complement);
+
+    // the cluster's maps, behind the stages: [2][S][32] of (A, H) per lane
+    auto block_map = [&](int par, int k) {
+        return reinterpret_cast<float *>(stages + kStages * bytes) + ((par * S + k) * 32 + lane) * 2 * V;
+    };
 
     // A tile holds the tokens from `low` up; step j of the block in scan order
     // is its row j, or from the other end backwards.
@@ -366,30 +372,38 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
         // round before is done with its tiles
         if (!kBack) fetch(r + kStages);
         if (kBack && r > 0) fetch(r - 1 + kStages);
-        // the map of the warps before this one, and of the whole block
-        Vec<V> Ab = all_v<V>(1.f), Hb = all_v<V>(0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) A = Ab, H = Hb;
-            const Vec<V> Aw = *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][0][lane * V]);
-            const Vec<V> Hw = *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][1][lane * V]);
-            Hb = fma_v(Aw, Hb, Hw);
+        // the map of the warps before this one; the last warp joins its own to it
+        // for the map of the whole block
+        auto map_of = [&](int w, int which) {
+            return *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][which][lane * V]);
+        };
+        Vec<V> Ab = all_v<V>(1.f), Hb = all_v<V>(0.f), state = all_v<V>(0.f);
+        for (int w = 0; w < warp; ++w) {
+            const Vec<V> Aw = map_of(w, 0);
+            Hb = fma_v(Aw, Hb, map_of(w, 1));
             Ab = mul_v(Ab, Aw);
         }
-        Vec<V> state = all_v<V>(0.f);
         if (S == 1) {
-            state = fma_v(A, carry, H);
+            state = fma_v(Ab, carry, Hb);
+            for (int w = warp; w < kWarps; ++w) {
+                const Vec<V> Aw = map_of(w, 0);
+                Hb = fma_v(Aw, Hb, map_of(w, 1));
+                Ab = mul_v(Ab, Aw);
+            }
             carry = fma_v(Ab, carry, Hb);
         } else {
             // A block sends its map of round r + 2, to the same place, only
             // after it has those of round r + 1, and this block's goes out after
             // it has read round r's: two places are enough.
             if (tid == 0) tc::mbar_arrive_expect_tx(&maps_in[par], S * 32 * 2 * V * 4);
-            if (warp < S) send_map<V>(block_map[par][rank][lane], &maps_in[par], warp, Ab, Hb);
+            if (warp == kWarps - 1) {
+                const Vec<V> At = mul_v(Ab, A), Ht = fma_v(A, Hb, H);
+                for (int k = 0; k < S; ++k) send_map<V>(block_map(par, rank), &maps_in[par], k, At, Ht);
+            }
             wait_for(&maps_in[par], (unsigned)(r >> 1) & 1u, dead, p.status);
             for (int k = 0; k < S; ++k) {
-                if (k == rank) state = fma_v(A, carry, H);
-                const Vec<V> *m = reinterpret_cast<const Vec<V> *>(block_map[par][k][lane]);
+                if (k == rank) state = fma_v(Ab, carry, Hb);
+                const Vec<V> *m = reinterpret_cast<const Vec<V> *>(block_map(par, k));
                 carry = fma_v(m[0], carry, m[1]);
             }
         }
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
                 if (at_edge.value && !ok) g = all_v<V>(0.f);
                 if (at_edge.value && s0 + i == p.N - 1) h = h0;
                 g = add_v(g, state);
-                if (p.complement) h = add_v(h, neg_v(tile(2)));
+                if (p.complement) h = fma_v(tile(2), all_v<V>(-1.f), h);
                 if (ok) {
                     put(o, p.complement ? mul_v(y[i], g) : g);
                     Vec<V> dz = mul_v(g, h);
@@ -580,11 +594,8 @@ cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
                 return cudaErrorInvalidValue;
     auto kern = tma ? rec_scan_kernel<T, G, V, L, kGate, true, kBack>
                     : rec_scan_kernel<T, G, V, L, kGate, false, kBack>;
-    const size_t smem = (size_t)kStages * stage_bytes<T, G, V, L, kBack>(p.complement);
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) p.status = device_status_word(&e);
     if (e != cudaSuccess) return e;
     p.strips = (p.C + 32 * V - 1) / (32 * V);
@@ -595,6 +606,12 @@ cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
     while (S < kMaxCluster && strips * S * 2 <= 2LL * sms && (long long)S * kWarps * L < p.N)
         S *= 2;
     if (strips * S > 2147483647LL) return cudaErrorInvalidConfiguration;
+    const size_t smem = (size_t)kStages * stage_bytes<T, G, V, L, kBack>(p.complement) +
+                        (S > 1 ? (size_t)2 * S * 32 * 2 * V * sizeof(float) : 0);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && S > 8)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(strips * S));
     cfg.blockDim = dim3(kThreads);
