@@ -9,20 +9,23 @@
 //   state <- a state + y   (forward),   state <- a (state + y)   (backward),
 // walked in scan order: tokens ascending, or descending for the gradient.
 //
-// The data is read once.  A block of 8 warps takes a strip of 32 lanes x V
-// channels (one 128-byte row per token) and walks the sequence in rounds of
-// 8 x L tokens, L consecutive ones per warp.  TMA brings a round's tiles into
-// shared memory, three rounds deep.  Each thread forms the affine map (A, H) of
-// its L tokens in registers, and one block barrier later applies the maps of
-// the warps before it to the state that the block carries from round to round,
-// walks its L tokens again from there and stores.
+// The data is read once.  A block takes a strip of 32 lanes x V channels (one
+// 128-byte row per token) and walks the sequence in rounds of 8 x L tokens, L
+// consecutive ones per warp.  TMA brings a round's tiles into shared memory some
+// rounds ahead.  Each thread forms the affine map (A, H) of its L tokens in
+// registers, the warps leave theirs in shared memory, and each applies those
+// before it to the state that reaches the round, walks its L tokens again from
+// there and stores.
 //
-// Where there are fewer strips than the GPU holds blocks, a cluster of S blocks
-// shares a strip: a round is then S x 8 x L tokens, and each block sends its map
-// into the shared memory of the others (st.async, counted by an mbarrier there:
-// a cluster barrier's release would wait for the round's global stores as
-// well, which took half of the time).  Maps are joined in scan order, the same
-// for every alignment, so repeated calls are bit-identical.
+// Two groups of 8 warps take the rounds in turn: while one waits for the state
+// that reaches its round, the other works.  The last warp of a group joins the
+// maps and hands the state behind its round to the other group.  Where there are
+// fewer strips than SMs, a cluster of S blocks shares a strip: a round is then
+// S x 8 x L tokens, and each block sends its map into the shared memory of all
+// (st.async, counted by an mbarrier there: a cluster barrier's release would
+// wait for the round's global stores as well, which took half of the time).
+// Maps are applied in scan order, so repeated calls are bit-identical.  The grid
+// is as many clusters as run at once; each takes strip after strip.
 //
 // Rows that TMA cannot take (strides or bases that are not multiples of 16
 // bytes) are read by the threads themselves, each its own tokens and channels
@@ -31,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 
 #include "la_internal.h"
@@ -40,10 +44,15 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;  // rounds of copies in flight
+constexpr int kThreads = 512;
+constexpr int kWarps = 8;        // of a group
+constexpr int kMaxStages = 6;    // rounds of copies in flight, an even number
+constexpr int kSlots = 4;        // rounds of maps and states kept
 constexpr int kMaxCluster = 16;
+constexpr int kMaxPieces = 64;
+constexpr int kStepThreads = 256;
+constexpr size_t kSmem = 208 * 1024;  // stages and maps; 227 KB with the static arrays
+
 constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait for a copy, about 2 s
 
 // V channels of one thread; two go through the packed fp32 instructions, which
@@ -190,7 +199,12 @@ struct Params {
     float *last;         // h_last; backward dh0
     const float *h0;     // backward: h_0, for the first token's gate
     int *status;
-    int B, N, C, complement, strips;
+    int B, N, C, complement, strips, stages;
+    // A sequence in more than one piece of `steps` tokens (in scan order): a
+    // launch with maps_only leaves the map of every piece but the last in
+    // `maps`, [piece][B][C] of (A, H); the next one starts each piece from them.
+    int pieces, steps, maps_only;
+    float2 *maps;
 };
 
 // Bytes of one stage: a tile [kWarps L][32 V] of the gates, then of each other
@@ -234,67 +248,97 @@ struct Flag {
     static constexpr bool value = k;
 };
 
-template <typename T, typename G, int V, int L, int kGate, bool kTma, bool kBack>
-__global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_constant__ Params p) {
+// kComp: the input's factor is 1 (0), 1 - a (1) or as p.complement says (2).
+template <typename T, typename G, int V, int L, int kGate, int kComp, bool kTma, bool kBack>
+__global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_constant__ Params p) {
     namespace cg = cooperative_groups;
     constexpr int kTile = kWarps * L;  // tokens per block and round
     constexpr int kRow = 32 * V;
     extern __shared__ __align__(128) char stages[];
-    __shared__ float warp_map[2][kWarps][2][kRow];
-    __shared__ uint64_t full[kStages], maps_in[2];
+    __shared__ __align__(16) float warp_maps[2][2][kWarps][32][2 * V];  // (A, H) per lane
+    __shared__ __align__(16) float states[kSlots][32][2 * V];  // (state, product of gates)
+    __shared__ uint64_t full[kMaxStages], maps_in[kSlots], state_in[kSlots];
+    const bool complement = kComp == 2 ? p.complement != 0 : kComp != 0;
 
     const cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x & 255, lane = threadIdx.x & 31;
     // the same in all lanes, so that row addresses are formed once per warp
+    const int group = __shfl_sync(~0u, threadIdx.x >> 8, 0);
     const int warp = __shfl_sync(~0u, tid >> 5, 0);
-    const int strip = (int)(blockIdx.x / S) % p.strips, b = (int)(blockIdx.x / S) / p.strips;
-    const int c0 = strip * kRow, c = c0 + lane * V;  // first channel
-    const int here = min(max(p.C - c, 0), V);        // channels that exist
-    const int rounds = (int)(((long long)p.N + (long long)S * kTile - 1) / ((long long)S * kTile));
-    const int bytes = stage_bytes<T, G, V, L, kBack>(p.complement);
+    const int bytes = stage_bytes<T, G, V, L, kBack>(complement);
+    const int round_steps = S * kTile;
+    const int rounds = (int)(((long long)p.steps + round_steps - 1) / round_steps);  // of a piece
+    const int items = p.B * p.strips * (p.pieces - p.maps_only);
+    const int cid = blockIdx.x / S, clusters = gridDim.x / S;
+    const int total = cid < items ? ((items - cid - 1) / clusters + 1) * rounds : 0;
 
-    // the cluster's maps, behind the stages: [2][S][32] of (A, H) per lane
-    auto block_map = [&](int par, int k) {
-        return reinterpret_cast<float *>(stages + kStages * bytes) + ((par * S + k) * 32 + lane) * 2 * V;
+    // the cluster's maps, behind the stages: [kSlots][S][32] of (A, H) per lane
+    auto block_map = [&](int slot, int k) {
+        return reinterpret_cast<float *>(stages + p.stages * bytes) +
+               ((slot * S + k) * 32 + lane) * 2 * V;
     };
 
-    // A tile holds the tokens from `low` up; step j of the block in scan order
-    // is its row j, or from the other end backwards.
-    auto first_step = [&](int r) { return ((long long)r * S + rank) * kTile; };
-    auto low = [&](int r) { return kBack ? p.N - first_step(r) - kTile : first_step(r); };
+    // Item k of this cluster: a piece of a strip of a sequence.  A tile holds
+    // the tokens from `low` up; step j of the block in scan order is its row j,
+    // or from the other end backwards.
+    struct Item {
+        int b, c0, piece;
+        long long begin;  // first step in scan order
+        int end;          // the step after the last
+    };
+    auto item = [&](int k) {
+        Item it;
+        int i = cid + k * clusters;
+        it.c0 = i % p.strips * kRow;
+        i /= p.strips;
+        it.b = i % p.B;
+        it.piece = i / p.B;
+        it.begin = (long long)it.piece * p.steps;
+        it.end = (int)min(it.begin + p.steps, (long long)p.N);
+        return it;
+    };
+    auto first_step = [&](const Item &it, int r) {
+        return it.begin + (long long)r * round_steps + rank * kTile;
+    };
     auto row = [&](int i) { return kBack ? kTile - 1 - (warp * L + i) : warp * L + i; };
     auto tile_z = [&](int stage) { return reinterpret_cast<G *>(stages + stage * bytes); };
     auto tile_x = [&](int stage, int which) {
         return reinterpret_cast<T *>(stages + stage * bytes + kTile * kRow * (int)sizeof(G)) +
                which * kTile * kRow;
     };
-    auto fetch = [&](int r) {
-        const int stage = r % kStages;
+    // round R of the cluster into a stage; called by the threads of one group
+    auto fetch = [&](int R, int stage) {
+        if (kTma && (tid != 0 || R >= total)) return;
+        const Item it = item(R < total ? R / rounds : 0);
+        const long long s0 = first_step(it, R % rounds);
+        const long long low = kBack ? p.N - s0 - kTile : s0;
+        const bool all = kBack && !p.maps_only;
         if (kTma) {
-            if (tid != 0 || r >= rounds) return;
-            const int t = (int)low(r);
+            const int t = (int)low;
             const uint64_t policy = tc::policy_evict_first();
-            tc::mbar_arrive_expect_tx(&full[stage], bytes);
-            tc::tma_load_3d(tile_z(stage), &p.map[1], &full[stage], c0, t, b, policy);
-            tc::tma_load_3d(tile_x(stage, 0), &p.map[0], &full[stage], c0, t, b, policy);
-            if (kBack) {
-                tc::tma_load_3d(tile_x(stage, 1), &p.map[2], &full[stage], c0, t - 1, b, policy);
-                if (p.complement)
-                    tc::tma_load_3d(tile_x(stage, 2), &p.map[3], &full[stage], c0, t, b, policy);
+            tc::mbar_arrive_expect_tx(
+                &full[stage], all ? bytes : kTile * kRow * (int)(sizeof(G) + sizeof(T)));
+            tc::tma_load_3d(tile_z(stage), &p.map[1], &full[stage], it.c0, t, it.b, policy);
+            tc::tma_load_3d(tile_x(stage, 0), &p.map[0], &full[stage], it.c0, t, it.b, policy);
+            if (all) {
+                tc::tma_load_3d(tile_x(stage, 1), &p.map[2], &full[stage], it.c0, t - 1, it.b, policy);
+                if (complement)
+                    tc::tma_load_3d(tile_x(stage, 2), &p.map[3], &full[stage], it.c0, t, it.b, policy);
             }
             return;
         }
+        const int c = it.c0 + lane * V;
         auto mine = [&](auto *tile, const Seq &q, int shift) {
             using E = std::remove_reference_t<decltype(*tile)>;
-            const E *src = static_cast<const E *>(q.p) + b * q.b + c;
+            const E *src = static_cast<const E *>(q.p) + it.b * q.b + c;
             for (int i = 0; i < L; ++i) {
-                const long long t = low(r) + row(i) - shift;
-                const bool ok = r < rounds && t >= 0 && t < p.N;
+                const long long t = low + row(i) - shift;
+                const bool ok = R < total && t >= 0 && t < p.N;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     E *dst = tile + row(i) * kRow + lane * V + e;
-                    if (!ok || e >= here)
+                    if (!ok || c + e >= p.C)
                         *dst = E(0.f);
                     else if (sizeof(E) == 4)
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
@@ -306,41 +350,75 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
         };
         mine(tile_z(stage), p.in[1], 0);
         mine(tile_x(stage, 0), p.in[0], 0);
-        if (kBack) {
+        if (all) {
             mine(tile_x(stage, 1), p.in[2], 1);
-            if (p.complement) mine(tile_x(stage, 2), p.in[3], 0);
+            if (complement) mine(tile_x(stage, 2), p.in[3], 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&maps_in[i], 1);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) tc::mbar_init(&full[i], 1);
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&maps_in[i], 1);
+            tc::mbar_init(&state_in[i], 32);
+        }
         tc::fence_mbar_init();
     }
     __syncthreads();
-    for (int r = 0; r < kStages; ++r) fetch(r);
-
-    Vec<V> carry = all_v<V>(0.f), h0 = all_v<V>(0.f);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const long long at = (long long)b * p.C + c + e;
-        if (p.first && e < here) carry.v[e] = p.first[at];
-        if (kBack && p.h0 && e < here) h0.v[e] = p.h0[at];
-    }
-    bool dead = false;
+    for (int i = group; i < p.stages; i += 2) fetch(i, i);
+    // round 0 has no state to wait for, but a phase like every other's
+    if (threadIdx.x < 32) tc::mbar_arrive(&state_in[0]);
     // the others' shared memory is written from here on
     if (S > 1) cluster.sync();
-    for (int r = 0; r < rounds; ++r) {
-        const int stage = r % kStages, par = r & 1;
-        const long long s0 = first_step(r) + warp * L;  // this thread's first step
-        const bool behind = s0 + L >= p.N;              // the sequence's end is in or before it
-        const bool edge = behind || c0 + kRow > p.C;
+
+    bool dead = false;
+    // ring positions of this group's round R, and the parities of their phases
+    int stage = group, stage_phase = 0, slot = group, slot_phase = 0, turn = 0;
+    int k = group / rounds, r = group % rounds;  // item and round of it
+    Item it = item(0);
+    int c = 0, here = 0;
+    bool part = false;  // the strip reaches beyond C
+    long long s0 = 0;   // this thread's first step
+    T *o = nullptr;     // its first token in the outputs
+    G *oz = nullptr;
+    const long long o_turn = (kBack ? -2LL : 2LL) * round_steps * p.out[0].n;
+    const long long oz_turn = -2LL * round_steps * p.out[1].n;
+    for (int R = group; R < total; R += 2) {
+        if (r <= 1 || turn == 0) {
+            it = item(k);
+            c = it.c0 + lane * V;
+            here = min(max(p.C - c, 0), V);
+            part = it.c0 + kRow > p.C;
+            s0 = first_step(it, r) + warp * L;
+            const long long t0 = kBack ? p.N - 1 - s0 : s0;
+            o = static_cast<T *>(p.out[0].p) + it.b * p.out[0].b + t0 * p.out[0].n + c;
+            if (kBack) oz = static_cast<G *>(p.out[1].p) + it.b * p.out[1].b + t0 * p.out[1].n + c;
+        }
+        const bool edge = s0 + L >= it.end || part;  // masks are needed
+        Vec<V> init = all_v<V>(0.f), h0 = all_v<V>(0.f);
+        if (r == 0 && !p.maps_only) {  // the state before the item's first token
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (p.first && e < here) init.v[e] = p.first[(long long)it.b * p.C + c + e];
+            for (int q = 0; q < it.piece; ++q)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (e < here) {
+                        const float2 m = p.maps[((long long)q * p.B + it.b) * p.C + c + e];
+                        init.v[e] = fmaf(m.x, init.v[e], m.y);
+                    }
+        }
+        if (kBack && edge && p.h0)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < here) h0.v[e] = p.h0[(long long)it.b * p.C + c + e];
         if (kTma)
-            wait_for(&full[stage], (unsigned)(r / kStages) & 1u, dead, p.status);
+            wait_for(&full[stage], stage_phase, dead, p.status);
+        else if (kBack || p.stages < 4)  // the newest copies are this round's or the next's
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         else
-            asm volatile("cp.async.wait_group %0;" ::"n"(kBack ? kStages - 2 : kStages - 1)
-                         : "memory");
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
         const G *zt = tile_z(stage) + lane * V;
         const T *xt = tile_x(stage, 0) + lane * V;
         // a and y (backward: a and 1 - a) of the L tokens, and their map
@@ -351,9 +429,9 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
                 const Vec<V> z = widen<G, V>(*reinterpret_cast<const Mem<G, V> *>(zt + row(i) * kRow));
                 Vec<V> x = widen<T, V>(*reinterpret_cast<const Mem<T, V> *>(xt + row(i) * kRow));
                 Vec<V> rest;
-                gate_of<kGate, V>(z, p.complement || kBack, a[i], rest);
-                y[i] = kBack ? rest : p.complement ? mul_v(rest, x) : x;
-                if (at_edge.value && s0 + i >= p.N) {
+                gate_of<kGate, V>(z, complement, a[i], rest);
+                y[i] = kBack ? rest : complement ? mul_v(rest, x) : x;
+                if (at_edge.value && s0 + i >= it.end) {
                     a[i] = all_v<V>(1.f);
                     x = y[i] = all_v<V>(0.f);
                 }
@@ -365,53 +443,76 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
             form(Flag<true>());
         else
             form(Flag<false>());
-        *reinterpret_cast<Vec<V> *>(&warp_map[par][warp][0][lane * V]) = A;
-        *reinterpret_cast<Vec<V> *>(&warp_map[par][warp][1][lane * V]) = H;
-        __syncthreads();
+        auto maps = warp_maps[group][turn & 1];
+        auto map_at = [&](float *m) { return reinterpret_cast<Vec<V> *>(m); };
+        map_at(maps[warp][lane])[0] = A;
+        map_at(maps[warp][lane])[1] = H;
+        tc::named_bar_sync(1 + group, 256);
         // forward, everything of this round is in registers now; backward, the
-        // round before is done with its tiles
-        if (!kBack) fetch(r + kStages);
-        if (kBack && r > 0) fetch(r - 1 + kStages);
-        // the map of the warps before this one; the last warp joins its own to it
-        // for the map of the whole block
-        auto map_of = [&](int w, int which) {
-            return *reinterpret_cast<const Vec<V> *>(&warp_map[par][w][which][lane * V]);
-        };
-        Vec<V> Ab = all_v<V>(1.f), Hb = all_v<V>(0.f), state = all_v<V>(0.f);
+        // group's round before is done with its tiles
+        if (!kBack) fetch(R + p.stages, stage);
+        if (kBack && turn > 0) fetch(R - 2 + p.stages, stage >= 2 ? stage - 2 : stage - 2 + p.stages);
+        // The block's map goes to all blocks of the cluster.  Four places for
+        // maps: a block sends that of round R + 4 after it has all of round
+        // R + 2, whose senders were past round R, the only one that reads R's.
+        const bool last_warp = warp == kWarps - 1;
+        if (S > 1 && last_warp) {
+            Vec<V> Ab = all_v<V>(1.f), Hb = all_v<V>(0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const Vec<V> *m = map_at(maps[w][lane]);
+                Hb = fma_v(m[0], Hb, m[1]);
+                Ab = mul_v(Ab, m[0]);
+            }
+            if (lane == 0) tc::mbar_arrive_expect_tx(&maps_in[slot], S * 32 * 2 * V * 4);
+            for (int to = 0; to < S; ++to)
+                send_map<V>(block_map(slot, rank), &maps_in[slot], to, Ab, Hb);
+        }
+        // The state that reaches the round, from the other group.  Its place is
+        // written again by round R + 3, after that group's barrier of round
+        // R + 2, before which this round's readers are done.
+        Vec<V> state = init, product = all_v<V>(1.f);
+        wait_for(&state_in[slot], slot_phase, dead, p.status);
+        if (r > 0) {
+            state = map_at(states[slot][lane])[0];
+            if (p.maps_only) product = map_at(states[slot][lane])[1];
+        }
+        if (S > 1) wait_for(&maps_in[slot], slot_phase, dead, p.status);
+        if (last_warp) {
+            Vec<V> next = state;
+            auto join = [&](const Vec<V> *m) {
+                next = fma_v(m[0], next, m[1]);
+                if (p.maps_only) product = mul_v(product, m[0]);
+            };
+            if (S == 1) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) join(map_at(maps[w][lane]));
+            } else {
+                for (int q = 0; q < S; ++q) join(map_at(block_map(slot, q)));
+            }
+            const int to = slot + 1 == kSlots ? 0 : slot + 1;
+            map_at(states[to][lane])[0] = next;
+            if (p.maps_only) {
+                map_at(states[to][lane])[1] = product;
+                if (r == rounds - 1 && rank == 0)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (e < here)
+                            p.maps[((long long)it.piece * p.B + it.b) * p.C + c + e] =
+                                make_float2(product.v[e], next.v[e]);
+            }
+            tc::mbar_arrive(&state_in[to]);
+        }
+        for (int q = 0; q < rank; ++q) {
+            const Vec<V> *m = map_at(block_map(slot, q));
+            state = fma_v(m[0], state, m[1]);
+        }
         for (int w = 0; w < warp; ++w) {
-            const Vec<V> Aw = map_of(w, 0);
-            Hb = fma_v(Aw, Hb, map_of(w, 1));
-            Ab = mul_v(Ab, Aw);
+            const Vec<V> *m = map_at(maps[w][lane]);
+            state = fma_v(m[0], state, m[1]);
         }
-        if (S == 1) {
-            state = fma_v(Ab, carry, Hb);
-            for (int w = warp; w < kWarps; ++w) {
-                const Vec<V> Aw = map_of(w, 0);
-                Hb = fma_v(Aw, Hb, map_of(w, 1));
-                Ab = mul_v(Ab, Aw);
-            }
-            carry = fma_v(Ab, carry, Hb);
-        } else {
-            // A block sends its map of round r + 2, to the same place, only
-            // after it has those of round r + 1, and this block's goes out after
-            // it has read round r's: two places are enough.
-            if (tid == 0) tc::mbar_arrive_expect_tx(&maps_in[par], S * 32 * 2 * V * 4);
-            if (warp == kWarps - 1) {
-                const Vec<V> At = mul_v(Ab, A), Ht = fma_v(A, Hb, H);
-                for (int k = 0; k < S; ++k) send_map<V>(block_map(par, rank), &maps_in[par], k, At, Ht);
-            }
-            wait_for(&maps_in[par], (unsigned)(r >> 1) & 1u, dead, p.status);
-            for (int k = 0; k < S; ++k) {
-                if (k == rank) state = fma_v(Ab, carry, Hb);
-                const Vec<V> *m = reinterpret_cast<const Vec<V> *>(block_map(par, k));
-                carry = fma_v(m[0], carry, m[1]);
-            }
-        }
-        // the L tokens again, from the state that reaches them
-        const long long t0 = kBack ? p.N - 1 - s0 : s0;
+        // the L tokens again, from there
         auto walk = [&](auto at_edge) {
-            T *o = static_cast<T *>(p.out[0].p) + b * p.out[0].b + t0 * p.out[0].n + c;
-            G *oz = static_cast<G *>(p.out[1].p) + b * p.out[1].b + t0 * p.out[1].n + c;
             auto put = [&](auto *dst, const Vec<V> &v) {
                 using E = std::remove_reference_t<decltype(*dst)>;
                 const Mem<E, V> m = narrow<E, V>(v);
@@ -423,13 +524,15 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
                         if (e < here) dst[e] = m.v[e];
                 }
             };
+            T *to = o;
+            G *toz = oz;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                const bool ok = !at_edge.value || s0 + i < p.N;
+                const bool ok = !at_edge.value || s0 + i < it.end;
                 if (!kBack) {
                     state = fma_v(a[i], state, y[i]);
-                    if (ok) put(o, state);
-                    o += p.out[0].n;
+                    if (ok) put(to, state);
+                    to += p.out[0].n;
                     continue;
                 }
                 auto tile = [&](int which) {
@@ -440,34 +543,43 @@ __global__ void __launch_bounds__(kThreads, 2) rec_scan_kernel(const __grid_cons
                 if (at_edge.value && !ok) g = all_v<V>(0.f);
                 if (at_edge.value && s0 + i == p.N - 1) h = h0;
                 g = add_v(g, state);
-                if (p.complement) h = fma_v(tile(2), all_v<V>(-1.f), h);
+                if (complement) h = fma_v(tile(2), all_v<V>(-1.f), h);
                 if (ok) {
-                    put(o, p.complement ? mul_v(y[i], g) : g);
+                    put(to, complement ? mul_v(y[i], g) : g);
                     Vec<V> dz = mul_v(g, h);
                     if (kGate != LA_GATE_VALUE) dz = mul_v(dz, a[i]);
                     if (kGate == LA_GATE_LOGIT) dz = mul_v(dz, y[i]);
-                    put(oz, dz);
+                    put(toz, dz);
                 }
                 state = mul_v(a[i], g);
-                o -= p.out[0].n;
-                oz -= p.out[1].n;
+                to -= p.out[0].n;
+                toz -= p.out[1].n;
             }
         };
-        if (edge)
-            walk(Flag<true>());
-        else
-            walk(Flag<false>());
-        // the state behind the last token, as its warp has it: forward, these
-        // are the bits that `out` was rounded from
-        if (p.last && behind && s0 < p.N)
+        if (!p.maps_only) {
+            if (edge)
+                walk(Flag<true>());
+            else
+                walk(Flag<false>());
+            // the state behind the last token, as its warp has it: forward, these
+            // are the bits that `out` was rounded from
+            if (edge && p.last && s0 < p.N && s0 + L >= p.N && it.end == p.N)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < here) p.last[(long long)b * p.C + c + e] = state.v[e];
+                for (int e = 0; e < V; ++e)
+                    if (e < here) p.last[(long long)it.b * p.C + c + e] = state.v[e];
+        }
+        s0 += 2 * round_steps;
+        o += o_turn;
+        if (kBack) oz += oz_turn;
+        ++turn;
+        if ((stage += 2) >= p.stages) stage -= p.stages, stage_phase ^= 1;
+        if ((slot += 2) >= kSlots) slot -= kSlots, slot_phase ^= 1;
+        for (r += 2; r >= rounds; r -= rounds) ++k;
     }
     if (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
     if (kTma && dead)  // copies may still be under way: leave after them
-        for (int r = max(0, rounds - kStages); r < rounds; ++r)
-            tc::mbar_wait(&full[r % kStages], (unsigned)(r / kStages) & 1u,
+        for (int i = max(0, total - p.stages); i < total; ++i)
+            tc::mbar_wait(&full[i % p.stages], (unsigned)(i / p.stages) & 1u,
                           clock64() + kWaitCycles, nullptr);
     if (S > 1) {  // no block leaves while another may still send to it
         asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
@@ -486,8 +598,8 @@ struct StepParams {
 };
 
 template <typename T, typename G, int V, int kGate>
-__global__ void __launch_bounds__(kThreads) rec_step_kernel(const StepParams p) {
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
+__global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const StepParams p) {
+    const long long i = ((long long)blockIdx.x * kStepThreads + threadIdx.x) * V;
     if (i >= (long long)p.B * p.C) return;
     const int b = (int)(i / p.C), c = (int)(i % p.C);
     auto get = [](const auto *q) {
@@ -584,44 +696,91 @@ bool make_map(CUtensorMap *map, const Seq &q, int B, int N, int C, int elem, int
            CUDA_SUCCESS;
 }
 
+// How a call is cut: clusters of S blocks, pieces of a sequence.
+struct Cut {
+    int S, clusters, pieces, steps, stages;
+    size_t smem;
+};
+
+// The cheapest cut by rounds: a cluster takes ceil(items / clusters) strips, one
+// after the other, each of ceil(steps / (S tile)) rounds and about two more for
+// the start.
+template <typename F>
+Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&clusters_of) {
+    const long long items = (long long)p.B * p.strips;
+    Cut best{};
+    double cost = 0;
+    for (int S = 1; S <= kMaxCluster; ++S) {
+        if (S > 1 && (long long)(S - 1) * tile >= p.N) break;
+        const size_t maps = (size_t)kSlots * S * 32 * 2 * V * sizeof(float);
+        const int stages = std::min<int>(kMaxStages, (int)((kSmem - maps) / bytes) / 2 * 2);
+        if (stages < least_stages) break;
+        const size_t smem = (size_t)stages * bytes + maps;
+        const long long most = clusters_of(S, smem);
+        if (most < 1) continue;
+        const long long waves = (items + most - 1) / most;
+        const long long rounds = ((long long)p.N + (long long)S * tile - 1) / ((long long)S * tile);
+        const double c = (double)waves * (double)(rounds + 2);
+        if (!best.S || c < cost) {
+            cost = c;
+            best = {S, (int)std::min(items, most), 1, p.N, stages, smem};
+        }
+    }
+    return best;
+}
+
 template <typename T, typename G, int V, int kGate, bool kBack>
 cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
-    constexpr int L = kBack ? 8 : 16;
+    constexpr int L = kBack ? 8 : 16, kTile = kWarps * L;
     if (tma)
         for (int i = 0; i < (kBack ? 3 + p.complement : 2); ++i)
             if (!make_map(&p.map[i], p.in[i], p.B, p.N, p.C,
-                          i == 1 ? (int)sizeof(G) : (int)sizeof(T), 32 * V, kWarps * L))
+                          i == 1 ? (int)sizeof(G) : (int)sizeof(T), 32 * V, kTile))
                 return cudaErrorInvalidValue;
-    auto kern = tma ? rec_scan_kernel<T, G, V, L, kGate, true, kBack>
-                    : rec_scan_kernel<T, G, V, L, kGate, false, kBack>;
-    int sms = 0;
-    cudaError_t e = tchost::sm_count(&sms);
-    if (e == cudaSuccess) p.status = device_status_word(&e);
-    if (e != cudaSuccess) return e;
-    p.strips = (p.C + 32 * V - 1) / (32 * V);
-    const long long strips = (long long)p.B * p.strips;
-    // as many blocks per strip as the GPU holds at once (two per SM) and the
-    // sequence has work for
-    int S = 1;
-    while (S < kMaxCluster && strips * S * 2 <= 2LL * sms && (long long)S * kWarps * L < p.N)
-        S *= 2;
-    if (strips * S > 2147483647LL) return cudaErrorInvalidConfiguration;
-    const size_t smem = (size_t)kStages * stage_bytes<T, G, V, L, kBack>(p.complement) +
-                        (S > 1 ? (size_t)2 * S * 32 * 2 * V * sizeof(float) : 0);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && S > 8)
+    auto kern = !tma ? rec_scan_kernel<T, G, V, L, kGate, 2, false, kBack>
+                : p.complement ? rec_scan_kernel<T, G, V, L, kGate, 1, true, kBack>
+                               : rec_scan_kernel<T, G, V, L, kGate, 0, true, kBack>;
+    cudaError_t e;
+    p.status = device_status_word(&e);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    p.strips = (p.C + 32 * V - 1) / (32 * V);
+    const int bytes = stage_bytes<T, G, V, L, kBack>(p.complement);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(strips * S));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)S, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    auto clusters_of = [&](int S, size_t smem) {
+        static std::atomic<int> known[3][kMaxCluster + 1];  // one block per SM whatever the stages
+        std::atomic<int> &n = known[tma ? p.complement : 2][S];
+        if (n.load() == 0) {
+            int got = 0;
+            cfg.gridDim = dim3((unsigned)S);
+            cfg.dynamicSmemBytes = smem;
+            at[0].val.clusterDim = {(unsigned)S, 1, 1};
+            if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                got = 0;
+            }
+            n.store(got > 0 ? got : -1);
+        }
+        return n.load();
+    };
+    // backward, a stage is refilled two rounds after its own
+    const Cut cut = best_cut(p, kTile, bytes, V, kBack ? 4 : 2, clusters_of);
+    if (!cut.S) return cudaErrorInvalidConfiguration;
+    p.stages = cut.stages;
+    p.pieces = cut.pieces;
+    p.steps = cut.steps;
+    cfg.gridDim = dim3((unsigned)(cut.clusters * cut.S));
+    cfg.dynamicSmemBytes = cut.smem;
+    at[0].val.clusterDim = {(unsigned)cut.S, 1, 1};
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -635,6 +794,8 @@ cudaError_t launch_gate(Params &p, la_gate gate, bool tma, cudaStream_t s) {
 template <bool kBack>
 la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dtype gate_dtype,
                  cudaStream_t s) {
+    if ((long long)p.B * ((p.C + 31) / 32) > 2147483647LL / kMaxPieces)
+        return rec_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     // a thread takes 4 bytes of x per token: two bf16 channels
     const int v = dtype == LA_F32 ? 1 : 2;
     const int ex = dtype == LA_F32 ? 4 : 2, ez = gate_dtype == LA_F32 ? 4 : 2;
@@ -656,13 +817,13 @@ la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dt
 
 template <typename T, typename G, int V>
 cudaError_t launch_step(const StepParams &p, la_gate gate, cudaStream_t s) {
-    const unsigned nb = (unsigned)(((long long)p.B * p.C / V + kThreads - 1) / kThreads);
+    const unsigned nb = (unsigned)(((long long)p.B * p.C / V + kStepThreads - 1) / kStepThreads);
     if (gate == LA_GATE_VALUE)
-        rec_step_kernel<T, G, V, LA_GATE_VALUE><<<nb, kThreads, 0, s>>>(p);
+        rec_step_kernel<T, G, V, LA_GATE_VALUE><<<nb, kStepThreads, 0, s>>>(p);
     else if (gate == LA_GATE_LOG)
-        rec_step_kernel<T, G, V, LA_GATE_LOG><<<nb, kThreads, 0, s>>>(p);
+        rec_step_kernel<T, G, V, LA_GATE_LOG><<<nb, kStepThreads, 0, s>>>(p);
     else
-        rec_step_kernel<T, G, V, LA_GATE_LOGIT><<<nb, kThreads, 0, s>>>(p);
+        rec_step_kernel<T, G, V, LA_GATE_LOGIT><<<nb, kStepThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
