@@ -442,14 +442,26 @@ typedef struct {
  *              token (unrounded), or NULL; may be h0 itself.
  *   strides    3 strides, of x, gates, out, or NULL: contiguous.
  *   B, N, C >= 0 (B*C == 0 is a no-op; N == 0 copies h0 to h_last).
+ *   workspace  device buffer, 16-byte aligned, of
+ *              la_recurrence_workspace_bytes(B, C, dtype) bytes, not used by
+ *              anything else until `stream` has passed the call; or NULL: a
+ *              call that needs one (few channels, a long sequence) allocates it
+ *              stream-ordered (LA_ERR_NO_MEMORY if that fails).
  * States and gate products are fp32.  Sequences are cut along N (the pieces
  * are joined in a fixed order: repeated calls are bit-identical).
- * A non-finite value stays within its sequence and channel.
+ * A non-finite value stays within its sequence and channel.  Rows are read in
+ * whole 16-byte units of memory: neighbouring bytes of a unit that holds part
+ * of a row may be read and are not used.
  */
 la_status la_forward_recurrence(const void *x, const void *gates, const float *h0,
                                 void *out, float *h_last, const la_seq_strides *strides,
                                 int B, int N, int C, la_gate gate, int complement,
-                                la_dtype dtype, la_dtype gate_dtype, la_stream_t stream);
+                                la_dtype dtype, la_dtype gate_dtype, void *workspace,
+                                size_t workspace_bytes, la_stream_t stream);
+
+/* Workspace bytes that la_forward_recurrence and la_backward_recurrence need
+ * at most for B sequences of C channels (0: none, or invalid arguments). */
+size_t la_recurrence_workspace_bytes(int B, int C, la_dtype dtype);
 
 /*
  * la_backward_recurrence -- gradients of la_forward_recurrence.  With c_t the
@@ -478,7 +490,8 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
                                  void *dx, void *dgates, float *dh0,
                                  const la_seq_strides *strides, int B, int N, int C,
                                  la_gate gate, int complement, la_dtype dtype,
-                                 la_dtype gate_dtype, la_stream_t stream);
+                                 la_dtype gate_dtype, void *workspace,
+                                 size_t workspace_bytes, la_stream_t stream);
 
 /*
  * la_decode_step_recurrence -- one token of la_forward_recurrence.

@@ -41,7 +41,8 @@ EXPORTED = ("la_forward", "la_forward_ex", "la_decode_step",
             "la_forward_gated", "la_decode_step_gated", "la_decode_step_delta",
             "la_debug_inject_timeout", "la_debug_fail_next_allocs", "la_forward_delta",
             "la_qk_norm_rope", "la_backward_qk_norm_rope",
-            "la_backward_qk_norm_rope_workspace_bytes", "la_forward_recurrence",
+            "la_backward_qk_norm_rope_workspace_bytes", "la_recurrence_workspace_bytes",
+            "la_forward_recurrence",
             "la_backward_recurrence", "la_decode_step_recurrence")
 
 FEATURE_MAPS = {"elu1": 0, "identity": 1}
@@ -101,9 +102,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                              V, ctypes.c_size_t, V]
     lib.la_backward_qk_norm_rope_workspace_bytes.argtypes = [I]
     lib.la_backward_qk_norm_rope_workspace_bytes.restype = ctypes.c_size_t
-    lib.la_forward_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, I, V]
+    lib.la_forward_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, I,
+                                          V, ctypes.c_size_t, V]
     lib.la_backward_recurrence.argtypes = [V, V, V, V, V, V, V, V, V, V,
-                                           I, I, I, I, I, I, I, V]
+                                           I, I, I, I, I, I, I, V, ctypes.c_size_t, V]
+    lib.la_recurrence_workspace_bytes.argtypes = [I, I, I]
+    lib.la_recurrence_workspace_bytes.restype = ctypes.c_size_t
     lib.la_decode_step_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, V]
     lib.la_debug_inject_timeout.argtypes = [ctypes.c_longlong, I]
     lib.la_debug_fail_next_allocs.argtypes = [I]
@@ -655,6 +659,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _recurrence_workspace(B, C, like, stream):
+    """(workspace or None, bytes): on the current stream torch's allocator
+    gives it; the library allocates on another one."""
+    if stream is not None:
+        return None, 0
+    n = load_library().la_recurrence_workspace_bytes(B, C, _dtype_code(like))
+    if n == 0:
+        return None, 0
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=like.device), n
+
+
 def _seq_strides(*ts):
     v = []
     for t in ts:
@@ -683,10 +699,11 @@ def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = 
     _check_seq(x, gates, out)
     _check_state(B, C, x, h0, h_last)
     with _on(x.device):
+        ws, ws_bytes = _recurrence_workspace(B, C, x, stream)
         st = load_library().la_forward_recurrence(
             x.data_ptr(), gates.data_ptr(), _ptr(h0), out.data_ptr(), h_last.data_ptr(),
             _seq_strides(x, gates, out), B, N, C, code, bool(complement), _dtype_code(x),
-            _dtype_code(gates), _raw_stream(stream, x.device))
+            _dtype_code(gates), _ptr(ws), ws_bytes, _raw_stream(stream, x.device))
     _raise_if(st)
     return out, h_last
 
@@ -719,11 +736,13 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
     _check_seq(dout, dgates)
     _check_state(B, C, dout, h0, dh_last, dh0)
     with _on(dout.device):
+        ws, ws_bytes = _recurrence_workspace(B, C, dout, stream)
         st = load_library().la_backward_recurrence(
             dout.data_ptr(), gates.data_ptr(), out.data_ptr(), _ptr(x), _ptr(h0),
             _ptr(dh_last), dx.data_ptr(), dgates.data_ptr(), dh0.data_ptr(),
             _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, code, bool(complement),
-            _dtype_code(dout), _dtype_code(gates), _raw_stream(stream, dout.device))
+            _dtype_code(dout), _dtype_code(gates), _ptr(ws), ws_bytes,
+            _raw_stream(stream, dout.device))
     _raise_if(st)
     return dx, dgates, dh0
 

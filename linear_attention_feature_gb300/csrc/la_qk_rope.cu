@@ -61,6 +61,43 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float &d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
 
+// bf16 pairs are taken apart and put together as 32-bit words: one instruction
+// a value, and one a pair.
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Pack<T, V> *p, float *e) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        struct alignas(2 * V) Words {
+            unsigned u[V / 2];
+        };
+        const Words w = *reinterpret_cast<const Words *>(p);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            e[2 * i] = __uint_as_float(w.u[i] << 16);
+            e[2 * i + 1] = __uint_as_float(w.u[i] & 0xffff0000u);
+        }
+    } else {
+        const Pack<T, V> a = *p;
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = to_f(a.v[i]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void narrow(T *dst, const float *e) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        struct alignas(2 * V) Words {
+            __nv_bfloat162 u[V / 2];
+        } w;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w.u[i] = __floats2bfloat162_rn(e[2 * i], e[2 * i + 1]);
+        *reinterpret_cast<Words *>(dst) = w;
+    } else {
+        Pack<T, V> a;
+#pragma unroll
+        for (int i = 0; i < V; ++i) from_f(a.v[i], e[i]);
+        *reinterpret_cast<Pack<T, V> *>(dst) = a;
+    }
+}
+
 // Global to shared memory, zeros where !ok; asynchronous from 4 bytes on.
 template <typename T, int V>
 __device__ __forceinline__ void fetch(Pack<T, V> *dst, const T *src, bool ok) {
@@ -264,10 +301,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
 
     // one vector pair of a slot as the pairs' first and second values
     auto open = [&](const Pack<T, V> *l, const Pack<T, V> *h, float2 (&m0)[P], float2 (&m1)[P]) {
-        const Pack<T, V> a = *l, c = *h;
         float e[2 * V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = to_f(a.v[i]), e[V + i] = to_f(c.v[i]);
+        widen(l, e);
+        widen(h, e + V);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             if (V == 1) {
@@ -389,17 +425,14 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                             r2, __ffma2_rn(n1, m2, __fmul2_rn(w1[j][i], g1[j][i])));
                     }
                 }
-                Pack<T, V> l, h;
+                float e[2 * V];  // as in memory: lo, then hi
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float a = e % 2 ? o0[e / 2].y : o0[e / 2].x;
-                    const float c = e % 2 ? o1[e / 2].y : o1[e / 2].x;
-                    const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
-                    from_f(i0 < V ? l.v[i0 % V] : h.v[i0 % V], a);
-                    from_f(i1 < V ? l.v[i1 % V] : h.v[i1 % V], c);
+                for (int i = 0; i < V; ++i) {
+                    e[kInter ? 2 * i : i] = i % 2 ? o0[i / 2].y : o0[i / 2].x;
+                    e[kInter ? 2 * i + 1 : V + i] = i % 2 ? o1[i / 2].y : o1[i / 2].x;
                 }
-                if (ok && l_ok[j]) *reinterpret_cast<Pack<T, V> *>(y + lo[j]) = l;
-                if (ok && h_ok[j]) *reinterpret_cast<Pack<T, V> *>(y + hi[j]) = h;
+                if (ok && l_ok[j]) narrow<T, V>(y + lo[j], e);
+                if (ok && h_ok[j]) narrow<T, V>(y + hi[j], e + V);
             }
             depth = depth + 1 == kDepth ? 0 : depth + 1;
         }

@@ -27,9 +27,14 @@
 // Maps are applied in scan order, so repeated calls are bit-identical.  The grid
 // is as many clusters as run at once; each takes strip after strip.
 //
-// Rows that TMA cannot take (strides or bases that are not multiples of 16
-// bytes) are read by the threads themselves, each its own tokens and channels
-// into the same places; 4-byte values with cp.async.
+// Rows that TMA tiles cannot take (strides or bases that are not multiples of 16
+// bytes) come by cp.async: the 16-byte units of memory that hold the strip's
+// part of the row, wherever it begins in the first of them.  (A bulk copy per
+// row was slower, 400 against XXX us at 2 x 32768 x 2047 bf16.)
+//
+// Where even clusters would leave most SMs idle (few channels, long sequences),
+// a sequence is cut into pieces and walked twice: once for the maps of the
+// pieces, once from the states that they give.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -38,22 +43,27 @@
 #include <cstdio>
 
 #include "la_internal.h"
+#include "la_tc.h"
 #include "la_tc_host.h"
 #include "la_tc_ptx.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kWarps = 8;        // of a group
+constexpr int kGroup = 32 * kWarps;
+constexpr int kThreads = 2 * kGroup;
 constexpr int kMaxStages = 6;    // rounds of copies in flight, an even number
 constexpr int kSlots = 4;        // rounds of maps and states kept
 constexpr int kMaxCluster = 16;
-constexpr int kMaxPieces = 64;
+constexpr int kMaxPieces = 128;  // of a sequence
+constexpr int kFewStrips = 16;   // more than that are not cut into pieces
 constexpr int kStepThreads = 256;
+constexpr int kMaxDevices = 64;  // as device_status_word
 constexpr size_t kSmem = 208 * 1024;  // stages and maps; 227 KB with the static arrays
 
-constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait for a copy, about 2 s
+constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait, about 2 s
+constexpr uint32_t kSuspendNs = 20000;  // a waiting warp sleeps this long between polls, at most
 
 // V channels of one thread; two go through the packed fp32 instructions, which
 // round like the single ones.
@@ -109,19 +119,37 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float &d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
+// bf16 pairs are taken apart and put together as 32-bit words: one instruction
+// a value, and one a pair.
 template <typename T, int V>
-__device__ __forceinline__ Vec<V> widen(Mem<T, V> m) {
+__device__ __forceinline__ Vec<V> widen(const Mem<T, V> *p) {
     Vec<V> r;
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) r.v[e] = to_f(m.v[e]);
+        for (int e = 0; e < V; e += 2) {
+            const unsigned u = reinterpret_cast<const unsigned *>(p)[e / 2];
+            r.v[e] = __uint_as_float(u << 16);
+            r.v[e + 1] = __uint_as_float(u & 0xffff0000u);
+        }
+    } else {
+        const Mem<T, V> m = *p;
+#pragma unroll
+        for (int e = 0; e < V; ++e) r.v[e] = to_f(m.v[e]);
+    }
     return r;
 }
 template <typename T, int V>
-__device__ __forceinline__ Mem<T, V> narrow(Vec<V> x) {
-    Mem<T, V> m;
+__device__ __forceinline__ void narrow(Mem<T, V> *p, const Vec<V> &x) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) from_f(m.v[e], x.v[e]);
-    return m;
+        for (int e = 0; e < V; e += 2)
+            reinterpret_cast<__nv_bfloat162 *>(p)[e / 2] = __floats2bfloat162_rn(x.v[e], x.v[e + 1]);
+    } else {
+        Mem<T, V> m;
+#pragma unroll
+        for (int e = 0; e < V; ++e) from_f(m.v[e], x.v[e]);
+        *p = m;
+    }
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -140,42 +168,46 @@ template <int kGate, int V>
 __device__ __forceinline__ void gate_of(Vec<V> z, bool need_rest, Vec<V> &a, Vec<V> &rest) {
     if (kGate == LA_GATE_VALUE) {
         a = z;
-        rest = fma_v(z, all_v<V>(-1.f), all_v<V>(1.f));
+        if (need_rest) rest = fma_v(z, all_v<V>(-1.f), all_v<V>(1.f));
     } else if (kGate == LA_GATE_LOG) {
+        // 1 - e^z = -z (1 + z/2 (1 + z/3 (...))) near 0, to 2^-24 for |z| <= 1/4; a
+        // as its complement is then the nearest fp32 value, without the bias that
+        // an approximate exponential adds up over a long memory
+        Vec<V> s = fma_v(z, all_v<V>(1.f / 720.f), all_v<V>(1.f / 120.f));
+        s = fma_v(s, z, all_v<V>(1.f / 24.f));
+        s = fma_v(s, z, all_v<V>(1.f / 6.f));
+        s = fma_v(s, z, all_v<V>(0.5f));
+        s = fma_v(s, z, all_v<V>(1.f));
+        s = mul_v(s, mul_v(z, all_v<V>(-1.f)));
+        const Vec<V> near = fma_v(s, all_v<V>(-1.f), all_v<V>(1.f));
+        const Vec<V> q = mul_v(z, all_v<V>(1.4426950408889634f));
+        Vec<V> far;
 #pragma unroll
-        for (int e = 0; e < V; ++e) a.v[e] = expf(z.v[e]);
-        rest = fma_v(a, all_v<V>(-1.f), all_v<V>(1.f));
-        if (need_rest) {
-            // 1 - e^z = -z (1 + z/2 (1 + z/3 (...))) near 0, to 2^-24 for |z| <= 1/4
-            Vec<V> s = fma_v(z, all_v<V>(1.f / 720.f), all_v<V>(1.f / 120.f));
-            s = fma_v(s, z, all_v<V>(1.f / 24.f));
-            s = fma_v(s, z, all_v<V>(1.f / 6.f));
-            s = fma_v(s, z, all_v<V>(0.5f));
-            s = fma_v(s, z, all_v<V>(1.f));
-            s = mul_v(s, neg_v(z));
+        for (int e = 0; e < V; ++e) far.v[e] = exp2_approx(q.v[e]);
+        const Vec<V> other = fma_v(far, all_v<V>(-1.f), all_v<V>(1.f));
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (fabsf(z.v[e]) <= 0.25f) rest.v[e] = s.v[e];
+        for (int e = 0; e < V; ++e) {
+            const bool close = fabsf(z.v[e]) <= 0.25f;
+            a.v[e] = close ? near.v[e] : far.v[e];
+            if (need_rest) rest.v[e] = close ? s.v[e] : other.v[e];
         }
     } else {
-        // t = e^-z; the smaller of a and 1 - a first, the other as its
-        // complement.  The product with log2(e) is off by 2^-24 |z| in t, but
-        // a is off by only (1 - a) of that.
-        const Vec<V> q = mul_v(z, all_v<V>(-1.4426950408889634f));
-        Vec<V> t, r, small;
+        // t = e^-|z|; the smaller of a and 1 - a is t / (1 + t), the other its
+        // complement and so the nearest fp32 value.  The product with log2(e) is
+        // off by 2^-24 |z| in t, and a by only (1 - a) of that.
+        const Vec<V> q = mul_v(z, all_v<V>(1.4426950408889634f));
+        Vec<V> t, r;
 #pragma unroll
-        for (int e = 0; e < V; ++e) t.v[e] = exp2_approx(q.v[e]);
+        for (int e = 0; e < V; ++e) t.v[e] = exp2_approx(-fabsf(q.v[e]));
         const Vec<V> d = add_v(t, all_v<V>(1.f));
 #pragma unroll
         for (int e = 0; e < V; ++e) r.v[e] = rcp_approx(d.v[e]);
-        const Vec<V> tr = mul_v(t, r);
-#pragma unroll
-        for (int e = 0; e < V; ++e) small.v[e] = z.v[e] < 0.f ? r.v[e] : tr.v[e];
+        const Vec<V> small = mul_v(t, r);
         const Vec<V> other = fma_v(small, all_v<V>(-1.f), all_v<V>(1.f));
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             a.v[e] = z.v[e] < 0.f ? small.v[e] : other.v[e];
-            rest.v[e] = z.v[e] < 0.f ? other.v[e] : small.v[e];
+            if (need_rest) rest.v[e] = z.v[e] < 0.f ? other.v[e] : small.v[e];
         }
     }
 }
@@ -200,6 +232,7 @@ struct Params {
     const float *h0;     // backward: h_0, for the first token's gate
     int *status;
     int B, N, C, complement, strips, stages;
+    int out_vec;  // rows of the outputs are aligned to V values
     // A sequence in more than one piece of `steps` tokens (in scan order): a
     // launch with maps_only leaves the map of every piece but the last in
     // `maps`, [piece][B][C] of (A, H); the next one starts each piece from them.
@@ -207,23 +240,30 @@ struct Params {
     float2 *maps;
 };
 
-// Bytes of one stage: a tile [kWarps L][32 V] of the gates, then of each other
+// Bytes of a tile's row: 32 V values, and where rows begin anywhere in a unit of
+// 16 bytes, one unit more.
+template <typename T, int V, bool kTma>
+constexpr int row_bytes() { return 32 * V * (int)sizeof(T) + (kTma ? 0 : 16); }
+// Bytes of one stage: a tile of kWarps L rows of the gates, then of each other
 // input.
-template <typename T, typename G, int V, int L, bool kBack>
+template <typename T, typename G, int V, int L, bool kTma, bool kBack>
 constexpr int stage_bytes(int complement) {
-    return kWarps * L * 32 * V *
-           ((int)sizeof(G) + (int)sizeof(T) * (kBack ? 2 + complement : 1));
+    return kWarps * L * (row_bytes<G, V, kTma>() +
+                         row_bytes<T, V, kTma>() * (kBack ? 2 + complement : 1));
 }
 
 // Waits for a stage's copies or the cluster's maps, with a limit: afterwards the
 // launch is marked as failed in the status word and goes on without waiting.
 __device__ __forceinline__ void wait_for(uint64_t *bar, unsigned parity, bool &dead, int *status) {
-    if (dead || tc::mbar_try_wait(bar, parity)) return;
-    if (!tc::mbar_wait(bar, parity, clock64() + kWaitCycles, nullptr)) {
-        dead = true;
-        if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
-            atomicExch(status + 1, (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
-    }
+    if (dead || tc::mbar_try_wait_ns(bar, parity, kSuspendNs)) return;
+    const long long deadline = clock64() + kWaitCycles;
+    while (!tc::mbar_try_wait_ns(bar, parity, kSuspendNs))
+        if (clock64() > deadline) {
+            dead = true;
+            if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
+                atomicExch(status + 1, (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
+            return;
+        }
 }
 
 // A thread's part (A, H) of a block's map to the same place in the block `to` of
@@ -262,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
 
     const cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int tid = threadIdx.x & 255, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x % kGroup, lane = threadIdx.x & 31;
     // the same in all lanes, so that row addresses are formed once per warp
-    const int group = __shfl_sync(~0u, threadIdx.x >> 8, 0);
+    const int group = __shfl_sync(~0u, threadIdx.x / kGroup, 0);
     const int warp = __shfl_sync(~0u, tid >> 5, 0);
-    const int bytes = stage_bytes<T, G, V, L, kBack>(complement);
+    const int bytes = stage_bytes<T, G, V, L, kTma, kBack>(complement);
     const int round_steps = S * kTile;
     const int rounds = (int)(((long long)p.steps + round_steps - 1) / round_steps);  // of a piece
     const int items = p.B * p.strips * (p.pieces - p.maps_only);
@@ -302,63 +342,91 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         return it.begin + (long long)r * round_steps + rank * kTile;
     };
     auto row = [&](int i) { return kBack ? kTile - 1 - (warp * L + i) : warp * L + i; };
-    auto tile_z = [&](int stage) { return reinterpret_cast<G *>(stages + stage * bytes); };
+    auto tile_z = [&](int stage) { return stages + stage * bytes; };
     auto tile_x = [&](int stage, int which) {
-        return reinterpret_cast<T *>(stages + stage * bytes + kTile * kRow * (int)sizeof(G)) +
-               which * kTile * kRow;
+        return stages + stage * bytes + kTile * (row_bytes<G, V, kTma>() +
+                                                 which * row_bytes<T, V, kTma>());
     };
-    // round R of the cluster into a stage; called by the threads of one group
-    auto fetch = [&](int R, int stage) {
-        if (kTma && (tid != 0 || R >= total)) return;
-        const Item it = item(R < total ? R / rounds : 0);
-        const long long s0 = first_step(it, R % rounds);
+    // round R of the cluster, round r of item `it` if there are that many, into
+    // a stage; called by the threads of one group
+    auto fetch = [&](int R, int stage, Item it, int r) {
+        if (R >= total || (kTma && tid != 0)) return;
+        if (r >= rounds) {
+            it = item(R / rounds);
+            r = R % rounds;
+        }
+        const long long s0 = first_step(it, r);
         const long long low = kBack ? p.N - s0 - kTile : s0;
-        const bool all = kBack && !p.maps_only;
+        // gates, x or dout, and for a backward walk out (a token earlier) and x
+        const int tensors = !kBack || p.maps_only ? 2 : complement ? 4 : 3;
         if (kTma) {
             const int t = (int)low;
-            const uint64_t policy = tc::policy_evict_first();
+            // read once, unless another launch comes for the same tiles
+            const uint64_t policy = p.maps_only ? tc::policy_evict_normal() : tc::policy_evict_first();
             tc::mbar_arrive_expect_tx(
-                &full[stage], all ? bytes : kTile * kRow * (int)(sizeof(G) + sizeof(T)));
+                &full[stage],
+                kTile * (row_bytes<G, V, true>() + (tensors - 1) * row_bytes<T, V, true>()));
             tc::tma_load_3d(tile_z(stage), &p.map[1], &full[stage], it.c0, t, it.b, policy);
             tc::tma_load_3d(tile_x(stage, 0), &p.map[0], &full[stage], it.c0, t, it.b, policy);
-            if (all) {
+            if (tensors > 2)
                 tc::tma_load_3d(tile_x(stage, 1), &p.map[2], &full[stage], it.c0, t - 1, it.b, policy);
-                if (complement)
-                    tc::tma_load_3d(tile_x(stage, 2), &p.map[3], &full[stage], it.c0, t, it.b, policy);
-            }
+            if (tensors > 3)
+                tc::tma_load_3d(tile_x(stage, 2), &p.map[3], &full[stage], it.c0, t, it.b, policy);
             return;
         }
-        const int c = it.c0 + lane * V;
-        auto mine = [&](auto *tile, const Seq &q, int shift) {
-            using E = std::remove_reference_t<decltype(*tile)>;
-            const E *src = static_cast<const E *>(q.p) + it.b * q.b + c;
-            for (int i = 0; i < L; ++i) {
-                const long long t = low + row(i) - shift;
-                const bool ok = R < total && t >= 0 && t < p.N;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    E *dst = tile + row(i) * kRow + lane * V + e;
-                    if (!ok || c + e >= p.C)
-                        *dst = E(0.f);
-                    else if (sizeof(E) == 4)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                                         tc::smem_u32(dst)), "l"(src + t * q.n + e) : "memory");
-                    else
-                        *dst = src[t * q.n + e];
-                }
+        // the 16-byte units that hold channels [c0, c0 + kRow) of C, row by row
+        auto units = [&](auto *like, const Seq &q, int shift, char *tile) {
+            using E = std::remove_pointer_t<decltype(like)>;
+            constexpr int kUnits = kRow * (int)sizeof(E) / 16 + 1;
+            const long long t0 = low - shift, line = q.n * (long long)sizeof(E);
+            const uintptr_t base =
+                (uintptr_t)q.p + (uintptr_t)(it.b * q.b + t0 * q.n + it.c0) * sizeof(E);
+            const int valid = min(kRow, p.C - it.c0) * (int)sizeof(E);
+            for (int i = tid; i < kTile * kUnits; i += kGroup) {
+                const int j = i / kUnits, u = i % kUnits;
+                const uintptr_t at = base + (uintptr_t)(j * line);
+                const uintptr_t from = (at & ~(uintptr_t)15) + 16 * u;
+                if (t0 + j >= 0 && t0 + j < p.N && from < at + valid)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     tc::smem_u32(tile + j * row_bytes<E, V, false>() + 16 * u)),
+                                 "l"(from) : "memory");
             }
         };
-        mine(tile_z(stage), p.in[1], 0);
-        mine(tile_x(stage, 0), p.in[0], 0);
-        if (all) {
-            mine(tile_x(stage, 1), p.in[2], 1);
-            if (complement) mine(tile_x(stage, 2), p.in[3], 0);
+        units((G *)nullptr, p.in[1], 0, tile_z(stage));
+        units((T *)nullptr, p.in[0], 0, tile_x(stage, 0));
+        if (tensors > 2) units((T *)nullptr, p.in[2], 1, tile_x(stage, 1));
+        if (tensors > 3) units((T *)nullptr, p.in[3], 0, tile_x(stage, 2));
+        // arrives when this thread's copies have
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         tc::smem_u32(&full[stage])) : "memory");
+    };
+    // A thread's V values of row i (in scan order, its own) of a tile.  `at` is
+    // the address of the first of them in memory and `step` the bytes between
+    // rows, both modulo 2^32: where the row begins in its first 16-byte unit.
+    auto values = [&](auto *like, const char *tile, unsigned at, unsigned step, int i) {
+        using E = std::remove_pointer_t<decltype(like)>;
+        const char *line = tile + row(i) * row_bytes<E, V, kTma>() + lane * V * (int)sizeof(E);
+        if constexpr (kTma) {
+            return widen(reinterpret_cast<const Mem<E, V> *>(line));
+        } else {
+            const unsigned off = (at + i * step) & 15u;
+            Vec<V> v;
+            if constexpr (sizeof(E) == 4) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    v.v[e] = *reinterpret_cast<const float *>(line + off + 4 * e);
+            } else {  // V = 2: a pair, which may lie across two words
+                const unsigned *w = reinterpret_cast<const unsigned *>(line + (off & ~3u));
+                const unsigned u = __funnelshift_r(w[0], w[1], (off & 2u) * 8u);
+                v.v[0] = __uint_as_float(u << 16);
+                v.v[V - 1] = __uint_as_float(u & 0xffff0000u);
+            }
+            return v;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxStages; ++i) tc::mbar_init(&full[i], 1);
+        for (int i = 0; i < kMaxStages; ++i) tc::mbar_init(&full[i], kTma ? 1 : kGroup);
         for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(&maps_in[i], 1);
             tc::mbar_init(&state_in[i], 32);
@@ -366,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         tc::fence_mbar_init();
     }
     __syncthreads();
-    for (int i = group; i < p.stages; i += 2) fetch(i, i);
+    for (int i = group; i < p.stages; i += 2) fetch(i, i, item(0), i);
     // round 0 has no state to wait for, but a phase like every other's
     if (threadIdx.x < 32) tc::mbar_arrive(&state_in[0]);
     // the others' shared memory is written from here on
@@ -401,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (p.first && e < here) init.v[e] = p.first[(long long)it.b * p.C + c + e];
+#pragma unroll 8
             for (int q = 0; q < it.piece; ++q)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
@@ -413,23 +482,29 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (e < here) h0.v[e] = p.h0[(long long)it.b * p.C + c + e];
-        if (kTma)
-            wait_for(&full[stage], stage_phase, dead, p.status);
-        else if (kBack || p.stages < 4)  // the newest copies are this round's or the next's
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const G *zt = tile_z(stage) + lane * V;
-        const T *xt = tile_x(stage, 0) + lane * V;
+        wait_for(&full[stage], stage_phase, dead, p.status);
+        // where this thread's rows begin, see values()
+        unsigned at[4] = {}, step[4] = {};
+        if (!kTma)
+#pragma unroll
+            for (int i = 0; i < (kBack ? 4 : 2); ++i) {
+                const Seq &q = p.in[i];
+                const unsigned elem = i == 1 ? sizeof(G) : sizeof(T);
+                const unsigned t = (unsigned)(kBack ? p.N - 1 - s0 : s0) - (i == 2 ? 1u : 0u);
+                step[i] = (kBack ? 0u - (unsigned)q.n : (unsigned)q.n) * elem;
+                at[i] = (unsigned)(uintptr_t)q.p +
+                        ((unsigned)(it.b * q.b) + t * (unsigned)q.n + (unsigned)it.c0) * elem;
+            }
+        const char *zt = tile_z(stage), *xt = tile_x(stage, 0);
         // a and y (backward: a and 1 - a) of the L tokens, and their map
         Vec<V> a[L], y[L], A = all_v<V>(1.f), H = all_v<V>(0.f);
         auto form = [&](auto at_edge) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                const Vec<V> z = widen<G, V>(*reinterpret_cast<const Mem<G, V> *>(zt + row(i) * kRow));
-                Vec<V> x = widen<T, V>(*reinterpret_cast<const Mem<T, V> *>(xt + row(i) * kRow));
-                Vec<V> rest;
-                gate_of<kGate, V>(z, complement, a[i], rest);
+                const Vec<V> z = values((G *)nullptr, zt, at[1], step[1], i);
+                Vec<V> x = values((T *)nullptr, xt, at[0], step[0], i);
+                Vec<V> rest = all_v<V>(0.f);
+                gate_of<kGate, V>(z, complement || (kBack && kGate == LA_GATE_LOGIT), a[i], rest);
                 y[i] = kBack ? rest : complement ? mul_v(rest, x) : x;
                 if (at_edge.value && s0 + i >= it.end) {
                     a[i] = all_v<V>(1.f);
@@ -447,11 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         auto map_at = [&](float *m) { return reinterpret_cast<Vec<V> *>(m); };
         map_at(maps[warp][lane])[0] = A;
         map_at(maps[warp][lane])[1] = H;
-        tc::named_bar_sync(1 + group, 256);
+        tc::named_bar_sync(1 + group, kGroup);
         // forward, everything of this round is in registers now; backward, the
         // group's round before is done with its tiles
-        if (!kBack) fetch(R + p.stages, stage);
-        if (kBack && turn > 0) fetch(R - 2 + p.stages, stage >= 2 ? stage - 2 : stage - 2 + p.stages);
+        if (!kBack) fetch(R + p.stages, stage, it, r + p.stages);
+        if (kBack && turn > 0)
+            fetch(R - 2 + p.stages, stage >= 2 ? stage - 2 : stage - 2 + p.stages, it,
+                  r - 2 + p.stages);
         // The block's map goes to all blocks of the cluster.  Four places for
         // maps: a block sends that of round R + 4 after it has all of round
         // R + 2, whose senders were past round R, the only one that reads R's.
@@ -515,13 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         auto walk = [&](auto at_edge) {
             auto put = [&](auto *dst, const Vec<V> &v) {
                 using E = std::remove_reference_t<decltype(*dst)>;
-                const Mem<E, V> m = narrow<E, V>(v);
-                if (kTma && (!at_edge.value || here == V)) {
-                    *reinterpret_cast<Mem<E, V> *>(dst) = m;
+                if ((kTma || p.out_vec) && (!at_edge.value || here == V)) {
+                    narrow(reinterpret_cast<Mem<E, V> *>(dst), v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        if (e < here) dst[e] = m.v[e];
+                        if (e < here) from_f(dst[e], v.v[e]);
                 }
             };
             T *to = o;
@@ -535,15 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
                     to += p.out[0].n;
                     continue;
                 }
-                auto tile = [&](int which) {
-                    return widen<T, V>(*reinterpret_cast<const Mem<T, V> *>(
-                        tile_x(stage, which) + lane * V + row(i) * kRow));
-                };
-                Vec<V> g = tile(0), h = tile(1);
+                Vec<V> g = values((T *)nullptr, xt, at[0], step[0], i);
+                Vec<V> h = values((T *)nullptr, tile_x(stage, 1), at[2], step[2], i);
                 if (at_edge.value && !ok) g = all_v<V>(0.f);
                 if (at_edge.value && s0 + i == p.N - 1) h = h0;
                 g = add_v(g, state);
-                if (complement) h = fma_v(tile(2), all_v<V>(-1.f), h);
+                if (complement)
+                    h = fma_v(values((T *)nullptr, tile_x(stage, 2), at[3], step[3], i),
+                              all_v<V>(-1.f), h);
                 if (ok) {
                     put(to, complement ? mul_v(y[i], g) : g);
                     Vec<V> dz = mul_v(g, h);
@@ -577,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         for (r += 2; r >= rounds; r -= rounds) ++k;
     }
     if (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (kTma && dead)  // copies may still be under way: leave after them
+    if (dead)  // copies may still be under way: leave after them
         for (int i = max(0, total - p.stages); i < total; ++i)
             tc::mbar_wait(&full[i % p.stages], (unsigned)(i / p.stages) & 1u,
                           clock64() + kWaitCycles, nullptr);
@@ -604,7 +679,7 @@ __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const StepParams
     const int b = (int)(i / p.C), c = (int)(i % p.C);
     auto get = [](const auto *q) {
         using E = std::remove_const_t<std::remove_reference_t<decltype(*q)>>;
-        return widen<E, V>(*reinterpret_cast<const Mem<E, V> *>(q));
+        return widen(reinterpret_cast<const Mem<E, V> *>(q));
     };
     const Vec<V> x = get(static_cast<const T *>(p.x) + b * p.sx + c);
     const Vec<V> z = get(static_cast<const G *>(p.gates) + b * p.sg + c);
@@ -614,8 +689,8 @@ __global__ void __launch_bounds__(kStepThreads) rec_step_kernel(const StepParams
 #pragma unroll
     for (int e = 0; e < V; ++e)
         s.v[e] = fmaf(a.v[e], h.v[e], p.complement ? __fmul_rn(rest.v[e], x.v[e]) : x.v[e]);
-    *reinterpret_cast<Mem<float, V> *>(p.h_out + i) = narrow<float, V>(s);
-    *reinterpret_cast<Mem<T, V> *>(static_cast<T *>(p.out) + b * p.so + c) = narrow<T, V>(s);
+    narrow(reinterpret_cast<Mem<float, V> *>(p.h_out + i), s);
+    narrow(reinterpret_cast<Mem<T, V> *>(static_cast<T *>(p.out) + b * p.so + c), s);
 }
 
 la_status rec_fail(la_status s, const char *who, const char *msg) {
@@ -702,20 +777,25 @@ struct Cut {
     size_t smem;
 };
 
-// The cheapest cut by rounds: a cluster takes ceil(items / clusters) strips, one
-// after the other, each of ceil(steps / (S tile)) rounds and about two more for
-// the start.
+// The cheapest cut, counted in rounds: a cluster takes ceil(items / clusters)
+// strips, one after the other, each of ceil(steps / (S tile)) rounds and about
+// two more for the start.  clusters_of: how many run at once.
 template <typename F>
 Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&clusters_of) {
     const long long items = (long long)p.B * p.strips;
     Cut best{};
     double cost = 0;
-    for (int S = 1; S <= kMaxCluster; ++S) {
-        if (S > 1 && (long long)(S - 1) * tile >= p.N) break;
+    auto stages_of = [&](int S, size_t &smem) {
         const size_t maps = (size_t)kSlots * S * 32 * 2 * V * sizeof(float);
         const int stages = std::min<int>(kMaxStages, (int)((kSmem - maps) / bytes) / 2 * 2);
+        smem = (size_t)stages * bytes + maps;
+        return stages;
+    };
+    for (int S = 1; S <= kMaxCluster; ++S) {
+        if (S > 1 && (long long)(S - 1) * tile >= p.N) break;
+        size_t smem;
+        const int stages = stages_of(S, smem);
         if (stages < least_stages) break;
-        const size_t smem = (size_t)stages * bytes + maps;
         const long long most = clusters_of(S, smem);
         if (most < 1) continue;
         const long long waves = (items + most - 1) / most;
@@ -726,29 +806,54 @@ Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&
             best = {S, (int)std::min(items, most), 1, p.N, stages, smem};
         }
     }
+    // In pieces, of blocks alone: the maps at about 0.6 of a walk, then the
+    // walk, 6 rounds for the second launch and one for each 8 maps to join.  It
+    // has to be clearly less, since it reads the input twice.
+    if (!best.S || items > kFewStrips) return best;
+    size_t smem;
+    const int stages = stages_of(1, smem);
+    const long long most = clusters_of(1, smem);
+    for (int P = 2; P <= kMaxPieces; ++P) {
+        const int steps = (int)(((long long)p.N + (long long)P * tile - 1) / ((long long)P * tile)) * tile;
+        const int pieces = (p.N + steps - 1) / steps;
+        if (pieces != P || steps < 4 * tile) continue;
+        const double rounds = steps / tile + 2;
+        const double c = 0.6 * rounds * (double)((items * (P - 1) + most - 1) / most) +
+                         rounds * (double)((items * P + most - 1) / most) + 6 + P / 8;
+        if (c < 0.9 * cost) {
+            cost = c / 0.9;
+            best = {1, (int)std::min(items * P, most), P, steps, stages, smem};
+        }
+    }
     return best;
 }
 
+struct Workspace {
+    void *p;
+    size_t bytes;
+};
+
 template <typename T, typename G, int V, int kGate, bool kBack>
-cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
+la_status launch_scan(const char *who, Params &p, bool tma, Workspace ws, cudaStream_t stream) {
     constexpr int L = kBack ? 8 : 16, kTile = kWarps * L;
+    auto cuda = [&](cudaError_t e) { return rec_fail(LA_ERR_CUDA, who, cudaGetErrorString(e)); };
     if (tma)
         for (int i = 0; i < (kBack ? 3 + p.complement : 2); ++i)
             if (!make_map(&p.map[i], p.in[i], p.B, p.N, p.C,
                           i == 1 ? (int)sizeof(G) : (int)sizeof(T), 32 * V, kTile))
-                return cudaErrorInvalidValue;
+                return rec_fail(LA_ERR_CUDA, who, "tensor map");
     auto kern = !tma ? rec_scan_kernel<T, G, V, L, kGate, 2, false, kBack>
                 : p.complement ? rec_scan_kernel<T, G, V, L, kGate, 1, true, kBack>
                                : rec_scan_kernel<T, G, V, L, kGate, 0, true, kBack>;
-    cudaError_t e;
-    p.status = device_status_word(&e);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    p.strips = (p.C + 32 * V - 1) / (32 * V);
-    const int bytes = stage_bytes<T, G, V, L, kBack>(p.complement);
+    const int form = tma ? p.complement : 2;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) p.status = device_status_word(&e);  // also bounds dev
+    if (e != cudaSuccess) return cuda(e);
+    // clusters that run at once (one block per SM whatever the stages), looked up
+    // once; 0: not yet, -1: none
+    static std::atomic<int> known[kMaxDevices][3][kMaxCluster + 1];
+    std::atomic<int> *at_once = known[dev][form];
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
@@ -756,44 +861,77 @@ cudaError_t launch_scan(Params &p, bool tma, cudaStream_t stream) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    auto clusters_of = [&](int S, size_t smem) {
-        static std::atomic<int> known[3][kMaxCluster + 1];  // one block per SM whatever the stages
-        std::atomic<int> &n = known[tma ? p.complement : 2][S];
-        if (n.load() == 0) {
+    if (at_once[1].load() == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda(e);
+        for (int S = kMaxCluster; S >= 1; --S) {
             int got = 0;
             cfg.gridDim = dim3((unsigned)S);
-            cfg.dynamicSmemBytes = smem;
+            cfg.dynamicSmemBytes = kSmem;
             at[0].val.clusterDim = {(unsigned)S, 1, 1};
-            if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess)
                 (void)cudaGetLastError();
-                got = 0;
-            }
-            n.store(got > 0 ? got : -1);
+            at_once[S].store(got > 0 ? got : -1);
         }
-        return n.load();
-    };
+    }
+    p.strips = (p.C + 32 * V - 1) / (32 * V);
+    const int bytes = tma ? stage_bytes<T, G, V, L, true, kBack>(p.complement)
+                          : stage_bytes<T, G, V, L, false, kBack>(p.complement);
     // backward, a stage is refilled two rounds after its own
-    const Cut cut = best_cut(p, kTile, bytes, V, kBack ? 4 : 2, clusters_of);
-    if (!cut.S) return cudaErrorInvalidConfiguration;
+    const Cut cut = best_cut(p, kTile, bytes, V, kBack ? 4 : 2,
+                             [&](int S, size_t) { return at_once[S].load(); });
+    if (!cut.S) return rec_fail(LA_ERR_UNSUPPORTED, who, "no kernel configuration fits");
     p.stages = cut.stages;
     p.pieces = cut.pieces;
     p.steps = cut.steps;
-    cfg.gridDim = dim3((unsigned)(cut.clusters * cut.S));
+    void *mine = nullptr;
+    if (cut.pieces > 1) {
+        const size_t need = sizeof(float2) * (size_t)(cut.pieces - 1) * p.B * p.C;
+        if (ws.p) {
+            if (ws.bytes < need || (uintptr_t)ws.p % 16)
+                return rec_fail(LA_ERR_INVALID_ARG, who, "workspace too small or not 16-byte aligned");
+            p.maps = static_cast<float2 *>(ws.p);
+        } else {
+            e = tc_workspace_alloc(&mine, need, stream);
+            if (e != cudaSuccess) {
+                (void)cudaGetLastError();
+                return rec_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
+            }
+            p.maps = static_cast<float2 *>(mine);
+        }
+    }
     cfg.dynamicSmemBytes = cut.smem;
     at[0].val.clusterDim = {(unsigned)cut.S, 1, 1};
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    int launches = 0;
+    for (int pass = cut.pieces > 1 ? 0 : 1; pass < 2 && e == cudaSuccess; ++pass) {
+        p.maps_only = pass == 0;
+        const int items = p.B * p.strips * (cut.pieces - p.maps_only);
+        cfg.gridDim = dim3((unsigned)(std::min(cut.clusters, items) * cut.S));
+        e = cudaLaunchKernelEx(&cfg, kern, p);
+        launches += e == cudaSuccess;
+    }
+    note_launches(launches);
+    if (mine) {
+        const cudaError_t ef = cudaFreeAsync(mine, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? LA_OK : cuda(e);
 }
 
 template <typename T, typename G, int V, bool kBack>
-cudaError_t launch_gate(Params &p, la_gate gate, bool tma, cudaStream_t s) {
-    if (gate == LA_GATE_VALUE) return launch_scan<T, G, V, LA_GATE_VALUE, kBack>(p, tma, s);
-    if (gate == LA_GATE_LOG) return launch_scan<T, G, V, LA_GATE_LOG, kBack>(p, tma, s);
-    return launch_scan<T, G, V, LA_GATE_LOGIT, kBack>(p, tma, s);
+la_status launch_gate(const char *who, Params &p, la_gate gate, bool tma, Workspace ws,
+                      cudaStream_t s) {
+    if (gate == LA_GATE_VALUE)
+        return launch_scan<T, G, V, LA_GATE_VALUE, kBack>(who, p, tma, ws, s);
+    if (gate == LA_GATE_LOG) return launch_scan<T, G, V, LA_GATE_LOG, kBack>(who, p, tma, ws, s);
+    return launch_scan<T, G, V, LA_GATE_LOGIT, kBack>(who, p, tma, ws, s);
 }
 
 template <bool kBack>
 la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dtype gate_dtype,
-                 cudaStream_t s) {
+                 Workspace ws, cudaStream_t s) {
     if ((long long)p.B * ((p.C + 31) / 32) > 2147483647LL / kMaxPieces)
         return rec_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     // a thread takes 4 bytes of x per token: two bf16 channels
@@ -802,17 +940,15 @@ la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dt
     bool tma = true;
     for (int i = 0; i < (kBack ? 3 + p.complement : 2); ++i)
         tma = tma && tma_ok(p.in[i], p.B, p.N, p.C, i == 1 ? ez : ex);
+    p.out_vec = 1;
     for (int i = 0; i < 2; ++i)
-        tma = tma && aligned(p.out[i].p, p.out[i].b, p.out[i].n, p.B, p.N, v, i == 1 ? ez : ex);
+        p.out_vec = p.out_vec && aligned(p.out[i].p, p.out[i].b, p.out[i].n, p.B, p.N, v,
+                                         i == 1 ? ez : ex);
+    tma = tma && p.out_vec;
     using bf16 = __nv_bfloat16;
-    cudaError_t e;
-    if (dtype == LA_F32)
-        e = launch_gate<float, float, 1, kBack>(p, gate, tma, s);
-    else if (gate_dtype == LA_F32)
-        e = launch_gate<bf16, float, 2, kBack>(p, gate, tma, s);
-    else
-        e = launch_gate<bf16, bf16, 2, kBack>(p, gate, tma, s);
-    return done(who, e);
+    if (dtype == LA_F32) return launch_gate<float, float, 1, kBack>(who, p, gate, tma, ws, s);
+    if (gate_dtype == LA_F32) return launch_gate<bf16, float, 2, kBack>(who, p, gate, tma, ws, s);
+    return launch_gate<bf16, bf16, 2, kBack>(who, p, gate, tma, ws, s);
 }
 
 template <typename T, typename G, int V>
@@ -849,7 +985,7 @@ __attribute__((visibility("default")))
 la_status la_forward_recurrence(const void *x, const void *gates, const float *h0, void *out,
                                 float *h_last, const la_seq_strides *strides, int B, int N, int C,
                                 la_gate gate, int complement, la_dtype dtype, la_dtype gate_dtype,
-                                la_stream_t stream) {
+                                void *workspace, size_t workspace_bytes, la_stream_t stream) {
     const char *who = "la_forward_recurrence";
     la_status st = rec_common(who, B, N, C, gate, complement, dtype, gate_dtype);
     if (st != LA_OK) return st;
@@ -876,7 +1012,7 @@ la_status la_forward_recurrence(const void *x, const void *gates, const float *h
     p.N = N;
     p.C = C;
     p.complement = complement;
-    return launch<false>(who, p, gate, dtype, gate_dtype, s);
+    return launch<false>(who, p, gate, dtype, gate_dtype, {workspace, workspace_bytes}, s);
 }
 
 __attribute__((visibility("default")))
@@ -884,7 +1020,8 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
                                  const void *x, const float *h0, const float *dh_last, void *dx,
                                  void *dgates, float *dh0, const la_seq_strides *strides, int B,
                                  int N, int C, la_gate gate, int complement, la_dtype dtype,
-                                 la_dtype gate_dtype, la_stream_t stream) {
+                                 la_dtype gate_dtype, void *workspace, size_t workspace_bytes,
+                                 la_stream_t stream) {
     const char *who = "la_backward_recurrence";
     la_status st = rec_common(who, B, N, C, gate, complement, dtype, gate_dtype);
     if (st != LA_OK) return st;
@@ -922,7 +1059,15 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
     p.N = N;
     p.C = C;
     p.complement = complement;
-    return launch<true>(who, p, gate, dtype, gate_dtype, s);
+    return launch<true>(who, p, gate, dtype, gate_dtype, {workspace, workspace_bytes}, s);
+}
+
+__attribute__((visibility("default")))
+size_t la_recurrence_workspace_bytes(int B, int C, la_dtype dtype) {
+    if (B < 1 || C < 1 || (dtype != LA_F32 && dtype != LA_BF16)) return 0;
+    const long long strips = (C + (dtype == LA_F32 ? 31LL : 63LL)) / (dtype == LA_F32 ? 32 : 64);
+    if (B * strips > kFewStrips) return 0;
+    return sizeof(float2) * (size_t)(kMaxPieces - 1) * B * C;
 }
 
 __attribute__((visibility("default")))

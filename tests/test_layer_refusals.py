@@ -127,7 +127,7 @@ def test_backward_qk_norm_rope_without_rows_or_gradients(lib):
 def rec(lib, x=P[0], z=P[1], h0=None, out=P[2], hl=None, st=None, B=2, N=3, C=8, gate=0, comp=0,
         dtype=1, gdtype=0):
     return lib.la_forward_recurrence(x, z, h0, out, hl, st, B, N, C, gate, comp, dtype, gdtype,
-                                     None)
+                                     None, 0, None)
 
 
 @pytest.mark.parametrize("kw, code, msg", [
@@ -164,7 +164,7 @@ def test_recurrence_empty_problems(lib):
 def rec_back(lib, dout=P[0], z=P[1], out=P[2], x=P[3], dx=P[4], dz=P[5], st=None, comp=1, N=3,
              gdtype=1):
     return lib.la_backward_recurrence(dout, z, out, x, None, None, dx, dz, None, st, 2, N, 8, 0,
-                                      comp, 1, gdtype, None)
+                                      comp, 1, gdtype, None, 0, None)
 
 
 @pytest.mark.parametrize("kw, msg", [
@@ -226,6 +226,10 @@ def test_workspace_query(lib):
     f = lib.la_backward_qk_norm_rope_workspace_bytes
     assert f(0) == 0 and f(257) == 0
     assert f(128) == 2 * f(64) > 0
+    g = lib.la_recurrence_workspace_bytes
+    assert g(0, 8, 1) == g(8, 0, 1) == g(1, 8, 7) == 0
+    assert g(1, 64, 1) > 0 and g(1, 64, 0) > 0
+    assert g(256, 4096, 1) == 0  # enough channels: nothing is cut into pieces
 
 
 def test_rope_frequencies():
