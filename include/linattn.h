@@ -368,7 +368,9 @@ typedef struct {
  * A decode step is N == 1 with one position per sequence.  Sums of squares
  * are fp32; the angle is exact in the position (64-bit fixed-point turns), so
  * far positions lose nothing.  A row's result does not depend on strides or
- * alignment.  One kernel, no workspace.
+ * alignment.  Rows may be read in whole 16-byte units of memory: neighbouring
+ * bytes of a unit that holds part of a row may be read and are not used.  One
+ * kernel, no workspace.
  */
 la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
                           const la_strides *strides, const void *q_weight,

@@ -85,10 +85,13 @@ template <typename T, int V>
 __device__ __forceinline__ void narrow(T *dst, const float *e) {
     if constexpr (sizeof(T) == 2 && V % 2 == 0) {
         struct alignas(2 * V) Words {
-            __nv_bfloat162 u[V / 2];
+            unsigned u[V / 2];
         } w;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) w.u[i] = __floats2bfloat162_rn(e[2 * i], e[2 * i + 1]);
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 pair = __floats2bfloat162_rn(e[2 * i], e[2 * i + 1]);
+            w.u[i] = reinterpret_cast<const unsigned &>(pair);
+        }
         *reinterpret_cast<Words *>(dst) = w;
     } else {
         Pack<T, V> a;
@@ -98,7 +101,7 @@ __device__ __forceinline__ void narrow(T *dst, const float *e) {
     }
 }
 
-// Global to shared memory, zeros where !ok; asynchronous from 4 bytes on.
+// Global to shared memory, 4 bytes or more, zeros where !ok.
 template <typename T, int V>
 __device__ __forceinline__ void fetch(Pack<T, V> *dst, const T *src, bool ok) {
     constexpr int kBytes = (int)sizeof(T) * V;
@@ -109,11 +112,9 @@ __device__ __forceinline__ void fetch(Pack<T, V> *dst, const T *src, bool ok) {
     else if (kBytes == 8)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src),
                      "r"(ok ? 8 : 0) : "memory");
-    else if (kBytes == 4)
+    else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src),
                      "r"(ok ? 4 : 0) : "memory");
-    else
-        for (int e = 0; e < V; ++e) dst->v[e] = ok ? src[e] : T(0.f);
 }
 
 __device__ __forceinline__ float weight_at(const void *w, int w_bf16, int i) {
@@ -182,9 +183,17 @@ __device__ __forceinline__ void row_sum(float2 (&t)[N][K][P], int bits, float (&
 // Rows in flight per thread.
 template <bool kBack>
 constexpr int ring_depth() { return kBack ? 3 : 4; }
+// Single bf16 values cannot be copied asynchronously: the lanes of a row copy the
+// 16-byte units of memory that hold it, wherever it begins in the first of them.
+template <typename T, int V>
+constexpr bool whole_rows() { return sizeof(T) * V < 4; }
+// Bytes that a row's units take.
+__host__ __device__ inline int row_units(int d) { return (2 * d + 14 + 15) / 16 * 16; }
 template <typename T, int V, int K, bool kBack>
-constexpr int ring_bytes() {
-    return ring_depth<kBack>() * (kBack ? 2 : 1) * K * 2 * kThreads * V * (int)sizeof(T);
+int ring_bytes(int d, int lane_bits) {
+    return ring_depth<kBack>() * (kBack ? 2 : 1) *
+           (whole_rows<T, V>() ? (kThreads >> lane_bits) * row_units(d)
+                               : K * 2 * kThreads * V * (int)sizeof(T));
 }
 
 // A row is shared by 2^lane_bits lanes of a warp.  A lane takes K chunks of V
@@ -199,12 +208,14 @@ constexpr int ring_bytes() {
 // the rows of all tiles form one list, of which every block takes an equal piece.
 // Angles are formed once per token and lane and serve the tile's rows.  Rows
 // travel through a ring in shared memory, filled by cp.async some rows ahead;
-// every thread reads only what it copied itself, so the ring needs no barrier.
+// every thread reads only what it copied itself, so the ring needs no barrier
+// (with whole_rows, what its row's lanes copied: a warp barrier).
 // Backward, the sums of g n stay in registers until the block's end.
 template <typename T, int V, int K, bool kInter, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_constant__ Params p) {
     constexpr int P = (V + 1) / 2;  // packed pairs per chunk (V = 1: half of one)
     constexpr int kDepth = ring_depth<kBack>(), kSrc = kBack ? 2 : 1;
+    constexpr bool kWhole = whole_rows<T, V>();
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long turns[kMaxPairs];
     __shared__ float weight[LA_MAX_D];
@@ -253,6 +264,17 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         return ring + (((depth * kSrc + src) * K + j) * 2 + half) * kThreads;
     };
 
+    auto row_slot = [&](int depth, int src) {  // with kWhole
+        return smem + ((depth * kSrc + src) * (kThreads >> bits) + group) * row_units(p.d);
+    };
+    auto fetch_units = [&](char *dst, const T *src) {
+        const uintptr_t at = (uintptr_t)src, from = at & ~(uintptr_t)15;
+        const int end = (int)(at & 15) + p.d * (int)sizeof(T);
+        for (int u = 16 * lane; u < end; u += 16 << bits)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             (unsigned)__cvta_generic_to_shared(dst + u)), "l"(from + u) : "memory");
+    };
+
     // the copying side of the ring
     long long f_it = it0, f_tile = it0 / rows;
     int f_row = (int)(it0 - f_tile * rows), f_depth = 0;
@@ -273,8 +295,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             const bool ok = f_ok && head_in + f_row * head_step < H;
             const T *x = ok ? fx : static_cast<const T *>(sd.x);
             const T *g = ok ? fg : static_cast<const T *>(sd.dy);
+            if (kWhole && ok) {
+                if (!kBack || p.norm) fetch_units(row_slot(f_depth, 0), x);
+                if (kBack) fetch_units(row_slot(f_depth, kSrc - 1), g);
+            }
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
+            for (int j = 0; j < K && !kWhole; ++j) {
                 const bool l = ok && l_ok[j], h = ok && h_ok[j];
                 if (!kBack || p.norm) {
                     fetch<T, V>(slot(f_depth, 0, j, 0), l ? x + lo[j] : x, l);
@@ -299,11 +325,19 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     };
     for (int i = 0; i < kDepth - 1; ++i) fetch_row();
 
-    // one vector pair of a slot as the pairs' first and second values
-    auto open = [&](const Pack<T, V> *l, const Pack<T, V> *h, float2 (&m0)[P], float2 (&m1)[P]) {
+    // chunk j of source src in a place of the ring, as the pairs' first and
+    // second values; `at` is the row's address where whole rows are copied
+    auto open = [&](int depth, int src, int j, bool ok, unsigned at, float2 (&m0)[P],
+                    float2 (&m1)[P]) {
         float e[2 * V];
-        widen(l, e);
-        widen(h, e + V);
+        if constexpr (kWhole) {
+            const T *r = reinterpret_cast<const T *>(row_slot(depth, src) + (at & 15u));
+            e[0] = ok && l_ok[j] ? to_f(r[lo[j]]) : 0.f;
+            e[1] = ok && h_ok[j] ? to_f(r[hi[j]]) : 0.f;
+        } else {
+            widen(slot(depth, src, j, 0), e);
+            widen(slot(depth, src, j, 1), e + V);
+        }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             if (V == 1) {
@@ -365,21 +399,31 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                 (e % 2 ? cs[j][e / 2].y : cs[j][e / 2].x) = c;
                 (e % 2 ? sn[j][e / 2].y : sn[j][e / 2].x) = s;
             }
+        unsigned at_x = 0, at_g = 0;  // addresses of the rows, with kWhole
+        if (kWhole) {
+            const long long h = head_in + row * head_step;
+            at_x = (unsigned)((uintptr_t)sd.x +
+                              (b * sd.sx.b + n * sd.sx.n + h * sd.sx.h) * sizeof(T));
+            at_g = (unsigned)((uintptr_t)sd.dy +
+                              (b * sd.sdy.b + n * sd.sdy.n + h * sd.sdy.h) * sizeof(T));
+        }
         for (; row < rows && it < it1; ++row, ++it, y += y_step) {
+            if (kWhole) __syncwarp();  // the place that is filled next has been read
             fetch_row();
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            if (kWhole) __syncwarp();
             const bool ok = t_ok && head_in + row * head_step < H;
 
             float2 v0[K][P], v1[K][P], g0[K][P], g1[K][P], t[kSrc][K][P];
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 if (!kBack || p.norm) {
-                    open(slot(depth, 0, j, 0), slot(depth, 0, j, 1), v0[j], v1[j]);
+                    open(depth, 0, j, ok, at_x, v0[j], v1[j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < P; ++i) v0[j][i] = v1[j][i] = make_float2(0.f, 0.f);
                 }
-                if (kBack) open(slot(depth, kSrc - 1, j, 0), slot(depth, kSrc - 1, j, 1), g0[j], g1[j]);
+                if (kBack) open(depth, kSrc - 1, j, ok, at_g, g0[j], g1[j]);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     t[0][j][i] = __ffma2_rn(v0[j][i], v0[j][i], __fmul2_rn(v1[j][i], v1[j][i]));
@@ -435,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                 if (ok && h_ok[j]) narrow<T, V>(y + hi[j], e + V);
             }
             depth = depth + 1 == kDepth ? 0 : depth + 1;
+            at_x += (unsigned)(fx_step * sizeof(T));
+            at_g += (unsigned)(fg_step * sizeof(T));
         }
         row = 0;
         ++tile;
@@ -559,7 +605,8 @@ cudaError_t launch_rows(const Params &p, unsigned blocks, cudaStream_t stream) {
     auto kern = p.interleaved ? qk_rows_kernel<T, V, K, true, kBack>
                               : qk_rows_kernel<T, V, K, false, kBack>;
     // the sums of the weight gradient, 8 rows of LA_MAX_D, share the ring
-    const int smem = std::max(ring_bytes<T, V, K, kBack>(), kThreads / 32 * LA_MAX_D * 4);
+    const int smem = std::max(ring_bytes<T, V, K, kBack>(p.d, p.lane_bits),
+                              kThreads / 32 * LA_MAX_D * 4);
     if (smem > 40 * 1024) {  // 48 KB with the static arrays need no attribute
         const cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -580,7 +627,9 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
     const int v = vector_of(p, 16 / (int)sizeof(T), (int)sizeof(T));
     const int chunks = ((p.d + 1) / 2 + v - 1) / v;  // of a row
-    while ((1 << p.lane_bits) < chunks && p.lane_bits < 5) ++p.lane_bits;
+    // chunks per lane: one of 4 or 8 pairs, up to two of 2, up to four of 1
+    const int per_lane = v >= 4 ? 1 : v == 2 ? (chunks > 32 ? 2 : 1) : (chunks > 64 ? 4 : 2);
+    while (per_lane << p.lane_bits < chunks) ++p.lane_bits;
     const int groups = kThreads >> p.lane_bits;
     const long long tokens = (long long)p.B * p.N;
     while ((1 << p.token_bits) < groups && (1 << p.token_bits) < tokens) ++p.token_bits;
@@ -617,8 +666,12 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
         e = launch_rows<T, sizeof(T) == 2 ? 8 : 4, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 4)
         e = launch_rows<T, 4, 1, kBack>(p, (unsigned)blocks, stream);
+    else if (v == 2 && per_lane == 1)
+        e = launch_rows<T, 2, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 2)
         e = launch_rows<T, 2, 2, kBack>(p, (unsigned)blocks, stream);
+    else if (per_lane == 2)
+        e = launch_rows<T, 1, 2, kBack>(p, (unsigned)blocks, stream);
     else
         e = launch_rows<T, 1, 4, kBack>(p, (unsigned)blocks, stream);
     if (e == cudaSuccess) note_launches(1);
