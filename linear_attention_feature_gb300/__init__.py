@@ -10,7 +10,6 @@ on a CUDA device, the call raises.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
 import os
 import struct
@@ -144,6 +143,20 @@ def _torch():
     return torch
 
 
+_CODES = {}
+
+
+def _code(dtype) -> int:
+    """LA_F32 or LA_BF16."""
+    if not _CODES:
+        torch = _torch()
+        _CODES[torch.float32], _CODES[torch.bfloat16] = LA_F32, LA_BF16
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return code
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.float32:
@@ -167,19 +180,24 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_AS_IS = contextlib.nullcontext()
+class _Device:
+    """The CUDA device of a call as the current one (with nothing to do where
+    it is already), and the stream that the call goes to."""
 
+    __slots__ = ("back", "stream")
 
-def _on(device):
-    """`device` as the current CUDA device while the library is called."""
-    torch = _torch()
-    return _AS_IS if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    def __init__(self, device, stream):
+        get = _torch()._C
+        index, now = device.index, get._cuda_getDevice()
+        self.back = None if index == now else now
+        if index != now:
+            _torch().cuda.set_device(index)
+        self.stream = stream.cuda_stream if stream is not None \
+            else get._cuda_getCurrentRawStream(index)
 
-
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    def leave(self):
+        if self.back is not None:
+            _torch().cuda.set_device(self.back)
 
 
 def _decay_arg(decay, H):
@@ -445,86 +463,87 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0):
 _ROPE = struct.Struct("@PiiPiqqq")
 
 
-def _rope(frequencies, positions, offset, interleaved, q):
-    """The packed la_rope (None: no rotation) and what has to outlive the call."""
+def _rope(frequencies, positions, offset, interleaved, shape, device):
+    """The packed la_rope (None: no rotation) and what has to outlive the call;
+    `shape`: q's."""
     if frequencies is None or len(frequencies) == 0:
         return None, None
     f = frequencies
     if not (isinstance(f, array.array) and f.typecode == "d"):
         f = array.array("d", [float(x) for x in f])
-    ptr, nbytes, sb, sn = 0, 0, 0, 0
-    if positions is not None:
-        torch = _torch()
-        shape, st = positions.shape, positions.stride()
-        want = q.shape[:1] if q.dim() == 3 else (q.shape[0], q.shape[2])
-        if shape == want:
-            sb, sn = (st[0], 0) if q.dim() == 3 else st
-        elif q.dim() == 4 and shape == want[1:]:
-            sn = st[0]
-        else:
-            raise ValueError(f"positions must have the shape {list(want)}"
-                             + (f" or {list(want[1:])}" if q.dim() == 4 else ""))
-        if positions.dtype == torch.int64:
-            nbytes = 8
-        elif positions.dtype == torch.int32:
-            nbytes = 4
-        else:
-            raise TypeError("positions must be int32 or int64")
-        if positions.device != q.device:
-            raise ValueError("positions must be on q's CUDA device")
-        ptr = positions.data_ptr()
-    return _ROPE.pack(f.buffer_info()[0], 2 * len(f), bool(interleaved), ptr, nbytes, sb, sn,
-                      offset), f
+    if positions is None:
+        return _ROPE.pack(f.buffer_info()[0], 2 * len(f), bool(interleaved), 0, 0, 0, 0, offset), f
+    st, sb, sn = positions.stride(), 0, 0
+    have, want = positions.shape, shape[:1] if len(shape) == 3 else (shape[0], shape[2])
+    if have == want:
+        sb, sn = (st[0], 0) if len(st) == 1 else st
+    elif len(shape) == 4 and have == want[1:]:
+        sn = st[0]
+    else:
+        raise ValueError(f"positions must have the shape {list(want)}"
+                         + (f" or {list(want[1:])}" if len(shape) == 4 else ""))
+    nbytes = positions.element_size()
+    if positions.is_floating_point() or nbytes not in (4, 8) or not positions.dtype.is_signed:
+        raise TypeError("positions must be int32 or int64")
+    if positions.device != device:
+        raise ValueError("positions must be on q's CUDA device")
+    return _ROPE.pack(f.buffer_info()[0], 2 * len(f), bool(interleaved), positions.data_ptr(),
+                      nbytes, sb, sn, offset), f
 
 
-def _check_rows(like, *ts):
-    """Tensors of rows: one dtype, one CUDA device, the last dimension contiguous."""
-    device, dtype = like.device, like.dtype
-    if not like.is_cuda:
+_STRIDES = {n: struct.Struct(f"@{n}q") for n in (3, 6, 12, 18)}
+
+
+def _check_rows(q, *ts):
+    """Tensors of rows with q's dtype and CUDA device and a contiguous last
+    dimension; returns the packed la_strides of all but q."""
+    if not q.is_cuda:
         raise ValueError("all tensors must be on a CUDA device")
+    device, dtype, v = q.device, q.dtype, []
     for t in ts:
         if t.device != device:
             raise ValueError("all tensors must be on one CUDA device")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("q, k, their outputs and gradients must share one dtype")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("the last dimension must be contiguous")
-
-
-def _row_strides(*ts):
-    """la_strides of [B, H, N, d] or [B, H, d] tensors."""
-    v = []
-    for t in ts:
         s = t.stride()
+        if s[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous")
         v += s[:3] if len(s) == 4 else (s[0], s[1], 0)
-    return struct.pack(f"@{len(v)}q", *v)
+    return _STRIDES[len(v)].pack(*v)
 
 
-def _weights(q_weight, k_weight, d, like):
+def _weights(q_weight, k_weight, d, device):
     """(q_weight's and k_weight's pointers or None, their dtype code)."""
-    ptr, code = [None, None], None
-    for i, w in enumerate((q_weight, k_weight)):
+    pq = pk = None
+    for w in (q_weight, k_weight):
         if w is None:
             continue
-        if w.dim() != 1 or w.shape[0] != d:
+        if w.shape != (d,):
             raise ValueError(f"a weight must have the shape [{d}]")
-        if w.device != like.device:
+        if w.device != device:
             raise ValueError("the weights must be on q's CUDA device")
-        if not w.is_contiguous():
+        if w.stride(0) != 1 and d > 1:
             raise ValueError("a weight must be contiguous")
-        if code is not None and w.dtype != q_weight.dtype:
-            raise TypeError("q_weight and k_weight must share one dtype")
-        ptr[i], code = w.data_ptr(), _dtype_code(w)
-    return ptr[0], ptr[1], code or LA_F32
+    if q_weight is not None:
+        pq, dtype = q_weight.data_ptr(), q_weight.dtype
+        if k_weight is not None:
+            if k_weight.dtype is not dtype:
+                raise TypeError("q_weight and k_weight must share one dtype")
+            pk = k_weight.data_ptr()
+        return pq, pk, _code(dtype)
+    if k_weight is not None:
+        return None, k_weight.data_ptr(), _code(k_weight.dtype)
+    return None, None, LA_F32
 
 
-def _check_qk(q, k):
-    qs, ks = q.shape, k.shape
-    if len(qs) not in (3, 4) or len(ks) != len(qs):
+def _check_qk(qs, ks):
+    """B, Hq, Hk, N, d of q's and k's shapes."""
+    n = len(qs)
+    if n not in (3, 4) or len(ks) != n:
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if ks[0] != qs[0] or ks[2:] != qs[2:]:
         raise ValueError("q and k may differ in the number of heads only")
-    return qs[0], qs[1], ks[1], qs[2] if len(qs) == 4 else 1, qs[-1]
+    return qs[0], qs[1], ks[1], qs[2] if n == 4 else 1, qs[-1]
 
 
 def _contiguous_like(t):
@@ -548,23 +567,27 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     int32 or int64 [B, N] or [N] ([B] for one token), or None for 0..N-1;
     `offset` is added.  interleaved: pairs (2i, 2i+1) instead of (i, i + R/2).
     Returns (q_out, k_out)."""
-    B, Hq, Hk, N, d = _check_qk(q, k)
+    qs, ks, device = q.shape, k.shape, q.device
+    B, Hq, Hk, N, d = _check_qk(qs, ks)
     if q_out is None:
         q_out = _contiguous_like(q)
     if k_out is None:
         k_out = _contiguous_like(k)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    if q_out.shape != qs or k_out.shape != ks:
         raise ValueError("q_out and k_out must have the shapes of q and k")
-    _check_rows(q, q, k, q_out, k_out)
-    wq, wk, wcode = _weights(q_weight, k_weight, d, q)
-    rope, keep = _rope(frequencies, positions, offset, interleaved, q)
-    device = q.device
-    with _on(device):
-        st = load_library().la_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-            _row_strides(q, k, q_out, k_out), wq, wk, bool(norm), eps, rope, B, Hq, Hk, N, d,
-            _dtype_code(q), wcode, _raw_stream(stream, device))
-    _raise_if(st)
+    strides = _check_rows(q, q, k, q_out, k_out)
+    wq, wk, wcode = _weights(q_weight, k_weight, d, device)
+    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
+    code, lib = _code(q.dtype), load_library()
+    on = _Device(device, stream)
+    try:
+        st = lib.la_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), strides, wq, wk,
+            bool(norm), eps, rope, B, Hq, Hk, N, d, code, wcode, on.stream)
+    finally:
+        on.leave()
+    if st:
+        _raise_if(st)
     return q_out, k_out
 
 
@@ -577,20 +600,22 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     there is no weight.  dq and dk take any strides, such as views of a fused
     projection's gradient (default: laid out like q and k)."""
     torch = _torch()
-    B, Hq, Hk, N, d = _check_qk(q, k)
-    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+    qs, ks, device = q.shape, k.shape, q.device
+    B, Hq, Hk, N, d = _check_qk(qs, ks)
+    if dq_out.shape != qs or dk_out.shape != ks:
         raise ValueError("dq_out and dk_out must have the shapes of q and k")
     if dq is None:
         dq = torch.empty_like(q)
     if dk is None:
         dk = torch.empty_like(k)
-    if dq.shape != q.shape or dk.shape != k.shape:
+    if dq.shape != qs or dk.shape != ks:
         raise ValueError("dq and dk must have the shapes of q and k")
-    _check_rows(q, dq_out, dk_out, q, k, dq, dk)
-    wq, wk, wcode = _weights(q_weight, k_weight, d, q)
-    device, lib = q.device, load_library()
-    rope, keep = _rope(frequencies, positions, offset, interleaved, q)
-    with _on(device):
+    strides = _check_rows(q, dq_out, dk_out, q, k, dq, dk)
+    wq, wk, wcode = _weights(q_weight, k_weight, d, device)
+    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
+    code, lib = _code(q.dtype), load_library()
+    on = _Device(device, stream)
+    try:
         dwq = dwk = ws = None
         ws_bytes = 0
         if wq is not None:
@@ -604,10 +629,12 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         st = lib.la_backward_qk_norm_rope(
             dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), _ptr(dwq), _ptr(dwk), _row_strides(dq_out, dk_out, q, k, dq, dk), wq,
-            wk, bool(norm), eps, rope, B, Hq, Hk, N, d, _dtype_code(q), wcode, _ptr(ws), ws_bytes,
-            _raw_stream(stream, device))
-    _raise_if(st)
+            dk.data_ptr(), _ptr(dwq), _ptr(dwk), strides, wq, wk, bool(norm), eps, rope, B, Hq,
+            Hk, N, d, code, wcode, _ptr(ws), ws_bytes, on.stream)
+    finally:
+        on.leave()
+    if st:
+        _raise_if(st)
     return dq, dk, dwq, dwk
 
 
@@ -627,11 +654,11 @@ def _check_seq(x, gates, *ts):
     for t in ts:
         if t.shape != shape:
             raise ValueError("x, gates, out and the gradients must share one shape")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("x, out and the gradients must share one dtype")
     if gates.shape != shape:
         raise ValueError("x, gates, out and the gradients must share one shape")
-    if gates.dtype != dtype and gates.dtype != _torch().float32:
+    if gates.dtype is not dtype and gates.dtype is not _torch().float32:
         raise TypeError("gates must be float32 or of x's dtype")
     if not x.is_cuda:
         raise ValueError("all tensors must be on one CUDA device")
@@ -642,14 +669,14 @@ def _check_seq(x, gates, *ts):
             raise ValueError("the last dimension must be contiguous")
 
 
-def _check_state(B, C, like, *hs):
+def _check_state(B, C, device, *hs):
     float32 = _torch().float32
     for h in hs:
         if h is None:
             continue
-        if h.dim() != 2 or h.shape[0] != B or h.shape[1] != C or h.dtype != float32:
+        if h.shape != (B, C) or h.dtype is not float32:
             raise ValueError("a state must be float32 [B, C]")
-        if h.device != like.device:
+        if h.device != device:
             raise ValueError("all tensors must be on one CUDA device")
         if not h.is_contiguous():
             raise ValueError("a state must be contiguous")
@@ -659,23 +686,23 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _recurrence_workspace(B, C, like, stream):
+def _recurrence_workspace(lib, B, C, code, device, stream):
     """(workspace or None, bytes): on the current stream torch's allocator
     gives it; the library allocates on another one."""
     if stream is not None:
         return None, 0
-    n = load_library().la_recurrence_workspace_bytes(B, C, _dtype_code(like))
+    n = lib.la_recurrence_workspace_bytes(B, C, code)
     if n == 0:
         return None, 0
     torch = _torch()
-    return torch.empty(n, dtype=torch.uint8, device=like.device), n
+    return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
 def _seq_strides(*ts):
     v = []
     for t in ts:
         v += (0, 0) if t is None else t.stride()[:2]
-    return struct.pack(f"@{len(v)}q", *v)
+    return _STRIDES[len(v)].pack(*v)
 
 
 def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = "value",
@@ -693,18 +720,24 @@ def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = 
     if out is None:
         out = _contiguous_like(x)
     B, N, C = x.shape
+    device = x.device
     if h_last is None:
-        h_last = torch.empty(B, C, dtype=torch.float32, device=x.device)
-    code = _gate(gate)
+        h_last = torch.empty(B, C, dtype=torch.float32, device=device)
+    form = _gate(gate)
     _check_seq(x, gates, out)
-    _check_state(B, C, x, h0, h_last)
-    with _on(x.device):
-        ws, ws_bytes = _recurrence_workspace(B, C, x, stream)
-        st = load_library().la_forward_recurrence(
+    _check_state(B, C, device, h0, h_last)
+    code, gcode, lib = _code(x.dtype), _code(gates.dtype), load_library()
+    on = _Device(device, stream)
+    try:
+        ws, ws_bytes = _recurrence_workspace(lib, B, C, code, device, stream)
+        st = lib.la_forward_recurrence(
             x.data_ptr(), gates.data_ptr(), _ptr(h0), out.data_ptr(), h_last.data_ptr(),
-            _seq_strides(x, gates, out), B, N, C, code, bool(complement), _dtype_code(x),
-            _dtype_code(gates), _ptr(ws), ws_bytes, _raw_stream(stream, x.device))
-    _raise_if(st)
+            _seq_strides(x, gates, out), B, N, C, form, bool(complement), code, gcode, _ptr(ws),
+            ws_bytes, on.stream)
+    finally:
+        on.leave()
+    if st:
+        _raise_if(st)
     return out, h_last
 
 
@@ -721,29 +754,34 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
     if complement and x is None:
         raise ValueError("x is needed with complement")
     B, N, C = dout.shape
+    device = dout.device
     if dx is None:
         dx = _contiguous_like(dout)
     if dgates is None:
         dgates = _contiguous_like(gates)
     if dh0 is None:
-        dh0 = torch.empty(B, C, dtype=torch.float32, device=dout.device)
-    code = _gate(gate)
+        dh0 = torch.empty(B, C, dtype=torch.float32, device=device)
+    form = _gate(gate)
     if not complement:
         x = None
     _check_seq(dout, gates, out, dx, *([x] if x is not None else []))
-    if dgates.dtype != gates.dtype:
+    if dgates.dtype is not gates.dtype:
         raise TypeError("dgates must have the dtype of gates")
     _check_seq(dout, dgates)
-    _check_state(B, C, dout, h0, dh_last, dh0)
-    with _on(dout.device):
-        ws, ws_bytes = _recurrence_workspace(B, C, dout, stream)
-        st = load_library().la_backward_recurrence(
+    _check_state(B, C, device, h0, dh_last, dh0)
+    code, gcode, lib = _code(dout.dtype), _code(gates.dtype), load_library()
+    on = _Device(device, stream)
+    try:
+        ws, ws_bytes = _recurrence_workspace(lib, B, C, code, device, stream)
+        st = lib.la_backward_recurrence(
             dout.data_ptr(), gates.data_ptr(), out.data_ptr(), _ptr(x), _ptr(h0),
             _ptr(dh_last), dx.data_ptr(), dgates.data_ptr(), dh0.data_ptr(),
-            _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, code, bool(complement),
-            _dtype_code(dout), _dtype_code(gates), _ptr(ws), ws_bytes,
-            _raw_stream(stream, dout.device))
-    _raise_if(st)
+            _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, form, bool(complement),
+            code, gcode, _ptr(ws), ws_bytes, on.stream)
+    finally:
+        on.leave()
+    if st:
+        _raise_if(st)
     return dx, dgates, dh0
 
 
@@ -759,16 +797,21 @@ def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "va
     if h_out is None:
         h_out = h
     B, C = x.shape
-    code = _gate(gate)
+    device = x.device
+    form = _gate(gate)
     _check_seq(x, gates, out)
-    _check_state(B, C, x, h, h_out)
-    with _on(x.device):
-        st = load_library().la_decode_step_recurrence(
+    _check_state(B, C, device, h, h_out)
+    code, gcode, lib = _code(x.dtype), _code(gates.dtype), load_library()
+    on = _Device(device, stream)
+    try:
+        st = lib.la_decode_step_recurrence(
             h.data_ptr(), h_out.data_ptr(), x.data_ptr(), gates.data_ptr(), out.data_ptr(),
-            struct.pack("@3q", x.stride(0), gates.stride(0), out.stride(0)), B, C, code,
-            bool(complement), _dtype_code(x), _dtype_code(gates),
-            _raw_stream(stream, x.device))
-    _raise_if(st)
+            _STRIDES[3].pack(x.stride(0), gates.stride(0), out.stride(0)), B, C, form,
+            bool(complement), code, gcode, on.stream)
+    finally:
+        on.leave()
+    if st:
+        _raise_if(st)
     return out
 
 

@@ -759,6 +759,13 @@ la_strides contiguous(int H, int N, int d) {
     return {(long long)H * N * d, (long long)N * d, d};
 }
 
+// Whether every pointer of a side is a multiple of its element's size.
+bool elements_aligned(const Side &s, la_dtype dtype, la_dtype weight_dtype) {
+    const uintptr_t elem = dtype == LA_F32 ? 4 : 2, w = weight_dtype == LA_BF16 ? 2 : 4;
+    return (uintptr_t)s.x % elem == 0 && (uintptr_t)s.dy % elem == 0 &&
+           (uintptr_t)s.y % elem == 0 && (uintptr_t)s.w % w == 0 && (uintptr_t)s.dw % 4 == 0;
+}
+
 bool negative(const la_strides &s) { return s.b < 0 || s.h < 0 || s.n < 0; }
 
 }  // namespace
@@ -788,6 +795,8 @@ la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out
         s.sx = strides ? strides[i] : contiguous(s.H, N, d);
         s.sy = strides ? strides[2 + i] : contiguous(s.H, N, d);
         if (!s.x || !s.y) return qk_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+        if (!elements_aligned(s, dtype, weight_dtype))
+            return qk_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
         if (negative(s.sx) || negative(s.sy))
             return qk_fail(LA_ERR_INVALID_ARG, who, "negative stride");
         if (!rows_disjoint(s.sy, B, s.H, N, d))
@@ -836,6 +845,8 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
         sd.dw = dw[i];
         if (!sd.dy || !sd.y || (norm && !sd.x))
             return qk_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+        if (!elements_aligned(sd, dtype, weight_dtype))
+            return qk_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
         if (negative(sd.sx) || negative(sd.sy) || negative(sd.sdy))
             return qk_fail(LA_ERR_INVALID_ARG, who, "negative stride");
         if (!rows_disjoint(sd.sy, B, sd.H, N, d))

@@ -2,6 +2,8 @@
 // forward scan and the step of one token (la_forward_recurrence,
 // la_backward_recurrence, la_decode_step_recurrence in include/linattn.h).  The
 // scan itself is in la_recurrence.cuh.
+#include <initializer_list>
+
 #include "la_recurrence.cuh"
 
 namespace la {
@@ -68,6 +70,13 @@ bool rows_disjoint(long long b, long long n, int B, int N, int C) {
     return b >= n ? n >= C && b >= n * (N - 1) + C : b >= C && n >= b * (B - 1) + C;
 }
 
+// Whether every pointer (may be NULL) is a multiple of its element's size.
+bool elements_aligned(int elem, std::initializer_list<const void *> ps) {
+    for (const void *q : ps)
+        if ((uintptr_t)q % (uintptr_t)elem) return false;
+    return true;
+}
+
 la_seq_strides pick(const la_seq_strides *s, int i, int N, int C) {
     return s ? s[i] : la_seq_strides{(long long)N * C, C};
 }
@@ -130,6 +139,10 @@ la_status la_forward_recurrence(const void *x, const void *gates, const float *h
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (N == 0) return rec_copy(who, h_last, h0, (size_t)B * C, s);
     if (!x || !gates || !out) return rec_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+    if (!elements_aligned(dtype == LA_F32 ? 4 : 2, {x, out}) ||
+        !elements_aligned(gate_dtype == LA_F32 ? 4 : 2, {gates}) ||
+        !elements_aligned(4, {h0, h_last}))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
     const la_seq_strides sx = pick(strides, 0, N, C), sg = pick(strides, 1, N, C),
                          so = pick(strides, 2, N, C);
     if (sx.b < 0 || sx.n < 0 || sg.b < 0 || sg.n < 0 || so.b < 0 || so.n < 0)
@@ -167,6 +180,10 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
     if (N == 0) return rec_copy(who, dh0, dh_last, (size_t)B * C, s);
     if (!dout || !gates || !out || !dx || !dgates || (complement && !x))
         return rec_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+    if (!elements_aligned(dtype == LA_F32 ? 4 : 2, {dout, out, x, dx}) ||
+        !elements_aligned(gate_dtype == LA_F32 ? 4 : 2, {gates, dgates}) ||
+        !elements_aligned(4, {h0, dh_last, dh0}))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
     la_seq_strides ss[6];
     for (int i = 0; i < 6; ++i) {
         if (i == 3 && !complement) {
@@ -204,7 +221,7 @@ size_t la_recurrence_workspace_bytes(int B, int C, la_dtype dtype) {
     if (B < 1 || C < 1 || (dtype != LA_F32 && dtype != LA_BF16)) return 0;
     const long long strips = (C + (dtype == LA_F32 ? 31LL : 63LL)) / (dtype == LA_F32 ? 32 : 64);
     if (B * strips > kFewStrips) return 0;
-    return sizeof(float2) * (size_t)(kMaxPieces - 1) * B * C;
+    return (sizeof(float2) * (kMaxPieces - 1) + sizeof(float)) * (size_t)B * C;
 }
 
 __attribute__((visibility("default")))
@@ -218,6 +235,10 @@ la_status la_decode_step_recurrence(const float *h, float *h_out, const void *x,
     if (B == 0 || C == 0) return LA_OK;
     if (!h || !h_out || !x || !gates || !out)
         return rec_fail(LA_ERR_INVALID_ARG, who, "null pointer");
+    if (!elements_aligned(dtype == LA_F32 ? 4 : 2, {x, out}) ||
+        !elements_aligned(gate_dtype == LA_F32 ? 4 : 2, {gates}) ||
+        !elements_aligned(4, {h, h_out}))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
     const long long sx = strides ? strides[0] : C, sg = strides ? strides[1] : C,
                     so = strides ? strides[2] : C;
     if (sx < 0 || sg < 0 || so < 0) return rec_fail(LA_ERR_INVALID_ARG, who, "negative stride");

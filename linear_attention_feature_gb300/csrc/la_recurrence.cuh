@@ -28,8 +28,8 @@
 //
 // Rows that TMA tiles cannot take (strides or bases that are not multiples of 16
 // bytes) come by cp.async: the 16-byte units of memory that hold the strip's
-// part of the row, wherever it begins in the first of them.  (A bulk copy per
-// row was slower, 400 against XXX us at 2 x 32768 x 2047 bf16.)
+// part of the row, wherever it begins in the first of them (2 x 32768 x 2047
+// bf16: 338 us; with a bulk copy per row 401 us).
 //
 // Where even clusters would leave most SMs idle (few channels, long sequences),
 // a sequence is cut into pieces and walked twice: once for the maps of the
@@ -238,6 +238,7 @@ struct Params {
     // `maps`, [piece][B][C] of (A, H); the next one starts each piece from them.
     int pieces, steps, maps_only;
     float2 *maps;
+    float *start;  // [B][C]: the state before the first piece, as maps_only found it
 };
 
 // Bytes of a tile's row: 32 V values, and where rows begin anywhere in a unit of
@@ -475,19 +476,37 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             if (kBack) oz = static_cast<G *>(p.out[1].p) + it.b * p.out[1].b + t0 * p.out[1].n + c;
         }
         const bool edge = s0 + L >= it.end || part;  // masks are needed
+        // The state before the item's first token enters the map of the first
+        // warp, and is read by that warp alone: it has been used when the state
+        // behind the last token is written, which may be to the same place.
         Vec<V> init = all_v<V>(0.f), h0 = all_v<V>(0.f);
-        if (r == 0 && !p.maps_only) {  // the state before the item's first token
+        const bool begins = r == 0 && rank == 0 && warp == 0;
+        if (begins) {
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (p.first && e < here) init.v[e] = p.first[(long long)it.b * p.C + c + e];
-#pragma unroll 8
-            for (int q = 0; q < it.piece; ++q)
+            if (p.maps_only) {  // kept for the next launch, whose last piece may write there
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (e < here) {
-                        const float2 m = p.maps[((long long)q * p.B + it.b) * p.C + c + e];
-                        init.v[e] = fmaf(m.x, init.v[e], m.y);
-                    }
+                for (int e = 0; e < V; ++e) {
+                    if (it.piece == 0 && e < here) p.start[(long long)it.b * p.C + c + e] = init.v[e];
+                    init.v[e] = 0.f;
+                }
+            }
+            const int joins = p.maps_only ? 0 : it.piece;
+            for (int q = 0; q < joins; q += 16) {  // 16 loads under way at once
+                float2 m[16][V];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        m[i][e] = q + i < joins && e < here
+                                      ? p.maps[((long long)(q + i) * p.B + it.b) * p.C + c + e]
+                                      : make_float2(1.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) init.v[e] = fmaf(m[i][e].x, init.v[e], m[i][e].y);
+            }
         }
         if (kBack && edge && p.h0)
 #pragma unroll
@@ -529,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             form(Flag<true>());
         else
             form(Flag<false>());
+        if (begins) H = fma_v(A, init, H);
         auto maps = warp_maps[group][turn & 1];
         auto map_at = [&](float *m) { return reinterpret_cast<Vec<V> *>(m); };
         map_at(maps[warp][lane])[0] = A;
@@ -828,7 +848,8 @@ la_status launch_scan(const char *who, Params &p, int read, Workspace ws, cudaSt
     p.steps = cut.steps;
     void *mine = nullptr;
     if (cut.pieces > 1) {
-        const size_t need = sizeof(float2) * (size_t)(cut.pieces - 1) * p.B * p.C;
+        const size_t states = (size_t)p.B * p.C;
+        const size_t need = (sizeof(float2) * (cut.pieces - 1) + sizeof(float)) * states;
         if (ws.p) {
             if (ws.bytes < need || (uintptr_t)ws.p % 16)
                 return rec_fail(LA_ERR_INVALID_ARG, who, "workspace too small or not 16-byte aligned");
@@ -841,6 +862,7 @@ la_status launch_scan(const char *who, Params &p, int read, Workspace ws, cudaSt
             }
             p.maps = static_cast<float2 *>(mine);
         }
+        p.start = reinterpret_cast<float *>(p.maps + (cut.pieces - 1) * states);
     }
     cfg.dynamicSmemBytes = cut.smem;
     at[0].val.clusterDim = {(unsigned)cut.S, 1, 1};
@@ -851,6 +873,7 @@ la_status launch_scan(const char *who, Params &p, int read, Workspace ws, cudaSt
         cfg.gridDim = dim3((unsigned)(std::min(cut.clusters, items) * cut.S));
         e = cudaLaunchKernelEx(&cfg, kern, p);
         launches += e == cudaSuccess;
+        p.first = p.start;  // of the second pass
     }
     note_launches(launches);
     if (mine) {

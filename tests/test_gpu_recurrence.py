@@ -142,6 +142,89 @@ def test_forward_and_backward(shape, types, complement, gate):
         close(a, ref, tol)
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("B, N, C", [(200, 90, 60), (90, 200, 130), (170, 300, 33), (70, 515, 201)])
+def test_more_strips_than_run_at_once(B, N, C, types):
+    # a block takes several strips one after the other, each of one, two, three
+    # or more rounds, so that its two groups of warps pass from one to the next
+    x, z, h0 = inputs(B, N, C, types, "logit", 11 + N)
+    out, hl = la.forward_recurrence(x.cuda(), z.cuda(), h0.cuda(), gate="logit", complement=True)
+    check_forward(x, z, h0, "logit", True, out, hl)
+    g = torch.Generator().manual_seed(12)
+    dout, dh = torch.randn(B, N, C, generator=g).to(x.dtype), torch.randn(B, C, generator=g)
+    got = la.backward_recurrence(dout.cuda(), z.cuda(), out, x.cuda(), h0.cuda(), dh.cuda(),
+                                 gate="logit", complement=True)
+    for a, (ref, tol) in zip(got, plain_back(dout, z, out.cpu(), x, h0, dh, "logit", True)):
+        close(a, ref, tol)
+
+
+@pytest.mark.parametrize("B, N, C", [(1, 200000, 64), (1, 30000, 64), (1, 3000, 512),
+                                     (3, 700, 1000), (1, 50, 40)])
+def test_state_in_place(B, N, C):
+    # h_last over h0, dh0 over dh_last, whatever the sequence is cut into:
+    # pieces, clusters, single blocks
+    x, z, h0 = (t.cuda() for t in inputs(B, N, C, ("bf16", "bf16"), "logit", 13 + N))
+    dh = torch.randn(B, C, generator=torch.Generator().manual_seed(14)).cuda()
+    out, hl = la.forward_recurrence(x, z, h0, gate="logit")
+    back = la.backward_recurrence(x, z, out, None, h0, dh, gate="logit")
+    for _ in range(5):
+        h, d = h0.clone(), dh.clone()
+        o, _ = la.forward_recurrence(x, z, h, h_last=h, gate="logit")
+        assert torch.equal(o, out) and torch.equal(h, hl)
+        got = la.backward_recurrence(x, z, out, None, h0, d, dh0=d, gate="logit")
+        for a, b in zip(got, back):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N, launches", [(40000, 1), (200000, 2)])
+def test_workspaces(N, launches):
+    # few channels: from some length on a sequence is cut into pieces (their
+    # maps, then the walk).  The binding brings a workspace on the current
+    # stream, the library allocates on one given by the caller
+    x, z, h0 = (t.cuda() for t in inputs(1, N, 40, ("f32", "f32"), "log", 15))
+    n0 = la.kernel_launch_count()
+    ref = la.forward_recurrence(x, z, h0, gate="log")
+    assert la.kernel_launch_count() == n0 + launches
+    here = torch.cuda.current_stream()
+    got = la.forward_recurrence(x, z, h0, gate="log", stream=here)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    if launches == 1:
+        return
+    lib = la.load_library()
+    assert lib.la_debug_fail_next_allocs(1) == 0
+    try:
+        la.forward_recurrence(x, z, h0, gate="log")
+        with pytest.raises(la.LinAttnError) as e:
+            la.forward_recurrence(x, z, h0, gate="log", stream=here)
+        assert e.value.status == 4
+    finally:
+        lib.la_debug_fail_next_allocs(0)
+    small = torch.empty(64, dtype=torch.uint8, device="cuda")
+    st = lib.la_forward_recurrence(x.data_ptr(), z.data_ptr(), None, ref[0].data_ptr(), None, None,
+                                   1, N, 40, 1, 0, 0, 0, small.data_ptr(), 64, None)
+    assert st == 1 and "workspace too small" in lib.la_last_error().decode()
+
+
+@pytest.mark.parametrize("types, C, complement", [(("f32", "f32"), 40, False),
+                                                  (("bf16", "bf16"), 64, True),
+                                                  (("bf16", "f32"), 7, False)])
+def test_sequences_in_pieces(types, C, complement):
+    N = 120007
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(1, N, C, generator=g).to(DT[types[0]])
+    z = (2 * torch.randn(1, N, C, generator=g) + 5).to(DT[types[1]])
+    h0, dh = torch.randn(1, C, generator=g), torch.randn(1, C, generator=g)
+    n0 = la.kernel_launch_count()
+    out, hl = la.forward_recurrence(x.cuda(), z.cuda(), h0.cuda(), gate="logit",
+                                    complement=complement)
+    assert la.kernel_launch_count() == n0 + 2
+    check_forward(x, z, h0, "logit", complement, out, hl)
+    got = la.backward_recurrence(x.cuda(), z.cuda(), out, x.cuda(), h0.cuda(), dh.cuda(),
+                                 gate="logit", complement=complement)
+    for a, (ref, tol) in zip(got, plain_back(x, z, out.cpu(), x, h0, dh, "logit", complement)):
+        close(a, ref, tol)
+
+
 def test_without_states():
     x, z, _ = inputs(2, 300, 65, ("f32", "f32"), "log", 21)
     zero = torch.zeros(2, 65)

@@ -10,6 +10,7 @@ from linear_attention_feature_gb300 import build as labuild
 
 INVALID, UNSUPPORTED, OK = 1, 2, 0
 P = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(8)]  # never dereferenced
+ODD = ctypes.c_void_p(0x10001)
 BAD_FREQ = {"nan": float("nan"), "inf": float("inf"), "big": 2e9}
 
 
@@ -65,6 +66,9 @@ CONT = (2 * 3 * 64, 3 * 64, 64)
     (dict(eps=float("nan")), INVALID, "eps"),
     (dict(eps=float("inf")), INVALID, "eps"),
     (dict(norm=0, wq=P[4]), INVALID, "weights need norm"),
+    (dict(q=ODD), INVALID, "unaligned"),
+    (dict(ko=ODD), INVALID, "unaligned"),
+    (dict(wq=ctypes.c_void_p(0x10002)), INVALID, "unaligned"),
     (dict(qo=P[1]), INVALID, "aliases"),
     (dict(ko=P[0]), INVALID, "aliases"),
     (dict(qo=P[3]), INVALID, "aliases"),
@@ -106,6 +110,9 @@ def back(lib, gq=P[0], gk=P[1], q=P[2], k=P[3], dq=P[4], dk=P[5], dwq=None, dwk=
     (dict(gq=None), "null"),
     (dict(q=None), "null"),
     (dict(dk=None), "null"),
+    (dict(gq=ODD), "unaligned"),
+    (dict(dk=ODD), "unaligned"),
+    (dict(dwq=ctypes.c_void_p(0x10002)), "unaligned"),
     (dict(dq=P[2]), "aliases"),
     (dict(dk=P[2]), "aliases"),
     (dict(dq=P[1]), "aliases"),
@@ -142,6 +149,9 @@ def rec(lib, x=P[0], z=P[1], h0=None, out=P[2], hl=None, st=None, B=2, N=3, C=8,
     (dict(dtype=9), INVALID, "dtype"),
     (dict(dtype=0, gdtype=1), INVALID, "gate_dtype"),
     (dict(gdtype=4), INVALID, "gate_dtype"),
+    (dict(x=ODD), INVALID, "unaligned"),
+    (dict(z=ctypes.c_void_p(0x10002)), INVALID, "unaligned"),
+    (dict(h0=ctypes.c_void_p(0x10002)), INVALID, "unaligned"),
     (dict(out=P[1]), INVALID, "aliases"),
     (dict(out=P[0], st=strides(48, 16, 24, 8, 24, 8)), INVALID, "in place"),
     (dict(st=strides(24, 8, 24, 8, 24, 7)), INVALID, "overlap"),
@@ -172,6 +182,8 @@ def rec_back(lib, dout=P[0], z=P[1], out=P[2], x=P[3], dx=P[4], dz=P[5], st=None
     (dict(out=None), "null"),
     (dict(x=None), "null"),
     (dict(dz=None), "null"),
+    (dict(dout=ODD), "unaligned"),
+    (dict(dz=ODD), "unaligned"),
     (dict(dx=P[1]), "aliases"),
     (dict(dx=P[2]), "aliases"),
     (dict(dx=P[3]), "aliases"),
@@ -201,6 +213,8 @@ def step(lib, h=P[0], ho=P[1], x=P[2], z=P[3], out=P[4], st=None, B=2, C=8, gate
     (dict(h=None), "null"),
     (dict(ho=None), "null"),
     (dict(out=None), "null"),
+    (dict(h=ctypes.c_void_p(0x10002)), "unaligned"),
+    (dict(x=ODD), "unaligned"),
     (dict(B=-2), "negative"),
     (dict(gate=5), "gate"),
     (dict(comp=-1), "complement"),
