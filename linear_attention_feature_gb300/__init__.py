@@ -494,14 +494,14 @@ def _rope(frequencies, positions, offset, interleaved, shape, device):
 _STRIDES = {n: struct.Struct(f"@{n}q") for n in (3, 6, 12, 18)}
 
 
-def _check_rows(q, *ts):
+def _check_rows(q, device, *ts):
     """Tensors of rows with q's dtype and CUDA device and a contiguous last
-    dimension; returns the packed la_strides of all but q."""
+    dimension; returns their packed la_strides."""
     if not q.is_cuda:
         raise ValueError("all tensors must be on a CUDA device")
-    device, dtype, v = q.device, q.dtype, []
+    dtype, v = q.dtype, []
     for t in ts:
-        if t.device != device:
+        if t is not q and t.device != device:
             raise ValueError("all tensors must be on one CUDA device")
         if t.dtype is not dtype:
             raise TypeError("q, k, their outputs and gradients must share one dtype")
@@ -571,11 +571,13 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     B, Hq, Hk, N, d = _check_qk(qs, ks)
     if q_out is None:
         q_out = _contiguous_like(q)
+    elif q_out.shape != qs:
+        raise ValueError("q_out must have q's shape")
     if k_out is None:
         k_out = _contiguous_like(k)
-    if q_out.shape != qs or k_out.shape != ks:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    strides = _check_rows(q, q, k, q_out, k_out)
+    elif k_out.shape != ks:
+        raise ValueError("k_out must have k's shape")
+    strides = _check_rows(q, device, q, k, q_out, k_out)
     wq, wk, wcode = _weights(q_weight, k_weight, d, device)
     rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
     code, lib = _code(q.dtype), load_library()
@@ -610,7 +612,7 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
         dk = torch.empty_like(k)
     if dq.shape != qs or dk.shape != ks:
         raise ValueError("dq and dk must have the shapes of q and k")
-    strides = _check_rows(q, dq_out, dk_out, q, k, dq, dk)
+    strides = _check_rows(q, device, dq_out, dk_out, q, k, dq, dk)
     wq, wk, wcode = _weights(q_weight, k_weight, d, device)
     rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
     code, lib = _code(q.dtype), load_library()

@@ -585,24 +585,25 @@ bool same(const la_strides &a, const la_strides &b) {
     return a.b == b.b && a.h == b.h && a.n == b.n;
 }
 
-bool aligned(const void *p, const la_strides &s, int B, int H, int N, int v, int elem) {
-    return (uintptr_t)p % (uintptr_t)(v * elem) == 0 && (B <= 1 || s.b % v == 0) &&
-           (H <= 1 || s.h % v == 0) && (N <= 1 || s.n % v == 0);
-}
-
-// Values per access: the most (up to `most`) that divide the row's two halves
-// and its rotated part and at which every row of every tensor is aligned.
+// Values per access: the most (a power of two, up to `most`) that divide the
+// row's two halves and its rotated part and at which every row of every tensor
+// is aligned.
 int vector_of(const Params &p, int most, int elem) {
-    for (int v = most; v > 1; v /= 2) {
-        bool ok = p.d % (2 * v) == 0 && p.half % v == 0;
-        for (const Side &s : p.side)
-            if (s.H > 0)
-                ok = ok && aligned(s.x, s.sx, p.B, s.H, p.N, v, elem) &&
-                     aligned(s.dy, s.sdy, p.B, s.H, p.N, v, elem) &&
-                     aligned(s.y, s.sy, p.B, s.H, p.N, v, elem);
-        if (ok) return v;
+    // a power of two divides all of these if it divides their union
+    unsigned long long all = (unsigned)(p.half | (p.d % 2 ? 1 : p.d / 2)) | (unsigned)most;
+    auto add = [&](const void *q, const la_strides &s, int H) {
+        all |= (uintptr_t)q / (uintptr_t)elem;
+        if (p.B > 1) all |= (unsigned long long)s.b;
+        if (H > 1) all |= (unsigned long long)s.h;
+        if (p.N > 1) all |= (unsigned long long)s.n;
+    };
+    for (const Side &s : p.side) {
+        if (s.H == 0) continue;
+        add(s.x, s.sx, s.H);
+        add(s.dy, s.sdy, s.H);
+        add(s.y, s.sy, s.H);
     }
-    return 1;
+    return (int)(all & (0 - all));
 }
 
 template <typename T, int V, int K, bool kBack>
