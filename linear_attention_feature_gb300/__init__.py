@@ -620,9 +620,11 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     try:
         dwq = dwk = ws = None
         ws_bytes = 0
-        if wq is not None:
+        if wq is not None and wk is not None:
+            dwq, dwk = torch.empty(2, d, dtype=torch.float32, device=device).unbind(0)
+        elif wq is not None:
             dwq = torch.empty(d, dtype=torch.float32, device=device)
-        if wk is not None:
+        elif wk is not None:
             dwk = torch.empty(d, dtype=torch.float32, device=device)
         # on the current stream torch's allocator gives the workspace; the
         # library allocates on another one

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     const long long it0 = total * block / blocks;
     const int count = (int)(total * (block + 1) / blocks - it0);  // rows of this block's groups
 
+    if (kBack) tc::grid_dep_launch();
     for (int i = threadIdx.x; i < p.half; i += kThreads) turns[i] = p.turns[i];
     for (int i = threadIdx.x; i < p.d; i += kThreads) weight[i] = weight_at(sd.w, p.w_bf16, i);
     __syncthreads();
@@ -528,6 +529,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
 // feature, joined in order.
 __global__ void __launch_bounds__(1024)
 qk_weight_kernel(const float *partial, int blocks_q, int blocks, int d, float *dwq, float *dwk) {
+    // started while the rows' kernel runs: its sums are there after this
+    tc::grid_dep_wait();
     float *dw = blockIdx.x ? dwk : dwq;
     if (!dw) return;
     __shared__ float sum[4][LA_MAX_D];
@@ -633,8 +636,10 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
     const int v = vector_of(p, 16 / (int)sizeof(T), (int)sizeof(T));
     const int chunks = ((p.d + 1) / 2 + v - 1) / v;  // of a row
-    // chunks per lane: one of 4 or 8 pairs, up to two of 2, up to four of 1
-    const int per_lane = v >= 4 ? 1 : v == 2 ? (chunks > 32 ? 2 : 1) : (chunks > 64 ? 4 : 2);
+    // Chunks per lane: more of the small ones, so that a warp takes more rows at a
+    // time (2 x 24 x 4000 rows of 66 bf16 values: 60 us with two single pairs per
+    // lane, 41 us with four; of 36: 20 us with one double pair, 14 us with two).
+    const int per_lane = v >= 4 ? 1 : v == 2 ? 2 : 4;
     while (per_lane << p.lane_bits < chunks) ++p.lane_bits;
     const int groups = kThreads >> p.lane_bits;
     const long long tokens = (long long)p.B * p.N;
@@ -672,19 +677,15 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
         e = launch_rows<T, sizeof(T) == 2 ? 8 : 4, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 4)
         e = launch_rows<T, 4, 1, kBack>(p, (unsigned)blocks, stream);
-    else if (v == 2 && per_lane == 1)
-        e = launch_rows<T, 2, 1, kBack>(p, (unsigned)blocks, stream);
     else if (v == 2)
         e = launch_rows<T, 2, 2, kBack>(p, (unsigned)blocks, stream);
-    else if (per_lane == 2)
-        e = launch_rows<T, 1, 2, kBack>(p, (unsigned)blocks, stream);
     else
         e = launch_rows<T, 1, 4, kBack>(p, (unsigned)blocks, stream);
     if (e == cudaSuccess) note_launches(1);
     if (e == cudaSuccess && want_dw) {
-        qk_weight_kernel<<<2, 1024, 0, stream>>>(p.partial, p.blocks_q, (int)blocks, p.d,
-                                                 p.side[0].dw, p.side[1].dw);
-        e = cudaGetLastError();
+        e = tchost::launch_dependent(qk_weight_kernel, 2, 1024, 0, stream,
+                                     static_cast<const float *>(p.partial), p.blocks_q,
+                                     (int)blocks, p.d, p.side[0].dw, p.side[1].dw);
         if (e == cudaSuccess) note_launches(1);
     }
     if (ws) {
