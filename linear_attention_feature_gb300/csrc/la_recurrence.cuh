@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
     Item it = item(0);
     int c = 0, here = 0;
     bool part = false;  // the strip reaches beyond C
-    long long s0 = 0;   // this thread's first step
+    bool ends = false;  // the item ends with the sequence
+    int ahead = 0;      // steps of the item from this thread's first one on
     T *o = nullptr;     // its first token in the outputs
     G *oz = nullptr;
     const long long o_turn = (kBack ? -2LL : 2LL) * round_steps * p.out[0].n;
@@ -470,12 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             c = it.c0 + lane * V;
             here = min(max(p.C - c, 0), V);
             part = it.c0 + kRow > p.C;
-            s0 = first_step(it, r) + warp * L;
+            const long long s0 = first_step(it, r) + warp * L;  // this thread's first step
             const long long t0 = kBack ? p.N - 1 - s0 : s0;
+            ahead = (int)(it.end - s0);
+            ends = it.end == p.N;
             o = static_cast<T *>(p.out[0].p) + it.b * p.out[0].b + t0 * p.out[0].n + c;
             if (kBack) oz = static_cast<G *>(p.out[1].p) + it.b * p.out[1].b + t0 * p.out[1].n + c;
         }
-        const bool edge = s0 + L >= it.end || part;  // masks are needed
+        const bool edge = ahead <= L || part;  // masks are needed
         // The state before the item's first token enters the map of the first
         // warp, and is read by that warp alone: it has been used when the state
         // behind the last token is written, which may be to the same place.
@@ -520,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             for (int i = 0; i < (kBack ? 4 : 2); ++i) {
                 const Seq &q = p.in[i];
                 const unsigned elem = i == 1 ? sizeof(G) : sizeof(T);
-                const unsigned t = (unsigned)(kBack ? p.N - 1 - s0 : s0) - (i == 2 ? 1u : 0u);
+                const unsigned s0 = (unsigned)it.end - (unsigned)ahead;
+                const unsigned t = (kBack ? (unsigned)p.N - 1u - s0 : s0) - (i == 2 ? 1u : 0u);
                 step[i] = (kBack ? 0u - (unsigned)q.n : (unsigned)q.n) * elem;
                 at[i] = (unsigned)(uintptr_t)q.p +
                         ((unsigned)(it.b * q.b) + t * (unsigned)q.n + (unsigned)it.c0) * elem;
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
                 Vec<V> rest = all_v<V>(0.f);
                 gate_of<kGate, V>(z, complement || (kBack && kGate == LA_GATE_LOGIT), a[i], rest);
                 y[i] = kBack ? rest : complement ? mul_v(rest, x) : x;
-                if (at_edge.value && s0 + i >= it.end) {
+                if (at_edge.value && i >= ahead) {
                     a[i] = all_v<V>(1.f);
                     x = y[i] = all_v<V>(0.f);
                 }
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             G *toz = oz;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                const bool ok = !at_edge.value || s0 + i < it.end;
+                const bool ok = !at_edge.value || i < ahead;
                 if (!kBack) {
                     state = fma_v(a[i], state, y[i]);
                     if (ok) put(to, state);
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
                 Vec<V> g = values((T *)nullptr, xt, at[0], step[0], i);
                 Vec<V> h = values((T *)nullptr, tile_x(stage, 1), at[2], step[2], i);
                 if (at_edge.value && !ok) g = all_v<V>(0.f);
-                if (at_edge.value && s0 + i == p.N - 1) h = h0;
+                if (at_edge.value && ends && i == ahead - 1) h = h0;
                 g = add_v(g, state);
                 if (complement)
                     h = fma_v(values((T *)nullptr, tile_x(stage, 2), at[3], step[3], i),
@@ -669,12 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
                 walk(Flag<false>());
             // the state behind the last token, as its warp has it: forward, these
             // are the bits that `out` was rounded from
-            if (edge && p.last && s0 < p.N && s0 + L >= p.N && it.end == p.N)
+            if (edge && p.last && ends && ahead > 0 && ahead <= L)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     if (e < here) p.last[(long long)it.b * p.C + c + e] = state.v[e];
         }
-        s0 += 2 * round_steps;
+        ahead -= 2 * round_steps;
         o += o_turn;
         if (kBack) oz += oz_turn;
         ++turn;
