@@ -11,6 +11,14 @@
 // fraction of a turn in 64-bit fixed point: f / 2 pi mod 1 is rounded to
 // 2^-64 on the host, and p times that wraps modulo one turn exactly, so an
 // angle far out costs one integer product and loses nothing.
+//
+// What bounds it (GB300, 6.78 TB/s measured copy): memory, once the angles are
+// shared by a token's heads, rows arrive asynchronously and the arithmetic goes
+// through the packed fp32 instructions.  Forward 2 x (16 + 16) x 32768 x 128 bf16,
+// token-major to head-major: 181 us, 5.9 TB/s (12 instructions a value); 4 x (16 +
+// 16) x 4096 x 64: 21 us, 6.4 TB/s.  Backward 4 x (8 + 8) x 16384 x 128: 148 us, 5.4
+// TB/s (26 instructions a value, the weights' sums among them).  First kernel,
+// one warp per row: 1332, 233 and 1021 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -526,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
 }
 
 // dw[i] = the sum of the blocks' partial sums: 1024 / 256 interleaved sums per
-// feature, joined in order.
+// feature, joined in order.  A few microseconds of latency, most of them hidden by
+// starting it while the rows' kernel ends.
 __global__ void __launch_bounds__(1024)
 qk_weight_kernel(const float *partial, int blocks_q, int blocks, int d, float *dwq, float *dwk) {
     // started while the rows' kernel runs: its sums are there after this
