@@ -547,8 +547,7 @@ def _check_qk(qs, ks):
 
 
 def _contiguous_like(t):
-    torch = _torch()
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _torch().empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions=None, *,
@@ -569,18 +568,19 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     Returns (q_out, k_out)."""
     qs, ks, device = q.shape, k.shape, q.device
     B, Hq, Hk, N, d = _check_qk(qs, ks)
+    empty, dtype = _torch().empty, q.dtype
     if q_out is None:
-        q_out = _contiguous_like(q)
+        q_out = empty(qs, dtype=dtype, device=device)
     elif q_out.shape != qs:
         raise ValueError("q_out must have q's shape")
     if k_out is None:
-        k_out = _contiguous_like(k)
+        k_out = empty(ks, dtype=dtype, device=device)
     elif k_out.shape != ks:
         raise ValueError("k_out must have k's shape")
     strides = _check_rows(q, device, q, k, q_out, k_out)
     wq, wk, wcode = _weights(q_weight, k_weight, d, device)
     rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
-    code, lib = _code(q.dtype), load_library()
+    code, lib = _code(dtype), load_library()
     on = _Device(device, stream)
     try:
         st = lib.la_qk_norm_rope(
@@ -620,11 +620,9 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     try:
         dwq = dwk = ws = None
         ws_bytes = 0
-        if wq is not None and wk is not None:
-            dwq, dwk = torch.empty(2, d, dtype=torch.float32, device=device).unbind(0)
-        elif wq is not None:
+        if wq is not None:
             dwq = torch.empty(d, dtype=torch.float32, device=device)
-        elif wk is not None:
+        if wk is not None:
             dwk = torch.empty(d, dtype=torch.float32, device=device)
         # on the current stream torch's allocator gives the workspace; the
         # library allocates on another one
