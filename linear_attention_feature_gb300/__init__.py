@@ -593,6 +593,10 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     return q_out, k_out
 
 
+# workspace bytes of the backward per feature, by device
+_BACK_WORKSPACE = {}
+
+
 def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
                           frequencies=None, positions=None, *, offset: int = 0,
                           norm: bool = True, eps: float = 1e-6, interleaved: bool = False,
@@ -627,7 +631,11 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
         # on the current stream torch's allocator gives the workspace; the
         # library allocates on another one
         if stream is None and (wq is not None or wk is not None):
-            ws_bytes = lib.la_backward_qk_norm_rope_workspace_bytes(d)
+            per_feature = _BACK_WORKSPACE.get(device.index)
+            if per_feature is None:
+                per_feature = lib.la_backward_qk_norm_rope_workspace_bytes(1)
+                _BACK_WORKSPACE[device.index] = per_feature
+            ws_bytes = per_feature * d
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         st = lib.la_backward_qk_norm_rope(
             dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
@@ -691,7 +699,7 @@ def _ptr(t):
 def _recurrence_workspace(lib, B, C, code, device, stream):
     """(workspace or None, bytes): on the current stream torch's allocator
     gives it; the library allocates on another one."""
-    if stream is not None:
+    if stream is not None or B * C > 1024:  # more channels never need one
         return None, 0
     n = lib.la_recurrence_workspace_bytes(B, C, code)
     if n == 0:

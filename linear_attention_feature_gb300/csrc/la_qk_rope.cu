@@ -580,17 +580,17 @@ bool rows_disjoint(const la_strides &s, int B, int H, int N, int d) {
     return true;
 }
 
-// f / (2 pi) mod 1 in 2^-64 turns.  1 / (2 pi) is the sum of two doubles, so
-// the product is good to about 2^-64 turns for |f| up to a few turns.
+// f / (2 pi) mod 1 in 2^-64 turns, |f| <= 1e9.  1 / (2 pi) is the sum of two
+// doubles, so the product is good to about 2^-64 turns for |f| up to a few turns.
 unsigned long long turns_of(double f) {
+    if (f < 0) return 0 - turns_of(-f);
     const double c = 0.15915494309189535, c_low = -9.839338337591243e-18;
     const double t = f * c;
-    const double low = std::fma(f, c, -t) + f * c_low;  // |low| < 2^-51 |t|
+    const double low = std::fma(f, c, -t) + f * c_low;  // |low| < 2^-51 |t| < 2^-23
     const double part = t - std::floor(t);              // exact, in [0, 1)
-    const double top = std::floor(part * 0x1p32);
-    const double rest = part * 0x1p32 - top;
-    return ((unsigned long long)top << 32) + (unsigned long long)(rest * 0x1p32) +
-           (unsigned long long)(long long)std::nearbyint((low - std::floor(low + 0.5)) * 0x1p64);
+    // a double below 1 is a whole number of 2^-64 from 2^-11 on, and loses less
+    // than one below
+    return (unsigned long long)(part * 0x1p64) + (unsigned long long)(long long)(low * 0x1p64);
 }
 
 bool same(const la_strides &a, const la_strides &b) {

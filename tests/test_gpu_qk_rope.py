@@ -258,6 +258,18 @@ def check_exact_angles(y, x, pos, freq):
         assert torch.all((y[b, :, i].cpu().double() - ref).abs() <= 40 * U * mag)
 
 
+@pytest.mark.parametrize("freq", [[1.0, -0.3, 1e-4, -1e-4], [6.5, 1e-9, 12345.678, -3.0],
+                                  [0.0, -0.0, 1e9, -1e9]])
+def test_any_frequencies(freq):
+    # any sign and size; far positions (a frequency is off by at most some
+    # 2^-64 turns per position beyond its own last bit)
+    q, k = rows(2, 2, 40, 8, "f32", 35), rows(2, 2, 40, 8, "f32", 36)
+    pos = torch.arange(40).expand(2, 40) + (1 << 33)
+    yq, yk = la.qk_norm_rope(q, k, None, None, freq, offset=1 << 33)
+    check_exact_angles(yq, q, pos, freq)
+    check_exact_angles(yk, k, pos, freq)
+
+
 def test_far_offset_keeps_relative_positions():
     # <y_q(p), y_k(p')> depends on p - p' alone, however far out p is
     d = 64

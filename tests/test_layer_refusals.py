@@ -244,6 +244,9 @@ def test_workspace_query(lib):
     assert g(0, 8, 1) == g(8, 0, 1) == g(1, 8, 7) == 0
     assert g(1, 64, 1) > 0 and g(1, 64, 0) > 0
     assert g(256, 4096, 1) == 0  # enough channels: nothing is cut into pieces
+    # what the binding goes by: none above 1024 channels, and bytes by feature
+    assert g(1, 1025, 1) == g(1, 1025, 0) == g(205, 5, 1) == g(205, 5, 0) == 0
+    assert all(f(d) == d * f(1) for d in (1, 7, 64, 256))
 
 
 def test_rope_frequencies():
