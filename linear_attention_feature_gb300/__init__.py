@@ -146,13 +146,17 @@ def _torch():
 _CODES = {}
 
 
+def _codes():
+    torch = _torch()
+    _CODES.update({torch.float32: LA_F32, torch.bfloat16: LA_BF16,
+                   torch.int32: 4, torch.int64: 8})  # positions: their bytes
+    return _CODES
+
+
 def _code(dtype) -> int:
     """LA_F32 or LA_BF16."""
-    if not _CODES:
-        torch = _torch()
-        _CODES[torch.float32], _CODES[torch.bfloat16] = LA_F32, LA_BF16
-    code = _CODES.get(dtype)
-    if code is None:
+    code = (_CODES or _codes()).get(dtype)
+    if code != LA_F32 and code != LA_BF16:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
     return code
 
@@ -180,24 +184,19 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-class _Device:
-    """The CUDA device of a call as the current one (with nothing to do where
-    it is already), and the stream that the call goes to."""
+def _enter(index, stream):
+    """Makes CUDA device `index` the current one.  Returns the stream that the
+    call goes to and the device to go back to (-1: it was current already)."""
+    c = _torch()._C
+    now, back = c._cuda_getDevice(), -1
+    if now != index:
+        _torch().cuda.set_device(index)
+        back = now
+    return (stream.cuda_stream if stream is not None else c._cuda_getCurrentRawStream(index)), back
 
-    __slots__ = ("back", "stream")
 
-    def __init__(self, device, stream):
-        get = _torch()._C
-        index, now = device.index, get._cuda_getDevice()
-        self.back = None if index == now else now
-        if index != now:
-            _torch().cuda.set_device(index)
-        self.stream = stream.cuda_stream if stream is not None \
-            else get._cuda_getCurrentRawStream(index)
-
-    def leave(self):
-        if self.back is not None:
-            _torch().cuda.set_device(self.back)
+def _leave(back):
+    _torch().cuda.set_device(back)
 
 
 def _decay_arg(decay, H):
@@ -463,9 +462,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0):
 _ROPE = struct.Struct("@PiiPiqqq")
 
 
-def _rope(frequencies, positions, offset, interleaved, shape, device):
+def _rope(frequencies, positions, offset, interleaved, shape, index):
     """The packed la_rope (None: no rotation) and what has to outlive the call;
-    `shape`: q's."""
+    `shape`: q's, `index`: its device's."""
     if frequencies is None or len(frequencies) == 0:
         return None, None
     f = frequencies
@@ -482,10 +481,10 @@ def _rope(frequencies, positions, offset, interleaved, shape, device):
     else:
         raise ValueError(f"positions must have the shape {list(want)}"
                          + (f" or {list(want[1:])}" if len(shape) == 4 else ""))
-    nbytes = positions.element_size()
-    if positions.is_floating_point() or nbytes not in (4, 8) or not positions.dtype.is_signed:
+    nbytes = (_CODES or _codes()).get(positions.dtype)
+    if nbytes not in (4, 8):
         raise TypeError("positions must be int32 or int64")
-    if positions.device != device:
+    if positions.get_device() != index:
         raise ValueError("positions must be on q's CUDA device")
     return _ROPE.pack(f.buffer_info()[0], 2 * len(f), bool(interleaved), positions.data_ptr(),
                       nbytes, sb, sn, offset), f
@@ -494,14 +493,14 @@ def _rope(frequencies, positions, offset, interleaved, shape, device):
 _STRIDES = {n: struct.Struct(f"@{n}q") for n in (3, 6, 12, 18)}
 
 
-def _check_rows(q, device, *ts):
+def _check_rows(q, *ts):
     """Tensors of rows with q's dtype and CUDA device and a contiguous last
-    dimension; returns their packed la_strides."""
-    if not q.is_cuda:
+    dimension; returns the device's index and their packed la_strides."""
+    index, dtype, v = q.get_device(), q.dtype, []
+    if index < 0:
         raise ValueError("all tensors must be on a CUDA device")
-    dtype, v = q.dtype, []
     for t in ts:
-        if t is not q and t.device != device:
+        if t.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
         if t.dtype is not dtype:
             raise TypeError("q, k, their outputs and gradients must share one dtype")
@@ -509,31 +508,29 @@ def _check_rows(q, device, *ts):
         if s[-1] != 1 and t.shape[-1] > 1:
             raise ValueError("the last dimension must be contiguous")
         v += s[:3] if len(s) == 4 else (s[0], s[1], 0)
-    return _STRIDES[len(v)].pack(*v)
+    return index, _STRIDES[len(v)].pack(*v)
 
 
-def _weights(q_weight, k_weight, d, device):
+def _weights(q_weight, k_weight, d, index):
     """(q_weight's and k_weight's pointers or None, their dtype code)."""
-    pq = pk = None
+    pq = pk = dtype = None
     for w in (q_weight, k_weight):
         if w is None:
             continue
         if w.shape != (d,):
             raise ValueError(f"a weight must have the shape [{d}]")
-        if w.device != device:
+        if w.get_device() != index:
             raise ValueError("the weights must be on q's CUDA device")
         if w.stride(0) != 1 and d > 1:
             raise ValueError("a weight must be contiguous")
+        if dtype is not None and w.dtype is not dtype:
+            raise TypeError("q_weight and k_weight must share one dtype")
+        dtype = w.dtype
     if q_weight is not None:
-        pq, dtype = q_weight.data_ptr(), q_weight.dtype
-        if k_weight is not None:
-            if k_weight.dtype is not dtype:
-                raise TypeError("q_weight and k_weight must share one dtype")
-            pk = k_weight.data_ptr()
-        return pq, pk, _code(dtype)
+        pq = q_weight.data_ptr()
     if k_weight is not None:
-        return None, k_weight.data_ptr(), _code(k_weight.dtype)
-    return None, None, LA_F32
+        pk = k_weight.data_ptr()
+    return pq, pk, LA_F32 if dtype is None else _code(dtype)
 
 
 def _check_qk(qs, ks):
@@ -577,17 +574,18 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
         k_out = empty(ks, dtype=dtype, device=device)
     elif k_out.shape != ks:
         raise ValueError("k_out must have k's shape")
-    strides = _check_rows(q, device, q, k, q_out, k_out)
-    wq, wk, wcode = _weights(q_weight, k_weight, d, device)
-    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
+    index, strides = _check_rows(q, q, k, q_out, k_out)
+    wq, wk, wcode = _weights(q_weight, k_weight, d, index)
+    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, index)
     code, lib = _code(dtype), load_library()
-    on = _Device(device, stream)
+    to, back = _enter(index, stream)
     try:
         st = lib.la_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), strides, wq, wk,
-            bool(norm), eps, rope, B, Hq, Hk, N, d, code, wcode, on.stream)
+            bool(norm), eps, rope, B, Hq, Hk, N, d, code, wcode, to)
     finally:
-        on.leave()
+        if back >= 0:
+            _leave(back)
     if st:
         _raise_if(st)
     return q_out, k_out
@@ -616,11 +614,11 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
         dk = torch.empty_like(k)
     if dq.shape != qs or dk.shape != ks:
         raise ValueError("dq and dk must have the shapes of q and k")
-    strides = _check_rows(q, device, dq_out, dk_out, q, k, dq, dk)
-    wq, wk, wcode = _weights(q_weight, k_weight, d, device)
-    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, device)
+    index, strides = _check_rows(q, dq_out, dk_out, q, k, dq, dk)
+    wq, wk, wcode = _weights(q_weight, k_weight, d, index)
+    rope, keep = _rope(frequencies, positions, offset, interleaved, qs, index)
     code, lib = _code(q.dtype), load_library()
-    on = _Device(device, stream)
+    to, back = _enter(index, stream)
     try:
         dwq = dwk = ws = None
         ws_bytes = 0
@@ -631,18 +629,19 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
         # on the current stream torch's allocator gives the workspace; the
         # library allocates on another one
         if stream is None and (wq is not None or wk is not None):
-            per_feature = _BACK_WORKSPACE.get(device.index)
+            per_feature = _BACK_WORKSPACE.get(index)
             if per_feature is None:
                 per_feature = lib.la_backward_qk_norm_rope_workspace_bytes(1)
-                _BACK_WORKSPACE[device.index] = per_feature
+                _BACK_WORKSPACE[index] = per_feature
             ws_bytes = per_feature * d
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         st = lib.la_backward_qk_norm_rope(
             dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
             dk.data_ptr(), _ptr(dwq), _ptr(dwk), strides, wq, wk, bool(norm), eps, rope, B, Hq,
-            Hk, N, d, code, wcode, _ptr(ws), ws_bytes, on.stream)
+            Hk, N, d, code, wcode, _ptr(ws), ws_bytes, to)
     finally:
-        on.leave()
+        if back >= 0:
+            _leave(back)
     if st:
         _raise_if(st)
     return dq, dk, dwq, dwk
@@ -659,8 +658,9 @@ def _gate(gate) -> int:
 
 
 def _check_seq(x, gates, *ts):
-    """[B, N, C] (or [B, C]) tensors of x's shape, dtype and device, and gates."""
-    shape, dtype, device = x.shape, x.dtype, x.device
+    """[B, N, C] (or [B, C]) tensors of x's shape, dtype and device, and gates;
+    returns the device's index."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
     for t in ts:
         if t.shape != shape:
             raise ValueError("x, gates, out and the gradients must share one shape")
@@ -670,23 +670,22 @@ def _check_seq(x, gates, *ts):
         raise ValueError("x, gates, out and the gradients must share one shape")
     if gates.dtype is not dtype and gates.dtype is not _torch().float32:
         raise TypeError("gates must be float32 or of x's dtype")
-    if not x.is_cuda:
-        raise ValueError("all tensors must be on one CUDA device")
     for t in (x, gates, *ts):
-        if t.device != device:
+        if index < 0 or t.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
         if t.stride(-1) != 1 and shape[-1] > 1:
             raise ValueError("the last dimension must be contiguous")
+    return index
 
 
-def _check_state(B, C, device, *hs):
+def _check_state(B, C, index, *hs):
     float32 = _torch().float32
     for h in hs:
         if h is None:
             continue
         if h.shape != (B, C) or h.dtype is not float32:
             raise ValueError("a state must be float32 [B, C]")
-        if h.device != device:
+        if h.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
         if not h.is_contiguous():
             raise ValueError("a state must be contiguous")
@@ -734,18 +733,19 @@ def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = 
     if h_last is None:
         h_last = torch.empty(B, C, dtype=torch.float32, device=device)
     form = _gate(gate)
-    _check_seq(x, gates, out)
-    _check_state(B, C, device, h0, h_last)
+    index = _check_seq(x, gates, out)
+    _check_state(B, C, index, h0, h_last)
     code, gcode, lib = _code(x.dtype), _code(gates.dtype), load_library()
-    on = _Device(device, stream)
+    to, back = _enter(index, stream)
     try:
         ws, ws_bytes = _recurrence_workspace(lib, B, C, code, device, stream)
         st = lib.la_forward_recurrence(
             x.data_ptr(), gates.data_ptr(), _ptr(h0), out.data_ptr(), h_last.data_ptr(),
             _seq_strides(x, gates, out), B, N, C, form, bool(complement), code, gcode, _ptr(ws),
-            ws_bytes, on.stream)
+            ws_bytes, to)
     finally:
-        on.leave()
+        if back >= 0:
+            _leave(back)
     if st:
         _raise_if(st)
     return out, h_last
@@ -774,22 +774,23 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
     form = _gate(gate)
     if not complement:
         x = None
-    _check_seq(dout, gates, out, dx, *([x] if x is not None else []))
+    index = _check_seq(dout, gates, out, dx, *([x] if x is not None else []))
     if dgates.dtype is not gates.dtype:
         raise TypeError("dgates must have the dtype of gates")
     _check_seq(dout, dgates)
-    _check_state(B, C, device, h0, dh_last, dh0)
+    _check_state(B, C, index, h0, dh_last, dh0)
     code, gcode, lib = _code(dout.dtype), _code(gates.dtype), load_library()
-    on = _Device(device, stream)
+    to, back = _enter(index, stream)
     try:
         ws, ws_bytes = _recurrence_workspace(lib, B, C, code, device, stream)
         st = lib.la_backward_recurrence(
             dout.data_ptr(), gates.data_ptr(), out.data_ptr(), _ptr(x), _ptr(h0),
             _ptr(dh_last), dx.data_ptr(), dgates.data_ptr(), dh0.data_ptr(),
             _seq_strides(dout, gates, out, x, dx, dgates), B, N, C, form, bool(complement),
-            code, gcode, _ptr(ws), ws_bytes, on.stream)
+            code, gcode, _ptr(ws), ws_bytes, to)
     finally:
-        on.leave()
+        if back >= 0:
+            _leave(back)
     if st:
         _raise_if(st)
     return dx, dgates, dh0
@@ -807,19 +808,19 @@ def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "va
     if h_out is None:
         h_out = h
     B, C = x.shape
-    device = x.device
     form = _gate(gate)
-    _check_seq(x, gates, out)
-    _check_state(B, C, device, h, h_out)
+    index = _check_seq(x, gates, out)
+    _check_state(B, C, index, h, h_out)
     code, gcode, lib = _code(x.dtype), _code(gates.dtype), load_library()
-    on = _Device(device, stream)
+    to, back = _enter(index, stream)
     try:
         st = lib.la_decode_step_recurrence(
             h.data_ptr(), h_out.data_ptr(), x.data_ptr(), gates.data_ptr(), out.data_ptr(),
             _STRIDES[3].pack(x.stride(0), gates.stride(0), out.stride(0)), B, C, form,
-            bool(complement), code, gcode, on.stream)
+            bool(complement), code, gcode, to)
     finally:
-        on.leave()
+        if back >= 0:
+            _leave(back)
     if st:
         _raise_if(st)
     return out
