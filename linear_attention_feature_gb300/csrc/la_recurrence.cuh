@@ -469,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
     int k = group / rounds, r = group % rounds;  // item and round of it
     Item it = item(0);
     int c = 0, here = 0;
-    bool part = false;  // the strip reaches beyond C
     bool ends = false;  // the item ends with the sequence
     int ahead = 0;      // steps of the item from this thread's first one on
     T *o = nullptr;     // its first token in the outputs
@@ -481,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             it = item(k);
             c = it.c0 + lane * V;
             here = min(max(p.C - c, 0), V);
-            part = it.c0 + kRow > p.C;
             const long long s0 = first_step(it, r) + warp * L;  // this thread's first step
             const long long t0 = kBack ? p.N - 1 - s0 : s0;
             ahead = (int)(it.end - s0);
@@ -489,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             o = static_cast<T *>(p.out[0].p) + it.b * p.out[0].b + t0 * p.out[0].n + c;
             if (kBack) oz = static_cast<G *>(p.out[1].p) + it.b * p.out[1].b + t0 * p.out[1].n + c;
         }
-        const bool edge = ahead <= L || part;  // masks are needed
+        const bool edge = ahead <= L;  // the item ends in or before these steps
         // The state before the item's first token enters the map of the first
         // warp, and is read by that warp alone: it has been used when the state
         // behind the last token is written, which may be to the same place.
@@ -635,10 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
             state = fma_v(m[0], state, m[1]);
         }
         // the L tokens again, from there
-        auto walk = [&](auto at_edge) {
+        auto walk = [&](auto at_edge, auto whole) {
             auto put = [&](auto *dst, const Vec<V> &v) {
                 using E = std::remove_reference_t<decltype(*dst)>;
-                if ((kTma || p.out_vec) && (!at_edge.value || here == V)) {
+                if ((kTma || p.out_vec) && (whole.value || here == V)) {
                     narrow(reinterpret_cast<Mem<E, V> *>(dst), v);
                 } else {
 #pragma unroll
@@ -679,12 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         };
         if (!p.maps_only) {
             if (edge)
-                walk(Flag<true>());
+                walk(Flag<true>(), Flag<false>());
+            else if (it.c0 + kRow > p.C)  // a strip that reaches beyond C
+                walk(Flag<false>(), Flag<false>());
             else
-                walk(Flag<false>());
+                walk(Flag<false>(), Flag<true>());
             // the state behind the last token, as its warp has it: forward, these
             // are the bits that `out` was rounded from
-            if (edge && p.last && ends && ahead > 0 && ahead <= L)
+            if (edge && p.last && ends && ahead > 0)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     if (e < here) p.last[(long long)it.b * p.C + c + e] = state.v[e];
