@@ -29,7 +29,8 @@
 // Rows that TMA tiles cannot take (strides or bases that are not multiples of 16
 // bytes) come by cp.async: the 16-byte units of memory that hold the strip's
 // part of the row, wherever it begins in the first of them (2 x 32768 x 2047
-// bf16: 338 us; with a bulk copy per row 401 us).
+// bf16: 298 us, against 152 us for the 2048 of whole units; when a bulk copy per
+// row was tried it took 401 us against 338 us).
 //
 // Where even clusters would leave most SMs idle (few channels, long sequences),
 // a sequence is cut into pieces and walked twice: once for the maps of the
