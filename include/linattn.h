@@ -597,7 +597,9 @@ unsigned long long la_kernel_launch_count(void);
  * la_debug_fail_next_allocs -- the next `n` stream-ordered workspace
  * allocations of the forward kernels (tensor-core launches given no
  * workspace, and CUDA-core launches over more than one segment per head, or
- * non-causal) fail: those calls return LA_ERR_NO_MEMORY and enqueue nothing.
+ * non-causal), of the recurrence and of la_backward_qk_norm_rope (given no
+ * workspace) fail: those calls return LA_ERR_NO_MEMORY and enqueue nothing,
+ * la_backward_qk_norm_rope at most the zeros of a side without rows.
  * n = 0 clears the hook; LA_ERR_INVALID_ARG for n < 0.
  */
 la_status la_debug_inject_timeout(long long wait_cycles, int hold_segment);

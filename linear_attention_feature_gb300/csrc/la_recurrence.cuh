@@ -790,7 +790,7 @@ Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&
     const long long most = clusters_of(1, smem);
     for (int P = 2; P <= kMaxPieces; ++P) {
         const int steps = (int)(((long long)p.N + (long long)P * tile - 1) / ((long long)P * tile)) * tile;
-        const int pieces = (p.N + steps - 1) / steps;
+        const int pieces = (int)(((long long)p.N + steps - 1) / steps);
         if (pieces != P || steps < 4 * tile) continue;
         const double rounds = steps / tile + 2;
         const double c = 0.6 * rounds * (double)((items * (P - 1) + most - 1) / most) +
