@@ -152,37 +152,40 @@ __device__ __forceinline__ void turn_of(long long pos, unsigned long long turns,
         __sincosf(t * 1.46291807926715968e-9f, s, c);  // pi 2^-31
 }
 
-// Sum over a row of K chunks of V terms in each of 2^bits lanes, N sums at
-// once.  Term e of chunk j in lane l stands for pair ((j << bits) + l) V + e; the
-// sum is the binary tree over the pair's bits from the lowest up, so that it
-// does not depend on V: a row gives the same bits whatever its alignment.
-template <int N, int K, int P>
+// Sum over a row of K S chunks of 2 P / S terms in each of 2^bits lanes, N sums
+// at once.  Term e of chunk c in lane l stands for pair ((c << bits) + l) 2 P / S +
+// e; the sum is the binary tree over the pair's bits from the lowest up, so that
+// it does not depend on the vectors: a row gives the same bits whatever its
+// alignment.
+template <int S, int N, int K, int P>
 __device__ __forceinline__ void row_sum(float2 (&t)[N][K][P], int bits, float (&sum)[N]) {
-    float u[N][K];
+    constexpr int C = K * S;
+    float u[N][C];
 #pragma unroll
     for (int q = 0; q < N; ++q)
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            float w[P];
+            float w[2 * P];
 #pragma unroll
-            for (int e = 0; e < P; ++e) w[e] = __fadd_rn(t[q][j][e].x, t[q][j][e].y);
+            for (int e = 0; e < P; ++e) w[2 * e] = t[q][j][e].x, w[2 * e + 1] = t[q][j][e].y;
 #pragma unroll
-            for (int o = 1; o < P; o *= 2)
+            for (int o = 1; o < 2 * P / S; o *= 2)
 #pragma unroll
-                for (int e = 0; e < P; e += 2 * o) w[e] = __fadd_rn(w[e], w[e + o]);
-            u[q][j] = w[0];
+                for (int e = 0; e < 2 * P; e += 2 * o) w[e] = __fadd_rn(w[e], w[e + o]);
+#pragma unroll
+            for (int c = 0; c < S; ++c) u[q][j * S + c] = w[c * (2 * P / S)];
         }
     for (int o = 1; o >> bits == 0; o <<= 1)
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
-            for (int j = 0; j < K; ++j) u[q][j] += __shfl_xor_sync(~0u, u[q][j], o);
+            for (int j = 0; j < C; ++j) u[q][j] += __shfl_xor_sync(~0u, u[q][j], o);
 #pragma unroll
     for (int q = 0; q < N; ++q) {
 #pragma unroll
-        for (int o = 1; o < K; o *= 2)
+        for (int o = 1; o < C; o *= 2)
 #pragma unroll
-            for (int j = 0; j < K; j += 2 * o) u[q][j] += u[q][j + o];
+            for (int j = 0; j < C; j += 2 * o) u[q][j] += u[q][j + o];
         sum[q] = u[q][0];
     }
 }
@@ -194,21 +197,27 @@ constexpr int ring_depth() { return kBack ? 3 : 4; }
 // 16-byte units of memory that hold it, wherever it begins in the first of them.
 template <typename T, int V>
 constexpr bool whole_rows() { return sizeof(T) * V < 4; }
+// Vectors of one of a lane's K parts of a row.
+template <int V>
+constexpr int vectors() { return V == 1 ? 4 : 2; }
 // Bytes that a row's units take.
 __host__ __device__ inline int row_units(int d) { return (2 * d + 14 + 15) / 16 * 16; }
 template <typename T, int V, int K, bool kBack>
 int ring_bytes(int d, int lane_bits) {
     return ring_depth<kBack>() * (kBack ? 2 : 1) *
            (whole_rows<T, V>() ? (kThreads >> lane_bits) * row_units(d)
-                               : K * 2 * kThreads * V * (int)sizeof(T));
+                               : K * vectors<V>() * kThreads * V * (int)sizeof(T));
 }
 
-// A row is shared by 2^lane_bits lanes of a warp.  A lane takes K chunks of V
-// pairs, each as two vectors of V values: (lo, hi) = features (2i, 2i + V)
-// where pairs are neighbours (kInter, and where d is odd, which leaves the last
-// alone), else (i, i + half) in the rotated part and (i + half, i + d / 2) in
-// the rest: both values of a pair are always in one thread and every access is
-// one vector.
+// A row is shared by 2^lane_bits lanes of a warp.  A lane takes K parts of V
+// pairs, each as two vectors of V values, such that both values of a pair are in
+// one thread and a warp's access covers memory without gaps: where pairs are
+// neighbours (kInter), the vectors of V / 2 pairs of two chunks 2^lane_bits
+// vectors apart (vectors side by side in a lane leave half of each 32 bytes to the
+// next access: 2 x (16 + 16) x 8192 x 128 fp32 127 us, 92 us with them apart); else
+// the features i and i + half in the rotated part, i + half and i + d / 2 in the
+// rest.  With V = 1 a part is two pairs of two chunks, four single values; an odd
+// d leaves the last alone and makes the unrotated pairs neighbours.
 //
 // A block keeps to one side.  Its groups of lanes are a tile of 2^token_bits
 // tokens times as many heads as are left, so a tile is H / heads rows per group;
@@ -220,7 +229,9 @@ int ring_bytes(int d, int lane_bits) {
 // Backward, the sums of g n stay in registers until the block's end.
 template <typename T, int V, int K, bool kInter, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_constant__ Params p) {
-    constexpr int P = (V + 1) / 2;  // packed pairs per chunk (V = 1: half of one)
+    constexpr int P = (V + 1) / 2;  // packed pairs per part
+    constexpr int kVecs = vectors<V>();
+    constexpr int kChunks = kInter || V == 1 ? 2 : 1;  // per part
     constexpr int kDepth = ring_depth<kBack>(), kSrc = kBack ? 2 : 1;
     constexpr bool kWhole = whole_rows<T, V>();
     extern __shared__ __align__(16) char smem[];
@@ -249,17 +260,26 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     for (int i = threadIdx.x; i < p.d; i += kThreads) weight[i] = weight_at(sd.w, p.w_bf16, i);
     __syncthreads();
 
-    int lo[K], hi[K];  // this lane's features
-    bool l_ok[K], h_ok[K];
+    auto pair = [&](int j, int e) {  // pair e < 2 P of part j
+        constexpr int n = 2 * P / kChunks;  // per chunk
+        return (lane + ((j * kChunks + e / n) << bits)) * n + e % n;
+    };
+    int at[K][kVecs];  // the vectors' first features
+    bool has[K][kVecs];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const int i = (lane + (j << bits)) * V;  // first pair of the chunk
-        const bool rot = i < p.half, next = kInter || (!rot && p.d % 2);
-        lo[j] = next ? 2 * i : rot ? i : i + p.half;
-        hi[j] = next ? 2 * i + V : rot ? i + p.half : i + p.d / 2;
-        l_ok[j] = i < pairs;
-        h_ok[j] = l_ok[j] && hi[j] < p.d;
-    }
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int m = 0; m < kVecs; ++m) {
+            const int i = pair(j, V == 1 ? m / 2 : kInter ? m * P : 0);
+            const bool rot = i < p.half, next = kInter || (!rot && p.d % 2);
+            if (kInter && V > 1)
+                at[j][m] = 2 * i;
+            else if (m % 2 == 0)
+                at[j][m] = next ? 2 * i : rot ? i : i + p.half;
+            else
+                at[j][m] = next ? 2 * i + 1 : rot ? i + p.half : i + p.d / 2;
+            has[j][m] = i < pairs && at[j][m] < p.d;
+        }
 
     // the batch entry and token of this group in a tile
     auto locate = [&](long long tile, int &b, int &n) {
@@ -269,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         n = ok ? (int)(tok - (long long)b * p.N) : 0;
         return ok;
     };
-    auto slot = [&](int depth, int src, int j, int half) {
-        return ring + (((depth * kSrc + src) * K + j) * 2 + half) * kThreads;
+    auto slot = [&](int depth, int src, int j, int m) {
+        return ring + (((depth * kSrc + src) * K + j) * kVecs + m) * kThreads;
     };
 
     auto row_slot = [&](int depth, int src) {  // with kWhole
@@ -308,16 +328,14 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                 if (kBack) fetch_units(row_slot(f_depth, kSrc - 1), fg);
             }
 #pragma unroll
-            for (int j = 0; j < K && !kWhole; ++j) {
-                if (ok && l_ok[j]) {
-                    if (!kBack || p.norm) fetch<T, V>(slot(f_depth, 0, j, 0), fx + lo[j], policy);
-                    if (kBack) fetch<T, V>(slot(f_depth, kSrc - 1, j, 0), fg + lo[j], policy);
+            for (int j = 0; j < K && !kWhole; ++j)
+#pragma unroll
+                for (int m = 0; m < kVecs; ++m) {
+                    if (!ok || !has[j][m]) continue;
+                    if (!kBack || p.norm)
+                        fetch<T, V>(slot(f_depth, 0, j, m), fx + at[j][m], policy);
+                    if (kBack) fetch<T, V>(slot(f_depth, kSrc - 1, j, m), fg + at[j][m], policy);
                 }
-                if (ok && h_ok[j]) {
-                    if (!kBack || p.norm) fetch<T, V>(slot(f_depth, 0, j, 1), fx + hi[j], policy);
-                    if (kBack) fetch<T, V>(slot(f_depth, kSrc - 1, j, 1), fg + hi[j], policy);
-                }
-            }
             f_depth = f_depth + 1 == kDepth ? 0 : f_depth + 1;
             --f_left;
             fx += fx_step;
@@ -332,62 +350,54 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     };
     if (!kWhole)  // lanes and rows without values read zeros, or what an earlier row left
 #pragma unroll
-        for (int i = 0; i < kDepth * kSrc * K * 2; ++i)
+        for (int i = 0; i < kDepth * kSrc * K * kVecs; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) ring[i * kThreads].v[e] = T(0.f);
     for (int i = 0; i < kDepth - 1; ++i) fetch_row();
 
-    // chunk j of source src in a place of the ring, as the pairs' first and
-    // second values; `at` is the row's address where whole rows are copied
-    auto open = [&](int depth, int src, int j, bool ok, unsigned at, float2 (&m0)[P],
-                    float2 (&m1)[P]) {
-        float e[2 * V];
-        if constexpr (kWhole) {
-            const T *r = reinterpret_cast<const T *>(row_slot(depth, src) + (at & 15u));
-            e[0] = ok && l_ok[j] ? to_f(r[lo[j]]) : 0.f;
-            e[1] = ok && h_ok[j] ? to_f(r[hi[j]]) : 0.f;
-        } else {
-            widen(slot(depth, src, j, 0), e);
-            widen(slot(depth, src, j, 1), e + V);
-        }
+    // the values of a part's vectors as the pairs' first and second ones, and
+    // where value i of those lies
+    auto sort = [&](const float (&e)[4 * P], float2 (&m0)[P], float2 (&m1)[P]) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            if (V == 1) {
-                m0[0] = make_float2(e[0], 0.f);
-                m1[0] = make_float2(e[1], 0.f);
-            } else if (kInter) {
-                m0[i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
-                m1[i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
+            if (kChunks == 2) {
+                m0[i] = make_float2(e[4 * i], e[4 * i + 2]);
+                m1[i] = make_float2(e[4 * i + 1], e[4 * i + 3]);
             } else {
-                m0[i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
-                m1[i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
+                m0[i] = make_float2(e[2 * i], e[2 * i + 1]);
+                m1[i] = make_float2(e[2 * P + 2 * i], e[2 * P + 2 * i + 1]);
             }
         }
+    };
+    auto place = [](int second, int i) {
+        return kChunks == 2 ? 2 * i + second : second * 2 * P + i;
+    };
+    // part j of source src in a place of the ring; `begin` is the row's address
+    // where whole rows are copied
+    auto open = [&](int depth, int src, int j, bool ok, unsigned begin, float2 (&m0)[P],
+                    float2 (&m1)[P]) {
+        float e[4 * P];
+#pragma unroll
+        for (int m = 0; m < kVecs; ++m)
+            if constexpr (kWhole) {
+                const T *r = reinterpret_cast<const T *>(row_slot(depth, src) + (begin & 15u));
+                e[m] = ok && has[j][m] ? to_f(r[at[j][m]]) : 0.f;
+            } else {
+                widen(slot(depth, src, j, m), e + m * V);
+            }
+        sort(e, m0, m1);
     };
 
     float2 w0[K][P], w1[K][P], dw0[K][P], dw1[K][P];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        float e[2 * V];
+        float e[4 * P];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            e[i] = l_ok[j] ? weight[lo[j] + i] : 0.f;
-            e[V + i] = h_ok[j] ? weight[hi[j] + i] : 0.f;
-        }
+        for (int i = 0; i < 4 * P; ++i)
+            e[i] = has[j][i / V] ? weight[at[j][i / V] + i % V] : 0.f;
+        sort(e, w0[j], w1[j]);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            if (V == 1) {
-                w0[j][0] = make_float2(e[0], 0.f);
-                w1[j][0] = make_float2(e[1], 0.f);
-            } else if (kInter) {
-                w0[j][i] = make_float2(e[4 * i % (2 * V)], e[(4 * i + 2) % (2 * V)]);
-                w1[j][i] = make_float2(e[(4 * i + 1) % (2 * V)], e[(4 * i + 3) % (2 * V)]);
-            } else {
-                w0[j][i] = make_float2(e[2 * i], e[(2 * i + 1) % (2 * V)]);
-                w1[j][i] = make_float2(e[V + 2 * i], e[(V + 2 * i + 1) % (2 * V)]);
-            }
-            dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
-        }
+        for (int i = 0; i < P; ++i) dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
     }
 
     int depth = 0;
@@ -405,9 +415,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         for (int j = 0; j < K; ++j)
 #pragma unroll
             for (int e = 0; e < 2 * P; ++e) {
-                const int i = (lane + (j << bits)) * V + e;
+                const int i = pair(j, e);
                 float c = 1.f, s = 0.f;
-                if (e < V && i < p.half) turn_of<sizeof(T) == 4>(pos, turns[i], &c, &s);
+                if (i < p.half) turn_of<sizeof(T) == 4>(pos, turns[i], &c, &s);
                 (e % 2 ? cs[j][e / 2].y : cs[j][e / 2].x) = c;
                 (e % 2 ? sn[j][e / 2].y : sn[j][e / 2].x) = s;
             }
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             float r = 1.f, m = 0.f;
             if (p.norm) {
                 float sum[kSrc];
-                row_sum<kSrc, K, P>(t, bits, sum);
+                row_sum<kChunks>(t, bits, sum);
                 r = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
                 // n w g summed is r sum(v w g)
                 if (kBack) m = __fmul_rn(__fmul_rn(sum[kSrc - 1], p.inv_d), r);
@@ -483,14 +493,15 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                             r2, __ffma2_rn(n1, m2, __fmul2_rn(w1[j][i], g1[j][i])));
                     }
                 }
-                float e[2 * V];  // as in memory: lo, then hi
+                float e[4 * P];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    e[kInter ? 2 * i : i] = i % 2 ? o0[i / 2].y : o0[i / 2].x;
-                    e[kInter ? 2 * i + 1 : V + i] = i % 2 ? o1[i / 2].y : o1[i / 2].x;
+                for (int i = 0; i < 2 * P; ++i) {
+                    e[place(0, i)] = i % 2 ? o0[i / 2].y : o0[i / 2].x;
+                    e[place(1, i)] = i % 2 ? o1[i / 2].y : o1[i / 2].x;
                 }
-                if (ok && l_ok[j]) narrow<T, V>(y + lo[j], e);
-                if (ok && h_ok[j]) narrow<T, V>(y + hi[j], e + V);
+#pragma unroll
+                for (int m = 0; m < kVecs; ++m)
+                    if (ok && has[j][m]) narrow<T, V>(y + at[j][m], e + m * V);
             }
             depth = depth + 1 == kDepth ? 0 : depth + 1;
             at_x += (unsigned)(fx_step * sizeof(T));
@@ -510,19 +521,17 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < 2 * P; ++e) {
             float a = e % 2 ? dw0[j][e / 2].y : dw0[j][e / 2].x;
             float c = e % 2 ? dw1[j][e / 2].y : dw1[j][e / 2].x;
             for (int o = 1 << bits; o < 32; o <<= 1) {
                 a += __shfl_xor_sync(~0u, a, o);
                 c += __shfl_xor_sync(~0u, c, o);
             }
-            const int i0 = kInter ? 2 * e : e, i1 = kInter ? 2 * e + 1 : V + e;
-            const int f0 = i0 < V ? lo[j] + i0 : hi[j] + i0 - V;
-            const int f1 = i1 < V ? lo[j] + i1 : hi[j] + i1 - V;
+            const int i0 = place(0, e), i1 = place(1, e);
             if ((threadIdx.x & 31) == lane) {
-                if (i0 < V ? l_ok[j] : h_ok[j]) sum[warp][f0] = a;
-                if (i1 < V ? l_ok[j] : h_ok[j]) sum[warp][f1] = c;
+                if (has[j][i0 / V]) sum[warp][at[j][i0 / V] + i0 % V] = a;
+                if (has[j][i1 / V]) sum[warp][at[j][i1 / V] + i1 % V] = c;
             }
         }
     __syncthreads();
@@ -597,12 +606,13 @@ bool same(const la_strides &a, const la_strides &b) {
     return a.b == b.b && a.h == b.h && a.n == b.n;
 }
 
-// Values per access: the most (a power of two, up to `most`) that divide the
-// row's two halves and its rotated part and at which every row of every tensor
-// is aligned.
+// Values per access: the most (a power of two, up to `most`) that divide the row
+// (its two halves and its rotated part, where pairs are not neighbours) and at
+// which every row of every tensor is aligned.
 int vector_of(const Params &p, int most, int elem) {
     // a power of two divides all of these if it divides their union
-    unsigned long long all = (unsigned)(p.half | (p.d % 2 ? 1 : p.d / 2)) | (unsigned)most;
+    unsigned long long all =
+        (unsigned)(p.interleaved ? p.d : p.half | (p.d % 2 ? 1 : p.d / 2)) | (unsigned)most;
     auto add = [&](const void *q, const la_strides &s, int H) {
         all |= (uintptr_t)q / (uintptr_t)elem;
         if (p.B > 1) all |= (unsigned long long)s.b;
@@ -645,7 +655,7 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
     const int v = vector_of(p, 16 / (int)sizeof(T), (int)sizeof(T));
     const int chunks = ((p.d + 1) / 2 + v - 1) / v;  // of a row
-    // Chunks per lane: more of the small ones, so that a warp takes more rows at a
+    // Pairs / V per lane: more of the small ones, so that a warp takes more rows at a
     // time (2 x 24 x 4000 rows of 66 bf16 values: 60 us with two single pairs per
     // lane, 41 us with four; of 36: 20 us with one double pair, 14 us with two).
     const int per_lane = v >= 4 ? 1 : v == 2 ? 2 : 4;
@@ -689,7 +699,7 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     else if (v == 2)
         e = launch_rows<T, 2, 2, kBack>(p, (unsigned)blocks, stream);
     else
-        e = launch_rows<T, 1, 4, kBack>(p, (unsigned)blocks, stream);
+        e = launch_rows<T, 1, 2, kBack>(p, (unsigned)blocks, stream);
     if (e == cudaSuccess) note_launches(1);
     if (e == cudaSuccess && want_dw) {
         e = tchost::launch_dependent(qk_weight_kernel, 2, 1024, 0, stream,
