@@ -752,10 +752,13 @@ struct Cut {
     size_t smem;
 };
 
-// The cheapest cut, counted in rounds: a cluster takes ceil(items / clusters)
-// strips, one after the other, each of ceil(steps / (S tile)) rounds and about
-// two more for the start.  clusters_of: how many run at once.
-template <typename F>
+// The cheapest cut, counted in rounds of a block alone (1.1 us forward, 0.95 us
+// backward for bf16 logits with complement): a cluster takes ceil(items /
+// clusters) strips, one after the other, each of ceil(steps / (S tile)) rounds and
+// about two more for the start.  Measured, a round of S blocks takes 1.2 to 1.3
+// times one of a block at S = 16 (more maps to join).  clusters_of: how many run
+// at once.
+template <bool kBack, typename F>
 Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&clusters_of) {
     const long long items = (long long)p.B * p.strips;
     Cut best{};
@@ -775,15 +778,17 @@ Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&
         if (most < 1) continue;
         const long long waves = (items + most - 1) / most;
         const long long rounds = ((long long)p.N + (long long)S * tile - 1) / ((long long)S * tile);
-        const double c = (double)waves * (double)(rounds + 2);
+        const double c = (double)waves * ((1 + 0.015 * S) * (double)rounds + 2) + 5;
         if (!best.S || c < cost) {
             cost = c;
             best = {S, (int)std::min(items, most), 1, p.N, stages, smem};
         }
     }
-    // In pieces, of blocks alone: the maps at about 0.6 of a walk, then the
-    // walk, 6 rounds for the second launch and one for each 8 maps to join.  It
-    // has to be clearly less, since it reads the input twice.
+    // In pieces, of blocks alone: a round of the maps takes 0.82 of one of the walk
+    // forward (of its three tensors two are read), 0.55 backward; two launches, the
+    // maps between them and the joining took 10 rounds more.  1 x N x C bf16, in
+    // clusters / in pieces: forward 65536 x 256 49 / 38 us, x 384 50 / 57; backward
+    // 65536 x 512 109 / 95, x 768 129 / 139; 16384 x 512 32 / 30, 8192 x 512 19 / 20.
     if (!best.S || items > kFewStrips) return best;
     size_t smem;
     const int stages = stages_of(1, smem);
@@ -793,10 +798,11 @@ Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&
         const int pieces = (int)(((long long)p.N + steps - 1) / steps);
         if (pieces != P || steps < 4 * tile) continue;
         const double rounds = steps / tile + 2;
-        const double c = 0.6 * rounds * (double)((items * (P - 1) + most - 1) / most) +
-                         rounds * (double)((items * P + most - 1) / most) + 6 + P / 8;
-        if (c < 0.9 * cost) {
-            cost = c / 0.9;
+        const double c =
+            (kBack ? 0.55 : 0.82) * rounds * (double)((items * (P - 1) + most - 1) / most) +
+            rounds * (double)((items * P + most - 1) / most) + 10;
+        if (c < cost) {
+            cost = c;
             best = {1, (int)std::min(items * P, most), P, steps, stages, smem};
         }
     }
@@ -856,7 +862,7 @@ la_status launch_scan(const char *who, Params &p, int read, Workspace ws, cudaSt
     const int bytes = tma ? stage_bytes<T, G, V, L, true, kBack>(p.complement)
                           : stage_bytes<T, G, V, L, false, kBack>(p.complement);
     // backward, a stage is refilled two rounds after its own
-    const Cut cut = best_cut(p, kTile, bytes, V, kBack ? 4 : 2,
+    const Cut cut = best_cut<kBack>(p, kTile, bytes, V, kBack ? 4 : 2,
                              [&](int S, size_t) { return at_once[S].load(); });
     if (!cut.S) return rec_fail(LA_ERR_UNSUPPORTED, who, "no kernel configuration fits");
     p.stages = cut.stages;

@@ -176,7 +176,7 @@ def test_state_in_place(B, N, C):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("N, launches", [(40000, 1), (200000, 2)])
+@pytest.mark.parametrize("N, launches", [(4000, 1), (40000, 2), (200000, 2)])
 def test_workspaces(N, launches):
     # few channels: from some length on a sequence is cut into pieces (their
     # maps, then the walk).  The binding brings a workspace on the current
