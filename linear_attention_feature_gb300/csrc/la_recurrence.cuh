@@ -265,12 +265,18 @@ constexpr int stage_bytes(int complement) {
                          row_bytes<T, V, kTma>() * (kBack ? 2 + complement : 1));
 }
 
-// Waits for a stage's copies or the cluster's maps, with a limit: afterwards the
-// launch is marked as failed in the status word and goes on without waiting.
+// Waits for a stage's copies, the other group's state or (kCluster) the maps of the
+// cluster's blocks, with a limit: afterwards the launch is marked as failed in the
+// status word and goes on without waiting.
+template <bool kCluster>
 __device__ __forceinline__ void wait_for(uint64_t *bar, unsigned parity, bool &dead, int *status) {
-    if (dead || tc::mbar_try_wait_ns(bar, parity, kSuspendNs)) return;
+    auto done = [&]() {
+        return kCluster ? tc::mbar_try_wait_cluster_ns(bar, parity, kSuspendNs)
+                        : tc::mbar_try_wait_ns(bar, parity, kSuspendNs);
+    };
+    if (dead || done()) return;
     const long long deadline = clock64() + kWaitCycles;
-    while (!tc::mbar_try_wait_ns(bar, parity, kSuspendNs))
+    while (!done())
         if (clock64() > deadline) {
             dead = true;
             if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (e < here) h0.v[e] = p.h0[(long long)it.b * p.C + c + e];
-        wait_for(&full[stage], stage_phase, dead, p.status);
+        wait_for<false>(&full[stage], stage_phase, dead, p.status);
         // where this thread's rows begin, see values()
         unsigned at[4] = {}, step[4] = {};
         if (!kTma)
@@ -594,12 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         // written again by round R + 3, after that group's barrier of round
         // R + 2, before which this round's readers are done.
         Vec<V> state = init, product = all_v<V>(1.f);
-        wait_for(&state_in[slot], slot_phase, dead, p.status);
+        wait_for<false>(&state_in[slot], slot_phase, dead, p.status);
         if (r > 0) {
             state = map_at(states[slot][lane])[0];
             if (p.maps_only) product = map_at(states[slot][lane])[1];
         }
-        if (S > 1) wait_for(&maps_in[slot], slot_phase, dead, p.status);
+        if (S > 1) wait_for<true>(&maps_in[slot], slot_phase, dead, p.status);
         if (last_warp) {
             Vec<V> next = state;
             auto join = [&](const Vec<V> *m) {

@@ -80,6 +80,21 @@ __device__ __forceinline__ bool mbar_try_wait_ns(uint64_t *bar, uint32_t parity,
     return ok != 0;
 }
 
+// The same where other blocks of the cluster complete the phase (st.async): what
+// they wrote is visible after the wait only if it acquires at cluster scope; the
+// form above acquires at the block's.
+__device__ __forceinline__ bool mbar_try_wait_cluster_ns(uint64_t *bar, uint32_t parity,
+                                                         uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, "
+        "%3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+
 // Non-blocking test of the phase with the given parity (never suspends).
 __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
