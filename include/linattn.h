@@ -593,6 +593,10 @@ unsigned long long la_kernel_launch_count(void);
  * LA_ERR_TIMEOUT in the device status word, every later wait of the launch
  * passes through, it finishes (outputs invalid) and la_check_device_status
  * reports LA_ERR_TIMEOUT.  LA_ERR_INVALID_ARG for wait_cycles < 4096.
+ * A launch of la_forward_recurrence or la_backward_recurrence takes the hook
+ * as well, whichever comes first: there, the first block of every thread-block
+ * cluster never fetches its rows of round `hold_segment` (0 or 1, of the
+ * first rounds; -1: fetches all).
  *
  * la_debug_fail_next_allocs -- the next `n` stream-ordered workspace
  * allocations of the forward kernels (tensor-core launches given no

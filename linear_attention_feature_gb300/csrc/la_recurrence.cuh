@@ -76,6 +76,7 @@ constexpr size_t kSmem = 208 * 1024;  // stages and maps; 227 KB with the static
 
 constexpr long long kWaitCycles = 1LL << 32;  // bound of a wait, about 2 s
 constexpr uint32_t kSuspendNs = 20000;  // a waiting warp sleeps this long between polls, at most
+constexpr long long kFlightCycles = 1 << 20;  // a store to another block takes far less
 
 // V channels of one thread; two go through the packed fp32 instructions, which
 // round like the single ones.
@@ -243,6 +244,8 @@ struct Params {
     float *last;         // h_last; backward dh0
     const float *h0;     // backward: h_0, for the first token's gate
     int *status;
+    long long wait_cycles;  // bound of a wait
+    int hold;               // test hook: first blocks never fetch this one of the first rounds
     int B, N, C, complement, strips, stages;
     int out_vec;  // rows of the outputs are aligned to V values
     // A sequence in more than one piece of `steps` tokens (in scan order): a
@@ -265,24 +268,25 @@ constexpr int stage_bytes(int complement) {
                          row_bytes<T, V, kTma>() * (kBack ? 2 + complement : 1));
 }
 
-// Waits for a stage's copies, the other group's state or (kCluster) the maps of the
-// cluster's blocks, with a limit: afterwards the launch is marked as failed in the
-// status word and goes on without waiting.
+// A warp's wait for a stage's copies, the other group's state or (kCluster) the maps
+// of the cluster's blocks, with a limit: afterwards the launch is marked as failed in
+// the status word, and the warp is out (false, in all lanes).
 template <bool kCluster>
-__device__ __forceinline__ void wait_for(uint64_t *bar, unsigned parity, bool &dead, int *status) {
+__device__ __forceinline__ bool wait_for(uint64_t *bar, unsigned parity, const Params &p) {
     auto done = [&]() {
-        return kCluster ? tc::mbar_try_wait_cluster_ns(bar, parity, kSuspendNs)
-                        : tc::mbar_try_wait_ns(bar, parity, kSuspendNs);
+        return __all_sync(~0u, kCluster ? tc::mbar_try_wait_cluster_ns(bar, parity, kSuspendNs)
+                                        : tc::mbar_try_wait_ns(bar, parity, kSuspendNs));
     };
-    if (dead || done()) return;
-    const long long deadline = clock64() + kWaitCycles;
+    if (done()) return true;
+    const long long deadline = clock64() + p.wait_cycles;
     while (!done())
-        if (clock64() > deadline) {
-            dead = true;
-            if (atomicCAS(status, 0, (int)LA_ERR_TIMEOUT) == 0)
-                atomicExch(status + 1, (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
-            return;
+        if (__any_sync(~0u, clock64() > deadline)) {
+            if (atomicCAS(p.status, 0, (int)LA_ERR_TIMEOUT) == 0)
+                atomicExch(p.status + 1,
+                           (int)((blockIdx.x << 20) | (tc::smem_u32(bar) & 0xFFFFFu)));
+            return false;
         }
+    return true;
 }
 
 // A thread's part (A, H) of a block's map to the same place in the block `to` of
@@ -464,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         tc::fence_mbar_init();
     }
     __syncthreads();
-    for (int i = group; i < p.stages; i += 2) fetch(i, i, item(0), i);
+    for (int i = group; i < p.stages; i += 2)
+        if (i != p.hold || rank != 0) fetch(i, i, item(0), i);
     // round 0 has no state to wait for, but a phase like every other's
     if (threadIdx.x < 32) tc::mbar_arrive(&state_in[0]);
     // the others' shared memory is written from here on
     if (S > 1) cluster.sync();
 
-    bool dead = false;
     // ring positions of this group's round R, and the parities of their phases
     int stage = group, stage_phase = 0, slot = group, slot_phase = 0, turn = 0;
     int k = group / rounds, r = group % rounds;  // item and round of it
@@ -482,6 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
     G *oz = nullptr;
     const long long o_turn = (kBack ? -2LL : 2LL) * round_steps * p.out[0].n;
     const long long oz_turn = -2LL * round_steps * p.out[1].n;
+    // A warp that waited in vain leaves the rounds, and from there on only takes part
+    // in its group's barriers: it starts no copies, sends no maps and arrives on no
+    // mbarrier, so that none is counted up out of turn (a warp that goes on has seen
+    // every phase before the one that it arrives for).  Who waits for it runs out of
+    // time in turn.  `lost`: the first round whose barrier it has not passed.
+    int lost = -1;
     for (int R = group; R < total; R += 2) {
         if (r <= 1 || turn == 0) {
             it = item(k);
@@ -531,7 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (e < here) h0.v[e] = p.h0[(long long)it.b * p.C + c + e];
-        wait_for<false>(&full[stage], stage_phase, dead, p.status);
+        if (!wait_for<false>(&full[stage], stage_phase, p)) {
+            lost = R;
+            break;
+        }
         // where this thread's rows begin, see values()
         unsigned at[4] = {}, step[4] = {};
         if (!kTma)
@@ -600,12 +613,18 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         // written again by round R + 3, after that group's barrier of round
         // R + 2, before which this round's readers are done.
         Vec<V> state = init, product = all_v<V>(1.f);
-        wait_for<false>(&state_in[slot], slot_phase, dead, p.status);
+        if (!wait_for<false>(&state_in[slot], slot_phase, p)) {
+            lost = R + 2;
+            break;
+        }
         if (r > 0) {
             state = map_at(states[slot][lane])[0];
             if (p.maps_only) product = map_at(states[slot][lane])[1];
         }
-        if (S > 1) wait_for<true>(&maps_in[slot], slot_phase, dead, p.status);
+        if (S > 1 && !wait_for<true>(&maps_in[slot], slot_phase, p)) {
+            lost = R + 2;
+            break;
+        }
         if (last_warp) {
             Vec<V> next = state;
             auto join = [&](const Vec<V> *m) {
@@ -705,13 +724,24 @@ __global__ void __launch_bounds__(kThreads, 1) rec_scan_kernel(const __grid_cons
         for (r += 2; r >= rounds; r -= rounds) ++k;
     }
     if (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (dead)  // copies may still be under way: leave after them
-        for (int i = max(0, total - p.stages); i < total; ++i)
-            tc::mbar_wait(&full[i % p.stages], (unsigned)(i / p.stages) & 1u,
-                          clock64() + kWaitCycles, nullptr);
+    if (lost >= 0) {
+        for (int R = lost; R < total; R += 2) tc::named_bar_sync(1 + group, kGroup);
+        // the tiles that this thread asked for and has not waited for: the last of
+        // each stage, the latest with round lost - 2, or before the rounds
+        if (kTma && tid == 0)
+            for (int left = p.stages, i = lost - 2 + left - (kBack && lost > group ? 2 : 0);
+                 left > 0; left -= 2, i -= 2)
+                if (i >= 0 && i < total && !(i == p.hold && rank == 0))
+                    tc::mbar_wait(&full[i % p.stages], (unsigned)(i / p.stages) & 1u,
+                                  clock64() + kWaitCycles, nullptr);
+    }
     if (S > 1) {  // no block leaves while another may still send to it
         asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
         asm volatile("barrier.cluster.wait;" ::: "memory");
+        // blocks that went on for longer have sent maps that nobody counts here
+        if (lost >= 0)
+            for (const long long until = clock64() + kFlightCycles; clock64() < until;)
+                __nanosleep(1000);
     }
 }
 
@@ -892,6 +922,9 @@ la_status launch_scan(const char *who, Params &p, int read, Workspace ws, cudaSt
         }
         p.start = reinterpret_cast<float *>(p.maps + (cut.pieces - 1) * states);
     }
+    p.wait_cycles = kWaitCycles;
+    p.hold = -1;
+    tc_debug_take_timeout(&p.wait_cycles, &p.hold);
     cfg.dynamicSmemBytes = cut.smem;
     at[0].val.clusterDim = {(unsigned)cut.S, 1, 1};
     int launches = 0;

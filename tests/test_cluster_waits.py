@@ -22,7 +22,7 @@ def test_waits_for_cluster_maps_acquire_at_cluster_scope():
     assert sorted(b for _, b in waits) == ["full", "maps_in", "state_in"]
     for scope, bar in waits:
         assert (scope == "<true>") == (bar in sent), (bar, scope)
-    body = text[text.index("void wait_for("):]
+    body = text[text.index("bool wait_for("):]
     assert re.search(r"kCluster \? tc::mbar_try_wait_cluster_ns", body)
     ptx = source("la_tc_ptx.cuh")
     form = ptx[ptx.index("bool mbar_try_wait_cluster_ns"):]
