@@ -443,7 +443,8 @@ typedef struct {
  *   h_last     [B][C] fp32 device, written with the state after the last
  *              token (unrounded), or NULL; may be h0 itself.
  *   strides    3 strides, of x, gates, out, or NULL: contiguous.
- *   B, N, C >= 0 (B*C == 0 is a no-op; N == 0 copies h0 to h_last).
+ *   B, N, C >= 0 (B*C == 0 is a no-op; N == 0 copies h0 to h_last); B * C / 32,
+ *              C / 32 rounded up, below 2^24, else LA_ERR_UNSUPPORTED.
  *   workspace  device buffer, 16-byte aligned, of
  *              la_recurrence_workspace_bytes(B, C, dtype) bytes, not used by
  *              anything else until `stream` has passed the call; or NULL: a

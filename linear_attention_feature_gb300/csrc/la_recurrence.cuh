@@ -962,7 +962,7 @@ la_status launch_gate(const char *who, Params &p, la_gate gate, int read, Worksp
 template <bool kBack>
 la_status launch(const char *who, Params &p, la_gate gate, la_dtype dtype, la_dtype gate_dtype,
                  Workspace ws, cudaStream_t s) {
-    if ((long long)p.B * ((p.C + 31) / 32) > 2147483647LL / kMaxPieces)
+    if (p.B * ((p.C + 31LL) / 32) > 2147483647LL / kMaxPieces)
         return rec_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     // a thread takes 4 bytes of x per token: two bf16 channels
     const int v = dtype == LA_F32 ? 1 : 2;
