@@ -389,7 +389,9 @@ la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out
  *   dq, dk     gradients of the inputs, written; may be dq_out and dk_out
  *              themselves with the same strides, otherwise no aliasing.
  *   dq_weight, dk_weight   [d] fp32 device, written, or NULL: not computed.
- *              Summed in a fixed order: repeated calls are bit-identical.
+ *              Summed in a fixed order (repeated calls are bit-identical) with
+ *              compensation: off by at most 19 * 2^-24 sum |g (.) n| over the
+ *              rows, however many, and the error of the terms themselves.
  *   strides    6 strides, of dq_out, dk_out, q, k, dq, dk, or NULL: contiguous.
  * Other arguments as la_qk_norm_rope (the same values as in the forward).
  *   workspace  device buffer for the weight gradients' partial sums, 16-byte

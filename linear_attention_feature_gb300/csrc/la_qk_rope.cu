@@ -55,6 +55,7 @@ struct Params {
     int B, N, d, half, interleaved, norm, w_bf16;
     float eps, inv_d;
     float *partial;  // backward: a row of d sums of g n for each block, or NULL
+    int sums_at;     // and where the threads' sums lie in shared memory
     // the split of the work, see qk_rows_kernel
     int lane_bits, token_bits, blocks_q;
     unsigned long long turns[kMaxPairs];  // frequency, 2^-64 turns per position
@@ -190,6 +191,23 @@ __device__ __forceinline__ void row_sum(float2 (&t)[N][K][P], int bits, float (&
     }
 }
 
+// a becomes the rounded a + x and x what the rounding left out, exactly.  (Where the
+// sum is not finite, x is left at some finite value: a minimum drops the NaN.)
+__device__ __forceinline__ void two_sum(float &a, float &x) {
+    const float s = __fadd_rn(a, x), b = __fsub_rn(s, a);
+    x = fminf(__fadd_rn(__fsub_rn(a, __fsub_rn(s, b)), __fsub_rn(x, b)), 1e30f);
+    a = s;
+}
+
+// The same in three operations, exactly where |x| <= |a|, else within u |x|.
+__device__ __forceinline__ void quick_two_sum(float &a, float &x) {
+    const float s = __fadd_rn(a, x);
+    x = fminf(__fsub_rn(x, __fsub_rn(s, a)), 1e30f);
+    a = s;
+}
+
+// Rows that a thread adds to its sums of g n before they go to its larger sums.
+constexpr int kFold = 16;
 // Rows in flight per thread.
 template <bool kBack>
 constexpr int ring_depth() { return kBack ? 3 : 4; }
@@ -208,6 +226,9 @@ int ring_bytes(int d, int lane_bits) {
            (whole_rows<T, V>() ? (kThreads >> lane_bits) * row_units(d)
                                : K * vectors<V>() * kThreads * V * (int)sizeof(T));
 }
+// Bytes of the threads' larger sums, behind the ring.
+template <int V, int K>
+constexpr int sums_bytes() { return kThreads * K * ((V + 1) / 2) * 2 * (int)sizeof(float2); }
 
 // A row is shared by 2^lane_bits lanes of a warp.  A lane takes K parts of V
 // pairs, each as two vectors of V values, such that both values of a pair are in
@@ -226,7 +247,13 @@ int ring_bytes(int d, int lane_bits) {
 // travel through a ring in shared memory, filled by cp.async some rows ahead;
 // every thread reads only what it copied itself, so the ring needs no barrier
 // (with whole_rows, what its row's lanes copied: a warp barrier).
-// Backward, the sums of g n stay in registers until the block's end.
+//
+// Backward, the sums of g n are in registers for kFold rows, then added to sums in
+// shared memory.  What that addition rounds off stays behind in the registers, so
+// the number of rows does not add to the error: dw is off by at most 19 u sum |g n|
+// (u = 2^-24: 8.5 for chains of 16 rows, 5 for the lanes, one each for a chain's
+// residue, a thread's sum, a block's, the last and the products).  One chain over
+// all rows of a thread was off by several times as much and grew with them.
 template <typename T, int V, int K, bool kInter, bool kBack>
 __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_constant__ Params p) {
     constexpr int P = (V + 1) / 2;  // packed pairs per part
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     constexpr bool kWhole = whole_rows<T, V>();
     extern __shared__ __align__(16) char smem[];
     __shared__ unsigned long long turns[kMaxPairs];
-    __shared__ float weight[LA_MAX_D];
+    __shared__ __align__(32) float weight[LA_MAX_D];
     Pack<T, V> *ring = reinterpret_cast<Pack<T, V> *>(smem) + threadIdx.x;
 
     const int bits = p.lane_bits, lane = threadIdx.x & ((1 << bits) - 1);
@@ -388,17 +415,48 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         sort(e, m0, m1);
     };
 
+    // Backward with the longest vectors the weights are read again for each row: in
+    // registers they made the kernel spill (4 x (8 + 8) x 16384 x 128: 149 us, 135 us
+    // read again; shorter vectors have the registers).
+    constexpr bool kReread = kBack && V == 8;
     float2 w0[K][P], w1[K][P], dw0[K][P], dw1[K][P];
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
+    auto weigh = [&](int j) {
         float e[4 * P];
 #pragma unroll
-        for (int i = 0; i < 4 * P; ++i)
-            e[i] = has[j][i / V] ? weight[at[j][i / V] + i % V] : 0.f;
+        for (int m = 0; m < kVecs; ++m) {
+            Pack<float, V> w = {};
+            if (has[j][m]) {
+                if constexpr (kReread) {
+                    w = *reinterpret_cast<const Pack<float, V> *>(weight + at[j][m]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) w.v[i] = weight[at[j][m] + i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[m * V + i] = w.v[i];
+        }
         sort(e, w0[j], w1[j]);
+    };
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (!kReread) weigh(j);
 #pragma unroll
         for (int i = 0; i < P; ++i) dw0[j][i] = dw1[j][i] = make_float2(0.f, 0.f);
     }
+    const bool summing = kBack && p.partial;
+    float2 *const sums = reinterpret_cast<float2 *>(smem + p.sums_at) + threadIdx.x;
+    if (summing)
+        for (int i = 0; i < 2 * K * P; ++i) sums[i * kThreads] = make_float2(0.f, 0.f);
+    auto fold = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2 * K * P; ++i) {
+            float2 &x = (i % 2 ? dw1 : dw0)[i / 2 / P][i / 2 % P], a = sums[i * kThreads];
+            quick_two_sum(a.x, x.x);
+            quick_two_sum(a.y, x.y);
+            sums[i * kThreads] = a;
+        }
+    };
 
     int depth = 0;
     long long tile = it0 / rows;
@@ -432,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         for (; row < rows && left > 0; ++row, --left, y += y_step) {
             if (kWhole) __syncwarp();  // the place that is filled next has been read
             fetch_row();
+            if (summing && left % kFold == 0) fold();
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
             if (kWhole) __syncwarp();
             const bool ok = t_ok && head_in + row * head_step < H;
@@ -446,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                     for (int i = 0; i < P; ++i) v0[j][i] = v1[j][i] = make_float2(0.f, 0.f);
                 }
                 if (kBack) open(depth, kSrc - 1, j, ok, at_g, g0[j], g1[j]);
+                if (kReread) weigh(j);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     t[0][j][i] = __ffma2_rn(v0[j][i], v0[j][i], __fmul2_rn(v1[j][i], v1[j][i]));
@@ -512,9 +572,13 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
-    if (!kBack || !p.partial) return;
+    if (!summing) return;
     // the block's sums: over the groups of each warp, then over the warps, in
     // the ring's memory
+    fold();
+#pragma unroll
+    for (int i = 0; i < 2 * K * P; ++i)
+        (i % 2 ? dw1 : dw0)[i / 2 / P][i / 2 % P] = sums[i * kThreads];
     __syncthreads();
     float(*sum)[LA_MAX_D] = reinterpret_cast<float(*)[LA_MAX_D]>(smem);
     const int warp = threadIdx.x >> 5;
@@ -536,32 +600,48 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         }
     __syncthreads();
     for (int i = threadIdx.x; i < p.d; i += kThreads) {
-        float t = 0.f;
-        for (int q = 0; q < kThreads / 32; ++q) t += sum[q][i];
-        p.partial[(long long)blockIdx.x * p.d + i] = t;
+        float t = 0.f, low = 0.f;
+        for (int q = 0; q < kThreads / 32; ++q) {
+            float x = sum[q][i];
+            two_sum(t, x);
+            low += x;
+        }
+        p.partial[(long long)blockIdx.x * p.d + i] = t + low;
     }
 }
 
-// dw[i] = the sum of the blocks' partial sums: 1024 / 256 interleaved sums per
-// feature, joined in order.  A few microseconds of latency, most of them hidden by
-// starting it while the rows' kernel ends.
+// dw[i] = the sum of the blocks' partial sums, in order for each of 32 interleaved
+// parts, then over the parts, every addition with what it rounds off kept in a second
+// sum.  A block takes 32 features of one side.  A few microseconds of latency, most
+// of them hidden by starting it while the rows' kernel ends.
 __global__ void __launch_bounds__(1024)
 qk_weight_kernel(const float *partial, int blocks_q, int blocks, int d, float *dwq, float *dwk) {
     // started while the rows' kernel runs: its sums are there after this
     tc::grid_dep_wait();
-    float *dw = blockIdx.x ? dwk : dwq;
+    const int chunks = (d + 31) / 32, side = (int)blockIdx.x >= chunks;
+    float *dw = side ? dwk : dwq;
     if (!dw) return;
-    __shared__ float sum[4][LA_MAX_D];
-    const int i = threadIdx.x & 255, part = threadIdx.x >> 8;
-    const int b0 = blockIdx.x ? blocks_q : 0, b1 = blockIdx.x ? blocks : blocks_q;
-    float t = 0.f;
-    if (i < d) {
+    __shared__ float2 sum[32][32];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int i = ((int)blockIdx.x - side * chunks) * 32 + lane;
+    const int b0 = side ? blocks_q : 0, b1 = side ? blocks : blocks_q;
+    float t = 0.f, low = 0.f;
+    if (i < d)
 #pragma unroll 8
-        for (int b = b0 + part; b < b1; b += 4) t += partial[(long long)b * d + i];
-        sum[part][i] = t;
-    }
+        for (int b = b0 + part; b < b1; b += 32) {
+            float x = partial[(long long)b * d + i];
+            two_sum(t, x);
+            low += x;
+        }
+    sum[part][lane] = make_float2(t, low);
     __syncthreads();
-    if (part == 0 && i < d) dw[i] = ((sum[0][i] + sum[1][i]) + sum[2][i]) + sum[3][i];
+    if (part > 0 || i >= d) return;
+    for (int q = 1; q < 32; ++q) {
+        float2 x = sum[q][lane];
+        two_sum(t, x.x);
+        low += x.x + x.y;
+    }
+    dw[i] = t + low;
 }
 
 la_status qk_fail(la_status s, const char *who, const char *msg) {
@@ -629,12 +709,16 @@ int vector_of(const Params &p, int most, int elem) {
 }
 
 template <typename T, int V, int K, bool kBack>
-cudaError_t launch_rows(const Params &p, unsigned blocks, cudaStream_t stream) {
+cudaError_t launch_rows(Params &p, unsigned blocks, cudaStream_t stream) {
     auto kern = p.interleaved ? qk_rows_kernel<T, V, K, true, kBack>
                               : qk_rows_kernel<T, V, K, false, kBack>;
     // the sums of the weight gradient, 8 rows of LA_MAX_D, share the ring
-    const int smem = std::max(ring_bytes<T, V, K, kBack>(p.d, p.lane_bits),
-                              kThreads / 32 * LA_MAX_D * 4);
+    int smem = std::max(ring_bytes<T, V, K, kBack>(p.d, p.lane_bits),
+                        kThreads / 32 * LA_MAX_D * 4);
+    if (p.partial) {
+        p.sums_at = smem;
+        smem += sums_bytes<V, K>();
+    }
     if (smem > 40 * 1024) {  // 48 KB with the static arrays need no attribute
         const cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -702,7 +786,7 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
         e = launch_rows<T, 1, 2, kBack>(p, (unsigned)blocks, stream);
     if (e == cudaSuccess) note_launches(1);
     if (e == cudaSuccess && want_dw) {
-        e = tchost::launch_dependent(qk_weight_kernel, 2, 1024, 0, stream,
+        e = tchost::launch_dependent(qk_weight_kernel, 2 * ((p.d + 31) / 32), 1024, 0, stream,
                                      static_cast<const float *>(p.partial), p.blocks_q,
                                      (int)blocks, p.d, p.side[0].dw, p.side[1].dw);
         if (e == cudaSuccess) note_launches(1);
