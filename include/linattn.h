@@ -348,7 +348,8 @@ typedef struct {
  * weight per feature and rotated by its position,
  *   n = x / sqrt(mean(x^2) + eps),  u = w (.) n,
  *   (y1, y2) = (u1 cos t - u2 sin t, u2 cos t + u1 sin t)  for each pair,
- * features from rotary_dim on pass without rotation.  The pages normalise k
+ * features from rotary_dim on pass without rotation (u as it is, whatever is in
+ * the others).  The pages normalise k
  * for the delta rule and rotate q and k in retention models without giving
  * the formulas; these are the usual ones.  With the identity feature map and
  * no normaliser, <y_q, y_k> then depends on positions by their difference.

@@ -38,7 +38,7 @@ constexpr int kMaxPairs = LA_MAX_D / 2;
 
 // One side (queries or keys) of a call.  Strides are in elements.
 struct Side {
-    const void *x;   // forward input (backward: may be NULL without norm)
+    const void *x;   // forward input
     const void *dy;  // backward: gradient of the output
     void *y;         // forward: output; backward: gradient of the input
     const void *w;   // weight or NULL
@@ -342,8 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         int b, n;
         f_ok = locate(f_tile, b, n);
         const int h = head_in + f_row * head_step;
-        if (!kBack || p.norm)
-            fx = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n + h * sd.sx.h;
+        fx = static_cast<const T *>(sd.x) + b * sd.sx.b + n * sd.sx.n + h * sd.sx.h;
         if (kBack) fg = static_cast<const T *>(sd.dy) + b * sd.sdy.b + n * sd.sdy.n + h * sd.sdy.h;
     };
     f_enter();
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
         if (f_left > 0) {
             const bool ok = f_ok && head_in + f_row * head_step < H;
             if (kWhole && ok) {
-                if (!kBack || p.norm) fetch_units(row_slot(f_depth, 0), fx);
+                fetch_units(row_slot(f_depth, 0), fx);
                 if (kBack) fetch_units(row_slot(f_depth, kSrc - 1), fg);
             }
 #pragma unroll
@@ -359,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
 #pragma unroll
                 for (int m = 0; m < kVecs; ++m) {
                     if (!ok || !has[j][m]) continue;
-                    if (!kBack || p.norm)
-                        fetch<T, V>(slot(f_depth, 0, j, m), fx + at[j][m], policy);
+                    fetch<T, V>(slot(f_depth, 0, j, m), fx + at[j][m], policy);
                     if (kBack) fetch<T, V>(slot(f_depth, kSrc - 1, j, m), fg + at[j][m], policy);
                 }
             f_depth = f_depth + 1 == kDepth ? 0 : f_depth + 1;
@@ -422,19 +420,18 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     float2 w0[K][P], w1[K][P], dw0[K][P], dw1[K][P];
     auto weigh = [&](int j) {
         float e[4 * P];
+        if constexpr (kReread) {
 #pragma unroll
-        for (int m = 0; m < kVecs; ++m) {
-            Pack<float, V> w = {};
-            if (has[j][m]) {
-                if constexpr (kReread) {
-                    w = *reinterpret_cast<const Pack<float, V> *>(weight + at[j][m]);
-                } else {
+            for (int m = 0; m < kVecs; ++m) {
+                Pack<float, V> w = {};
+                if (has[j][m]) w = *reinterpret_cast<const Pack<float, V> *>(weight + at[j][m]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) w.v[i] = weight[at[j][m] + i];
-                }
+                for (int i = 0; i < V; ++i) e[m * V + i] = w.v[i];
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) e[m * V + i] = w.v[i];
+            for (int i = 0; i < 4 * P; ++i)
+                e[i] = has[j][i / V] ? weight[at[j][i / V] + i % V] : 0.f;
         }
         sort(e, w0[j], w1[j]);
     };
@@ -457,6 +454,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             sums[i * kThreads] = a;
         }
     };
+
+    // Features beyond the rotated ones pass as they are: a cosine of 1 and a sine of 0
+    // would make a NaN of one beside a value that is not finite.  With halves as pairs
+    // a lane's part of long vectors is rotated or passes as a whole; elsewhere each
+    // pair is looked at, where any pass (backward 4 x (8 + 8) x 16384 x 128, half of
+    // the features rotated: a branch around each chunk of neighbouring pairs took 147
+    // us, but 153 with all rotated; selects 149 and 140).
+    constexpr bool kWholeParts = V >= 4 && !kInter;
+    const bool some_pass = p.half < pairs;
+    auto passes = [&](int j, int e) { return pair(j, e) >= p.half; };
 
     int depth = 0;
     long long tile = it0 / rows;
@@ -498,31 +505,41 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             float2 v0[K][P], v1[K][P], g0[K][P], g1[K][P], t[kSrc][K][P];
 #pragma unroll
             for (int j = 0; j < K; ++j) {
-                if (!kBack || p.norm) {
-                    open(depth, 0, j, ok, at_x, v0[j], v1[j]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < P; ++i) v0[j][i] = v1[j][i] = make_float2(0.f, 0.f);
-                }
+                open(depth, 0, j, ok, at_x, v0[j], v1[j]);
                 if (kBack) open(depth, kSrc - 1, j, ok, at_g, g0[j], g1[j]);
                 if (kReread) weigh(j);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
+                for (int i = 0; i < P; ++i)
                     t[0][j][i] = __ffma2_rn(v0[j][i], v0[j][i], __fmul2_rn(v1[j][i], v1[j][i]));
-                    if (!kBack) continue;
-                    // turned back, then times the weight for dx
-                    const float2 a = g0[j][i], c = g1[j][i];
-                    const float2 as = __fmul2_rn(a, sn[j][i]);
-                    g0[j][i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(c, sn[j][i]));
-                    g1[j][i] = make_float2(fmaf(c.x, cs[j][i].x, -as.x),
-                                           fmaf(c.y, cs[j][i].y, -as.y));
+                if (!kBack) continue;
+                // turned back; what the sine multiplies is 0 where a pair passes
+                float2 ga[P], gc[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) ga[i] = g0[j][i], gc[i] = g1[j][i];
+                if (!kWholeParts && some_pass)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        if (passes(j, 2 * i)) ga[i].x = gc[i].x = 0.f;
+                        if (passes(j, 2 * i + 1)) ga[i].y = gc[i].y = 0.f;
+                    }
+                if (!kWholeParts || !passes(j, 0))
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 a = g0[j][i], c = g1[j][i], as = __fmul2_rn(ga[i], sn[j][i]);
+                        g0[j][i] = __ffma2_rn(a, cs[j][i], __fmul2_rn(gc[i], sn[j][i]));
+                        g1[j][i] = make_float2(fmaf(c.x, cs[j][i].x, -as.x),
+                                               fmaf(c.y, cs[j][i].y, -as.y));
+                    }
+                // then times the weight for dx
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
                     t[kSrc - 1][j][i] =
                         __ffma2_rn(v0[j][i], __fmul2_rn(w0[j][i], g0[j][i]),
                                    __fmul2_rn(v1[j][i], __fmul2_rn(w1[j][i], g1[j][i])));
                 }
             }
             float r = 1.f, m = 0.f;
-            if (p.norm) {
+            if (kBack || p.norm) {
                 float sum[kSrc];
                 row_sum<kChunks>(t, bits, sum);
                 r = rsqrtf(fmaf(sum[0], p.inv_d, p.eps));
@@ -538,10 +555,18 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                     const float2 n0 = __fmul2_rn(v0[j][i], r2), n1 = __fmul2_rn(v1[j][i], r2);
                     if (!kBack) {
                         const float2 a = __fmul2_rn(n0, w0[j][i]), c = __fmul2_rn(n1, w1[j][i]);
-                        const float2 cn = __fmul2_rn(c, sn[j][i]);
-                        o0[i] = make_float2(fmaf(a.x, cs[j][i].x, -cn.x),
-                                            fmaf(a.y, cs[j][i].y, -cn.y));
-                        o1[i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
+                        o0[i] = a;
+                        o1[i] = c;
+                        if (!kWholeParts || !passes(j, 0)) {
+                            const float2 cn = __fmul2_rn(c, sn[j][i]);
+                            o0[i] = make_float2(fmaf(a.x, cs[j][i].x, -cn.x),
+                                                fmaf(a.y, cs[j][i].y, -cn.y));
+                            o1[i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
+                        }
+                        if (!kWholeParts && some_pass) {
+                            if (passes(j, 2 * i)) o0[i].x = a.x, o1[i].x = c.x;
+                            if (passes(j, 2 * i + 1)) o0[i].y = a.y, o1[i].y = c.y;
+                        }
                     } else {
                         if (ok) {  // other rows hold what an earlier one left
                             dw0[j][i] = __ffma2_rn(g0[j][i], n0, dw0[j][i]);
@@ -686,13 +711,13 @@ bool same(const la_strides &a, const la_strides &b) {
     return a.b == b.b && a.h == b.h && a.n == b.n;
 }
 
-// Values per access: the most (a power of two, up to `most`) that divide the row
-// (its two halves and its rotated part, where pairs are not neighbours) and at
-// which every row of every tensor is aligned.
+// Values per access: the most (a power of two, up to `most`) that divide the row and
+// its rotated part (where pairs are not neighbours, their halves) and at which every
+// row of every tensor is aligned.
 int vector_of(const Params &p, int most, int elem) {
     // a power of two divides all of these if it divides their union
     unsigned long long all =
-        (unsigned)(p.interleaved ? p.d : p.half | (p.d % 2 ? 1 : p.d / 2)) | (unsigned)most;
+        (unsigned)(p.interleaved ? p.d | 2 * p.half : p.half | (p.d % 2 ? 1 : p.d / 2)) | (unsigned)most;
     auto add = [&](const void *q, const la_strides &s, int H) {
         all |= (uintptr_t)q / (uintptr_t)elem;
         if (p.B > 1) all |= (unsigned long long)s.b;
@@ -970,6 +995,16 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
             if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
         }
     if (B == 0 || N == 0 || Hq + Hk == 0) return LA_OK;
+    if (!norm) {  // turned back and nothing else: the forward of the other sense
+        for (Side &sd : p.side) {
+            sd.x = sd.dy;
+            sd.sx = sd.sdy;
+            sd.dy = nullptr;
+        }
+        for (int i = 0; i < p.half; ++i) p.turns[i] = 0 - p.turns[i];
+        return dtype == LA_F32 ? launch<float, false>(who, p, nullptr, 0, s)
+                               : launch<__nv_bfloat16, false>(who, p, nullptr, 0, s);
+    }
     return dtype == LA_F32 ? launch<float, true>(who, p, workspace, workspace_bytes, s)
                            : launch<__nv_bfloat16, true>(who, p, workspace, workspace_bytes, s);
 }

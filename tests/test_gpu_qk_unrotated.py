@@ -1,0 +1,89 @@
+"""Features that the rotation leaves alone (those from its dimension on, or all of
+them) pass as they are: a value that is not finite stays with its own feature, and
+with its pair where it is rotated.  Forward and backward; no tolerance, since
+without norm such a feature's result is its input."""
+import pytest
+
+import linear_attention_feature_gb300 as la
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+BAD = [float("inf"), -float("inf"), float("nan")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    la.build.build()
+    la.load_library()
+
+
+def partner(i, R, interleaved):
+    if i >= R:
+        return i
+    if interleaved:
+        return i ^ 1
+    return (i + R // 2) % R
+
+
+def rows(d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(1, 3, d + 2, d, generator=g).to(DT[dtype])
+    for n in range(d):  # token n has a bad value at feature n
+        x[0, 0, n, n] = BAD[n % 3]
+    x[0, 1, :, 0] = -0.0
+    return x.cuda()
+
+
+def same(a, b):
+    """Equal values, zeros with their sign, NaN for NaN."""
+    both = torch.isnan(a) & torch.isnan(b)
+    return both | ((a == b) & (torch.signbit(a) == torch.signbit(b)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d, R", [(64, 0), (64, 16), (128, 32), (80, 40), (66, 2), (37, 10),
+                                  (256, 254), (128, 128)])
+def test_without_norm(d, R, interleaved, dtype):
+    x = rows(d, dtype, d + R)
+    freq = la.rope_frequencies(R)
+    y, _ = la.qk_norm_rope(x, x[:, :1], None, None, freq, offset=3, norm=False,
+                           interleaved=interleaved)
+    dx = la.backward_qk_norm_rope(x, x[:, :1], x, x[:, :1], None, None, freq, offset=3,
+                                  norm=False, interleaved=interleaved)[0]
+    for got in (y, dx):
+        assert same(got[..., R:], x[..., R:]).all()
+        bad = ~torch.isfinite(got.cpu())
+        want = torch.zeros_like(bad)
+        for n in range(d):
+            want[0, 0, n, n] = want[0, 0, n, partner(n, R, interleaved)] = True
+        assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d, R", [(64, 0), (128, 32), (37, 10)])
+def test_infinite_value_under_the_norm(d, R, dtype):
+    # an infinite square makes the norm's factor 0: the row's other values become 0,
+    # the value itself (and its pair, where rotated) has none
+    x = torch.ones(1, 1, d, d, dtype=DT[dtype], device="cuda")
+    x[0, 0].fill_diagonal_(float("inf"))
+    y, _ = la.qk_norm_rope(x, x, None, None, la.rope_frequencies(R), offset=3)
+    want = torch.zeros(d, d, dtype=torch.bool)
+    for n in range(d):
+        want[n, n] = want[n, partner(n, R, False)] = True
+    assert torch.equal(torch.isnan(y[0, 0].cpu()), want)
+    assert torch.all(y[0, 0].cpu()[~want] == 0)
+
+
+def test_weight_gradient_of_an_unrotated_feature():
+    x = torch.randn(1, 2, 40, 64, generator=torch.Generator().manual_seed(5)).cuda()
+    dy = torch.ones_like(x)
+    dy[0, 1, 7, 50] = float("inf")
+    w = torch.ones(64, device="cuda")
+    dw = la.backward_qk_norm_rope(dy, dy, x, x, w, w, la.rope_frequencies(16))[2]
+    want = torch.zeros(64, dtype=torch.bool)
+    want[50] = True
+    assert torch.equal(~torch.isfinite(dw.cpu()), want)
