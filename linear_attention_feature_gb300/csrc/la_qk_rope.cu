@@ -139,18 +139,36 @@ __device__ __forceinline__ long long position_of(const Params &p, int b, int n) 
     return v + p.offset;
 }
 
-// cos and sin of pos * turns (2^-64 turns).  The top 32 bits as a signed
-// number are the angle in 2^-31 half turns, in [-1, 1).  For bf16 rows the
-// special function unit is exact enough: within [-pi, pi] it is off by 2^-21 at
-// most, 2^-12 of half a step of the result.
+// cos and sin of pos * turns (2^-64 turns).  The top 32 bits are the angle in 2^-32
+// turns.  For bf16 results the special function unit is exact enough: within [-pi,
+// pi] it is off by 2^-21 at most, 2^-12 of half a step of the result.  Elsewhere (fp32
+// rows, and backward, whose weight gradients are fp32) the angle is taken apart into
+// quarter turns and a rest z of at most half a quarter, exactly, so that rounding the
+// rest to fp32 costs 0.4 u (u = 2^-24; of the whole angle 1.6 u).  sin(pi/4 z) = z (s0
+// + w S(w)) and cos(pi/4 z) = 1 + w C(w), w = z^2; S and C interpolate the exact
+// quotients at the Chebyshev nodes of [0, 1], off by 0.2 u at most, s0 is pi/4 as two
+// fp32 numbers.  Each result is within 1.4 u.
 template <bool kFine>
 __device__ __forceinline__ void turn_of(long long pos, unsigned long long turns, float *c,
                                         float *s) {
-    const float t = (float)(int)(((unsigned long long)pos * turns) >> 32);
-    if (kFine)
-        sincospif(t * 0x1p-31f, s, c);
-    else
-        __sincosf(t * 1.46291807926715968e-9f, s, c);  // pi 2^-31
+    const unsigned t = (unsigned)(((unsigned long long)pos * turns) >> 32);
+    if (!kFine) {
+        __sincosf((float)(int)t * 1.46291807926715968e-9f, s, c);  // pi 2^-31
+        return;
+    }
+    const unsigned quarter = (t + 0x20000000u) >> 30;
+    const float z = (float)(int)(t - (quarter << 30)) * 0x1p-29f, w = z * z;
+    float a = fmaf(w, -3.61091152e-5f, 2.49021966e-3f);
+    a = fmaf(w, a, -8.07455033e-2f);
+    a = fmaf(w, a, -2.18556941e-8f);
+    a = fmaf(z, 0.785398185f, z * a);
+    float b = fmaf(w, 3.54195276e-6f, -3.25961388e-4f);
+    b = fmaf(w, b, 1.58543382e-2f);
+    b = fmaf(w, b, -0.308425128f);
+    b = fmaf(w, b, 1.f);
+    const float sine = quarter & 1 ? b : a, cosine = quarter & 1 ? a : b;
+    *s = quarter & 2 ? -sine : sine;
+    *c = (quarter + 1) & 2 ? -cosine : cosine;
 }
 
 // Sum over a row of K S chunks of 2 P / S terms in each of 2^bits lanes, N sums
@@ -482,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
             for (int e = 0; e < 2 * P; ++e) {
                 const int i = pair(j, e);
                 float c = 1.f, s = 0.f;
-                if (i < p.half) turn_of<sizeof(T) == 4>(pos, turns[i], &c, &s);
+                if (i < p.half) turn_of<sizeof(T) == 4 || kBack>(pos, turns[i], &c, &s);
                 (e % 2 ? cs[j][e / 2].y : cs[j][e / 2].x) = c;
                 (e % 2 ? sn[j][e / 2].y : sn[j][e / 2].x) = s;
             }
