@@ -6,6 +6,11 @@ computation runs in the library's CUDA kernels; PyTorch is used for device
 memory and streams.  There is no CPU fallback: if the library has not been
 built (``python -m linear_attention_feature_gb300.build``) or a tensor is not
 on a CUDA device, the call raises.
+
+A call goes to the current stream, or to the one given as ``stream``.  What it
+allocates is then that stream's memory; inputs have to stay until the stream
+has passed the call (``record_stream``), and another stream has to wait for it
+before it reads the results.
 """
 from __future__ import annotations
 
@@ -184,6 +189,31 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _memory_of(stream, device):
+    """Context in which new tensors come out of `stream`'s memory.  What another
+    stream's allocator gives may still be read there by work that was enqueued
+    before it was freed."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(stream, shape, dtype, device):
+    """A new tensor in the memory of `stream` (None: of the current stream)."""
+    if stream is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    with _memory_of(stream, device):
+        return _torch().empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(stream, t):
+    if stream is None:
+        return _torch().empty_like(t)
+    with _memory_of(stream, t.device):
+        return _torch().empty_like(t)
+
+
 def _enter(index, stream):
     """Makes CUDA device `index` the current one.  Returns the stream that the
     call goes to and the device to go back to (-1: it was current already)."""
@@ -222,7 +252,7 @@ def forward(q, k, v, causal: bool = True, decay=None, out=None, *,
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share one dtype")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(q, k, v, out)
     B, H, N, d = q.shape
     lib = load_library()
@@ -249,7 +279,7 @@ def forward_variant(q, k, v, causal: bool = True, decay=None, out=None, *,
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share one dtype")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(q, k, v, out)
     B, H, N, d = q.shape
     lib = load_library()
@@ -277,7 +307,7 @@ def forward_gated(q, k, v, gates, out=None, *, feature_map: str = "elu1",
     if tuple(gates.shape) != (B, H, N) or gates.dtype != torch.float32:
         raise ValueError("gates must be float32 [B, H, N]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(q, k, v, out, gates)
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -303,7 +333,7 @@ def decode_step_gated(S, z, q, k, v, gates, out=None, *, feature_map="elu1",
     if tuple(gates.shape) != (B, H) or gates.dtype != torch.float32:
         raise ValueError("gates must be float32 [B, H]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(S, z, q, k, v, out, gates)
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -331,7 +361,7 @@ def decode_step_delta(S, q, k, v, beta, alpha=None, out=None, *, stream=None):
         if t is not None and (tuple(t.shape) != (B, H) or t.dtype != torch.float32):
             raise ValueError(f"{name} must be float32 [B, H]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(S, q, k, v, out, beta, *([alpha] if alpha is not None else []))
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -363,7 +393,7 @@ def forward_delta(q, k, v, beta, alpha=None, out=None, S=None, *, stream=None):
     if S is not None and (tuple(S.shape) != (B, H, d, d) or S.dtype != torch.float32):
         raise ValueError("S must be float32 [B, H, d, d]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(q, k, v, out, beta, *[t for t in (alpha, S) if t is not None])
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -391,11 +421,11 @@ def forward_causal_state(q, k, v, decay=None, out=None, S=None, z=None, *,
         raise TypeError("q, k, v must share one dtype")
     B, H, N, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     if S is None:
-        S = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
+        S = _empty(stream, (B, H, d, d), torch.float32, q.device)
     if z is None:
-        z = torch.empty(B, H, d, dtype=torch.float32, device=q.device)
+        z = _empty(stream, (B, H, d), torch.float32, q.device)
     if tuple(S.shape) != (B, H, d, d) or tuple(z.shape) != (B, H, d):
         raise ValueError("S must be [B, H, d, d] and z [B, H, d]")
     if S.dtype != torch.float32 or z.dtype != torch.float32:
@@ -431,7 +461,7 @@ def decode_step(S, z, q, k, v, out=None, *, decay=None, feature_map="elu1",
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share one dtype")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(stream, q)
     _check_cuda(S, z, q, k, v, out)
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -543,10 +573,6 @@ def _check_qk(qs, ks):
     return qs[0], qs[1], ks[1], qs[2] if n == 4 else 1, qs[-1]
 
 
-def _contiguous_like(t):
-    return _torch().empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions=None, *,
                  offset: int = 0, norm: bool = True, eps: float = 1e-6,
                  interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -565,13 +591,13 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, frequencies=None, positions
     Returns (q_out, k_out)."""
     qs, ks, device = q.shape, k.shape, q.device
     B, Hq, Hk, N, d = _check_qk(qs, ks)
-    empty, dtype = _torch().empty, q.dtype
+    dtype = q.dtype
     if q_out is None:
-        q_out = empty(qs, dtype=dtype, device=device)
+        q_out = _empty(stream, qs, dtype, device)
     elif q_out.shape != qs:
         raise ValueError("q_out must have q's shape")
     if k_out is None:
-        k_out = empty(ks, dtype=dtype, device=device)
+        k_out = _empty(stream, ks, dtype, device)
     elif k_out.shape != ks:
         raise ValueError("k_out must have k's shape")
     index, strides = _check_rows(q, q, k, q_out, k_out)
@@ -609,9 +635,9 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
     if dq_out.shape != qs or dk_out.shape != ks:
         raise ValueError("dq_out and dk_out must have the shapes of q and k")
     if dq is None:
-        dq = torch.empty_like(q)
+        dq = _empty_like(stream, q)
     if dk is None:
-        dk = torch.empty_like(k)
+        dk = _empty_like(stream, k)
     if dq.shape != qs or dk.shape != ks:
         raise ValueError("dq and dk must have the shapes of q and k")
     index, strides = _check_rows(q, dq_out, dk_out, q, k, dq, dk)
@@ -623,9 +649,9 @@ def backward_qk_norm_rope(dq_out, dk_out, q, k, q_weight=None, k_weight=None,
         dwq = dwk = ws = None
         ws_bytes = 0
         if wq is not None:
-            dwq = torch.empty(d, dtype=torch.float32, device=device)
+            dwq = _empty(stream, d, torch.float32, device)
         if wk is not None:
-            dwk = torch.empty(d, dtype=torch.float32, device=device)
+            dwk = _empty(stream, d, torch.float32, device)
         # on the current stream torch's allocator gives the workspace; the
         # library allocates on another one
         if stream is None and (wq is not None or wk is not None):
@@ -727,11 +753,11 @@ def forward_recurrence(x, gates, h0=None, out=None, *, h_last=None, gate: str = 
     if x.dim() != 3:
         raise ValueError("x must be [B, N, C]")
     if out is None:
-        out = _contiguous_like(x)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     B, N, C = x.shape
     device = x.device
     if h_last is None:
-        h_last = torch.empty(B, C, dtype=torch.float32, device=device)
+        h_last = _empty(stream, (B, C), torch.float32, device)
     form = _gate(gate)
     index = _check_seq(x, gates, out)
     _check_state(B, C, index, h0, h_last)
@@ -766,11 +792,11 @@ def backward_recurrence(dout, gates, out, x=None, h0=None, dh_last=None, *, dx=N
     B, N, C = dout.shape
     device = dout.device
     if dx is None:
-        dx = _contiguous_like(dout)
+        dx = _empty(stream, dout.shape, dout.dtype, device)
     if dgates is None:
-        dgates = _contiguous_like(gates)
+        dgates = _empty(stream, gates.shape, gates.dtype, device)
     if dh0 is None:
-        dh0 = torch.empty(B, C, dtype=torch.float32, device=device)
+        dh0 = _empty(stream, (B, C), torch.float32, device)
     form = _gate(gate)
     if not complement:
         x = None
@@ -804,7 +830,7 @@ def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "va
     if x.dim() != 2:
         raise ValueError("x must be [B, C]")
     if out is None:
-        out = _contiguous_like(x)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if h_out is None:
         h_out = h
     B, C = x.shape
@@ -876,7 +902,7 @@ def forward_host(q, k, v, causal: bool = True, decay=None, out=None, *,
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     need = host_workspace_bytes(q.shape, q.dtype)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, max(need, 1), torch.uint8, dev)
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a CUDA tensor of at least {need} bytes")
     B, H, N, d = q.shape
