@@ -444,7 +444,8 @@ typedef struct {
  *   out        [B][N][C] device, dtype `dtype`, written; may be x itself with
  *              the same strides, otherwise no aliasing.
  *   h_last     [B][C] fp32 device, written with the state after the last
- *              token (unrounded), or NULL; may be h0 itself.
+ *              token (unrounded), or NULL; may be h0 itself, otherwise no
+ *              aliasing.
  *   strides    3 strides, of x, gates, out, or NULL: contiguous.
  *   B, N, C >= 0 (B*C == 0 is a no-op; N == 0 copies h0 to h_last); B * C / 32,
  *              C / 32 rounded up, below 2^24, else LA_ERR_UNSUPPORTED.
@@ -486,7 +487,8 @@ size_t la_recurrence_workspace_bytes(int B, int C, la_dtype dtype);
  *              with the same strides.
  *   dgates     [B][N][C] device, dtype `gate_dtype`, written: the gradient of
  *              the gate tensor as given (value, logarithm or logit).
- *   dh0        [B][C] fp32 device, written, or NULL; may be dh_last itself.
+ *   dh0        [B][C] fp32 device, written, or NULL; may be dh_last itself,
+ *              otherwise no aliasing.
  *   strides    6 strides, of dout, gates, out, x, dx, dgates, or NULL:
  *              contiguous.
  * Other arguments as la_forward_recurrence.  N == 0 copies dh_last to dh0.
@@ -503,7 +505,7 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
  * la_decode_step_recurrence -- one token of la_forward_recurrence.
  *   h          [B][C] fp32 device, the state, read.
  *   h_out      [B][C] fp32 device, the new state, written; h itself for an
- *              update in place.
+ *              update in place (or an fp32 x or gates laid out as h is).
  *   x, gates   [B][C] device; out [B][C] device, dtype `dtype`, written (h_out
  *              rounded); may be x itself with the same stride.
  *   strides    3 strides between batch entries, of x, gates, out, or NULL: C.

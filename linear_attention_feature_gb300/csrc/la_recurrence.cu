@@ -151,6 +151,8 @@ la_status la_forward_recurrence(const void *x, const void *gates, const float *h
     if (!rows_disjoint(so.b, so.n, B, N, C))
         return rec_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
     if (out == gates) return rec_fail(LA_ERR_INVALID_ARG, who, "out aliases gates");
+    if (h_last && (h_last == x || h_last == gates || (h_last == out && N > 1)))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "h_last aliases a tensor of the sequence");
     if (out == x && (sx.b != so.b || sx.n != so.n))
         return rec_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
     Params p{};
@@ -200,6 +202,9 @@ la_status la_backward_recurrence(const void *dout, const void *gates, const void
     if (dx == gates || dx == out || (complement && dx == x) || dx == dgates || dgates == dout ||
         dgates == gates || dgates == out || (complement && dgates == x))
         return rec_fail(LA_ERR_INVALID_ARG, who, "an output aliases another tensor");
+    if (dh0 && (dh0 == dout || dh0 == gates || dh0 == out || (complement && dh0 == x) ||
+                dh0 == dx || dh0 == dgates))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "dh0 aliases a tensor of the sequence");
     if (dx == dout && (ss[0].b != ss[4].b || ss[0].n != ss[4].n))
         return rec_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
     Params p{};
@@ -249,6 +254,10 @@ la_status la_decode_step_recurrence(const float *h, float *h_out, const void *x,
         return rec_fail(LA_ERR_INVALID_ARG, who, "out aliases another tensor");
     if (out == x && sx != so)
         return rec_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
+    // over x or the gates each value of the state lies where its own input does, or not
+    if ((h_out == x && !(dtype == LA_F32 && (sx == C || B == 1))) ||
+        (h_out == gates && !(gate_dtype == LA_F32 && (sg == C || B == 1))))
+        return rec_fail(LA_ERR_INVALID_ARG, who, "h_out aliases an input");
     const StepParams p{h, h_out, x, gates, out, sx, sg, so, B, C, complement};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == LA_F32) return step<float, float>(who, p, gate, s);
