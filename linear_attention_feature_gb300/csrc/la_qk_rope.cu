@@ -565,42 +565,50 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
                 if (kBack) m = __fmul_rn(__fmul_rn(sum[kSrc - 1], p.inv_d), r);
             }
             const float2 r2 = make_float2(r, r), m2 = make_float2(-m, -m);
+            float2 o0[K][P], o1[K][P];
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
-                float2 o0[P], o1[P];
+            for (int j = 0; j < K; ++j)
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     const float2 n0 = __fmul2_rn(v0[j][i], r2), n1 = __fmul2_rn(v1[j][i], r2);
                     if (!kBack) {
                         const float2 a = __fmul2_rn(n0, w0[j][i]), c = __fmul2_rn(n1, w1[j][i]);
-                        o0[i] = a;
-                        o1[i] = c;
+                        o0[j][i] = a;
+                        o1[j][i] = c;
                         if (!kWholeParts || !passes(j, 0)) {
                             const float2 cn = __fmul2_rn(c, sn[j][i]);
-                            o0[i] = make_float2(fmaf(a.x, cs[j][i].x, -cn.x),
+                            o0[j][i] = make_float2(fmaf(a.x, cs[j][i].x, -cn.x),
                                                 fmaf(a.y, cs[j][i].y, -cn.y));
-                            o1[i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
-                        }
-                        if (!kWholeParts && some_pass) {
-                            if (passes(j, 2 * i)) o0[i].x = a.x, o1[i].x = c.x;
-                            if (passes(j, 2 * i + 1)) o0[i].y = a.y, o1[i].y = c.y;
+                            o1[j][i] = __ffma2_rn(c, cs[j][i], __fmul2_rn(a, sn[j][i]));
                         }
                     } else {
                         if (ok) {  // other rows hold what an earlier one left
                             dw0[j][i] = __ffma2_rn(g0[j][i], n0, dw0[j][i]);
                             dw1[j][i] = __ffma2_rn(g1[j][i], n1, dw1[j][i]);
                         }
-                        o0[i] = __fmul2_rn(
+                        o0[j][i] = __fmul2_rn(
                             r2, __ffma2_rn(n0, m2, __fmul2_rn(w0[j][i], g0[j][i])));
-                        o1[i] = __fmul2_rn(
+                        o1[j][i] = __fmul2_rn(
                             r2, __ffma2_rn(n1, m2, __fmul2_rn(w1[j][i], g1[j][i])));
                     }
                 }
+            if (!kBack && !kWholeParts && some_pass)
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const float2 a = __fmul2_rn(__fmul2_rn(v0[j][i], r2), w0[j][i]);
+                        const float2 c = __fmul2_rn(__fmul2_rn(v1[j][i], r2), w1[j][i]);
+                        if (passes(j, 2 * i)) o0[j][i].x = a.x, o1[j][i].x = c.x;
+                        if (passes(j, 2 * i + 1)) o0[j][i].y = a.y, o1[j][i].y = c.y;
+                    }
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
                 float e[4 * P];
 #pragma unroll
                 for (int i = 0; i < 2 * P; ++i) {
-                    e[place(0, i)] = i % 2 ? o0[i / 2].y : o0[i / 2].x;
-                    e[place(1, i)] = i % 2 ? o1[i / 2].y : o1[i / 2].x;
+                    e[place(0, i)] = i % 2 ? o0[j][i / 2].y : o0[j][i / 2].x;
+                    e[place(1, i)] = i % 2 ? o1[j][i / 2].y : o1[j][i / 2].x;
                 }
 #pragma unroll
                 for (int m = 0; m < kVecs; ++m)
