@@ -11,6 +11,9 @@ A call goes to the current stream, or to the one given as ``stream``.  What it
 allocates is then that stream's memory; inputs have to stay until the stream
 has passed the call (``record_stream``), and another stream has to wait for it
 before it reads the results.
+
+Automatic differentiation does not record the calls: results are detached.  The
+backward_* functions are the gradients of their forwards.
 """
 from __future__ import annotations
 

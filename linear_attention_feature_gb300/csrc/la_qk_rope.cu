@@ -15,9 +15,9 @@
 // What bounds it (GB300, 6.78 TB/s measured copy): memory, once the angles are
 // shared by a token's heads, rows arrive asynchronously and the arithmetic goes
 // through the packed fp32 instructions.  Forward 2 x (16 + 16) x 32768 x 128 bf16,
-// token-major to head-major: 181 us, 5.9 TB/s (12 instructions a value); 4 x (16 +
-// 16) x 4096 x 64: 21 us, 6.4 TB/s.  Backward 4 x (8 + 8) x 16384 x 128: 148 us, 5.4
-// TB/s (26 instructions a value, the weights' sums among them).  First kernel,
+// token-major to head-major: 182 us, 5.9 TB/s (13 instructions a value); 4 x (16 +
+// 16) x 4096 x 64: 21 us, 6.4 TB/s.  Backward 4 x (8 + 8) x 16384 x 128: 135 us, 6.0
+// TB/s (25 instructions a value, the weights' sums among them).  First kernel,
 // one warp per row: 1332, 233 and 1021 us.
 #include <cuda_bf16.h>
 
@@ -476,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rows_kernel(const __grid_const
     // Features beyond the rotated ones pass as they are: a cosine of 1 and a sine of 0
     // would make a NaN of one beside a value that is not finite.  With halves as pairs
     // a lane's part of long vectors is rotated or passes as a whole; elsewhere each
-    // pair is looked at, where any pass (backward 4 x (8 + 8) x 16384 x 128, half of
-    // the features rotated: a branch around each chunk of neighbouring pairs took 147
-    // us, but 153 with all rotated; selects 149 and 140).
+    // pair is looked at, where any pass (backward 4 x (8 + 8) x 16384 x 128: 152 us with
+    // half of the features rotated, as neighbours, 146 with all; a branch around each
+    // chunk of neighbouring pairs was 1 % faster with half of them, 9 % slower with all).
     constexpr bool kWholeParts = V >= 4 && !kInter;
     const bool some_pass = p.half < pairs;
     auto passes = [&](int j, int e) { return pair(j, e) >= p.half; };

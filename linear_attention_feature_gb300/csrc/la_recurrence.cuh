@@ -29,23 +29,27 @@
 // Rows that TMA tiles cannot take (strides or bases that are not multiples of 16
 // bytes) come by cp.async: the 16-byte units of memory that hold the strip's
 // part of the row, wherever it begins in the first of them (2 x 32768 x 2047
-// bf16: 298 us, against 152 us for the 2048 of whole units; when a bulk copy per
+// bf16: 273 us, against 145 us for the 2048 of whole units; when a bulk copy per
 // row was tried it took 401 us against 338 us).
 //
 // Where even clusters would leave most SMs idle (few channels, long sequences),
 // a sequence is cut into pieces and walked twice: once for the maps of the
-// pieces, once from the states that they give (1 x 262144 x 64 bf16: 179 us in
-// one piece, 44 us in pieces).
+// pieces, once from the states that they give (1 x 262144 x 64 bf16, when it was
+// added: 179 us in one piece, 44 us in pieces; now 43).
 //
-// What bounds it (GB300, 6.78 TB/s measured copy): the instructions.  A warp
-// spends about 700 on 16 rows of 64 bf16 channels (logistic gates with
-// complement; 440 with gates as values), of which 0.56 a cycle issue on each
-// scheduler with the 16 warps that 128 registers allow, so an SM takes 1.1 us for
-// a round of 128 x 64 values.  2 x 32768 x 2048 bf16 takes 151 us (5.3 TB/s) on the
-// 128 SMs that 64 strips in clusters of two occupy, and 68 us per half with gates
-// as values (6.0 TB/s); backward 4 x 16384 x 1024 140 us (5.7 TB/s).  L = 16
-// forward and 8 backward: half of that doubles the share of the joining, twice
-// needs more than 128 registers (32 rows with half the warps: the same time).
+// What bounds it (GB300, 6.78 TB/s measured copy): the latency of its instructions
+// with the 16 warps that 128 registers allow, on the SMs that the strips occupy.  A
+// warp spends about 660 on 16 rows of 64 bf16 channels (logistic gates with
+// complement; 420 with gates as values).  A scheduler issues 0.56 a cycle (0.45),
+// and no pipe is full: integer and logic 49 % (38), fp32 36 % (25), special
+// functions 26 % (0), loads and stores 24 % (30); a warp's first stall is the fixed
+// latency of what it just issued.  2 x 32768 x 2048 bf16 takes 145 us (5.5 TB/s) on
+// the 128 SMs that 64 strips in clusters of two occupy, with gates as values 132 us
+// (6.1 TB/s), with fp32 logarithms 170 us (6.3 TB/s); backward 4 x 16384 x 1024 143
+// us (5.6 TB/s), 2 x 16384 x 1024 fp32 133 us (6.0 TB/s).  A warp waits as one, by a
+// vote: when each lane tested for itself the forward took 152 us.  L = 16 forward
+// and 8 backward: half of that doubles the share of the joining, twice needs more
+// than 128 registers (32 rows with half the warps: the same time).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -116,13 +120,6 @@ __device__ __forceinline__ Vec<V> all_v(float x) {
     for (int e = 0; e < V; ++e) r.v[e] = x;
     return r;
 }
-template <int V>
-__device__ __forceinline__ Vec<V> neg_v(Vec<V> a) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) a.v[e] = -a.v[e];
-    return a;
-}
-
 // V adjacent values in memory.
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Mem {
@@ -788,8 +785,8 @@ struct Cut {
     size_t smem;
 };
 
-// The cheapest cut, counted in rounds of a block alone (1.1 us forward, 0.95 us
-// backward for bf16 logits with complement): a cluster takes ceil(items /
+// The cheapest cut, counted in rounds of a block alone (about 1.1 us forward, 0.95
+// us backward for bf16 logits with complement): a cluster takes ceil(items /
 // clusters) strips, one after the other, each of ceil(steps / (S tile)) rounds and
 // about two more for the start.  Measured, a round of S blocks takes 1.2 to 1.3
 // times one of a block at S = 16 (more maps to join).  clusters_of: how many run
@@ -823,7 +820,7 @@ Cut best_cut(const Params &p, int tile, int bytes, int V, int least_stages, F &&
     // In pieces, of blocks alone: a round of the maps takes 0.82 of one of the walk
     // forward (of its three tensors two are read), 0.55 backward; two launches, the
     // maps between them and the joining took 10 rounds more.  1 x N x C bf16, in
-    // clusters / in pieces: forward 65536 x 256 49 / 38 us, x 384 50 / 57; backward
+    // clusters / in pieces, when the weights were fitted: forward 65536 x 256 49 / 38 us, x 384 50 / 57; backward
     // 65536 x 512 109 / 95, x 768 129 / 139; 16384 x 512 32 / 30, 8192 x 512 19 / 20.
     if (!best.S || items > kFewStrips) return best;
     size_t smem;
