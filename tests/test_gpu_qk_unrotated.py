@@ -87,3 +87,36 @@ def test_weight_gradient_of_an_unrotated_feature():
     want = torch.zeros(64, dtype=torch.bool)
     want[50] = True
     assert torch.equal(~torch.isfinite(dw.cpu()), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d, R", [(64, 64), (128, 32), (37, 10), (66, 66)])
+def test_backward_without_norm_is_the_rotation_back(d, R, interleaved, dtype):
+    # into a strided gradient and in place: the same bits; and the forward with the
+    # opposite frequencies, whose turns differ by 2^-64 of a turn per position, gives
+    # them but for a step of 2^-32 turns (2^-29 radians) of the angle and the roundings
+    g = torch.Generator().manual_seed(d)
+    dy = torch.randn(2, 5, 33, d, generator=g).to(DT[dtype]).cuda()
+    freq = la.rope_frequencies(R)
+    back = [-f for f in freq]
+    kw = dict(norm=False, interleaved=interleaved)
+    pos = torch.randint(0, 1 << 20, (2, 33), generator=g).cuda()
+    want, wk = la.qk_norm_rope(dy, dy[:, :2], None, None, back, pos, **kw)
+    dq, dk, dwq, dwk = la.backward_qk_norm_rope(dy, dy[:, :2], dy, dy[:, :2], None, None, freq,
+                                                pos, **kw)
+    assert dwq is None and dwk is None
+    # two values of up to |dy| by sines and cosines that a step of the angle, its
+    # rounding (8 u at most for bf16) and the functions move, then the result's rounding
+    tol = 2 * (2.0 ** -29 + (16 if dtype == "bf16" else 4) * 2.0 ** -24) * 2
+    tol += 2 * torch.finfo(DT[dtype]).eps
+    for a, b in ((dq, want), (dk, wk)):
+        assert float((a.double() - b.double()).abs().max()) <= tol * float(dy.double().abs().max())
+    room = torch.full((2, 33, 5 * d + 3), 9.0, dtype=DT[dtype], device="cuda")
+    out = room[..., 1:1 + 5 * d].view(2, 33, 5, d).transpose(1, 2)
+    la.backward_qk_norm_rope(dy, dy[:, :0], dy, dy[:, :0], None, None, freq, pos, dq=out, **kw)
+    assert torch.equal(out, dq)
+    assert torch.all(room[..., 0] == 9.0) and torch.all(room[..., 1 + 5 * d:] == 9.0)
+    inp = dy.clone()
+    got = la.backward_qk_norm_rope(inp, dk, inp, dk, None, None, freq, pos, dq=inp, **kw)
+    assert got[0].data_ptr() == inp.data_ptr() and torch.equal(inp, dq)
