@@ -517,6 +517,167 @@ la_status la_decode_step_recurrence(const float *h, float *h_out, const void *x,
                                     la_dtype dtype, la_dtype gate_dtype,
                                     la_stream_t stream);
 
+/*
+ * A paged cache of keys and values: pages of page_size tokens each, in any
+ * order, and a table that names the pages of each sequence.  Position p of
+ * sequence b is in page table[b][p / page_size], slot p % page_size.
+ */
+typedef struct {
+    void *k, *v;         /* DEVICE [pages][Hk][page_size][d], dtype `dtype`  */
+    la_strides k_strides, v_strides; /* b: from page to page, h: from head to
+                            head, n: from slot to slot; d is contiguous      */
+    const int *table;    /* DEVICE [B][max_pages] page numbers; an entry that
+                            is not in 0..pages-1 is no page                  */
+    long long table_stride; /* elements from sequence to sequence           */
+    const int *lengths;  /* DEVICE [B]: tokens of each sequence before this
+                            call's; negative: a place of the batch that is
+                            not in use                                       */
+    int pages, page_size, max_pages; /* max_pages * page_size <= 2^30       */
+} la_cache;
+
+/*
+ * la_append_cache -- T new tokens per sequence into a paged cache, keys and
+ * queries rotated by their position on the way (the rotation of
+ * la_qk_norm_rope).  Token t of sequence b is at position p = lengths[b] + t;
+ * its key and value go to the cache's place for p, in all heads.
+ *   q          [B][Hq][T][d] device, dtype `dtype`, read only; q_out likewise,
+ *              written (every row): the queries as la_decode_step_paged takes
+ *              them.  q_out may be q itself with the same strides.
+ *   k, v       [B][Hk][T][d] device, dtype `dtype`, read only.
+ *   cache      k and v are written at the new tokens' places, nowhere else.
+ *   counts     DEVICE [B]: how many of the T tokens sequence b really has
+ *              (a padded batch of prompts), or NULL: all T.
+ *   strides    4 strides, of q, k, v, q_out, or NULL: contiguous.
+ *   rope       the rotation, by p + offset (rope->positions must be NULL), or
+ *              NULL for none.  Values, and features from rotary_dim on, pass
+ *              bit for bit.
+ *   B, Hq, Hk, T >= 0 (Hq == 0 leaves the queries out), d in 1..LA_MAX_D.
+ * A token whose place has no page (past the table, a table entry that is no
+ * page) or whose sequence is not in use is not stored.  Two sequences that
+ * append to one page at one slot leave either's token there.  Angles are exact
+ * in the position.  One kernel, no workspace.
+ */
+la_status la_append_cache(const void *q, const void *k, const void *v, void *q_out,
+                          const la_cache *cache, const int *counts,
+                          const la_strides *strides, const la_rope *rope, int B, int Hq,
+                          int Hk, int T, int d, la_dtype dtype, la_stream_t stream);
+
+/*
+ * la_decode_step_paged -- softmax attention of a sequence's newest T tokens
+ * over its paged cache, the softmax layer of a stack that has a few of them
+ * between its linear ones:
+ *   o_t = sum_j exp(scale q_t . k_j) v_j / sum_j exp(scale q_t . k_j)
+ * over the keys j <= p_t = lengths[b] + t, with window > 0 only those with
+ * j > p_t - window.  The call's own keys are in the cache already
+ * (la_append_cache with the same lengths): a step appends, attends, and adds T
+ * to lengths once all layers are done.
+ *   q          [B][Hq][T][d] device, dtype `dtype`, read only.
+ *   out        [B][Hq][T][d] device, dtype `dtype`, written.
+ *   cache      read only.  A key whose place has no page is left out.  Pages
+ *              that lie wholly before all windows are not read and need no
+ *              table entry.
+ *   strides    2 strides, of q and out, or NULL: contiguous.
+ *   scale      finite; usually 1 / sqrt(d).
+ *   window     0: all keys.
+ *   B, Hq, Hk, T >= 0, T <= 2^20, Hq a multiple of Hk (query head h reads
+ *              head h / (Hq / Hk) of the cache), d in 1..LA_MAX_D.
+ *   workspace  device buffer, 16-byte aligned, of
+ *              la_decode_step_paged_workspace_bytes(...) bytes, not used by
+ *              anything else until `stream` has passed the call; or NULL:
+ *              allocated stream-ordered (LA_ERR_NO_MEMORY if that fails).
+ * A query without keys (a sequence not in use) gives zeros.  What lies in the
+ * cache outside the keys that a query looks at does not reach its output,
+ * whatever it is.  Scores, the softmax's maximum and sum and the outputs are
+ * fp32; with bf16 the weights are rounded to bf16 for their product with the
+ * values (the sum is of the rounded ones).  The work is cut into equal pieces
+ * along all sequences' lengths and joined in a fixed order: repeated calls are
+ * bit-identical.  Two kernels.
+ */
+la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
+                               const la_strides *strides, float scale, int window,
+                               int B, int Hq, int Hk, int T, int d, la_dtype dtype,
+                               void *workspace, size_t workspace_bytes,
+                               la_stream_t stream);
+
+/* Workspace bytes that la_decode_step_paged needs at most on the current
+ * device, whatever B and the lengths are (0 for invalid arguments). */
+size_t la_decode_step_paged_workspace_bytes(int Hq, int Hk, int T, int d,
+                                            la_dtype dtype);
+
+/*
+ * la_forward_cross -- linear attention of N queries per head to M keys and
+ * values of another sequence, an encoder's (the non-causal form of la_forward
+ * with two lengths, shared heads and padding):
+ *   S = sum_j phi(k_j) v_j^T,  z = sum_j phi(k_j)   over j < lengths[b],
+ *   y_i = phi(q_i)^T S / phi(q_i)^T z.
+ *   q          [B][Hq][N][d] device, dtype `dtype`, read only.
+ *   k, v       [B][Hk][M][d] device, dtype `dtype`, read only; what lies behind
+ *              a sequence's length is not used, whatever it is.
+ *   out        [B][Hq][N][d] device, dtype `dtype`, written.
+ *   S, z       [B][Hk][d][d] and [B][Hk][d] fp32 device, written: the states,
+ *              as la_decode_step has them (S[a][c], a the key feature).  They
+ *              are all that la_decode_step_cross and la_backward_cross need of
+ *              the encoder's side and of the forward.
+ *   lengths    DEVICE [B]: tokens of each sequence's keys (taken as 0 below 0
+ *              and M above M), or NULL: M.
+ *   strides    4 strides, of q, k, v, out, or NULL: contiguous.
+ *   B, Hq, Hk, N, M >= 0, Hq a multiple of Hk (query head h reads the state of
+ *              head h / (Hq / Hk)), d in 1..LA_MAX_D.
+ *   variant    as la_forward_variant.
+ *   workspace  device buffer, 16-byte aligned, of la_cross_workspace_bytes(...,
+ *              0) bytes, not used by anything else until `stream` has passed
+ *              the call; or NULL: allocated stream-ordered (LA_ERR_NO_MEMORY if
+ *              that fails).
+ * A denominator of exactly 0 (a sequence without keys) gives zeros.  No output
+ * may alias another tensor.  The parts of a sum are joined in a fixed order:
+ * repeated calls are bit-identical.
+ */
+la_status la_forward_cross(const void *q, const void *k, const void *v, void *out,
+                           float *S, float *z, const int *lengths,
+                           const la_strides *strides, int B, int Hq, int Hk, int N,
+                           int M, int d, const la_variant *variant, la_dtype dtype,
+                           void *workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * la_backward_cross -- gradients of la_forward_cross's `out` (S and z as
+ * results of their own have none).  With f = phi(q_i), r = 1 / (f . z):
+ *   t = r f . (S dy_i),  dphi(q_i) = r (S dy_i - t z),
+ *   dS = sum r f dy_i^T,  dz = -sum r t f   over the queries of all heads that
+ *   share the state,  dphi(k_j) = dS v_j + dz,  dv_j = dS^T phi(k_j).
+ *   dout, dq   [B][Hq][N][d], dtype `dtype`: gradient of out, read; of q, written.
+ *   dk, dv     [B][Hk][M][d], dtype `dtype`, written; 0 behind a sequence's
+ *              length.
+ *   S, z       what the forward wrote, read only.
+ *   strides    7 strides, of dout, q, k, v, dq, dk, dv, or NULL: contiguous.
+ *   workspace  as la_forward_cross, of la_cross_workspace_bytes(..., 1) bytes.
+ * Other arguments as la_forward_cross (the same values as in the forward).
+ * Where the denominator is 0 the gradients are 0.
+ */
+la_status la_backward_cross(const void *dout, const void *q, const void *k, const void *v,
+                            const float *S, const float *z, const int *lengths, void *dq,
+                            void *dk, void *dv, const la_strides *strides, int B, int Hq,
+                            int Hk, int N, int M, int d, const la_variant *variant,
+                            la_dtype dtype, void *workspace, size_t workspace_bytes,
+                            la_stream_t stream);
+
+/* Workspace bytes that la_forward_cross (backward == 0) or la_backward_cross
+ * (1) needs at most on the current device (0: none, or invalid arguments). */
+size_t la_cross_workspace_bytes(int B, int Hq, int Hk, int N, int M, int d,
+                                la_dtype dtype, int backward);
+
+/*
+ * la_decode_step_cross -- a decoder's next token, or N of them, against the
+ * states that la_forward_cross wrote once for the encoder's tokens: y =
+ * phi(q)^T S / phi(q)^T z.  The states are read, not updated.
+ *   q, out     [B][Hq][N][d] device, dtype `dtype`.
+ *   strides    2 strides, of q and out, or NULL: contiguous.
+ * Other arguments as la_forward_cross.  One kernel, no workspace.
+ */
+la_status la_decode_step_cross(const float *S, const float *z, const void *q, void *out,
+                               const la_strides *strides, int B, int Hq, int Hk, int N,
+                               int d, const la_variant *variant, la_dtype dtype,
+                               la_stream_t stream);
+
 /* Size of the fixed device scratch used by la_forward_causal_noalloc. */
 #define LA_NOALLOC_SCRATCH_BYTES (16u << 20)
 

@@ -30,6 +30,8 @@ __all__ = ["forward", "forward_variant", "forward_gated", "decode_step_gated",
            "host_workspace_bytes", "decode_step",
            "rope_frequencies", "qk_norm_rope", "backward_qk_norm_rope",
            "forward_recurrence", "backward_recurrence", "decode_step_recurrence",
+           "append_cache", "decode_step_paged",
+           "forward_cross", "backward_cross", "decode_step_cross",
            "check_device_status",
            "kernel_launch_count", "LinAttnError",
            "load_library", "LA_F32", "LA_BF16", "STATUS", "EXPORTED"]
@@ -50,7 +52,10 @@ EXPORTED = ("la_forward", "la_forward_ex", "la_decode_step",
             "la_qk_norm_rope", "la_backward_qk_norm_rope",
             "la_backward_qk_norm_rope_workspace_bytes", "la_recurrence_workspace_bytes",
             "la_forward_recurrence",
-            "la_backward_recurrence", "la_decode_step_recurrence")
+            "la_backward_recurrence", "la_decode_step_recurrence",
+            "la_append_cache", "la_decode_step_paged",
+            "la_decode_step_paged_workspace_bytes", "la_forward_cross", "la_backward_cross",
+            "la_cross_workspace_bytes", "la_decode_step_cross")
 
 FEATURE_MAPS = {"elu1": 0, "identity": 1}
 GATES = {"value": 0, "log": 1, "logit": 2}
@@ -116,6 +121,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.la_recurrence_workspace_bytes.argtypes = [I, I, I]
     lib.la_recurrence_workspace_bytes.restype = ctypes.c_size_t
     lib.la_decode_step_recurrence.argtypes = [V, V, V, V, V, V, I, I, I, I, I, I, V]
+    lib.la_append_cache.argtypes = [V, V, V, V, V, V, V, V, I, I, I, I, I, I, V]
+    lib.la_decode_step_paged.argtypes = [V, V, V, V, ctypes.c_float, I, I, I, I, I, I, I,
+                                         V, ctypes.c_size_t, V]
+    lib.la_decode_step_paged_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.la_decode_step_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_forward_cross.argtypes = [V, V, V, V, V, V, V, V, I, I, I, I, I, I, VP, I,
+                                     V, ctypes.c_size_t, V]
+    lib.la_backward_cross.argtypes = [V, V, V, V, V, V, V, V, V, V, V, I, I, I, I, I, I, VP, I,
+                                      V, ctypes.c_size_t, V]
+    lib.la_cross_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
+    lib.la_cross_workspace_bytes.restype = ctypes.c_size_t
+    lib.la_decode_step_cross.argtypes = [V, V, V, V, V, I, I, I, I, I, VP, I, V]
     lib.la_debug_inject_timeout.argtypes = [ctypes.c_longlong, I]
     lib.la_debug_fail_next_allocs.argtypes = [I]
     lib.la_check_device_status.argtypes = [V]
@@ -133,7 +150,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
               "la_debug_inject_timeout", "la_debug_fail_next_allocs",
               "la_forward_delta", "la_check_device_status", "la_abi_version",
               "la_qk_norm_rope", "la_backward_qk_norm_rope", "la_forward_recurrence",
-              "la_backward_recurrence", "la_decode_step_recurrence"):
+              "la_backward_recurrence", "la_decode_step_recurrence", "la_append_cache",
+              "la_decode_step_paged", "la_forward_cross", "la_backward_cross",
+              "la_decode_step_cross"):
         getattr(lib, n).restype = I
     if path is None:
         _lib = lib
@@ -523,7 +542,7 @@ def _rope(frequencies, positions, offset, interleaved, shape, index):
                       nbytes, sb, sn, offset), f
 
 
-_STRIDES = {n: struct.Struct(f"@{n}q") for n in (3, 6, 12, 18)}
+_STRIDES = {n: struct.Struct(f"@{n}q") for n in (3, 6, 12, 18, 21)}
 
 
 def _check_rows(q, *ts):
@@ -847,6 +866,295 @@ def decode_step_recurrence(h, x, gates, out=None, *, h_out=None, gate: str = "va
             h.data_ptr(), h_out.data_ptr(), x.data_ptr(), gates.data_ptr(), out.data_ptr(),
             _STRIDES[3].pack(x.stride(0), gates.stride(0), out.stride(0)), B, C, form,
             bool(complement), code, gcode, to)
+    finally:
+        if back >= 0:
+            _leave(back)
+    if st:
+        _raise_if(st)
+    return out
+
+
+# ------------------------------------------------------------------ a paged
+# cache and the softmax attention over it
+
+# la_cache: k, v, k_strides, v_strides, table, table_stride, lengths, pages,
+# page_size, max_pages
+_CACHE = struct.Struct("@PP6qPqPiii")
+
+
+def _int32s(t, name, shape, index):
+    if t.dtype is not _torch().int32:
+        raise TypeError(f"{name} must be int32")
+    if t.dim() != len(shape) or t.shape[0] != shape[0]:
+        raise ValueError(f"{name} must have the shape {list(shape)}")
+    if t.get_device() != index:
+        raise ValueError("all tensors must be on one CUDA device")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index):
+    """The packed la_cache."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != Hk or shape[3] != d or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise TypeError("the cache must have the dtype of q, k and v")
+    for t in (k_cache, v_cache):
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one CUDA device")
+        if t.stride(-1) != 1 and d > 1:
+            raise ValueError("the last dimension must be contiguous")
+    _int32s(page_table, "page_table", (B, "pages"), index)
+    _int32s(lengths, "lengths", (B,), index)
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
+                       *v_cache.stride()[:3], page_table.data_ptr(), page_table.stride(0),
+                       lengths.data_ptr(), shape[0], shape[2], page_table.shape[1])
+
+
+def append_cache(k, v, k_cache, v_cache, page_table, lengths, frequencies=None, *, q=None,
+                 counts=None, offset: int = 0, interleaved: bool = False, q_out=None,
+                 stream=None):
+    """New tokens k, v [B, Hk, T, d] (or [B, Hk, d]: one each) into a paged cache
+    k_cache, v_cache [pages, Hk, page_size, d]: token t of sequence b is at
+    position p = lengths[b] + t and goes to page page_table[b, p // page_size],
+    slot p % page_size.  Keys, and queries q [B, Hq, T, d] if given, are rotated by
+    p + offset on the way (frequencies, interleaved: as qk_norm_rope).
+
+    page_table int32 [B, pages of the longest]; lengths int32 [B]: tokens before
+    this call's, negative for a place of the batch that is not in use; counts
+    int32 [B]: how many of the T tokens a sequence really has (None: all).  A token
+    without a page (a table entry outside the pages) is not stored.  Any strides
+    with a contiguous last dimension.  Returns the rotated queries (q_out; None
+    without q); the cache is written in place."""
+    ks, device, dtype = k.shape, k.device, k.dtype
+    n = len(ks)
+    if n not in (3, 4) or v.shape != ks:
+        raise ValueError("k and v must share one shape, [B, H, T, d] or [B, H, d]")
+    B, Hk, T, d = ks[0], ks[1], ks[2] if n == 4 else 1, ks[-1]
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        Hq = 0
+        index, strides = _check_rows(k, k, k, v, k)
+    else:
+        qs = q.shape
+        if len(qs) != n or qs[0] != B or qs[2:] != ks[2:]:
+            raise ValueError("q and k may differ in the number of heads only")
+        Hq = qs[1]
+        if q_out is None:
+            q_out = _empty(stream, qs, dtype, device)
+        elif q_out.shape != qs:
+            raise ValueError("q_out must have q's shape")
+        index, strides = _check_rows(k, q, k, v, q_out)
+    cache = _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index)
+    if counts is not None:
+        _int32s(counts, "counts", (B,), index)
+    rope, keep = _rope(frequencies, None, offset, interleaved, ks, index)
+    code, lib = _code(dtype), load_library()
+    to, back = _enter(index, stream)
+    try:
+        st = lib.la_append_cache(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), cache,
+                                 _ptr(counts), strides, rope, B, Hq, Hk, T, d, code, to)
+    finally:
+        if back >= 0:
+            _leave(back)
+    if st:
+        _raise_if(st)
+    return q_out
+
+
+# workspace bytes of decode_step_paged, by device and sizes
+_PAGED_WORKSPACE = {}
+
+
+def decode_step_paged(q, k_cache, v_cache, page_table, lengths, out=None, *, scale=None,
+                      window: int = 0, stream=None):
+    """Softmax attention of each sequence's newest tokens q [B, Hq, d], or T of them
+    [B, Hq, T, d], over its paged cache: token t at position p = lengths[b] + t looks
+    at the keys 0..p, with `window` at the last `window` of them.  The call's own keys
+    are in the cache already (append_cache with the same lengths); heads of queries
+    share those of the cache in order (Hq a multiple of Hk).  scale: 1 / sqrt(d) if
+    None.  A sequence with a negative length gives zeros.  Other arguments as
+    append_cache.  Returns out, like q."""
+    torch = _torch()
+    qs, device, dtype = q.shape, q.device, q.dtype
+    if len(qs) not in (3, 4):
+        raise ValueError("q must be [B, H, T, d], or [B, H, d] for one token")
+    B, Hq, T, d = qs[0], qs[1], qs[2] if len(qs) == 4 else 1, qs[-1]
+    if out is None:
+        out = _empty(stream, qs, dtype, device)
+    elif out.shape != qs:
+        raise ValueError("out must have q's shape")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
+    Hk = k_cache.shape[1]
+    index, strides = _check_rows(q, q, out)
+    cache = _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index)
+    if scale is None:
+        scale = d ** -0.5 if d else 1.0
+    code, lib = _code(dtype), load_library()
+    to, back = _enter(index, stream)
+    try:
+        ws, ws_bytes = None, 0
+        if stream is None:  # as for the other operators
+            key = (index, Hq, Hk, T, d, code)
+            ws_bytes = _PAGED_WORKSPACE.get(key)
+            if ws_bytes is None:
+                ws_bytes = lib.la_decode_step_paged_workspace_bytes(Hq, Hk, T, d, code)
+                _PAGED_WORKSPACE[key] = ws_bytes
+            if ws_bytes:
+                ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        st = lib.la_decode_step_paged(q.data_ptr(), out.data_ptr(), cache, strides, scale, window,
+                                      B, Hq, Hk, T, d, code, _ptr(ws), ws_bytes, to)
+    finally:
+        if back >= 0:
+            _leave(back)
+    if st:
+        _raise_if(st)
+    return out
+
+
+# ------------------------------------------------------------------ linear
+# cross attention
+
+def _check_cross(q, k, v):
+    """B, Hq, Hk, N, M, d."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or v.shape != ks:
+        raise ValueError("q must be [B, Hq, N, d], k and v [B, Hk, M, d]")
+    if qs[0] != ks[0] or qs[3] != ks[3]:
+        raise ValueError("q and k may differ in the number of heads and tokens only")
+    return qs[0], qs[1], ks[1], qs[2], ks[2], qs[3]
+
+
+def _check_cross_states(S, z, B, Hk, d, index):
+    float32 = _torch().float32
+    if S.shape != (B, Hk, d, d) or z.shape != (B, Hk, d):
+        raise ValueError("S must be [B, Hk, d, d] and z [B, Hk, d]")
+    if S.dtype is not float32 or z.dtype is not float32:
+        raise TypeError("S and z must be float32")
+    for t in (S, z):
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("a state must be contiguous")
+
+
+def _cross_workspace(lib, sizes, code, backward, device, stream):
+    """(workspace or None, bytes): on the current stream torch's allocator
+    gives it; the library allocates on another one."""
+    if stream is not None:
+        return None, 0
+    n = lib.la_cross_workspace_bytes(*sizes, code, backward)
+    if n == 0:
+        return None, 0
+    torch = _torch()
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def forward_cross(q, k, v, lengths=None, out=None, *, S=None, z=None,
+                  feature_map: str = "elu1", normalise: bool = True, stream=None):
+    """Linear attention of queries q [B, Hq, N, d] to another sequence's keys and
+    values k, v [B, Hk, M, d], an encoder's: y_i = phi(q_i)^T S / phi(q_i)^T z with S =
+    sum_j phi(k_j) v_j^T and z = sum_j phi(k_j).  Heads of queries share those of the
+    keys in order (Hq a multiple of Hk).  lengths int32 [B]: tokens of each sequence's
+    keys, the rest is padding (None: M).  Any strides with a contiguous last dimension.
+    Returns (out [B, Hq, N, d], S [B, Hk, d, d], z [B, Hk, d]), the states in float32
+    for decode_step_cross and backward_cross; a sequence without keys gives zeros."""
+    torch = _torch()
+    sizes = B, Hq, Hk, N, M, d = _check_cross(q, k, v)
+    device, dtype = q.device, q.dtype
+    if out is None:
+        out = _empty(stream, q.shape, dtype, device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if S is None:
+        S = _empty(stream, (B, Hk, d, d), torch.float32, device)
+    if z is None:
+        z = _empty(stream, (B, Hk, d), torch.float32, device)
+    index, strides = _check_rows(q, q, k, v, out)
+    _check_cross_states(S, z, B, Hk, d, index)
+    if lengths is not None:
+        _int32s(lengths, "lengths", (B,), index)
+    form = _variant(feature_map, normalise)
+    code, lib = _code(dtype), load_library()
+    to, back = _enter(index, stream)
+    try:
+        ws, ws_bytes = _cross_workspace(lib, sizes, code, 0, device, stream)
+        st = lib.la_forward_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                  S.data_ptr(), z.data_ptr(), _ptr(lengths), strides, *sizes,
+                                  form, code, _ptr(ws), ws_bytes, to)
+    finally:
+        if back >= 0:
+            _leave(back)
+    if st:
+        _raise_if(st)
+    return out, S, z
+
+
+def backward_cross(dout, q, k, v, S, z, lengths=None, *, dq=None, dk=None, dv=None,
+                   feature_map: str = "elu1", normalise: bool = True, stream=None):
+    """Gradients of forward_cross's out (same arguments as the forward call, S and z as
+    it returned them): returns (dq, dk, dv), laid out contiguously unless given, 0 at
+    the padding's keys and values."""
+    sizes = B, Hq, Hk, N, M, d = _check_cross(q, k, v)
+    device, dtype = q.device, q.dtype
+    if dout.shape != q.shape:
+        raise ValueError("dout must have q's shape")
+    if dq is None:
+        dq = _empty(stream, q.shape, dtype, device)
+    if dk is None:
+        dk = _empty(stream, k.shape, dtype, device)
+    if dv is None:
+        dv = _empty(stream, k.shape, dtype, device)
+    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("dq, dk and dv must have the shapes of q, k and v")
+    index, strides = _check_rows(q, dout, q, k, v, dq, dk, dv)
+    _check_cross_states(S, z, B, Hk, d, index)
+    if lengths is not None:
+        _int32s(lengths, "lengths", (B,), index)
+    form = _variant(feature_map, normalise)
+    code, lib = _code(dtype), load_library()
+    to, back = _enter(index, stream)
+    try:
+        ws, ws_bytes = _cross_workspace(lib, sizes, code, 1, device, stream)
+        st = lib.la_backward_cross(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   S.data_ptr(), z.data_ptr(), _ptr(lengths), dq.data_ptr(),
+                                   dk.data_ptr(), dv.data_ptr(), strides, *sizes, form, code,
+                                   _ptr(ws), ws_bytes, to)
+    finally:
+        if back >= 0:
+            _leave(back)
+    if st:
+        _raise_if(st)
+    return dq, dk, dv
+
+
+def decode_step_cross(S, z, q, out=None, *, feature_map: str = "elu1", normalise: bool = True,
+                      stream=None):
+    """A decoder's next token q [B, Hq, d], or N of them [B, Hq, N, d], against the states
+    S [B, Hk, d, d] and z [B, Hk, d] that forward_cross returned for the encoder's tokens
+    (read, not updated): returns out, like q."""
+    qs, dtype = q.shape, q.dtype
+    if len(qs) not in (3, 4):
+        raise ValueError("q must be [B, H, N, d], or [B, H, d] for one token")
+    if out is None:
+        out = _empty(stream, qs, dtype, q.device)
+    elif out.shape != qs:
+        raise ValueError("out must have q's shape")
+    if S.dim() != 4:
+        raise ValueError("S must be [B, Hk, d, d] and z [B, Hk, d]")
+    B, Hq, N, d = qs[0], qs[1], qs[2] if len(qs) == 4 else 1, qs[-1]
+    Hk = S.shape[1]
+    index, strides = _check_rows(q, q, out)
+    _check_cross_states(S, z, B, Hk, d, index)
+    form = _variant(feature_map, normalise)
+    code, lib = _code(dtype), load_library()
+    to, back = _enter(index, stream)
+    try:
+        st = lib.la_decode_step_cross(S.data_ptr(), z.data_ptr(), q.data_ptr(), out.data_ptr(),
+                                      strides, B, Hq, Hk, N, d, form, code, to)
     finally:
         if back >= 0:
             _leave(back)

@@ -1,0 +1,751 @@
+// Linear cross attention to an encoder's tokens, forward, backward and for single
+// tokens (la_forward_cross, la_backward_cross, la_decode_step_cross in
+// include/linattn.h).  With f = phi(q_i), g = phi(k_j):
+//   S = sum_j g_j v_j^T,  z = sum_j g_j,  y_i = S^T f_i / den_i,  den_i = f_i . z;
+// backwards, with r_i = 1 / den_i,
+//   G_i = S dy_i,  t_i = r_i f_i . G_i (which is y_i . dy_i),
+//   df_i = r_i (G_i - t_i z),
+//   dS = sum_i r_i f_i dy_i^T,  dz = -sum_i r_i t_i f_i,
+//   dg_j = dS v_j + dz,  dv_j = dS^T g_j,
+// and dq, dk are df, dg times phi'.  Neither the outputs nor anything else of a
+// token's is kept from the forward: S and z are all that the backward needs.
+//
+// This file has the argument checks and the fp32 CUDA-core kernels, which take any
+// head size, stride and type; bound by the fp32 units.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "la_cross.h"
+#include "la_internal.h"
+#include "la_layer.cuh"
+#include "la_tc.h"
+#include "la_tc_host.h"
+#include "la_tc_ptx.cuh"
+
+namespace la {
+namespace cross {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float phi_of(float x, int phi) {
+    return !phi ? x : x > 0.f ? x + 1.f : expf(x);
+}
+__device__ __forceinline__ float slope_of(float x, int phi) {
+    return !phi || x > 0.f ? 1.f : expf(x);
+}
+__device__ __forceinline__ int tokens_of(const int *lengths, int b, int M) {
+    return lengths ? min(max(lengths[b], 0), M) : M;
+}
+
+// ---------------------------------------------------------------- sums of outer products
+
+struct SumParams {
+    const void *x, *y;  // rows of features (phi is taken) and of values
+    la_strides sx, sy;
+    const float2 *rt;    // backward: r and t of each row of x, [B][Hk][group][L]
+    const int *lengths;  // forward, or NULL
+    int Hk, group, L, d, phi, segs;
+    long long per, heads;
+    float *S, *z;  // [segs][heads][d d], [segs][heads][d]
+};
+
+// S[a][c] += w_i f(x_i)[a] y_i[c] and z[a] += u_i w_i f(x_i)[a] over a part of the
+// tokens, w = r or 1 and u = -t or 1: 64 x 64 sums per block, 4 x 4 per thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
+    constexpr int kTok = 32, kTile = 64, kPitch = kTile + 4;
+    __shared__ __align__(16) float A[kTok][kPitch], Y[kTok][kPitch];
+    __shared__ float U[kTok];
+    const int tiles = (p.d + kTile - 1) / kTile;
+    const long long head = blockIdx.x / (tiles * tiles);
+    const int tile = (int)(blockIdx.x - head * (tiles * tiles)), seg = blockIdx.y;
+    const int a0 = tile / tiles * kTile, c0 = tile % tiles * kTile;
+    const int b = (int)(head / p.Hk), h = (int)(head % p.Hk);
+    const int len = tokens_of(p.lengths, b, p.L);
+    const long long all = (long long)p.group * p.L;
+    const long long i0 = seg * p.per, i1 = min(i0 + p.per, all);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float acc[4][4] = {}, zacc[4] = {};
+    for (long long i = i0; i < i1; i += kTok) {
+        if (p.group == 1 && i >= len) break;
+        __syncthreads();
+        for (int e = threadIdx.x; e < kTok * kTile; e += kThreads) {
+            const int row = e / kTile, f = e % kTile;
+            const long long tok = i + row;
+            const int g = (int)(tok / p.L), n = (int)(tok - (long long)g * p.L);
+            const bool ok = tok < i1 && n < len;
+            float2 rt = make_float2(1.f, -1.f);
+            if (ok && p.rt) rt = p.rt[(head * p.group + g) * p.L + n];
+            float x = 0.f, y = 0.f;
+            const long long hh = (long long)h * p.group + g;
+            if (ok && a0 + f < p.d)
+                x = rt.x * phi_of(to_f(static_cast<const T *>(p.x)[b * p.sx.b + hh * p.sx.h +
+                                                                  n * p.sx.n + a0 + f]),
+                                  p.phi);
+            if (ok && c0 + f < p.d)
+                y = to_f(static_cast<const T *>(p.y)[b * p.sy.b + hh * p.sy.h + n * p.sy.n +
+                                                    c0 + f]);
+            A[row][f] = x;
+            Y[row][f] = y;
+            if (f == 0) U[row] = -rt.y;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int row = 0; row < kTok; ++row) {
+            const float4 a = *reinterpret_cast<const float4 *>(&A[row][ty * 4]);
+            const float4 y = *reinterpret_cast<const float4 *>(&Y[row][tx * 4]);
+            const float av[4] = {a.x, a.y, a.z, a.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(av[m], yv[n], acc[m][n]);
+            if (tx == 0)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) zacc[m] = fmaf(av[m], U[row], zacc[m]);
+        }
+    }
+    float *S = p.S + (seg * p.heads + head) * p.d * p.d;
+    float *z = p.z + (seg * p.heads + head) * p.d;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int a = a0 + ty * 4 + m;
+        if (a >= p.d) continue;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (c0 + tx * 4 + n < p.d) S[a * p.d + c0 + tx * 4 + n] = acc[m][n];
+        if (tx == 0 && c0 == 0) z[a] = zacc[m];
+    }
+}
+
+// The parts of the states together, in order: out[i] = sum over segs of part[seg][i].
+__global__ void __launch_bounds__(kThreads)
+join_kernel(const float *S_part, const float *z_part, float *S, float *z, long long nS,
+            long long nz, int segs) {
+    for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < nS + nz;
+         i += (long long)gridDim.x * kThreads) {
+        const bool inS = i < nS;
+        const float *from = inS ? S_part + i : z_part + (i - nS);
+        const long long step = inS ? nS : nz;
+        float t[4] = {};
+        int s = 0;
+        for (; s + 4 <= segs; s += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] += from[(s + e) * step];
+        for (; s < segs; ++s) t[0] += from[s * step];
+        (inS ? S[i] : z[i - nS]) = (t[0] + t[1]) + (t[2] + t[3]);
+    }
+}
+
+// ---------------------------------------------------------------- rows times a state
+
+struct ReadParams {
+    const void *x;
+    void *y;
+    la_strides sx, sy;
+    const float *S, *z;
+    const int *lengths;  // rows behind are written as 0, or NULL
+    int Hk, group, L, d, phi, norm;
+};
+
+// y_i = S^T f(x_i), over f . z with norm: 64 rows x 64 columns per block.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
+    constexpr int kTile = 64, kStep = 32, kPitch = kTile + 4;
+    __shared__ __align__(16) float A[kStep][kPitch], Y[kStep][kPitch];
+    __shared__ float Z[kStep];
+    const int tiles = (p.d + kTile - 1) / kTile, row_tiles = (p.L + kTile - 1) / kTile;
+    const long long u = blockIdx.x / tiles;
+    const int c0 = (int)(blockIdx.x - u * tiles) * kTile;
+    const long long bh = u / row_tiles;  // of x's heads
+    const int n0 = (int)(u - bh * row_tiles) * kTile;
+    const int H = p.Hk * p.group, b = (int)(bh / H), h = (int)(bh % H);
+    const long long state = (long long)b * p.Hk + h / p.group;
+    const int len = tokens_of(p.lengths, b, p.L);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
+    float acc[4][4] = {}, den[4] = {};
+    for (int k0 = 0; k0 < p.d; k0 += kStep) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < kTile * kStep; e += kThreads) {
+            const int row = e / kStep, f = e % kStep;
+            float v = 0.f;
+            if (n0 + row < len && k0 + f < p.d)
+                v = phi_of(to_f(x[(n0 + row) * p.sx.n + k0 + f]), p.phi);
+            A[f][row] = v;
+            const int a = e / kTile, c = e % kTile;
+            Y[a][c] = k0 + a < p.d && c0 + c < p.d
+                          ? p.S[(state * p.d + k0 + a) * p.d + c0 + c] : 0.f;
+        }
+        if (threadIdx.x < kStep)
+            Z[threadIdx.x] = p.norm && k0 + threadIdx.x < p.d
+                                 ? p.z[state * p.d + k0 + threadIdx.x] : 0.f;
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < kStep; ++k) {
+            const float4 a = *reinterpret_cast<const float4 *>(&A[k][ty * 4]);
+            const float4 y = *reinterpret_cast<const float4 *>(&Y[k][tx * 4]);
+            const float av[4] = {a.x, a.y, a.z, a.w}, yv[4] = {y.x, y.y, y.z, y.w};
+            const float zk = Z[k];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(av[m], yv[n], acc[m][n]);
+                den[m] = fmaf(av[m], zk, den[m]);
+            }
+        }
+    }
+    T *y = static_cast<T *>(p.y) + b * p.sy.b + h * p.sy.h;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int n = n0 + ty * 4 + m;
+        if (n >= p.L) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = c0 + tx * 4 + e;
+            if (c >= p.d) continue;
+            // without keys there is nothing to average: 0
+            const float v = !p.norm ? acc[m][e] : den[m] == 0.f ? 0.f : acc[m][e] / den[m];
+            from_f(y[n * p.sy.n + c], n < len ? v : 0.f);
+        }
+    }
+}
+
+struct GradParams {
+    const void *y, *x;  // what is multiplied, and what phi is taken of
+    void *dx;
+    la_strides sy, sx, sdx;
+    const float *S, *z;
+    float2 *rt;          // q's side: written
+    const int *lengths;  // k's side: rows behind are written as 0, or NULL
+    int Hk, group, L, d, phi, norm, keys;
+};
+
+// G_i = S y_i, and from it the gradient of row i: on q's side
+// r (G - t z) phi'(x) with r and t left for the sums, on k's side (G + z) phi'(x)
+// (z is then dz).  A warp takes 4 rows whole, a lane every 32nd feature.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
+    constexpr int kRows = 32, kStep = 32, kCols = LA_MAX_D / 32;
+    __shared__ float Y[kRows][kStep], W[LA_MAX_D][kStep + 1];
+    const int row_tiles = (p.L + kRows - 1) / kRows;
+    const long long bh = blockIdx.x / row_tiles;
+    const int n0 = (int)(blockIdx.x - bh * row_tiles) * kRows;
+    const int H = p.Hk * p.group, b = (int)(bh / H), h = (int)(bh % H);
+    const long long state = (long long)b * p.Hk + h / p.group;
+    const int len = tokens_of(p.lengths, b, p.L);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cols = (p.d + 31) / 32;
+    const T *y = static_cast<const T *>(p.y) + b * p.sy.b + h * p.sy.h;
+    float acc[4][kCols] = {};
+    for (int k0 = 0; k0 < p.d; k0 += kStep) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < kRows * kStep; e += kThreads) {
+            const int row = e / kStep, c = e % kStep;
+            Y[row][c] = n0 + row < len && k0 + c < p.d
+                            ? to_f(y[(n0 + row) * p.sy.n + k0 + c]) : 0.f;
+        }
+        for (int e = threadIdx.x; e < cols * 32 * kStep; e += kThreads) {
+            const int a = e / kStep, c = e % kStep;
+            W[a][c] = a < p.d && k0 + c < p.d ? p.S[(state * p.d + a) * p.d + k0 + c] : 0.f;
+        }
+        __syncthreads();
+        for (int k = 0; k < kStep; ++k) {
+            float v[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v[m] = Y[warp * 4 + m][k];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+                if (j >= cols) break;
+                const float w = W[lane + 32 * j][k];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) acc[m][j] = fmaf(w, v[m], acc[m][j]);
+            }
+        }
+    }
+    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
+    T *dx = static_cast<T *>(p.dx) + b * p.sdx.b + h * p.sdx.h;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int n = n0 + warp * 4 + m;
+        if (n >= p.L) continue;
+        float xv[kCols], zv[kCols], dot = 0.f, den = 0.f;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const int a = lane + 32 * j;
+            const bool ok = a < p.d;
+            xv[j] = ok && n < len ? to_f(x[n * p.sx.n + a]) : 0.f;
+            zv[j] = ok && (p.norm || p.keys) ? p.z[state * p.d + a] : 0.f;
+            if (ok) {
+                const float f = phi_of(xv[j], p.phi);
+                dot = fmaf(f, acc[m][j], dot);
+                den = fmaf(f, zv[j], den);
+            }
+        }
+        float r = 1.f, t = p.keys ? -1.f : 0.f;
+        if (!p.keys) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                dot += __shfl_xor_sync(~0u, dot, o);
+                den += __shfl_xor_sync(~0u, den, o);
+            }
+            if (p.norm) {
+                r = den == 0.f ? 0.f : 1.f / den;
+                t = dot * r;
+            }
+            if (lane == 0) p.rt[bh * p.L + n] = make_float2(r, t);
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const int a = lane + 32 * j;
+            if (a >= p.d) continue;
+            const float g = r * fmaf(-t, zv[j], acc[m][j]) * slope_of(xv[j], p.phi);
+            from_f(dx[n * p.sdx.n + a], n < len ? g : 0.f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+
+struct StepParams {
+    const float *S, *z;
+    const void *q;
+    void *out;
+    la_strides sq, so;
+    int Hk, G, N, d, phi, norm;
+};
+
+// kR queries of one state: the state is read once, a row of it by as many threads as
+// it has vectors of V, the rows in turn by the rest.  Bound by that read.
+template <typename T, int kR, int V>
+__global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p) {
+    __shared__ float F[kR][LA_MAX_D], den[kR];
+    __shared__ __align__(16) float sum[kThreads * V];
+    const int rows = p.G * p.N, chunks = (rows + kR - 1) / kR;
+    const long long state = blockIdx.x / chunks;
+    const int r0 = (int)(blockIdx.x - state * chunks) * kR;
+    const int b = (int)(state / p.Hk), h = (int)(state % p.Hk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto offset = [&](const la_strides &s, int r) {
+        const int g = r / p.N, n = r - g * p.N;
+        return b * s.b + (long long)(h * p.G + g) * s.h + n * s.n;
+    };
+    const int vecs = (p.d + V - 1) / V;
+    int lanes = 1;
+    while (lanes < vecs) lanes <<= 1;
+    const int c = threadIdx.x & (lanes - 1), part = threadIdx.x / lanes;
+    const int parts = kThreads / lanes;
+
+    for (int i = threadIdx.x; i < kR * p.d; i += kThreads) {
+        const int r = i / p.d, a = i - r * p.d;
+        F[r][a] = r0 + r < rows
+                      ? phi_of(to_f(static_cast<const T *>(p.q)[offset(p.sq, r0 + r) + a]), p.phi)
+                      : 0.f;
+    }
+    __syncthreads();
+    if (p.norm)
+        for (int r = warp; r < kR; r += kThreads / 32) {
+            float t = 0.f;
+            for (int a = lane; a < p.d; a += 32) t = fmaf(F[r][a], p.z[state * p.d + a], t);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+            if (lane == 0) den[r] = t;
+        }
+    float acc[kR][V] = {};
+    if (c < vecs) {
+        const float *S = p.S + state * p.d * p.d + c * V;
+#pragma unroll 8
+        for (int a = part; a < p.d; a += parts) {
+            const Pack<float, V> w = *reinterpret_cast<const Pack<float, V> *>(S + a * p.d);
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[r][e] = fmaf(F[r][a], w.v[e], acc[r][e]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[threadIdx.x * V + e] = acc[r][e];
+        __syncthreads();
+        if (r0 + r < rows && threadIdx.x < p.d) {
+            float t = 0.f;
+            for (int q = 0; q < parts; ++q) t += sum[q * lanes * V + threadIdx.x];
+            if (p.norm) t = den[r] == 0.f ? 0.f : t / den[r];
+            from_f(static_cast<T *>(p.out)[offset(p.so, r0 + r) + threadIdx.x], t);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+cudaError_t counted(cudaError_t e) {
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Parts of the tokens of one head's sums: enough that all SMs are busy twice over, at
+// most 1024 tokens each (a longer chain of fp32 additions rounds more off).
+Cut cut_of(const Shape &sh, long long tokens, int sms) {
+    const int tiles = (sh.d + 63) / 64;
+    const long long blocks = std::max(1LL, sh.heads() * tiles * tiles);
+    long long segs = std::max((tokens + 1023) / 1024,
+                              std::min((2LL * sms + blocks - 1) / blocks, tokens / 64));
+    segs = std::max(1LL, std::min(segs, 65535LL));
+    Cut c;
+    c.per = ((tokens + segs - 1) / segs + 31) / 32 * 32;
+    c.segs = c.per ? (int)((tokens + c.per - 1) / c.per) : 1;
+    if (c.segs < 1) c.segs = 1;
+    return c;
+}
+
+size_t part_bytes(const Shape &sh, const Cut &c) {
+    return c.segs == 1 ? 0
+                       : up(sizeof(float) * (size_t)c.segs * sh.heads() * sh.state()) +
+                             up(sizeof(float) * (size_t)c.segs * sh.heads() * sh.d);
+}
+
+struct Plan {
+    Cut keys, queries;
+    size_t off_dS, off_dz, off_rt, off_part, total;
+};
+
+Plan plan_of(const Shape &sh, int sms, bool back) {
+    Plan p{};
+    p.keys = cut_of(sh, sh.M, sms);
+    p.queries = cut_of(sh, (long long)sh.G() * sh.N, sms);
+    if (!back) {
+        p.total = part_bytes(sh, p.keys);
+        return p;
+    }
+    p.off_dz = up(sizeof(float) * (size_t)sh.heads() * sh.state());
+    p.off_rt = p.off_dz + up(sizeof(float) * (size_t)sh.heads() * sh.d);
+    p.off_part = p.off_rt + up(sizeof(float2) * (size_t)sh.B * sh.Hq * sh.N);
+    p.total = p.off_part + part_bytes(sh, p.queries);
+    return p;
+}
+
+// The sums over x's and y's tokens into S and z, through `part` where they are cut.
+template <typename T>
+cudaError_t sums(const Shape &sh, Rows x, Rows y, int group, int L, const float2 *rt,
+                 const int *lengths, Cut cut, float *S, float *z, char *part, cudaStream_t s) {
+    SumParams p{};
+    p.x = x.x;
+    p.y = y.x;
+    p.sx = x.s;
+    p.sy = y.s;
+    p.rt = rt;
+    p.lengths = lengths;
+    p.Hk = sh.Hk;
+    p.group = group;
+    p.L = L;
+    p.d = sh.d;
+    p.phi = sh.phi;
+    p.segs = cut.segs;
+    p.per = cut.per;
+    p.heads = sh.heads();
+    float *pz = reinterpret_cast<float *>(
+        part + up(sizeof(float) * (size_t)cut.segs * sh.heads() * sh.state()));
+    p.S = cut.segs == 1 ? S : reinterpret_cast<float *>(part);
+    p.z = cut.segs == 1 ? z : pz;
+    const int tiles = (sh.d + 63) / 64;
+    const dim3 grid((unsigned)(sh.heads() * tiles * tiles), (unsigned)cut.segs);
+    sum_kernel<T><<<grid, kThreads, 0, s>>>(p);
+    cudaError_t e = counted(cudaSuccess);
+    if (e != cudaSuccess || cut.segs == 1) return e;
+    const long long nS = sh.heads() * sh.state(), nz = sh.heads() * sh.d;
+    const unsigned blocks = (unsigned)std::min((nS + nz + kThreads - 1) / kThreads, 4096LL);
+    join_kernel<<<blocks, kThreads, 0, s>>>(p.S, p.z, S, z, nS, nz, cut.segs);
+    return counted(cudaSuccess);
+}
+
+template <typename T>
+cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float *S,
+                 const float *z, int norm, const int *lengths, cudaStream_t s) {
+    ReadParams p{x.x, y.x, x.s, y.s, S, z, lengths, sh.Hk, group, L, sh.d, sh.phi, norm};
+    const long long blocks =
+        sh.heads() * group * ((L + 63) / 64) * (long long)((sh.d + 63) / 64);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    read_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return counted(cudaSuccess);
+}
+
+template <typename T>
+cudaError_t grads(const Shape &sh, Rows y, Rows x, Rows dx, int group, int L, const float *S,
+                  const float *z, float2 *rt, const int *lengths, int keys, cudaStream_t s) {
+    GradParams p{y.x, x.x, dx.x, y.s, x.s, dx.s, S, z, rt, lengths,
+                 sh.Hk, group, L, sh.d, sh.phi, sh.norm, keys};
+    const long long blocks = sh.heads() * group * ((L + 31) / 32);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    grad_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return counted(cudaSuccess);
+}
+
+template <typename T>
+cudaError_t forward(const Shape &sh, const Plan &pl, Rows q, Rows k, Rows v, Rows out, float *S,
+                    float *z, char *ws, cudaStream_t s) {
+    cudaError_t e =
+        sums<T>(sh, k, v, 1, sh.M, nullptr, sh.lengths, pl.keys, S, z, ws, s);
+    if (e != cudaSuccess || sh.N == 0) return e;
+    return read<T>(sh, q, out, sh.G(), sh.N, S, z, sh.norm, nullptr, s);
+}
+
+template <typename T>
+cudaError_t backward(const Shape &sh, const Plan &pl, Rows dout, Rows q, Rows k, Rows v,
+                     const float *S, const float *z, Rows dq, Rows dk, Rows dv, char *ws,
+                     cudaStream_t s) {
+    float *dS = reinterpret_cast<float *>(ws), *dz = reinterpret_cast<float *>(ws + pl.off_dz);
+    float2 *rt = reinterpret_cast<float2 *>(ws + pl.off_rt);
+    cudaError_t e = cudaSuccess;
+    if (sh.N > 0)
+        e = grads<T>(sh, dout, q, dq, sh.G(), sh.N, S, z, rt, nullptr, 0, s);
+    if (e != cudaSuccess || sh.M == 0) return e;
+    e = sums<T>(sh, q, dout, sh.G(), sh.N, rt, nullptr, pl.queries, dS, dz, ws + pl.off_part, s);
+    if (e == cudaSuccess)
+        e = grads<T>(sh, v, k, dk, 1, sh.M, dS, dz, nullptr, sh.lengths, 1, s);
+    if (e == cudaSuccess) e = read<T>(sh, k, dv, 1, sh.M, dS, dz, 0, sh.lengths, s);
+    return e;
+}
+
+template <typename T, int V>
+cudaError_t launch_step(const StepParams &p, long long states, cudaStream_t s) {
+    const int rows = p.G * p.N;
+    auto go = [&](auto kern, int per) {
+        const long long blocks = states * ((rows + per - 1) / per);
+        if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        kern<<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        return counted(cudaSuccess);
+    };
+    if (rows <= 1) return go(step_kernel<T, 1, V>, 1);
+    if (rows <= 2) return go(step_kernel<T, 2, V>, 2);
+    if (rows <= 4) return go(step_kernel<T, 4, V>, 4);
+    return go(step_kernel<T, 8, V>, 8);
+}
+
+template <typename T>
+cudaError_t step(const Shape &sh, Rows q, Rows out, const float *S, const float *z,
+                 cudaStream_t s) {
+    // more queries than this per state: tiles of them
+    if ((long long)sh.G() * sh.N > 16)
+        return read<T>(sh, q, out, sh.G(), sh.N, S, z, sh.norm, nullptr, s);
+    const StepParams p{S, z, q.x, out.x, q.s, out.s, sh.Hk, sh.G(), sh.N, sh.d, sh.phi, sh.norm};
+    return sh.d % 4 == 0 && (uintptr_t)S % 16 == 0 ? launch_step<T, 4>(p, sh.heads(), s)
+                                                  : launch_step<T, 1>(p, sh.heads(), s);
+}
+
+// ---------------------------------------------------------------- checks
+
+la_status shape_of(const char *who, Shape &sh, const int *lengths, int B, int Hq, int Hk, int N,
+                   int M, int d, const la_variant *variant, la_dtype dtype) {
+    if (B < 0 || Hq < 0 || Hk < 0 || N < 0 || M < 0)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "negative B, Hq, Hk, N or M");
+    if (d < 1 || d > LA_MAX_D) return layer_fail(LA_ERR_INVALID_ARG, who, "d must be in 1..256");
+    if (dtype != LA_F32 && dtype != LA_BF16)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unknown dtype");
+    if (Hk == 0 ? Hq != 0 : Hq % Hk != 0)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "Hq must be a multiple of Hk");
+    if (variant && ((variant->feature_map != LA_PHI_ELU1 &&
+                     variant->feature_map != LA_PHI_IDENTITY) ||
+                    (variant->normalise != 0 && variant->normalise != 1)))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unknown variant");
+    if ((uintptr_t)lengths % 4) return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned lengths");
+    if ((double)B * std::max(Hq, Hk) * ((double)std::max(N, M) + 1) > 1e10 ||
+        (double)B * Hk * 64 > 2147483647.0)
+        return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
+    sh = {B, Hq, Hk, N, M, d, !variant || variant->feature_map == LA_PHI_ELU1,
+          variant ? variant->normalise : 1, lengths};
+    return LA_OK;
+}
+
+// One of the call's tensors: [B][H][L][d] at its strides, `written` or read.
+la_status rows_of(const char *who, Rows &r, const void *x, const la_strides *s, int H, int L,
+                  const Shape &sh, la_dtype dtype, bool written) {
+    r = {const_cast<void *>(x), s ? *s : contiguous(H, L, sh.d)};
+    if (sh.B == 0 || H == 0 || L == 0) return LA_OK;
+    if (!x) return layer_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+    if ((uintptr_t)x % (dtype == LA_F32 ? 4 : 2))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
+    if (negative(r.s)) return layer_fail(LA_ERR_INVALID_ARG, who, "negative stride");
+    if (written && !rows_disjoint(r.s, sh.B, H, L, sh.d))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
+    return LA_OK;
+}
+
+la_status states_fine(const char *who, const float *S, const float *z) {
+    if (!S || !z) return layer_fail(LA_ERR_INVALID_ARG, who, "null state pointer");
+    if ((uintptr_t)S % 4 || (uintptr_t)z % 4)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned state pointer");
+    return LA_OK;
+}
+
+// The caller's workspace, or one of the stream's (then in `own`).
+la_status workspace_of(const char *who, void *workspace, size_t bytes, size_t need, char **ws,
+                       void **own, cudaStream_t s) {
+    *own = nullptr;
+    *ws = static_cast<char *>(workspace);
+    if (need == 0) return LA_OK;
+    if (workspace) {
+        if (bytes < need || (uintptr_t)workspace % 16)
+            return layer_fail(LA_ERR_INVALID_ARG, who,
+                              "workspace too small or not 16-byte aligned");
+        return LA_OK;
+    }
+    if (tc_workspace_alloc(own, need, s) != cudaSuccess) {
+        (void)cudaGetLastError();
+        *own = nullptr;
+        return layer_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
+    }
+    *ws = static_cast<char *>(*own);
+    return LA_OK;
+}
+
+la_status finish(const char *who, cudaError_t e, void *own, cudaStream_t s) {
+    if (own) {
+        const cudaError_t ef = cudaFreeAsync(own, s);
+        if (e == cudaSuccess) e = ef;
+    }
+    if (e == cudaSuccess) return LA_OK;
+    return layer_fail(e == cudaErrorInvalidConfiguration ? LA_ERR_UNSUPPORTED : LA_ERR_CUDA, who,
+                      cudaGetErrorString(e));
+}
+
+template <int kIn, int kOut>
+bool aliased(const void *const (&in)[kIn], const void *const (&out)[kOut]) {
+    for (int i = 0; i < kOut; ++i) {
+        if (!out[i]) continue;
+        for (const void *x : in)
+            if (x == out[i]) return true;
+        for (int j = 0; j < i; ++j)
+            if (out[j] == out[i]) return true;
+    }
+    return false;
+}
+
+}  // namespace
+}  // namespace cross
+}  // namespace la
+
+using namespace la;
+using namespace la::cross;
+
+extern "C" {
+
+__attribute__((visibility("default")))
+la_status la_forward_cross(const void *q, const void *k, const void *v, void *out, float *S,
+                           float *z, const int *lengths, const la_strides *strides, int B, int Hq,
+                           int Hk, int N, int M, int d, const la_variant *variant, la_dtype dtype,
+                           void *workspace, size_t workspace_bytes, la_stream_t stream) {
+    const char *who = "la_forward_cross";
+    Shape sh;
+    la_status st = shape_of(who, sh, lengths, B, Hq, Hk, N, M, d, variant, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || Hk == 0) return LA_OK;
+    Rows rq, rk, rv, ro;
+    if ((st = rows_of(who, rq, q, strides, Hq, N, sh, dtype, false)) != LA_OK ||
+        (st = rows_of(who, rk, k, strides ? strides + 1 : nullptr, Hk, M, sh, dtype, false)) !=
+            LA_OK ||
+        (st = rows_of(who, rv, v, strides ? strides + 2 : nullptr, Hk, M, sh, dtype, false)) !=
+            LA_OK ||
+        (st = rows_of(who, ro, out, strides ? strides + 3 : nullptr, Hq, N, sh, dtype, true)) !=
+            LA_OK ||
+        (st = states_fine(who, S, z)) != LA_OK)
+        return st;
+    if (aliased({q, k, v}, {static_cast<const void *>(out), S, z}))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "an output aliases another tensor");
+    int sms = 0;
+    cudaError_t e = tchost::sm_count(&sms);
+    if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+    const Plan pl = plan_of(sh, sms, false);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char *ws;
+    void *own;
+    st = workspace_of(who, workspace, workspace_bytes, pl.total, &ws, &own, s);
+    if (st != LA_OK) return st;
+    e = dtype == LA_F32 ? forward<float>(sh, pl, rq, rk, rv, ro, S, z, ws, s)
+                        : forward<__nv_bfloat16>(sh, pl, rq, rk, rv, ro, S, z, ws, s);
+    return finish(who, e, own, s);
+}
+
+__attribute__((visibility("default")))
+la_status la_backward_cross(const void *dout, const void *q, const void *k, const void *v,
+                            const float *S, const float *z, const int *lengths, void *dq,
+                            void *dk, void *dv, const la_strides *strides, int B, int Hq, int Hk,
+                            int N, int M, int d, const la_variant *variant, la_dtype dtype,
+                            void *workspace, size_t workspace_bytes, la_stream_t stream) {
+    const char *who = "la_backward_cross";
+    Shape sh;
+    la_status st = shape_of(who, sh, lengths, B, Hq, Hk, N, M, d, variant, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || Hk == 0) return LA_OK;
+    const void *x[7] = {dout, q, k, v, dq, dk, dv};
+    Rows r[7];
+    for (int i = 0; i < 7; ++i) {
+        const bool queries = i < 2 || i == 4;
+        st = rows_of(who, r[i], x[i], strides ? strides + i : nullptr, queries ? Hq : Hk,
+                     queries ? N : M, sh, dtype, i >= 4);
+        if (st != LA_OK) return st;
+    }
+    if ((st = states_fine(who, S, z)) != LA_OK) return st;
+    if (aliased({dout, q, k, v, static_cast<const void *>(S), static_cast<const void *>(z)},
+                {static_cast<const void *>(dq), static_cast<const void *>(dk),
+                 static_cast<const void *>(dv)}))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "an output aliases another tensor");
+    int sms = 0;
+    cudaError_t e = tchost::sm_count(&sms);
+    if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+    const Plan pl = plan_of(sh, sms, true);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char *ws;
+    void *own;
+    st = workspace_of(who, workspace, workspace_bytes, pl.total, &ws, &own, s);
+    if (st != LA_OK) return st;
+    e = dtype == LA_F32
+            ? backward<float>(sh, pl, r[0], r[1], r[2], r[3], S, z, r[4], r[5], r[6], ws, s)
+            : backward<__nv_bfloat16>(sh, pl, r[0], r[1], r[2], r[3], S, z, r[4], r[5], r[6], ws,
+                                      s);
+    return finish(who, e, own, s);
+}
+
+__attribute__((visibility("default")))
+la_status la_decode_step_cross(const float *S, const float *z, const void *q, void *out,
+                               const la_strides *strides, int B, int Hq, int Hk, int N, int d,
+                               const la_variant *variant, la_dtype dtype, la_stream_t stream) {
+    const char *who = "la_decode_step_cross";
+    Shape sh;
+    la_status st = shape_of(who, sh, nullptr, B, Hq, Hk, N, 0, d, variant, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || Hq == 0 || N == 0) return LA_OK;
+    Rows rq, ro;
+    if ((st = rows_of(who, rq, q, strides, Hq, N, sh, dtype, false)) != LA_OK ||
+        (st = rows_of(who, ro, out, strides ? strides + 1 : nullptr, Hq, N, sh, dtype, true)) !=
+            LA_OK ||
+        (st = states_fine(who, S, z)) != LA_OK)
+        return st;
+    if (aliased({q, static_cast<const void *>(S), static_cast<const void *>(z)},
+                {static_cast<const void *>(out)}))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "out aliases an input");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(who,
+                  dtype == LA_F32 ? step<float>(sh, rq, ro, S, z, s)
+                                  : step<__nv_bfloat16>(sh, rq, ro, S, z, s),
+                  nullptr, s);
+}
+
+__attribute__((visibility("default")))
+size_t la_cross_workspace_bytes(int B, int Hq, int Hk, int N, int M, int d, la_dtype dtype,
+                                int backward) {
+    if (B < 1 || Hk < 1 || Hq < 0 || Hq % Hk || N < 0 || M < 0 || d < 1 || d > LA_MAX_D) return 0;
+    if (dtype != LA_F32 && dtype != LA_BF16) return 0;
+    int sms = 0;
+    if (tchost::sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
+    const Shape sh{B, Hq, Hk, N, M, d, 1, 1, nullptr};
+    return plan_of(sh, sms, backward != 0).total;
+}
+
+}  // extern "C"

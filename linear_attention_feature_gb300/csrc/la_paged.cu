@@ -1,0 +1,985 @@
+// Softmax attention of new tokens over a paged cache (la_decode_step_paged in
+// include/linattn.h):
+//   o_t = sum_j exp(s_tj) v_j / sum_j exp(s_tj),  s_tj = scale q_t . k_j,
+// over the keys j in (p_t - window, p_t], p_t = lengths[b] + t.
+//
+// One pass over keys and values: each warp keeps the running maximum m, the sum l
+// of exp(s - m) and the output times l, all fp32, and multiplies the last two by
+// exp(m_old - m_new) where the maximum moves.  Bound by reading the cache.
+//
+// The split.  The call's work is one list: for each sequence, head of keys and tile
+// of queries the tiles of kTile keys that it looks at.  Every block finds the list's
+// length from `lengths` itself and takes an equal piece, whatever the sequences'
+// lengths.  A stretch of tiles with the same queries that lies in one block is
+// written at once; what lies in several leaves (m, l, output) of each piece in the
+// workspace, and a second kernel joins the pieces in order.  Repeated calls are
+// bit-identical.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "la_internal.h"
+#include "la_layer.cuh"
+#include "la_tc.h"
+#include "la_tc_host.h"
+#include "la_tc_ptx.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kMostTokens = 1 << 30, kMostNew = 1 << 20;  // of a sequence, of a call
+constexpr int kRowTile = 16;  // queries of one head of keys that a block takes at most
+
+struct Params {
+    const void *q, *k, *v;
+    void *out;
+    la_strides sq, so, sk, sv;
+    const int *table, *lengths;
+    long long table_stride;
+    int pages, page_size, max_pages;
+    int B, Hk, G, T, d, window;
+    int row_tile, row_tiles;  // queries of a block, tiles of them per head of keys
+    float scale2;             // scale log2(e)
+    int4 *info;               // of each block: see Plan
+    float *part;              // [blocks][2][row_tile][d + 2]
+};
+
+// Where a sequence's keys lie: [lo, hi) in tiles of kTile from the one of lo on.  One
+// that takes no keys (an unused place in the batch) has one tile, all masked, so that
+// its zeros get written.
+struct Span {
+    int before, lo, hi, first, tiles;
+};
+
+template <int kTile>
+__device__ __forceinline__ Span span_of(const Params &p, int b) {
+    Span s;
+    s.before = min(p.lengths[b], kMostTokens);
+    s.hi = s.before < 0 ? 0 : min(s.before + p.T, p.max_pages * p.page_size);
+    s.lo = p.window > 0 ? min(max(s.before + 1 - p.window, 0), s.hi) : 0;
+    s.first = s.lo / kTile;
+    s.tiles = max(1, (s.hi + kTile - 1) / kTile - s.first);
+    return s;
+}
+
+// Whether all queries of the call look at all of n keys from key0 on.
+__device__ __forceinline__ bool all_see(const Params &p, const Span &s, int key0, int n) {
+    return key0 + n - 1 <= s.before && (p.window == 0 || key0 > s.before + p.T - 1 - p.window);
+}
+
+// A place in the list of tiles.
+template <int kTile>
+struct Place {
+    Span s;
+    int b, seg, tile;  // seg: head of keys and tile of queries
+
+    __device__ __forceinline__ void next(const Params &p, int segs) {
+        if (++tile < s.tiles) return;
+        tile = 0;
+        if (++seg < segs) return;
+        seg = 0;
+        if (++b < p.B) s = span_of<kTile>(p, b);
+    }
+};
+
+// This block's piece of the list, [x0, x1), and the place of x0.  A list shorter than
+// the grid has a piece of one tile for each of its first blocks, so that no piece
+// between others is empty.  `shared` has kWarps + 4 numbers.
+template <int kTile>
+__device__ __forceinline__ Place<kTile> find_piece(const Params &p, long long *shared,
+                                                   long long &total, int &pieces,
+                                                   long long &x0, long long &x1) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int segs = p.Hk * p.row_tiles;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += span_of<kTile>(p, b).tiles;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long other = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += other;
+    }
+    if (lane == 31) shared[warp] = upto;
+    __syncthreads();
+    long long base = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += shared[w];
+        total += shared[w];
+    }
+    total *= segs;
+    pieces = (int)min((long long)gridDim.x, total);
+    x0 = total * min((int)blockIdx.x, pieces) / pieces;
+    x1 = total * min((int)blockIdx.x + 1, pieces) / pieces;
+    long long at = (base + upto - mine) * segs;  // of this thread's first sequence
+    if (x0 >= at && x0 < at + mine * segs) {
+        int b = b0;
+        for (;; ++b) {
+            const long long n = (long long)span_of<kTile>(p, b).tiles * segs;
+            if (x0 < at + n) break;
+            at += n;
+        }
+        shared[kWarps] = b;
+        shared[kWarps + 1] = x0 - at;
+    }
+    __syncthreads();
+    Place<kTile> c;
+    c.b = (int)shared[kWarps];
+    const long long rest = shared[kWarps + 1];
+    if (x0 < x1) {
+        c.s = span_of<kTile>(p, c.b);
+        c.seg = (int)(rest / c.s.tiles);
+        c.tile = (int)(rest - (long long)c.seg * c.s.tiles);
+    }
+    return c;
+}
+
+// The block whose piece holds place x.
+__device__ __forceinline__ int block_of(long long x, long long total, int blocks) {
+    return (int)(((x + 1) * blocks - 1) / total);
+}
+
+// One (m, l) pair of running statistics and its merge: the factor of what went before.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ void copy16(unsigned dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(unsigned dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 4 : 0) : "memory");
+}
+
+// Copies kKeys rows of keys and of values into one stage of a warp's ring.  Lane l <
+// kKeys holds where row l lies (offsets in elements) and whether it is to be read; the
+// others are filled with zeros.  kUnit: bytes of a copy; 2: plain loads.
+template <typename T, int kD, int kPitch, int kKeys, int kUnit>
+__device__ __forceinline__ void copy_rows(const Params &p, T *stage, long long ko, long long vo,
+                                          bool ok) {
+    const int lane = threadIdx.x & 31;
+    const T *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
+    const int units = p.d * (int)sizeof(T) / kUnit;
+    constexpr int kPer = kUnit / (int)sizeof(T);  // elements
+    constexpr int kMost = kD / kPer;
+    constexpr int kLanes = kUnit < 16 || kMost > 16 ? 32 : kMost > 8 ? 16 : kMost > 4 ? 8 : 4;
+#pragma unroll
+    for (int r = 0; r < kKeys; r += 32 / kLanes) {
+        const int row = r + lane / kLanes;
+        const long long kr = __shfl_sync(~0u, ko, row), vr = __shfl_sync(~0u, vo, row);
+        const bool fine = __shfl_sync(~0u, (int)ok, row);
+        const unsigned dst = tc::smem_u32(stage + row * kPitch);
+        constexpr unsigned kOther = kKeys * kPitch * sizeof(T);
+        for (int u = lane % kLanes; u < units; u += kLanes) {
+            const T *ks = fine ? k + kr + u * kPer : k, *vs = fine ? v + vr + u * kPer : v;
+            if constexpr (kUnit == 16) {
+                copy16(dst + u * 16, ks, fine);
+                copy16(dst + kOther + u * 16, vs, fine);
+            } else if constexpr (kUnit == 4) {
+                copy4(dst + u * 4, ks, fine);
+                copy4(dst + kOther + u * 4, vs, fine);
+            } else {
+                stage[row * kPitch + u] = fine ? *ks : T(0.f);
+                stage[(kKeys + row) * kPitch + u] = fine ? *vs : T(0.f);
+            }
+        }
+    }
+}
+
+// Where a key lies: the page that the table names and the slot in it.
+struct Slot {
+    int key, page, slot;
+};
+
+template <int kTile, int kKeys>
+__device__ __forceinline__ Slot slot_of(const Params &p, const Place<kTile> &c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Slot s;
+    s.key = (c.s.first + c.tile) * kTile + warp * kKeys + lane;
+    s.page = -1;
+    s.slot = 0;
+    if (lane < kKeys && s.key >= c.s.lo && s.key < c.s.hi) {
+        const int column = s.key / p.page_size;
+        s.slot = s.key - column * p.page_size;
+        s.page = p.table[c.b * p.table_stride + column];
+        if (s.page >= p.pages) s.page = -1;
+    }
+    return s;
+}
+
+// Output rows of a block: the queries of one tile.  Row r of the head's G T queries is
+// query t = r % T of head r / T of the group.
+template <typename T>
+__device__ __forceinline__ long long row_offset(const Params &p, const la_strides &s, int b, int h,
+                                                int r) {
+    const int g = r / p.T, t = r - g * p.T;
+    return b * s.b + (long long)(h * p.G + g) * s.h + t * s.n;
+}
+
+// Writes a finished stretch, or leaves it for the join.  o: [row][pitch] outputs times
+// l, ml: (m, l) of each row, in shared memory.
+template <typename T>
+__device__ __forceinline__ void write_rows(const Params &p, int b, int h, int row0, int rows,
+                                           const float *o, int pitch, const float2 *ml,
+                                           int slot) {
+    for (int i = threadIdx.x; i < rows * p.d; i += kThreads) {
+        const int r = i / p.d, c = i - r * p.d;
+        const float2 s = ml[r];
+        if (slot < 0) {
+            T *y = static_cast<T *>(p.out) + row_offset<T>(p, p.so, b, h, row0 + r);
+            from_f(y[c], s.y == 0.f ? 0.f : o[r * pitch + c] / s.y);
+        } else {
+            float *w = p.part +
+                       ((long long)(blockIdx.x * 2 + slot) * p.row_tile + r) * (p.d + 2);
+            w[c] = o[r * pitch + c];
+            if (c == 0) w[p.d] = s.x, w[p.d + 1] = s.y;
+        }
+    }
+}
+
+// What the join has to know of a block: in .x the stretch that its first piece
+// continues (b segs + seg is 64 bits: .x low, .y high; .y = -1: none), in .z and .w
+// the first and the last block of that stretch.
+__device__ __forceinline__ void note_first(const Params &p, long long stretch, int i0, int i1) {
+    p.info[blockIdx.x] = make_int4((int)(unsigned)stretch, (int)(stretch >> 32), i0, i1);
+}
+
+// ------------------------------------------------------------------ bf16
+
+__device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(unsigned (&r)[4], unsigned at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// c += a b, 16 x 16 times 16 x 8.
+__device__ __forceinline__ void mma(float (&c)[4], const unsigned (&a)[4], unsigned b0,
+                                    unsigned b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int kD>
+struct Half {
+    static constexpr int kKeys = 16, kTile = kWarps * kKeys;
+    static constexpr int kPitch = kD + 8;  // 16 bytes more than the row: no bank conflicts
+    static constexpr int kStage = 2 * kKeys * kPitch * 2;  // bytes, of a warp
+    static constexpr int kStages = kD == 64 ? 5 : kD == 96 || kD == 192 ? 4 : 3;
+    static constexpr int kBlocks = kD <= 128 ? 2 : 1;  // per SM
+    static constexpr int kOutPitch = kD + 4;
+    static constexpr int kOffOut = kWarps * kStages * kStage;
+    static constexpr int kOffMl = kOffOut + kRowTile * kOutPitch * 4;
+    static constexpr int kOffMask = kOffMl + (kWarps + 1) * kRowTile * 8;
+    static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4 + (kStages % 2 ? 0 : 0);
+    static constexpr int kSmem = kOffPlan + (kWarps + 4) * 8;
+    static_assert(kOffPlan % 8 == 0 && kSmem <= 232448 / 1, "shared memory");
+    static_assert(kSmem + 1024 <= 233472 / kBlocks, "blocks per SM");
+};
+
+// 16 queries of one head of keys (the heads that share it, and the call's tokens)
+// against 16 keys per warp and step: m16n8k16 products, whose 16 rows would be empty
+// for one query, but the tensor cores wait for the memory all the same.  P is rounded
+// to bf16 for its product with the values; l sums the rounded ones, so that the
+// weights still add to one.
+template <int kD, int kUnit>
+__global__ void __launch_bounds__(kThreads, Half<kD>::kBlocks)
+paged_half_kernel(const __grid_constant__ Params p) {
+    using L = Half<kD>;
+    using T = __nv_bfloat16;
+    constexpr int kTile = L::kTile, kKeys = L::kKeys;
+    extern __shared__ __align__(128) char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    char *ring = smem + warp * L::kStages * L::kStage;
+    float *obuf = reinterpret_cast<float *>(smem + L::kOffOut);
+    float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
+    unsigned *masks = reinterpret_cast<unsigned *>(smem + L::kOffMask) + warp * L::kStages;
+    const int segs = p.Hk * p.row_tiles;
+
+    tc::grid_dep_launch();
+    for (int i = threadIdx.x; i < L::kOffOut / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+    long long total, x0, x1;
+    int pieces;
+    Place<kTile> c = find_piece<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan),
+                                       total, pieces, x0, x1);
+    if (threadIdx.x == 0) note_first(p, -1, 0, 0);
+    if (x0 >= x1) return;
+    const int steps = (int)(x1 - x0);
+
+    // the copying side, some tiles ahead
+    Place<kTile> f = c;
+    int f_left = steps, f_stage = 0;
+    Slot ahead = slot_of<kTile, kKeys>(p, f);
+    auto fetch = [&]() {
+        if (f_left > 0) {
+            const int h = f.seg / p.row_tiles;
+            const bool ok = ahead.page >= 0;
+            copy_rows<T, kD, L::kPitch, kKeys, kUnit>(
+                p, reinterpret_cast<T *>(ring + f_stage * L::kStage),
+                ahead.page * p.sk.b + h * p.sk.h + ahead.slot * p.sk.n,
+                ahead.page * p.sv.b + h * p.sv.h + ahead.slot * p.sv.n, ok);
+            const unsigned mask = __ballot_sync(~0u, ok);
+            if (lane == 0) masks[f_stage] = mask;
+            f_stage = f_stage + 1 == L::kStages ? 0 : f_stage + 1;
+            if (--f_left > 0) {
+                f.next(p, segs);
+                ahead = slot_of<kTile, kKeys>(p, f);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < L::kStages - 1; ++i) fetch();
+
+    int stage = 0;
+    for (int left = steps; left > 0;) {
+        // ---- a stretch of tiles with the same queries
+        const int h = c.seg / p.row_tiles, row0 = (c.seg - h * p.row_tiles) * p.row_tile;
+        const int rows = min(p.row_tile, p.G * p.T - row0);
+        const bool began = c.tile > 0;  // in an earlier block
+        const long long x = x1 - left;
+        const long long seg0 = x - c.tile, seg1 = seg0 + c.s.tiles;
+        const int n = (int)min((long long)left, seg1 - x);
+        unsigned a[kD / 16][4];
+        {
+            T *qbuf = reinterpret_cast<T *>(obuf);
+            for (int i = threadIdx.x; i < kRowTile * kD; i += kThreads) {
+                const int r = i / kD, e = i % kD;
+                T value = T(0.f);
+                if (r < rows && e < p.d)
+                    value = static_cast<const T *>(
+                        p.q)[row_offset<T>(p, p.sq, c.b, h, row0 + r) + e];
+                qbuf[r * L::kPitch + e] = value;
+            }
+            __syncthreads();
+            const unsigned at =
+                tc::smem_u32(qbuf + (lane & 15) * L::kPitch + (lane >> 4) * 8);
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) ldmatrix4(a[ks], at + ks * 32);
+        }
+        float o[kD / 8][4];
+#pragma unroll
+        for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        // the last key of this lane's two queries
+        int last[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            last[i] = c.s.before + (row0 + (lane >> 2) + 8 * i) % p.T;
+
+        for (int it = 0; it < n; ++it) {
+            fetch();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+            __syncwarp();
+            const char *st = ring + stage * L::kStage;
+            const unsigned mask = masks[stage];
+            const int key0 = (c.s.first + c.tile) * kTile + warp * kKeys;
+            float s[2][4] = {};
+            {
+                const unsigned at =
+                    tc::smem_u32(st) +
+                    ((lane & 7) + (lane >> 4) * 8) * (L::kPitch * 2) + ((lane >> 3) & 1) * 16;
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    unsigned b[4];
+                    ldmatrix4(b, at + ks * 32);
+                    mma(s[0], a[ks], b[0], b[1]);
+                    mma(s[1], a[ks], b[2], b[3]);
+                }
+            }
+            const bool whole = mask == 0xffffu && all_see(p, c.s, key0, kKeys);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j][e] *= p.scale2;
+                    if (!whole) {
+                        const int i = j * 8 + (lane & 3) * 2 + (e & 1), key = key0 + i;
+                        const int end = last[e >> 1];
+                        if (!(mask >> i & 1) || key > end ||
+                            (p.window > 0 && key <= end - p.window))
+                            s[j][e] = -INFINITY;
+                    }
+                }
+            float top[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]),
+                               fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 1));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 2));
+                top[i] = fmaxf(top[i], m[i]);
+            }
+            if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[i] = exp2f(m[i] - finite_max(top[i]));
+                    m[i] = top[i];
+                    l[i] *= w[i];
+                }
+#pragma unroll
+                for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] *= w[e >> 1];
+            }
+            unsigned pa[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float mi = finite_max(m[i]);
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(exp2f(s[j][2 * i] - mi),
+                                                                   exp2f(s[j][2 * i + 1] - mi));
+                    l[i] += __low2float(w) + __high2float(w);
+                    pa[2 * j + i] = reinterpret_cast<const unsigned &>(w);
+                }
+            {
+                const unsigned at = tc::smem_u32(st) + kKeys * L::kPitch * 2 +
+                                    (lane & 15) * (L::kPitch * 2) + (lane >> 4) * 16;
+                // A weight of 0 does not keep a value that is not finite out of a sum: a
+                // tile where queries look at different keys takes such values singly.
+                bool singly = false;
+                if (p.T > 1 && !whole) {
+                    const T *v = reinterpret_cast<const T *>(st) + kKeys * L::kPitch;
+                    bool odd = false;
+                    for (int i = lane; i < kKeys * L::kPitch; i += 32)
+                        odd |= i % L::kPitch < kD && !(fabsf(to_f(v[i])) < INFINITY);
+                    singly = __any_sync(~0u, odd);
+                }
+                if (singly) {
+                    const T *v = reinterpret_cast<const T *>(st) + kKeys * L::kPitch;
+                    for (int i = 0; i < kKeys; ++i) {
+                        const int from = (lane & 28) + (i & 7) / 2;
+                        unsigned u[2];  // of the two queries
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const unsigned lo = __shfl_sync(~0u, pa[r], from);
+                            const unsigned hi = __shfl_sync(~0u, pa[2 + r], from);
+                            u[r] = i < 8 ? lo : hi;
+                            u[r] = i & 1 ? u[r] & 0xffff0000u : u[r] << 16;
+                        }
+#pragma unroll
+                        for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (u[e >> 1])
+                                    o[j][e] = fmaf(__uint_as_float(u[e >> 1]),
+                                                   to_f(v[i * L::kPitch + 8 * j +
+                                                          (lane & 3) * 2 + (e & 1)]),
+                                                   o[j][e]);
+                    }
+                } else
+#pragma unroll
+                for (int j = 0; j < kD / 16; ++j) {
+                    unsigned b[4];
+                    ldmatrix4_t(b, at + j * 32);
+                    mma(o[2 * j], pa, b[0], b[1]);
+                    mma(o[2 * j + 1], pa, b[2], b[3]);
+                }
+            }
+            __syncwarp();  // the stage may be filled again
+            stage = stage + 1 == L::kStages ? 0 : stage + 1;
+            c.tile += 1;
+        }
+        // ---- the warps' parts together, in order
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(~0u, l[i], 1);
+            l[i] += __shfl_xor_sync(~0u, l[i], 2);
+            if ((lane & 3) == 0)
+                ml[warp * kRowTile + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+        }
+        __syncthreads();
+        float w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[q * kRowTile + r].x);
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q)
+                sum += ml[q * kRowTile + r].y * exp2f(ml[q * kRowTile + r].x - finite_max(top));
+            w[i] = exp2f(m[i] - finite_max(top));
+            if (warp == 0 && (lane & 3) == 0) ml[kWarps * kRowTile + r] = make_float2(top, sum);
+        }
+        for (int q = 0; q < kWarps; ++q) {
+            if (warp == q)
+#pragma unroll
+                for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        float2 *y = reinterpret_cast<float2 *>(
+                            obuf + ((lane >> 2) + 4 * e) * L::kOutPitch + 8 * j + (lane & 3) * 2);
+                        float2 u = make_float2(o[j][e] * w[e >> 1], o[j][e + 1] * w[e >> 1]);
+                        if (q > 0) u = make_float2(y->x + u.x, y->y + u.y);
+                        *y = u;
+                    }
+            __syncthreads();
+        }
+        const bool ends = seg1 <= x1;
+        const int slot = began ? 0 : ends ? -1 : 1;
+        write_rows<T>(p, c.b, h, row0, rows, obuf, L::kOutPitch, ml + kWarps * kRowTile, slot);
+        if (began && threadIdx.x == 0)
+            note_first(p, (long long)c.b * segs + c.seg, block_of(seg0, total, pieces),
+                       block_of(seg1 - 1, total, pieces));
+        __syncthreads();
+        left -= n;
+        c.tile -= 1;
+        if (left > 0) c.next(p, segs);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ fp32
+
+template <int kD>
+struct Full {
+    static constexpr int kKeys = kD == 64 ? 16 : 8, kTile = kWarps * kKeys;
+    static constexpr int kParts = 32 / kKeys;  // lanes that share a key
+    static constexpr int kPitch = kD + 4;
+    static constexpr int kStage = 2 * kKeys * kPitch * 4;
+    static constexpr int kStages = 3;
+    static constexpr int kBlocks = kD <= 128 ? 2 : 1;
+    static constexpr int kOffQ = kWarps * kStages * kStage;  // then the output
+    static constexpr int kOffP = kOffQ + 8 * kPitch * 4;     // [warp][row][key]
+    static constexpr int kOffMl = kOffP + kWarps * 8 * kKeys * 4;
+    static constexpr int kOffMask = kOffMl + (kWarps + 1) * 8 * 8;
+    static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4;
+    static constexpr int kSmem = kOffPlan + (kWarps + 4) * 8;
+    static_assert(kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
+    static_assert(kSmem + 1024 <= 233472 / kBlocks, "blocks per SM");
+};
+
+// kR queries per block.  A warp takes kKeys keys per step: kParts lanes share a key's
+// scores, each with every kParts-th 16 bytes of it; then each lane takes every 32nd
+// feature of the values.  fp32 throughout.
+template <int kD, int kR, int kUnit>
+__global__ void __launch_bounds__(kThreads, Full<kD>::kBlocks)
+paged_full_kernel(const __grid_constant__ Params p) {
+    using L = Full<kD>;
+    using T = float;
+    constexpr int kTile = L::kTile, kKeys = L::kKeys, kCols = kD / 32;
+    extern __shared__ __align__(128) char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    char *ring = smem + warp * L::kStages * L::kStage;
+    float *qbuf = reinterpret_cast<float *>(smem + L::kOffQ);
+    float *pbuf = reinterpret_cast<float *>(smem + L::kOffP) + warp * 8 * kKeys;
+    float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
+    unsigned *masks = reinterpret_cast<unsigned *>(smem + L::kOffMask) + warp * L::kStages;
+    const int segs = p.Hk * p.row_tiles;
+
+    tc::grid_dep_launch();
+    for (int i = threadIdx.x; i < L::kOffQ / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+    long long total, x0, x1;
+    int pieces;
+    Place<kTile> c = find_piece<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan),
+                                       total, pieces, x0, x1);
+    if (threadIdx.x == 0) note_first(p, -1, 0, 0);
+    if (x0 >= x1) return;
+    const int steps = (int)(x1 - x0);
+
+    Place<kTile> f = c;
+    int f_left = steps, f_stage = 0;
+    Slot ahead = slot_of<kTile, kKeys>(p, f);
+    auto fetch = [&]() {
+        if (f_left > 0) {
+            const int h = f.seg / p.row_tiles;
+            const bool ok = ahead.page >= 0;
+            copy_rows<T, kD, L::kPitch, kKeys, kUnit>(
+                p, reinterpret_cast<T *>(ring + f_stage * L::kStage),
+                ahead.page * p.sk.b + h * p.sk.h + ahead.slot * p.sk.n,
+                ahead.page * p.sv.b + h * p.sv.h + ahead.slot * p.sv.n, ok);
+            const unsigned mask = __ballot_sync(~0u, ok);
+            if (lane == 0) masks[f_stage] = mask;
+            f_stage = f_stage + 1 == L::kStages ? 0 : f_stage + 1;
+            if (--f_left > 0) {
+                f.next(p, segs);
+                ahead = slot_of<kTile, kKeys>(p, f);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < L::kStages - 1; ++i) fetch();
+
+    const int key_in = lane % kKeys, part = lane / kKeys;
+    int stage = 0;
+    for (int left = steps; left > 0;) {
+        const int h = c.seg / p.row_tiles, row0 = (c.seg - h * p.row_tiles) * p.row_tile;
+        const int rows = min(p.row_tile, p.G * p.T - row0);
+        const bool began = c.tile > 0;
+        const long long x = x1 - left;
+        const long long seg0 = x - c.tile, seg1 = seg0 + c.s.tiles;
+        const int n = (int)min((long long)left, seg1 - x);
+        for (int i = threadIdx.x; i < kR * kD; i += kThreads) {
+            const int r = i / kD, e = i % kD;
+            float value = 0.f;
+            if (r < rows && e < p.d)
+                value = static_cast<const float *>(
+                    p.q)[row_offset<T>(p, p.sq, c.b, h, row0 + r) + e];
+            qbuf[r * L::kPitch + e] = value;
+        }
+        __syncthreads();
+        float o[kR][kCols] = {}, m[kR], l[kR];
+        int last[kR];  // the last key of each query
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            m[r] = -INFINITY, l[r] = 0.f;
+            last[r] = c.s.before + (row0 + r) % p.T;
+        }
+
+        for (int it = 0; it < n; ++it) {
+            fetch();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+            __syncwarp();
+            const float *ks = reinterpret_cast<const float *>(ring + stage * L::kStage);
+            const float *vs = ks + kKeys * L::kPitch;
+            const unsigned mask = masks[stage];
+            const int key = (c.s.first + c.tile) * kTile + warp * kKeys + key_in;
+            const bool whole = all_see(p, c.s, key - key_in, kKeys);
+            float s[kR] = {};
+            for (int e = 4 * part; e < p.d; e += 4 * L::kParts) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + key_in * L::kPitch + e);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float4 q4 =
+                        *reinterpret_cast<const float4 *>(qbuf + r * L::kPitch + e);
+                    s[r] = fmaf(q4.x, k4.x, s[r]);
+                    s[r] = fmaf(q4.y, k4.y, s[r]);
+                    s[r] = fmaf(q4.z, k4.z, s[r]);
+                    s[r] = fmaf(q4.w, k4.w, s[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+#pragma unroll
+                for (int w = kKeys; w < 32; w <<= 1) s[r] += __shfl_xor_sync(~0u, s[r], w);
+                s[r] *= p.scale2;
+                if (!(mask >> key_in & 1) || key > last[r] ||
+                    (p.window > 0 && key <= last[r] - p.window))
+                    s[r] = -INFINITY;
+                float top = s[r];
+#pragma unroll
+                for (int w = 1; w < kKeys; w <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+                top = fmaxf(top, m[r]);
+                if (top > m[r]) {  // the same in all lanes
+                    const float w = exp2f(m[r] - top);
+                    l[r] *= w;
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) o[r][j] *= w;
+                    m[r] = top;
+                }
+                const float w = exp2f(s[r] - finite_max(m[r]));
+                if (part == 0) {
+                    l[r] += w;
+                    pbuf[r * kKeys + key_in] = w;
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kKeys; i += 4) {
+                float4 w[kR];
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+                    w[r] = *reinterpret_cast<const float4 *>(pbuf + r * kKeys + i);
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    const float *v0 = vs + i * L::kPitch + lane + 32 * j;
+                    const float v[4] = {v0[0], v0[L::kPitch], v0[2 * L::kPitch],
+                                        v0[3 * L::kPitch]};
+                    if (!whole) {  // a key that one query looks at may not reach another
+#pragma unroll
+                        for (int r = 0; r < kR; ++r) {
+                            if (w[r].x != 0.f) o[r][j] = fmaf(w[r].x, v[0], o[r][j]);
+                            if (w[r].y != 0.f) o[r][j] = fmaf(w[r].y, v[1], o[r][j]);
+                            if (w[r].z != 0.f) o[r][j] = fmaf(w[r].z, v[2], o[r][j]);
+                            if (w[r].w != 0.f) o[r][j] = fmaf(w[r].w, v[3], o[r][j]);
+                        }
+                        continue;
+                    }
+#pragma unroll
+                    for (int r = 0; r < kR; ++r) {
+                        o[r][j] = fmaf(w[r].x, v[0], o[r][j]);
+                        o[r][j] = fmaf(w[r].y, v[1], o[r][j]);
+                        o[r][j] = fmaf(w[r].z, v[2], o[r][j]);
+                        o[r][j] = fmaf(w[r].w, v[3], o[r][j]);
+                    }
+                }
+            }
+            __syncwarp();
+            stage = stage + 1 == L::kStages ? 0 : stage + 1;
+            c.tile += 1;
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+#pragma unroll
+            for (int w = 1; w < kKeys; w <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], w);
+            if (lane == 0) ml[warp * 8 + r] = make_float2(m[r], l[r]);
+        }
+        __syncthreads();
+        float w[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[q * 8 + r].x);
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q)
+                sum += ml[q * 8 + r].y * exp2f(ml[q * 8 + r].x - finite_max(top));
+            w[r] = exp2f(m[r] - finite_max(top));
+            if (threadIdx.x == 0) ml[kWarps * 8 + r] = make_float2(top, sum);
+        }
+        for (int q = 0; q < kWarps; ++q) {
+            if (warp == q)
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        float *y = qbuf + r * L::kPitch + lane + 32 * j;
+                        *y = q > 0 ? *y + o[r][j] * w[r] : o[r][j] * w[r];
+                    }
+            __syncthreads();
+        }
+        const bool ends = seg1 <= x1;
+        const int slot = began ? 0 : ends ? -1 : 1;
+        write_rows<T>(p, c.b, h, row0, rows, qbuf, L::kPitch, ml + kWarps * 8, slot);
+        if (began && threadIdx.x == 0)
+            note_first(p, (long long)c.b * segs + c.seg, block_of(seg0, total, pieces),
+                       block_of(seg1 - 1, total, pieces));
+        __syncthreads();
+        left -= n;
+        c.tile -= 1;
+        if (left > 0) c.next(p, segs);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Joins the stretches that lie in several blocks: block i looks at the stretch that
+// piece i + 1 continues, if it began in piece i, one query of it.
+template <typename T>
+__global__ void __launch_bounds__(LA_MAX_D) paged_join_kernel(const __grid_constant__ Params p) {
+    tc::grid_dep_wait();
+    const int i = blockIdx.x + 1, r = blockIdx.y;
+    const int4 info = p.info[i];
+    if (info.y < 0 || info.z != i - 1) return;
+    const long long stretch = (long long)info.y << 32 | (unsigned)info.x;
+    const int segs = p.Hk * p.row_tiles;
+    const int b = (int)(stretch / segs), seg = (int)(stretch - (long long)b * segs);
+    const int h = seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * p.row_tile;
+    if (row0 + r >= p.G * p.T) return;
+    const int i0 = info.z, i1 = info.w;
+    auto part = [&](int q) {
+        return p.part + ((long long)(2 * q + (q == i0)) * p.row_tile + r) * (p.d + 2);
+    };
+    float top = -INFINITY;
+    for (int q = i0; q <= i1; ++q) top = fmaxf(top, __ldcg(part(q) + p.d));
+    top = finite_max(top);
+    const int e = threadIdx.x;
+    if (e >= p.d) return;
+    float sum = 0.f, y = 0.f;
+#pragma unroll 4
+    for (int q = i0; q <= i1; ++q) {
+        const float *w = part(q), f = exp2f(__ldcg(w + p.d) - top);
+        sum = fmaf(__ldcg(w + p.d + 1), f, sum);
+        y = fmaf(__ldcg(w + e), f, y);
+    }
+    T *out = static_cast<T *>(p.out) + row_offset<T>(p, p.so, b, h, row0 + r);
+    from_f(out[e], sum == 0.f ? 0.f : y / sum);
+}
+
+struct Choice {
+    const void *kern;
+    int smem, tile, blocks_per_sm;
+};
+
+template <int kD, int kUnit>
+Choice choose_half() {
+    return {reinterpret_cast<const void *>(&paged_half_kernel<kD, kUnit>), Half<kD>::kSmem,
+            Half<kD>::kTile, Half<kD>::kBlocks};
+}
+template <int kUnit>
+Choice choose_half(int d) {
+    if (d <= 64) return choose_half<64, kUnit>();
+    if (d <= 96) return choose_half<96, kUnit>();
+    if (d <= 128) return choose_half<128, kUnit>();
+    if (d <= 192) return choose_half<192, kUnit>();
+    return choose_half<256, kUnit>();
+}
+template <int kD, int kR, int kUnit>
+Choice choose_full() {
+    return {reinterpret_cast<const void *>(&paged_full_kernel<kD, kR, kUnit>), Full<kD>::kSmem,
+            Full<kD>::kTile, Full<kD>::kBlocks};
+}
+template <int kD, int kUnit>
+Choice choose_full(int row_tile) {
+    if (row_tile <= 1) return choose_full<kD, 1, kUnit>();
+    if (row_tile <= 2) return choose_full<kD, 2, kUnit>();
+    if (row_tile <= 4) return choose_full<kD, 4, kUnit>();
+    return choose_full<kD, 8, kUnit>();
+}
+template <int kUnit>
+Choice choose_full(int d, int row_tile) {
+    if (d <= 64) return choose_full<64, kUnit>(row_tile);
+    if (d <= 128) return choose_full<128, kUnit>(row_tile);
+    return choose_full<256, kUnit>(row_tile);
+}
+
+int row_tile_of(long long rows, la_dtype dtype) {
+    const int most = dtype == LA_F32 ? 8 : kRowTile;
+    return (int)std::min<long long>(rows, most);
+}
+
+int blocks_of(int sms) { return 2 * sms; }  // at most
+
+// Bytes of the workspace: the blocks' notes, then their two parts.
+size_t workspace_of(int blocks, int row_tile, int d) {
+    return sizeof(int4) * (size_t)blocks +
+           sizeof(float) * 2 * (size_t)blocks * row_tile * (d + 2);
+}
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+extern "C" {
+
+__attribute__((visibility("default")))
+la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
+                               const la_strides *strides, float scale, int window, int B, int Hq,
+                               int Hk, int T, int d, la_dtype dtype, void *workspace,
+                               size_t workspace_bytes, la_stream_t stream) {
+    const char *who = "la_decode_step_paged";
+    if (Hq < 0 || T < 0) return layer_fail(LA_ERR_INVALID_ARG, who, "negative Hq or T");
+    la_status st = check_cache(who, cache, B, Hk, d, dtype);
+    if (st != LA_OK) return st;
+    if (!std::isfinite(scale)) return layer_fail(LA_ERR_INVALID_ARG, who, "scale must be finite");
+    if (window < 0) return layer_fail(LA_ERR_INVALID_ARG, who, "negative window");
+    if (Hk == 0 ? Hq != 0 : Hq % Hk != 0)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "Hq must be a multiple of Hk");
+    if (B == 0 || T == 0 || Hq == 0) return LA_OK;
+    if (!q || !out) return layer_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+    const uintptr_t elem = dtype == LA_F32 ? 4 : 2;
+    if ((uintptr_t)q % elem || (uintptr_t)out % elem)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
+    Params p{};
+    p.q = q;
+    p.out = out;
+    p.sq = strides ? strides[0] : contiguous(Hq, T, d);
+    p.so = strides ? strides[1] : contiguous(Hq, T, d);
+    if (negative(p.sq) || negative(p.so))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "negative stride");
+    if (!rows_disjoint(p.so, B, Hq, T, d))
+        return layer_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
+    if (out == q || out == cache->k || out == cache->v)
+        return layer_fail(LA_ERR_INVALID_ARG, who, "out aliases an input");
+    const long long rows = (long long)(Hq / Hk) * T;
+    p.row_tile = row_tile_of(rows, dtype);
+    const long long row_tiles = (rows + p.row_tile - 1) / p.row_tile;
+    if (T > kMostNew || rows > 0x7fffffff)
+        return layer_fail(LA_ERR_UNSUPPORTED, who, "too many queries");
+    p.row_tiles = (int)row_tiles;
+    p.k = cache->pages ? cache->k : q;  // without pages nothing is read
+    p.v = cache->pages ? cache->v : q;
+    p.sk = cache->k_strides;
+    p.sv = cache->v_strides;
+    p.table = cache->table;
+    p.lengths = cache->lengths;
+    p.table_stride = cache->table_stride;
+    p.pages = cache->pages;
+    p.page_size = cache->page_size;
+    p.max_pages = cache->max_pages;
+    p.B = B;
+    p.Hk = Hk;
+    p.G = Hq / Hk;
+    p.T = T;
+    p.d = d;
+    p.window = window;
+    p.scale2 = scale * 1.44269504088896341f;
+
+    // bytes per copy: 16, or 4, if every row of the cache is aligned to that
+    unsigned long long all = (uintptr_t)p.k | (uintptr_t)p.v | (unsigned)d * elem;
+    auto add = [&](const la_strides &s) {
+        if (p.pages > 1) all |= (unsigned long long)s.b * elem;
+        if (Hk > 1) all |= (unsigned long long)s.h * elem;
+        if (p.page_size > 1) all |= (unsigned long long)s.n * elem;
+    };
+    add(p.sk);
+    add(p.sv);
+    Choice c;
+    if (dtype == LA_F32)
+        c = all % 16 == 0 ? choose_full<16>(d, p.row_tile) : choose_full<4>(d, p.row_tile);
+    else
+        c = all % 16 == 0 ? choose_half<16>(d)
+                          : all % 4 == 0 ? choose_half<4>(d) : choose_half<2>(d);
+
+    int sms = 0;
+    cudaError_t e = tchost::sm_count(&sms);
+    if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+    // No more blocks than tiles that the table could hold.
+    const long long cap = (long long)p.max_pages * p.page_size;
+    const long long tiles = std::max(1LL, (cap + c.tile - 1) / c.tile + 1);
+    const double list = (double)B * Hk * (double)row_tiles * (double)tiles;
+    if (list > 1e11) return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
+    const int blocks = (int)std::min((double)c.blocks_per_sm * sms, list);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t need = workspace_of(blocks, p.row_tile, d);
+    void *ws = workspace, *own = nullptr;
+    if (ws) {
+        if (workspace_bytes < need || (uintptr_t)ws % 16)
+            return layer_fail(LA_ERR_INVALID_ARG, who,
+                              "workspace too small or not 16-byte aligned");
+    } else {
+        e = tc_workspace_alloc(&own, need, s);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return layer_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
+        }
+        ws = own;
+    }
+    p.info = static_cast<int4 *>(ws);
+    p.part = reinterpret_cast<float *>(p.info + blocks);
+    e = cudaFuncSetAttribute(c.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
+    if (e == cudaSuccess) {
+        void *args[] = {&p};
+        e = cudaLaunchKernel(c.kern, dim3((unsigned)blocks), dim3(kThreads), args, (size_t)c.smem, s);
+        if (e == cudaSuccess) note_launches(1);
+    }
+    if (e == cudaSuccess && blocks > 1) {
+        const dim3 grid((unsigned)blocks - 1, (unsigned)p.row_tile);
+        const unsigned threads = (unsigned)(d + 31) / 32 * 32;
+        e = dtype == LA_F32
+                ? tchost::launch_dependent(paged_join_kernel<float>, grid, threads, 0, s, p)
+                : tchost::launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, threads, 0, s, p);
+        if (e == cudaSuccess) note_launches(1);
+    }
+    if (own) {
+        const cudaError_t ef = cudaFreeAsync(own, s);
+        if (e == cudaSuccess) e = ef;
+    }
+    return e == cudaSuccess ? LA_OK : layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+}
+
+__attribute__((visibility("default")))
+size_t la_decode_step_paged_workspace_bytes(int Hq, int Hk, int T, int d, la_dtype dtype) {
+    if (Hk < 1 || Hq < 1 || Hq % Hk || T < 1 || d < 1 || d > LA_MAX_D) return 0;
+    if (dtype != LA_F32 && dtype != LA_BF16) return 0;
+    int sms = 0;
+    if (tchost::sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
+    return workspace_of(blocks_of(sms), row_tile_of((long long)(Hq / Hk) * T, dtype), d);
+}
+
+}  // extern "C"

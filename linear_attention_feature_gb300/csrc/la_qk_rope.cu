@@ -23,9 +23,9 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdio>
 
 #include "la_internal.h"
+#include "la_layer.cuh"
 #include "la_tc.h"
 #include "la_tc_host.h"
 #include "la_tc_ptx.cuh"
@@ -61,56 +61,6 @@ struct Params {
     unsigned long long turns[kMaxPairs];  // frequency, 2^-64 turns per position
 };
 
-// V values of T as they lie in memory: one load or store of V * sizeof(T) bytes.
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float &d, float x) { d = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
-
-// bf16 pairs are taken apart and put together as 32-bit words: one instruction
-// a value, and one a pair.
-template <typename T, int V>
-__device__ __forceinline__ void widen(const Pack<T, V> *p, float *e) {
-    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
-        struct alignas(2 * V) Words {
-            unsigned u[V / 2];
-        };
-        const Words w = *reinterpret_cast<const Words *>(p);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            e[2 * i] = __uint_as_float(w.u[i] << 16);
-            e[2 * i + 1] = __uint_as_float(w.u[i] & 0xffff0000u);
-        }
-    } else {
-        const Pack<T, V> a = *p;
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = to_f(a.v[i]);
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void narrow(T *dst, const float *e) {
-    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
-        struct alignas(2 * V) Words {
-            unsigned u[V / 2];
-        } w;
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const __nv_bfloat162 pair = __floats2bfloat162_rn(e[2 * i], e[2 * i + 1]);
-            w.u[i] = reinterpret_cast<const unsigned &>(pair);
-        }
-        *reinterpret_cast<Words *>(dst) = w;
-    } else {
-        Pack<T, V> a;
-#pragma unroll
-        for (int i = 0; i < V; ++i) from_f(a.v[i], e[i]);
-        *reinterpret_cast<Pack<T, V> *>(dst) = a;
-    }
-}
-
 // V values to shared memory, asynchronously (4 bytes or more).  The input is read
 // once: it leaves L2 first (the 2 x 16 x 32768 x 128 call 190 -> 182 us).
 template <typename T, int V>
@@ -137,38 +87,6 @@ __device__ __forceinline__ long long position_of(const Params &p, int b, int n) 
     const long long v = p.pos_bytes == 8 ? static_cast<const long long *>(p.positions)[i]
                                          : static_cast<const int *>(p.positions)[i];
     return v + p.offset;
-}
-
-// cos and sin of pos * turns (2^-64 turns).  The top 32 bits are the angle in 2^-32
-// turns.  For bf16 results the special function unit is exact enough: within [-pi,
-// pi] it is off by 2^-21 at most, 2^-12 of half a step of the result.  Elsewhere (fp32
-// rows, and backward, whose weight gradients are fp32) the angle is taken apart into
-// quarter turns and a rest z of at most half a quarter, exactly, so that rounding the
-// rest to fp32 costs 0.4 u (u = 2^-24; of the whole angle 1.6 u).  sin(pi/4 z) = z (s0
-// + w S(w)) and cos(pi/4 z) = 1 + w C(w), w = z^2; S and C interpolate the exact
-// quotients at the Chebyshev nodes of [0, 1], off by 0.2 u at most, s0 is pi/4 as two
-// fp32 numbers.  Each result is within 1.4 u.
-template <bool kFine>
-__device__ __forceinline__ void turn_of(long long pos, unsigned long long turns, float *c,
-                                        float *s) {
-    const unsigned t = (unsigned)(((unsigned long long)pos * turns) >> 32);
-    if (!kFine) {
-        __sincosf((float)(int)t * 1.46291807926715968e-9f, s, c);  // pi 2^-31
-        return;
-    }
-    const unsigned quarter = (t + 0x20000000u) >> 30;
-    const float z = (float)(int)(t - (quarter << 30)) * 0x1p-29f, w = z * z;
-    float a = fmaf(w, -3.61091152e-5f, 2.49021966e-3f);
-    a = fmaf(w, a, -8.07455033e-2f);
-    a = fmaf(w, a, -2.18556941e-8f);
-    a = fmaf(z, 0.785398185f, z * a);
-    float b = fmaf(w, 3.54195276e-6f, -3.25961388e-4f);
-    b = fmaf(w, b, 1.58543382e-2f);
-    b = fmaf(w, b, -0.308425128f);
-    b = fmaf(w, b, 1.f);
-    const float sine = quarter & 1 ? b : a, cosine = quarter & 1 ? a : b;
-    *s = quarter & 2 ? -sine : sine;
-    *c = (quarter + 1) & 2 ? -cosine : cosine;
 }
 
 // Sum over a row of K S chunks of 2 P / S terms in each of 2^bits lanes, N sums
@@ -695,44 +613,6 @@ qk_weight_kernel(const float *partial, int blocks_q, int blocks, int d, float *d
     dw[i] = t + low;
 }
 
-la_status qk_fail(la_status s, const char *who, const char *msg) {
-    char text[200];
-    std::snprintf(text, sizeof(text), "%s: %s", who, msg);
-    set_last_error(text);
-    return s;
-}
-
-// Whether no two rows of d elements overlap.
-bool rows_disjoint(const la_strides &s, int B, int H, int N, int d) {
-    long long st[3] = {s.b, s.h, s.n}, ex[3] = {B, H, N};
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2 - i; ++j)
-            if (st[j] > st[j + 1]) {
-                std::swap(st[j], st[j + 1]);
-                std::swap(ex[j], ex[j + 1]);
-            }
-    long long span = d;  // elements from the first row's start to the last one's end
-    for (int i = 0; i < 3; ++i) {
-        if (ex[i] <= 1) continue;
-        if (st[i] < span) return false;
-        span += st[i] * (ex[i] - 1);
-    }
-    return true;
-}
-
-// f / (2 pi) mod 1 in 2^-64 turns, |f| <= 1e9.  1 / (2 pi) is the sum of two
-// doubles, so the product is good to about 2^-64 turns for |f| up to a few turns.
-unsigned long long turns_of(double f) {
-    if (f < 0) return 0 - turns_of(-f);
-    const double c = 0.15915494309189535, c_low = -9.839338337591243e-18;
-    const double t = f * c;
-    const double low = std::fma(f, c, -t) + f * c_low;  // |low| < 2^-51 |t| < 2^-23
-    const double part = t - std::floor(t);              // exact, in [0, 1)
-    // a double below 1 is a whole number of 2^-64 from 2^-11 on, and loses less
-    // than one below
-    return (unsigned long long)(part * 0x1p64) + (unsigned long long)(long long)(low * 0x1p64);
-}
-
 bool same(const la_strides &a, const la_strides &b) {
     return a.b == b.b && a.h == b.h && a.n == b.n;
 }
@@ -787,7 +667,7 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
                  cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
-    if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+    if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
     const int v = vector_of(p, 16 / (int)sizeof(T), (int)sizeof(T));
     const int chunks = ((p.d + 1) / 2 + v - 1) / v;  // of a row
     // Pairs / V per lane: more of the small ones, so that a warp takes more rows at a
@@ -817,13 +697,13 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
     const size_t need = sizeof(float) * (size_t)blocks * p.d;
     if (want_dw && workspace) {
         if (workspace_bytes < need || (uintptr_t)workspace % 16)
-            return qk_fail(LA_ERR_INVALID_ARG, who, "workspace too small or not 16-byte aligned");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "workspace too small or not 16-byte aligned");
         p.partial = static_cast<float *>(workspace);
     } else if (want_dw) {
         e = tc_workspace_alloc(&ws, need, stream);
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
-            return qk_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
+            return layer_fail(LA_ERR_NO_MEMORY, who, "workspace allocation");
         }
         p.partial = static_cast<float *>(ws);
     }
@@ -846,7 +726,7 @@ la_status launch(const char *who, Params &p, void *workspace, size_t workspace_b
         const cudaError_t ef = cudaFreeAsync(ws, stream);
         if (e == cudaSuccess) e = ef;
     }
-    return e == cudaSuccess ? LA_OK : qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+    return e == cudaSuccess ? LA_OK : layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
 }
 
 // Checks shared by both directions; fills everything but the tensors.
@@ -854,19 +734,19 @@ la_status qk_common(const char *who, Params &p, const void *q_weight, const void
                     int norm, float eps, const la_rope *rope, int B, int Hq, int Hk, int N, int d,
                     la_dtype dtype, la_dtype weight_dtype) {
     if (B < 0 || N < 0 || Hq < 0 || Hk < 0)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "negative B, Hq, Hk or N");
-    if (d < 1 || d > LA_MAX_D) return qk_fail(LA_ERR_INVALID_ARG, who, "d must be in 1..256");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "negative B, Hq, Hk or N");
+    if (d < 1 || d > LA_MAX_D) return layer_fail(LA_ERR_INVALID_ARG, who, "d must be in 1..256");
     if (dtype != LA_F32 && dtype != LA_BF16)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "unknown dtype");
-    if (norm != 0 && norm != 1) return qk_fail(LA_ERR_INVALID_ARG, who, "norm must be 0 or 1");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unknown dtype");
+    if (norm != 0 && norm != 1) return layer_fail(LA_ERR_INVALID_ARG, who, "norm must be 0 or 1");
     if (norm && !(eps > 0.f && std::isfinite(eps)))
-        return qk_fail(LA_ERR_INVALID_ARG, who, "eps must be positive and finite");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "eps must be positive and finite");
     if (!norm && (q_weight || k_weight))
-        return qk_fail(LA_ERR_INVALID_ARG, who, "weights need norm");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "weights need norm");
     if ((q_weight || k_weight) && weight_dtype != LA_F32 && weight_dtype != LA_BF16)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "unknown weight dtype");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "unknown weight dtype");
     if ((double)B * N * ((double)Hq + Hk) > 1e11)
-        return qk_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
+        return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     p = Params{};
     p.B = B;
     p.N = N;
@@ -882,23 +762,23 @@ la_status qk_common(const char *who, Params &p, const void *q_weight, const void
     if (!rope) return LA_OK;
     const int R = rope->rotary_dim;
     if (R < 0 || R > d || R % 2)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "rotary_dim must be even and in 0..d");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "rotary_dim must be even and in 0..d");
     if (rope->interleaved != 0 && rope->interleaved != 1)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "interleaved must be 0 or 1");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "interleaved must be 0 or 1");
     if (R == 0) return LA_OK;
-    if (!rope->frequencies) return qk_fail(LA_ERR_INVALID_ARG, who, "null frequencies");
+    if (!rope->frequencies) return layer_fail(LA_ERR_INVALID_ARG, who, "null frequencies");
     if (rope->positions) {
         if (rope->position_bytes != 4 && rope->position_bytes != 8)
-            return qk_fail(LA_ERR_INVALID_ARG, who, "position_bytes must be 4 or 8");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "position_bytes must be 4 or 8");
         if (rope->position_stride_b < 0 || rope->position_stride_n < 0)
-            return qk_fail(LA_ERR_INVALID_ARG, who, "negative position stride");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "negative position stride");
         if ((uintptr_t)rope->positions % (uintptr_t)rope->position_bytes)
-            return qk_fail(LA_ERR_INVALID_ARG, who, "unaligned positions");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned positions");
     }
     for (int i = 0; i < R / 2; ++i) {
         const double f = rope->frequencies[i];
         if (!(std::fabs(f) <= 1e9))  // also rejects NaN
-            return qk_fail(LA_ERR_INVALID_ARG, who, "frequencies must lie in [-1e9, 1e9]");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "frequencies must lie in [-1e9, 1e9]");
         p.turns[i] = turns_of(f);
     }
     p.half = R / 2;
@@ -911,18 +791,12 @@ la_status qk_common(const char *who, Params &p, const void *q_weight, const void
     return LA_OK;
 }
 
-la_strides contiguous(int H, int N, int d) {
-    return {(long long)H * N * d, (long long)N * d, d};
-}
-
 // Whether every pointer of a side is a multiple of its element's size.
 bool elements_aligned(const Side &s, la_dtype dtype, la_dtype weight_dtype) {
     const uintptr_t elem = dtype == LA_F32 ? 4 : 2, w = weight_dtype == LA_BF16 ? 2 : 4;
     return (uintptr_t)s.x % elem == 0 && (uintptr_t)s.dy % elem == 0 &&
            (uintptr_t)s.y % elem == 0 && (uintptr_t)s.w % w == 0 && (uintptr_t)s.dw % 4 == 0;
 }
-
-bool negative(const la_strides &s) { return s.b < 0 || s.h < 0 || s.n < 0; }
 
 }  // namespace
 }  // namespace la
@@ -950,19 +824,19 @@ la_status la_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out
         s.y = out[i];
         s.sx = strides ? strides[i] : contiguous(s.H, N, d);
         s.sy = strides ? strides[2 + i] : contiguous(s.H, N, d);
-        if (!s.x || !s.y) return qk_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+        if (!s.x || !s.y) return layer_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
         if (!elements_aligned(s, dtype, weight_dtype))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
         if (negative(s.sx) || negative(s.sy))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "negative stride");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "negative stride");
         if (!rows_disjoint(s.sy, B, s.H, N, d))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
         if (s.y == s.x && !same(s.sx, s.sy))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
     }
     if (B == 0 || N == 0 || Hq + Hk == 0) return LA_OK;
     if (Hq && Hk && (q_out == k || k_out == q || q_out == k_out))
-        return qk_fail(LA_ERR_INVALID_ARG, who, "an output aliases the other side");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "an output aliases the other side");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return dtype == LA_F32 ? launch<float, false>(who, p, nullptr, 0, s)
                            : launch<__nv_bfloat16, false>(who, p, nullptr, 0, s);
@@ -982,9 +856,9 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
                              weight_dtype);
     if (st != LA_OK) return st;
     if (!norm && (dq_weight || dk_weight))
-        return qk_fail(LA_ERR_INVALID_ARG, who, "weight gradients need norm");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "weight gradients need norm");
     if (dq_weight && dq_weight == dk_weight)
-        return qk_fail(LA_ERR_INVALID_ARG, who, "one buffer for both weight gradients");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "one buffer for both weight gradients");
     const void *gin[2] = {dq_out, dk_out}, *xin[2] = {q, k};
     void *out[2] = {dq, dk};
     float *dw[2] = {dq_weight, dk_weight};
@@ -1000,25 +874,25 @@ la_status la_backward_qk_norm_rope(const void *dq_out, const void *dk_out, const
         sd.sy = strides ? strides[4 + i] : contiguous(sd.H, N, d);
         sd.dw = dw[i];
         if (!sd.dy || !sd.y || (norm && !sd.x))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "null tensor pointer");
         if (!elements_aligned(sd, dtype, weight_dtype))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned tensor pointer");
         if (negative(sd.sx) || negative(sd.sy) || negative(sd.sdy))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "negative stride");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "negative stride");
         if (!rows_disjoint(sd.sy, B, sd.H, N, d))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "output rows overlap");
         if (sd.y == sd.dy && !same(sd.sdy, sd.sy))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "in place needs equal strides");
         if (norm && (sd.y == xin[0] || sd.y == xin[1]))
-            return qk_fail(LA_ERR_INVALID_ARG, who, "an output aliases an input");
+            return layer_fail(LA_ERR_INVALID_ARG, who, "an output aliases an input");
     }
     if (B && N && Hq && Hk && (dq == dk_out || dk == dq_out || dq == dk))
-        return qk_fail(LA_ERR_INVALID_ARG, who, "an output aliases the other side");
+        return layer_fail(LA_ERR_INVALID_ARG, who, "an output aliases the other side");
     // a side without rows has a zero weight gradient
     for (int i = 0; i < 2; ++i)
         if (dw[i] && !p.side[i].dw) {
             const cudaError_t e = cudaMemsetAsync(dw[i], 0, sizeof(float) * d, s);
-            if (e != cudaSuccess) return qk_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
+            if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
         }
     if (B == 0 || N == 0 || Hq + Hk == 0) return LA_OK;
     if (!norm) {  // turned back and nothing else: the forward of the other sense

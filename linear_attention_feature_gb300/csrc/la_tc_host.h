@@ -73,10 +73,10 @@ inline cudaError_t sm_count(int *out) {
 // while the kernel before it in the stream, the workspace clear, still runs.
 // The kernel calls griddepcontrol.wait before it touches any global memory.
 template <typename... P, typename... A>
-inline cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block,
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block,
                                     size_t smem, cudaStream_t stream, A &&...args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
