@@ -416,18 +416,21 @@ struct Plan {
     size_t off_dS, off_dz, off_rt, off_part, total;
 };
 
-Plan plan_of(const Shape &sh, int sms, bool back) {
+// The workspace serves either set of kernels: the tensors' strides decide which runs.
+Plan plan_of(const Shape &sh, la_dtype dtype, int sms, bool back) {
     Plan p{};
+    const size_t tc = dtype == LA_BF16 && sh.d <= 128 && sh.d % 8 == 0
+                          ? tc_workspace(sh, sms, back) : 0;
     p.keys = cut_of(sh, sh.M, sms);
     p.queries = cut_of(sh, (long long)sh.G() * sh.N, sms);
     if (!back) {
-        p.total = part_bytes(sh, p.keys);
+        p.total = std::max(tc, part_bytes(sh, p.keys));
         return p;
     }
     p.off_dz = up(sizeof(float) * (size_t)sh.heads() * sh.state());
     p.off_rt = p.off_dz + up(sizeof(float) * (size_t)sh.heads() * sh.d);
     p.off_part = p.off_rt + up(sizeof(float2) * (size_t)sh.B * sh.Hq * sh.N);
-    p.total = p.off_part + part_bytes(sh, p.queries);
+    p.total = std::max(tc, p.off_part + part_bytes(sh, p.queries));
     return p;
 }
 
@@ -532,6 +535,13 @@ template <typename T>
 cudaError_t step(const Shape &sh, Rows q, Rows out, const float *S, const float *z,
                  cudaStream_t s) {
     // more queries than this per state: tiles of them
+    const Rows rows[2] = {q, out};
+    if (sizeof(T) == 2 && (long long)sh.G() * sh.N > 16 && tc_rows(sh, rows, 2, nullptr, 0, S, z)) {
+        int sms = 0;
+        cudaError_t e = tchost::sm_count(&sms);
+        int *status = e == cudaSuccess ? device_status_word(&e) : nullptr;
+        return e == cudaSuccess ? tc_read(sh, q, out, S, z, false, sms, status, s) : e;
+    }
     if ((long long)sh.G() * sh.N > 16)
         return read<T>(sh, q, out, sh.G(), sh.N, S, z, sh.norm, nullptr, s);
     const StepParams p{S, z, q.x, out.x, q.s, out.s, sh.Hk, sh.G(), sh.N, sh.d, sh.phi, sh.norm};
@@ -661,14 +671,22 @@ la_status la_forward_cross(const void *q, const void *k, const void *v, void *ou
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
     if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
-    const Plan pl = plan_of(sh, sms, false);
+    const Plan pl = plan_of(sh, dtype, sms, false);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char *ws;
     void *own;
     st = workspace_of(who, workspace, workspace_bytes, pl.total, &ws, &own, s);
     if (st != LA_OK) return st;
-    e = dtype == LA_F32 ? forward<float>(sh, pl, rq, rk, rv, ro, S, z, ws, s)
-                        : forward<__nv_bfloat16>(sh, pl, rq, rk, rv, ro, S, z, ws, s);
+    const Rows qs[2] = {rq, ro}, ks[2] = {rk, rv};
+    if (dtype == LA_BF16 && M > 0 && tc_rows(sh, qs, N > 0 ? 2 : 0, ks, 2, S, z)) {
+        int *status = device_status_word(&e);
+        if (e == cudaSuccess) e = tc_state(sh, rk, rv, S, z, ws, sms, status, s);
+        if (e == cudaSuccess && N > 0 && Hq > 0)
+            e = tc_read(sh, rq, ro, S, z, true, sms, status, s);
+    } else {
+        e = dtype == LA_F32 ? forward<float>(sh, pl, rq, rk, rv, ro, S, z, ws, s)
+                            : forward<__nv_bfloat16>(sh, pl, rq, rk, rv, ro, S, z, ws, s);
+    }
     return finish(who, e, own, s);
 }
 
@@ -699,12 +717,19 @@ la_status la_backward_cross(const void *dout, const void *q, const void *k, cons
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
     if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
-    const Plan pl = plan_of(sh, sms, true);
+    const Plan pl = plan_of(sh, dtype, sms, true);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char *ws;
     void *own;
     st = workspace_of(who, workspace, workspace_bytes, pl.total, &ws, &own, s);
     if (st != LA_OK) return st;
+    const Rows qs[3] = {r[0], r[1], r[4]}, ks[4] = {r[2], r[3], r[5], r[6]};
+    if (dtype == LA_BF16 && M > 0 && N > 0 && Hq > 0 && tc_rows(sh, qs, 3, ks, 4, S, z)) {
+        int *status = device_status_word(&e);
+        if (e == cudaSuccess)
+            e = tc_backward(sh, r[0], r[1], r[2], r[3], S, z, r[4], r[5], r[6], ws, sms, status, s);
+        return finish(who, e, own, s);
+    }
     e = dtype == LA_F32
             ? backward<float>(sh, pl, r[0], r[1], r[2], r[3], S, z, r[4], r[5], r[6], ws, s)
             : backward<__nv_bfloat16>(sh, pl, r[0], r[1], r[2], r[3], S, z, r[4], r[5], r[6], ws,
@@ -745,7 +770,7 @@ size_t la_cross_workspace_bytes(int B, int Hq, int Hk, int N, int M, int d, la_d
     int sms = 0;
     if (tchost::sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
     const Shape sh{B, Hq, Hk, N, M, d, 1, 1, nullptr};
-    return plan_of(sh, sms, backward != 0).total;
+    return plan_of(sh, dtype, sms, backward != 0).total;
 }
 
 }  // extern "C"

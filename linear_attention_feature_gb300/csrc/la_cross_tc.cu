@@ -1,0 +1,1390 @@
+// Linear cross attention on tcgen05 tensor cores (bf16, head sizes up to 128 that are
+// multiples of 8, rows on 16-byte boundaries); the formulas are in la_cross.cu.
+//
+// Four persistent kernels, one block per SM, each over an equal piece of one list of
+// tiles of tokens (for each sequence and head of keys), whatever the sequences'
+// lengths:
+//   state   S, z of the keys:        [S | z] = phi(K)^T [V | 1]
+//   read    outputs:                 [y den | den] = phi(Q) [S | z]
+//   qgrad   dq, and sums dS, dz:     [G | .] = dY S'^T, [dS | -dz] = psi^T [dY | t]
+//   kgrad   dk and dv:               dphi(K) = V dS^T + dz, dV = phi(K) dS
+// All of them are bound by reading and writing the tokens once; the products run
+// beside that.  A state whose tokens lie in several pieces is left in parts, which
+// join_kernel adds in order.
+//
+// What is rounded to bf16, and why that is enough:
+//   state   phi(k) is kept as two bf16 numbers, high and low (2^-16 of it), since S and
+//           z are results in fp32; V is exact.  The accumulators are emptied into fp32
+//           registers every kGroup tokens: the tensor cores cut off what they add.
+//   read    phi(q) and S as one each, z as two: 2^-8 of a weighted mean's terms, as
+//           much as y's own rounding.
+//   qgrad   r (S dy - t z) is the same for S' = S - z m^T, any m.  With m = S^T z / z.z,
+//           the mean of the values as z weighs it, S' has none of the large common part
+//           that cancels, and one bf16 number is enough.  psi = r phi(q) as one; the
+//           sums of psi and of psi t then go by the same rounded psi, t as two.
+//   kgrad   dS as two for dphi(K), where dS v and dz cancel for values with a mean far
+//           from 0; as one for dV.
+//
+// Roles (352 threads): warp 0 fetches tiles (TMA), warp 1 issues products, warps 2-9
+// take phi, empty TMEM and compute what lies between, warp 10 stores tiles (TMA).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "la_cross.h"
+#include "la_layer.cuh"
+#include "la_tc.h"
+#include "la_tc_common.cuh"
+#include "la_tc_host.h"
+#include "la_tc_ptx.cuh"
+
+namespace la {
+namespace cross {
+namespace {
+
+using namespace la::tc;
+using namespace la::tcc;
+
+constexpr int kThreads = 352, kC0 = 64, kC = 256;  // all; the computing ones: from, number
+constexpr int kWarpsC = kC / 32;
+constexpr int BAR_C = 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr long long kTimeout = 1LL << 32;
+
+struct Params {
+    int B, Hk, G, L, d, phi, norm;  // L: tokens of a head
+    const int *lengths;             // keys' side, or NULL
+    const float *S, *z;             // read, qgrad, kgrad (there dS, dz)
+    float *So, *zo;                 // state, qgrad: whole states
+    float *part;                    // and parts, [blocks][2][d d + d]
+    int4 *info;                     // of each block: the state that its first part
+                                    // continues (-1: none), first and last block of it
+    float zsign;
+    int *status;
+};
+
+__device__ __forceinline__ int tokens_of(const Params &p, int b) {
+    return p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
+}
+
+// A place in the list: tile of head `seg` of sequence b.  F: tiles of a sequence's head.
+template <typename F>
+struct Walk {
+    F count;
+    int B, segs, b, seg, tile, tiles;
+
+    __device__ __forceinline__ Walk(F f, const Params &p, const Piece &x)
+        : count(f), B(p.B), segs(p.Hk), b(x.b), seg(0), tile(0), tiles(1) {
+        if (x.x0 < x.x1) {
+            tiles = count(b);
+            seg = (int)(x.rest / tiles);
+            tile = (int)(x.rest - (long long)seg * tiles);
+        }
+    }
+    __device__ __forceinline__ bool last() const { return tile == tiles - 1; }
+    __device__ __forceinline__ void next() {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++seg < segs) return;
+        seg = 0;
+        do {
+            ++b;
+            tiles = b < B ? count(b) : 1;
+        } while (tiles == 0);
+    }
+};
+template <typename F>
+__device__ __forceinline__ Walk<F> walk(F f, const Params &p, const Piece &x) {
+    return Walk<F>(f, p, x);
+}
+
+// ------------------------------------------------------------------ TMA, 4-D maps
+
+__device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int c,
+                                          int tok, int h, int b, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c), "r"(tok), "r"(h), "r"(b), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void store_tile(const CUtensorMap *map, const void *src, int c, int tok,
+                                           int h, int b) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::
+            "l"(map), "r"(smem_u32(src)), "r"(c), "r"(tok), "r"(h), "r"(b) : "memory");
+}
+
+// ------------------------------------------------------------------ tiles
+
+// Bytes from a tile's start to feature `col` (a multiple of 8) of row `row`; a tile has
+// an atom of 64 features after the other, `rows` rows each.
+__device__ __forceinline__ uint32_t tile_at(int rows, int row, int col) {
+    return (uint32_t)(col >> 6) * (uint32_t)rows * 128u + sw128_offset(row, col & 63);
+}
+
+__device__ __forceinline__ void open8(const uint4 x, float (&e)[8]) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[2 * i] = __uint_as_float(u[i] << 16);
+        e[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 shut8(const float (&e)[8]) {
+    return make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                      pack_bf16x2(e[6], e[7]));
+}
+__device__ __forceinline__ float phi_fast(float x, int phi) {
+    return !phi ? x : x > 0.f ? x + 1.f : exp2f(x * 1.44269504088896341f);
+}
+// phi' from phi: where x > 0, phi > 1 and the slope is 1; elsewhere it is phi itself.
+__device__ __forceinline__ float slope_of_phi(float f, int phi) {
+    return !phi ? 1.f : fminf(f, 1.f);
+}
+// What eight numbers lose as bf16, as bf16.
+__device__ __forceinline__ uint4 low8(const float (&e)[8], const uint4 high) {
+    float h[8], l[8];
+    open8(high, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = e[i] - h[i];
+    return shut8(l);
+}
+
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void sync_compute() { named_bar_sync(BAR_C, kC); }
+
+// Set-up that all kernels share: barriers are initialised by `init` (one thread), TMEM is
+// taken, the dependency on the kernel before is waited for.
+template <typename F>
+__device__ __forceinline__ uint32_t begin(uint32_t *tmem_base, F init) {
+    grid_dep_launch();
+    if (threadIdx.x == 0) {
+        init();
+        fence_mbar_init();
+    }
+    if (threadIdx.x >> 5 == 1) {
+        tmem_alloc(tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    fence_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dep_wait();
+    return *tmem_base;
+}
+__device__ __forceinline__ void end(uint32_t tmem) {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x >> 5 == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+__device__ __forceinline__ void clear(uint8_t *at, int bytes) {
+    for (int i = threadIdx.x; i < bytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(at)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Where a computing thread's results lie in TMEM: lane (row of the product) and half of
+// the columns.
+struct Mine {
+    int et, row, half;
+    uint32_t lane_base;
+    __device__ __forceinline__ explicit Mine(uint32_t tmem) {
+        et = threadIdx.x - kC0;
+        const int quarter = (threadIdx.x >> 5) & 3;
+        row = quarter * 32 + (threadIdx.x & 31);
+        half = et >= kC / 2;
+        lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    }
+};
+
+// The sums of one state that a computing thread holds: DK / 2 columns of row a, and z[a]
+// (half 0).  In TMEM: the first 64 columns, 16 more of which zc are z's, and (DK = 128)
+// the other 64 columns.
+template <int DK>
+struct Sums {
+    static constexpr int kCols = DK / 2;
+    float s[kCols], z;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) s[i] = 0.f;
+        z = 0.f;
+    }
+    template <int kZ>
+    __device__ __forceinline__ void add(const Mine &me, uint32_t base) {
+        const uint32_t at = me.lane_base + base;
+#pragma unroll
+        for (int h = 0; h < kCols / 32; ++h) {
+            uint32_t v[32];
+            tmem_ld32(at + (DK == 128 ? me.half * 80 : me.half * 32) + 32 * h, v);
+            tmem_wait_ld();
+            reg_fence(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[32 * h + e] += u2f(v[e]);
+        }
+        uint32_t v0 = tmem_ld1(at + 64), v1 = 0;
+        if (kZ == 2) v1 = tmem_ld1(at + 65);
+        tmem_wait_ld();
+        reg_fence(v0);
+        reg_fence(v1);
+        z += kZ == 2 ? u2f(v0) + u2f(v1) : u2f(v0);
+    }
+    // To the state itself, or to part `slot` (>= 0) of this block.
+    __device__ __forceinline__ void write(const Params &p, const Mine &me, long long state,
+                                          int slot) const {
+        const int a = me.row, c0 = me.half * kCols;
+        if (a >= p.d) return;
+        const long long dd = (long long)p.d * p.d;
+        float *S, *z_to;
+        if (slot < 0) {
+            S = p.So + state * dd;
+            z_to = p.zo + state * p.d;
+        } else {
+            S = p.part + (2 * (long long)blockIdx.x + slot) * (dd + p.d);
+            z_to = S + dd;
+        }
+        S += (long long)a * p.d + c0;
+#pragma unroll
+        for (int e = 0; e < kCols; e += 4)
+            if (c0 + e < p.d)
+                *reinterpret_cast<float4 *>(S + e) =
+                    make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+        if (me.half == 0) z_to[a] = p.zsign * z;
+    }
+};
+
+// ------------------------------------------------------------------ state
+
+template <int DK>
+struct StateLayout {
+    static constexpr int TOK = DK == 128 ? 64 : 128, KB = DK / 64;
+    static constexpr int ATOM = TOK * 128, TILE = KB * ATOM, STAGE = 2 * TILE, STAGES = 5;
+    static constexpr int OFF_LOW = STAGES * STAGE, OFF_ONE = OFF_LOW + 2 * TILE;
+    static constexpr int OFF_SMALL = OFF_ONE + ATOM;
+    static constexpr int GROUP = 512 / TOK;  // tiles between two emptyings
+};
+struct StateSmall {
+    uint64_t full[5], empty[5], ready[5], low_empty[2], acc_full[2], acc_empty[2], fin;
+    long long plan[kThreads / 32 + 2];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+             const Params p) {
+    using L = StateLayout<DK>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                ~uintptr_t(1023));
+    StateSmall &sm = *reinterpret_cast<StateSmall *>(smem + L::OFF_SMALL);
+    clear(smem + L::OFF_ONE, L::ATOM);
+    __syncthreads();
+    if (threadIdx.x < L::TOK)
+        *reinterpret_cast<uint16_t *>(smem + L::OFF_ONE + sw128_offset(threadIdx.x, 0)) =
+            (uint16_t)(kBf16One2 & 0xFFFFu);
+    const uint32_t tmem = begin(&sm.tmem, [&] {
+        sm.abort = 0;
+        for (int i = 0; i < L::STAGES; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.ready[i], kWarpsC);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.low_empty[i], 1);
+            mbar_init(&sm.acc_full[i], 1);
+            mbar_init(&sm.acc_empty[i], kWarpsC);
+        }
+        mbar_init(&sm.fin, 1);
+    });
+    const Ctx cx{&sm.abort, p.status, kTimeout};
+    auto count = [&](int b) { return max(1, (tokens_of(p, b) + L::TOK - 1) / L::TOK); };
+    const Piece x = find_piece<kThreads>(p.B, p.Hk, 4, count, sm.plan);
+    const int steps = (int)(x.x1 - x.x0);
+    if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    auto w = walk(count, p, x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            int j = 0;
+            for (; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                uint8_t *at = smem + st * L::STAGE;
+                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                for (int a = 0; a < L::KB; ++a) {
+                    load_tile(at + a * L::ATOM, &tk, &sm.full[st], 64 * a, w.tile * L::TOK, w.seg,
+                              w.b, pol);
+                    load_tile(at + L::TILE + a * L::ATOM, &tv, &sm.full[st], 64 * a,
+                              w.tile * L::TOK, w.seg, w.b, pol);
+                }
+            }
+            for (int i = max(0, j - L::STAGES); i < j; ++i)  // all have landed
+                settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t id0 = idesc_bf16(128, 80, 1, 1), id1 = idesc_bf16(128, 64, 1, 1);
+            constexpr uint32_t lboA = DK == 128 ? L::ATOM : 0;  // DK = 64: rows 64.. repeat
+            const uint32_t one = smem_u32(smem + L::OFF_ONE);
+            int g = 0, in = 0;
+            for (int j = 0; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (in == 0) wait_bar_spin(&sm.acc_empty[g & 1], ((g >> 1) & 1) ^ 1, cx);
+                wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
+                tc_fence_after();
+                const uint32_t hi = smem_u32(smem + st * L::STAGE), vb = hi + L::TILE;
+                const uint32_t lo = smem_u32(smem + L::OFF_LOW + (j & 1) * L::TILE);
+                const uint32_t acc = tmem + (g & 1) * 160;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < L::TOK / 16; ++ks) {
+                        const uint64_t a = sdesc_sw128((part ? lo : hi) + ks * 2048, lboA, 1024);
+                        const uint32_t more = in > 0 || part > 0 || ks > 0;
+                        mma_ss(acc, a, sdesc_sw128(vb + ks * 2048, one - vb, 1024), id0, more);
+                        if (DK == 128)
+                            mma_ss(acc + 80, a, sdesc_sw128(vb + L::ATOM + ks * 2048, 0, 1024),
+                                   id1, more);
+                    }
+                mma_commit(&sm.empty[st]);
+                mma_commit(&sm.low_empty[j & 1]);
+                if (++in == L::GROUP || w.last() || j == steps - 1) {
+                    mma_commit(&sm.acc_full[g & 1]);
+                    ++g;
+                    in = 0;
+                }
+            }
+            mma_commit(&sm.fin);
+            settle_wait(&sm.fin, 0);
+        }
+    } else if (warp < 2 + kWarpsC) {
+        const Mine me(tmem);
+        constexpr int kParts = kC / L::TOK, kChunks = DK / 8 / kParts;
+        const int row = me.et % L::TOK, part = me.et / L::TOK;
+        Sums<DK> acc;
+        acc.clear();
+        int g = 0, in = 0, first = w.tile;
+        // a group whose products are under way
+        bool pending = false, whole = false;
+        int slot = 0;
+        long long state = 0;
+        auto drain = [&]() {
+            wait_bar(&sm.acc_full[(g - 1) & 1], ((g - 1) >> 1) & 1, cx);
+            tc_fence_after();
+            acc.template add<1>(me, ((g - 1) & 1) * 160);
+            tc_fence_before();
+            arrive_warp(&sm.acc_empty[(g - 1) & 1]);
+            if (whole) {
+                acc.write(p, me, state, slot);
+                acc.clear();
+            }
+            pending = false;
+        };
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES, len = tokens_of(p, w.b) - w.tile * L::TOK;
+            wait_bar(&sm.low_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
+            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+            uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+            uint8_t *lt = smem + L::OFF_LOW + (j & 1) * L::TILE;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int col = (part * kChunks + i) * 8;
+                const uint32_t at = tile_at(L::TOK, row, col);
+                float e[8];
+                open8(*reinterpret_cast<const uint4 *>(kt + at), e);
+                const bool ok = row < len && col < p.d;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) e[q] = ok ? phi_fast(e[q], p.phi) : 0.f;
+                const uint4 high = shut8(e);
+                *reinterpret_cast<uint4 *>(kt + at) = high;
+                *reinterpret_cast<uint4 *>(lt + at) = low8(e, high);
+                if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            arrive_warp(&sm.ready[st]);
+            if (pending) drain();
+            if (++in == L::GROUP || w.last() || j == steps - 1) {
+                const bool began = first > 0, ends = w.last();
+                pending = true;
+                whole = ends || j == steps - 1;
+                slot = began ? 0 : ends ? -1 : 1;
+                state = (long long)w.b * p.Hk + w.seg;
+                if (whole) {
+                    if (began && me.et == 0) {
+                        const long long s0 = x.x0 + j - w.tile;
+                        p.info[blockIdx.x] =
+                            make_int4((int)state, x.of(s0), x.of(s0 + w.tiles - 1), 0);
+                    }
+                    first = 0;
+                }
+                ++g;
+                in = 0;
+            }
+        }
+        if (pending) drain();
+    }
+    end(tmem);
+}
+
+// Adds the parts of states that lie in several blocks: blockIdx.y + 1 is the first block
+// that continues a state.
+__global__ void __launch_bounds__(256) join_parts_kernel(const Params p) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int i = blockIdx.y + 1;
+    const int4 info = p.info[i];
+    if (info.x < 0 || info.y != i - 1) return;
+    const long long dd = (long long)p.d * p.d, all = dd + p.d;
+    const long long e = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (e >= all) return;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int q = info.y; q <= info.z; ++q) {
+        const float4 u = __ldcg(
+            reinterpret_cast<const float4 *>(p.part + (2 * (long long)q + (q == info.y)) * all + e));
+        t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
+    }
+    float *to = e < dd ? p.So + info.x * dd + e : p.zo + (long long)info.x * p.d + (e - dd);
+    *reinterpret_cast<float4 *>(to) = t;
+}
+
+// ------------------------------------------------------------------ read
+
+template <int DK>
+struct ReadLayout {
+    static constexpr int KB = DK / 64, TILE = KB * 16384, STAGES = DK == 128 ? 4 : 8;
+    static constexpr int SATOM = DK * 128;  // rows are features a
+    static constexpr int OFF_S = STAGES * TILE, OFF_Z = OFF_S + KB * SATOM;
+    static constexpr int OFF_SMALL = OFF_Z + SATOM;
+};
+struct ReadSmall {
+    uint64_t full[8], empty[8], ready[8], out[8], s_ready, o_full[2], o_empty[2], fin;
+    long long plan[kThreads / 32 + 2];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap to,
+            const Params p) {
+    using L = ReadLayout<DK>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                ~uintptr_t(1023));
+    ReadSmall &sm = *reinterpret_cast<ReadSmall *>(smem + L::OFF_SMALL);
+    clear(smem + L::OFF_Z, L::SATOM);
+    const int tiles = (p.L + 127) / 128;  // of a head of queries
+    const uint32_t tmem = begin(&sm.tmem, [&] {
+        sm.abort = 0;
+        for (int i = 0; i < L::STAGES; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.ready[i], kWarpsC);
+            mbar_init(&sm.out[i], kWarpsC);
+        }
+        mbar_init(&sm.s_ready, kWarpsC);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.o_empty[i], kWarpsC);
+        }
+        mbar_init(&sm.fin, 1);
+    });
+    const Ctx cx{&sm.abort, p.status, kTimeout};
+    auto count = [&](int) { return p.G * tiles; };
+    const Piece x = find_piece<kThreads>(p.B, p.Hk, 1, count, sm.plan);
+    const int steps = (int)(x.x1 - x.x0);
+    auto w = walk(count, p, x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            int j = 0;
+            for (; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES, g = w.tile / tiles;
+                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                mbar_arrive_expect_tx(&sm.full[st], L::TILE);
+                for (int a = 0; a < L::KB; ++a)
+                    load_tile(smem + st * L::TILE + a * 16384, &tq, &sm.full[st], 64 * a,
+                              (w.tile - g * tiles) * 128, w.seg * p.G + g, w.b, pol);
+            }
+            for (int i = max(0, j - L::STAGES); i < j; ++i)
+                settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t id0 = idesc_bf16(128, 80, 0, 1), id1 = idesc_bf16(128, 64, 0, 1);
+            const uint32_t sb = smem_u32(smem + L::OFF_S), zb = smem_u32(smem + L::OFF_Z);
+            int states = 0;
+            for (int j = 0; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (j == 0 || w.tile == 0) wait_bar_spin(&sm.s_ready, states++ & 1, cx);
+                wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
+                wait_bar_spin(&sm.o_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
+                tc_fence_after();
+                const uint32_t qb = smem_u32(smem + st * L::TILE), o = tmem + (j & 1) * 160;
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    const uint64_t a = sdesc_sw128(qb + kmajor_off(ks, 16384), 16, 1024);
+                    mma_ss(o, a, sdesc_sw128(sb + ks * 2048, zb - sb, 1024), id0, ks > 0);
+                    if (DK == 128)
+                        mma_ss(o + 80, a, sdesc_sw128(sb + L::SATOM + ks * 2048, 0, 1024), id1,
+                               ks > 0);
+                }
+                mma_commit(&sm.o_full[j & 1]);
+            }
+            mma_commit(&sm.fin);
+            settle_wait(&sm.fin, 0);
+        }
+    } else if (warp < 2 + kWarpsC) {
+        const Mine me(tmem);
+        constexpr int kChunks = DK / 16;
+        auto output = [&](int j) {
+            const int st = j % L::STAGES;
+            wait_bar(&sm.o_full[j & 1], (j >> 1) & 1, cx);
+            tc_fence_after();
+            const uint32_t o = me.lane_base + (j & 1) * 160;
+            float inv = 1.f;
+            if (p.norm) {
+                uint32_t d0 = tmem_ld1(o + 64), d1 = tmem_ld1(o + 65);
+                tmem_wait_ld();
+                reg_fence(d0);
+                reg_fence(d1);
+                const float den = u2f(d0) + u2f(d1);
+                inv = den == 0.f ? 0.f : 1.f / den;
+            }
+            uint4 y[DK / 16];
+#pragma unroll
+            for (int h = 0; h < DK / 64; ++h) {
+                uint32_t v[32];
+                tmem_ld32(o + me.half * (DK == 128 ? 80 : 32) + 32 * h, v);
+                tmem_wait_ld();
+                reg_fence(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float e[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) e[q] = u2f(v[8 * i + q]) * inv;
+                    y[4 * h + i] = shut8(e);
+                }
+            }
+            tc_fence_before();
+            arrive_warp(&sm.o_empty[j & 1]);
+            uint8_t *tile = smem + st * L::TILE;
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
+                *reinterpret_cast<uint4 *>(tile + tile_at(128, me.row, me.half * (DK / 2) + 8 * i)) =
+                    y[i];
+            fence_async_shared();
+            arrive_warp(&sm.out[st]);
+        };
+        const int row = me.et & 127, part = me.et >> 7;
+        bool pending = false;
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES;
+            if (j == 0 || w.tile == 0) {
+                // another state: the products with the one before are done once the last
+                // of their outputs has been taken by all
+                if (pending) output(j - 1);
+                pending = false;
+                sync_compute();
+                const long long state = (long long)w.b * p.Hk + w.seg;
+                const float *S = p.S + state * p.d * p.d;
+                for (int i = me.et; i < DK * DK / 8; i += kC) {
+                    const int a = i / (DK / 8), c = i % (DK / 8) * 8;
+                    float e[8] = {};
+                    if (a < p.d && c < p.d) {
+                        const float4 *s4 = reinterpret_cast<const float4 *>(S + (long long)a * p.d + c);
+                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
+                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
+                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
+                    }
+                    *reinterpret_cast<uint4 *>(smem + L::OFF_S + tile_at(DK, a, c)) = shut8(e);
+                }
+                if (me.et < DK) {
+                    const float z = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                    const float high = __bfloat162float(__float2bfloat16_rn(z));
+                    *reinterpret_cast<uint32_t *>(smem + L::OFF_Z + sw128_offset(me.et, 0)) =
+                        pack_bf16x2(z, z - high);
+                }
+                fence_async_shared();
+                arrive_warp(&sm.s_ready);
+            }
+            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+            uint8_t *tile = smem + st * L::TILE;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int col = (part * kChunks + i) * 8;
+                uint4 *at = reinterpret_cast<uint4 *>(tile + tile_at(128, row, col));
+                float e[8];
+                open8(*at, e);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) e[q] = col < p.d ? phi_fast(e[q], p.phi) : 0.f;
+                *at = shut8(e);
+            }
+            fence_async_shared();
+            arrive_warp(&sm.ready[st]);
+            if (pending) output(j - 1);
+            pending = true;
+        }
+        if (pending) output(steps - 1);
+    } else if (lane == 0) {
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES, g = w.tile / tiles;
+            if (!wait_bar(&sm.out[st], (j / L::STAGES) & 1, cx)) break;
+            for (int a = 0; a < L::KB; ++a)
+                if (64 * a < p.d)
+                    store_tile(&to, smem + st * L::TILE + a * 16384, 64 * a,
+                               (w.tile - g * tiles) * 128, w.seg * p.G + g, w.b);
+            tma_store_commit();
+            tma_store_wait_read<0>();
+            mbar_arrive(&sm.empty[st]);
+        }
+        tma_store_wait_all<0>();
+    }
+    end(tmem);
+}
+
+// ------------------------------------------------------------------ qgrad
+
+template <int DK>
+struct QLayout {
+    static constexpr int KB = DK / 64, TILE = KB * 16384, STAGE = 2 * TILE;
+    static constexpr int STAGES = DK == 128 ? 2 : 4;
+    static constexpr int SROWS = DK + 16, SATOM = SROWS * 128;  // rows of S', then m
+    static constexpr int OFF_T = STAGES * STAGE, OFF_S = OFF_T + 16384;
+    static constexpr int OFF_OUT = (OFF_S + KB * SATOM + 1023) / 1024 * 1024;
+    static constexpr int OFF_SMALL = OFF_OUT + TILE;
+};
+struct QSmall {
+    uint64_t full[4], empty[4], psi[4], s_ready, g_full[2], g_empty[2], t_free, ds_full, ds_empty;
+    uint64_t out_full, out_empty, fin;
+    long long plan[kThreads / 32 + 2];
+    float z[128], m[256], zz[8];
+    float2 red[2][256];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdy,
+             const __grid_constant__ CUtensorMap tdq, const Params p) {
+    using L = QLayout<DK>;
+    constexpr uint32_t kG = 0, kGStep = 144, kDs = 288;  // TMEM columns
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                ~uintptr_t(1023));
+    QSmall &sm = *reinterpret_cast<QSmall *>(smem + L::OFF_SMALL);
+    clear(smem + L::OFF_T, 16384);
+    clear(smem + L::OFF_S, L::KB * L::SATOM);
+    const int tiles = (p.L + 127) / 128;
+    const uint32_t tmem = begin(&sm.tmem, [&] {
+        sm.abort = 0;
+        for (int i = 0; i < L::STAGES; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.psi[i], kWarpsC);
+        }
+        mbar_init(&sm.s_ready, kWarpsC);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.g_full[i], 1);
+            mbar_init(&sm.g_empty[i], kWarpsC);
+        }
+        mbar_init(&sm.t_free, 1);
+        mbar_init(&sm.ds_full, 1);
+        mbar_init(&sm.ds_empty, kWarpsC);
+        mbar_init(&sm.out_full, kWarpsC);
+        mbar_init(&sm.out_empty, 1);
+        mbar_init(&sm.fin, 1);
+    });
+    const Ctx cx{&sm.abort, p.status, kTimeout};
+    auto count = [&](int) { return p.G * tiles; };
+    const Piece x = find_piece<kThreads>(p.B, p.Hk, 2, count, sm.plan);
+    const int steps = (int)(x.x1 - x.x0);
+    if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    auto w = walk(count, p, x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            int j = 0;
+            for (; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES, g = w.tile / tiles;
+                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                uint8_t *at = smem + st * L::STAGE;
+                const int tok = (w.tile - g * tiles) * 128, h = w.seg * p.G + g;
+                for (int a = 0; a < L::KB; ++a) {
+                    load_tile(at + L::TILE + a * 16384, &tdy, &sm.full[st], 64 * a, tok, h, w.b, pol);
+                    load_tile(at + a * 16384, &tq, &sm.full[st], 64 * a, tok, h, w.b, pol);
+                }
+            }
+            for (int i = max(0, j - L::STAGES); i < j; ++i)
+                settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idG = idesc_bf16(128, DK + 16, 0, 0);
+            constexpr uint32_t id0 = idesc_bf16(128, 80, 1, 1), id1 = idesc_bf16(128, 64, 1, 1);
+            constexpr uint32_t lboA = DK == 128 ? 16384 : 0;
+            const uint32_t sb = smem_u32(smem + L::OFF_S), tb = smem_u32(smem + L::OFF_T);
+            int states = 0, ended = 0;
+            bool first = true, last = false;  // of the tile before: in its state's piece
+            // the sums of tile j, once psi and t are there
+            auto sums = [&](int j, bool first, bool last) {
+                const int st = j % L::STAGES;
+                if (first) wait_bar_spin(&sm.ds_empty, (ended & 1) ^ 1, cx);
+                wait_bar_spin(&sm.psi[st], (j / L::STAGES) & 1, cx);
+                tc_fence_after();
+                const uint32_t qb = smem_u32(smem + st * L::STAGE), yb = qb + L::TILE;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t a = sdesc_sw128(qb + ks * 2048, lboA, 1024);
+                    const uint32_t more = !first || ks > 0;
+                    mma_ss(tmem + kDs, a, sdesc_sw128(yb + ks * 2048, tb - yb, 1024), id0, more);
+                    if (DK == 128)
+                        mma_ss(tmem + kDs + 80, a, sdesc_sw128(yb + 16384 + ks * 2048, 0, 1024),
+                               id1, more);
+                }
+                mma_commit(&sm.empty[st]);
+                mma_commit(&sm.t_free);
+                if (last) {
+                    mma_commit(&sm.ds_full);
+                    ++ended;
+                }
+            };
+            for (int j = 0; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (j == 0 || w.tile == 0) wait_bar_spin(&sm.s_ready, states++ & 1, cx);
+                wait_bar_spin(&sm.full[st], (j / L::STAGES) & 1, cx);
+                wait_bar_spin(&sm.g_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
+                tc_fence_after();
+                const uint32_t yb = smem_u32(smem + st * L::STAGE + L::TILE);
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_ss(tmem + kG + (j & 1) * kGStep,
+                           sdesc_sw128(yb + kmajor_off(ks, 16384), 16, 1024),
+                           sdesc_sw128(sb + kmajor_off(ks, L::SATOM), 16, 1024), idG, ks > 0);
+                mma_commit(&sm.g_full[j & 1]);
+                if (j > 0) sums(j - 1, first, last);
+                first = j == 0 || w.tile == 0;
+                last = w.last() || j == steps - 1;
+            }
+            if (steps > 0) sums(steps - 1, first, last);
+            mma_commit(&sm.fin);
+            settle_wait(&sm.fin, 0);
+        }
+    } else if (warp < 2 + kWarpsC) {
+        const Mine me(tmem);
+        constexpr int kHalf = DK / 2;
+        const int f0 = me.half * kHalf;  // this thread's features of its row
+        int first_tile = w.tile, drained = 0;
+        auto drain = [&](long long state, int slot) {  // a state's sums are complete
+            wait_bar(&sm.ds_full, drained & 1, cx);
+            ++drained;
+            tc_fence_after();
+            Sums<DK> acc;
+            acc.clear();
+            acc.template add<2>(me, kDs);
+            tc_fence_before();
+            arrive_warp(&sm.ds_empty);
+            acc.write(p, me, state, slot);
+        };
+        long long old_state = -1;
+        int old_slot = 0;
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES;
+            const long long state = (long long)w.b * p.Hk + w.seg;
+            if (j == 0 || w.tile == 0) {
+                sync_compute();  // all are through with the state before
+                const float *S = p.S + state * p.d * p.d;
+                // m = S^T z / z.z, two threads per column
+                if (me.et < 128) sm.z[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                sync_compute();
+                float zz = 0.f;
+                for (int a = 0; a < p.d; ++a) zz = fmaf(sm.z[a], sm.z[a], zz);
+                const int c = me.et & 127, a0 = (me.et >> 7) * ((p.d + 1) / 2);
+                const int a1 = min(a0 + (p.d + 1) / 2, p.d);
+                float t = 0.f;
+                if (c < p.d && p.norm)
+#pragma unroll 8
+                    for (int a = a0; a < a1; ++a)
+                        t = fmaf(__ldcg(S + (long long)a * p.d + c), sm.z[a], t);
+                sm.m[me.et] = t;
+                sync_compute();
+                const float over = zz > 0.f && p.norm ? 1.f / zz : 0.f;
+                const float mc = (sm.m[c] + sm.m[c + 128]) * over;
+                sync_compute();
+                if (me.et < 128) sm.m[me.et] = mc;
+                sync_compute();
+                for (int i = me.et; i < DK * DK / 8; i += kC) {
+                    const int a = i / (DK / 8), c8 = i % (DK / 8) * 8;
+                    float e[8] = {};
+                    if (a < p.d && c8 < p.d) {
+                        const float4 *s4 =
+                            reinterpret_cast<const float4 *>(S + (long long)a * p.d + c8);
+                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
+                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
+                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
+                        const float z = sm.z[a];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) e[q] = fmaf(-z, sm.m[c8 + q], e[q]);
+                    }
+                    *reinterpret_cast<uint4 *>(smem + L::OFF_S + tile_at(L::SROWS, a, c8)) = shut8(e);
+                }
+                if (me.et < DK) {  // row DK: m, row DK + 1: what it loses
+                    const float m = me.et < p.d ? sm.m[me.et] : 0.f;
+                    const __nv_bfloat16 high = __float2bfloat16_rn(m);
+                    uint8_t *at = smem + L::OFF_S + (me.et >> 6) * L::SATOM;
+                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(DK, me.et & 63)) = high;
+                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(DK + 1, me.et & 63)) =
+                        __float2bfloat16_rn(m - __bfloat162float(high));
+                }
+                fence_async_shared();
+                arrive_warp(&sm.s_ready);
+                if (old_state >= 0) drain(old_state, old_slot);
+                first_tile = w.tile;
+            }
+            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+            uint8_t *qt = smem + st * L::STAGE;
+            // phi(q), its product with z and, behind the products' end, with G
+            float f[kHalf], den = 0.f, dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < kHalf / 8; ++i) {
+                float e[8];
+                open8(*reinterpret_cast<const uint4 *>(qt + tile_at(128, me.row, f0 + 8 * i)), e);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    f[8 * i + q] = f0 + 8 * i < p.d ? phi_fast(e[q], p.phi) : 0.f;
+                    den = fmaf(f[8 * i + q], sm.z[f0 + 8 * i + q], den);
+                }
+            }
+            wait_bar(&sm.g_full[j & 1], (j >> 1) & 1, cx);
+            tc_fence_after();
+            const uint32_t gb = me.lane_base + kG + (j & 1) * kGStep;
+#pragma unroll
+            for (int h = 0; h < kHalf / 32; ++h) {
+                uint32_t v[32];
+                tmem_ld32(gb + f0 + 32 * h, v);
+                tmem_wait_ld();
+                reg_fence(v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) dot = fmaf(f[32 * h + e], u2f(v[e]), dot);
+            }
+            uint32_t m0 = tmem_ld1(gb + DK), m1 = tmem_ld1(gb + DK + 1);
+            tmem_wait_ld();
+            reg_fence(m0);
+            reg_fence(m1);
+            sm.red[j & 1][me.half * 128 + me.row] = make_float2(den, dot);
+            // the staging tile and t's column are free again
+            wait_bar(&sm.out_empty, (j & 1) ^ 1, cx);
+            wait_bar(&sm.t_free, (j & 1) ^ 1, cx);
+            sync_compute();
+            const float2 r0 = sm.red[j & 1][me.row], r1 = sm.red[j & 1][128 + me.row];
+            den = r0.x + r1.x;
+            dot = r0.y + r1.y;
+            float r = 1.f, t = 0.f, t_all = 0.f;
+            if (p.norm) {
+                r = den == 0.f ? 0.f : 1.f / den;
+                t = dot * r;
+                // of an unused row r is 0, and so is what it adds
+                t_all = t + u2f(m0) + u2f(m1);
+            }
+            uint8_t *ot = smem + L::OFF_OUT;
+#pragma unroll
+            for (int h = 0; h < kHalf / 32; ++h) {
+                uint32_t v[32];
+                tmem_ld32(gb + f0 + 32 * h, v);
+                tmem_wait_ld();
+                reg_fence(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float g[8], s[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int e = 32 * h + 8 * i + q;
+                        g[q] = r * fmaf(-t, sm.z[f0 + e], u2f(v[8 * i + q])) *
+                               slope_of_phi(f[e], p.phi);
+                        s[q] = r * f[e];
+                    }
+                    const uint32_t at = tile_at(128, me.row, f0 + 32 * h + 8 * i);
+                    *reinterpret_cast<uint4 *>(ot + at) = shut8(g);
+                    *reinterpret_cast<uint4 *>(qt + at) = shut8(s);
+                }
+            }
+            if (me.half == 0) {
+                const float high = __bfloat162float(__float2bfloat16_rn(t_all));
+                *reinterpret_cast<uint32_t *>(smem + L::OFF_T + sw128_offset(me.row, 0)) =
+                    pack_bf16x2(t_all, t_all - high);
+            }
+            tc_fence_before();
+            arrive_warp(&sm.g_empty[j & 1]);
+            fence_async_shared();
+            arrive_warp(&sm.psi[st]);
+            if (lane == 0) mbar_arrive(&sm.out_full);
+            if (w.last() || j == steps - 1) {
+                const bool began = first_tile > 0, ends = w.last();
+                old_state = state;
+                old_slot = began ? 0 : ends ? -1 : 1;
+                if (began && me.et == 0) {
+                    const long long s0 = x.x0 + j - w.tile;
+                    p.info[blockIdx.x] =
+                        make_int4((int)state, x.of(s0), x.of(s0 + w.tiles - 1), 0);
+                }
+            }
+        }
+        if (old_state >= 0) drain(old_state, old_slot);
+    } else if (lane == 0) {
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int g = w.tile / tiles;
+            if (!wait_bar(&sm.out_full, j & 1, cx)) break;
+            for (int a = 0; a < L::KB; ++a)
+                if (64 * a < p.d)
+                    store_tile(&tdq, smem + L::OFF_OUT + a * 16384, 64 * a,
+                               (w.tile - g * tiles) * 128, w.seg * p.G + g, w.b);
+            tma_store_commit();
+            tma_store_wait_read<0>();
+            mbar_arrive(&sm.out_empty);
+        }
+        tma_store_wait_all<0>();
+    }
+    end(tmem);
+}
+
+// ------------------------------------------------------------------ kgrad
+
+template <int DK>
+struct KLayout {
+    static constexpr int KB = DK / 64, TILE = KB * 16384, STAGE = 2 * TILE;
+    static constexpr int STAGES = DK == 128 ? 2 : 4;
+    static constexpr int SATOM = DK * 128, SBLK = KB * SATOM;
+    static constexpr int OFF_S = STAGES * STAGE, OFF_SMALL = OFF_S + 2 * SBLK;
+    static_assert(2 * SBLK >= 16384, "a tile of zeros fits");
+};
+struct KSmall {
+    uint64_t full[4], empty[4], ready[4], out[4], s_ready, d_full[2], d_empty[2], fin;
+    long long plan[kThreads / 32 + 2];
+    float dz[128];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+             const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
+             const Params p) {
+    using L = KLayout<DK>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                ~uintptr_t(1023));
+    KSmall &sm = *reinterpret_cast<KSmall *>(smem + L::OFF_SMALL);
+    const uint32_t tmem = begin(&sm.tmem, [&] {
+        sm.abort = 0;
+        for (int i = 0; i < L::STAGES; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.ready[i], kWarpsC);
+            mbar_init(&sm.out[i], kWarpsC);
+        }
+        mbar_init(&sm.s_ready, kWarpsC);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.d_full[i], 1);
+            mbar_init(&sm.d_empty[i], kWarpsC);
+        }
+        mbar_init(&sm.fin, 1);
+    });
+    const Ctx cx{&sm.abort, p.status, kTimeout};
+    auto count = [&](int b) { return (tokens_of(p, b) + 127) / 128; };
+    const Piece x = find_piece<kThreads>(p.B, p.Hk, 1, count, sm.plan);
+    const int steps = (int)(x.x1 - x.x0);
+    auto w = walk(count, p, x);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_first();
+            int j = 0;
+            for (; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                uint8_t *at = smem + st * L::STAGE;
+                for (int a = 0; a < L::KB; ++a) {
+                    load_tile(at + a * 16384, &tk, &sm.full[st], 64 * a, w.tile * 128, w.seg, w.b, pol);
+                    load_tile(at + L::TILE + a * 16384, &tv, &sm.full[st], 64 * a, w.tile * 128,
+                              w.seg, w.b, pol);
+                }
+            }
+            for (int i = max(0, j - L::STAGES); i < j; ++i)
+                settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idK = idesc_bf16(128, DK, 0, 0), idV = idesc_bf16(128, DK, 0, 1);
+            const uint32_t hi = smem_u32(smem + L::OFF_S), lo = hi + L::SBLK;
+            int states = 0;
+            for (int j = 0; j < steps; ++j, w.next()) {
+                const int st = j % L::STAGES;
+                if (j == 0 || w.tile == 0) wait_bar_spin(&sm.s_ready, states++ & 1, cx);
+                wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
+                wait_bar_spin(&sm.d_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
+                tc_fence_after();
+                const uint32_t kb = smem_u32(smem + st * L::STAGE), vb = kb + L::TILE;
+                const uint32_t dk = tmem + (j & 1) * 2 * DK, dv = dk + DK;
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                    const uint64_t a = sdesc_sw128(vb + kmajor_off(ks, 16384), 16, 1024);
+                    mma_ss(dk, a, sdesc_sw128(hi + kmajor_off(ks, L::SATOM), 16, 1024), idK, ks > 0);
+                    mma_ss(dk, a, sdesc_sw128(lo + kmajor_off(ks, L::SATOM), 16, 1024), idK, 1);
+                }
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_ss(dv, sdesc_sw128(kb + kmajor_off(ks, 16384), 16, 1024),
+                           sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
+                mma_commit(&sm.d_full[j & 1]);
+            }
+            mma_commit(&sm.fin);
+            settle_wait(&sm.fin, 0);
+        }
+    } else if (warp < 2 + kWarpsC) {
+        const Mine me(tmem);
+        constexpr int kHalf = DK / 2, kChunks = DK / 16;
+        const int f0 = me.half * kHalf;
+        auto output = [&](int j, int len) {
+            const int st = j % L::STAGES;
+            wait_bar(&sm.d_full[j & 1], (j >> 1) & 1, cx);
+            tc_fence_after();
+            const uint32_t dk = me.lane_base + (j & 1) * 2 * DK + f0;
+            uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+#pragma unroll
+            for (int h = 0; h < kHalf / 32; ++h) {
+                uint32_t v[32], u[32];
+                tmem_ld32(dk + 32 * h, v);
+                tmem_ld32(dk + DK + 32 * h, u);
+                tmem_wait_ld();
+                reg_fence(v);
+                reg_fence(u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t at = tile_at(128, me.row, f0 + 32 * h + 8 * i);
+                    float f[8], g[8], o[8];
+                    open8(*reinterpret_cast<const uint4 *>(kt + at), f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float s = slope_of_phi(f[q], p.phi);
+                        g[q] = me.row < len
+                                   ? (u2f(v[8 * i + q]) + sm.dz[f0 + 32 * h + 8 * i + q]) * s
+                                   : 0.f;
+                        o[q] = u2f(u[8 * i + q]);
+                    }
+                    *reinterpret_cast<uint4 *>(kt + at) = shut8(g);
+                    *reinterpret_cast<uint4 *>(vt + at) = shut8(o);
+                }
+            }
+            tc_fence_before();
+            arrive_warp(&sm.d_empty[j & 1]);
+            fence_async_shared();
+            arrive_warp(&sm.out[st]);
+        };
+        const int row = me.et & 127, part = me.et >> 7;
+        bool pending = false;
+        int len = 0, len_before = 0;
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES;
+            len_before = len;
+            len = tokens_of(p, w.b) - w.tile * 128;
+            if (j == 0 || w.tile == 0) {
+                if (pending) output(j - 1, len_before);
+                pending = false;
+                sync_compute();
+                const long long state = (long long)w.b * p.Hk + w.seg;
+                const float *S = p.S + state * p.d * p.d;
+                for (int i = me.et; i < DK * DK / 8; i += kC) {
+                    const int a = i / (DK / 8), c = i % (DK / 8) * 8;
+                    float e[8] = {};
+                    if (a < p.d && c < p.d) {
+                        const float4 *s4 = reinterpret_cast<const float4 *>(S + (long long)a * p.d + c);
+                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
+                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
+                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
+                    }
+                    uint8_t *at = smem + L::OFF_S + tile_at(DK, a, c);
+                    const uint4 high = shut8(e);
+                    *reinterpret_cast<uint4 *>(at) = high;
+                    *reinterpret_cast<uint4 *>(at + L::SBLK) = low8(e, high);
+                }
+                if (me.et < 128)
+                    sm.dz[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                fence_async_shared();
+                sync_compute();
+                arrive_warp(&sm.s_ready);
+            }
+            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+            uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int col = (part * kChunks + i) * 8;
+                const uint32_t at = tile_at(128, row, col);
+                float e[8];
+                open8(*reinterpret_cast<const uint4 *>(kt + at), e);
+                const bool ok = row < len && col < p.d;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) e[q] = ok ? phi_fast(e[q], p.phi) : 0.f;
+                *reinterpret_cast<uint4 *>(kt + at) = shut8(e);
+                if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            arrive_warp(&sm.ready[st]);
+            if (pending) output(j - 1, len_before);
+            pending = true;
+        }
+        if (pending) output(steps - 1, len);
+    } else if (lane == 0) {
+        for (int j = 0; j < steps; ++j, w.next()) {
+            const int st = j % L::STAGES;
+            if (!wait_bar(&sm.out[st], (j / L::STAGES) & 1, cx)) break;
+            uint8_t *at = smem + st * L::STAGE;
+            for (int a = 0; a < L::KB; ++a)
+                if (64 * a < p.d) {
+                    store_tile(&tdk, at + a * 16384, 64 * a, w.tile * 128, w.seg, w.b);
+                    store_tile(&tdv, at + L::TILE + a * 16384, 64 * a, w.tile * 128, w.seg, w.b);
+                }
+            tma_store_commit();
+            tma_store_wait_read<0>();
+            mbar_arrive(&sm.empty[st]);
+        }
+    }
+    // tiles that are padding alone: zeros
+    __syncthreads();
+    if (p.lengths) {
+        const int all = (p.L + 127) / 128;
+        auto pads = [&](int b) { return all - (tokens_of(p, b) + 127) / 128; };
+        const Piece y = find_piece<kThreads>(p.B, p.Hk, 1, pads, sm.plan);
+        clear(smem + L::OFF_S, 16384);
+        fence_async_shared();
+        __syncthreads();
+        if (warp == 2 + kWarpsC && lane == 0) {
+            auto v = walk(pads, p, y);
+            for (long long i = y.x0; i < y.x1; ++i, v.next())
+                for (int c = 0; c < p.d; c += 64) {
+                    const int tok = (all - v.tiles + v.tile) * 128;
+                    store_tile(&tdk, smem + L::OFF_S, c, tok, v.seg, v.b);
+                    store_tile(&tdv, smem + L::OFF_S, c, tok, v.seg, v.b);
+                }
+        }
+    }
+    if (warp == 2 + kWarpsC && lane == 0) {
+        tma_store_commit();
+        tma_store_wait_all<0>();
+    }
+    end(tmem);
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows of one tensor for tiles of `rows` tokens and 64 features, 128-byte swizzle; what
+// lies outside reads as 0 and is not written.
+cudaError_t make_map(CUtensorMap *map, const Rows &r, int B, int H, int L, int d, int rows) {
+    cudaError_t err;
+    auto enc = tchost::encode_fn(&err);
+    if (!enc) return err == cudaSuccess ? cudaErrorNotSupported : err;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)B};
+    // a dimension of one has no stride to go by
+    const long long n = L > 1 ? r.s.n : (d + 7) / 8 * 8;
+    const long long h = H > 1 ? r.s.h : n, b = B > 1 ? r.s.b : n;
+    const cuuint64_t strides[3] = {(cuuint64_t)n * 2, (cuuint64_t)h * 2, (cuuint64_t)b * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, r.x, dims, strides, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+bool rows_fit(const Rows &r, int B, int H, int L) {
+    if ((uintptr_t)r.x % 16) return false;
+    const long long s[3] = {r.s.b, r.s.h, r.s.n};
+    const int n[3] = {B, H, L};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] % 8 || s[i] < 8 || s[i] >= 1LL << 38)) return false;
+    return true;
+}
+
+Params params_of(const Shape &sh, int L, int *status) {
+    Params p{};
+    p.B = sh.B;
+    p.Hk = sh.Hk;
+    p.G = sh.G();
+    p.L = L;
+    p.d = sh.d;
+    p.phi = sh.phi;
+    p.norm = sh.norm;
+    p.zsign = 1.f;
+    p.status = status;
+    return p;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Blocks of a kernel over tiles of `tok` of L tokens: no more than there can be.
+int blocks_of(const Shape &sh, long long per_state, int sms) {
+    return (int)std::max(1LL, std::min((long long)sms, sh.heads() * per_state));
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), int blocks, size_t small, int off_small, bool dependent,
+                   cudaStream_t s, A &&...args) {
+    const size_t smem = (size_t)off_small + small + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dependent) {
+        e = tchost::launch_dependent(kern, dim3((unsigned)blocks), kThreads, smem, s,
+                                     std::forward<A>(args)...);
+    } else {
+        kern<<<(unsigned)blocks, kThreads, smem, s>>>(std::forward<A>(args)...);
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+cudaError_t join(const Params &p, int blocks, cudaStream_t s) {
+    if (blocks == 1) return cudaSuccess;
+    const int all = p.d * p.d + p.d;
+    const cudaError_t e =
+        tchost::launch_dependent(join_parts_kernel, dim3((unsigned)(all + 1023) / 1024, (unsigned)blocks - 1),
+                                 256, 0, s, p);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+}
+
+template <int DK>
+constexpr bool fits() {
+    return StateLayout<DK>::OFF_SMALL + sizeof(StateSmall) + 1024 <= 232448 &&
+           ReadLayout<DK>::OFF_SMALL + sizeof(ReadSmall) + 1024 <= 232448 &&
+           QLayout<DK>::OFF_SMALL + sizeof(QSmall) + 1024 <= 232448 &&
+           KLayout<DK>::OFF_SMALL + sizeof(KSmall) + 1024 <= 232448;
+}
+static_assert(fits<64>() && fits<128>(), "shared memory");
+
+template <int DK>
+cudaError_t state(const Shape &sh, Rows k, Rows v, float *S, float *z, char *ws, int sms,
+                  int *status, cudaStream_t s) {
+    using L = StateLayout<DK>;
+    CUtensorMap tk, tv;
+    cudaError_t e = make_map(&tk, k, sh.B, sh.Hk, sh.M, sh.d, L::TOK);
+    if (e == cudaSuccess) e = make_map(&tv, v, sh.B, sh.Hk, sh.M, sh.d, L::TOK);
+    if (e != cudaSuccess) return e;
+    Params p = params_of(sh, sh.M, status);
+    p.lengths = sh.lengths;
+    p.So = S;
+    p.zo = z;
+    p.info = reinterpret_cast<int4 *>(ws);
+    p.part = reinterpret_cast<float *>(ws + up(sizeof(int4) * (size_t)sms));
+    const int blocks = blocks_of(sh, (sh.M + L::TOK - 1) / L::TOK, sms);
+    e = launch(state_kernel<DK>, blocks, sizeof(StateSmall), L::OFF_SMALL, false, s, tk, tv, p);
+    return e == cudaSuccess ? join(p, blocks, s) : e;
+}
+
+template <int DK>
+cudaError_t read(const Shape &sh, Rows q, Rows out, const float *S, const float *z, bool dependent,
+                 int sms, int *status, cudaStream_t s) {
+    using L = ReadLayout<DK>;
+    CUtensorMap tq, to;
+    cudaError_t e = make_map(&tq, q, sh.B, sh.Hq, sh.N, sh.d, 128);
+    if (e == cudaSuccess) e = make_map(&to, out, sh.B, sh.Hq, sh.N, sh.d, 128);
+    if (e != cudaSuccess) return e;
+    Params p = params_of(sh, sh.N, status);
+    p.S = S;
+    p.z = z;
+    const int blocks = blocks_of(sh, (long long)sh.G() * ((sh.N + 127) / 128), sms);
+    return launch(read_kernel<DK>, blocks, sizeof(ReadSmall), L::OFF_SMALL, dependent, s, tq, to, p);
+}
+
+template <int DK>
+cudaError_t back(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, const float *S,
+                 const float *z, Rows dq, Rows dk, Rows dv, char *ws, int sms, int *status,
+                 cudaStream_t s) {
+    CUtensorMap m[7];
+    const Rows *r[7] = {&q, &dout, &dq, &k, &v, &dk, &dv};
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 7 && e == cudaSuccess; ++i)
+        e = i < 3 ? make_map(&m[i], *r[i], sh.B, sh.Hq, sh.N, sh.d, 128)
+                  : make_map(&m[i], *r[i], sh.B, sh.Hk, sh.M, sh.d, 128);
+    if (e != cudaSuccess) return e;
+    Params p = params_of(sh, sh.N, status);
+    float *dS = reinterpret_cast<float *>(ws);
+    float *dz = reinterpret_cast<float *>(ws + up(sizeof(float) * (size_t)(sh.heads() * sh.state())));
+    char *rest = reinterpret_cast<char *>(dz) + up(sizeof(float) * (size_t)(sh.heads() * sh.d));
+    p.S = S;
+    p.z = z;
+    p.So = dS;
+    p.zo = dz;
+    p.zsign = -1.f;
+    p.info = reinterpret_cast<int4 *>(rest);
+    p.part = reinterpret_cast<float *>(rest + up(sizeof(int4) * (size_t)sms));
+    const int blocks = blocks_of(sh, (long long)sh.G() * ((sh.N + 127) / 128), sms);
+    e = launch(qgrad_kernel<DK>, blocks, sizeof(QSmall), QLayout<DK>::OFF_SMALL, false, s, m[0],
+               m[1], m[2], p);
+    if (e == cudaSuccess) e = join(p, blocks, s);
+    if (e != cudaSuccess) return e;
+    Params c = params_of(sh, sh.M, status);
+    c.lengths = sh.lengths;
+    c.S = dS;
+    c.z = dz;
+    return launch(kgrad_kernel<DK>, blocks_of(sh, (sh.M + 127) / 128, sms), sizeof(KSmall),
+                  KLayout<DK>::OFF_SMALL, true, s, m[3], m[4], m[5], m[6], c);
+}
+
+}  // namespace
+
+bool tc_rows(const Shape &sh, const Rows *q_side, int nq, const Rows *k_side, int nk,
+             const float *S, const float *z) {
+    if (sh.d > 128 || sh.d % 8 || (uintptr_t)S % 16 || (uintptr_t)z % 16) return false;
+    for (int i = 0; i < nq; ++i)
+        if (!rows_fit(q_side[i], sh.B, sh.Hq, sh.N)) return false;
+    for (int i = 0; i < nk; ++i)
+        if (!rows_fit(k_side[i], sh.B, sh.Hk, sh.M)) return false;
+    return true;
+}
+
+size_t tc_workspace(const Shape &sh, int sms, bool backward) {
+    const size_t part = up(sizeof(int4) * (size_t)sms) +
+                        up(sizeof(float) * 2 * (size_t)sms * (sh.state() + sh.d));
+    return backward ? part + up(sizeof(float) * (size_t)(sh.heads() * sh.state())) +
+                          up(sizeof(float) * (size_t)(sh.heads() * sh.d))
+                    : part;
+}
+
+cudaError_t tc_state(const Shape &sh, Rows k, Rows v, float *S, float *z, char *ws, int sms,
+                     int *status, cudaStream_t s) {
+    return sh.d <= 64 ? state<64>(sh, k, v, S, z, ws, sms, status, s)
+                      : state<128>(sh, k, v, S, z, ws, sms, status, s);
+}
+
+cudaError_t tc_read(const Shape &sh, Rows q, Rows out, const float *S, const float *z,
+                    bool dependent, int sms, int *status, cudaStream_t s) {
+    return sh.d <= 64 ? read<64>(sh, q, out, S, z, dependent, sms, status, s)
+                      : read<128>(sh, q, out, S, z, dependent, sms, status, s);
+}
+
+cudaError_t tc_backward(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, const float *S,
+                        const float *z, Rows dq, Rows dk, Rows dv, char *ws, int sms, int *status,
+                        cudaStream_t s) {
+    return sh.d <= 64 ? back<64>(sh, dout, q, k, v, S, z, dq, dk, dv, ws, sms, status, s)
+                      : back<128>(sh, dout, q, k, v, S, z, dq, dk, dv, ws, sms, status, s);
+}
+
+}  // namespace cross
+}  // namespace la

@@ -138,6 +138,68 @@ inline la_strides contiguous(int H, int N, int d) {
 
 inline bool negative(const la_strides &s) { return s.b < 0 || s.h < 0 || s.n < 0; }
 
+// Equal pieces of a list of work whose length only the device knows: for each of B
+// entries, `segs` stretches of tiles_of(b) > 0 tiles.  A block's piece is [x0, x1) of
+// `total` tiles, and x0 is tile `rest` of entry b's stretches.  There are `pieces` of
+// them, at most one for each block and of `least` tiles or more where the list is that
+// long, so that no piece between others is empty; later blocks have x0 == x1.
+struct Piece {
+    long long total, x0, x1, rest;
+    int pieces, b;
+
+    // The piece that holds tile x.
+    __device__ __forceinline__ int of(long long x) const {
+        return (int)(((x + 1) * pieces - 1) / total);
+    }
+};
+
+// All kThreads threads of a block call this; `shared` has kThreads / 32 + 2 numbers.
+template <int kThreads, typename F>
+__device__ __forceinline__ Piece find_piece(int B, int segs, int least, F tiles_of,
+                                            long long *shared) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long other = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += other;
+    }
+    if (lane == 31) shared[warp] = upto;
+    __syncthreads();
+    Piece p;
+    long long base = 0;
+    p.total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += shared[w];
+        p.total += shared[w];
+    }
+    p.total *= segs;
+    p.pieces = (int)min((long long)gridDim.x, max(1LL, p.total / least));
+    p.x0 = p.total * min((int)blockIdx.x, p.pieces) / p.pieces;
+    p.x1 = p.total * min((int)blockIdx.x + 1, p.pieces) / p.pieces;
+    long long at = (base + upto - mine) * segs;  // of this thread's first entry
+    if (p.x0 >= at && p.x0 < at + mine * segs) {
+        int b = b0;
+        for (;; ++b) {
+            const long long n = (long long)tiles_of(b) * segs;
+            if (p.x0 < at + n) break;
+            at += n;
+        }
+        shared[kWarps] = b;
+        shared[kWarps + 1] = p.x0 - at;
+    }
+    __syncthreads();
+    p.b = (int)shared[kWarps];
+    p.rest = shared[kWarps + 1];
+    return p;
+}
+
 // The checks of a paged cache that every call of one makes.
 inline la_status check_cache(const char *who, const la_cache *c, int B, int Hk, int d,
                              la_dtype dtype) {

@@ -84,64 +84,20 @@ struct Place {
     }
 };
 
-// This block's piece of the list, [x0, x1), and the place of x0.  A list shorter than
-// the grid has a piece of one tile for each of its first blocks, so that no piece
-// between others is empty.  `shared` has kWarps + 4 numbers.
+// This block's piece of the list and the place of its first tile.
 template <int kTile>
-__device__ __forceinline__ Place<kTile> find_piece(const Params &p, long long *shared,
-                                                   long long &total, int &pieces,
-                                                   long long &x0, long long &x1) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int segs = p.Hk * p.row_tiles;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += span_of<kTile>(p, b).tiles;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long other = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += other;
-    }
-    if (lane == 31) shared[warp] = upto;
-    __syncthreads();
-    long long base = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) base += shared[w];
-        total += shared[w];
-    }
-    total *= segs;
-    pieces = (int)min((long long)gridDim.x, total);
-    x0 = total * min((int)blockIdx.x, pieces) / pieces;
-    x1 = total * min((int)blockIdx.x + 1, pieces) / pieces;
-    long long at = (base + upto - mine) * segs;  // of this thread's first sequence
-    if (x0 >= at && x0 < at + mine * segs) {
-        int b = b0;
-        for (;; ++b) {
-            const long long n = (long long)span_of<kTile>(p, b).tiles * segs;
-            if (x0 < at + n) break;
-            at += n;
-        }
-        shared[kWarps] = b;
-        shared[kWarps + 1] = x0 - at;
-    }
-    __syncthreads();
+__device__ __forceinline__ Place<kTile> find_place(const Params &p, long long *shared,
+                                                   Piece &piece) {
+    piece = find_piece<kThreads>(
+        p.B, p.Hk * p.row_tiles, 1, [&](int b) { return span_of<kTile>(p, b).tiles; }, shared);
     Place<kTile> c;
-    c.b = (int)shared[kWarps];
-    const long long rest = shared[kWarps + 1];
-    if (x0 < x1) {
+    c.b = piece.b;
+    if (piece.x0 < piece.x1) {
         c.s = span_of<kTile>(p, c.b);
-        c.seg = (int)(rest / c.s.tiles);
-        c.tile = (int)(rest - (long long)c.seg * c.s.tiles);
+        c.seg = (int)(piece.rest / c.s.tiles);
+        c.tile = (int)(piece.rest - (long long)c.seg * c.s.tiles);
     }
     return c;
-}
-
-// The block whose piece holds place x.
-__device__ __forceinline__ int block_of(long long x, long long total, int blocks) {
-    return (int)(((x + 1) * blocks - 1) / total);
 }
 
 // One (m, l) pair of running statistics and its merge: the factor of what went before.
@@ -279,9 +235,9 @@ struct Half {
     static constexpr int kOffOut = kWarps * kStages * kStage;
     static constexpr int kOffMl = kOffOut + kRowTile * kOutPitch * 4;
     static constexpr int kOffMask = kOffMl + (kWarps + 1) * kRowTile * 8;
-    static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4 + (kStages % 2 ? 0 : 0);
-    static constexpr int kSmem = kOffPlan + (kWarps + 4) * 8;
-    static_assert(kOffPlan % 8 == 0 && kSmem <= 232448 / 1, "shared memory");
+    static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4;
+    static constexpr int kSmem = kOffPlan + (kWarps + 2) * 8;
+    static_assert(kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
     static_assert(kSmem + 1024 <= 233472 / kBlocks, "blocks per SM");
 };
 
@@ -307,13 +263,13 @@ paged_half_kernel(const __grid_constant__ Params p) {
     tc::grid_dep_launch();
     for (int i = threadIdx.x; i < L::kOffOut / 16; i += kThreads)
         reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
-    long long total, x0, x1;
-    int pieces;
-    Place<kTile> c = find_piece<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan),
-                                       total, pieces, x0, x1);
+    Piece piece;
+    Place<kTile> c =
+        find_place<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan), piece);
     if (threadIdx.x == 0) note_first(p, -1, 0, 0);
-    if (x0 >= x1) return;
-    const int steps = (int)(x1 - x0);
+    const long long x1 = piece.x1;
+    const int steps = (int)(x1 - piece.x0);
+    if (steps == 0) return;
 
     // the copying side, some tiles ahead
     Place<kTile> f = c;
@@ -532,8 +488,7 @@ paged_half_kernel(const __grid_constant__ Params p) {
         const int slot = began ? 0 : ends ? -1 : 1;
         write_rows<T>(p, c.b, h, row0, rows, obuf, L::kOutPitch, ml + kWarps * kRowTile, slot);
         if (began && threadIdx.x == 0)
-            note_first(p, (long long)c.b * segs + c.seg, block_of(seg0, total, pieces),
-                       block_of(seg1 - 1, total, pieces));
+            note_first(p, (long long)c.b * segs + c.seg, piece.of(seg0), piece.of(seg1 - 1));
         __syncthreads();
         left -= n;
         c.tile -= 1;
@@ -557,7 +512,7 @@ struct Full {
     static constexpr int kOffMl = kOffP + kWarps * 8 * kKeys * 4;
     static constexpr int kOffMask = kOffMl + (kWarps + 1) * 8 * 8;
     static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4;
-    static constexpr int kSmem = kOffPlan + (kWarps + 4) * 8;
+    static constexpr int kSmem = kOffPlan + (kWarps + 2) * 8;
     static_assert(kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
     static_assert(kSmem + 1024 <= 233472 / kBlocks, "blocks per SM");
 };
@@ -583,13 +538,13 @@ paged_full_kernel(const __grid_constant__ Params p) {
     tc::grid_dep_launch();
     for (int i = threadIdx.x; i < L::kOffQ / 16; i += kThreads)
         reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
-    long long total, x0, x1;
-    int pieces;
-    Place<kTile> c = find_piece<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan),
-                                       total, pieces, x0, x1);
+    Piece piece;
+    Place<kTile> c =
+        find_place<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan), piece);
     if (threadIdx.x == 0) note_first(p, -1, 0, 0);
-    if (x0 >= x1) return;
-    const int steps = (int)(x1 - x0);
+    const long long x1 = piece.x1;
+    const int steps = (int)(x1 - piece.x0);
+    if (steps == 0) return;
 
     Place<kTile> f = c;
     int f_left = steps, f_stage = 0;
@@ -757,8 +712,7 @@ paged_full_kernel(const __grid_constant__ Params p) {
         const int slot = began ? 0 : ends ? -1 : 1;
         write_rows<T>(p, c.b, h, row0, rows, qbuf, L::kPitch, ml + kWarps * 8, slot);
         if (began && threadIdx.x == 0)
-            note_first(p, (long long)c.b * segs + c.seg, block_of(seg0, total, pieces),
-                       block_of(seg1 - 1, total, pieces));
+            note_first(p, (long long)c.b * segs + c.seg, piece.of(seg0), piece.of(seg1 - 1));
         __syncthreads();
         left -= n;
         c.tile -= 1;

@@ -174,7 +174,7 @@ def test_forward_and_backward(dtype, B, Hq, Hk, N, M, d, lengths, layout, fmap, 
     back = la.backward_cross(dout, q, k, v, S, z, lens, dq=to[1], dk=to[2], dv=to[3], stream=s,
                              **form)
     s.synchronize()
-    aligned = layout != "apart" and d in (64, 128) and dtype == "bf16"
+    aligned = layout != "apart" and d % 8 == 0 and d <= 128 and dtype == "bf16"
     if not aligned:  # one kernel whatever the outputs' strides are
         assert torch.equal(out2, out) and torch.equal(S2, S) and torch.equal(z2, z)
         assert all(torch.equal(a, b) for a, b in zip(back, (dq, dk, dv)))
