@@ -25,8 +25,10 @@
 //   kgrad   dS as two for dphi(K), where dS v and dz cancel for values with a mean far
 //           from 0; as one for dV.
 //
-// Roles (352 threads): warp 0 fetches tiles (TMA), warp 1 issues products, warps 2-9
-// take phi, empty TMEM and compute what lies between, warp 10 stores tiles (TMA).
+// Roles (608 threads): warp 0 fetches tiles (TMA), warp 1 issues products, warps 2-17
+// take phi, empty TMEM and compute what lies between, warp 18 stores tiles (TMA).  The
+// computing warps set the pace: with 8 of them, and phi with a branch, the kernels were
+// bound by latency and instructions at a third of the memory's rate.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -45,8 +47,8 @@ namespace {
 using namespace la::tc;
 using namespace la::tcc;
 
-constexpr int kThreads = 352, kC0 = 64, kC = 256;  // all; the computing ones: from, number
-constexpr int kWarpsC = kC / 32;
+constexpr int kThreads = 608, kC0 = 64, kC = 512;  // all; the computing ones: from, number
+constexpr int kWarpsC = kC / 32, kParts = kWarpsC / 4;  // warps that share rows of TMEM
 constexpr int BAR_C = 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kTimeout = 1LL << 32;
@@ -67,16 +69,19 @@ __device__ __forceinline__ int tokens_of(const Params &p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.L) : p.L;
 }
 
-// A place in the list: tile of head `seg` of sequence b.  F: tiles of a sequence's head.
+// A place in the list: tile of head `seg` of sequence b, which has `len` tokens.  F:
+// tiles of a head of so many tokens.
 template <typename F>
 struct Walk {
     F count;
-    int B, segs, b, seg, tile, tiles;
+    const Params &p;
+    int segs, b, seg, tile, tiles, len;
 
     __device__ __forceinline__ Walk(F f, const Params &p, const Piece &x)
-        : count(f), B(p.B), segs(p.Hk), b(x.b), seg(0), tile(0), tiles(1) {
+        : count(f), p(p), segs(p.Hk), b(x.b), seg(0), tile(0), tiles(1), len(0) {
         if (x.x0 < x.x1) {
-            tiles = count(b);
+            len = tokens_of(p, b);
+            tiles = count(len);
             seg = (int)(x.rest / tiles);
             tile = (int)(x.rest - (long long)seg * tiles);
         }
@@ -88,8 +93,9 @@ struct Walk {
         if (++seg < segs) return;
         seg = 0;
         do {
-            ++b;
-            tiles = b < B ? count(b) : 1;
+            if (++b >= p.B) return;
+            len = tokens_of(p, b);
+            tiles = count(len);
         } while (tiles == 0);
     }
 };
@@ -134,8 +140,32 @@ __device__ __forceinline__ uint4 shut8(const float (&e)[8]) {
     return make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                       pack_bf16x2(e[6], e[7]));
 }
-__device__ __forceinline__ float phi_fast(float x, int phi) {
-    return !phi ? x : x > 0.f ? x + 1.f : exp2f(x * 1.44269504088896341f);
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// max(x, 0), and NaN of NaN.
+__device__ __forceinline__ float above(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+// elu(x) + 1 = max(x, 0) + exp(min(x, 0)), of pairs.
+__device__ __forceinline__ float2 exp_below(float2 x) {
+    const float2 u = __fmul2_rn(make_float2(fminf(x.x, 0.f), fminf(x.y, 0.f)),
+                                make_float2(1.44269504088896341f, 1.44269504088896341f));
+    return make_float2(exp2_fast(u.x), exp2_fast(u.y));
+}
+__device__ __forceinline__ void phi8(float (&e)[8], int phi) {
+    if (!phi) return;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 x = make_float2(e[i], e[i + 1]);
+        const float2 f = __fadd2_rn(make_float2(above(x.x), above(x.y)), exp_below(x));
+        e[i] = f.x;
+        e[i + 1] = f.y;
+    }
 }
 // phi' from phi: where x > 0, phi > 1 and the slope is 1; elsewhere it is phi itself.
 __device__ __forceinline__ float slope_of_phi(float f, int phi) {
@@ -143,11 +173,15 @@ __device__ __forceinline__ float slope_of_phi(float f, int phi) {
 }
 // What eight numbers lose as bf16, as bf16.
 __device__ __forceinline__ uint4 low8(const float (&e)[8], const uint4 high) {
-    float h[8], l[8];
+    float h[8];
     open8(high, h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = e[i] - h[i];
-    return shut8(l);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 l = __fadd2_rn(make_float2(e[i], e[i + 1]), make_float2(-h[i], -h[i + 1]));
+        h[i] = l.x;
+        h[i + 1] = l.y;
+    }
+    return shut8(h);
 }
 
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
@@ -188,26 +222,50 @@ __device__ __forceinline__ void clear(uint8_t *at, int bytes) {
         reinterpret_cast<uint4 *>(at)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Where a computing thread's results lie in TMEM: lane (row of the product) and half of
+// Where a computing thread's results lie in TMEM: lane (row of the product) and part of
 // the columns.
 struct Mine {
-    int et, row, half;
+    int et, row, part;
     uint32_t lane_base;
     __device__ __forceinline__ explicit Mine(uint32_t tmem) {
         et = threadIdx.x - kC0;
         const int quarter = (threadIdx.x >> 5) & 3;
         row = quarter * 32 + (threadIdx.x & 31);
-        half = et >= kC / 2;
+        part = et / (kC / kParts);
         lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     }
 };
 
-// The sums of one state that a computing thread holds: DK / 2 columns of row a, and z[a]
-// (half 0).  In TMEM: the first 64 columns, 16 more of which zc are z's, and (DK = 128)
+// N consecutive columns of this thread's lane, as fp32, after the wait.
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&v)[32]) {
+    tmem_ld32(at, v);
+    tmem_wait_ld();
+    reg_fence(v);
+}
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+    tmem_wait_ld();
+    reg_fence(r);
+}
+
+// The sums of one state that a computing thread holds: kCols columns of row a, and z[a]
+// (part 0).  In TMEM: the first 64 columns, 16 more of which kZ are z's, and (DK = 128)
 // the other 64 columns.
 template <int DK>
+__device__ __forceinline__ int column(const Mine &me) {  // of its first, from the sums' start
+    const int c = me.part * (DK / kParts);
+    return c < 64 ? c : c + 16;
+}
+template <int DK>
 struct Sums {
-    static constexpr int kCols = DK / 2;
+    static constexpr int kCols = DK / kParts;
     float s[kCols], z;
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -217,15 +275,11 @@ struct Sums {
     template <int kZ>
     __device__ __forceinline__ void add(const Mine &me, uint32_t base) {
         const uint32_t at = me.lane_base + base;
+        uint32_t v[kCols];
+        tmem_get(at + column<DK>(me), v);
 #pragma unroll
-        for (int h = 0; h < kCols / 32; ++h) {
-            uint32_t v[32];
-            tmem_ld32(at + (DK == 128 ? me.half * 80 : me.half * 32) + 32 * h, v);
-            tmem_wait_ld();
-            reg_fence(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[32 * h + e] += u2f(v[e]);
-        }
+        for (int e = 0; e < kCols; ++e) s[e] += u2f(v[e]);
+        if (me.part > 0) return;
         uint32_t v0 = tmem_ld1(at + 64), v1 = 0;
         if (kZ == 2) v1 = tmem_ld1(at + 65);
         tmem_wait_ld();
@@ -236,7 +290,7 @@ struct Sums {
     // To the state itself, or to part `slot` (>= 0) of this block.
     __device__ __forceinline__ void write(const Params &p, const Mine &me, long long state,
                                           int slot) const {
-        const int a = me.row, c0 = me.half * kCols;
+        const int a = me.row, c0 = me.part * kCols;
         if (a >= p.d) return;
         const long long dd = (long long)p.d * p.d;
         float *S, *z_to;
@@ -253,7 +307,7 @@ struct Sums {
             if (c0 + e < p.d)
                 *reinterpret_cast<float4 *>(S + e) =
                     make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
-        if (me.half == 0) z_to[a] = p.zsign * z;
+        if (me.part == 0) z_to[a] = p.zsign * z;
     }
 };
 
@@ -265,7 +319,7 @@ struct StateLayout {
     static constexpr int ATOM = TOK * 128, TILE = KB * ATOM, STAGE = 2 * TILE, STAGES = 5;
     static constexpr int OFF_LOW = STAGES * STAGE, OFF_ONE = OFF_LOW + 2 * TILE;
     static constexpr int OFF_SMALL = OFF_ONE + ATOM;
-    static constexpr int GROUP = 512 / TOK;  // tiles between two emptyings
+    static constexpr int GROUP = 256 / TOK;  // tiles between two emptyings
 };
 struct StateSmall {
     uint64_t full[5], empty[5], ready[5], low_empty[2], acc_full[2], acc_empty[2], fin;
@@ -303,8 +357,9 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         mbar_init(&sm.fin, 1);
     });
     const Ctx cx{&sm.abort, p.status, kTimeout};
-    auto count = [&](int b) { return max(1, (tokens_of(p, b) + L::TOK - 1) / L::TOK); };
-    const Piece x = find_piece<kThreads>(p.B, p.Hk, 4, count, sm.plan);
+    auto count = [](int len) { return max(1, (len + L::TOK - 1) / L::TOK); };
+    const Piece x = find_piece<kThreads>(
+        p.B, p.Hk, 4, [&](int b) { return count(tokens_of(p, b)); }, sm.plan);
     const int steps = (int)(x.x1 - x.x0);
     if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
     auto w = walk(count, p, x);
@@ -367,7 +422,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kParts = kC / L::TOK, kChunks = DK / 8 / kParts;
+        constexpr int kChunks = DK / 8 / (kC / L::TOK);
         const int row = me.et % L::TOK, part = me.et / L::TOK;
         Sums<DK> acc;
         acc.clear();
@@ -389,7 +444,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             pending = false;
         };
         for (int j = 0; j < steps; ++j, w.next()) {
-            const int st = j % L::STAGES, len = tokens_of(p, w.b) - w.tile * L::TOK;
+            const int st = j % L::STAGES, len = w.len - w.tile * L::TOK;
             wait_bar(&sm.low_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
             wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
             uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
@@ -400,12 +455,11 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const uint32_t at = tile_at(L::TOK, row, col);
                 float e[8];
                 open8(*reinterpret_cast<const uint4 *>(kt + at), e);
-                const bool ok = row < len && col < p.d;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) e[q] = ok ? phi_fast(e[q], p.phi) : 0.f;
-                const uint4 high = shut8(e);
+                phi8(e, p.phi);
+                uint4 high = shut8(e), low = low8(e, high);
+                if (row >= len || col >= p.d) high = low = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(kt + at) = high;
-                *reinterpret_cast<uint4 *>(lt + at) = low8(e, high);
+                *reinterpret_cast<uint4 *>(lt + at) = low;
                 if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
             }
             fence_async_shared();
@@ -547,7 +601,8 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kChunks = DK / 16;
+        constexpr int kCols = DK / kParts, kChunks = kCols / 8;
+        const int f0 = me.part * kCols;
         auto output = [&](int j) {
             const int st = j % L::STAGES;
             wait_bar(&sm.o_full[j & 1], (j >> 1) & 1, cx);
@@ -562,28 +617,18 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                 const float den = u2f(d0) + u2f(d1);
                 inv = den == 0.f ? 0.f : 1.f / den;
             }
-            uint4 y[DK / 16];
-#pragma unroll
-            for (int h = 0; h < DK / 64; ++h) {
-                uint32_t v[32];
-                tmem_ld32(o + me.half * (DK == 128 ? 80 : 32) + 32 * h, v);
-                tmem_wait_ld();
-                reg_fence(v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float e[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) e[q] = u2f(v[8 * i + q]) * inv;
-                    y[4 * h + i] = shut8(e);
-                }
-            }
+            uint32_t v[kCols];
+            tmem_get(o + column<DK>(me), v);
             tc_fence_before();
             arrive_warp(&sm.o_empty[j & 1]);
             uint8_t *tile = smem + st * L::TILE;
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
-                *reinterpret_cast<uint4 *>(tile + tile_at(128, me.row, me.half * (DK / 2) + 8 * i)) =
-                    y[i];
+            for (int i = 0; i < kChunks; ++i) {
+                float e[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) e[q] = u2f(v[8 * i + q]) * inv;
+                *reinterpret_cast<uint4 *>(tile + tile_at(128, me.row, f0 + 8 * i)) = shut8(e);
+            }
             fence_async_shared();
             arrive_warp(&sm.out[st]);
         };
@@ -627,9 +672,8 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                 uint4 *at = reinterpret_cast<uint4 *>(tile + tile_at(128, row, col));
                 float e[8];
                 open8(*at, e);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) e[q] = col < p.d ? phi_fast(e[q], p.phi) : 0.f;
-                *at = shut8(e);
+                phi8(e, p.phi);
+                *at = col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
             }
             fence_async_shared();
             arrive_warp(&sm.ready[st]);
@@ -669,8 +713,8 @@ struct QSmall {
     uint64_t full[4], empty[4], psi[4], s_ready, g_full[2], g_empty[2], t_free, ds_full, ds_empty;
     uint64_t out_full, out_empty, fin;
     long long plan[kThreads / 32 + 2];
-    float z[128], m[256], zz[8];
-    float2 red[2][256];
+    float z[128], m[kC];
+    float2 red[2][kC];
     uint32_t tmem;
     int abort;
 };
@@ -787,8 +831,8 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kHalf = DK / 2;
-        const int f0 = me.half * kHalf;  // this thread's features of its row
+        constexpr int kCols = DK / kParts;
+        const int f0 = me.part * kCols;  // this thread's features of its row
         int first_tile = w.tile, drained = 0;
         auto drain = [&](long long state, int slot) {  // a state's sums are complete
             wait_bar(&sm.ds_full, drained & 1, cx);
@@ -809,13 +853,13 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             if (j == 0 || w.tile == 0) {
                 sync_compute();  // all are through with the state before
                 const float *S = p.S + state * p.d * p.d;
-                // m = S^T z / z.z, two threads per column
+                // m = S^T z / z.z, four threads per column
                 if (me.et < 128) sm.z[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 sync_compute();
                 float zz = 0.f;
                 for (int a = 0; a < p.d; ++a) zz = fmaf(sm.z[a], sm.z[a], zz);
-                const int c = me.et & 127, a0 = (me.et >> 7) * ((p.d + 1) / 2);
-                const int a1 = min(a0 + (p.d + 1) / 2, p.d);
+                const int c = me.et & 127, a0 = (me.et >> 7) * (p.d / 4);
+                const int a1 = a0 + p.d / 4;
                 float t = 0.f;
                 if (c < p.d && p.norm)
 #pragma unroll 8
@@ -824,7 +868,8 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 sm.m[me.et] = t;
                 sync_compute();
                 const float over = zz > 0.f && p.norm ? 1.f / zz : 0.f;
-                const float mc = (sm.m[c] + sm.m[c + 128]) * over;
+                const float mc =
+                    ((sm.m[c] + sm.m[c + 128]) + (sm.m[c + 256] + sm.m[c + 384])) * over;
                 sync_compute();
                 if (me.et < 128) sm.m[me.et] = mc;
                 sync_compute();
@@ -859,41 +904,43 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
             uint8_t *qt = smem + st * L::STAGE;
             // phi(q), its product with z and, behind the products' end, with G
-            float f[kHalf], den = 0.f, dot = 0.f;
+            float f[kCols], den = 0.f, dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < kHalf / 8; ++i) {
+            for (int i = 0; i < kCols; i += 8) {
                 float e[8];
-                open8(*reinterpret_cast<const uint4 *>(qt + tile_at(128, me.row, f0 + 8 * i)), e);
+                open8(*reinterpret_cast<const uint4 *>(qt + tile_at(128, me.row, f0 + i)), e);
+                phi8(e, p.phi);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    f[8 * i + q] = f0 + 8 * i < p.d ? phi_fast(e[q], p.phi) : 0.f;
-                    den = fmaf(f[8 * i + q], sm.z[f0 + 8 * i + q], den);
+                    f[i + q] = f0 + i < p.d ? e[q] : 0.f;
+                    den = fmaf(f[i + q], sm.z[f0 + i + q], den);
                 }
             }
             wait_bar(&sm.g_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
             const uint32_t gb = me.lane_base + kG + (j & 1) * kGStep;
+            uint32_t v[kCols];
+            tmem_get(gb + f0, v);
 #pragma unroll
-            for (int h = 0; h < kHalf / 32; ++h) {
-                uint32_t v[32];
-                tmem_ld32(gb + f0 + 32 * h, v);
-                tmem_wait_ld();
-                reg_fence(v);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) dot = fmaf(f[32 * h + e], u2f(v[e]), dot);
-            }
+            for (int e = 0; e < kCols; ++e) dot = fmaf(f[e], u2f(v[e]), dot);
             uint32_t m0 = tmem_ld1(gb + DK), m1 = tmem_ld1(gb + DK + 1);
             tmem_wait_ld();
             reg_fence(m0);
             reg_fence(m1);
-            sm.red[j & 1][me.half * 128 + me.row] = make_float2(den, dot);
+            tc_fence_before();
+            arrive_warp(&sm.g_empty[j & 1]);
+            sm.red[j & 1][me.part * 128 + me.row] = make_float2(den, dot);
             // the staging tile and t's column are free again
             wait_bar(&sm.out_empty, (j & 1) ^ 1, cx);
             wait_bar(&sm.t_free, (j & 1) ^ 1, cx);
             sync_compute();
-            const float2 r0 = sm.red[j & 1][me.row], r1 = sm.red[j & 1][128 + me.row];
-            den = r0.x + r1.x;
-            dot = r0.y + r1.y;
+            den = dot = 0.f;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+                const float2 r = sm.red[j & 1][128 * q + me.row];
+                den += r.x;
+                dot += r.y;
+            }
             float r = 1.f, t = 0.f, t_all = 0.f;
             if (p.norm) {
                 r = den == 0.f ? 0.f : 1.f / den;
@@ -903,33 +950,23 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             }
             uint8_t *ot = smem + L::OFF_OUT;
 #pragma unroll
-            for (int h = 0; h < kHalf / 32; ++h) {
-                uint32_t v[32];
-                tmem_ld32(gb + f0 + 32 * h, v);
-                tmem_wait_ld();
-                reg_fence(v);
+            for (int i = 0; i < kCols; i += 8) {
+                float g[8], s[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float g[8], s[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int e = 32 * h + 8 * i + q;
-                        g[q] = r * fmaf(-t, sm.z[f0 + e], u2f(v[8 * i + q])) *
-                               slope_of_phi(f[e], p.phi);
-                        s[q] = r * f[e];
-                    }
-                    const uint32_t at = tile_at(128, me.row, f0 + 32 * h + 8 * i);
-                    *reinterpret_cast<uint4 *>(ot + at) = shut8(g);
-                    *reinterpret_cast<uint4 *>(qt + at) = shut8(s);
+                for (int q = 0; q < 8; ++q) {
+                    g[q] = r * fmaf(-t, sm.z[f0 + i + q], u2f(v[i + q])) *
+                           slope_of_phi(f[i + q], p.phi);
+                    s[q] = r * f[i + q];
                 }
+                const uint32_t at = tile_at(128, me.row, f0 + i);
+                *reinterpret_cast<uint4 *>(ot + at) = shut8(g);
+                *reinterpret_cast<uint4 *>(qt + at) = shut8(s);
             }
-            if (me.half == 0) {
+            if (me.part == 0) {
                 const float high = __bfloat162float(__float2bfloat16_rn(t_all));
                 *reinterpret_cast<uint32_t *>(smem + L::OFF_T + sw128_offset(me.row, 0)) =
                     pack_bf16x2(t_all, t_all - high);
             }
-            tc_fence_before();
-            arrive_warp(&sm.g_empty[j & 1]);
             fence_async_shared();
             arrive_warp(&sm.psi[st]);
             if (lane == 0) mbar_arrive(&sm.out_full);
@@ -969,11 +1006,12 @@ struct KLayout {
     static constexpr int KB = DK / 64, TILE = KB * 16384, STAGE = 2 * TILE;
     static constexpr int STAGES = DK == 128 ? 2 : 4;
     static constexpr int SATOM = DK * 128, SBLK = KB * SATOM;
-    static constexpr int OFF_S = STAGES * STAGE, OFF_SMALL = OFF_S + 2 * SBLK;
+    static constexpr int OFF_PHI = STAGES * STAGE, OFF_S = OFF_PHI + TILE;
+    static constexpr int OFF_SMALL = OFF_S + 2 * SBLK;
     static_assert(2 * SBLK >= 16384, "a tile of zeros fits");
 };
 struct KSmall {
-    uint64_t full[4], empty[4], ready[4], out[4], s_ready, d_full[2], d_empty[2], fin;
+    uint64_t full[4], empty[4], ready[4], out[4], s_ready, phi_empty, d_full[2], d_empty[2], fin;
     long long plan[kThreads / 32 + 2];
     float dz[128];
     uint32_t tmem;
@@ -999,6 +1037,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&sm.out[i], kWarpsC);
         }
         mbar_init(&sm.s_ready, kWarpsC);
+        mbar_init(&sm.phi_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.d_full[i], 1);
             mbar_init(&sm.d_empty[i], kWarpsC);
@@ -1006,8 +1045,9 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         mbar_init(&sm.fin, 1);
     });
     const Ctx cx{&sm.abort, p.status, kTimeout};
-    auto count = [&](int b) { return (tokens_of(p, b) + 127) / 128; };
-    const Piece x = find_piece<kThreads>(p.B, p.Hk, 1, count, sm.plan);
+    auto count = [](int len) { return (len + 127) / 128; };
+    const Piece x = find_piece<kThreads>(
+        p.B, p.Hk, 1, [&](int b) { return count(tokens_of(p, b)); }, sm.plan);
     const int steps = (int)(x.x1 - x.x0);
     auto w = walk(count, p, x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1041,18 +1081,20 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
                 wait_bar_spin(&sm.d_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
                 tc_fence_after();
-                const uint32_t kb = smem_u32(smem + st * L::STAGE), vb = kb + L::TILE;
+                const uint32_t vb = smem_u32(smem + st * L::STAGE + L::TILE);
+                const uint32_t fb = smem_u32(smem + L::OFF_PHI);
                 const uint32_t dk = tmem + (j & 1) * 2 * DK, dv = dk + DK;
+#pragma unroll
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_ss(dv, sdesc_sw128(fb + kmajor_off(ks, 16384), 16, 1024),
+                           sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
+                mma_commit(&sm.phi_empty);
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     const uint64_t a = sdesc_sw128(vb + kmajor_off(ks, 16384), 16, 1024);
                     mma_ss(dk, a, sdesc_sw128(hi + kmajor_off(ks, L::SATOM), 16, 1024), idK, ks > 0);
                     mma_ss(dk, a, sdesc_sw128(lo + kmajor_off(ks, L::SATOM), 16, 1024), idK, 1);
                 }
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_ss(dv, sdesc_sw128(kb + kmajor_off(ks, 16384), 16, 1024),
-                           sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
                 mma_commit(&sm.d_full[j & 1]);
             }
             mma_commit(&sm.fin);
@@ -1060,38 +1102,38 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kHalf = DK / 2, kChunks = DK / 16;
-        const int f0 = me.half * kHalf;
+        constexpr int kCols = DK / kParts, kChunks = kCols / 8;
+        const int f0 = me.part * kCols;
         auto output = [&](int j, int len) {
             const int st = j % L::STAGES;
             wait_bar(&sm.d_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
             const uint32_t dk = me.lane_base + (j & 1) * 2 * DK + f0;
             uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+            uint32_t v[kCols];
+            tmem_get(dk, v);
 #pragma unroll
-            for (int h = 0; h < kHalf / 32; ++h) {
-                uint32_t v[32], u[32];
-                tmem_ld32(dk + 32 * h, v);
-                tmem_ld32(dk + DK + 32 * h, u);
-                tmem_wait_ld();
-                reg_fence(v);
-                reg_fence(u);
+            for (int i = 0; i < kCols; i += 8) {
+                uint8_t *at = kt + tile_at(128, me.row, f0 + i);
+                float x[8];
+                open8(*reinterpret_cast<const uint4 *>(at), x);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = tile_at(128, me.row, f0 + 32 * h + 8 * i);
-                    float f[8], g[8], o[8];
-                    open8(*reinterpret_cast<const uint4 *>(kt + at), f);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float s = slope_of_phi(f[q], p.phi);
-                        g[q] = me.row < len
-                                   ? (u2f(v[8 * i + q]) + sm.dz[f0 + 32 * h + 8 * i + q]) * s
-                                   : 0.f;
-                        o[q] = u2f(u[8 * i + q]);
-                    }
-                    *reinterpret_cast<uint4 *>(kt + at) = shut8(g);
-                    *reinterpret_cast<uint4 *>(vt + at) = shut8(o);
+                for (int q = 0; q < 8; q += 2) {
+                    const float2 dz = *reinterpret_cast<const float2 *>(&sm.dz[f0 + i + q]);
+                    float2 g = __fadd2_rn(make_float2(u2f(v[i + q]), u2f(v[i + q + 1])), dz);
+                    if (p.phi) g = __fmul2_rn(g, exp_below(make_float2(x[q], x[q + 1])));
+                    x[q] = g.x;
+                    x[q + 1] = g.y;
                 }
+                *reinterpret_cast<uint4 *>(at) = me.row < len ? shut8(x) : make_uint4(0, 0, 0, 0);
+            }
+            tmem_get(dk + DK, v);
+#pragma unroll
+            for (int i = 0; i < kCols; i += 8) {
+                float o[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) o[q] = u2f(v[i + q]);
+                *reinterpret_cast<uint4 *>(vt + tile_at(128, me.row, f0 + i)) = shut8(o);
             }
             tc_fence_before();
             arrive_warp(&sm.d_empty[j & 1]);
@@ -1104,7 +1146,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES;
             len_before = len;
-            len = tokens_of(p, w.b) - w.tile * 128;
+            len = w.len - w.tile * 128;
             if (j == 0 || w.tile == 0) {
                 if (pending) output(j - 1, len_before);
                 pending = false;
@@ -1131,6 +1173,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 sync_compute();
                 arrive_warp(&sm.s_ready);
             }
+            wait_bar(&sm.phi_empty, (j & 1) ^ 1, cx);
             wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
             uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
 #pragma unroll
@@ -1139,10 +1182,9 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const uint32_t at = tile_at(128, row, col);
                 float e[8];
                 open8(*reinterpret_cast<const uint4 *>(kt + at), e);
-                const bool ok = row < len && col < p.d;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) e[q] = ok ? phi_fast(e[q], p.phi) : 0.f;
-                *reinterpret_cast<uint4 *>(kt + at) = shut8(e);
+                phi8(e, p.phi);
+                *reinterpret_cast<uint4 *>(smem + L::OFF_PHI + at) =
+                    row < len && col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
                 if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
             }
             fence_async_shared();
@@ -1170,8 +1212,9 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     __syncthreads();
     if (p.lengths) {
         const int all = (p.L + 127) / 128;
-        auto pads = [&](int b) { return all - (tokens_of(p, b) + 127) / 128; };
-        const Piece y = find_piece<kThreads>(p.B, p.Hk, 1, pads, sm.plan);
+        auto pads = [&](int len) { return all - (len + 127) / 128; };
+        const Piece y = find_piece<kThreads>(
+            p.B, p.Hk, 1, [&](int b) { return pads(tokens_of(p, b)); }, sm.plan);
         clear(smem + L::OFF_S, 16384);
         fence_async_shared();
         __syncthreads();
