@@ -49,6 +49,9 @@ using namespace la::tcc;
 
 constexpr int kThreads = 608, kC0 = 64, kC = 512;  // all; the computing ones: from, number
 constexpr int kWarpsC = kC / 32, kParts = kWarpsC / 4;  // warps that share rows of TMEM
+// Where tiles are independent, two groups of computing warps take them in turn, so that
+// one works while the other waits.
+constexpr int kG = kC / 2, kWarpsG = kG / 32;
 constexpr int BAR_C = 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kTimeout = 1LL << 32;
@@ -225,13 +228,14 @@ __device__ __forceinline__ void clear(uint8_t *at, int bytes) {
 // Where a computing thread's results lie in TMEM: lane (row of the product) and part of
 // the columns.
 struct Mine {
-    int et, row, part;
+    int et, row, part, group;
     uint32_t lane_base;
     __device__ __forceinline__ explicit Mine(uint32_t tmem) {
         et = threadIdx.x - kC0;
         const int quarter = (threadIdx.x >> 5) & 3;
         row = quarter * 32 + (threadIdx.x & 31);
         part = et / (kC / kParts);
+        group = et / kG;
         lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     }
 };
@@ -256,13 +260,8 @@ __device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
 }
 
 // The sums of one state that a computing thread holds: kCols columns of row a, and z[a]
-// (part 0).  In TMEM: the first 64 columns, 16 more of which kZ are z's, and (DK = 128)
-// the other 64 columns.
-template <int DK>
-__device__ __forceinline__ int column(const Mine &me) {  // of its first, from the sums' start
-    const int c = me.part * (DK / kParts);
-    return c < 64 ? c : c + 16;
-}
+// (part 0).  In TMEM: S's columns from kSplit on lie 16 further on, behind z's, of which
+// there are kZ.
 template <int DK>
 struct Sums {
     static constexpr int kCols = DK / kParts;
@@ -272,16 +271,17 @@ struct Sums {
         for (int i = 0; i < kCols; ++i) s[i] = 0.f;
         z = 0.f;
     }
-    template <int kZ>
+    template <int kZ, int kSplit>
     __device__ __forceinline__ void add(const Mine &me, uint32_t base) {
         const uint32_t at = me.lane_base + base;
         uint32_t v[kCols];
-        tmem_get(at + column<DK>(me), v);
+        const int c = me.part * kCols;
+        tmem_get(at + c + (c < kSplit ? 0 : 16), v);
 #pragma unroll
         for (int e = 0; e < kCols; ++e) s[e] += u2f(v[e]);
         if (me.part > 0) return;
-        uint32_t v0 = tmem_ld1(at + 64), v1 = 0;
-        if (kZ == 2) v1 = tmem_ld1(at + 65);
+        uint32_t v0 = tmem_ld1(at + kSplit), v1 = 0;
+        if (kZ == 2) v1 = tmem_ld1(at + kSplit + 1);
         tmem_wait_ld();
         reg_fence(v0);
         reg_fence(v1);
@@ -311,18 +311,48 @@ struct Sums {
     }
 };
 
+// A state S in registers, 8 numbers at a time: number i of a computing thread is row
+// (et + 512 i) / (DK / 8), columns (et + 512 i) % (DK / 8) 8 on.  All loads are under way
+// at once.
+template <int DK>
+struct Loaded {
+    static constexpr int kN = DK * DK / 8 / kC;
+    float4 u[kN], v[kN];
+    static __device__ __forceinline__ int row(int et, int i) { return (et + kC * i) / (DK / 8); }
+    static __device__ __forceinline__ int col(int et, int i) {
+        return (et + kC * i) % (DK / 8) * 8;
+    }
+    __device__ __forceinline__ void load(const float *S, int d, int et) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int a = row(et, i), c = col(et, i);
+            u[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a < d && c < d) {
+                const float4 *s4 = reinterpret_cast<const float4 *>(S + (long long)a * d + c);
+                u[i] = __ldcg(s4);
+                v[i] = __ldcg(s4 + 1);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int i, float (&e)[8]) const {
+        e[0] = u[i].x, e[1] = u[i].y, e[2] = u[i].z, e[3] = u[i].w;
+        e[4] = v[i].x, e[5] = v[i].y, e[6] = v[i].z, e[7] = v[i].w;
+    }
+};
+
 // ------------------------------------------------------------------ state
 
 template <int DK>
 struct StateLayout {
     static constexpr int TOK = DK == 128 ? 64 : 128, KB = DK / 64;
-    static constexpr int ATOM = TOK * 128, TILE = KB * ATOM, STAGE = 2 * TILE, STAGES = 5;
-    static constexpr int OFF_LOW = STAGES * STAGE, OFF_ONE = OFF_LOW + 2 * TILE;
-    static constexpr int OFF_SMALL = OFF_ONE + ATOM;
+    // A stage: K, V and behind V the column of ones, one operand of DK + 16 columns.
+    static constexpr int ATOM = TOK * 128, TILE = KB * ATOM, STAGE = 2 * TILE + ATOM;
+    static constexpr int STAGES = DK == 128 ? 4 : 3, LOWS = 3;
+    static constexpr int OFF_LOW = STAGES * STAGE, OFF_SMALL = OFF_LOW + LOWS * TILE;
     static constexpr int GROUP = 256 / TOK;  // tiles between two emptyings
 };
 struct StateSmall {
-    uint64_t full[5], empty[5], ready[5], low_empty[2], acc_full[2], acc_empty[2], fin;
+    uint64_t full[4], empty[4], ready[4], low_empty[3], acc_full[2], acc_empty[2], fin;
     long long plan[kThreads / 32 + 2];
     uint32_t tmem;
     int abort;
@@ -337,20 +367,21 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                 ~uintptr_t(1023));
     StateSmall &sm = *reinterpret_cast<StateSmall *>(smem + L::OFF_SMALL);
-    clear(smem + L::OFF_ONE, L::ATOM);
+    for (int i = 0; i < L::STAGES; ++i) clear(smem + i * L::STAGE + 2 * L::TILE, L::ATOM);
     __syncthreads();
-    if (threadIdx.x < L::TOK)
-        *reinterpret_cast<uint16_t *>(smem + L::OFF_ONE + sw128_offset(threadIdx.x, 0)) =
+    for (int i = threadIdx.x; i < L::STAGES * L::TOK; i += kThreads)
+        *reinterpret_cast<uint16_t *>(smem + i / L::TOK * L::STAGE + 2 * L::TILE +
+                                      sw128_offset(i % L::TOK, 0)) =
             (uint16_t)(kBf16One2 & 0xFFFFu);
     const uint32_t tmem = begin(&sm.tmem, [&] {
         sm.abort = 0;
         for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
-            mbar_init(&sm.ready[i], kWarpsC);
+            mbar_init(&sm.ready[i], kWarpsG);
         }
+        for (int i = 0; i < L::LOWS; ++i) mbar_init(&sm.low_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.low_empty[i], 1);
             mbar_init(&sm.acc_full[i], 1);
             mbar_init(&sm.acc_empty[i], kWarpsC);
         }
@@ -373,7 +404,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const int st = j % L::STAGES;
                 if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
                 uint8_t *at = smem + st * L::STAGE;
-                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                mbar_arrive_expect_tx(&sm.full[st], 2 * L::TILE);
                 for (int a = 0; a < L::KB; ++a) {
                     load_tile(at + a * L::ATOM, &tk, &sm.full[st], 64 * a, w.tile * L::TOK, w.seg,
                               w.b, pol);
@@ -386,9 +417,8 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t id0 = idesc_bf16(128, 80, 1, 1), id1 = idesc_bf16(128, 64, 1, 1);
+            constexpr uint32_t id = idesc_bf16(128, DK + 16, 1, 1);
             constexpr uint32_t lboA = DK == 128 ? L::ATOM : 0;  // DK = 64: rows 64.. repeat
-            const uint32_t one = smem_u32(smem + L::OFF_ONE);
             int g = 0, in = 0;
             for (int j = 0; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES;
@@ -396,21 +426,18 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
                 tc_fence_after();
                 const uint32_t hi = smem_u32(smem + st * L::STAGE), vb = hi + L::TILE;
-                const uint32_t lo = smem_u32(smem + L::OFF_LOW + (j & 1) * L::TILE);
+                const uint32_t lo = smem_u32(smem + L::OFF_LOW + j % L::LOWS * L::TILE);
                 const uint32_t acc = tmem + (g & 1) * 160;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < L::TOK / 16; ++ks) {
                         const uint64_t a = sdesc_sw128((part ? lo : hi) + ks * 2048, lboA, 1024);
-                        const uint32_t more = in > 0 || part > 0 || ks > 0;
-                        mma_ss(acc, a, sdesc_sw128(vb + ks * 2048, one - vb, 1024), id0, more);
-                        if (DK == 128)
-                            mma_ss(acc + 80, a, sdesc_sw128(vb + L::ATOM + ks * 2048, 0, 1024),
-                                   id1, more);
+                        mma_ss(acc, a, sdesc_sw128(vb + ks * 2048, L::ATOM, 1024), id,
+                               in > 0 || part > 0 || ks > 0);
                     }
                 mma_commit(&sm.empty[st]);
-                mma_commit(&sm.low_empty[j & 1]);
+                mma_commit(&sm.low_empty[j % L::LOWS]);
                 if (++in == L::GROUP || w.last() || j == steps - 1) {
                     mma_commit(&sm.acc_full[g & 1]);
                     ++g;
@@ -422,52 +449,61 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kChunks = DK / 8 / (kC / L::TOK);
-        const int row = me.et % L::TOK, part = me.et / L::TOK;
+        constexpr int kChunks = DK / 8 / (kG / L::TOK);
+        const int row = me.et % L::TOK, part = me.et % kG / L::TOK;
         Sums<DK> acc;
         acc.clear();
         int g = 0, in = 0, first = w.tile;
-        // a group whose products are under way
-        bool pending = false, whole = false;
-        int slot = 0;
+        // The group of tiles before is emptied when this one's are on their way: its
+        // products are done by then, and nothing waits.
+        int pending = -1, slot = 0;  // that group, and the state it completes
+        bool whole = false;
         long long state = 0;
         auto drain = [&]() {
-            wait_bar(&sm.acc_full[(g - 1) & 1], ((g - 1) >> 1) & 1, cx);
+            const int g = pending;
+            wait_bar(&sm.acc_full[g & 1], (g >> 1) & 1, cx);
             tc_fence_after();
-            acc.template add<1>(me, ((g - 1) & 1) * 160);
+            acc.template add<1, DK>(me, (g & 1) * 160);
             tc_fence_before();
-            arrive_warp(&sm.acc_empty[(g - 1) & 1]);
+            arrive_warp(&sm.acc_empty[g & 1]);
             if (whole) {
                 acc.write(p, me, state, slot);
                 acc.clear();
             }
-            pending = false;
         };
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES, len = w.len - w.tile * L::TOK;
-            wait_bar(&sm.low_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
-            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
-            uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
-            uint8_t *lt = smem + L::OFF_LOW + (j & 1) * L::TILE;
+            if ((j & 1) == me.group) {
+                uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+                uint8_t *lt = smem + L::OFF_LOW + j % L::LOWS * L::TILE;
+                wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+                uint4 u[kChunks];
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int col = (part * kChunks + i) * 8;
-                const uint32_t at = tile_at(L::TOK, row, col);
-                float e[8];
-                open8(*reinterpret_cast<const uint4 *>(kt + at), e);
-                phi8(e, p.phi);
-                uint4 high = shut8(e), low = low8(e, high);
-                if (row >= len || col >= p.d) high = low = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(kt + at) = high;
-                *reinterpret_cast<uint4 *>(lt + at) = low;
-                if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kChunks; ++i)
+                    u[i] = *reinterpret_cast<const uint4 *>(
+                        kt + tile_at(L::TOK, row, (part * kChunks + i) * 8));
+                wait_bar(&sm.low_empty[j % L::LOWS], ((j / L::LOWS) & 1) ^ 1, cx);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int col = (part * kChunks + i) * 8;
+                    const uint32_t at = tile_at(L::TOK, row, col);
+                    float e[8];
+                    open8(u[i], e);
+                    phi8(e, p.phi);
+                    uint4 high = shut8(e), low = low8(e, high);
+                    if (row >= len || col >= p.d) high = low = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(kt + at) = high;
+                    *reinterpret_cast<uint4 *>(lt + at) = low;
+                    if (row >= len)
+                        *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+                arrive_warp(&sm.ready[st]);
             }
-            fence_async_shared();
-            arrive_warp(&sm.ready[st]);
-            if (pending) drain();
             if (++in == L::GROUP || w.last() || j == steps - 1) {
+                if (pending >= 0) drain();
                 const bool began = first > 0, ends = w.last();
-                pending = true;
+                pending = g;
                 whole = ends || j == steps - 1;
                 slot = began ? 0 : ends ? -1 : 1;
                 state = (long long)w.b * p.Hk + w.seg;
@@ -483,7 +519,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 in = 0;
             }
         }
-        if (pending) drain();
+        if (pending >= 0) drain();
     }
     end(tmem);
 }
@@ -542,13 +578,13 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
-            mbar_init(&sm.ready[i], kWarpsC);
-            mbar_init(&sm.out[i], kWarpsC);
+            mbar_init(&sm.ready[i], kWarpsG);
+            mbar_init(&sm.out[i], kWarpsG);
         }
         mbar_init(&sm.s_ready, kWarpsC);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.o_full[i], 1);
-            mbar_init(&sm.o_empty[i], kWarpsC);
+            mbar_init(&sm.o_empty[i], kWarpsG);
         }
         mbar_init(&sm.fin, 1);
     });
@@ -601,10 +637,54 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kCols = DK / kParts, kChunks = kCols / 8;
-        const int f0 = me.part * kCols;
-        auto output = [&](int j) {
+        constexpr int kChunks = DK / 16;
+        const int row = me.et & 127, half = me.part & 1;  // of the tile that the group has
+        for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES;
+            if (j == 0 || w.tile == 0) {
+                // another state: the products with the one before are done, all their
+                // outputs having been taken
+                Loaded<DK> S;
+                const long long state = (long long)w.b * p.Hk + w.seg;
+                S.load(p.S + state * p.d * p.d, p.d, me.et);
+                sync_compute();
+#pragma unroll
+                for (int i = 0; i < S.kN; ++i) {
+                    float e[8];
+                    S.get(i, e);
+                    *reinterpret_cast<uint4 *>(smem + L::OFF_S +
+                                               tile_at(DK, S.row(me.et, i), S.col(me.et, i))) =
+                        shut8(e);
+                }
+                if (me.et < DK) {
+                    const float z = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                    const float high = __bfloat162float(__float2bfloat16_rn(z));
+                    *reinterpret_cast<uint32_t *>(smem + L::OFF_Z + sw128_offset(me.et, 0)) =
+                        pack_bf16x2(z, z - high);
+                }
+                fence_async_shared();
+                arrive_warp(&sm.s_ready);
+            }
+            if ((j & 1) != me.group) continue;
+            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
+            uint8_t *tile = smem + st * L::TILE;
+            uint4 u[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                u[i] = *reinterpret_cast<const uint4 *>(
+                    tile + tile_at(128, row, (half * kChunks + i) * 8));
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int col = (half * kChunks + i) * 8;
+                float e[8];
+                open8(u[i], e);
+                phi8(e, p.phi);
+                *reinterpret_cast<uint4 *>(tile + tile_at(128, row, col)) =
+                    col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            arrive_warp(&sm.ready[st]);
+
             wait_bar(&sm.o_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
             const uint32_t o = me.lane_base + (j & 1) * 160;
@@ -617,70 +697,26 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                 const float den = u2f(d0) + u2f(d1);
                 inv = den == 0.f ? 0.f : 1.f / den;
             }
-            uint32_t v[kCols];
-            tmem_get(o + column<DK>(me), v);
-            tc_fence_before();
-            arrive_warp(&sm.o_empty[j & 1]);
-            uint8_t *tile = smem + st * L::TILE;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                float e[8];
+            for (int h = 0; h < DK / 64; ++h) {
+                uint32_t v[32];
+                tmem_get(o + half * (DK == 128 ? 80 : 32) + 32 * h, v);
+                if (h == DK / 64 - 1) {
+                    tc_fence_before();
+                    arrive_warp(&sm.o_empty[j & 1]);
+                }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) e[q] = u2f(v[8 * i + q]) * inv;
-                *reinterpret_cast<uint4 *>(tile + tile_at(128, me.row, f0 + 8 * i)) = shut8(e);
+                for (int i = 0; i < 4; ++i) {
+                    float e[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) e[q] = u2f(v[8 * i + q]) * inv;
+                    *reinterpret_cast<uint4 *>(
+                        tile + tile_at(128, me.row, half * (DK / 2) + 32 * h + 8 * i)) = shut8(e);
+                }
             }
             fence_async_shared();
             arrive_warp(&sm.out[st]);
-        };
-        const int row = me.et & 127, part = me.et >> 7;
-        bool pending = false;
-        for (int j = 0; j < steps; ++j, w.next()) {
-            const int st = j % L::STAGES;
-            if (j == 0 || w.tile == 0) {
-                // another state: the products with the one before are done once the last
-                // of their outputs has been taken by all
-                if (pending) output(j - 1);
-                pending = false;
-                sync_compute();
-                const long long state = (long long)w.b * p.Hk + w.seg;
-                const float *S = p.S + state * p.d * p.d;
-                for (int i = me.et; i < DK * DK / 8; i += kC) {
-                    const int a = i / (DK / 8), c = i % (DK / 8) * 8;
-                    float e[8] = {};
-                    if (a < p.d && c < p.d) {
-                        const float4 *s4 = reinterpret_cast<const float4 *>(S + (long long)a * p.d + c);
-                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
-                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
-                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
-                    }
-                    *reinterpret_cast<uint4 *>(smem + L::OFF_S + tile_at(DK, a, c)) = shut8(e);
-                }
-                if (me.et < DK) {
-                    const float z = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
-                    const float high = __bfloat162float(__float2bfloat16_rn(z));
-                    *reinterpret_cast<uint32_t *>(smem + L::OFF_Z + sw128_offset(me.et, 0)) =
-                        pack_bf16x2(z, z - high);
-                }
-                fence_async_shared();
-                arrive_warp(&sm.s_ready);
-            }
-            wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
-            uint8_t *tile = smem + st * L::TILE;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int col = (part * kChunks + i) * 8;
-                uint4 *at = reinterpret_cast<uint4 *>(tile + tile_at(128, row, col));
-                float e[8];
-                open8(*at, e);
-                phi8(e, p.phi);
-                *at = col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-            arrive_warp(&sm.ready[st]);
-            if (pending) output(j - 1);
-            pending = true;
         }
-        if (pending) output(steps - 1);
     } else if (lane == 0) {
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES, g = w.tile / tiles;
@@ -713,8 +749,11 @@ struct QSmall {
     uint64_t full[4], empty[4], psi[4], s_ready, g_full[2], g_empty[2], t_free, ds_full, ds_empty;
     uint64_t out_full, out_empty, fin;
     long long plan[kThreads / 32 + 2];
-    float z[128], m[kC];
-    float2 red[2][kC];
+    float z[128], m[128];
+    union {
+        float2 red[2][kC];
+        float sum[kWarpsC][128];
+    };
     uint32_t tmem;
     int abort;
 };
@@ -724,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdy,
              const __grid_constant__ CUtensorMap tdq, const Params p) {
     using L = QLayout<DK>;
-    constexpr uint32_t kG = 0, kGStep = 144, kDs = 288;  // TMEM columns
+    constexpr uint32_t kTmG = 0, kTmStep = 144, kDs = 288;  // TMEM columns
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -817,7 +856,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 const uint32_t yb = smem_u32(smem + st * L::STAGE + L::TILE);
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_ss(tmem + kG + (j & 1) * kGStep,
+                    mma_ss(tmem + kTmG + (j & 1) * kTmStep,
                            sdesc_sw128(yb + kmajor_off(ks, 16384), 16, 1024),
                            sdesc_sw128(sb + kmajor_off(ks, L::SATOM), 16, 1024), idG, ks > 0);
                 mma_commit(&sm.g_full[j & 1]);
@@ -840,7 +879,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             tc_fence_after();
             Sums<DK> acc;
             acc.clear();
-            acc.template add<2>(me, kDs);
+            acc.template add<2, 64>(me, kDs);
             tc_fence_before();
             arrive_warp(&sm.ds_empty);
             acc.write(p, me, state, slot);
@@ -852,41 +891,48 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             const long long state = (long long)w.b * p.Hk + w.seg;
             if (j == 0 || w.tile == 0) {
                 sync_compute();  // all are through with the state before
-                const float *S = p.S + state * p.d * p.d;
-                // m = S^T z / z.z, four threads per column
+                Loaded<DK> S;
+                S.load(p.S + state * p.d * p.d, p.d, me.et);
                 if (me.et < 128) sm.z[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 sync_compute();
-                float zz = 0.f;
-                for (int a = 0; a < p.d; ++a) zz = fmaf(sm.z[a], sm.z[a], zz);
-                const int c = me.et & 127, a0 = (me.et >> 7) * (p.d / 4);
-                const int a1 = a0 + p.d / 4;
-                float t = 0.f;
-                if (c < p.d && p.norm)
-#pragma unroll 8
-                    for (int a = a0; a < a1; ++a)
-                        t = fmaf(__ldcg(S + (long long)a * p.d + c), sm.z[a], t);
-                sm.m[me.et] = t;
-                sync_compute();
-                const float over = zz > 0.f && p.norm ? 1.f / zz : 0.f;
-                const float mc =
-                    ((sm.m[c] + sm.m[c + 128]) + (sm.m[c + 256] + sm.m[c + 384])) * over;
-                sync_compute();
-                if (me.et < 128) sm.m[me.et] = mc;
-                sync_compute();
-                for (int i = me.et; i < DK * DK / 8; i += kC) {
-                    const int a = i / (DK / 8), c8 = i % (DK / 8) * 8;
-                    float e[8] = {};
-                    if (a < p.d && c8 < p.d) {
-                        const float4 *s4 =
-                            reinterpret_cast<const float4 *>(S + (long long)a * p.d + c8);
-                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
-                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
-                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
-                        const float z = sm.z[a];
+                // m = S^T z / z.z; the threads of a column chunk are DK / 8 apart
+                float zz = 0.f, mine[8] = {};
+                for (int a = lane; a < DK; a += 32) zz = fmaf(sm.z[a], sm.z[a], zz);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) e[q] = fmaf(-z, sm.m[c8 + q], e[q]);
-                    }
-                    *reinterpret_cast<uint4 *>(smem + L::OFF_S + tile_at(L::SROWS, a, c8)) = shut8(e);
+                for (int o = 16; o > 0; o >>= 1) zz += __shfl_xor_sync(~0u, zz, o);
+#pragma unroll
+                for (int i = 0; i < S.kN; ++i) {
+                    float e[8];
+                    S.get(i, e);
+                    const float za = sm.z[S.row(me.et, i)];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) mine[q] = fmaf(e[q], za, mine[q]);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int o = DK / 8; o < 32; o <<= 1)
+                        mine[q] += __shfl_xor_sync(~0u, mine[q], o);
+                if (lane < DK / 8)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) sm.sum[me.et >> 5][lane * 8 + q] = mine[q];
+                sync_compute();
+                if (me.et < DK) {
+                    float t = 0.f;
+#pragma unroll
+                    for (int q = 0; q < kWarpsC; ++q) t += sm.sum[q][me.et];
+                    sm.m[me.et] = zz > 0.f && p.norm ? t / zz : 0.f;
+                }
+                sync_compute();
+#pragma unroll
+                for (int i = 0; i < S.kN; ++i) {
+                    float e[8];
+                    S.get(i, e);
+                    const int a = S.row(me.et, i), c = S.col(me.et, i);
+                    const float z = sm.z[a];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) e[q] = fmaf(-z, sm.m[c + q], e[q]);
+                    *reinterpret_cast<uint4 *>(smem + L::OFF_S + tile_at(L::SROWS, a, c)) = shut8(e);
                 }
                 if (me.et < DK) {  // row DK: m, row DK + 1: what it loses
                     const float m = me.et < p.d ? sm.m[me.et] : 0.f;
@@ -918,7 +964,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             }
             wait_bar(&sm.g_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
-            const uint32_t gb = me.lane_base + kG + (j & 1) * kGStep;
+            const uint32_t gb = me.lane_base + kTmG + (j & 1) * kTmStep;
             uint32_t v[kCols];
             tmem_get(gb + f0, v);
 #pragma unroll
@@ -1033,14 +1079,14 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
-            mbar_init(&sm.ready[i], kWarpsC);
-            mbar_init(&sm.out[i], kWarpsC);
+            mbar_init(&sm.ready[i], kWarpsG);
+            mbar_init(&sm.out[i], kWarpsG);
         }
         mbar_init(&sm.s_ready, kWarpsC);
         mbar_init(&sm.phi_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.d_full[i], 1);
-            mbar_init(&sm.d_empty[i], kWarpsC);
+            mbar_init(&sm.d_empty[i], kWarpsG);
         }
         mbar_init(&sm.fin, 1);
     });
@@ -1102,67 +1148,21 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
-        constexpr int kCols = DK / kParts, kChunks = kCols / 8;
-        const int f0 = me.part * kCols;
-        auto output = [&](int j, int len) {
-            const int st = j % L::STAGES;
-            wait_bar(&sm.d_full[j & 1], (j >> 1) & 1, cx);
-            tc_fence_after();
-            const uint32_t dk = me.lane_base + (j & 1) * 2 * DK + f0;
-            uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
-            uint32_t v[kCols];
-            tmem_get(dk, v);
-#pragma unroll
-            for (int i = 0; i < kCols; i += 8) {
-                uint8_t *at = kt + tile_at(128, me.row, f0 + i);
-                float x[8];
-                open8(*reinterpret_cast<const uint4 *>(at), x);
-#pragma unroll
-                for (int q = 0; q < 8; q += 2) {
-                    const float2 dz = *reinterpret_cast<const float2 *>(&sm.dz[f0 + i + q]);
-                    float2 g = __fadd2_rn(make_float2(u2f(v[i + q]), u2f(v[i + q + 1])), dz);
-                    if (p.phi) g = __fmul2_rn(g, exp_below(make_float2(x[q], x[q + 1])));
-                    x[q] = g.x;
-                    x[q + 1] = g.y;
-                }
-                *reinterpret_cast<uint4 *>(at) = me.row < len ? shut8(x) : make_uint4(0, 0, 0, 0);
-            }
-            tmem_get(dk + DK, v);
-#pragma unroll
-            for (int i = 0; i < kCols; i += 8) {
-                float o[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) o[q] = u2f(v[i + q]);
-                *reinterpret_cast<uint4 *>(vt + tile_at(128, me.row, f0 + i)) = shut8(o);
-            }
-            tc_fence_before();
-            arrive_warp(&sm.d_empty[j & 1]);
-            fence_async_shared();
-            arrive_warp(&sm.out[st]);
-        };
-        const int row = me.et & 127, part = me.et >> 7;
-        bool pending = false;
-        int len = 0, len_before = 0;
+        constexpr int kChunks = DK / 16;
+        const int row = me.et & 127, half = me.part & 1, f0 = half * (DK / 2);
         for (int j = 0; j < steps; ++j, w.next()) {
-            const int st = j % L::STAGES;
-            len_before = len;
-            len = w.len - w.tile * 128;
+            const int st = j % L::STAGES, len = w.len - w.tile * 128;
             if (j == 0 || w.tile == 0) {
-                if (pending) output(j - 1, len_before);
-                pending = false;
-                sync_compute();
+                Loaded<DK> S;
                 const long long state = (long long)w.b * p.Hk + w.seg;
-                const float *S = p.S + state * p.d * p.d;
-                for (int i = me.et; i < DK * DK / 8; i += kC) {
-                    const int a = i / (DK / 8), c = i % (DK / 8) * 8;
-                    float e[8] = {};
-                    if (a < p.d && c < p.d) {
-                        const float4 *s4 = reinterpret_cast<const float4 *>(S + (long long)a * p.d + c);
-                        const float4 u = __ldcg(s4), v = __ldcg(s4 + 1);
-                        e[0] = u.x, e[1] = u.y, e[2] = u.z, e[3] = u.w;
-                        e[4] = v.x, e[5] = v.y, e[6] = v.z, e[7] = v.w;
-                    }
-                    uint8_t *at = smem + L::OFF_S + tile_at(DK, a, c);
+                S.load(p.S + state * p.d * p.d, p.d, me.et);
+                sync_compute();  // all are through with the state before
+#pragma unroll
+                for (int i = 0; i < S.kN; ++i) {
+                    float e[8];
+                    S.get(i, e);
+                    uint8_t *at =
+                        smem + L::OFF_S + tile_at(DK, S.row(me.et, i), S.col(me.et, i));
                     const uint4 high = shut8(e);
                     *reinterpret_cast<uint4 *>(at) = high;
                     *reinterpret_cast<uint4 *>(at + L::SBLK) = low8(e, high);
@@ -1173,15 +1173,21 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 sync_compute();
                 arrive_warp(&sm.s_ready);
             }
-            wait_bar(&sm.phi_empty, (j & 1) ^ 1, cx);
+            if ((j & 1) != me.group) continue;
             wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
             uint8_t *kt = smem + st * L::STAGE, *vt = kt + L::TILE;
+            uint4 u[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                u[i] = *reinterpret_cast<const uint4 *>(
+                    kt + tile_at(128, row, (half * kChunks + i) * 8));
+            wait_bar(&sm.phi_empty, (j & 1) ^ 1, cx);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int col = (part * kChunks + i) * 8;
+                const int col = (half * kChunks + i) * 8;
                 const uint32_t at = tile_at(128, row, col);
                 float e[8];
-                open8(*reinterpret_cast<const uint4 *>(kt + at), e);
+                open8(u[i], e);
                 phi8(e, p.phi);
                 *reinterpret_cast<uint4 *>(smem + L::OFF_PHI + at) =
                     row < len && col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
@@ -1189,10 +1195,53 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             fence_async_shared();
             arrive_warp(&sm.ready[st]);
-            if (pending) output(j - 1, len_before);
-            pending = true;
+
+            wait_bar(&sm.d_full[j & 1], (j >> 1) & 1, cx);
+            tc_fence_after();
+            const uint32_t dk = me.lane_base + (j & 1) * 2 * DK + f0;
+#pragma unroll
+            for (int h = 0; h < DK / 64; ++h) {
+                uint32_t v[32];
+                uint4 u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    u[i] = *reinterpret_cast<const uint4 *>(
+                        kt + tile_at(128, me.row, f0 + 32 * h + 8 * i));
+                tmem_get(dk + 32 * h, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint8_t *at = kt + tile_at(128, me.row, f0 + 32 * h + i);
+                    float x[8];
+                    open8(u[i / 8], x);
+#pragma unroll
+                    for (int q = 0; q < 8; q += 2) {
+                        const float2 dz =
+                            *reinterpret_cast<const float2 *>(&sm.dz[f0 + 32 * h + i + q]);
+                        float2 g = __fadd2_rn(make_float2(u2f(v[i + q]), u2f(v[i + q + 1])), dz);
+                        if (p.phi) g = __fmul2_rn(g, exp_below(make_float2(x[q], x[q + 1])));
+                        x[q] = g.x;
+                        x[q + 1] = g.y;
+                    }
+                    *reinterpret_cast<uint4 *>(at) =
+                        me.row < len ? shut8(x) : make_uint4(0, 0, 0, 0);
+                }
+                tmem_get(dk + DK + 32 * h, v);
+                if (h == DK / 64 - 1) {
+                    tc_fence_before();
+                    arrive_warp(&sm.d_empty[j & 1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    float o[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) o[q] = u2f(v[i + q]);
+                    *reinterpret_cast<uint4 *>(vt + tile_at(128, me.row, f0 + 32 * h + i)) =
+                        shut8(o);
+                }
+            }
+            fence_async_shared();
+            arrive_warp(&sm.out[st]);
         }
-        if (pending) output(steps - 1, len);
     } else if (lane == 0) {
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES;
