@@ -14,8 +14,10 @@
 //
 // What is rounded to bf16, and why that is enough:
 //   state   phi(k) is kept as two bf16 numbers, high and low (2^-16 of it), since S and
-//           z are results in fp32; V is exact.  The accumulators are emptied into fp32
-//           registers every kGroup tokens: the tensor cores cut off what they add.
+//           z are results in fp32; V is exact.  The tensor cores cut off what they add,
+//           so a product's sum ends after 256 tokens and is added to the ones before,
+//           rounded, by the computing warps.  (That running sum is in TMEM, too: held in
+//           registers it made phi spill, 60 us instead of XX for 4 x 8 x 16384 x 128.)
 //   read    phi(q) and S as one each, z as two: 2^-8 of a weighted mean's terms, as
 //           much as y's own rounding.
 //   qgrad   r (S dy - t z) is the same for S' = S - z m^T, any m.  With m = S^T z / z.z,
@@ -259,37 +261,30 @@ __device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
     reg_fence(r);
 }
 
-// The sums of one state that a computing thread holds: kCols columns of row a, and z[a]
-// (part 0).  In TMEM: S's columns from kSplit on lie 16 further on, behind z's, of which
-// there are kZ.
-template <int DK>
+__device__ __forceinline__ void tmem_put(uint32_t at, const uint32_t (&v)[32]) { tmem_st32(at, v); }
+__device__ __forceinline__ void tmem_put(uint32_t at, const uint32_t (&v)[16]) { tmem_st16(at, v); }
+
+// The sums of one state, of which a computing thread has kCols columns of row a, and
+// z[a] (part 0).  In TMEM the product's columns from kSplit on lie 16 further on, behind
+// z's, of which there are kZ.
+template <int DK, int kSplit, int kZ>
 struct Sums {
     static constexpr int kCols = DK / kParts;
-    float s[kCols], z;
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) s[i] = 0.f;
-        z = 0.f;
-    }
-    template <int kZ, int kSplit>
-    __device__ __forceinline__ void add(const Mine &me, uint32_t base) {
-        const uint32_t at = me.lane_base + base;
-        uint32_t v[kCols];
+    static __device__ __forceinline__ void get(const Mine &me, uint32_t base, uint32_t (&v)[kCols],
+                                               float &z) {
         const int c = me.part * kCols;
-        tmem_get(at + c + (c < kSplit ? 0 : 16), v);
-#pragma unroll
-        for (int e = 0; e < kCols; ++e) s[e] += u2f(v[e]);
+        tmem_get(me.lane_base + base + c + (c < kSplit ? 0 : 16), v);
         if (me.part > 0) return;
-        uint32_t v0 = tmem_ld1(at + kSplit), v1 = 0;
-        if (kZ == 2) v1 = tmem_ld1(at + kSplit + 1);
+        uint32_t v0 = tmem_ld1(me.lane_base + base + kSplit), v1 = 0;
+        if (kZ == 2) v1 = tmem_ld1(me.lane_base + base + kSplit + 1);
         tmem_wait_ld();
         reg_fence(v0);
         reg_fence(v1);
-        z += kZ == 2 ? u2f(v0) + u2f(v1) : u2f(v0);
+        z = kZ == 2 ? u2f(v0) + u2f(v1) : u2f(v0);
     }
     // To the state itself, or to part `slot` (>= 0) of this block.
-    __device__ __forceinline__ void write(const Params &p, const Mine &me, long long state,
-                                          int slot) const {
+    static __device__ __forceinline__ void write(const Params &p, const Mine &me, long long state,
+                                                 int slot, const uint32_t (&v)[kCols], float z) {
         const int a = me.row, c0 = me.part * kCols;
         if (a >= p.d) return;
         const long long dd = (long long)p.d * p.d;
@@ -306,7 +301,7 @@ struct Sums {
         for (int e = 0; e < kCols; e += 4)
             if (c0 + e < p.d)
                 *reinterpret_cast<float4 *>(S + e) =
-                    make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+                    make_float4(u2f(v[e]), u2f(v[e + 1]), u2f(v[e + 2]), u2f(v[e + 3]));
         if (me.part == 0) z_to[a] = p.zsign * z;
     }
 };
@@ -451,9 +446,11 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         const Mine me(tmem);
         constexpr int kChunks = DK / 8 / (kG / L::TOK);
         const int row = me.et % L::TOK, part = me.et % kG / L::TOK;
-        Sums<DK> acc;
-        acc.clear();
+        using Sum = Sums<DK, DK, 1>;
+        constexpr uint32_t kTotal = 320;  // TMEM column of the running sum
         int g = 0, in = 0, first = w.tile;
+        bool fresh = true;  // nothing in the running sum yet
+        float z = 0.f;
         // The group of tiles before is emptied when this one's are on their way: its
         // products are done by then, and nothing waits.
         int pending = -1, slot = 0;  // that group, and the state it completes
@@ -463,12 +460,30 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int g = pending;
             wait_bar(&sm.acc_full[g & 1], (g >> 1) & 1, cx);
             tc_fence_after();
-            acc.template add<1, DK>(me, (g & 1) * 160);
+            uint32_t v[Sum::kCols];
+            float zg = 0.f;
+            Sum::get(me, (g & 1) * 160, v, zg);
             tc_fence_before();
             arrive_warp(&sm.acc_empty[g & 1]);
+            const uint32_t total = me.lane_base + kTotal + me.part * Sum::kCols;
+            if (!fresh) {
+#pragma unroll
+                for (int h = 0; h < Sum::kCols; h += 16) {
+                    uint32_t u[16];
+                    tmem_get(total + h, u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[h + e] = __float_as_uint(u2f(v[h + e]) + u2f(u[e]));
+                }
+                zg += z;
+            }
+            fresh = whole;
+            z = zg;
             if (whole) {
-                acc.write(p, me, state, slot);
-                acc.clear();
+                Sum::write(p, me, state, slot, v, z);
+            } else {
+                tmem_put(total, v);
+                tmem_wait_st();
             }
         };
         for (int j = 0; j < steps; ++j, w.next()) {
@@ -877,12 +892,13 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             wait_bar(&sm.ds_full, drained & 1, cx);
             ++drained;
             tc_fence_after();
-            Sums<DK> acc;
-            acc.clear();
-            acc.template add<2, 64>(me, kDs);
+            using Sum = Sums<DK, 64, 2>;
+            uint32_t v[Sum::kCols];
+            float z = 0.f;
+            Sum::get(me, kDs, v, z);
             tc_fence_before();
             arrive_warp(&sm.ds_empty);
-            acc.write(p, me, state, slot);
+            Sum::write(p, me, state, slot, v, z);
         };
         long long old_state = -1;
         int old_slot = 0;
