@@ -567,6 +567,7 @@ template <int DK>
 struct ReadLayout {
     static constexpr int KB = DK / 64, TILE = KB * 16384, STAGES = DK == 128 ? 4 : 8;
     static constexpr int SATOM = DK * 128;  // rows are features a
+    // S and behind it the columns of z, one operand of DK + 16 columns
     static constexpr int OFF_S = STAGES * TILE, OFF_Z = OFF_S + KB * SATOM;
     static constexpr int OFF_SMALL = OFF_Z + SATOM;
 };
@@ -605,7 +606,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     });
     const Ctx cx{&sm.abort, p.status, kTimeout};
     auto count = [&](int) { return p.G * tiles; };
-    const Piece x = find_piece<kThreads>(p.B, p.Hk, 1, count, sm.plan);
+    const Piece x = even_piece(p.B, p.Hk, 1, p.G * tiles);
     const int steps = (int)(x.x1 - x.x0);
     auto w = walk(count, p, x);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -627,8 +628,8 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t id0 = idesc_bf16(128, 80, 0, 1), id1 = idesc_bf16(128, 64, 0, 1);
-            const uint32_t sb = smem_u32(smem + L::OFF_S), zb = smem_u32(smem + L::OFF_Z);
+            constexpr uint32_t id = idesc_bf16(128, DK + 16, 0, 1);
+            const uint32_t sb = smem_u32(smem + L::OFF_S);
             int states = 0;
             for (int j = 0; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES;
@@ -638,13 +639,9 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                 tc_fence_after();
                 const uint32_t qb = smem_u32(smem + st * L::TILE), o = tmem + (j & 1) * 160;
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint64_t a = sdesc_sw128(qb + kmajor_off(ks, 16384), 16, 1024);
-                    mma_ss(o, a, sdesc_sw128(sb + ks * 2048, zb - sb, 1024), id0, ks > 0);
-                    if (DK == 128)
-                        mma_ss(o + 80, a, sdesc_sw128(sb + L::SATOM + ks * 2048, 0, 1024), id1,
-                               ks > 0);
-                }
+                for (int ks = 0; ks < DK / 16; ++ks)
+                    mma_ss(o, sdesc_sw128(qb + kmajor_off(ks, 16384), 16, 1024),
+                           sdesc_sw128(sb + ks * 2048, L::SATOM, 1024), id, ks > 0);
                 mma_commit(&sm.o_full[j & 1]);
             }
             mma_commit(&sm.fin);
@@ -662,6 +659,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                 Loaded<DK> S;
                 const long long state = (long long)w.b * p.Hk + w.seg;
                 S.load(p.S + state * p.d * p.d, p.d, me.et);
+                const float z = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 sync_compute();
 #pragma unroll
                 for (int i = 0; i < S.kN; ++i) {
@@ -672,7 +670,6 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                         shut8(e);
                 }
                 if (me.et < DK) {
-                    const float z = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                     const float high = __bfloat162float(__float2bfloat16_rn(z));
                     *reinterpret_cast<uint32_t *>(smem + L::OFF_Z + sw128_offset(me.et, 0)) =
                         pack_bf16x2(z, z - high);
@@ -705,7 +702,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
             const uint32_t o = me.lane_base + (j & 1) * 160;
             float inv = 1.f;
             if (p.norm) {
-                uint32_t d0 = tmem_ld1(o + 64), d1 = tmem_ld1(o + 65);
+                uint32_t d0 = tmem_ld1(o + DK), d1 = tmem_ld1(o + DK + 1);
                 tmem_wait_ld();
                 reg_fence(d0);
                 reg_fence(d1);
@@ -715,7 +712,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 #pragma unroll
             for (int h = 0; h < DK / 64; ++h) {
                 uint32_t v[32];
-                tmem_get(o + half * (DK == 128 ? 80 : 32) + 32 * h, v);
+                tmem_get(o + half * (DK / 2) + 32 * h, v);
                 if (h == DK / 64 - 1) {
                     tc_fence_before();
                     arrive_warp(&sm.o_empty[j & 1]);
@@ -807,7 +804,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     });
     const Ctx cx{&sm.abort, p.status, kTimeout};
     auto count = [&](int) { return p.G * tiles; };
-    const Piece x = find_piece<kThreads>(p.B, p.Hk, 2, count, sm.plan);
+    const Piece x = even_piece(p.B, p.Hk, 2, p.G * tiles);
     const int steps = (int)(x.x1 - x.x0);
     if (threadIdx.x == 0) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
     auto w = walk(count, p, x);
@@ -837,49 +834,73 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             constexpr uint32_t id0 = idesc_bf16(128, 80, 1, 1), id1 = idesc_bf16(128, 64, 1, 1);
             constexpr uint32_t lboA = DK == 128 ? 16384 : 0;
             const uint32_t sb = smem_u32(smem + L::OFF_S), tb = smem_u32(smem + L::OFF_T);
-            int states = 0, ended = 0;
-            bool first = true, last = false;  // of the tile before: in its state's piece
-            // the sums of tile j, once psi and t are there
-            auto sums = [&](int j, bool first, bool last) {
-                const int st = j % L::STAGES;
-                if (first) wait_bar_spin(&sm.ds_empty, (ended & 1) ^ 1, cx);
-                wait_bar_spin(&sm.psi[st], (j / L::STAGES) & 1, cx);
-                tc_fence_after();
-                const uint32_t qb = smem_u32(smem + st * L::STAGE), yb = qb + L::TILE;
+            // G of tile i and the sums of tile j <= i, whichever has its operands: a tile
+            // that is still under way holds back no sums, which free a place for the next
+            auto v = w;
+            int i = 0, j = 0, states = 0, ended = 0;
+            long long deadline = 0;
+            for (int polls = 0; j < steps;) {
+                if (j < i) {
+                    const int st = j % L::STAGES;
+                    const bool first = j == 0 || v.tile == 0, last = v.last() || j == steps - 1;
+                    if (mbar_test_wait(&sm.psi[st], (j / L::STAGES) & 1) &&
+                        (!first || mbar_test_wait(&sm.ds_empty, (ended & 1) ^ 1))) {
+                        tc_fence_after();
+                        const uint32_t qb = smem_u32(smem + st * L::STAGE), yb = qb + L::TILE;
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint64_t a = sdesc_sw128(qb + ks * 2048, lboA, 1024);
-                    const uint32_t more = !first || ks > 0;
-                    mma_ss(tmem + kDs, a, sdesc_sw128(yb + ks * 2048, tb - yb, 1024), id0, more);
-                    if (DK == 128)
-                        mma_ss(tmem + kDs + 80, a, sdesc_sw128(yb + 16384 + ks * 2048, 0, 1024),
-                               id1, more);
+                        for (int ks = 0; ks < 8; ++ks) {
+                            const uint64_t a = sdesc_sw128(qb + ks * 2048, lboA, 1024);
+                            const uint32_t more = !first || ks > 0;
+                            mma_ss(tmem + kDs, a, sdesc_sw128(yb + ks * 2048, tb - yb, 1024), id0,
+                                   more);
+                            if (DK == 128)
+                                mma_ss(tmem + kDs + 80, a,
+                                       sdesc_sw128(yb + 16384 + ks * 2048, 0, 1024), id1, more);
+                        }
+                        mma_commit(&sm.empty[st]);
+                        mma_commit(&sm.t_free);
+                        if (last) {
+                            mma_commit(&sm.ds_full);
+                            ++ended;
+                        }
+                        ++j;
+                        v.next();
+                        polls = 0;
+                        continue;
+                    }
                 }
-                mma_commit(&sm.empty[st]);
-                mma_commit(&sm.t_free);
-                if (last) {
-                    mma_commit(&sm.ds_full);
-                    ++ended;
-                }
-            };
-            for (int j = 0; j < steps; ++j, w.next()) {
-                const int st = j % L::STAGES;
-                if (j == 0 || w.tile == 0) wait_bar_spin(&sm.s_ready, states++ & 1, cx);
-                wait_bar_spin(&sm.full[st], (j / L::STAGES) & 1, cx);
-                wait_bar_spin(&sm.g_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
-                tc_fence_after();
-                const uint32_t yb = smem_u32(smem + st * L::STAGE + L::TILE);
+                if (i < steps) {
+                    const int st = i % L::STAGES;
+                    const bool first = i == 0 || w.tile == 0;
+                    if (mbar_test_wait(&sm.full[st], (i / L::STAGES) & 1) &&
+                        mbar_test_wait(&sm.g_empty[i & 1], ((i >> 1) & 1) ^ 1) &&
+                        (!first || mbar_test_wait(&sm.s_ready, states & 1))) {
+                        tc_fence_after();
+                        const uint32_t yb = smem_u32(smem + st * L::STAGE + L::TILE);
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_ss(tmem + kTmG + (j & 1) * kTmStep,
-                           sdesc_sw128(yb + kmajor_off(ks, 16384), 16, 1024),
-                           sdesc_sw128(sb + kmajor_off(ks, L::SATOM), 16, 1024), idG, ks > 0);
-                mma_commit(&sm.g_full[j & 1]);
-                if (j > 0) sums(j - 1, first, last);
-                first = j == 0 || w.tile == 0;
-                last = w.last() || j == steps - 1;
+                        for (int ks = 0; ks < DK / 16; ++ks)
+                            mma_ss(tmem + kTmG + (i & 1) * kTmStep,
+                                   sdesc_sw128(yb + kmajor_off(ks, 16384), 16, 1024),
+                                   sdesc_sw128(sb + kmajor_off(ks, L::SATOM), 16, 1024), idG,
+                                   ks > 0);
+                        mma_commit(&sm.g_full[i & 1]);
+                        states += first;
+                        ++i;
+                        w.next();
+                        polls = 0;
+                        continue;
+                    }
+                }
+                if ((++polls & 63) == 0) {
+                    if (*cx.abort) break;
+                    const long long now = clock64();
+                    if (polls == 64) deadline = now + cx.timeout;
+                    if (now > deadline) {
+                        raise_timeout(cx, smem_u32(&sm.psi[0]));
+                        break;
+                    }
+                }
             }
-            if (steps > 0) sums(steps - 1, first, last);
             mma_commit(&sm.fin);
             settle_wait(&sm.fin, 0);
         }
@@ -906,10 +927,11 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             const int st = j % L::STAGES;
             const long long state = (long long)w.b * p.Hk + w.seg;
             if (j == 0 || w.tile == 0) {
-                sync_compute();  // all are through with the state before
                 Loaded<DK> S;
+                const float z_mine = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 S.load(p.S + state * p.d * p.d, p.d, me.et);
-                if (me.et < 128) sm.z[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                sync_compute();  // all are through with the state before
+                if (me.et < 128) sm.z[me.et] = z_mine;
                 sync_compute();
                 // m = S^T z / z.z; the threads of a column chunk are DK / 8 apart
                 float zz = 0.f, mine[8] = {};
@@ -1172,6 +1194,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 Loaded<DK> S;
                 const long long state = (long long)w.b * p.Hk + w.seg;
                 S.load(p.S + state * p.d * p.d, p.d, me.et);
+                const float dz = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 sync_compute();  // all are through with the state before
 #pragma unroll
                 for (int i = 0; i < S.kN; ++i) {
@@ -1183,8 +1206,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     *reinterpret_cast<uint4 *>(at) = high;
                     *reinterpret_cast<uint4 *>(at + L::SBLK) = low8(e, high);
                 }
-                if (me.et < 128)
-                    sm.dz[me.et] = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                if (me.et < 128) sm.dz[me.et] = dz;
                 fence_async_shared();
                 sync_compute();
                 arrive_warp(&sm.s_ready);

@@ -153,6 +153,19 @@ struct Piece {
     }
 };
 
+// The same where every entry has `tiles` tiles a stretch.
+__device__ __forceinline__ Piece even_piece(int B, int segs, int least, int tiles) {
+    Piece p;
+    p.total = (long long)B * segs * tiles;
+    p.pieces = (int)min((long long)gridDim.x, max(1LL, p.total / least));
+    p.x0 = p.total * min((int)blockIdx.x, p.pieces) / p.pieces;
+    p.x1 = p.total * min((int)blockIdx.x + 1, p.pieces) / p.pieces;
+    const long long per = (long long)segs * tiles;
+    p.b = (int)(p.x0 / per);
+    p.rest = p.x0 - p.b * per;
+    return p;
+}
+
 // All kThreads threads of a block call this; `shared` has kThreads / 32 + 2 numbers.
 template <int kThreads, typename F>
 __device__ __forceinline__ Piece find_piece(int B, int segs, int least, F tiles_of,

@@ -22,6 +22,7 @@
 #include "la_internal.h"
 #include "la_layer.cuh"
 #include "la_tc.h"
+#include "la_tc_common.cuh"
 #include "la_tc_host.h"
 #include "la_tc_ptx.cuh"
 
@@ -38,8 +39,9 @@ struct Params {
     la_strides sq, so, sk, sv;
     const int *table, *lengths;
     long long table_stride;
-    int pages, page_size, max_pages;
+    int pages, page_size, max_pages, page_shift;  // page_size is 2^page_shift, or -1
     int B, Hk, G, T, d, window;
+    int *status;
     int row_tile, row_tiles;  // queries of a block, tiles of them per head of keys
     float scale2;             // scale log2(e)
     int4 *info;               // of each block: see Plan
@@ -168,6 +170,22 @@ __device__ __forceinline__ Slot slot_of(const Params &p, const Place<kTile> &c) 
     return s;
 }
 
+// The same of a warp's whole tile, where pages hold whole tiles: the first key, whatever
+// the bounds are.
+template <int kTile, int kKeys>
+__device__ __forceinline__ Slot tile_of(const Params &p, const Place<kTile> &c) {
+    Slot s;
+    s.key = (c.s.first + c.tile) * kTile + (threadIdx.x >> 5) * kKeys;
+    s.page = -1;
+    const int column = p.page_shift >= 0 ? s.key >> p.page_shift : s.key / p.page_size;
+    s.slot = s.key - column * p.page_size;
+    if (s.key < c.s.hi && s.key + kKeys > c.s.lo) {
+        s.page = __ldg(p.table + c.b * p.table_stride + column);
+        if (s.page >= p.pages) s.page = -1;
+    }
+    return s;
+}
+
 // Output rows of a block: the queries of one tile.  Row r of the head's G T queries is
 // query t = r % T of head r / T of the group.
 template <typename T>
@@ -224,45 +242,80 @@ __device__ __forceinline__ void mma(float (&c)[4], const unsigned (&a)[4], unsig
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int kD>
+// kUnit: bytes of a copy (4 or 16 with cp.async, 2 with plain loads, rows kPitch apart in
+// shared memory), or 0: tiles by TMA, in atoms of 64 features with the 128-byte swizzle.
+template <int kD, int kUnit>
 struct Half {
     static constexpr int kKeys = 16, kTile = kWarps * kKeys;
     static constexpr int kPitch = kD + 8;  // 16 bytes more than the row: no bank conflicts
-    static constexpr int kStage = 2 * kKeys * kPitch * 2;  // bytes, of a warp
-    static constexpr int kStages = kD == 64 ? 5 : kD == 96 || kD == 192 ? 4 : 3;
+    static constexpr int kSide = kUnit ? kKeys * kPitch * 2 : kKeys * kD * 2;  // keys, or values
+    static constexpr int kStage = 2 * kSide;                                   // of a warp
+    static constexpr int kStages = kD == 64 ? 5 : kD == 192 ? 4 : 3;
     static constexpr int kBlocks = kD <= 128 ? 2 : 1;  // per SM
     static constexpr int kOutPitch = kD + 4;
     static constexpr int kOffOut = kWarps * kStages * kStage;
     static constexpr int kOffMl = kOffOut + kRowTile * kOutPitch * 4;
     static constexpr int kOffMask = kOffMl + (kWarps + 1) * kRowTile * 8;
-    static constexpr int kOffPlan = kOffMask + kWarps * kStages * 4;
-    static constexpr int kSmem = kOffPlan + (kWarps + 2) * 8;
-    static_assert(kOffPlan % 8 == 0 && kSmem <= 232448, "shared memory");
+    static constexpr int kOffBar = kOffMask + kWarps * kStages * 4;
+    static constexpr int kOffPlan = kOffBar + kWarps * kStages * 8;
+    static constexpr int kSmem = kOffPlan + (kWarps + 2) * 8 + 16 + (kUnit ? 0 : 1024);
+    static_assert(kOffBar % 8 == 0 && kSmem <= 232448, "shared memory");
     static_assert(kSmem + 1024 <= 233472 / kBlocks, "blocks per SM");
 };
+
+// Rows of one side of the cache as a TMA tensor [page][head][slot][feature].
+__device__ __forceinline__ void load_keys(unsigned dst, const CUtensorMap *map, uint64_t *bar,
+                                          int c, int slot, int h, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map), "r"(c), "r"(slot), "r"(h),
+        "r"(page), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // 16 queries of one head of keys (the heads that share it, and the call's tokens)
 // against 16 keys per warp and step: m16n8k16 products, whose 16 rows would be empty
 // for one query, but the tensor cores wait for the memory all the same.  P is rounded
-// to bf16 for its product with the values; l sums the rounded ones, so that the
-// weights still add to one.
+// to bf16 for its product with the values; l sums the rounded ones (a product with a
+// column of ones), so that the weights still add to one.
 template <int kD, int kUnit>
-__global__ void __launch_bounds__(kThreads, Half<kD>::kBlocks)
-paged_half_kernel(const __grid_constant__ Params p) {
-    using L = Half<kD>;
+__global__ void __launch_bounds__(kThreads, Half<kD, kUnit>::kBlocks)
+paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv) {
+    using L = Half<kD, kUnit>;
     using T = __nv_bfloat16;
     constexpr int kTile = L::kTile, kKeys = L::kKeys;
-    extern __shared__ __align__(128) char smem[];
+    constexpr unsigned kAtom = kUnit ? 128 : kKeys * 128;  // bytes from 64 features to the next
+    extern __shared__ __align__(128) char raw[];
+    char *smem = kUnit ? raw
+                       : reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                  ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     char *ring = smem + warp * L::kStages * L::kStage;
     float *obuf = reinterpret_cast<float *>(smem + L::kOffOut);
     float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
     unsigned *masks = reinterpret_cast<unsigned *>(smem + L::kOffMask) + warp * L::kStages;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * L::kStages;
+    int *abort = reinterpret_cast<int *>(smem + L::kOffPlan + (kWarps + 2) * 8);
+    const tcc::Ctx cx{abort, p.status, 1LL << 32};
     const int segs = p.Hk * p.row_tiles;
 
     tc::grid_dep_launch();
     for (int i = threadIdx.x; i < L::kOffOut / 16; i += kThreads)
         reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) *abort = 0;
+    if (kUnit == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < L::kStages; ++i) tc::mbar_init(bars + i, 1);
+            tc::fence_mbar_init();
+        }
+        tc::fence_async_shared();
+    }
     Piece piece;
     Place<kTile> c =
         find_place<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan), piece);
@@ -271,31 +324,73 @@ paged_half_kernel(const __grid_constant__ Params p) {
     const int steps = (int)(x1 - piece.x0);
     if (steps == 0) return;
 
-    // the copying side, some tiles ahead
+    // the copying side, some tiles ahead; `ahead` is where the next tile's keys lie
     Place<kTile> f = c;
     int f_left = steps, f_stage = 0;
-    Slot ahead = slot_of<kTile, kKeys>(p, f);
+    Slot ahead;
+    auto look = [&]() {
+        if constexpr (kUnit)
+            ahead = slot_of<kTile, kKeys>(p, f);
+        else
+            ahead = tile_of<kTile, kKeys>(p, f);
+    };
+    look();
     auto fetch = [&]() {
         if (f_left > 0) {
-            const int h = f.seg / p.row_tiles;
-            const bool ok = ahead.page >= 0;
-            copy_rows<T, kD, L::kPitch, kKeys, kUnit>(
-                p, reinterpret_cast<T *>(ring + f_stage * L::kStage),
-                ahead.page * p.sk.b + h * p.sk.h + ahead.slot * p.sk.n,
-                ahead.page * p.sv.b + h * p.sv.h + ahead.slot * p.sv.n, ok);
-            const unsigned mask = __ballot_sync(~0u, ok);
+            const int h = p.row_tiles == 1 ? f.seg : f.seg / p.row_tiles;
+            char *stage = ring + f_stage * L::kStage;
+            unsigned mask;
+            if constexpr (kUnit) {
+                const bool ok = ahead.page >= 0;
+                copy_rows<T, kD, L::kPitch, kKeys, kUnit ? kUnit : 16>(
+                    p, reinterpret_cast<T *>(stage),
+                    ahead.page * p.sk.b + h * p.sk.h + ahead.slot * p.sk.n,
+                    ahead.page * p.sv.b + h * p.sv.h + ahead.slot * p.sv.n, ok);
+                mask = __ballot_sync(~0u, ok);
+            } else {
+                // the tile's keys are in one page
+                const int first = max(f.s.lo - ahead.key, 0), n = min(f.s.hi - ahead.key, kKeys);
+                mask = ahead.page >= 0 && n > first ? (0xffffu >> (kKeys - n)) >> first << first : 0;
+                if (lane == 0) {
+                    if (mask == 0) {
+                        tc::mbar_arrive(bars + f_stage);
+                    } else {
+                        const int atoms = (p.d + 63) / 64;
+                        tc::mbar_arrive_expect_tx(bars + f_stage, atoms * 2 * kKeys * 128);
+                        for (int a = 0; a < atoms; ++a) {
+                            const unsigned at = tc::smem_u32(stage) + a * kAtom;
+                            load_keys(at, &tk, bars + f_stage, 64 * a, ahead.slot, h, ahead.page);
+                            load_keys(at + L::kSide, &tv, bars + f_stage, 64 * a, ahead.slot, h,
+                                      ahead.page);
+                        }
+                    }
+                }
+            }
             if (lane == 0) masks[f_stage] = mask;
             f_stage = f_stage + 1 == L::kStages ? 0 : f_stage + 1;
             if (--f_left > 0) {
                 f.next(p, segs);
-                ahead = slot_of<kTile, kKeys>(p, f);
+                look();
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (kUnit != 0) asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int i = 0; i < L::kStages - 1; ++i) fetch();
 
+    // where a lane's rows for ldmatrix lie: 16 features further on, and 64
+    unsigned k_at[4], v_at[4];
+    {
+        const int kr = (lane & 7) + (lane >> 4) * 8, vr = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int kc = 2 * i + ((lane >> 3) & 1), vc = 2 * i + (lane >> 4);
+            k_at[i] = kUnit ? kr * L::kPitch * 2 + kc * 16 : kr * 128 + (kc ^ (kr & 7)) * 16;
+            v_at[i] = kUnit ? vr * L::kPitch * 2 + vc * 16 : vr * 128 + (vc ^ (vr & 7)) * 16;
+            v_at[i] += L::kSide;
+        }
+    }
     int stage = 0;
+    unsigned parity = 0;
     for (int left = steps; left > 0;) {
         // ---- a stretch of tiles with the same queries
         const int h = c.seg / p.row_tiles, row0 = (c.seg - h * p.row_tiles) * p.row_tile;
@@ -321,12 +416,12 @@ paged_half_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) ldmatrix4(a[ks], at + ks * 32);
         }
-        float o[kD / 8][4];
+        float o[kD / 8][4], sums[4] = {};  // the outputs times l, and l
 #pragma unroll
         for (int j = 0; j < kD / 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float m[2] = {-INFINITY, -INFINITY};
         // the last key of this lane's two queries
         int last[2];
 #pragma unroll
@@ -335,38 +430,60 @@ paged_half_kernel(const __grid_constant__ Params p) {
 
         for (int it = 0; it < n; ++it) {
             fetch();
-            asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+            if constexpr (kUnit != 0)
+                asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+            else
+                tcc::wait_bar(bars + stage, parity, cx);
             __syncwarp();
-            const char *st = ring + stage * L::kStage;
+            const unsigned st = tc::smem_u32(ring + stage * L::kStage);
+            T *values = reinterpret_cast<T *>(ring + stage * L::kStage + L::kSide);
             const unsigned mask = masks[stage];
             const int key0 = (c.s.first + c.tile) * kTile + warp * kKeys;
             float s[2][4] = {};
-            {
-                const unsigned at =
-                    tc::smem_u32(st) +
-                    ((lane & 7) + (lane >> 4) * 8) * (L::kPitch * 2) + ((lane >> 3) & 1) * 16;
 #pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    unsigned b[4];
-                    ldmatrix4(b, at + ks * 32);
-                    mma(s[0], a[ks], b[0], b[1]);
-                    mma(s[1], a[ks], b[2], b[3]);
-                }
+            for (int ks = 0; ks < kD / 16; ++ks) {
+                unsigned b[4];
+                ldmatrix4(b, st + k_at[ks & 3] + (ks >> 2) * kAtom);
+                mma(s[0], a[ks], b[0], b[1]);
+                mma(s[1], a[ks], b[2], b[3]);
             }
-            const bool whole = mask == 0xffffu && all_see(p, c.s, key0, kKeys);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[j][e] *= p.scale2;
-                    if (!whole) {
+                for (int e = 0; e < 4; ++e) s[j][e] *= p.scale2;
+            const bool whole = mask == 0xffffu && all_see(p, c.s, key0, kKeys);
+            // A weight of 0 does not keep a value that is not finite out of a sum: slots
+            // that hold no key of the sequence become 0, and a tile where queries look at
+            // different keys takes values that are not finite singly.
+            bool singly = false;
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int i = j * 8 + (lane & 3) * 2 + (e & 1), key = key0 + i;
                         const int end = last[e >> 1];
                         if (!(mask >> i & 1) || key > end ||
                             (p.window > 0 && key <= end - p.window))
                             s[j][e] = -INFINITY;
                     }
+                if (kUnit == 0 && mask != 0xffffu) {
+                    for (int i = 0; i < kKeys; ++i)
+                        if (!(mask >> i & 1))
+                            for (int q = 0; q < kD / 64; ++q)
+                                reinterpret_cast<unsigned *>(values)[(q * kAtom + i * 128) / 4 +
+                                                                     lane] = 0;
+                    tc::fence_async_shared();  // before the next tile arrives here
+                    __syncwarp();
                 }
+                if (p.T > 1) {
+                    bool odd = false;
+                    for (int i = lane; i < L::kSide / 2; i += 32)
+                        odd |= (kUnit == 0 || i % L::kPitch < kD) &&
+                               !(fabsf(to_f(values[i])) < INFINITY);
+                    singly = __any_sync(~0u, odd);
+                }
+            }
             float top[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -380,10 +497,11 @@ paged_half_kernel(const __grid_constant__ Params p) {
                 float w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    w[i] = exp2f(m[i] - finite_max(top[i]));
+                    w[i] = exp2_fast(m[i] - finite_max(top[i]));
                     m[i] = top[i];
-                    l[i] *= w[i];
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[e] *= w[e >> 1];
 #pragma unroll
                 for (int j = 0; j < kD / 8; ++j)
 #pragma unroll
@@ -391,71 +509,57 @@ paged_half_kernel(const __grid_constant__ Params p) {
             }
             unsigned pa[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int i = 0; i < 2; ++i) {
+                const float mi = finite_max(m[i]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float mi = finite_max(m[i]);
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(exp2f(s[j][2 * i] - mi),
-                                                                   exp2f(s[j][2 * i + 1] - mi));
-                    l[i] += __low2float(w) + __high2float(w);
-                    pa[2 * j + i] = reinterpret_cast<const unsigned &>(w);
-                }
-            {
-                const unsigned at = tc::smem_u32(st) + kKeys * L::kPitch * 2 +
-                                    (lane & 15) * (L::kPitch * 2) + (lane >> 4) * 16;
-                // A weight of 0 does not keep a value that is not finite out of a sum: a
-                // tile where queries look at different keys takes such values singly.
-                bool singly = false;
-                if (p.T > 1 && !whole) {
-                    const T *v = reinterpret_cast<const T *>(st) + kKeys * L::kPitch;
-                    bool odd = false;
-                    for (int i = lane; i < kKeys * L::kPitch; i += 32)
-                        odd |= i % L::kPitch < kD && !(fabsf(to_f(v[i])) < INFINITY);
-                    singly = __any_sync(~0u, odd);
-                }
-                if (singly) {
-                    const T *v = reinterpret_cast<const T *>(st) + kKeys * L::kPitch;
-                    for (int i = 0; i < kKeys; ++i) {
-                        const int from = (lane & 28) + (i & 7) / 2;
-                        unsigned u[2];  // of the two queries
+                for (int j = 0; j < 2; ++j)
+                    pa[2 * j + i] = tc::pack_bf16x2(exp2_fast(s[j][2 * i] - mi),
+                                                    exp2_fast(s[j][2 * i + 1] - mi));
+            }
+            mma(sums, pa, 0x3F803F80u, 0x3F803F80u);
+            if (singly) {
+                for (int i = 0; i < kKeys; ++i) {
+                    const int from = (lane & 28) + (i & 7) / 2;
+                    unsigned u[2];  // of the two queries
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const unsigned lo = __shfl_sync(~0u, pa[r], from);
-                            const unsigned hi = __shfl_sync(~0u, pa[2 + r], from);
-                            u[r] = i < 8 ? lo : hi;
-                            u[r] = i & 1 ? u[r] & 0xffff0000u : u[r] << 16;
-                        }
-#pragma unroll
-                        for (int j = 0; j < kD / 8; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (u[e >> 1])
-                                    o[j][e] = fmaf(__uint_as_float(u[e >> 1]),
-                                                   to_f(v[i * L::kPitch + 8 * j +
-                                                          (lane & 3) * 2 + (e & 1)]),
-                                                   o[j][e]);
+                    for (int r = 0; r < 2; ++r) {
+                        const unsigned lo = __shfl_sync(~0u, pa[r], from);
+                        const unsigned hi = __shfl_sync(~0u, pa[2 + r], from);
+                        u[r] = i < 8 ? lo : hi;
+                        u[r] = i & 1 ? u[r] & 0xffff0000u : u[r] << 16;
                     }
-                } else
+#pragma unroll
+                    for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int col = 8 * j + (lane & 3) * 2 + (e & 1);
+                            const unsigned at =
+                                kUnit ? i * L::kPitch * 2 + col * 2
+                                      : (col >> 6) * kAtom + tc::sw128_offset(i, col & 63);
+                            if (u[e >> 1])
+                                o[j][e] = fmaf(__uint_as_float(u[e >> 1]), to_f(values[at / 2]),
+                                               o[j][e]);
+                        }
+                }
+            } else {
 #pragma unroll
                 for (int j = 0; j < kD / 16; ++j) {
                     unsigned b[4];
-                    ldmatrix4_t(b, at + j * 32);
+                    ldmatrix4_t(b, st + v_at[j & 3] + (j >> 2) * kAtom);
                     mma(o[2 * j], pa, b[0], b[1]);
                     mma(o[2 * j + 1], pa, b[2], b[3]);
                 }
             }
             __syncwarp();  // the stage may be filled again
-            stage = stage + 1 == L::kStages ? 0 : stage + 1;
+            if (++stage == L::kStages) stage = 0, parity ^= 1;
             c.tile += 1;
         }
         // ---- the warps' parts together, in order
+        const float l[2] = {sums[0], sums[2]};
+        if ((lane & 3) == 0)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(~0u, l[i], 1);
-            l[i] += __shfl_xor_sync(~0u, l[i], 2);
-            if ((lane & 3) == 0)
+            for (int i = 0; i < 2; ++i)
                 ml[warp * kRowTile + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
-        }
         __syncthreads();
         float w[2];
 #pragma unroll
@@ -466,8 +570,8 @@ paged_half_kernel(const __grid_constant__ Params p) {
             for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[q * kRowTile + r].x);
 #pragma unroll
             for (int q = 0; q < kWarps; ++q)
-                sum += ml[q * kRowTile + r].y * exp2f(ml[q * kRowTile + r].x - finite_max(top));
-            w[i] = exp2f(m[i] - finite_max(top));
+                sum += ml[q * kRowTile + r].y * exp2_fast(ml[q * kRowTile + r].x - finite_max(top));
+            w[i] = exp2_fast(m[i] - finite_max(top));
             if (warp == 0 && (lane & 3) == 0) ml[kWarps * kRowTile + r] = make_float2(top, sum);
         }
         for (int q = 0; q < kWarps; ++q) {
@@ -494,7 +598,14 @@ paged_half_kernel(const __grid_constant__ Params p) {
         c.tile -= 1;
         if (left > 0) c.next(p, segs);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (kUnit != 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (*abort) {  // a wait gave up: what is under way lands before the block ends
+        for (int i = 0, q = 0, ph = 0; i < steps; ++i) {
+            if (i + L::kStages >= steps) tcc::settle_wait(bars + q, ph);
+            if (++q == L::kStages) q = 0, ph ^= 1;
+        }
+    }
 }
 
 // ------------------------------------------------------------------ fp32
@@ -722,10 +833,15 @@ paged_full_kernel(const __grid_constant__ Params p) {
 }
 
 // Joins the stretches that lie in several blocks: block i looks at the stretch that
-// piece i + 1 continues, if it began in piece i, one query of it.
+// piece i + 1 continues, if it began in piece i, one query of it.  A warp's lanes find
+// the pieces' factors, 32 at a time; then kJoin groups of threads take every kJoin-th
+// piece of the output.
+constexpr int kJoin = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(LA_MAX_D) paged_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoin *LA_MAX_D) paged_join_kernel(const __grid_constant__ Params p) {
     tc::grid_dep_wait();
+    __shared__ float sum[kJoin][LA_MAX_D], factor[32], stat[2];
     const int i = blockIdx.x + 1, r = blockIdx.y;
     const int4 info = p.info[i];
     if (info.y < 0 || info.z != i - 1) return;
@@ -734,24 +850,42 @@ __global__ void __launch_bounds__(LA_MAX_D) paged_join_kernel(const __grid_const
     const int b = (int)(stretch / segs), seg = (int)(stretch - (long long)b * segs);
     const int h = seg / p.row_tiles, row0 = (seg - h * p.row_tiles) * p.row_tile;
     if (row0 + r >= p.G * p.T) return;
-    const int i0 = info.z, i1 = info.w;
+    const int i0 = info.z, i1 = info.w, lane = threadIdx.x & 31;
+    const int cols = blockDim.x / kJoin, e = threadIdx.x % cols, group = threadIdx.x / cols;
     auto part = [&](int q) {
         return p.part + ((long long)(2 * q + (q == i0)) * p.row_tile + r) * (p.d + 2);
     };
-    float top = -INFINITY;
-    for (int q = i0; q <= i1; ++q) top = fmaxf(top, __ldcg(part(q) + p.d));
-    top = finite_max(top);
-    const int e = threadIdx.x;
-    if (e >= p.d) return;
-    float sum = 0.f, y = 0.f;
-#pragma unroll 4
-    for (int q = i0; q <= i1; ++q) {
-        const float *w = part(q), f = exp2f(__ldcg(w + p.d) - top);
-        sum = fmaf(__ldcg(w + p.d + 1), f, sum);
-        y = fmaf(__ldcg(w + e), f, y);
+    if (threadIdx.x < 32) {
+        float top = -INFINITY;
+        for (int q = i0 + lane; q <= i1; q += 32) top = fmaxf(top, __ldcg(part(q) + p.d));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        top = finite_max(top);
+        float l = 0.f;
+        for (int q = i0 + lane; q <= i1; q += 32)
+            l = fmaf(__ldcg(part(q) + p.d + 1), exp2f(__ldcg(part(q) + p.d) - top), l);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        if (lane == 0) stat[0] = top, stat[1] = l;
     }
+    float y = 0.f;
+    for (int q0 = i0; q0 <= i1; q0 += 32) {
+        __syncthreads();
+        if (threadIdx.x < 32 && q0 + lane <= i1)
+            factor[lane] = exp2f(__ldcg(part(q0 + lane) + p.d) - stat[0]);
+        __syncthreads();
+        if (e < p.d)
+#pragma unroll 4
+            for (int q = group; q < min(32, i1 + 1 - q0); q += kJoin)
+                y = fmaf(__ldcg(part(q0 + q) + e), factor[q], y);
+    }
+    if (e < p.d) sum[group][e] = y;
+    __syncthreads();
+    if (group > 0 || e >= p.d) return;
+#pragma unroll
+    for (int g = 1; g < kJoin; ++g) y += sum[g][e];
     T *out = static_cast<T *>(p.out) + row_offset<T>(p, p.so, b, h, row0 + r);
-    from_f(out[e], sum == 0.f ? 0.f : y / sum);
+    from_f(out[e], stat[1] == 0.f ? 0.f : y / stat[1]);
 }
 
 struct Choice {
@@ -761,16 +895,33 @@ struct Choice {
 
 template <int kD, int kUnit>
 Choice choose_half() {
-    return {reinterpret_cast<const void *>(&paged_half_kernel<kD, kUnit>), Half<kD>::kSmem,
-            Half<kD>::kTile, Half<kD>::kBlocks};
+    using L = Half<kD, kUnit>;
+    return {reinterpret_cast<const void *>(&paged_half_kernel<kD, kUnit>), L::kSmem, L::kTile,
+            L::kBlocks};
 }
 template <int kUnit>
 Choice choose_half(int d) {
     if (d <= 64) return choose_half<64, kUnit>();
-    if (d <= 96) return choose_half<96, kUnit>();
     if (d <= 128) return choose_half<128, kUnit>();
     if (d <= 192) return choose_half<192, kUnit>();
     return choose_half<256, kUnit>();
+}
+
+// One side of the cache for tiles of 16 slots and 64 features.
+bool make_map(CUtensorMap *map, const void *x, const la_strides &s, const la_cache &c, int Hk,
+              int d) {
+    cudaError_t e;
+    auto enc = tchost::encode_fn(&e);
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.page_size, (cuuint64_t)Hk,
+                                (cuuint64_t)c.pages};
+    const long long n = c.page_size > 1 ? s.n : d, h = Hk > 1 ? s.h : n, b = c.pages > 1 ? s.b : n;
+    const cuuint64_t strides[3] = {(cuuint64_t)n * 2, (cuuint64_t)h * 2, (cuuint64_t)b * 2};
+    const cuuint32_t box[4] = {64, 16, 1, 1}, one[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(x), dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <int kD, int kR, int kUnit>
 Choice choose_full() {
@@ -863,6 +1014,9 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     p.d = d;
     p.window = window;
     p.scale2 = scale * 1.44269504088896341f;
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (p.page_size == 1 << i) p.page_shift = i;
 
     // bytes per copy: 16, or 4, if every row of the cache is aligned to that
     unsigned long long all = (uintptr_t)p.k | (uintptr_t)p.v | (unsigned)d * elem;
@@ -874,7 +1028,20 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     add(p.sk);
     add(p.sv);
     Choice c;
-    if (dtype == LA_F32)
+    CUtensorMap maps[2] = {};
+    // TMA: pages of whole tiles, rows in 16-byte units, no stride of 0 or of 2^38 and more
+    auto fit = [&](const la_strides &s) {
+        const long long most = 1LL << 38;
+        return (p.pages <= 1 || (s.b >= 8 && s.b < most)) && (Hk <= 1 || (s.h >= 8 && s.h < most)) &&
+               s.n >= 8 && s.n < most;
+    };
+    const bool tiles_fit = dtype == LA_BF16 && all % 16 == 0 && p.page_size % 16 == 0 &&
+                           p.pages > 0 && fit(p.sk) && fit(p.sv) &&
+                           make_map(&maps[0], p.k, p.sk, *cache, Hk, d) &&
+                           make_map(&maps[1], p.v, p.sv, *cache, Hk, d);
+    if (tiles_fit)
+        c = choose_half<0>(d);
+    else if (dtype == LA_F32)
         c = all % 16 == 0 ? choose_full<16>(d, p.row_tile) : choose_full<4>(d, p.row_tile);
     else
         c = all % 16 == 0 ? choose_half<16>(d)
@@ -882,6 +1049,7 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
 
     int sms = 0;
     cudaError_t e = tchost::sm_count(&sms);
+    if (e == cudaSuccess) p.status = device_status_word(&e);
     if (e != cudaSuccess) return layer_fail(LA_ERR_CUDA, who, cudaGetErrorString(e));
     // No more blocks than tiles that the table could hold.
     const long long cap = (long long)p.max_pages * p.page_size;
@@ -908,13 +1076,13 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     p.part = reinterpret_cast<float *>(p.info + blocks);
     e = cudaFuncSetAttribute(c.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
     if (e == cudaSuccess) {
-        void *args[] = {&p};
+        void *args[] = {&p, &maps[0], &maps[1]};  // the fp32 kernels take the first alone
         e = cudaLaunchKernel(c.kern, dim3((unsigned)blocks), dim3(kThreads), args, (size_t)c.smem, s);
         if (e == cudaSuccess) note_launches(1);
     }
     if (e == cudaSuccess && blocks > 1) {
         const dim3 grid((unsigned)blocks - 1, (unsigned)p.row_tile);
-        const unsigned threads = (unsigned)(d + 31) / 32 * 32;
+        const unsigned threads = kJoin * ((unsigned)(d + 31) / 32 * 32);
         e = dtype == LA_F32
                 ? tchost::launch_dependent(paged_join_kernel<float>, grid, threads, 0, s, p)
                 : tchost::launch_dependent(paged_join_kernel<__nv_bfloat16>, grid, threads, 0, s, p);
