@@ -758,7 +758,7 @@ struct QLayout {
     static constexpr int OFF_SMALL = OFF_OUT + TILE;
 };
 struct QSmall {
-    uint64_t full[4], empty[4], psi[4], s_ready, g_full[2], g_empty[2], t_free, ds_full, ds_empty;
+    uint64_t full[4], y_full[4], empty[4], psi[4], s_ready, g_full[2], g_empty[2], t_free, ds_full, ds_empty;
     uint64_t out_full, out_empty, fin;
     long long plan[kThreads / 32 + 2];
     float z[128], m[128];
@@ -787,6 +787,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         sm.abort = 0;
         for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.y_full[i], 1);
             mbar_init(&sm.empty[i], 1);
             mbar_init(&sm.psi[i], kWarpsC);
         }
@@ -817,16 +818,21 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES, g = w.tile / tiles;
                 if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
-                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                // the first product needs dY alone: it comes first and is waited for apart
+                mbar_arrive_expect_tx(&sm.y_full[st], L::TILE);
+                mbar_arrive_expect_tx(&sm.full[st], L::TILE);
                 uint8_t *at = smem + st * L::STAGE;
                 const int tok = (w.tile - g * tiles) * 128, h = w.seg * p.G + g;
-                for (int a = 0; a < L::KB; ++a) {
-                    load_tile(at + L::TILE + a * 16384, &tdy, &sm.full[st], 64 * a, tok, h, w.b, pol);
+                for (int a = 0; a < L::KB; ++a)
+                    load_tile(at + L::TILE + a * 16384, &tdy, &sm.y_full[st], 64 * a, tok, h, w.b,
+                              pol);
+                for (int a = 0; a < L::KB; ++a)
                     load_tile(at + a * 16384, &tq, &sm.full[st], 64 * a, tok, h, w.b, pol);
-                }
             }
-            for (int i = max(0, j - L::STAGES); i < j; ++i)
+            for (int i = max(0, j - L::STAGES); i < j; ++i) {
                 settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+                settle_wait(&sm.y_full[i % L::STAGES], (i / L::STAGES) & 1);
+            }
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -872,7 +878,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 if (i < steps) {
                     const int st = i % L::STAGES;
                     const bool first = i == 0 || w.tile == 0;
-                    if (mbar_test_wait(&sm.full[st], (i / L::STAGES) & 1) &&
+                    if (mbar_test_wait(&sm.y_full[st], (i / L::STAGES) & 1) &&
                         mbar_test_wait(&sm.g_empty[i & 1], ((i >> 1) & 1) ^ 1) &&
                         (!first || mbar_test_wait(&sm.s_ready, states & 1))) {
                         tc_fence_after();
@@ -1095,7 +1101,7 @@ struct KLayout {
     static_assert(2 * SBLK >= 16384, "a tile of zeros fits");
 };
 struct KSmall {
-    uint64_t full[4], empty[4], ready[4], out[4], s_ready, phi_empty, d_full[2], d_empty[2], fin;
+    uint64_t full[4], v_full[4], empty[4], ready[4], out[4], s_ready, phi_empty, d_full[2], d_empty[2], fin;
     long long plan[kThreads / 32 + 2];
     float dz[128];
     uint32_t tmem;
@@ -1116,6 +1122,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         sm.abort = 0;
         for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.empty[i], 1);
             mbar_init(&sm.ready[i], kWarpsG);
             mbar_init(&sm.out[i], kWarpsG);
@@ -1143,16 +1150,21 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES;
                 if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
-                mbar_arrive_expect_tx(&sm.full[st], L::STAGE);
+                // phi needs the keys alone: they come first and are waited for apart
+                mbar_arrive_expect_tx(&sm.full[st], L::TILE);
+                mbar_arrive_expect_tx(&sm.v_full[st], L::TILE);
                 uint8_t *at = smem + st * L::STAGE;
-                for (int a = 0; a < L::KB; ++a) {
-                    load_tile(at + a * 16384, &tk, &sm.full[st], 64 * a, w.tile * 128, w.seg, w.b, pol);
-                    load_tile(at + L::TILE + a * 16384, &tv, &sm.full[st], 64 * a, w.tile * 128,
+                for (int a = 0; a < L::KB; ++a)
+                    load_tile(at + a * 16384, &tk, &sm.full[st], 64 * a, w.tile * 128, w.seg, w.b,
+                              pol);
+                for (int a = 0; a < L::KB; ++a)
+                    load_tile(at + L::TILE + a * 16384, &tv, &sm.v_full[st], 64 * a, w.tile * 128,
                               w.seg, w.b, pol);
-                }
             }
-            for (int i = max(0, j - L::STAGES); i < j; ++i)
+            for (int i = max(0, j - L::STAGES); i < j; ++i) {
                 settle_wait(&sm.full[i % L::STAGES], (i / L::STAGES) & 1);
+                settle_wait(&sm.v_full[i % L::STAGES], (i / L::STAGES) & 1);
+            }
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -1173,6 +1185,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     mma_ss(dv, sdesc_sw128(fb + kmajor_off(ks, 16384), 16, 1024),
                            sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
                 mma_commit(&sm.phi_empty);
+                wait_bar_spin(&sm.v_full[st], (j / L::STAGES) & 1, cx);
 #pragma unroll
                 for (int ks = 0; ks < DK / 16; ++ks) {
                     const uint64_t a = sdesc_sw128(vb + kmajor_off(ks, 16384), 16, 1024);
@@ -1219,6 +1232,8 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             for (int i = 0; i < kChunks; ++i)
                 u[i] = *reinterpret_cast<const uint4 *>(
                     kt + tile_at(128, row, (half * kChunks + i) * 8));
+            const bool whole_tile = len >= 128 && p.d == DK;
+            if (len < 128) wait_bar(&sm.v_full[st], (j / L::STAGES) & 1, cx);
             wait_bar(&sm.phi_empty, (j & 1) ^ 1, cx);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
@@ -1227,9 +1242,12 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 float e[8];
                 open8(u[i], e);
                 phi8(e, p.phi);
-                *reinterpret_cast<uint4 *>(smem + L::OFF_PHI + at) =
-                    row < len && col < p.d ? shut8(e) : make_uint4(0, 0, 0, 0);
-                if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+                uint4 f = shut8(e);
+                if (!whole_tile) {
+                    if (row >= len || col >= p.d) f = make_uint4(0, 0, 0, 0);
+                    if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
+                }
+                *reinterpret_cast<uint4 *>(smem + L::OFF_PHI + at) = f;
             }
             fence_async_shared();
             arrive_warp(&sm.ready[st]);
