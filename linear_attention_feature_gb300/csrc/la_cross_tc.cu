@@ -1101,7 +1101,8 @@ struct KLayout {
     static_assert(2 * SBLK >= 16384, "a tile of zeros fits");
 };
 struct KSmall {
-    uint64_t full[4], v_full[4], empty[4], ready[4], out[4], s_ready, phi_empty, d_full[2], d_empty[2], fin;
+    uint64_t full[4], v_full[4], empty[4], ready[4], out[4], s_ready, phi_empty, dk_full[2], dv_full[2],
+        d_empty[2], fin;
     long long plan[kThreads / 32 + 2];
     float dz[128];
     uint32_t tmem;
@@ -1130,7 +1131,8 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         mbar_init(&sm.s_ready, kWarpsC);
         mbar_init(&sm.phi_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.d_full[i], 1);
+            mbar_init(&sm.dk_full[i], 1);
+            mbar_init(&sm.dv_full[i], 1);
             mbar_init(&sm.d_empty[i], kWarpsG);
         }
         mbar_init(&sm.fin, 1);
@@ -1170,29 +1172,59 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         if (lane == 0) {
             constexpr uint32_t idK = idesc_bf16(128, DK, 0, 0), idV = idesc_bf16(128, DK, 0, 1);
             const uint32_t hi = smem_u32(smem + L::OFF_S), lo = hi + L::SBLK;
-            int states = 0;
-            for (int j = 0; j < steps; ++j, w.next()) {
-                const int st = j % L::STAGES;
-                if (j == 0 || w.tile == 0) wait_bar_spin(&sm.s_ready, states++ & 1, cx);
-                wait_bar_spin(&sm.ready[st], (j / L::STAGES) & 1, cx);
-                wait_bar_spin(&sm.d_empty[j & 1], ((j >> 1) & 1) ^ 1, cx);
-                tc_fence_after();
-                const uint32_t vb = smem_u32(smem + st * L::STAGE + L::TILE);
-                const uint32_t fb = smem_u32(smem + L::OFF_PHI);
-                const uint32_t dk = tmem + (j & 1) * 2 * DK, dv = dk + DK;
+            // dphi(K) of tile i needs V alone, dV of tile j <= i needs phi(K): whichever has
+            // its operands
+            int i = 0, j = 0, states = 0;
+            long long deadline = 0;
+            for (int polls = 0; j < steps;) {
+                if (j < i && mbar_test_wait(&sm.ready[j % L::STAGES], (j / L::STAGES) & 1)) {
+                    tc_fence_after();
+                    const uint32_t dv = tmem + (j & 1) * 2 * DK + DK;
+                    const uint32_t fb = smem_u32(smem + L::OFF_PHI);
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks)
-                    mma_ss(dv, sdesc_sw128(fb + kmajor_off(ks, 16384), 16, 1024),
-                           sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
-                mma_commit(&sm.phi_empty);
-                wait_bar_spin(&sm.v_full[st], (j / L::STAGES) & 1, cx);
-#pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint64_t a = sdesc_sw128(vb + kmajor_off(ks, 16384), 16, 1024);
-                    mma_ss(dk, a, sdesc_sw128(hi + kmajor_off(ks, L::SATOM), 16, 1024), idK, ks > 0);
-                    mma_ss(dk, a, sdesc_sw128(lo + kmajor_off(ks, L::SATOM), 16, 1024), idK, 1);
+                    for (int ks = 0; ks < DK / 16; ++ks)
+                        mma_ss(dv, sdesc_sw128(fb + kmajor_off(ks, 16384), 16, 1024),
+                               sdesc_sw128(hi + ks * 2048, L::SATOM, 1024), idV, ks > 0);
+                    mma_commit(&sm.phi_empty);
+                    mma_commit(&sm.dv_full[j & 1]);
+                    ++j;
+                    polls = 0;
+                    continue;
                 }
-                mma_commit(&sm.d_full[j & 1]);
+                if (i < steps) {
+                    const int st = i % L::STAGES;
+                    const bool first = i == 0 || w.tile == 0;
+                    if (mbar_test_wait(&sm.v_full[st], (i / L::STAGES) & 1) &&
+                        mbar_test_wait(&sm.d_empty[i & 1], ((i >> 1) & 1) ^ 1) &&
+                        (!first || mbar_test_wait(&sm.s_ready, states & 1))) {
+                        tc_fence_after();
+                        const uint32_t vb = smem_u32(smem + st * L::STAGE + L::TILE);
+                        const uint32_t dk = tmem + (i & 1) * 2 * DK;
+#pragma unroll
+                        for (int ks = 0; ks < DK / 16; ++ks) {
+                            const uint64_t a = sdesc_sw128(vb + kmajor_off(ks, 16384), 16, 1024);
+                            mma_ss(dk, a, sdesc_sw128(hi + kmajor_off(ks, L::SATOM), 16, 1024),
+                                   idK, ks > 0);
+                            mma_ss(dk, a, sdesc_sw128(lo + kmajor_off(ks, L::SATOM), 16, 1024),
+                                   idK, 1);
+                        }
+                        mma_commit(&sm.dk_full[i & 1]);
+                        states += first;
+                        ++i;
+                        w.next();
+                        polls = 0;
+                        continue;
+                    }
+                }
+                if ((++polls & 63) == 0) {
+                    if (*cx.abort) break;
+                    const long long now = clock64();
+                    if (polls == 64) deadline = now + cx.timeout;
+                    if (now > deadline) {
+                        raise_timeout(cx, smem_u32(&sm.ready[0]));
+                        break;
+                    }
+                }
             }
             mma_commit(&sm.fin);
             settle_wait(&sm.fin, 0);
@@ -1200,7 +1232,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     } else if (warp < 2 + kWarpsC) {
         const Mine me(tmem);
         constexpr int kChunks = DK / 16;
-        const int row = me.et & 127, half = me.part & 1, f0 = half * (DK / 2);
+        const int row = me.row, half = me.part & 1, f0 = half * (DK / 2);
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES, len = w.len - w.tile * 128;
             if (j == 0 || w.tile == 0) {
@@ -1233,7 +1265,6 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 u[i] = *reinterpret_cast<const uint4 *>(
                     kt + tile_at(128, row, (half * kChunks + i) * 8));
             const bool whole_tile = len >= 128 && p.d == DK;
-            if (len < 128) wait_bar(&sm.v_full[st], (j / L::STAGES) & 1, cx);
             wait_bar(&sm.phi_empty, (j & 1) ^ 1, cx);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
@@ -1243,16 +1274,15 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 open8(u[i], e);
                 phi8(e, p.phi);
                 uint4 f = shut8(e);
-                if (!whole_tile) {
-                    if (row >= len || col >= p.d) f = make_uint4(0, 0, 0, 0);
-                    if (row >= len) *reinterpret_cast<uint4 *>(vt + at) = make_uint4(0, 0, 0, 0);
-                }
+                if (!whole_tile && (row >= len || col >= p.d)) f = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(smem + L::OFF_PHI + at) = f;
             }
             fence_async_shared();
             arrive_warp(&sm.ready[st]);
 
-            wait_bar(&sm.d_full[j & 1], (j >> 1) & 1, cx);
+            // dk over k, by the threads that have read it; dv over V, which is no operand any
+            // more.  What lies behind the length in V stays in its own rows.
+            wait_bar(&sm.dk_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
             const uint32_t dk = me.lane_base + (j & 1) * 2 * DK + f0;
 #pragma unroll
@@ -1262,11 +1292,10 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     u[i] = *reinterpret_cast<const uint4 *>(
-                        kt + tile_at(128, me.row, f0 + 32 * h + 8 * i));
+                        kt + tile_at(128, row, f0 + 32 * h + 8 * i));
                 tmem_get(dk + 32 * h, v);
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
-                    uint8_t *at = kt + tile_at(128, me.row, f0 + 32 * h + i);
                     float x[8];
                     open8(u[i / 8], x);
 #pragma unroll
@@ -1278,9 +1307,15 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         x[q] = g.x;
                         x[q + 1] = g.y;
                     }
-                    *reinterpret_cast<uint4 *>(at) =
-                        me.row < len ? shut8(x) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(kt + tile_at(128, row, f0 + 32 * h + i)) =
+                        row < len ? shut8(x) : make_uint4(0, 0, 0, 0);
                 }
+            }
+            wait_bar(&sm.dv_full[j & 1], (j >> 1) & 1, cx);
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < DK / 64; ++h) {
+                uint32_t v[32];
                 tmem_get(dk + DK + 32 * h, v);
                 if (h == DK / 64 - 1) {
                     tc_fence_before();
@@ -1291,8 +1326,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     float o[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) o[q] = u2f(v[i + q]);
-                    *reinterpret_cast<uint4 *>(vt + tile_at(128, me.row, f0 + 32 * h + i)) =
-                        shut8(o);
+                    *reinterpret_cast<uint4 *>(vt + tile_at(128, row, f0 + 32 * h + i)) = shut8(o);
                 }
             }
             fence_async_shared();
