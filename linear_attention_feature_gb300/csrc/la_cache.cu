@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = LA_MAX_D / 2;
-constexpr int kRows = 3;  // rows of a thread in flight
+constexpr int kRows = 4;  // heads of a thread under way at a time
 
 struct Tensor {
     const void *x;
@@ -38,12 +38,56 @@ struct Params {
     unsigned long long turns[kMaxPairs];
 };
 
+// cos and sin of a thread's V pairs, as the packed instructions take them.
+template <int V, bool kInter>
+struct Turn {
+    float2 c[V], s[V];
+
+    __device__ __forceinline__ void set(int i, float cs, float sn) {
+        if (kInter || V == 1) {  // one pair: (x0, x1) (c, c) + (x1, x0) (-s, s)
+            c[i] = make_float2(cs, cs);
+            s[i] = make_float2(-sn, sn);
+        } else {  // two pairs: x0 c - x1 s and x1 c + x0 s
+            (i % 2 ? c[i / 2].y : c[i / 2].x) = cs;
+            (i % 2 ? s[i / 2].y : s[i / 2].x) = sn;
+        }
+    }
+    // e: V first and V second values, or V pairs
+    __device__ __forceinline__ void apply(float (&e)[2 * V]) const {
+        if (kInter || V == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float2 x = make_float2(e[2 * i], e[2 * i + 1]);
+                const float2 y =
+                    __ffma2_rn(x, c[i], __fmul2_rn(make_float2(x.y, x.x), s[i]));
+                e[2 * i] = y.x, e[2 * i + 1] = y.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 x0 = make_float2(e[2 * i], e[2 * i + 1]);
+                const float2 x1 = make_float2(e[V + 2 * i], e[V + 2 * i + 1]);
+                const float2 ns = make_float2(-s[i].x, -s[i].y);
+                const float2 y0 = __ffma2_rn(x0, c[i], __fmul2_rn(x1, ns));
+                const float2 y1 = __ffma2_rn(x1, c[i], __fmul2_rn(x0, s[i]));
+                e[2 * i] = y0.x, e[2 * i + 1] = y0.y;
+                e[V + 2 * i] = y1.x, e[V + 2 * i + 1] = y1.y;
+            }
+        }
+    }
+};
+
 // A block takes 2^token_bits tokens, one for each part of its threads; the part's
-// groups of 2^lane_bits threads take the token's rows (queries, keys, values) in
-// turn.  A thread keeps to two vectors of V features, the two halves of V pairs, in
-// all rows, so that angles, position and page are found once for all heads.
+// groups of 2^lane_bits threads take the token's heads (queries, keys, values) in turn.
+// A thread keeps to two vectors of V features, the two halves of V pairs, in all heads,
+// so that angles, position and page are found once for many of them, kRows of which are
+// under way at a time.
+//
+// Bound by memory: 8 x 8192 tokens (fewer in some sequences) of 32 + 8 + 8 heads of 128
+// bf16 values: 247 us, 6.0 TB/s.  (Two heads under way 272 us; three or four blocks per SM
+// spill: 275 to 293 us.  Angles found for three heads at a time instead of twelve: 367 us.)
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ Params p) {
     const int unit = threadIdx.x & ((1 << p.lane_bits) - 1);
     const int group = threadIdx.x >> p.lane_bits;
     const int step = (kThreads >> p.lane_bits) >> p.token_bits;
@@ -63,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         at[0] = 2 * V * unit;  // 2 half + 2 (unit V - half)
         at[1] = at[0] + V;
     }
-    const bool has[2] = {at[0] < p.d, at[1] < p.d};
-    if (!has[0]) return;
+    if (at[0] >= p.d) return;
+    const bool second = at[1] < p.d;
 
     const int before = p.lengths[b];
     const long long pos = (long long)before + t;
@@ -80,67 +124,65 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             keep = page >= 0 && page < p.pages;
         }
     }
-    float c[V], s[V];
+    Turn<V, kInter> turn;
+    bool all = true, any = false;  // of this thread's pairs are rotated
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int pair = unit * V + i;
-        c[i] = 1.f, s[i] = 0.f;
-        if (pair < p.half) turn_of<sizeof(T) == 4>(pos + p.offset, p.turns[pair], &c[i], &s[i]);
+        float c = 1.f, s = 0.f;
+        if (pair < p.half) turn_of<sizeof(T) == 4>(pos + p.offset, p.turns[pair], &c, &s);
+        all &= pair < p.half;
+        any |= pair < p.half;
+        turn.set(i, c, s);
     }
 
-    const int rows = p.Hq + 2 * p.Hk;
-    for (int r0 = group >> p.token_bits; r0 < rows; r0 += kRows * step) {
-        Pack<T, V> x[kRows][2];
-        T *dst[kRows];
+    // One side: this group's heads of H, `skip` heads of other sides having been dealt
+    // out before.
+    auto side = [&](const Tensor &in, void *out, const la_strides &so, long long to, int H,
+                    int skip, bool rotate) {
+        int h = (group >> p.token_bits) - skip % step;
+        if (h < 0) h += step;
+        const T *src = static_cast<const T *>(in.x) + b * in.s.b + t * in.s.n + h * in.s.h;
+        T *dst = static_cast<T *>(out) + to + h * so.h;
+        const long long src_step = step * in.s.h, dst_step = step * so.h;
+        for (; h < H; h += kRows * step) {
+            Pack<T, V> x[kRows][2];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i * step;
-            const T *src = nullptr;
-            dst[i] = nullptr;
-            if (r < p.Hq) {
-                src = static_cast<const T *>(p.q.x) + b * p.q.s.b + r * p.q.s.h + t * p.q.s.n;
-                dst[i] = static_cast<T *>(p.q_out) + b * p.sq_out.b + r * p.sq_out.h +
-                         t * p.sq_out.n;
-            } else if (r < rows && keep) {
-                const bool key = r < p.Hq + p.Hk;
-                const int h = r - p.Hq - (key ? 0 : p.Hk);
-                const Tensor &in = key ? p.k : p.v;
-                const la_strides &so = key ? p.sk_cache : p.sv_cache;
-                src = static_cast<const T *>(in.x) + b * in.s.b + h * in.s.h + t * in.s.n;
-                dst[i] = static_cast<T *>(key ? p.k_cache : p.v_cache) + page * so.b +
-                         h * so.h + slot * so.n;
-            }
-            if (src) {
-                x[i][0] = *reinterpret_cast<const Pack<T, V> *>(src + at[0]);
-                if (has[1]) x[i][1] = *reinterpret_cast<const Pack<T, V> *>(src + at[1]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (!dst[i]) continue;
-            // values, and features beyond the rotated ones, pass bit for bit
-            const bool turn = r0 + i * step < p.Hq + p.Hk;
-            if (turn && unit * V < p.half) {
-                float e[2 * V];
-                widen(&x[i][0], e);
-                if (has[1]) widen(&x[i][1], e + V);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int i0 = kInter ? 2 * j : j, i1 = kInter ? 2 * j + 1 : V + j;
-                    const float x0 = e[i0], x1 = e[i1];
-                    if (unit * V + j < p.half) {
-                        e[i0] = fmaf(x0, c[j], -__fmul_rn(x1, s[j]));
-                        e[i1] = fmaf(x1, c[j], __fmul_rn(x0, s[j]));
-                    }
+            for (int i = 0; i < kRows; ++i, src += src_step)
+                if (h + i * step < H) {
+                    x[i][0] = *reinterpret_cast<const Pack<T, V> *>(src + at[0]);
+                    if (second) x[i][1] = *reinterpret_cast<const Pack<T, V> *>(src + at[1]);
                 }
-                narrow<T, V>(dst[i] + at[0], e);
-                if (has[1]) narrow<T, V>(dst[i] + at[1], e + V);
-            } else {
-                *reinterpret_cast<Pack<T, V> *>(dst[i] + at[0]) = x[i][0];
-                if (has[1]) *reinterpret_cast<Pack<T, V> *>(dst[i] + at[1]) = x[i][1];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i, dst += dst_step) {
+                if (h + i * step >= H) continue;
+                // values, and features beyond the rotated ones, pass bit for bit
+                if (rotate && any) {
+                    float e[2 * V], keep_e[2 * V];
+                    widen(&x[i][0], e);
+                    if (second) widen(&x[i][1], e + V);
+                    if (!all)
+#pragma unroll
+                        for (int j = 0; j < 2 * V; ++j) keep_e[j] = e[j];
+                    turn.apply(e);
+                    if (!all)  // neighbouring pairs of which some pass
+#pragma unroll
+                        for (int j = 0; j < 2 * V; ++j)
+                            if (unit * V + (kInter ? j / 2 : j % V) >= p.half) e[j] = keep_e[j];
+                    narrow<T, V>(dst + at[0], e);
+                    if (second) narrow<T, V>(dst + at[1], e + V);
+                } else {
+                    *reinterpret_cast<Pack<T, V> *>(dst + at[0]) = x[i][0];
+                    if (second) *reinterpret_cast<Pack<T, V> *>(dst + at[1]) = x[i][1];
+                }
             }
         }
-    }
+    };
+    side(p.q, p.q_out, p.sq_out, b * p.sq_out.b + t * p.sq_out.n, p.Hq, 0, true);
+    if (!keep) return;
+    side(p.k, p.k_cache, p.sk_cache, page * p.sk_cache.b + slot * p.sk_cache.n, p.Hk, p.Hq, true);
+    side(p.v, p.v_cache, p.sv_cache, page * p.sv_cache.b + slot * p.sv_cache.n, p.Hk,
+         p.Hq + p.Hk, false);
 }
 
 template <typename T>
@@ -167,12 +209,12 @@ la_status launch(const char *who, Params &p, int interleaved, cudaStream_t strea
     const int v = (int)(all & (0 - all));
     const int units = (p.d + 2 * v - 1) / (2 * v);
     while (1 << p.lane_bits < units) ++p.lane_bits;
-    // More tokens per block while a thread has fewer than kRows rows of each and
-    // enough blocks are left for every SM.
+    // More tokens per block while a thread has fewer than 12 heads of its token, whose
+    // angles serve them all, and enough blocks are left for every SM.
     const int groups = kThreads >> p.lane_bits, rows = p.Hq + 2 * p.Hk;
     const long long tokens = (long long)p.B * p.T;
-    while ((2 << p.token_bits) <= groups && rows * (1 << p.token_bits) < kRows * groups &&
-           tokens >> (p.token_bits + 1) >= 4 * sms)
+    while ((2 << p.token_bits) <= groups && rows * (1 << p.token_bits) < 12 * groups &&
+           tokens >> (p.token_bits + 1) >= 6 * sms)
         ++p.token_bits;
     const long long blocks = (tokens + (1 << p.token_bits) - 1) >> p.token_bits;
     if (blocks > 0x7fffffff) return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");

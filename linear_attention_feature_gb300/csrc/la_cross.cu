@@ -69,30 +69,43 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
     const long long i0 = seg * p.per, i1 = min(i0 + p.per, all);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float acc[4][4] = {}, zacc[4] = {};
-    for (long long i = i0; i < i1; i += kTok) {
-        if (p.group == 1 && i >= len) break;
-        __syncthreads();
-        for (int e = threadIdx.x; e < kTok * kTile; e += kThreads) {
-            const int row = e / kTile, f = e % kTile;
-            const long long tok = i + row;
-            const int g = (int)(tok / p.L), n = (int)(tok - (long long)g * p.L);
-            const bool ok = tok < i1 && n < len;
-            float2 rt = make_float2(1.f, -1.f);
-            if (ok && p.rt) rt = p.rt[(head * p.group + g) * p.L + n];
-            float x = 0.f, y = 0.f;
+    // a thread brings feature f of every fourth row, the next tokens' while these are summed
+    constexpr int kPer = kTok * kTile / kThreads;
+    const int f = threadIdx.x % kTile, r0 = threadIdx.x / kTile;
+    const bool in_x = a0 + f < p.d, in_y = c0 + f < p.d;
+    const T *xs = static_cast<const T *>(p.x) + b * p.sx.b + a0 + f;
+    const T *ys = static_cast<const T *>(p.y) + b * p.sy.b + c0 + f;
+    float x[kPer], y[kPer];
+    float2 rt[kPer];
+    auto fetch = [&](long long i) {
+        const int g0 = (int)(i / p.L), n0 = (int)(i - (long long)g0 * p.L);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int row = r0 + k * (kThreads / kTile);
+            int g = g0, n = n0 + row;
+            if (n >= p.L) g += n / p.L, n %= p.L;
+            const bool ok = i + row < i1 && n < len;
             const long long hh = (long long)h * p.group + g;
-            if (ok && a0 + f < p.d)
-                x = rt.x * phi_of(to_f(static_cast<const T *>(p.x)[b * p.sx.b + hh * p.sx.h +
-                                                                  n * p.sx.n + a0 + f]),
-                                  p.phi);
-            if (ok && c0 + f < p.d)
-                y = to_f(static_cast<const T *>(p.y)[b * p.sy.b + hh * p.sy.h + n * p.sy.n +
-                                                    c0 + f]);
-            A[row][f] = x;
-            Y[row][f] = y;
-            if (f == 0) U[row] = -rt.y;
+            x[k] = y[k] = 0.f;
+            rt[k] = make_float2(1.f, -1.f);
+            if (ok && p.rt) rt[k] = p.rt[(head * p.group + g) * p.L + n];
+            if (ok && in_x) x[k] = phi_of(to_f(xs[hh * p.sx.h + n * p.sx.n]), p.phi);
+            if (ok && in_y) y[k] = to_f(ys[hh * p.sy.h + n * p.sy.n]);
+        }
+    };
+    const long long end = p.group == 1 ? min(i1, (long long)len) : i1;
+    if (i0 < end) fetch(i0);
+    for (long long i = i0; i < end; i += kTok) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int row = r0 + k * (kThreads / kTile);
+            A[row][f] = rt[k].x * x[k];
+            Y[row][f] = y[k];
+            if (f == 0) U[row] = -rt[k].y;
         }
         __syncthreads();
+        if (i + kTok < end) fetch(i + kTok);
 #pragma unroll 8
         for (int row = 0; row < kTok; ++row) {
             const float4 a = *reinterpret_cast<const float4 *>(&A[row][ty * 4]);
@@ -167,22 +180,35 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
     float acc[4][4] = {}, den[4] = {};
-    for (int k0 = 0; k0 < p.d; k0 += kStep) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < kTile * kStep; e += kThreads) {
-            const int row = e / kStep, f = e % kStep;
-            float v = 0.f;
+    // the next features' values come while these are multiplied
+    constexpr int kPer = kTile * kStep / kThreads;
+    float av[kPer], yv[kPer], zv = 0.f;
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            const int row = e / kStep, f = e % kStep, a = e / kTile, c = e % kTile;
+            av[i] = yv[i] = 0.f;
             if (n0 + row < len && k0 + f < p.d)
-                v = phi_of(to_f(x[(n0 + row) * p.sx.n + k0 + f]), p.phi);
-            A[f][row] = v;
-            const int a = e / kTile, c = e % kTile;
-            Y[a][c] = k0 + a < p.d && c0 + c < p.d
-                          ? p.S[(state * p.d + k0 + a) * p.d + c0 + c] : 0.f;
+                av[i] = phi_of(to_f(x[(n0 + row) * p.sx.n + k0 + f]), p.phi);
+            if (k0 + a < p.d && c0 + c < p.d)
+                yv[i] = p.S[(state * p.d + k0 + a) * p.d + c0 + c];
         }
         if (threadIdx.x < kStep)
-            Z[threadIdx.x] = p.norm && k0 + threadIdx.x < p.d
-                                 ? p.z[state * p.d + k0 + threadIdx.x] : 0.f;
+            zv = p.norm && k0 + (int)threadIdx.x < p.d ? p.z[state * p.d + k0 + threadIdx.x] : 0.f;
+    };
+    fetch(0);
+    for (int k0 = 0; k0 < p.d; k0 += kStep) {
         __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            A[e % kStep][e / kStep] = av[i];
+            Y[e / kTile][e % kTile] = yv[i];
+        }
+        if (threadIdx.x < kStep) Z[threadIdx.x] = zv;
+        __syncthreads();
+        if (k0 + kStep < p.d) fetch(k0 + kStep);
 #pragma unroll 8
         for (int k = 0; k < kStep; ++k) {
             const float4 a = *reinterpret_cast<const float4 *>(&A[k][ty * 4]);
@@ -226,10 +252,11 @@ struct GradParams {
 // G_i = S y_i, and from it the gradient of row i: on q's side
 // r (G - t z) phi'(x) with r and t left for the sums, on k's side (G + z) phi'(x)
 // (z is then dz).  A warp takes 4 rows whole, a lane every 32nd feature.
-template <typename T>
+template <typename T, int kCols>  // kCols: 32 features each, of d
 __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
-    constexpr int kRows = 32, kStep = 32, kCols = LA_MAX_D / 32;
-    __shared__ float Y[kRows][kStep], W[LA_MAX_D][kStep + 1];
+    constexpr int kRows = 32, kStep = 32, kPerY = kRows * kStep / kThreads;
+    constexpr int kPerW = kCols * 32 * kStep / kThreads;
+    __shared__ float Y[kRows][kStep], W[kCols * 32][kStep + 1];
     const int row_tiles = (p.L + kRows - 1) / kRows;
     const long long bh = blockIdx.x / row_tiles;
     const int n0 = (int)(blockIdx.x - bh * row_tiles) * kRows;
@@ -237,53 +264,75 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
     const long long state = (long long)b * p.Hk + h / p.group;
     const int len = tokens_of(p.lengths, b, p.L);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cols = (p.d + 31) / 32;
     const T *y = static_cast<const T *>(p.y) + b * p.sy.b + h * p.sy.h;
+    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
+    // the next features' values come while these are multiplied
+    float yv[kPerY], wv[kPerW];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < kPerY; ++i) {
+            const int e = threadIdx.x + i * kThreads, row = e / kStep, c = e % kStep;
+            yv[i] = n0 + row < len && k0 + c < p.d ? to_f(y[(n0 + row) * p.sy.n + k0 + c]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kPerW; ++i) {
+            const int e = threadIdx.x + i * kThreads, a = e / kStep, c = e % kStep;
+            wv[i] = a < p.d && k0 + c < p.d ? p.S[(state * p.d + a) * p.d + k0 + c] : 0.f;
+        }
+    };
+    fetch(0);
     float acc[4][kCols] = {};
     for (int k0 = 0; k0 < p.d; k0 += kStep) {
         __syncthreads();
-        for (int e = threadIdx.x; e < kRows * kStep; e += kThreads) {
-            const int row = e / kStep, c = e % kStep;
-            Y[row][c] = n0 + row < len && k0 + c < p.d
-                            ? to_f(y[(n0 + row) * p.sy.n + k0 + c]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerY; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            Y[e / kStep][e % kStep] = yv[i];
         }
-        for (int e = threadIdx.x; e < cols * 32 * kStep; e += kThreads) {
-            const int a = e / kStep, c = e % kStep;
-            W[a][c] = a < p.d && k0 + c < p.d ? p.S[(state * p.d + a) * p.d + k0 + c] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerW; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            W[e / kStep][e % kStep] = wv[i];
         }
         __syncthreads();
+        if (k0 + kStep < p.d) fetch(k0 + kStep);
+#pragma unroll 4
         for (int k = 0; k < kStep; ++k) {
             float v[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) v[m] = Y[warp * 4 + m][k];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) {
-                if (j >= cols) break;
                 const float w = W[lane + 32 * j][k];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) acc[m][j] = fmaf(w, v[m], acc[m][j]);
             }
         }
     }
-    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
     T *dx = static_cast<T *>(p.dx) + b * p.sdx.b + h * p.sdx.h;
+    float xv[4][kCols], zv[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+        const int a = lane + 32 * j;
+        zv[j] = a < p.d && (p.norm || p.keys) ? p.z[state * p.d + a] : 0.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int n = n0 + warp * 4 + m;
+            xv[m][j] = a < p.d && n < len ? to_f(x[n * p.sx.n + a]) : 0.f;
+        }
+    }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         const int n = n0 + warp * 4 + m;
         if (n >= p.L) continue;
-        float xv[kCols], zv[kCols], dot = 0.f, den = 0.f;
+        float dot = 0.f, den = 0.f;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-            const int a = lane + 32 * j;
-            const bool ok = a < p.d;
-            xv[j] = ok && n < len ? to_f(x[n * p.sx.n + a]) : 0.f;
-            zv[j] = ok && (p.norm || p.keys) ? p.z[state * p.d + a] : 0.f;
-            if (ok) {
-                const float f = phi_of(xv[j], p.phi);
+        for (int j = 0; j < kCols; ++j)
+            if (lane + 32 * j < p.d) {
+                const float f = phi_of(xv[m][j], p.phi);
                 dot = fmaf(f, acc[m][j], dot);
                 den = fmaf(f, zv[j], den);
             }
-        }
         float r = 1.f, t = p.keys ? -1.f : 0.f;
         if (!p.keys) {
 #pragma unroll
@@ -301,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
         for (int j = 0; j < kCols; ++j) {
             const int a = lane + 32 * j;
             if (a >= p.d) continue;
-            const float g = r * fmaf(-t, zv[j], acc[m][j]) * slope_of(xv[j], p.phi);
+            const float g = r * fmaf(-t, zv[j], acc[m][j]) * slope_of(xv[m][j], p.phi);
             from_f(dx[n * p.sdx.n + a], n < len ? g : 0.f);
         }
     }
@@ -486,8 +535,15 @@ cudaError_t grads(const Shape &sh, Rows y, Rows x, Rows dx, int group, int L, co
                  sh.Hk, group, L, sh.d, sh.phi, sh.norm, keys};
     const long long blocks = sh.heads() * group * ((L + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    grad_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    return counted(cudaSuccess);
+    auto go = [&](auto kern) {
+        kern<<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        return counted(cudaSuccess);
+    };
+    if (sh.d <= 32) return go(grad_kernel<T, 1>);
+    if (sh.d <= 64) return go(grad_kernel<T, 2>);
+    if (sh.d <= 96) return go(grad_kernel<T, 3>);
+    if (sh.d <= 128) return go(grad_kernel<T, 4>);
+    return go(grad_kernel<T, 8>);
 }
 
 template <typename T>

@@ -87,7 +87,7 @@ struct Walk {
         if (x.x0 < x.x1) {
             len = tokens_of(p, b);
             tiles = count(len);
-            seg = (int)(x.rest / tiles);
+            seg = (int)(x.rest <= 0x7fffffff ? (unsigned)x.rest / (unsigned)tiles : x.rest / tiles);
             tile = (int)(x.rest - (long long)seg * tiles);
         }
     }

@@ -138,6 +138,12 @@ inline la_strides contiguous(int H, int N, int d) {
 
 inline bool negative(const la_strides &s) { return s.b < 0 || s.h < 0 || s.n < 0; }
 
+// a i / n, in 32 bits where that is enough.
+__device__ __forceinline__ long long share_of(long long a, int i, int n) {
+    const long long x = a * i;
+    return x <= 0xffffffffLL ? (long long)((unsigned)x / (unsigned)n) : x / n;
+}
+
 // Equal pieces of a list of work whose length only the device knows: for each of B
 // entries, `segs` stretches of tiles_of(b) > 0 tiles.  A block's piece is [x0, x1) of
 // `total` tiles, and x0 is tile `rest` of entry b's stretches.  There are `pieces` of
@@ -157,11 +163,12 @@ struct Piece {
 __device__ __forceinline__ Piece even_piece(int B, int segs, int least, int tiles) {
     Piece p;
     p.total = (long long)B * segs * tiles;
-    p.pieces = (int)min((long long)gridDim.x, max(1LL, p.total / least));
-    p.x0 = p.total * min((int)blockIdx.x, p.pieces) / p.pieces;
-    p.x1 = p.total * min((int)blockIdx.x + 1, p.pieces) / p.pieces;
+    p.pieces = (int)min((long long)gridDim.x, max(1LL, share_of(p.total, 1, least)));
+    p.x0 = share_of(p.total, min((int)blockIdx.x, p.pieces), p.pieces);
+    p.x1 = share_of(p.total, min((int)blockIdx.x + 1, p.pieces), p.pieces);
     const long long per = (long long)segs * tiles;
-    p.b = (int)(p.x0 / per);
+    p.b = (int)(p.x0 <= 0x7fffffff && per <= 0x7fffffff ? (unsigned)p.x0 / (unsigned)per
+                                                         : p.x0 / per);
     p.rest = p.x0 - p.b * per;
     return p;
 }
@@ -193,9 +200,9 @@ __device__ __forceinline__ Piece find_piece(int B, int segs, int least, F tiles_
         p.total += shared[w];
     }
     p.total *= segs;
-    p.pieces = (int)min((long long)gridDim.x, max(1LL, p.total / least));
-    p.x0 = p.total * min((int)blockIdx.x, p.pieces) / p.pieces;
-    p.x1 = p.total * min((int)blockIdx.x + 1, p.pieces) / p.pieces;
+    p.pieces = (int)min((long long)gridDim.x, max(1LL, share_of(p.total, 1, least)));
+    p.x0 = share_of(p.total, min((int)blockIdx.x, p.pieces), p.pieces);
+    p.x1 = share_of(p.total, min((int)blockIdx.x + 1, p.pieces), p.pieces);
     long long at = (base + upto - mine) * segs;  // of this thread's first entry
     if (p.x0 >= at && p.x0 < at + mine * segs) {
         int b = b0;

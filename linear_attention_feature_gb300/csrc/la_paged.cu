@@ -97,7 +97,8 @@ __device__ __forceinline__ Place<kTile> find_place(const Params &p, long long *s
     c.b = piece.b;
     if (piece.x0 < piece.x1) {
         c.s = span_of<kTile>(p, c.b);
-        c.seg = (int)(piece.rest / c.s.tiles);
+        c.seg = (int)(piece.rest <= 0x7fffffff ? (unsigned)piece.rest / (unsigned)c.s.tiles
+                                               : piece.rest / c.s.tiles);
         c.tile = (int)(piece.rest - (long long)c.seg * c.s.tiles);
     }
     return c;
