@@ -43,6 +43,7 @@ struct Params {
     int B, Hk, G, T, d, window;
     int *status;
     int by_stretch;  // see note()
+    int q_words;     // queries lie in 32-bit words
     int row_tile, row_tiles;  // queries of a block, tiles of them per head of keys
     float scale2;             // scale log2(e)
     int4 *info;               // of each block: see Plan
@@ -197,24 +198,18 @@ __device__ __forceinline__ long long row_offset(const Params &p, const la_stride
     return b * s.b + (long long)(h * p.G + g) * s.h + t * s.n;
 }
 
-// Writes a finished stretch, or leaves it for the join.  o: [row][pitch] outputs times
-// l, ml: (m, l) of each row, in shared memory.
+// One value of a finished stretch, or of one that is left for the join (slot >= 0): the
+// output y times l, the maximum and l.
 template <typename T>
-__device__ __forceinline__ void write_rows(const Params &p, int b, int h, int row0, int rows,
-                                           const float *o, int pitch, const float2 *ml,
-                                           int slot) {
-    for (int i = threadIdx.x; i < rows * p.d; i += kThreads) {
-        const int r = i / p.d, c = i - r * p.d;
-        const float2 s = ml[r];
-        if (slot < 0) {
-            T *y = static_cast<T *>(p.out) + row_offset<T>(p, p.so, b, h, row0 + r);
-            from_f(y[c], s.y == 0.f ? 0.f : o[r * pitch + c] / s.y);
-        } else {
-            float *w = p.part +
-                       ((long long)(blockIdx.x * 2 + slot) * p.row_tile + r) * (p.d + 2);
-            w[c] = o[r * pitch + c];
-            if (c == 0) w[p.d] = s.x, w[p.d + 1] = s.y;
-        }
+__device__ __forceinline__ void write_value(const Params &p, int b, int h, int row0, int r, int c,
+                                            int slot, float y, float m, float l) {
+    if (slot < 0) {
+        T *out = static_cast<T *>(p.out) + row_offset<T>(p, p.so, b, h, row0 + r);
+        from_f(out[c], l == 0.f ? 0.f : y / l);
+    } else {
+        float *w = p.part + ((long long)(blockIdx.x * 2 + slot) * p.row_tile + r) * (p.d + 2);
+        w[c] = y;
+        if (c == 0) w[p.d] = m, w[p.d + 1] = l;
     }
 }
 
@@ -266,11 +261,10 @@ struct Half {
     static constexpr int kStage = 2 * kSide;                                   // of a warp
     static constexpr int kStages = kD == 64 || kD == 192 ? 4 : 3;
     static constexpr int kBlocks = kD == 64 && kUnit == 0 ? 3 : kD <= 128 ? 2 : 1;  // per SM
-    static constexpr int kOutPitch = kD + 4;
-    static constexpr int kOffOut = kWarps * kStages * kStage;
-    static constexpr int kOffMl = kOffOut + kRowTile * kOutPitch * 4;
-    static constexpr int kOffMask = kOffMl + (kWarps + 1) * kRowTile * 8;
+    static constexpr int kOffMl = kWarps * kStages * kStage;
+    static constexpr int kOffMask = kOffMl + kWarps * kRowTile * 8;
     static constexpr int kOffBar = kOffMask + kWarps * kStages * 4;
+    static_assert(kRowTile * kD * 4 <= kStage, "a warp's outputs fit into a stage");
     static constexpr int kOffPlan = kOffBar + kWarps * kStages * 8;
     static constexpr int kSmem = kOffPlan + (kWarps + 2) * 8 + 16 + (kUnit ? 0 : 1024);
     static_assert(kOffBar % 8 == 0 && kSmem <= 232448, "shared memory");
@@ -311,7 +305,6 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                                                   ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     char *ring = smem + warp * L::kStages * L::kStage;
-    float *obuf = reinterpret_cast<float *>(smem + L::kOffOut);
     float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
     unsigned *masks = reinterpret_cast<unsigned *>(smem + L::kOffMask) + warp * L::kStages;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * L::kStages;
@@ -320,7 +313,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     const int segs = p.Hk * p.row_tiles;
 
     if (kUnit != 0)  // features from d on
-        for (int i = threadIdx.x; i < L::kOffOut / 16; i += kThreads)
+        for (int i = threadIdx.x; i < L::kOffMl / 16; i += kThreads)
             reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) *abort = 0;
     if (kUnit == 0) {
@@ -403,6 +396,39 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             v_at[i] += L::kSide;
         }
     }
+    // The queries as the products take them, straight from memory: rows lane / 4 and 8
+    // further on, features 2 (lane % 4) and 8 further on of each 16.
+    unsigned a[kD / 16][4];
+    auto load_queries = [&]() {
+        const int h = c.seg / p.row_tiles, row0 = (c.seg - h * p.row_tiles) * p.row_tile;
+        const int rows = min(p.row_tile, p.G * p.T - row0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            const T *q = static_cast<const T *>(p.q) +
+                         (r < rows ? row_offset<T>(p, p.sq, c.b, h, row0 + r) : 0);
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = 16 * ks + 8 * j + 2 * (lane & 3);
+                    unsigned u = 0;
+                    if (r < rows && e < p.d) {
+                        if (p.q_words) {
+                            u = *reinterpret_cast<const unsigned *>(q + e);
+                        } else {
+                            u = *reinterpret_cast<const unsigned short *>(q + e);
+                            if (e + 1 < p.d)
+                                u |= (unsigned)*reinterpret_cast<const unsigned short *>(q + e + 1)
+                                     << 16;
+                        }
+                    }
+                    a[ks][2 * j + i] = u;
+                }
+        }
+    };
+    load_queries();
+
     int stage = 0;
     unsigned parity = 0;
     for (int left = steps; left > 0;) {
@@ -413,23 +439,6 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
         const long long x = x1 - left;
         const long long seg0 = x - c.tile, seg1 = seg0 + c.s.tiles;
         const int n = (int)min((long long)left, seg1 - x);
-        unsigned a[kD / 16][4];
-        {
-            T *qbuf = reinterpret_cast<T *>(obuf);
-            for (int i = threadIdx.x; i < kRowTile * kD; i += kThreads) {
-                const int r = i / kD, e = i % kD;
-                T value = T(0.f);
-                if (r < rows && e < p.d)
-                    value = static_cast<const T *>(
-                        p.q)[row_offset<T>(p, p.sq, c.b, h, row0 + r) + e];
-                qbuf[r * L::kPitch + e] = value;
-            }
-            __syncthreads();
-            const unsigned at =
-                tc::smem_u32(qbuf + (lane & 15) * L::kPitch + (lane >> 4) * 8);
-#pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) ldmatrix4(a[ks], at + ks * 32);
-        }
         float o[kD / 8][4], sums[4] = {};  // the outputs times l, and l
 #pragma unroll
         for (int j = 0; j < kD / 8; ++j)
@@ -568,48 +577,57 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             if (++stage == L::kStages) stage = 0, parity ^= 1;
             c.tile += 1;
         }
-        // ---- the warps' parts together, in order
-        const float l[2] = {sums[0], sums[2]};
+        // ---- the warps' parts together, through the places that they have just read; the
+        // next stretch's queries come meanwhile
+        const int b = c.b, seg = c.seg;
+        left -= n;
+        c.tile -= 1;
+        if (left > 0) {
+            c.next(p, segs);
+            load_queries();
+        }
+        const int mine = stage == 0 ? L::kStages - 1 : stage - 1;
+        auto place = [&](int q) {
+            return reinterpret_cast<float *>(smem + (q * L::kStages + mine) * L::kStage);
+        };
+        // (columns turned by 8 per row: no bank conflicts)
+        auto at = [](int r, int col) { return r * kD + (col ^ (r & 3) << 3); };
+#pragma unroll
+        for (int j = 0; j < kD / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float2 *>(
+                    place(warp) + at((lane >> 2) + 8 * i, 8 * j + (lane & 3) * 2)) =
+                    make_float2(o[j][2 * i], o[j][2 * i + 1]);
         if ((lane & 3) == 0)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                ml[warp * kRowTile + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+                ml[warp * kRowTile + (lane >> 2) + 8 * i] = make_float2(m[i], sums[2 * i]);
         __syncthreads();
-        float w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = (lane >> 2) + 8 * i;
-            float top = -INFINITY, sum = 0.f;
+        const bool ends = seg1 <= x1;
+        const int slot = began ? 0 : ends ? -1 : 1;
+        for (int i = threadIdx.x; i < rows * p.d; i += kThreads) {
+            const int r = i / p.d, col = i - r * p.d;
+            float top = -INFINITY, sum = 0.f, y = 0.f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) top = fmaxf(top, ml[q * kRowTile + r].x);
 #pragma unroll
-            for (int q = 0; q < kWarps; ++q)
-                sum += ml[q * kRowTile + r].y * exp2_fast(ml[q * kRowTile + r].x - finite_max(top));
-            w[i] = exp2_fast(m[i] - finite_max(top));
-            if (warp == 0 && (lane & 3) == 0) ml[kWarps * kRowTile + r] = make_float2(top, sum);
+            for (int q = 0; q < kWarps; ++q) {
+                const float2 v = ml[q * kRowTile + r];
+                const float w = exp2_fast(v.x - finite_max(top));
+                sum = fmaf(v.y, w, sum);
+                y = fmaf(place(q)[at(r, col)], w, y);
+            }
+            write_value<T>(p, b, h, row0, r, col, slot, y, top, sum);
         }
-        for (int q = 0; q < kWarps; ++q) {
-            if (warp == q)
-#pragma unroll
-                for (int j = 0; j < kD / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        float2 *y = reinterpret_cast<float2 *>(
-                            obuf + ((lane >> 2) + 4 * e) * L::kOutPitch + 8 * j + (lane & 3) * 2);
-                        float2 u = make_float2(o[j][e] * w[e >> 1], o[j][e + 1] * w[e >> 1]);
-                        if (q > 0) u = make_float2(y->x + u.x, y->y + u.y);
-                        *y = u;
-                    }
-            __syncthreads();
-        }
-        const bool ends = seg1 <= x1;
-        const int slot = began ? 0 : ends ? -1 : 1;
-        write_rows<T>(p, c.b, h, row0, rows, obuf, L::kOutPitch, ml + kWarps * kRowTile, slot);
-        note_stretch(p, piece, (long long)c.b * segs + c.seg, began, ends, seg0, seg1);
+        note_stretch(p, piece, (long long)b * segs + seg, began, ends, seg0, seg1);
+        if (kUnit == 0) tc::fence_async_shared();  // before the next tile arrives there
         __syncthreads();
-        left -= n;
-        c.tile -= 1;
-        if (left > 0) c.next(p, segs);
+        if (kUnit != 0 && p.d < kD) {  // features from d on are 0 again
+            for (int i = lane; i < L::kStage / 16; i += 32)
+                reinterpret_cast<uint4 *>(place(warp))[i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
     }
     if constexpr (kUnit != 0) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -833,7 +851,11 @@ paged_full_kernel(const __grid_constant__ Params p) {
         }
         const bool ends = seg1 <= x1;
         const int slot = began ? 0 : ends ? -1 : 1;
-        write_rows<T>(p, c.b, h, row0, rows, qbuf, L::kPitch, ml + kWarps * 8, slot);
+        for (int i = threadIdx.x; i < rows * p.d; i += kThreads) {
+            const int r = i / p.d, col = i - r * p.d;
+            const float2 v = ml[kWarps * 8 + r];
+            write_value<T>(p, c.b, h, row0, r, col, slot, qbuf[r * L::kPitch + col], v.x, v.y);
+        }
         note_stretch(p, piece, (long long)c.b * segs + c.seg, began, ends, seg0, seg1);
         __syncthreads();
         left -= n;
@@ -1022,6 +1044,13 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     p.d = d;
     p.window = window;
     p.scale2 = scale * 1.44269504088896341f;
+    {
+        unsigned long long words = (uintptr_t)q / 2 | (unsigned)d;
+        if (B > 1) words |= (unsigned long long)p.sq.b;
+        if (Hq > 1) words |= (unsigned long long)p.sq.h;
+        if (T > 1) words |= (unsigned long long)p.sq.n;
+        p.q_words = words % 2 == 0;
+    }
     p.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (p.page_size == 1 << i) p.page_shift = i;

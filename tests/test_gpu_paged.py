@@ -338,21 +338,24 @@ def test_offsets_beyond_32_bits():
                  bound_of("bf16", ref, mean, size, 128, 250)).all())
 
 
-def test_many_sequences_and_one_list():
-    # more sequences than threads of a block, of all lengths: the pieces' borders fall anywhere
+@pytest.mark.parametrize("dtype, d, page", [("bf16", 64, 16), ("bf16", 80, 7), ("bf16", 33, 16),
+                                            ("bf16", 256, 32), ("f32", 48, 16)])
+def test_many_sequences_and_one_list(dtype, d, page):
+    # more sequences than threads of a block, of all lengths: the pieces' borders fall
+    # anywhere, and a block has many stretches
     g = gen(12)
     lengths = [int(x) for x in torch.randint(1, 300, (700,), generator=g, device="cuda")]
-    table, pages = table_of(lengths, 16, g)
-    kc, vc = (pool_of("heads", pages, 2, 16, 64, torch.bfloat16) for _ in range(2))
+    table, pages = table_of(lengths, page, g)
+    kc, vc = (pool_of("heads", pages, 2, page, d, DT[dtype]) for _ in range(2))
     for x in (kc, vc):
         x.normal_(generator=g)
-    q = torch.randn(700, 4, 64, generator=g, device="cuda").bfloat16()
+    q = torch.randn(700, 4, d, generator=g, device="cuda").to(DT[dtype])
     got = la.decode_step_paged(q, kc, vc, table, ints([n - 1 for n in lengths]))
     some = list(range(0, 700, 41))
     ref, mean, size = plain_attention(q[some][:, :, None], kc, vc, table[some],
-                                      [lengths[b] - 1 for b in some], 0.125, 0)
+                                      [lengths[b] - 1 for b in some], d ** -0.5, 0)
     assert bool(((got[some][:, :, None].double() - ref).abs() <=
-                 bound_of("bf16", ref, mean, size, 64, 300)).all())
+                 bound_of(dtype, ref, mean, size, d, 300)).all())
     # each sequence alone: other pieces, the same within rounding
     for b in some[:4]:
         one = la.decode_step_paged(q[b:b + 1], kc, vc, table[b:b + 1], ints([lengths[b] - 1]))
