@@ -883,14 +883,17 @@ _CACHE = struct.Struct("@PP6qPqPiii")
 
 
 def _int32s(t, name, shape, index):
-    if t.dtype is not _torch().int32:
+    """The pointer of an int32 tensor [B] or [B, any] with contiguous rows."""
+    have = t.shape
+    if (_CODES or _codes()).get(t.dtype) != 4:
         raise TypeError(f"{name} must be int32")
-    if t.dim() != len(shape) or t.shape[0] != shape[0]:
+    if len(have) != len(shape) or have[0] != shape[0]:
         raise ValueError(f"{name} must have the shape {list(shape)}")
     if t.get_device() != index:
         raise ValueError("all tensors must be on one CUDA device")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if have[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index):
@@ -900,16 +903,16 @@ def _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index):
         raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
     if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("the cache must have the dtype of q, k and v")
-    for t in (k_cache, v_cache):
-        if t.get_device() != index:
-            raise ValueError("all tensors must be on one CUDA device")
-        if t.stride(-1) != 1 and d > 1:
-            raise ValueError("the last dimension must be contiguous")
-    _int32s(page_table, "page_table", (B, "pages"), index)
-    _int32s(lengths, "lengths", (B,), index)
-    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
-                       *v_cache.stride()[:3], page_table.data_ptr(), page_table.stride(0),
-                       lengths.data_ptr(), shape[0], shape[2], page_table.shape[1])
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError("all tensors must be on one CUDA device")
+    kp, kh, kn, kd = k_cache.stride()
+    vp, vh, vn, vd = v_cache.stride()
+    if d > 1 and (kd != 1 or vd != 1):
+        raise ValueError("the last dimension must be contiguous")
+    table = _int32s(page_table, "page_table", (B, "pages"), index)
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, kh, kn, vp, vh, vn, table,
+                       page_table.stride(0), _int32s(lengths, "lengths", (B,), index), shape[0],
+                       shape[2], page_table.shape[1])
 
 
 def append_cache(k, v, k_cache, v_cache, page_table, lengths, frequencies=None, *, q=None,
@@ -948,14 +951,13 @@ def append_cache(k, v, k_cache, v_cache, page_table, lengths, frequencies=None, 
             raise ValueError("q_out must have q's shape")
         index, strides = _check_rows(k, q, k, v, q_out)
     cache = _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index)
-    if counts is not None:
-        _int32s(counts, "counts", (B,), index)
+    pc = None if counts is None else _int32s(counts, "counts", (B,), index)
     rope, keep = _rope(frequencies, None, offset, interleaved, ks, index)
     code, lib = _code(dtype), load_library()
     to, back = _enter(index, stream)
     try:
         st = lib.la_append_cache(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), cache,
-                                 _ptr(counts), strides, rope, B, Hq, Hk, T, d, code, to)
+                                 pc, strides, rope, B, Hq, Hk, T, d, code, to)
     finally:
         if back >= 0:
             _leave(back)
@@ -977,7 +979,6 @@ def decode_step_paged(q, k_cache, v_cache, page_table, lengths, out=None, *, sca
     share those of the cache in order (Hq a multiple of Hk).  scale: 1 / sqrt(d) if
     None.  A sequence with a negative length gives zeros.  Other arguments as
     append_cache.  Returns out, like q."""
-    torch = _torch()
     qs, device, dtype = q.shape, q.device, q.dtype
     if len(qs) not in (3, 4):
         raise ValueError("q must be [B, H, T, d], or [B, H, d] for one token")
@@ -988,6 +989,8 @@ def decode_step_paged(q, k_cache, v_cache, page_table, lengths, out=None, *, sca
         raise ValueError("out must have q's shape")
     if k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, Hk, page_size, d]")
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be in 0..2^31-1")
     Hk = k_cache.shape[1]
     index, strides = _check_rows(q, q, out)
     cache = _cache(k_cache, v_cache, page_table, lengths, B, Hk, d, dtype, index)
@@ -1004,6 +1007,7 @@ def decode_step_paged(q, k_cache, v_cache, page_table, lengths, out=None, *, sca
                 ws_bytes = lib.la_decode_step_paged_workspace_bytes(Hq, Hk, T, d, code)
                 _PAGED_WORKSPACE[key] = ws_bytes
             if ws_bytes:
+                torch = _torch()
                 ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         st = lib.la_decode_step_paged(q.data_ptr(), out.data_ptr(), cache, strides, scale, window,
                                       B, Hq, Hk, T, d, code, _ptr(ws), ws_bytes, to)
@@ -1028,17 +1032,27 @@ def _check_cross(q, k, v):
     return qs[0], qs[1], ks[1], qs[2], ks[2], qs[3]
 
 
+_FORMS = {}
+
+
+def _form(feature_map, normalise):
+    """_variant, one object for each of the four."""
+    form = _FORMS.get((feature_map, normalise))
+    if form is None:
+        form = _FORMS[feature_map, normalise] = _variant(feature_map, normalise)
+    return form
+
+
 def _check_cross_states(S, z, B, Hk, d, index):
-    float32 = _torch().float32
+    codes = _CODES or _codes()
     if S.shape != (B, Hk, d, d) or z.shape != (B, Hk, d):
         raise ValueError("S must be [B, Hk, d, d] and z [B, Hk, d]")
-    if S.dtype is not float32 or z.dtype is not float32:
+    if codes.get(S.dtype) != LA_F32 or codes.get(z.dtype) != LA_F32:
         raise TypeError("S and z must be float32")
-    for t in (S, z):
-        if t.get_device() != index:
-            raise ValueError("all tensors must be on one CUDA device")
-        if not t.is_contiguous():
-            raise ValueError("a state must be contiguous")
+    if S.get_device() != index or z.get_device() != index:
+        raise ValueError("all tensors must be on one CUDA device")
+    if not (S.is_contiguous() and z.is_contiguous()):
+        raise ValueError("a state must be contiguous")
 
 
 def _cross_workspace(lib, sizes, code, backward, device, stream):
@@ -1077,7 +1091,7 @@ def forward_cross(q, k, v, lengths=None, out=None, *, S=None, z=None,
     _check_cross_states(S, z, B, Hk, d, index)
     if lengths is not None:
         _int32s(lengths, "lengths", (B,), index)
-    form = _variant(feature_map, normalise)
+    form = _form(feature_map, normalise)
     code, lib = _code(dtype), load_library()
     to, back = _enter(index, stream)
     try:
@@ -1114,7 +1128,7 @@ def backward_cross(dout, q, k, v, S, z, lengths=None, *, dq=None, dk=None, dv=No
     _check_cross_states(S, z, B, Hk, d, index)
     if lengths is not None:
         _int32s(lengths, "lengths", (B,), index)
-    form = _variant(feature_map, normalise)
+    form = _form(feature_map, normalise)
     code, lib = _code(dtype), load_library()
     to, back = _enter(index, stream)
     try:
@@ -1149,7 +1163,7 @@ def decode_step_cross(S, z, q, out=None, *, feature_map: str = "elu1", normalise
     Hk = S.shape[1]
     index, strides = _check_rows(q, q, out)
     _check_cross_states(S, z, B, Hk, d, index)
-    form = _variant(feature_map, normalise)
+    form = _form(feature_map, normalise)
     code, lib = _code(dtype), load_library()
     to, back = _enter(index, stream)
     try:

@@ -293,6 +293,9 @@ def test_binding_refuses(lib):
         la.decode_step_paged(k[0, 0], pool, pool, table, lengths)
     with pytest.raises(ValueError, match="page_size"):
         la.decode_step_paged(k, pool[0], pool[0], table, lengths)
+    for window in (-1, 1 << 31, 1 << 32):
+        with pytest.raises(ValueError, match="window"):
+            la.decode_step_paged(k, pool, pool, table, lengths, window=window)
     with pytest.raises(ValueError, match="CUDA"):
         la.forward_cross(k, k, k)
     with pytest.raises(ValueError, match="heads and tokens"):
