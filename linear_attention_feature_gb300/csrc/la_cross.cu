@@ -31,7 +31,9 @@ namespace {
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ float phi_of(float x, int phi) {
-    return !phi ? x : x > 0.f ? x + 1.f : expf(x);
+    if (!phi) return x;
+    const float e = expf(fminf(x, 0.f));
+    return x > 0.f ? x + 1.f : x <= 0.f ? e : x;  // NaN of NaN
 }
 __device__ __forceinline__ float slope_of(float x, int phi) {
     return !phi || x > 0.f ? 1.f : expf(x);
@@ -52,11 +54,24 @@ struct SumParams {
     float *S, *z;  // [segs][heads][d d], [segs][heads][d]
 };
 
+// Number i of a thread's M of a tile's side, from its place t in 16: runs of four, 64
+// apart, so that a warp's 16-byte reads of shared memory meet no bank twice.
+__device__ __forceinline__ int in_tile(int t, int i) { return i / 4 * 64 + t * 4 + i % 4; }
+
+template <int M>
+__device__ __forceinline__ void read_side(const float *row, int t, float (&v)[M]) {
+#pragma unroll
+    for (int i = 0; i < M; i += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(row + in_tile(t, i));
+        v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+    }
+}
+
 // S[a][c] += w_i f(x_i)[a] y_i[c] and z[a] += u_i w_i f(x_i)[a] over a part of the
-// tokens, w = r or 1 and u = -t or 1: 64 x 64 sums per block, 4 x 4 per thread.
-template <typename T>
+// tokens, w = r or 1 and u = -t or 1: kTile x kTile sums per block, M x M per thread.
+template <typename T, int kTile>
 __global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
-    constexpr int kTok = 32, kTile = 64, kPitch = kTile + 4;
+    constexpr int kTok = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kTok][kPitch], Y[kTok][kPitch];
     __shared__ float U[kTok];
     const int tiles = (p.d + kTile - 1) / kTile;
@@ -68,30 +83,32 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
     const long long all = (long long)p.group * p.L;
     const long long i0 = seg * p.per, i1 = min(i0 + p.per, all);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, zacc[4] = {};
-    // a thread brings feature f of every fourth row, the next tokens' while these are summed
-    constexpr int kPer = kTok * kTile / kThreads;
+    float acc[M][M] = {}, zacc[M] = {};
+    // a thread brings feature f of some rows, the next tokens' while these are summed
+    constexpr int kPer = kTok * kTile / kThreads, kStep = kThreads / kTile;
     const int f = threadIdx.x % kTile, r0 = threadIdx.x / kTile;
     const bool in_x = a0 + f < p.d, in_y = c0 + f < p.d;
     const T *xs = static_cast<const T *>(p.x) + b * p.sx.b + a0 + f;
     const T *ys = static_cast<const T *>(p.y) + b * p.sy.b + c0 + f;
     float x[kPer], y[kPer];
     float2 rt[kPer];
+    int g0 = (int)(i0 / max(p.L, 1)), n0 = (int)(i0 - (long long)g0 * p.L);  // of token i
     auto fetch = [&](long long i) {
-        const int g0 = (int)(i / p.L), n0 = (int)(i - (long long)g0 * p.L);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int row = r0 + k * (kThreads / kTile);
+            const int row = r0 + k * kStep;
             int g = g0, n = n0 + row;
             if (n >= p.L) g += n / p.L, n %= p.L;
             const bool ok = i + row < i1 && n < len;
             const long long hh = (long long)h * p.group + g;
             x[k] = y[k] = 0.f;
-            rt[k] = make_float2(1.f, -1.f);
+            rt[k] = make_float2(ok ? 1.f : 0.f, -1.f);
             if (ok && p.rt) rt[k] = p.rt[(head * p.group + g) * p.L + n];
-            if (ok && in_x) x[k] = phi_of(to_f(xs[hh * p.sx.h + n * p.sx.n]), p.phi);
+            if (ok && in_x) x[k] = to_f(xs[hh * p.sx.h + n * p.sx.n]);
             if (ok && in_y) y[k] = to_f(ys[hh * p.sy.h + n * p.sy.n]);
         }
+        n0 += kTok;
+        if (n0 >= p.L) g0 += n0 / p.L, n0 %= p.L;
     };
     const long long end = p.group == 1 ? min(i1, (long long)len) : i1;
     if (i0 < end) fetch(i0);
@@ -99,36 +116,38 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int row = r0 + k * (kThreads / kTile);
-            A[row][f] = rt[k].x * x[k];
+            const int row = r0 + k * kStep;
+            A[row][f] = in_x ? rt[k].x * phi_of(x[k], p.phi) : 0.f;
             Y[row][f] = y[k];
             if (f == 0) U[row] = -rt[k].y;
         }
         __syncthreads();
         if (i + kTok < end) fetch(i + kTok);
-#pragma unroll 8
+#pragma unroll
         for (int row = 0; row < kTok; ++row) {
-            const float4 a = *reinterpret_cast<const float4 *>(&A[row][ty * 4]);
-            const float4 y = *reinterpret_cast<const float4 *>(&Y[row][tx * 4]);
-            const float av[4] = {a.x, a.y, a.z, a.w}, yv[4] = {y.x, y.y, y.z, y.w};
+            float av[M], yv[M];
+            read_side(A[row], ty, av);
+            read_side(Y[row], tx, yv);
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(av[m], yv[n], acc[m][n]);
+                for (int n = 0; n < M; ++n) acc[m][n] = fmaf(av[m], yv[n], acc[m][n]);
             if (tx == 0)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) zacc[m] = fmaf(av[m], U[row], zacc[m]);
+                for (int m = 0; m < M; ++m) zacc[m] = fmaf(av[m], U[row], zacc[m]);
         }
     }
     float *S = p.S + (seg * p.heads + head) * p.d * p.d;
     float *z = p.z + (seg * p.heads + head) * p.d;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int a = a0 + ty * 4 + m;
+    for (int m = 0; m < M; ++m) {
+        const int a = a0 + in_tile(ty, m);
         if (a >= p.d) continue;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (c0 + tx * 4 + n < p.d) S[a * p.d + c0 + tx * 4 + n] = acc[m][n];
+        for (int n = 0; n < M; ++n) {
+            const int c = c0 + in_tile(tx, n);
+            if (c < p.d) S[a * p.d + c] = acc[m][n];
+        }
         if (tx == 0 && c0 == 0) z[a] = zacc[m];
     }
 }
@@ -163,10 +182,11 @@ struct ReadParams {
     int Hk, group, L, d, phi, norm;
 };
 
-// y_i = S^T f(x_i), over f . z with norm: 64 rows x 64 columns per block.
-template <typename T>
+// y_i = S^T f(x_i), over f . z with norm: kTile rows x kTile columns per block, M x M
+// per thread.
+template <typename T, int kTile>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
-    constexpr int kTile = 64, kStep = 32, kPitch = kTile + 4;
+    constexpr int kStep = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kStep][kPitch], Y[kStep][kPitch];
     __shared__ float Z[kStep];
     const int tiles = (p.d + kTile - 1) / kTile, row_tiles = (p.L + kTile - 1) / kTile;
@@ -179,7 +199,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
     const int len = tokens_of(p.lengths, b, p.L);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
-    float acc[4][4] = {}, den[4] = {};
+    const float *S = p.S + state * p.d * p.d;
+    float acc[M][M] = {}, den[M] = {};
     // the next features' values come while these are multiplied
     constexpr int kPer = kTile * kStep / kThreads;
     float av[kPer], yv[kPer], zv = 0.f;
@@ -187,12 +208,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = threadIdx.x + i * kThreads;
-            const int row = e / kStep, f = e % kStep, a = e / kTile, c = e % kTile;
-            av[i] = yv[i] = 0.f;
-            if (n0 + row < len && k0 + f < p.d)
-                av[i] = phi_of(to_f(x[(n0 + row) * p.sx.n + k0 + f]), p.phi);
-            if (k0 + a < p.d && c0 + c < p.d)
-                yv[i] = p.S[(state * p.d + k0 + a) * p.d + c0 + c];
+            const int row = n0 + e / kStep, f = k0 + e % kStep, a = k0 + e / kTile,
+                      c = c0 + e % kTile;
+            av[i] = row < len && f < p.d ? to_f(x[row * p.sx.n + f]) : 0.f;
+            yv[i] = a < p.d && c < p.d ? S[a * p.d + c] : 0.f;
         }
         if (threadIdx.x < kStep)
             zv = p.norm && k0 + (int)threadIdx.x < p.d ? p.z[state * p.d + k0 + threadIdx.x] : 0.f;
@@ -203,34 +222,35 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = threadIdx.x + i * kThreads;
-            A[e % kStep][e / kStep] = av[i];
+            // features from d on meet zeros of S; rows behind the length are not used
+            A[e % kStep][e / kStep] = phi_of(av[i], p.phi);
             Y[e / kTile][e % kTile] = yv[i];
         }
         if (threadIdx.x < kStep) Z[threadIdx.x] = zv;
         __syncthreads();
         if (k0 + kStep < p.d) fetch(k0 + kStep);
-#pragma unroll 8
+#pragma unroll
         for (int k = 0; k < kStep; ++k) {
-            const float4 a = *reinterpret_cast<const float4 *>(&A[k][ty * 4]);
-            const float4 y = *reinterpret_cast<const float4 *>(&Y[k][tx * 4]);
-            const float av[4] = {a.x, a.y, a.z, a.w}, yv[4] = {y.x, y.y, y.z, y.w};
-            const float zk = Z[k];
+            float a[M], y[M];
+            read_side(A[k], ty, a);
+            read_side(Y[k], tx, y);
+            const float z = Z[k];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < M; ++m) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(av[m], yv[n], acc[m][n]);
-                den[m] = fmaf(av[m], zk, den[m]);
+                for (int n = 0; n < M; ++n) acc[m][n] = fmaf(a[m], y[n], acc[m][n]);
+                den[m] = fmaf(a[m], z, den[m]);
             }
         }
     }
     T *y = static_cast<T *>(p.y) + b * p.sy.b + h * p.sy.h;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int n = n0 + ty * 4 + m;
+    for (int m = 0; m < M; ++m) {
+        const int n = n0 + in_tile(ty, m);
         if (n >= p.L) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = c0 + tx * 4 + e;
+        for (int e = 0; e < M; ++e) {
+            const int c = c0 + in_tile(tx, e);
             if (c >= p.d) continue;
             // without keys there is nothing to average: 0
             const float v = !p.norm ? acc[m][e] : den[m] == 0.f ? 0.f : acc[m][e] / den[m];
@@ -439,16 +459,21 @@ cudaError_t counted(cudaError_t e) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Parts of the tokens of one head's sums: enough that all SMs are busy twice over, at
-// most 1024 tokens each (a longer chain of fp32 additions rounds more off).
+// The side of the sums' and products' square tiles: 8 x 8 values per thread, which read
+// the least of shared memory, where a tile of 128 is not mostly empty (8 x 8 x 2048 x 128
+// fp32: XX us, 465 us by 4 x 4).
+int tile_of(int d) { return d > 64 ? 128 : 64; }
+
+// Parts of the tokens of one head's sums: enough that all SMs are busy three times over,
+// at most 1024 tokens each (a longer chain of fp32 additions rounds more off).
 Cut cut_of(const Shape &sh, long long tokens, int sms) {
-    const int tiles = (sh.d + 63) / 64;
+    const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
     const long long blocks = std::max(1LL, sh.heads() * tiles * tiles);
     long long segs = std::max((tokens + 1023) / 1024,
-                              std::min((2LL * sms + blocks - 1) / blocks, tokens / 64));
+                              std::min((3LL * sms + blocks - 1) / blocks, tokens / 64));
     segs = std::max(1LL, std::min(segs, 65535LL));
     Cut c;
-    c.per = ((tokens + segs - 1) / segs + 31) / 32 * 32;
+    c.per = ((tokens + segs - 1) / segs + 15) / 16 * 16;
     c.segs = c.per ? (int)((tokens + c.per - 1) / c.per) : 1;
     if (c.segs < 1) c.segs = 1;
     return c;
@@ -506,9 +531,12 @@ cudaError_t sums(const Shape &sh, Rows x, Rows y, int group, int L, const float2
         part + up(sizeof(float) * (size_t)cut.segs * sh.heads() * sh.state()));
     p.S = cut.segs == 1 ? S : reinterpret_cast<float *>(part);
     p.z = cut.segs == 1 ? z : pz;
-    const int tiles = (sh.d + 63) / 64;
+    const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
     const dim3 grid((unsigned)(sh.heads() * tiles * tiles), (unsigned)cut.segs);
-    sum_kernel<T><<<grid, kThreads, 0, s>>>(p);
+    if (tile_of(sh.d) == 128)
+        sum_kernel<T, 128><<<grid, kThreads, 0, s>>>(p);
+    else
+        sum_kernel<T, 64><<<grid, kThreads, 0, s>>>(p);
     cudaError_t e = counted(cudaSuccess);
     if (e != cudaSuccess || cut.segs == 1) return e;
     const long long nS = sh.heads() * sh.state(), nz = sh.heads() * sh.d;
@@ -521,10 +549,19 @@ template <typename T>
 cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float *S,
                  const float *z, int norm, const int *lengths, cudaStream_t s) {
     ReadParams p{x.x, y.x, x.s, y.s, S, z, lengths, sh.Hk, group, L, sh.d, sh.phi, norm};
+    // (tiles of 64 where those of 128 would leave SMs without one)
+    const long long heads = sh.heads() * group;
+    int sms = 0;
+    const cudaError_t e = tchost::sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int tile = sh.d > 64 && heads * ((L + 127) / 128) * ((sh.d + 127) / 128) >= sms ? 128 : 64;
     const long long blocks =
-        sh.heads() * group * ((L + 63) / 64) * (long long)((sh.d + 63) / 64);
+        heads * (((long long)L + tile - 1) / tile) * ((sh.d + tile - 1) / tile);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    read_kernel<T><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    if (tile == 128)
+        read_kernel<T, 128><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    else
+        read_kernel<T, 64><<<(unsigned)blocks, kThreads, 0, s>>>(p);
     return counted(cudaSuccess);
 }
 
