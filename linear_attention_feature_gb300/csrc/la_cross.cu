@@ -70,7 +70,7 @@ __device__ __forceinline__ void read_side(const float *row, int t, float (&v)[M]
 // S[a][c] += w_i f(x_i)[a] y_i[c] and z[a] += u_i w_i f(x_i)[a] over a part of the
 // tokens, w = r or 1 and u = -t or 1: kTile x kTile sums per block, M x M per thread.
 template <typename T, int kTile>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const SumParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sum_kernel(const SumParams p) {
     constexpr int kTok = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kTok][kPitch], Y[kTok][kPitch];
     __shared__ float U[kTok];
@@ -183,9 +183,10 @@ struct ReadParams {
 };
 
 // y_i = S^T f(x_i), over f . z with norm: kTile rows x kTile columns per block, M x M
-// per thread.
+// per thread.  (8 x 8 x 2048 x 128 fp32: 164 us with all the registers a thread takes, 191
+// us with half of them; bf16, d = 256, is faster by a quarter with two blocks per SM.)
 template <typename T, int kTile>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(const ReadParams p) {
     constexpr int kStep = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kStep][kPitch], Y[kStep][kPitch];
     __shared__ float Z[kStep];
@@ -461,7 +462,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // The side of the sums' and products' square tiles: 8 x 8 values per thread, which read
 // the least of shared memory, where a tile of 128 is not mostly empty (8 x 8 x 2048 x 128
-// fp32: XX us, 465 us by 4 x 4).
+// fp32 into states: 175 us, 465 us by 4 x 4).
 int tile_of(int d) { return d > 64 ? 128 : 64; }
 
 // Parts of the tokens of one head's sums: enough that all SMs are busy three times over,
