@@ -572,7 +572,8 @@ la_status la_append_cache(const void *q, const void *k, const void *v, void *q_o
  * (la_append_cache with the same lengths): a step appends, attends, and adds T
  * to lengths once all layers are done.
  *   q          [B][Hq][T][d] device, dtype `dtype`, read only.
- *   out        [B][Hq][T][d] device, dtype `dtype`, written.
+ *   out        [B][Hq][T][d] device, dtype `dtype`, written; may alias neither q
+ *              nor the cache.
  *   cache      read only.  A key whose place has no page is left out.  Pages
  *              that lie wholly before all windows are not read and need no
  *              table entry.

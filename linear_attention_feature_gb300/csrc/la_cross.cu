@@ -466,11 +466,13 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int tile_of(int d) { return d > 64 ? 128 : 64; }
 
 // Parts of the tokens of one head's sums: enough that all SMs are busy three times over,
-// at most 1024 tokens each (a longer chain of fp32 additions rounds more off).
+// and of at most 1024 tokens each (a longer chain of fp32 additions rounds more off) as
+// long as the parts of all states stay within 256 MB.
 Cut cut_of(const Shape &sh, long long tokens, int sms) {
     const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
     const long long blocks = std::max(1LL, sh.heads() * tiles * tiles);
-    long long segs = std::max((tokens + 1023) / 1024,
+    const long long most = (1LL << 26) / std::max(1LL, sh.heads() * (sh.state() + sh.d));
+    long long segs = std::max(std::min((tokens + 1023) / 1024, most),
                               std::min((3LL * sms + blocks - 1) / blocks, tokens / 64));
     segs = std::max(1LL, std::min(segs, 65535LL));
     Cut c;

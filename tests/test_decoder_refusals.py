@@ -268,6 +268,16 @@ def test_workspace_queries(lib):
     assert g(0, 4, 2, 5, 7, 64, 1, 0) == g(1, 3, 2, 5, 7, 64, 1, 0) == g(1, 4, 2, 5, 7, 0, 1, 1) == 0
 
 
+def test_workspaces_stay_bounded(lib):
+    # the parts of many states over long sequences: 256 MB and the states themselves
+    g = lib.la_cross_workspace_bytes
+    states = 1024 * (256 * 256 + 256) * 4
+    assert g(64, 16, 16, 1, 1 << 20, 256, 0, 0) <= (1 << 28) + 2 * states
+    assert g(64, 16, 16, 1 << 16, 1, 256, 0, 1) <= (1 << 28) + 3 * states + 8 * 1024 * (1 << 16)
+    f = lib.la_decode_step_paged_workspace_bytes
+    assert f(128, 1, 1 << 20, 256, 1) == f(16, 1, 1, 256, 1)  # whatever the queries are
+
+
 def test_the_packed_cache_is_the_struct():
     assert la._CACHE.size <= ctypes.sizeof(Cache)  # the struct is padded behind its last member
     packed = la._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14)

@@ -138,6 +138,10 @@ CASES = [
     ("bf16", 2, 2, 2, 50, 140, 64, [140, 100], "apart"),
     ("bf16", 1, 2, 1, 40, 61, 37, None, "apart"),
     ("bf16", 1, 1, 1, 40, 300, 256, [299], "heads"),
+    ("bf16", 2, 2, 1, 50, 70, 8, [70, 33], "tokens"),
+    ("bf16", 1, 4, 2, 140, 130, 72, None, "tokens"),
+    ("bf16", 2, 2, 2, 300, 700, 120, [64, 700], "heads"),
+    ("f32", 1, 2, 1, 260, 300, 200, [290], "tokens"),
 ]
 
 
@@ -186,6 +190,30 @@ def test_forward_and_backward(dtype, B, Hq, Hk, N, M, d, lengths, layout, fmap, 
     assert all(torch.equal(a, b) for a, b in zip(again, (out, S, z)))
     again = la.backward_cross(dout, q, k, v, S, z, lens, **form)
     assert all(torch.equal(a, b) for a, b in zip(again, (dq, dk, dv)))
+
+
+@pytest.mark.parametrize("d", [8, 64, 72, 128])
+def test_outputs_inside_larger_tensors(d):
+    # token-major outputs with other features beside them: the tiles' columns and rows
+    # beyond the tensor leave those as they were
+    B, H, N, M, pad = 2, 2, 130, 200, 16
+    q, k, v, dout = case("bf16", B, H, H, N, M, d, [200, 90])
+    lens = ints([200, 90])
+    want = la.forward_cross(q, k, v, lens)
+    grads = la.backward_cross(dout, q, k, v, want[1], want[2], lens)
+
+    def inside(L):
+        whole = torch.full((B, L + 3, H, d + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        return whole, whole[:, 1:L + 1, :, 8:d + 8].transpose(1, 2)
+
+    whole, views = zip(*(inside(L) for L in (N, N, M, M)))
+    la.forward_cross(q, k, v, lens, views[0])
+    la.backward_cross(dout, q, k, v, want[1], want[2], lens, dq=views[1], dk=views[2], dv=views[3])
+    la.check_device_status()
+    for got, ref, w in zip(views, (want[0], *grads), whole):
+        assert torch.equal(got, ref)
+        got.fill_(7.0)
+        assert bool((w == 7.0).all())
 
 
 @pytest.mark.parametrize("dtype, d", [("bf16", 64), ("bf16", 128), ("f32", 40)])

@@ -261,6 +261,27 @@ def test_attention(dtype, lengths, Hq, Hk, T, d, page, window, layout):
     assert torch.equal(out, got)
 
 
+@pytest.mark.parametrize("dtype, Hq, Hk, T, d, page, scale", [
+    ("bf16", 6, 2, 40, 64, 48, -0.2),   # a short prompt: many tiles of queries
+    ("bf16", 2, 1, 33, 200, 16, 0.05),
+    ("bf16", 8, 8, 5, 128, 112, 0.0),   # all keys alike
+    ("f32", 6, 2, 40, 64, 48, -0.2),
+])
+def test_more_queries_and_other_scales(dtype, Hq, Hk, T, d, page, scale):
+    g, t = gen(T), DT[dtype]
+    lengths = [T + 250, T, T + 17]
+    table, pages = table_of(lengths, page, g)
+    kc, vc = (pool_of("tokens", pages, Hk, page, d, t) for _ in range(2))
+    fill(lengths, table, page, kc, vc, g)
+    q = torch.randn(3, Hq, T, d, generator=g, device="cuda").to(t)
+    before = [n - T for n in lengths]
+    got = la.decode_step_paged(q, kc, vc, table, ints(before), scale=scale)
+    ref, mean, size = plain_attention(q, kc, vc, table, before, scale, 0)
+    bound = bound_of(dtype, ref, mean, size, d, max(lengths))
+    assert bool(((got.double() - ref).abs() <= bound).all())
+    la.check_device_status()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_batch_with_unused_places_and_missing_pages(dtype):
     g, t = gen(8), DT[dtype]
