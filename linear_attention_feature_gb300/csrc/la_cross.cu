@@ -388,7 +388,9 @@ struct StepParams {
 };
 
 // kR queries of one state: the state is read once, a row of it by as many threads as
-// it has vectors of V, the rows in turn by the rest.  Bound by that read.
+// it has vectors of V, the rows in turn by the rest.  Bound by that read: 256 x 32 states
+// of 128 x 128 in 91 us, 6.0 TB/s.  (Vectors of 32 bytes 97 us; 16 rows under way per
+// thread instead of 8 94 us.)
 template <typename T, int kR, int V>
 __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p) {
     __shared__ float F[kR][LA_MAX_D], den[kR];
@@ -552,12 +554,14 @@ template <typename T>
 cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float *S,
                  const float *z, int norm, const int *lengths, cudaStream_t s) {
     ReadParams p{x.x, y.x, x.s, y.s, S, z, lengths, sh.Hk, group, L, sh.d, sh.phi, norm};
-    // (tiles of 64 where those of 128 would leave SMs without one)
+    // Tiles of 64 where those of 128 would be half empty (8192 states, 32 rows of each: 650
+    // us, 980 us with 128) or leave SMs without one (4 x 256 rows, 256 keys: forward 30 us, 42
+    // us with 128; 2 x 16 x 1024 rows: 111 us, 102 us with 128).
     const long long heads = sh.heads() * group;
     int sms = 0;
     const cudaError_t e = tchost::sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int tile = sh.d > 64 && heads * ((L + 127) / 128) * ((sh.d + 127) / 128) >= sms ? 128 : 64;
+    const int tile = sh.d > 64 && L > 64 && heads * ((L + 127) / 128) * ((sh.d + 127) / 128) >= sms ? 128 : 64;
     const long long blocks =
         heads * (((long long)L + tile - 1) / tile) * ((sh.d + tile - 1) / tile);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -630,15 +634,18 @@ cudaError_t launch_step(const StepParams &p, long long states, cudaStream_t s) {
 template <typename T>
 cudaError_t step(const Shape &sh, Rows q, Rows out, const float *S, const float *z,
                  cudaStream_t s) {
-    // more queries than this per state: tiles of them
+    // Many queries per state go as tiles of them.  With 256 x 32 states of 128, 4 queries
+    // of each take 154 us singly and 187 us as a tile on the tensor cores, 8 take 231 and
+    // 188; without tensor cores 16 take 437 and 641, 32 take 837 and 650.
     const Rows rows[2] = {q, out};
-    if (sizeof(T) == 2 && (long long)sh.G() * sh.N > 16 && tc_rows(sh, rows, 2, nullptr, 0, S, z)) {
+    const long long queries = (long long)sh.G() * sh.N;
+    if (sizeof(T) == 2 && queries > 4 && tc_rows(sh, rows, 2, nullptr, 0, S, z)) {
         int sms = 0;
         cudaError_t e = tchost::sm_count(&sms);
         int *status = e == cudaSuccess ? device_status_word(&e) : nullptr;
         return e == cudaSuccess ? tc_read(sh, q, out, S, z, false, sms, status, s) : e;
     }
-    if ((long long)sh.G() * sh.N > 16)
+    if (queries > 24)
         return read<T>(sh, q, out, sh.G(), sh.N, S, z, sh.norm, nullptr, s);
     const StepParams p{S, z, q.x, out.x, q.s, out.s, sh.Hk, sh.G(), sh.N, sh.d, sh.phi, sh.norm};
     return sh.d % 4 == 0 && (uintptr_t)S % 16 == 0 ? launch_step<T, 4>(p, sh.heads(), s)

@@ -14,6 +14,12 @@
 // written at once; what lies in several leaves (m, l, output) of each piece in the
 // workspace, and a second kernel joins the pieces in order.  Repeated calls are
 // bit-identical.
+//
+// Measured, bf16, join included: 32 heads on 8 of 128, 1 x 131072 keys 93 us, 5.8 TB/s;
+// 256 x up to 4096 keys 397 us, 6.3 TB/s; 4 new tokens, 16 heads of 64, against 32 x up to
+// 8192 keys 119 us, 5.6 TB/s.  A call takes 10 to 14 us more than its bytes:
+// the way to the first keys (lengths, table, tile: one after the other), the pieces'
+// unequal ends, the join.  Small calls take 7 to 18 us, whatever they read.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -42,7 +48,6 @@ struct Params {
     int pages, page_size, max_pages, page_shift;  // page_size is 2^page_shift, or -1
     int B, Hk, G, T, d, window;
     int *status;
-    int by_stretch;  // see note()
     int q_words;     // queries lie in 32-bit words
     int row_tile, row_tiles;  // queries of a block, tiles of them per head of keys
     float scale2;             // scale log2(e)
@@ -213,23 +218,11 @@ __device__ __forceinline__ void write_value(const Params &p, int b, int h, int r
     }
 }
 
-// What the join has to know: a stretch (b segs + seg, 64 bits: .x low, .y high; .y = -1:
-// none) and the first and the last block that have pieces of it (.z, .w).  Where the call
-// has fewer stretches than blocks there is a note for each stretch, from the block where
-// it begins; else one for each block, of the stretch that its piece continues.
-__device__ __forceinline__ void note(const Params &p, int i, long long stretch, int i0, int i1) {
-    p.info[i] = make_int4((int)(unsigned)stretch, (int)(stretch >> 32), i0, i1);
-}
-__device__ __forceinline__ void note_stretch(const Params &p, const Piece &piece, long long stretch,
-                                             bool began, bool ends, long long seg0,
-                                             long long seg1) {
-    if (threadIdx.x) return;
-    if (p.by_stretch) {
-        if (!began)
-            note(p, (int)stretch, ends ? -1 : stretch, piece.of(seg0), piece.of(seg1 - 1));
-    } else if (began) {
-        note(p, blockIdx.x, stretch, piece.of(seg0), piece.of(seg1 - 1));
-    }
+// What the join has to know of each block: the stretch that its piece continues (b segs +
+// seg, 64 bits: .x low, .y high; .y = -1: none) and the first and the last block that have
+// pieces of it (.z, .w).
+__device__ __forceinline__ void note(const Params &p, long long stretch, int i0, int i1) {
+    p.info[blockIdx.x] = make_int4((int)(unsigned)stretch, (int)(stretch >> 32), i0, i1);
 }
 
 // ------------------------------------------------------------------ bf16
@@ -261,7 +254,10 @@ struct Half {
     static constexpr int kStage = 2 * kSide;                                   // of a warp
     static constexpr int kStages = kD == 64 || kD == 192 ? 4 : 3;
     static constexpr int kBlocks = kD == 64 && kUnit == 0 ? 3 : kD <= 128 ? 2 : 1;  // per SM
-    static constexpr int kOffMl = kWarps * kStages * kStage;
+    // Steps of the products' 16 features whose queries lie in registers; the rest of
+    // them, which would spill, in each lane's 16 bytes of shared memory.
+    static constexpr int kHeld = kD <= 128 ? kD / 16 : kD == 192 ? 8 : 6, kOffQ = kWarps * kStages * kStage;
+    static constexpr int kOffMl = kOffQ + kWarps * (kD / 16 - kHeld) * 512;
     static constexpr int kOffMask = kOffMl + kWarps * kRowTile * 8;
     static constexpr int kOffBar = kOffMask + kWarps * kStages * 4;
     static_assert(kRowTile * kD * 4 <= kStage, "a warp's outputs fit into a stage");
@@ -291,6 +287,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // for one query, but the tensor cores wait for the memory all the same.  P is rounded
 // to bf16 for its product with the values; l sums the rounded ones (a product with a
 // column of ones), so that the weights still add to one.
+//
+// Each warp has its own ring of stages, so no warp waits for another before the stretch's
+// end.  32 sequences of up to 8192 keys (4096 with d = 256), 4 heads shared by 4 each: d =
+// 64 39 us, 128 65 us, 256 96 us (102 us with all queries in registers, which spills).
+// Sums in two chains per score change nothing: the products are not what it waits for.
 template <int kD, int kUnit>
 __global__ void __launch_bounds__(kThreads, Half<kD, kUnit>::kBlocks)
 paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tk,
@@ -326,7 +327,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     Piece piece;
     Place<kTile> c =
         find_place<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan), piece);
-    if (threadIdx.x == 0 && !p.by_stretch) note(p, blockIdx.x, -1, 0, 0);
+    if (threadIdx.x == 0) note(p, -1, 0, 0);
     const long long x1 = piece.x1;
     const int steps = (int)(x1 - piece.x0);
     if (steps == 0) return;
@@ -398,33 +399,46 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     }
     // The queries as the products take them, straight from memory: rows lane / 4 and 8
     // further on, features 2 (lane % 4) and 8 further on of each 16.
-    unsigned a[kD / 16][4];
+    unsigned a[L::kHeld][4];
+    uint4 *rest = reinterpret_cast<uint4 *>(smem + L::kOffQ) + warp * (kD / 16 - L::kHeld) * 32 + lane;
     auto load_queries = [&]() {
         const int h = c.seg / p.row_tiles, row0 = (c.seg - h * p.row_tiles) * p.row_tile;
         const int rows = min(p.row_tile, p.G * p.T - row0);
+        const T *q[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = (lane >> 2) + 8 * i;
-            const T *q = static_cast<const T *>(p.q) +
-                         (r < rows ? row_offset<T>(p, p.sq, c.b, h, row0 + r) : 0);
+            q[i] = static_cast<const T *>(p.q) +
+                   (r < rows ? row_offset<T>(p, p.sq, c.b, h, row0 + r) : 0);
+        }
+        auto load_step = [&](int ks, unsigned (&to)[4]) {
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                    const int r = (lane >> 2) + 8 * i;
                     const int e = 16 * ks + 8 * j + 2 * (lane & 3);
                     unsigned u = 0;
                     if (r < rows && e < p.d) {
                         if (p.q_words) {
-                            u = *reinterpret_cast<const unsigned *>(q + e);
+                            u = *reinterpret_cast<const unsigned *>(q[i] + e);
                         } else {
-                            u = *reinterpret_cast<const unsigned short *>(q + e);
+                            u = *reinterpret_cast<const unsigned short *>(q[i] + e);
                             if (e + 1 < p.d)
-                                u |= (unsigned)*reinterpret_cast<const unsigned short *>(q + e + 1)
+                                u |= (unsigned)*reinterpret_cast<const unsigned short *>(q[i] + e + 1)
                                      << 16;
                         }
                     }
-                    a[ks][2 * j + i] = u;
+                    to[2 * j + i] = u;
                 }
+        };
+#pragma unroll
+        for (int ks = 0; ks < L::kHeld; ++ks) load_step(ks, a[ks]);
+#pragma unroll 4
+        for (int ks = L::kHeld; ks < kD / 16; ++ks) {
+            unsigned u[4];
+            load_step(ks, u);
+            rest[(ks - L::kHeld) * 32] = make_uint4(u[0], u[1], u[2], u[3]);
         }
     };
     load_queries();
@@ -467,8 +481,16 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             for (int ks = 0; ks < kD / 16; ++ks) {
                 unsigned b[4];
                 ldmatrix4(b, st + k_at[ks & 3] + (ks >> 2) * kAtom);
-                mma(s[0], a[ks], b[0], b[1]);
-                mma(s[1], a[ks], b[2], b[3]);
+                unsigned w[4];
+                if (ks < L::kHeld) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = a[ks < L::kHeld ? ks : 0][i];
+                } else {
+                    const uint4 u = rest[(ks - L::kHeld) * 32];
+                    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+                }
+                mma(s[0], w, b[0], b[1]);
+                mma(s[1], w, b[2], b[3]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -620,7 +642,8 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             }
             write_value<T>(p, b, h, row0, r, col, slot, y, top, sum);
         }
-        note_stretch(p, piece, (long long)b * segs + seg, began, ends, seg0, seg1);
+        if (began && threadIdx.x == 0)
+            note(p, (long long)b * segs + seg, piece.of(seg0), piece.of(seg1 - 1));
         if (kUnit == 0) tc::fence_async_shared();  // before the next tile arrives there
         __syncthreads();
         if (kUnit != 0 && p.d < kD) {  // features from d on are 0 again
@@ -661,7 +684,10 @@ struct Full {
 
 // kR queries per block.  A warp takes kKeys keys per step: kParts lanes share a key's
 // scores, each with every kParts-th 16 bytes of it; then each lane takes every 32nd
-// feature of the values.  fp32 throughout.
+// feature of the values.  fp32 throughout.  The case above with d = 128: 193 us with 4
+// queries per key (3.5 TB/s), 131 us with one (5.1 TB/s); bound by shared memory and the
+// fp32 units, since each key is read once for the scores of all queries but multiplied
+// for each.
 template <int kD, int kR, int kUnit>
 __global__ void __launch_bounds__(kThreads, Full<kD>::kBlocks)
 paged_full_kernel(const __grid_constant__ Params p) {
@@ -682,7 +708,7 @@ paged_full_kernel(const __grid_constant__ Params p) {
     Piece piece;
     Place<kTile> c =
         find_place<kTile>(p, reinterpret_cast<long long *>(smem + L::kOffPlan), piece);
-    if (threadIdx.x == 0 && !p.by_stretch) note(p, blockIdx.x, -1, 0, 0);
+    if (threadIdx.x == 0) note(p, -1, 0, 0);
     const long long x1 = piece.x1;
     const int steps = (int)(x1 - piece.x0);
     if (steps == 0) return;
@@ -856,7 +882,8 @@ paged_full_kernel(const __grid_constant__ Params p) {
             const float2 v = ml[kWarps * 8 + r];
             write_value<T>(p, c.b, h, row0, r, col, slot, qbuf[r * L::kPitch + col], v.x, v.y);
         }
-        note_stretch(p, piece, (long long)c.b * segs + c.seg, began, ends, seg0, seg1);
+        if (began && threadIdx.x == 0)
+            note(p, (long long)c.b * segs + c.seg, piece.of(seg0), piece.of(seg1 - 1));
         __syncthreads();
         left -= n;
         c.tile -= 1;
@@ -865,7 +892,8 @@ paged_full_kernel(const __grid_constant__ Params p) {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Joins the stretches that lie in several blocks, one query of one stretch a block.
+// Joins the stretches that lie in several blocks, one query of one stretch a block: the
+// first of a stretch's blocks that continues it.
 // Every warp finds the pieces' factors by itself, 32 at a time in its lanes; kJoin groups
 // of threads take every kJoin-th piece of the output.
 constexpr int kJoin = 4;
@@ -874,9 +902,9 @@ template <typename T>
 __global__ void __launch_bounds__(kJoin *LA_MAX_D) paged_join_kernel(const __grid_constant__ Params p) {
     tc::grid_dep_wait();
     __shared__ float sum[kJoin][LA_MAX_D];
-    const int i = blockIdx.x + !p.by_stretch, r = blockIdx.y;
-    const int4 info = p.info[i];
-    if (info.y < 0 || (!p.by_stretch && info.z != i - 1)) return;
+    const int r = blockIdx.y;
+    const int4 info = p.info[blockIdx.x + 1];
+    if (info.y < 0 || info.z != (int)blockIdx.x) return;
     const long long stretch = (long long)info.y << 32 | (unsigned)info.x;
     const int segs = p.Hk * p.row_tiles;
     const int b = (int)(stretch / segs), seg = (int)(stretch - (long long)b * segs);
@@ -1077,8 +1105,9 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
                            make_map(&maps[0], p.k, p.sk, *cache, Hk, d) &&
                            make_map(&maps[1], p.v, p.sv, *cache, Hk, d);
     if (tiles_fit)
-        c = choose_half<0>(d);
-    else if (dtype == LA_F32)
+        c = choose_half<0>(d);  // d = 128, the case at paged_half_kernel: 65 us; 16-byte copies 80
+                                // us, 4-byte 143 us, plain loads 482 us
+    else if (dtype == LA_F32)  // 193 us; 4-byte copies 241 us
         c = all % 16 == 0 ? choose_full<16>(d, p.row_tile) : choose_full<4>(d, p.row_tile);
     else
         c = all % 16 == 0 ? choose_half<16>(d)
@@ -1094,8 +1123,6 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     const double list = (double)B * Hk * (double)row_tiles * (double)tiles;
     if (list > 1e11) return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     const int blocks = (int)std::min((double)c.blocks_per_sm * sms, list);
-    const double stretches = (double)B * Hk * (double)row_tiles;
-    p.by_stretch = stretches < blocks;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t need = workspace_of(blocks, p.row_tile, d);
     void *ws = workspace, *own = nullptr;
@@ -1122,8 +1149,7 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     // The join is a dependent launch whose blocks start as the pieces' blocks end.  (Let in
     // from the start they cost 10 % of 1 x 131072 keys: 109 us, 98 us without.)
     if (e == cudaSuccess && blocks > 1) {
-        const dim3 grid(p.by_stretch ? (unsigned)stretches : (unsigned)blocks - 1,
-                        (unsigned)p.row_tile);
+        const dim3 grid((unsigned)blocks - 1, (unsigned)p.row_tile);
         const unsigned threads = kJoin * ((unsigned)(d + 31) / 32 * 32);
         e = dtype == LA_F32
                 ? tchost::launch_dependent(paged_join_kernel<float>, grid, threads, 0, s, p)
