@@ -309,6 +309,20 @@ def test_decode_step(dtype, B, Hq, Hk, N, d, shift, fmap, norm):
     check(name, got.reshape(num.shape), (num, size), dtype, 600)
 
 
+@pytest.mark.parametrize("dtype, rows", [("bf16", 4), ("bf16", 5), ("bf16", 17), ("f32", 24),
+                                         ("f32", 25), ("f32", 65)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_steps_of_several_queries(dtype, rows, d):
+    # either side of the sizes where queries go as tiles, shared heads and tokens alike
+    for Hq, N in ((rows, 1), (1, rows)):
+        q, k, v, _ = case(dtype, 2, Hq, 1, N, 90, d, [90, 0])
+        _, S, z = la.forward_cross(q, k, v, ints([90, 0]))
+        ref = plain(q, k, v, q, [90, 0], "elu1", True)
+        got = la.decode_step_cross(S, z, q)
+        check("out", got, ref["out"], dtype, 600)
+        assert not got[1].any()
+
+
 def test_decode_step_continues_the_forward():
     q, k, v, _ = case("bf16", 2, 4, 2, 60, 300, 128, [300, 99])
     out, S, z = la.forward_cross(q, k, v, ints([300, 99]))
