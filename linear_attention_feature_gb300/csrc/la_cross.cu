@@ -10,8 +10,8 @@
 // and dq, dk are df, dg times phi'.  Neither the outputs nor anything else of a
 // token's is kept from the forward: S and z are all that the backward needs.
 //
-// This file has the argument checks and the fp32 CUDA-core kernels, which take any
-// head size, stride and type; bound by the fp32 units.
+// This file has the argument checks, the fp32 kernels on CUDA cores, which take any head
+// size and stride and are bound by the fp32 units, and the single tokens' kernel.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,21 +38,8 @@ __device__ __forceinline__ float phi_of(float x, int phi) {
 __device__ __forceinline__ float slope_of(float x, int phi) {
     return !phi || x > 0.f ? 1.f : expf(x);
 }
-__device__ __forceinline__ int tokens_of(const int *lengths, int b, int M) {
-    return lengths ? min(max(lengths[b], 0), M) : M;
-}
 
 // ---------------------------------------------------------------- sums of outer products
-
-struct SumParams {
-    const void *x, *y;  // rows of features (phi is taken) and of values
-    la_strides sx, sy;
-    const float2 *rt;    // backward: r and t of each row of x, [B][Hk][group][L]
-    const int *lengths;  // forward, or NULL
-    int Hk, group, L, d, phi, segs;
-    long long per, heads;
-    float *S, *z;  // [segs][heads][d d], [segs][heads][d]
-};
 
 // Number i of a thread's M of a tile's side, from its place t in 16: runs of four, 64
 // apart, so that a warp's 16-byte reads of shared memory meet no bank twice.
@@ -69,7 +56,7 @@ __device__ __forceinline__ void read_side(const float *row, int t, float (&v)[M]
 
 // S[a][c] += w_i f(x_i)[a] y_i[c] and z[a] += u_i w_i f(x_i)[a] over a part of the
 // tokens, w = r or 1 and u = -t or 1: kTile x kTile sums per block, M x M per thread.
-template <typename T, int kTile>
+template <int kTile>
 __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const SumParams p) {
     constexpr int kTok = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kTok][kPitch], Y[kTok][kPitch];
@@ -88,8 +75,8 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const SumParams p) {
     constexpr int kPer = kTok * kTile / kThreads, kStep = kThreads / kTile;
     const int f = threadIdx.x % kTile, r0 = threadIdx.x / kTile;
     const bool in_x = a0 + f < p.d, in_y = c0 + f < p.d;
-    const T *xs = static_cast<const T *>(p.x) + b * p.sx.b + a0 + f;
-    const T *ys = static_cast<const T *>(p.y) + b * p.sy.b + c0 + f;
+    const float *xs = static_cast<const float *>(p.x) + b * p.sx.b + a0 + f;
+    const float *ys = static_cast<const float *>(p.y) + b * p.sy.b + c0 + f;
     float x[kPer], y[kPer];
     float2 rt[kPer];
     int g0 = (int)(i0 / max(p.L, 1)), n0 = (int)(i0 - (long long)g0 * p.L);  // of token i
@@ -104,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const SumParams p) {
             x[k] = y[k] = 0.f;
             rt[k] = make_float2(ok ? 1.f : 0.f, -1.f);
             if (ok && p.rt) rt[k] = p.rt[(head * p.group + g) * p.L + n];
-            if (ok && in_x) x[k] = to_f(xs[hh * p.sx.h + n * p.sx.n]);
-            if (ok && in_y) y[k] = to_f(ys[hh * p.sy.h + n * p.sy.n]);
+            if (ok && in_x) x[k] = xs[hh * p.sx.h + n * p.sx.n];
+            if (ok && in_y) y[k] = ys[hh * p.sy.h + n * p.sy.n];
         }
         n0 += kTok;
         if (n0 >= p.L) g0 += n0 / p.L, n0 %= p.L;
@@ -173,20 +160,11 @@ join_kernel(const float *S_part, const float *z_part, float *S, float *z, long l
 
 // ---------------------------------------------------------------- rows times a state
 
-struct ReadParams {
-    const void *x;
-    void *y;
-    la_strides sx, sy;
-    const float *S, *z;
-    const int *lengths;  // rows behind are written as 0, or NULL
-    int Hk, group, L, d, phi, norm;
-};
-
 // y_i = S^T f(x_i), over f . z with norm: kTile rows x kTile columns per block, M x M
-// per thread.  (8 x 8 x 2048 x 128 fp32: 164 us with all the registers a thread takes, 191
-// us with half of them; bf16, d = 256, is faster by a quarter with two blocks per SM.)
-template <typename T, int kTile>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(const ReadParams p) {
+// per thread.  (8 x 8 x 2048 x 128: 164 us with all the registers a thread takes, 191 us
+// with half of them.)
+template <int kTile>
+__global__ void __launch_bounds__(kThreads, 1) read_kernel(const ReadParams p) {
     constexpr int kStep = 16, kPitch = kTile + 4, M = kTile / 16;
     __shared__ __align__(16) float A[kStep][kPitch], Y[kStep][kPitch];
     __shared__ float Z[kStep];
@@ -199,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(
     const long long state = (long long)b * p.Hk + h / p.group;
     const int len = tokens_of(p.lengths, b, p.L);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
+    const float *x = static_cast<const float *>(p.x) + b * p.sx.b + h * p.sx.h;
     const float *S = p.S + state * p.d * p.d;
     float acc[M][M] = {}, den[M] = {};
     // the next features' values come while these are multiplied
@@ -211,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(
             const int e = threadIdx.x + i * kThreads;
             const int row = n0 + e / kStep, f = k0 + e % kStep, a = k0 + e / kTile,
                       c = c0 + e % kTile;
-            av[i] = row < len && f < p.d ? to_f(x[row * p.sx.n + f]) : 0.f;
+            av[i] = row < len && f < p.d ? x[row * p.sx.n + f] : 0.f;
             yv[i] = a < p.d && c < p.d ? S[a * p.d + c] : 0.f;
         }
         if (threadIdx.x < kStep)
@@ -244,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(
             }
         }
     }
-    T *y = static_cast<T *>(p.y) + b * p.sy.b + h * p.sy.h;
+    float *y = static_cast<float *>(p.y) + b * p.sy.b + h * p.sy.h;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const int n = n0 + in_tile(ty, m);
@@ -255,25 +233,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) read_kernel(
             if (c >= p.d) continue;
             // without keys there is nothing to average: 0
             const float v = !p.norm ? acc[m][e] : den[m] == 0.f ? 0.f : acc[m][e] / den[m];
-            from_f(y[n * p.sy.n + c], n < len ? v : 0.f);
+            y[n * p.sy.n + c] = n < len ? v : 0.f;
         }
     }
 }
 
-struct GradParams {
-    const void *y, *x;  // what is multiplied, and what phi is taken of
-    void *dx;
-    la_strides sy, sx, sdx;
-    const float *S, *z;
-    float2 *rt;          // q's side: written
-    const int *lengths;  // k's side: rows behind are written as 0, or NULL
-    int Hk, group, L, d, phi, norm, keys;
-};
-
 // G_i = S y_i, and from it the gradient of row i: on q's side
 // r (G - t z) phi'(x) with r and t left for the sums, on k's side (G + z) phi'(x)
 // (z is then dz).  A warp takes 4 rows whole, a lane every 32nd feature.
-template <typename T, int kCols>  // kCols: 32 features each, of d
+template <int kCols>  // kCols: 32 features each, of d
 __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
     constexpr int kRows = 32, kStep = 32, kPerY = kRows * kStep / kThreads;
     constexpr int kPerW = kCols * 32 * kStep / kThreads;
@@ -285,15 +253,15 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
     const long long state = (long long)b * p.Hk + h / p.group;
     const int len = tokens_of(p.lengths, b, p.L);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T *y = static_cast<const T *>(p.y) + b * p.sy.b + h * p.sy.h;
-    const T *x = static_cast<const T *>(p.x) + b * p.sx.b + h * p.sx.h;
+    const float *y = static_cast<const float *>(p.y) + b * p.sy.b + h * p.sy.h;
+    const float *x = static_cast<const float *>(p.x) + b * p.sx.b + h * p.sx.h;
     // the next features' values come while these are multiplied
     float yv[kPerY], wv[kPerW];
     auto fetch = [&](int k0) {
 #pragma unroll
         for (int i = 0; i < kPerY; ++i) {
             const int e = threadIdx.x + i * kThreads, row = e / kStep, c = e % kStep;
-            yv[i] = n0 + row < len && k0 + c < p.d ? to_f(y[(n0 + row) * p.sy.n + k0 + c]) : 0.f;
+            yv[i] = n0 + row < len && k0 + c < p.d ? y[(n0 + row) * p.sy.n + k0 + c] : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < kPerW; ++i) {
@@ -330,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
             }
         }
     }
-    T *dx = static_cast<T *>(p.dx) + b * p.sdx.b + h * p.sdx.h;
+    float *dx = static_cast<float *>(p.dx) + b * p.sdx.b + h * p.sdx.h;
     float xv[4][kCols], zv[kCols];
 #pragma unroll
     for (int j = 0; j < kCols; ++j) {
@@ -339,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int n = n0 + warp * 4 + m;
-            xv[m][j] = a < p.d && n < len ? to_f(x[n * p.sx.n + a]) : 0.f;
+            xv[m][j] = a < p.d && n < len ? x[n * p.sx.n + a] : 0.f;
         }
     }
 #pragma unroll
@@ -372,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
             const int a = lane + 32 * j;
             if (a >= p.d) continue;
             const float g = r * fmaf(-t, zv[j], acc[m][j]) * slope_of(xv[m][j], p.phi);
-            from_f(dx[n * p.sdx.n + a], n < len ? g : 0.f);
+            dx[n * p.sdx.n + a] = n < len ? g : 0.f;
         }
     }
 }
@@ -462,7 +430,7 @@ cudaError_t counted(cudaError_t e) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The side of the sums' and products' square tiles: 8 x 8 values per thread, which read
+// The side of the fp32 sums' and products' square tiles: 8 x 8 values per thread, which read
 // the least of shared memory, where a tile of 128 is not mostly empty (8 x 8 x 2048 x 128
 // fp32 into states: 175 us, 465 us by 4 x 4).
 int tile_of(int d) { return d > 64 ? 128 : 64; }
@@ -470,9 +438,10 @@ int tile_of(int d) { return d > 64 ? 128 : 64; }
 // Parts of the tokens of one head's sums: enough that all SMs are busy three times over,
 // and of at most 1024 tokens each (a longer chain of fp32 additions rounds more off) as
 // long as the parts of all states stay within 256 MB.
-Cut cut_of(const Shape &sh, long long tokens, int sms) {
-    const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
-    const long long blocks = std::max(1LL, sh.heads() * tiles * tiles);
+Cut cut_of(const Shape &sh, la_dtype dtype, long long tokens, int sms) {
+    const int side = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
+    const int tiles = dtype == LA_F32 ? side * side : (sh.d + 63) / 64;  // of a state
+    const long long blocks = std::max(1LL, sh.heads() * tiles);
     const long long most = (1LL << 26) / std::max(1LL, sh.heads() * (sh.state() + sh.d));
     long long segs = std::max(std::min((tokens + 1023) / 1024, most),
                               std::min((3LL * sms + blocks - 1) / blocks, tokens / 64));
@@ -500,8 +469,8 @@ Plan plan_of(const Shape &sh, la_dtype dtype, int sms, bool back) {
     Plan p{};
     const size_t tc = dtype == LA_BF16 && sh.d <= 128 && sh.d % 8 == 0
                           ? tc_workspace(sh, sms, back) : 0;
-    p.keys = cut_of(sh, sh.M, sms);
-    p.queries = cut_of(sh, (long long)sh.G() * sh.N, sms);
+    p.keys = cut_of(sh, dtype, sh.M, sms);
+    p.queries = cut_of(sh, dtype, (long long)sh.G() * sh.N, sms);
     if (!back) {
         p.total = std::max(tc, part_bytes(sh, p.keys));
         return p;
@@ -536,13 +505,18 @@ cudaError_t sums(const Shape &sh, Rows x, Rows y, int group, int L, const float2
         part + up(sizeof(float) * (size_t)cut.segs * sh.heads() * sh.state()));
     p.S = cut.segs == 1 ? S : reinterpret_cast<float *>(part);
     p.z = cut.segs == 1 ? z : pz;
-    const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
-    const dim3 grid((unsigned)(sh.heads() * tiles * tiles), (unsigned)cut.segs);
-    if (tile_of(sh.d) == 128)
-        sum_kernel<T, 128><<<grid, kThreads, 0, s>>>(p);
-    else
-        sum_kernel<T, 64><<<grid, kThreads, 0, s>>>(p);
-    cudaError_t e = counted(cudaSuccess);
+    cudaError_t e = cudaSuccess;
+    if constexpr (sizeof(T) == 2) {
+        e = half_sums(p, s);
+    } else {
+        const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
+        const dim3 grid((unsigned)(sh.heads() * tiles * tiles), (unsigned)cut.segs);
+        if (tile_of(sh.d) == 128)
+            sum_kernel<128><<<grid, kThreads, 0, s>>>(p);
+        else
+            sum_kernel<64><<<grid, kThreads, 0, s>>>(p);
+        e = counted(cudaSuccess);
+    }
     if (e != cudaSuccess || cut.segs == 1) return e;
     const long long nS = sh.heads() * sh.state(), nz = sh.heads() * sh.d;
     const unsigned blocks = (unsigned)std::min((nS + nz + kThreads - 1) / kThreads, 4096LL);
@@ -558,6 +532,7 @@ cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float 
     // us, 980 us with 128) or leave SMs without one (4 x 256 rows, 256 keys: forward 30 us, 42
     // us with 128; 2 x 16 x 1024 rows: 111 us, 102 us with 128).
     const long long heads = sh.heads() * group;
+    if constexpr (sizeof(T) == 2) return half_read(p, heads, s);
     int sms = 0;
     const cudaError_t e = tchost::sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -566,9 +541,9 @@ cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float 
         heads * (((long long)L + tile - 1) / tile) * ((sh.d + tile - 1) / tile);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (tile == 128)
-        read_kernel<T, 128><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        read_kernel<128><<<(unsigned)blocks, kThreads, 0, s>>>(p);
     else
-        read_kernel<T, 64><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        read_kernel<64><<<(unsigned)blocks, kThreads, 0, s>>>(p);
     return counted(cudaSuccess);
 }
 
@@ -577,17 +552,18 @@ cudaError_t grads(const Shape &sh, Rows y, Rows x, Rows dx, int group, int L, co
                   const float *z, float2 *rt, const int *lengths, int keys, cudaStream_t s) {
     GradParams p{y.x, x.x, dx.x, y.s, x.s, dx.s, S, z, rt, lengths,
                  sh.Hk, group, L, sh.d, sh.phi, sh.norm, keys};
+    if constexpr (sizeof(T) == 2) return half_grads(p, sh.heads() * group, s);
     const long long blocks = sh.heads() * group * ((L + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     auto go = [&](auto kern) {
         kern<<<(unsigned)blocks, kThreads, 0, s>>>(p);
         return counted(cudaSuccess);
     };
-    if (sh.d <= 32) return go(grad_kernel<T, 1>);
-    if (sh.d <= 64) return go(grad_kernel<T, 2>);
-    if (sh.d <= 96) return go(grad_kernel<T, 3>);
-    if (sh.d <= 128) return go(grad_kernel<T, 4>);
-    return go(grad_kernel<T, 8>);
+    if (sh.d <= 32) return go(grad_kernel<1>);
+    if (sh.d <= 64) return go(grad_kernel<2>);
+    if (sh.d <= 96) return go(grad_kernel<3>);
+    if (sh.d <= 128) return go(grad_kernel<4>);
+    return go(grad_kernel<8>);
 }
 
 template <typename T>

@@ -42,5 +42,50 @@ cudaError_t tc_backward(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, cons
                         const float *z, Rows dq, Rows dk, Rows dv, char *ws, int sms, int *status,
                         cudaStream_t s);
 
+#ifdef __CUDACC__
+__device__ __forceinline__ int tokens_of(const int *lengths, int b, int M) {
+    return lengths ? min(max(lengths[b], 0), M) : M;
+}
+#endif
+
+// ---- The parts of a call without those tiles: fp32 in la_cross.cu, bf16 in
+// la_cross_half.cu.
+
+// Sums of outer products.
+struct SumParams {
+    const void *x, *y;  // rows of features (phi is taken) and of values
+    la_strides sx, sy;
+    const float2 *rt;    // backward: r and t of each row of x, [B][Hk][group][L]
+    const int *lengths;  // forward, or NULL
+    int Hk, group, L, d, phi, segs;
+    long long per, heads;
+    float *S, *z;  // [segs][heads][d d], [segs][heads][d]
+};
+
+// Rows times a state.
+struct ReadParams {
+    const void *x;
+    void *y;
+    la_strides sx, sy;
+    const float *S, *z;
+    const int *lengths;  // rows behind are written as 0, or NULL
+    int Hk, group, L, d, phi, norm;
+};
+
+struct GradParams {
+    const void *y, *x;  // what is multiplied, and what phi is taken of
+    void *dx;
+    la_strides sy, sx, sdx;
+    const float *S, *z;
+    float2 *rt;          // q's side: written
+    const int *lengths;  // k's side: rows behind are written as 0, or NULL
+    int Hk, group, L, d, phi, norm, keys;
+};
+
+// `heads`: of the rows' tensor, of all sequences.
+cudaError_t half_sums(const SumParams &p, cudaStream_t s);
+cudaError_t half_read(const ReadParams &p, long long heads, cudaStream_t s);
+cudaError_t half_grads(const GradParams &p, long long heads, cudaStream_t s);
+
 }  // namespace cross
 }  // namespace la
