@@ -12,9 +12,11 @@
 // phi(x) and S as one each for the outputs and dv; S and dS as two for G = S dy and dS v,
 // where large parts cancel.
 //
-// 8 x 8 (on 4) x 2048 to 2048 x 256: 203 us forward, 602 us backward (1367 and 2862 us by
-// fp32 products on CUDA cores); 8 x 8 x 2048 to 2048 x 128 on odd strides 199 and 395 us (551
-// and 932).  Bound by staging: loads, phi and conversions.
+// 8 x 8 (on 4) x 2048 to 2048 x 256: 190 us forward, 533 us backward (1367 and 2862 us by
+// fp32 products on CUDA cores; on odd strides 278 and 766 us); 8 x 8 x 2048 to 2048 x 128 on
+// odd strides 153 and 333 us (551 and 932).  Bound by instructions and latency, 0.3 to 0.5
+// issued per cycle: addresses, phi and conversions on the way to shared memory, and the
+// gradients' ends.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -131,6 +133,22 @@ __global__ void __launch_bounds__(2 * kC, kC == 256 ? 1 : 2) half_sum_kernel(con
             if (n >= p.L) g += n / p.L, n %= p.L;
             return i + row < i1 && n < len;
         };
+        if (i + kTok <= i1 && n0 + kTok <= min(p.L, len)) {  // rows of one head, all of them
+            const long long hh = (long long)h * p.group + g0;
+            const T *px = xs + hh * p.sx.h + (n0 + rx) * p.sx.n;
+            const T *py = ys + hh * p.sy.h + (n0 + ry) * p.sy.n;
+#pragma unroll
+            for (int k = 0; k < kX; ++k) {
+                rt[k] = p.rt ? p.rt[(head * p.group + g0) * p.L + n0 + rx + k * kStepX]
+                             : make_float2(1.f, -1.f);
+                x[k] = load4(px + k * kStepX * p.sx.n, nx, wide);
+            }
+#pragma unroll
+            for (int k = 0; k < kY; ++k) y[k] = load4(py + k * kStepY * p.sy.n, ny, wide);
+            n0 += kTok;
+            if (n0 == p.L) ++g0, n0 = 0;
+            return;
+        }
         int g, n;
 #pragma unroll
         for (int k = 0; k < kX; ++k) {
@@ -358,6 +376,7 @@ template <int kC>
 struct GradSmem {
     T Wh[kC][kStep + kPad], Wl[kC][kStep + kPad], Y[kRows][kStep + kPad];
     float2 red[kC / 64][kRows];  // f . G and f . z of a row, of 64 features each
+    float2 z[kC / 2];            // 0 where it is not used
 };
 
 template <int kC>
@@ -398,6 +417,9 @@ half_grad_kernel(const GradParams p, int wide, int wide_s, int words) {
         }
     };
     fetch(0);
+    if (threadIdx.x < kC)
+        reinterpret_cast<float *>(sm.z)[threadIdx.x] =
+            (p.norm || p.keys) && (int)threadIdx.x < p.d ? z[threadIdx.x] : 0.f;
     for (int k0 = 0; k0 < p.d; k0 += kStep) {
         __syncthreads();
 #pragma unroll
@@ -444,8 +466,6 @@ half_grad_kernel(const GradParams p, int wide, int wide_s, int words) {
         const unsigned short *s = reinterpret_cast<const unsigned short *>(row);
         return (a < p.d ? s[a] : 0u) | (a + 1 < p.d ? (unsigned)s[a + 1] << 16 : 0u);
     };
-    const bool with_z = p.norm || p.keys;
-    auto z_of = [&](int a) { return with_z && a < p.d ? z[a] : 0.f; };
     if (!p.keys) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -462,7 +482,8 @@ half_grad_kernel(const GradParams p, int wide, int wide_s, int words) {
                         const float e0 = phi_fast(low_of(u), p.phi);
                         const float e1 = a + 1 < p.d ? phi_fast(high_of(u), p.phi) : 0.f;
                         dot = fmaf(e0, acc[m][j][2 * i], fmaf(e1, acc[m][j][2 * i + 1], dot));
-                        den = fmaf(e0, z_of(a), fmaf(e1, z_of(a + 1), den));
+                        const float2 za = sm.z[a / 2];
+                        den = fmaf(e0, za.x, fmaf(e1, za.y, den));
                     }
 #pragma unroll
                 for (int o = 1; o < 4; o <<= 1) {
@@ -499,10 +520,11 @@ half_grad_kernel(const GradParams p, int wide, int wide_s, int words) {
                 float g[2] = {};
                 if (n < len) {
                     const unsigned u = pair_of(x + n * p.sx.n, a);
+                    const float2 za = sm.z[a / 2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float xe = e ? high_of(u) : low_of(u);
-                        g[e] = r * fmaf(-t, z_of(a + e), acc[m][j][2 * i + e]) *
+                        g[e] = r * fmaf(-t, e ? za.y : za.x, acc[m][j][2 * i + e]) *
                                slope_fast(xe, phi_fast(xe, p.phi), p.phi);
                     }
                 }
