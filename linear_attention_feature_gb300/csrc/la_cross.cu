@@ -532,6 +532,7 @@ cudaError_t read(const Shape &sh, Rows x, Rows y, int group, int L, const float 
     // us, 980 us with 128) or leave SMs without one (4 x 256 rows, 256 keys: forward 30 us, 42
     // us with 128; 2 x 16 x 1024 rows: 111 us, 102 us with 128).
     const long long heads = sh.heads() * group;
+    if (heads == 0) return cudaSuccess;
     if constexpr (sizeof(T) == 2) return half_read(p, heads, s);
     int sms = 0;
     const cudaError_t e = tchost::sm_count(&sms);
@@ -552,6 +553,7 @@ cudaError_t grads(const Shape &sh, Rows y, Rows x, Rows dx, int group, int L, co
                   const float *z, float2 *rt, const int *lengths, int keys, cudaStream_t s) {
     GradParams p{y.x, x.x, dx.x, y.s, x.s, dx.s, S, z, rt, lengths,
                  sh.Hk, group, L, sh.d, sh.phi, sh.norm, keys};
+    if (sh.heads() * group == 0) return cudaSuccess;
     if constexpr (sizeof(T) == 2) return half_grads(p, sh.heads() * group, s);
     const long long blocks = sh.heads() * group * ((L + 31) / 32);
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;

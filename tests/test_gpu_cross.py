@@ -279,6 +279,20 @@ def test_a_mean_far_from_zero_does_not_cost_the_gradient():
         assert rel <= 2.0 ** -16 * 8 * 2048 ** 0.5 / 1.4 + 3 * 2.0 ** -8, (name, rel)
 
 
+@pytest.mark.parametrize("dtype, d", [("bf16", 64), ("bf16", 256), ("f32", 40)])
+def test_keys_without_queries(dtype, d):
+    # no heads of queries, or no tokens of them: states all the same, gradients of 0
+    for Hq, N in ((0, 5), (2, 0)):
+        q, k, v, dout = case(dtype, 2, Hq, 2, N, 70, d, None, layout="heads")
+        out, S, z = la.forward_cross(q, k, v)
+        ref = plain(q.new_zeros(2, 2, 1, d), k, v, k.new_zeros(2, 2, 1, d), None, "elu1", True)
+        check("S", S, ref["S"], dtype, 600)
+        check("z", z, ref["z"], dtype, 600)
+        assert out.shape == q.shape
+        dq, dk, dv = la.backward_cross(dout, q, k, v, S, z)
+        assert dq.shape == q.shape and not dk.any() and not dv.any()
+
+
 # ---------------------------------------------------------------- single tokens
 
 @pytest.mark.parametrize("fmap, norm", [("elu1", True), ("identity", False)])
