@@ -684,10 +684,10 @@ struct Full {
 
 // kR queries per block.  A warp takes kKeys keys per step: kParts lanes share a key's
 // scores, each with every kParts-th 16 bytes of it; then each lane takes every 32nd
-// feature of the values.  fp32 throughout.  The case above with d = 128: 193 us with 4
-// queries per key (3.5 TB/s), 131 us with one (5.1 TB/s); bound by shared memory and the
-// fp32 units, since each key is read once for the scores of all queries but multiplied
-// for each.
+// feature of the values.  fp32 throughout.  The case above with d = 128: 169 us with 4
+// queries per key (4.0 TB/s), 133 us with one (5.0 TB/s); bound by the latency of a warp's
+// step, 8 warps per SM.  (A running maximum per query, each with its branch, and features
+// counted up to d: 192 us.  Queries in registers, where they fit: 166 us.)
 template <int kD, int kR, int kUnit>
 __global__ void __launch_bounds__(kThreads, Full<kD>::kBlocks)
 paged_full_kernel(const __grid_constant__ Params p) {
@@ -772,7 +772,10 @@ paged_full_kernel(const __grid_constant__ Params p) {
             const int key = (c.s.first + c.tile) * kTile + warp * kKeys + key_in;
             const bool whole = all_see(p, c.s, key - key_in, kKeys);
             float s[kR] = {};
-            for (int e = 4 * part; e < p.d; e += 4 * L::kParts) {
+#pragma unroll
+            for (int i = 0; i < kD; i += 4 * L::kParts) {
+                const int e = i + 4 * part;  // (features from d on are 0)
+                if (i >= p.d) break;
                 const float4 k4 = *reinterpret_cast<const float4 *>(ks + key_in * L::kPitch + e);
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
@@ -784,6 +787,8 @@ paged_full_kernel(const __grid_constant__ Params p) {
                     s[r] = fmaf(q4.w, k4.w, s[r]);
                 }
             }
+            float top[kR];
+            bool moved = false;  // the same in all lanes
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
 #pragma unroll
@@ -792,18 +797,23 @@ paged_full_kernel(const __grid_constant__ Params p) {
                 if (!(mask >> key_in & 1) || key > last[r] ||
                     (p.window > 0 && key <= last[r] - p.window))
                     s[r] = -INFINITY;
-                float top = s[r];
+                top[r] = s[r];
 #pragma unroll
                 for (int w = 1; w < kKeys; w <<= 1)
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-                top = fmaxf(top, m[r]);
-                if (top > m[r]) {  // the same in all lanes
-                    const float w = exp2f(m[r] - top);
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], w));
+                moved |= top[r] > m[r];
+            }
+            if (moved)
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const float t = fmaxf(top[r], m[r]), w = exp2f(m[r] - finite_max(t));
                     l[r] *= w;
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) o[r][j] *= w;
-                    m[r] = top;
+                    m[r] = t;
                 }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
                 const float w = exp2f(s[r] - finite_max(m[r]));
                 if (part == 0) {
                     l[r] += w;
@@ -1107,7 +1117,7 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     if (tiles_fit)
         c = choose_half<0>(d);  // d = 128, the case at paged_half_kernel: 65 us; 16-byte copies 80
                                 // us, 4-byte 143 us, plain loads 482 us
-    else if (dtype == LA_F32)  // 193 us; 4-byte copies 241 us
+    else if (dtype == LA_F32)  // 4-byte copies take 1.25 times as long
         c = all % 16 == 0 ? choose_full<16>(d, p.row_tile) : choose_full<4>(d, p.row_tile);
     else
         c = all % 16 == 0 ? choose_half<16>(d)
