@@ -430,23 +430,28 @@ cudaError_t counted(cudaError_t e) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The side of the fp32 sums' and products' square tiles: 8 x 8 values per thread, which read
-// the least of shared memory, where a tile of 128 is not mostly empty (8 x 8 x 2048 x 128
-// fp32 into states: 175 us, 465 us by 4 x 4).
-int tile_of(int d) { return d > 64 ? 128 : 64; }
+// The side of the fp32 sums' square tiles: 8 x 8 values per thread, which read the least
+// of shared memory, where a tile of 128 is not mostly empty and there are enough of them
+// (8 x 8 x 2048 x 128 into states: 175 us, 465 us by 4 x 4; forward of 16 heads x
+// 1024 x 96 52 us, 60 us with 64; of 8 heads x 512 x 128 31 us, 23 us with 64).
+int tile_of(const Shape &sh, long long tokens, int sms) {
+    const long long side = (sh.d + 127) / 128;
+    return sh.d > 64 && sh.heads() * side * side * (tokens / 256) >= sms / 3 ? 128 : 64;
+}
 
 // Parts of the tokens of one head's sums: enough that all SMs are busy three times over,
 // and of at most 1024 tokens each (a longer chain of fp32 additions rounds more off) as
 // long as the parts of all states stay within 256 MB.
 Cut cut_of(const Shape &sh, la_dtype dtype, long long tokens, int sms) {
-    const int side = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
+    Cut c;
+    c.tile = tile_of(sh, tokens, sms);
+    const int side = (sh.d + c.tile - 1) / c.tile;
     const int tiles = dtype == LA_F32 ? side * side : (sh.d + 63) / 64;  // of a state
     const long long blocks = std::max(1LL, sh.heads() * tiles);
     const long long most = (1LL << 26) / std::max(1LL, sh.heads() * (sh.state() + sh.d));
     long long segs = std::max(std::min((tokens + 1023) / 1024, most),
                               std::min((3LL * sms + blocks - 1) / blocks, tokens / 64));
     segs = std::max(1LL, std::min(segs, 65535LL));
-    Cut c;
     c.per = ((tokens + segs - 1) / segs + 15) / 16 * 16;
     c.segs = c.per ? (int)((tokens + c.per - 1) / c.per) : 1;
     if (c.segs < 1) c.segs = 1;
@@ -509,9 +514,9 @@ cudaError_t sums(const Shape &sh, Rows x, Rows y, int group, int L, const float2
     if constexpr (sizeof(T) == 2) {
         e = half_sums(p, s);
     } else {
-        const int tiles = (sh.d + tile_of(sh.d) - 1) / tile_of(sh.d);
+        const int tiles = (sh.d + cut.tile - 1) / cut.tile;
         const dim3 grid((unsigned)(sh.heads() * tiles * tiles), (unsigned)cut.segs);
-        if (tile_of(sh.d) == 128)
+        if (cut.tile == 128)
             sum_kernel<128><<<grid, kThreads, 0, s>>>(p);
         else
             sum_kernel<64><<<grid, kThreads, 0, s>>>(p);

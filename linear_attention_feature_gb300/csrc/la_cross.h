@@ -24,7 +24,7 @@ struct Rows {
 
 // Tokens of one head whose sums make up a state, cut into `segs` parts of `per`.
 struct Cut {
-    int segs;
+    int segs, tile;  // tile: the side of a block's sums in fp32
     long long per;
 };
 
