@@ -192,6 +192,60 @@ def test_forward_and_backward(dtype, B, Hq, Hk, N, M, d, lengths, layout, fmap, 
     assert all(torch.equal(a, b) for a, b in zip(again, (dq, dk, dv)))
 
 
+@pytest.mark.parametrize("B, Hq, Hk, N, M, d, lengths, layout", [
+    (1, 2, 1, 3000, 5000, 256, None, "tokens"), (2, 8, 1, 129, 257, 200, [257, 31], "tokens"),
+    (2, 6, 3, 31, 1100, 129, [1100, 1], "apart"), (1, 2, 2, 128, 33, 3, None, "heads"),
+    (2, 2, 1, 200, 700, 65, [700, 640], "tokens"), (1, 3, 1, 127, 300, 254, None, "heads"),
+    (1, 4, 2, 300, 513, 128, [512], "apart"), (3, 2, 2, 40, 64, 66, [64, 0, 63], "tokens"),
+])
+def test_bf16_of_any_size(B, Hq, Hk, N, M, d, lengths, layout):
+    # widths of 64, 128 and 256 columns, rows by 8 bytes, by words and by single values
+    test_forward_and_backward("bf16", B, Hq, Hk, N, M, d, lengths, layout, "elu1", True)
+    test_forward_and_backward("bf16", B, Hq, Hk, N, M, d, lengths, layout, "identity", False)
+
+
+@pytest.mark.parametrize("d, bad", [(256, float("nan")), (61, float("inf")), (130, float("nan"))])
+def test_padding_of_bf16_rows_of_any_size(d, bad):
+    # what lies behind a sequence's length, and beside a row, reaches nothing
+    lengths, N, M = [70, 5], 33, 100
+    q, k, v, dout = case("bf16", 2, 2, 1, N, M, d, lengths, layout="apart")
+    lens = ints(lengths)
+    clean = la.forward_cross(q, k, v, lens)
+    grads = la.backward_cross(dout, q, k, v, clean[1], clean[2], lens)
+    for x in (k, v):
+        for b, n in enumerate(lengths):
+            x[b, :, n:] = bad
+    for x in (q, k, v, dout):  # the rows' neighbours in memory
+        whole = torch.as_strided(x, x.shape[:3] + (d + 5,), x.stride(), x.storage_offset() - 1)
+        whole[..., 0] = bad
+        whole[..., d + 1:] = bad
+    got = la.forward_cross(q, k, v, lens)
+    assert all(torch.equal(a, b) for a, b in zip(got, clean))
+    got = la.backward_cross(dout, q, k, v, clean[1], clean[2], lens)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+@pytest.mark.parametrize("d", [61, 66, 132, 250])
+def test_outputs_of_any_size_inside_larger_tensors(d):
+    B, H, N, M = 2, 2, 130, 90
+    q, k, v, dout = case("bf16", B, H, H, N, M, d, [90, 40])
+    lens = ints([90, 40])
+    want = la.forward_cross(q, k, v, lens)
+    grads = la.backward_cross(dout, q, k, v, want[1], want[2], lens)
+
+    def inside(L):
+        whole = torch.full((B, L + 3, H, d + 6), 7.0, dtype=torch.bfloat16, device="cuda")
+        return whole, whole[:, 1:L + 1, :, 3:d + 3].transpose(1, 2)
+
+    whole, views = zip(*(inside(L) for L in (N, N, M, M)))
+    la.forward_cross(q, k, v, lens, views[0])
+    la.backward_cross(dout, q, k, v, want[1], want[2], lens, dq=views[1], dk=views[2], dv=views[3])
+    for got, ref, w in zip(views, (want[0], *grads), whole):
+        assert torch.equal(got, ref)
+        got.fill_(7.0)
+        assert bool((w == 7.0).all())
+
+
 @pytest.mark.parametrize("d", [8, 64, 72, 128])
 def test_outputs_inside_larger_tensors(d):
     # token-major outputs with other features beside them: the tiles' columns and rows
