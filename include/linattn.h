@@ -673,8 +673,8 @@ size_t la_cross_workspace_bytes(int B, int Hq, int Hk, int N, int M, int d,
  *   q, out     [B][Hq][N][d] device, dtype `dtype`.
  *   strides    2 strides, of q and out, or NULL: contiguous.
  * Other arguments as la_forward_cross.  One kernel, no workspace.  fp32
- * throughout, but with bf16 and five or more queries per state phi(q) and S are
- * rounded to bf16 for their product, as in la_forward_cross.
+ * throughout, but with bf16 and five or more tokens phi(q) and S may be rounded
+ * to bf16 for their product, as in la_forward_cross.
  */
 la_status la_decode_step_cross(const float *S, const float *z, const void *q, void *out,
                                const la_strides *strides, int B, int Hq, int Hk, int N,

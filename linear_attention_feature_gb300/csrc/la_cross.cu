@@ -617,18 +617,19 @@ cudaError_t launch_step(const StepParams &p, long long states, cudaStream_t s) {
 template <typename T>
 cudaError_t step(const Shape &sh, Rows q, Rows out, const float *S, const float *z,
                  cudaStream_t s) {
-    // Many queries per state go as tiles of them.  With 256 x 32 states of 128, 4 queries
-    // of each take 154 us singly and 187 us as a tile on the tensor cores, 8 take 231 and
-    // 188; without tensor cores 16 take 437 and 641, 32 take 837 and 650.
+    // Many tokens go as tiles, each of one head of queries; heads that share a state do not
+    // make a tile fuller.  With 256 x 32 states of 128, 4 tokens take 154 us singly and 187 us
+    // as a tile of la_cross_tc.cu, 8 take 231 and 188 (and 8 heads of one token, with 256 x 8
+    // states, 65 and 179); with 128 x 16 of 100 in bf16 8 take 50 and 52, 12 take 98 and 54; in
+    // fp32, 256 x 32 of 128, 16 take 437 and 641, 32 take 837 and 650.
     const Rows rows[2] = {q, out};
-    const long long queries = (long long)sh.G() * sh.N;
-    if (sizeof(T) == 2 && queries > 4 && tc_rows(sh, rows, 2, nullptr, 0, S, z)) {
+    if (sizeof(T) == 2 && sh.N > 4 && tc_rows(sh, rows, 2, nullptr, 0, S, z)) {
         int sms = 0;
         cudaError_t e = tchost::sm_count(&sms);
         int *status = e == cudaSuccess ? device_status_word(&e) : nullptr;
         return e == cudaSuccess ? tc_read(sh, q, out, S, z, false, sms, status, s) : e;
     }
-    if (queries > 24)
+    if (sh.N > (sizeof(T) == 2 ? 8 : 24))
         return read<T>(sh, q, out, sh.G(), sh.N, S, z, sh.norm, nullptr, s);
     const StepParams p{S, z, q.x, out.x, q.s, out.s, sh.Hk, sh.G(), sh.N, sh.d, sh.phi, sh.norm};
     return sh.d % 4 == 0 && (uintptr_t)S % 16 == 0 ? launch_step<T, 4>(p, sh.heads(), s)

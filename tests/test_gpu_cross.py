@@ -377,9 +377,9 @@ def test_decode_step(dtype, B, Hq, Hk, N, d, shift, fmap, norm):
     check(name, got.reshape(num.shape), (num, size), dtype, 600)
 
 
-@pytest.mark.parametrize("dtype, rows", [("bf16", 4), ("bf16", 5), ("bf16", 17), ("f32", 24),
-                                         ("f32", 25), ("f32", 65)])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype, rows", [("bf16", 4), ("bf16", 5), ("bf16", 9), ("bf16", 17),
+                                         ("f32", 24), ("f32", 25), ("f32", 65)])
+@pytest.mark.parametrize("d", [64, 128, 100])
 def test_steps_of_several_queries(dtype, rows, d):
     # either side of the sizes where queries go as tiles, shared heads and tokens alike
     for Hq, N in ((rows, 1), (1, rows)):
