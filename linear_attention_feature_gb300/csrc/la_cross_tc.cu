@@ -1349,7 +1349,9 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     float o[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) o[q] = u2f(v[i + q]);
-                    *reinterpret_cast<uint4 *>(vt + tile_at(128, row, f0 + 32 * h + i)) = shut8(o);
+                    // (0 times dS is not 0 where dS is not finite)
+                    *reinterpret_cast<uint4 *>(vt + tile_at(128, row, f0 + 32 * h + i)) =
+                        row < len ? shut8(o) : make_uint4(0, 0, 0, 0);
                 }
             }
             fence_async_shared();

@@ -1,0 +1,85 @@
+"""Linear cross attention where values are not finite: what the formula makes of them in
+the results that they reach, zeros where zeros are promised, and the other results
+bit for bit as without them, on each set of kernels."""
+import math
+
+import pytest
+
+import linear_attention_feature_gb300 as la
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+INF, NAN = math.inf, math.nan
+
+# bf16 by tiles, with a head that fills them and one that does not; bf16 of any size and
+# stride; fp32
+PATHS = [("bf16", 64, 0), ("bf16", 80, 0), ("bf16", 128, 0), ("bf16", 256, 0), ("bf16", 61, 0),
+         ("bf16", 64, 5), ("f32", 64, 0), ("f32", 100, 0)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    la.build.build()
+    la.load_library()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+LENGTHS, N, M = [70, 200, 0], 150, 200
+
+
+def inputs(dtype, d, pad, shift=0.0):
+    """q, dout [3, 4, N, d] and k, v [3, 2, M, d], rows d + pad apart."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+
+    def rows(H, L):
+        x = torch.randn(3, H, L, d + pad, generator=g, device="cuda").mul_(0.7).add_(shift).to(t)
+        return x[..., 1:d + 1] if pad else x
+
+    return rows(4, N), rows(4, N), rows(2, M), rows(2, M)
+
+
+def same(a, b):
+    """Bit for bit, every NaN being like any other."""
+    return torch.equal(a.isnan(), b.isnan()) and torch.equal(torch.nan_to_num(a, 9.0, INF, -INF),
+                                                             torch.nan_to_num(b, 9.0, INF, -INF))
+
+
+def but(x, *at):
+    """x without what lies at `at`."""
+    x = x.clone()
+    x[at] = 0
+    return x
+
+
+def padding_is_zero(*xs):
+    for x in xs:
+        for b, n in enumerate(LENGTHS):
+            assert not bool(x[b, :, n:].ne(0).any()), b  # (a NaN is not 0)
+
+
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_a_gradient_that_is_not_finite(dtype, d, pad, bad):
+    q, dout, k, v = inputs(dtype, d, pad)
+    lens, at, c = ints(LENGTHS), (0, 1, 100), d // 3
+    _, S, z = la.forward_cross(q, k, v, lens)
+    want = la.backward_cross(dout, q, k, v, S, z, lens)
+    dout[(*at, c)] = bad
+    dq, dk, dv = la.backward_cross(dout, q, k, v, S, z, lens)
+    assert not bool(dq[at].isfinite().any()) and torch.equal(but(dq, *at), but(want[0], *at))
+    # the state of heads 0 and 1: its dS is not finite in one column, its dz in all rows
+    # (with bf16 NaN may stand for an infinity: a low part of 0 times it)
+    assert not bool(dk[0, 0, :70].isfinite().any())
+    assert torch.equal(but(dk, 0, 0, slice(70)), but(want[1], 0, 0, slice(70)))
+    column = (0, 0, slice(70), c)
+    assert not bool(dv[column].isfinite().any())
+    assert torch.equal(but(dv, *column), but(want[2], *column))
+    padding_is_zero(dk, dv)
+    la.check_device_status()
