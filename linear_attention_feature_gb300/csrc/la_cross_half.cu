@@ -271,7 +271,7 @@ half_read_kernel(const ReadParams p, int wide, int wide_s, int words) {
     constexpr int kT = 2 * kC;
     constexpr int kX = kRows * kStep / 4 / kT, kS = kStep * kC / 4 / kT;
     __shared__ __align__(16) T A[kRows][kStep + kPad], Y[kStep][kC + kPad];
-    __shared__ float inv[kRows];
+    __shared__ float rows_den[kRows];
     const int row_tiles = (p.L + kRows - 1) / kRows;
     const long long bh = blockIdx.x / row_tiles;  // of x's heads
     const int n0 = (int)(blockIdx.x - bh * row_tiles) * kRows;
@@ -349,8 +349,7 @@ half_read_kernel(const ReadParams p, int wide, int wide_s, int words) {
     for (int i = 0; i < kX; ++i) {
 #pragma unroll
         for (int o = 1; o < kStep / 4; o <<= 1) den[i] += __shfl_xor_sync(~0u, den[i], o);
-        if (fx == 0)  // without keys there is nothing to average: 0
-            inv[rx + i * (kT / (kStep / 4))] = !p.norm ? 1.f : den[i] == 0.f ? 0.f : 1.f / den[i];
+        if (fx == 0) rows_den[rx + i * (kT / (kStep / 4))] = p.norm ? den[i] : 1.f;
     }
     __syncthreads();
     T *y = static_cast<T *>(p.y) + b * p.sy.b + h * p.sy.h;
@@ -360,12 +359,15 @@ half_read_kernel(const ReadParams p, int wide, int wide_s, int words) {
         for (int i = 0; i < 2; ++i) {
             const int row = wr + 16 * m + 8 * i + (lane >> 2), n = n0 + row;
             if (n >= p.L) continue;
-            const bool ok = n < len && inv[row] != 0.f;
+            // Without keys there is nothing to average: 0.  (The sign for that is the
+            // denominator itself: 1 / den is 0 for an infinite one, too.)
+            const float d = rows_den[row], inv = 1.f / d;
+            const bool ok = n < len && d != 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 store2(y + n * p.sy.n, wc + 8 * j + (lane & 3) * 2, p.d,
-                       ok ? acc[m][j][2 * i] * inv[row] : 0.f,
-                       ok ? acc[m][j][2 * i + 1] * inv[row] : 0.f, words);
+                       ok ? acc[m][j][2 * i] * inv : 0.f,
+                       ok ? acc[m][j][2 * i + 1] * inv : 0.f, words);
         }
 }
 

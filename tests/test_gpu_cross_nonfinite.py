@@ -64,6 +64,33 @@ def padding_is_zero(*xs):
             assert not bool(x[b, :, n:].ne(0).any()), b  # (a NaN is not 0)
 
 
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_an_infinite_query(dtype, d, pad):
+    # one feature's phi and the denominator are infinite: inf / inf in all of the row
+    q, dout, k, v = inputs(dtype, d, pad)
+    lens, at = ints(LENGTHS), (0, 3, 77)
+    want = la.forward_cross(q, k, v, lens)
+    grads = la.backward_cross(dout, q, k, v, *want[1:], lens)
+    q[(*at, d // 2)] = INF
+    out, S, z = la.forward_cross(q, k, v, lens)
+    assert bool(out[at].isnan().all()) and torch.equal(but(out, *at), but(want[0], *at))
+    assert torch.equal(S, want[1]) and torch.equal(z, want[2])
+    # tokens of a head by ones and by many: the same row of NaN
+    for n in (1, 3, 9, 40):
+        some = la.decode_step_cross(S, z, q[:, :, 77 - n // 2:77 - n // 2 + n])
+        assert bool(some[0, 3, n // 2].isnan().all())
+        some[0, 3, n // 2] = 0
+        assert bool(some.isfinite().all())
+    # the head's state is the one that heads 2 and 3 share: its dk and dv are NaN
+    dq, dk, dv = la.backward_cross(dout, q, k, v, S, z, lens)
+    assert bool(dq[at].isnan().all()) and torch.equal(but(dq, *at), but(grads[0], *at))
+    for x, y in ((dk, grads[1]), (dv, grads[2])):
+        assert bool(x[0, 1, :70].isnan().all())
+        assert torch.equal(but(x, 0, 1, slice(70)), but(y, 0, 1, slice(70)))
+    padding_is_zero(dk, dv)
+    la.check_device_status()
+
+
 @pytest.mark.parametrize("bad", [INF, -INF, NAN])
 @pytest.mark.parametrize("dtype, d, pad", PATHS)
 def test_a_gradient_that_is_not_finite(dtype, d, pad, bad):
