@@ -179,10 +179,13 @@ __device__ __forceinline__ void phi8(float (&e)[8], int phi) {
 __device__ __forceinline__ float slope_of_phi(float f, int phi) {
     return !phi ? 1.f : fminf(f, 1.f);
 }
-// What eight numbers lose as bf16, as bf16.
+// What eight numbers lose as bf16, as bf16.  Of an infinity that is the same infinity (less
+// the largest number below it), so that the two parts have a sum.  (The bounds cost the
+// states' kernel 2 %; a look at the keys' largest instead costs as much.)
 __device__ __forceinline__ uint4 low8(const float (&e)[8], const uint4 high) {
+    const auto bound = [](uint32_t u) { return bf2_max(bf2_min(u, 0x7F7F7F7Fu), 0xFF7FFF7Fu); };
     float h[8];
-    open8(high, h);
+    open8(make_uint4(bound(high.x), bound(high.y), bound(high.z), bound(high.w)), h);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const float2 l = __fadd2_rn(make_float2(e[i], e[i + 1]), make_float2(-h[i], -h[i + 1]));
@@ -190,6 +193,11 @@ __device__ __forceinline__ uint4 low8(const float (&e)[8], const uint4 high) {
         h[i + 1] = l.y;
     }
     return shut8(h);
+}
+// A number as a pair of bf16, high and low; the low one of an infinity is 0.
+__device__ __forceinline__ uint32_t split(float x) {
+    const float high = __bfloat162float(__float2bfloat16_rn(x));
+    return pack_bf16x2(x, fabsf(high) < INFINITY ? x - high : 0.f);
 }
 
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
@@ -681,11 +689,9 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                                                tile_at(DK, S.row(me.et, i), S.col(me.et, i))) =
                         shut8(e);
                 }
-                if (me.et < DK) {
-                    const float high = __bfloat162float(__float2bfloat16_rn(z));
+                if (me.et < DK)
                     *reinterpret_cast<uint32_t *>(smem + L::OFF_Z + sw128_offset(me.et, 0)) =
-                        pack_bf16x2(z, z - high);
-                }
+                        split(z);
                 fence_async_shared();
                 arrive_warp(&sm.s_ready);
             }
@@ -998,11 +1004,12 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 }
                 if (me.et < DK) {  // row DK: m, row DK + 1: what it loses
                     const float m = me.et < p.d ? sm.m[me.et] : 0.f;
-                    const __nv_bfloat16 high = __float2bfloat16_rn(m);
+                    const uint32_t both = split(m);
                     uint8_t *at = smem + L::OFF_S + (me.et >> 6) * L::SATOM;
-                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(DK, me.et & 63)) = high;
-                    *reinterpret_cast<__nv_bfloat16 *>(at + sw128_offset(DK + 1, me.et & 63)) =
-                        __float2bfloat16_rn(m - __bfloat162float(high));
+                    *reinterpret_cast<uint16_t *>(at + sw128_offset(DK, me.et & 63)) =
+                        (uint16_t)both;
+                    *reinterpret_cast<uint16_t *>(at + sw128_offset(DK + 1, me.et & 63)) =
+                        (uint16_t)(both >> 16);
                 }
                 fence_async_shared();
                 arrive_warp(&sm.s_ready);
@@ -1070,11 +1077,9 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 *reinterpret_cast<uint4 *>(ot + at) = shut8(g);
                 *reinterpret_cast<uint4 *>(qt + at) = shut8(s);
             }
-            if (me.part == 0) {
-                const float high = __bfloat162float(__float2bfloat16_rn(t_all));
+            if (me.part == 0)
                 *reinterpret_cast<uint32_t *>(smem + L::OFF_T + sw128_offset(me.row, 0)) =
-                    pack_bf16x2(t_all, t_all - high);
-            }
+                    split(t_all);
             fence_async_shared();
             arrive_warp(&sm.psi[st]);
             if (lane == 0) mbar_arrive(&sm.out_full);

@@ -110,3 +110,45 @@ def test_a_gradient_that_is_not_finite(dtype, d, pad, bad):
     assert torch.equal(but(dv, *column), but(want[2], *column))
     padding_is_zero(dk, dv)
     la.check_device_status()
+
+
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_a_key_that_is_not_finite(dtype, d, pad, bad):
+    # with the identity, whose phi takes both signs
+    q, dout, k, v = inputs(dtype, d, pad)
+    lens, a, form = ints(LENGTHS), d // 2, {"feature_map": "identity", "normalise": False}
+    want = la.forward_cross(q, k, v, lens, **form)
+    k[1, 1, 150, a] = bad
+    out, S, z = la.forward_cross(q, k, v, lens, **form)
+    row = (1, 1, a)
+    assert same(S[row], bad * v[1, 1, 150].float())  # (no value is 0)
+    assert same(z[row], torch.full_like(z[row], bad))
+    assert torch.equal(but(S, *row), but(want[1], *row)) and torch.equal(but(z, *row), but(want[2], *row))
+    # the heads 2 and 3 of the second sequence: that row of S times q's feature
+    f = q[1, 2:, :, a].float()
+    ref = f[..., None] * (bad * v[1, 1, 150].float())
+    assert same(out[1, 2:].float(), ref)
+    assert torch.equal(but(out, 1, slice(2, 4)), but(want[0], 1, slice(2, 4)))
+    dq, dk, dv = la.backward_cross(dout, q, k, v, S, z, lens, **form)
+    assert not bool(dq[1, 2:, :, a].isfinite().any())
+    assert bool(but(dq, 1, slice(2, 4), slice(None), a).isfinite().all())
+    assert bool(dk.isfinite().all())  # dS v, without the key itself
+    assert not bool(dv[1, 1, 150].isfinite().any())
+    assert bool(but(dv, 1, 1, 150).isfinite().all())
+    padding_is_zero(dk, dv)
+    la.check_device_status()
+
+
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_an_infinite_key_with_the_normaliser(dtype, d, pad):
+    q, dout, k, v = inputs(dtype, d, pad)
+    lens, a = ints(LENGTHS), d // 2
+    want = la.forward_cross(q, k, v, lens)
+    k[1, 1, 150, a] = INF
+    out, S, z = la.forward_cross(q, k, v, lens)
+    row = (1, 1, a)
+    assert same(S[row], INF * v[1, 1, 150].float()) and float(z[row]) == INF
+    assert torch.equal(but(S, *row), but(want[1], *row)) and torch.equal(but(z, *row), but(want[2], *row))
+    assert bool(out[1, 2:].isnan().all())  # inf / inf
+    assert torch.equal(but(out, 1, slice(2, 4)), but(want[0], 1, slice(2, 4)))
