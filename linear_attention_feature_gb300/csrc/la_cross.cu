@@ -104,9 +104,10 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const SumParams p) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const int row = r0 + k * kStep;
+            const bool none = is_none(rt[k]);
             A[row][f] = in_x ? rt[k].x * phi_of(x[k], p.phi) : 0.f;
-            Y[row][f] = y[k];
-            if (f == 0) U[row] = -rt[k].y;
+            Y[row][f] = none ? 0.f : y[k];
+            if (f == 0) U[row] = none ? 0.f : -rt[k].y;
         }
         __syncthreads();
         if (i + kTok < end) fetch(i + kTok);
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
                 den = fmaf(f, zv[j], den);
             }
         float r = 1.f, t = p.keys ? -1.f : 0.f;
+        bool none = false;
         if (!p.keys) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -330,17 +332,18 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const GradParams p) {
                 den += __shfl_xor_sync(~0u, den, o);
             }
             if (p.norm) {
-                r = den == 0.f ? 0.f : 1.f / den;
+                none = den == 0.f;
+                r = none ? 0.f : 1.f / den;
                 t = dot * r;
             }
-            if (lane == 0) p.rt[bh * p.L + n] = make_float2(r, t);
+            if (lane == 0) p.rt[bh * p.L + n] = none ? no_row() : make_float2(r, t);
         }
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
             const int a = lane + 32 * j;
             if (a >= p.d) continue;
             const float g = r * fmaf(-t, zv[j], acc[m][j]) * slope_of(xv[m][j], p.phi);
-            dx[n * p.sdx.n + a] = n < len ? g : 0.f;
+            dx[n * p.sdx.n + a] = n < len && !none ? g : 0.f;
         }
     }
 }

@@ -2,6 +2,8 @@
 // la_backward_cross, la_decode_step_cross in include/linattn.h).
 #pragma once
 
+#include <cmath>
+
 #include "la_internal.h"
 
 namespace la {
@@ -46,6 +48,10 @@ cudaError_t tc_backward(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, cons
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int M) {
     return lengths ? min(max(lengths[b], 0), M) : M;
 }
+// r and t of a row whose denominator is 0, which adds nothing to dS and dz whatever its dy
+// is: t is not infinite where r = 0 is 1 / den.
+__device__ __forceinline__ float2 no_row() { return make_float2(0.f, INFINITY); }
+__device__ __forceinline__ bool is_none(float2 rt) { return rt.x == 0.f && rt.y == INFINITY; }
 #endif
 
 // ---- The parts of a call without those tiles: fp32 in la_cross.cu, bf16 in
@@ -55,7 +61,7 @@ __device__ __forceinline__ int tokens_of(const int *lengths, int b, int M) {
 struct SumParams {
     const void *x, *y;  // rows of features (phi is taken) and of values
     la_strides sx, sy;
-    const float2 *rt;    // backward: r and t of each row of x, [B][Hk][group][L]
+    const float2 *rt;    // backward: r and t of each row of x, [B][Hk][group][L], or no_row()
     const int *lengths;  // forward, or NULL
     int Hk, group, L, d, phi, segs;
     long long per, heads;

@@ -182,15 +182,19 @@ __global__ void __launch_bounds__(2 * kC, kC == 256 ? 1 : 2) half_sum_kernel(con
     int steps = 0;
     for (long long i = i0; i < end; i += kTok) {
         __syncthreads();
+        bool none = false;
 #pragma unroll
         for (int k = 0; k < kX; ++k) {
             const int row = rx + k * kStepX;
+            const bool gone = is_none(rt[k]);
+            const float u = gone ? 0.f : -rt[k].y;
+            none |= gone;
             float e[4];
             open4(x[k], e);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 e[j] = j < nx ? rt[k].x * phi_fast(e[j], p.phi) : 0.f;
-                zacc[j] = fmaf(e[j], -rt[k].y, zacc[j]);
+                zacc[j] = fmaf(e[j], u, zacc[j]);
             }
             const uint2 high = shut4(e);
             *reinterpret_cast<uint2 *>(&Ah[row][fx]) = high;
@@ -198,7 +202,14 @@ __global__ void __launch_bounds__(2 * kC, kC == 256 ? 1 : 2) half_sum_kernel(con
         }
 #pragma unroll
         for (int k = 0; k < kY; ++k) *reinterpret_cast<uint2 *>(&Y[ry + k * kStepY][fy]) = y[k];
-        __syncthreads();
+        if (__syncthreads_or(none)) {  // rows of 0 times what may not be finite
+#pragma unroll
+            for (int k = 0; k < kX; ++k)
+                if (is_none(rt[k]))
+                    for (int c = fx; c < kC; c += kA)
+                        *reinterpret_cast<uint2 *>(&Y[rx + k * kStepX][c]) = make_uint2(0, 0);
+            __syncthreads();
+        }
         if (i + kTok < end) fetch(i + kTok);
 #pragma unroll
         for (int ks = 0; ks < kTok; ks += 16) {
@@ -504,23 +515,26 @@ half_grad_kernel(const GradParams p, int wide, int wide_s, int words) {
             const int row = wr + 16 * m + 8 * i + (lane >> 2), n = n0 + row;
             if (n >= p.L) continue;
             float r = 1.f, t = p.keys ? -1.f : 0.f;
+            bool none = false;
             if (!p.keys) {
                 float dot = 0.f, den = 0.f;
 #pragma unroll
                 for (int q = 0; q < kC / 64; ++q)
                     dot += sm.red[q][row].x, den += sm.red[q][row].y;
                 if (p.norm) {
-                    r = den == 0.f ? 0.f : 1.f / den;
+                    none = den == 0.f;
+                    r = none ? 0.f : 1.f / den;
                     t = dot * r;
                 }
-                if (wa == 0 && (lane & 3) == 0) p.rt[bh * p.L + n] = make_float2(r, t);
+                if (wa == 0 && (lane & 3) == 0)
+                    p.rt[bh * p.L + n] = none ? no_row() : make_float2(r, t);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int a = wa + 8 * j + (lane & 3) * 2;
                 if (a >= p.d) continue;
                 float g[2] = {};
-                if (n < len) {
+                if (n < len && !none) {
                     const unsigned u = pair_of(x + n * p.sx.n, a);
                     const float2 za = sm.z[a / 2];
 #pragma unroll

@@ -719,13 +719,15 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
             tc_fence_after();
             const uint32_t o = me.lane_base + (j & 1) * 160;
             float inv = 1.f;
+            bool none = false;
             if (p.norm) {
                 uint32_t d0 = tmem_ld1(o + DK), d1 = tmem_ld1(o + DK + 1);
                 tmem_wait_ld();
                 reg_fence(d0);
                 reg_fence(d1);
                 const float den = u2f(d0) + u2f(d1);
-                inv = den == 0.f ? 0.f : 1.f / den;
+                none = den == 0.f;
+                inv = none ? 0.f : 1.f / den;
             }
 #pragma unroll
             for (int h = 0; h < DK / 64; ++h) {
@@ -735,6 +737,9 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
                     tc_fence_before();
                     arrive_warp(&sm.o_empty[j & 1]);
                 }
+                if (none)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float e[8];
@@ -1060,8 +1065,18 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             if (p.norm) {
                 r = den == 0.f ? 0.f : 1.f / den;
                 t = dot * r;
-                // of an unused row r is 0, and so is what it adds
                 t_all = t + u2f(m0) + u2f(m1);
+            }
+            if (p.norm && den == 0.f) {
+                // the row's gradient is 0 and it adds nothing, whatever S and its dY are (G
+                // has been formed of that)
+                t = t_all = 0.f;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) v[i] = 0;
+#pragma unroll
+                for (int i = 0; i < kCols; i += 8)
+                    *reinterpret_cast<uint4 *>(qt + L::TILE + tile_at(128, me.row, f0 + i)) =
+                        make_uint4(0, 0, 0, 0);
             }
             uint8_t *ot = smem + L::OFF_OUT;
 #pragma unroll

@@ -152,3 +152,34 @@ def test_an_infinite_key_with_the_normaliser(dtype, d, pad):
     assert torch.equal(but(S, *row), but(want[1], *row)) and torch.equal(but(z, *row), but(want[2], *row))
     assert bool(out[1, 2:].isnan().all())  # inf / inf
     assert torch.equal(but(out, 1, slice(2, 4)), but(want[0], 1, slice(2, 4)))
+
+
+@pytest.mark.parametrize("bad", [INF, NAN])
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_a_denominator_of_zero_gives_zeros_whatever_the_rest_is(dtype, d, pad, bad):
+    # a query of zeros has phi = 0 with the identity, and a sequence without keys has z = 0
+    q, dout, k, v = inputs(dtype, d, pad, shift=0.5)
+    lens, at, form = ints(LENGTHS), (1, 2, 33), {"feature_map": "identity", "normalise": True}
+    q[at] = 0
+    dout[at] = 0
+    out, S, z = la.forward_cross(q, k, v, lens, **form)
+    assert not bool(out[at].any()) and not bool(out[2].any())
+    want = la.backward_cross(dout, q, k, v, S, z, lens, **form)
+    dout[at] = bad
+    dout[2, :, 5] = bad
+    got = la.backward_cross(dout, q, k, v, S, z, lens, **form)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert not bool(got[0][at].any()) and not bool(got[0][2].any())
+    # the state not finite: the row's outputs and gradients are still zeros
+    v[1, 1, 40, 3] = bad
+    out, S, z = la.forward_cross(q, k, v, lens, **form)
+    assert not bool(S[1, 1, :, 3].isfinite().any())
+    assert not bool(out[at].ne(0).any())
+    for n in (1, 9, 40):
+        some = la.decode_step_cross(S, z, q[:, :, 33 - n // 2:33 - n // 2 + n], **form)
+        assert not bool(some[1, 2, n // 2].ne(0).any())
+    dq, dk, dv = la.backward_cross(dout, q, k, v, S, z, lens, **form)
+    assert not bool(dq[at].ne(0).any())
+    padding_is_zero(dk, dv)
+    la.check_device_status()
