@@ -158,19 +158,19 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
                 if (h + i * step >= H) continue;
                 // values, and features beyond the rotated ones, pass bit for bit
                 if (rotate && any) {
-                    float e[2 * V], keep_e[2 * V];
+                    float e[2 * V];
                     widen(&x[i][0], e);
                     if (second) widen(&x[i][1], e + V);
-                    if (!all)
-#pragma unroll
-                        for (int j = 0; j < 2 * V; ++j) keep_e[j] = e[j];
                     turn.apply(e);
-                    if (!all)  // neighbouring pairs of which some pass
+                    Pack<T, V> y[2];
+                    narrow<T, V>(y[0].v, e);
+                    narrow<T, V>(y[1].v, e + V);
+                    if (kInter && !all)  // neighbouring pairs of which some pass
 #pragma unroll
                         for (int j = 0; j < 2 * V; ++j)
-                            if (unit * V + (kInter ? j / 2 : j % V) >= p.half) e[j] = keep_e[j];
-                    narrow<T, V>(dst + at[0], e);
-                    if (second) narrow<T, V>(dst + at[1], e + V);
+                            if (unit * V + j / 2 >= p.half) y[j / V].v[j % V] = x[i][j / V].v[j % V];
+                    *reinterpret_cast<Pack<T, V> *>(dst + at[0]) = y[0];
+                    if (second) *reinterpret_cast<Pack<T, V> *>(dst + at[1]) = y[1];
                 } else {
                     *reinterpret_cast<Pack<T, V> *>(dst + at[0]) = x[i][0];
                     if (second) *reinterpret_cast<Pack<T, V> *>(dst + at[1]) = x[i][1];
