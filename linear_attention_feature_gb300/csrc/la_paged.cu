@@ -60,14 +60,23 @@ struct Params {
 // its zeros get written.
 struct Span {
     int before, lo, hi, first, tiles;
+    int reach;  // query t looks at keys above before + t - reach
 };
 
 template <int kTile>
 __device__ __forceinline__ Span span_of(const Params &p, int b) {
     Span s;
-    s.before = min(p.lengths[b], kMostTokens);
+    // Beyond all that a table can hold, queries look at its last keys from nearer by: the
+    // window is as much shorter.
+    const int length = p.lengths[b];
+    s.before = min(length, kMostTokens);
     s.hi = s.before < 0 ? 0 : min(s.before + p.T, p.max_pages * p.page_size);
-    s.lo = p.window > 0 ? min(max(s.before + 1 - p.window, 0), s.hi) : 0;
+    // the key before those of the first query; -kMostNew: none is before any query's
+    const int low = p.window > 0 ? (int)min(max((long long)length - p.window, -(long long)kMostNew),
+                                            (long long)kMostTokens)
+                                 : -kMostNew;
+    s.lo = min(max(low + 1, 0), s.hi);
+    s.reach = s.before - low;
     s.first = s.lo / kTile;
     s.tiles = max(1, (s.hi + kTile - 1) / kTile - s.first);
     return s;
@@ -75,7 +84,7 @@ __device__ __forceinline__ Span span_of(const Params &p, int b) {
 
 // Whether all queries of the call look at all of n keys from key0 on.
 __device__ __forceinline__ bool all_see(const Params &p, const Span &s, int key0, int n) {
-    return key0 + n - 1 <= s.before && (p.window == 0 || key0 > s.before + p.T - 1 - p.window);
+    return key0 + n - 1 <= s.before && key0 > s.before + p.T - 1 - s.reach;
 }
 
 // A place in the list of tiles.
@@ -508,8 +517,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                     for (int e = 0; e < 4; ++e) {
                         const int i = j * 8 + (lane & 3) * 2 + (e & 1), key = key0 + i;
                         const int end = last[e >> 1];
-                        if (!(mask >> i & 1) || key > end ||
-                            (p.window > 0 && key <= end - p.window))
+                        if (!(mask >> i & 1) || key > end || key <= end - c.s.reach)
                             s[j][e] = -INFINITY;
                     }
                 if (kUnit == 0 && mask != 0xffffu) {
@@ -794,8 +802,7 @@ paged_full_kernel(const __grid_constant__ Params p) {
 #pragma unroll
                 for (int w = kKeys; w < 32; w <<= 1) s[r] += __shfl_xor_sync(~0u, s[r], w);
                 s[r] *= p.scale2;
-                if (!(mask >> key_in & 1) || key > last[r] ||
-                    (p.window > 0 && key <= last[r] - p.window))
+                if (!(mask >> key_in & 1) || key > last[r] || key <= last[r] - c.s.reach)
                     s[r] = -INFINITY;
                 top[r] = s[r];
 #pragma unroll
