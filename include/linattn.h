@@ -623,7 +623,7 @@ size_t la_decode_step_paged_workspace_bytes(int Hq, int Hk, int T, int d,
  *              and M above M), or NULL: M.
  *   strides    4 strides, of q, k, v, out, or NULL: contiguous.
  *   B, Hq, Hk, N, M >= 0, Hq a multiple of Hk (query head h reads the state of
- *              head h / (Hq / Hk)), d in 1..LA_MAX_D.
+ *              head h / (Hq / Hk)), d in 1..LA_MAX_D; N, M <= 2^31 - 256.
  *   variant    as la_forward_variant.
  *   workspace  device buffer, 16-byte aligned, of la_cross_workspace_bytes(...,
  *              0) bytes, not used by anything else until `stream` has passed

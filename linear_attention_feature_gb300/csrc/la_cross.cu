@@ -604,10 +604,10 @@ cudaError_t backward(const Shape &sh, const Plan &pl, Rows dout, Rows q, Rows k,
 
 template <typename T, int V>
 cudaError_t launch_step(const StepParams &p, long long states, cudaStream_t s) {
-    const int rows = p.G * p.N;
+    const long long rows = (long long)p.G * p.N;
     auto go = [&](auto kern, int per) {
         const long long blocks = states * ((rows + per - 1) / per);
-        if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        if (blocks > 0x7fffffff || rows > 0x7fffffff - 8) return cudaErrorInvalidConfiguration;
         kern<<<(unsigned)blocks, kThreads, 0, s>>>(p);
         return counted(cudaSuccess);
     };
@@ -655,8 +655,10 @@ la_status shape_of(const char *who, Shape &sh, const int *lengths, int B, int Hq
                     (variant->normalise != 0 && variant->normalise != 1)))
         return layer_fail(LA_ERR_INVALID_ARG, who, "unknown variant");
     if ((uintptr_t)lengths % 4) return layer_fail(LA_ERR_INVALID_ARG, who, "unaligned lengths");
+    // (the last tile's rows are counted in 32 bits, too, some of them behind the tokens)
+    constexpr int kMostTokens = 0x7fffffff - 255;
     if ((double)B * std::max(Hq, Hk) * ((double)std::max(N, M) + 1) > 1e10 ||
-        (double)B * Hk * 64 > 2147483647.0)
+        (double)B * Hk * 64 > 2147483647.0 || std::max(N, M) > kMostTokens)
         return layer_fail(LA_ERR_UNSUPPORTED, who, "problem too large");
     sh = {B, Hq, Hk, N, M, d, !variant || variant->feature_map == LA_PHI_ELU1,
           variant ? variant->normalise : 1, lengths};
