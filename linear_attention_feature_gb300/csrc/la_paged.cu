@@ -1069,7 +1069,7 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
     const long long rows = (long long)(Hq / Hk) * T;
     p.row_tile = row_tile_of(rows, dtype);
     const long long row_tiles = (rows + p.row_tile - 1) / p.row_tile;
-    if (T > kMostNew || rows > 0x7fffffff)
+    if (T > kMostNew || rows > 0x7fffffff || Hk * row_tiles > 0x7fffffff)
         return layer_fail(LA_ERR_UNSUPPORTED, who, "too many queries");
     p.row_tiles = (int)row_tiles;
     p.k = cache->pages ? cache->k : q;  // without pages nothing is read

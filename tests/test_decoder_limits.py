@@ -43,3 +43,18 @@ def test_the_most_tokens_are_not_refused(lib):
 def test_more_tokens_of_one_state_than_a_count(lib, dtype, N):
     Hq = (1 << 31) // N + 1
     assert lib.la_decode_step_cross(*P[:4], None, 1, Hq, 1, N, 1, None, dtype, None) == UNSUPPORTED
+
+
+def test_more_tiles_of_queries_than_a_count(lib):
+    class Cache(ctypes.Structure):
+        _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_longlong * 3),
+                    ("vs", ctypes.c_longlong * 3), ("table", ctypes.c_void_p),
+                    ("table_stride", ctypes.c_longlong), ("lengths", ctypes.c_void_p),
+                    ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+    Hk, T = 1 << 11, 1 << 20
+    c = Cache(P[0], P[1], (Hk, 1, 1), (Hk, 1, 1), P[2], 1, P[3], 1, 1, 1)
+    # 2^24 queries of each of 2048 heads, 16 a tile: 2^31 tiles of a sequence
+    assert lib.la_decode_step_paged(P[4], P[5], ctypes.byref(c), None, 1.0, 0, 1, 16 * Hk, Hk, T, 1, 1,
+                                    P[8], 1 << 40, None) == UNSUPPORTED
+    assert "too many" in lib.la_last_error().decode()
