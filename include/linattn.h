@@ -551,7 +551,8 @@ typedef struct {
  *   rope       the rotation, by p + offset (rope->positions must be NULL), or
  *              NULL for none.  Values, and features from rotary_dim on, pass
  *              bit for bit.
- *   B, Hq, Hk, T >= 0 (Hq == 0 leaves the queries out), d in 1..LA_MAX_D.
+ *   B, Hq, Hk, T >= 0 (Hq == 0 leaves the queries out), Hq + 2 Hk < 2^31 - 4097,
+ *              d in 1..LA_MAX_D.
  * A token whose place has no page (past the table, a table entry that is no
  * page) or whose sequence is not in use is not stored.  Two sequences that
  * append to one page at one slot leave either's token there.  Angles are exact

@@ -252,6 +252,9 @@ la_status la_append_cache(const void *q, const void *k, const void *v, void *q_o
     if (Hq < 0 || T < 0) return layer_fail(LA_ERR_INVALID_ARG, who, "negative Hq or T");
     la_status st = check_cache(who, cache, B, Hk, d, dtype);
     if (st != LA_OK) return st;
+    // a thread's heads are counted in 32 bits, up to kRows kThreads behind the last one
+    if (Hq + 2LL * Hk >= 0x7fffffff - 4 * kRows * kThreads)
+        return layer_fail(LA_ERR_UNSUPPORTED, who, "too many heads");
     Params p{};
     if (rope && rope->rotary_dim != 0) {
         const int R = rope->rotary_dim;

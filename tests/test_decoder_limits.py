@@ -58,3 +58,18 @@ def test_more_tiles_of_queries_than_a_count(lib):
     assert lib.la_decode_step_paged(P[4], P[5], ctypes.byref(c), None, 1.0, 0, 1, 16 * Hk, Hk, T, 1, 1,
                                     P[8], 1 << 40, None) == UNSUPPORTED
     assert "too many" in lib.la_last_error().decode()
+
+
+@pytest.mark.parametrize("Hq, Hk", [((1 << 31) - 1, 1), (0, 1 << 30), ((1 << 31) - 4096, 0)])
+def test_more_heads_than_a_count(lib, Hq, Hk):
+    # (a thread takes its token's heads in strides, and stops behind the last of them)
+    class Cache(ctypes.Structure):
+        _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_longlong * 3),
+                    ("vs", ctypes.c_longlong * 3), ("table", ctypes.c_void_p),
+                    ("table_stride", ctypes.c_longlong), ("lengths", ctypes.c_void_p),
+                    ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+    c = Cache(P[0], P[1], (Hk, 1, 1), (Hk, 1, 1), P[2], 1, P[3], 1, 1, 1)
+    assert lib.la_append_cache(P[4], P[5], P[6], P[7], ctypes.byref(c), None, None, None, 1, Hq, Hk, 1,
+                               1, 1, None) == UNSUPPORTED
+    assert "too many heads" in lib.la_last_error().decode()
