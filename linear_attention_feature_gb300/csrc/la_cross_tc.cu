@@ -23,7 +23,8 @@
 //   qgrad   r (S dy - t z) is the same for S' = S - z m^T, any m.  With m = S^T z / z.z,
 //           the mean of the values as z weighs it, S' has none of the large common part
 //           that cancels, and one bf16 number is enough.  psi = r phi(q) as one; the
-//           sums of psi and of psi t then go by the same rounded psi, t as two.
+//           sums of psi and of psi t then go by the same rounded psi, t as two.  A
+//           product's sum ends after 2048 tokens; the sums are added in fp32.
 //   kgrad   dS as two for dphi(K), where dS v and dz cancel for values with a mean far
 //           from 0; as one for dV.
 //
@@ -293,9 +294,11 @@ struct Sums {
         reg_fence(v1);
         z = kZ == 2 ? u2f(v0) + u2f(v1) : u2f(v0);
     }
-    // To the state itself, or to part `slot` (>= 0) of this block.
+    // To the state itself, or to part `slot` (>= 0) of this block; `more`: added to what this
+    // thread wrote there before (nobody else adds to it, so the order is fixed).
     static __device__ __forceinline__ void write(const Params &p, const Mine &me, long long state,
-                                                 int slot, const uint32_t (&v)[kCols], float z) {
+                                                 int slot, const uint32_t (&v)[kCols], float z,
+                                                 bool more = false) {
         const int a = me.row, c0 = me.part * kCols;
         if (a >= p.d) return;
         const long long dd = (long long)p.d * p.d;
@@ -310,10 +313,18 @@ struct Sums {
         S += (long long)a * p.d + c0;
 #pragma unroll
         for (int e = 0; e < kCols; e += 4)
-            if (c0 + e < p.d)
-                *reinterpret_cast<float4 *>(S + e) =
-                    make_float4(u2f(v[e]), u2f(v[e + 1]), u2f(v[e + 2]), u2f(v[e + 3]));
-        if (me.part == 0) z_to[a] = p.zsign * z;
+            if (c0 + e < p.d) {
+                const float4 u = make_float4(u2f(v[e]), u2f(v[e + 1]), u2f(v[e + 2]), u2f(v[e + 3]));
+                if (more)
+                    atomicAdd(reinterpret_cast<float4 *>(S + e), u);
+                else
+                    *reinterpret_cast<float4 *>(S + e) = u;
+            }
+        if (me.part > 0) return;
+        if (more)
+            atomicAdd(z_to + a, p.zsign * z);
+        else
+            z_to[a] = p.zsign * z;
     }
 };
 
@@ -772,7 +783,8 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 // ------------------------------------------------------------------ qgrad
 //
 // Two products depend on one another for each tile (psi needs the first's t), and the
-// second's sums stay in TMEM over a whole state.  4 x 8 x 4096 x 128 (101 MB in and out):
+// second's sums stay in TMEM over up to 16 tiles of a state: then they are added to those
+// before in memory, by reductions that nothing waits for.  4 x 8 x 4096 x 128 (101 MB in and out):
 // 41 us, 2.4 TB/s: 7 tiles per block, each at the latency of fetch, product, psi, product
 // and store.  Two groups of computing warps 48 us (a state's sums then meet at its end);
 // dq straight from registers 51 us.
@@ -782,6 +794,11 @@ struct QLayout {
     static constexpr int KB = DK / 64, TILE = KB * 16384, STAGE = 2 * TILE;
     static constexpr int STAGES = DK == 128 ? 2 : 4;
     static constexpr int SROWS = DK + 16, SATOM = SROWS * 128;  // rows of S', then m
+    // Tiles of a chain of sums.  2048 tokens are 128 products, of which the cut takes 2^-16 at
+    // most, as much as dS loses in two bf16 numbers; over a million tokens without an end dk
+    // was off by 7 % where values have a mean of 64 deviations.  20 x (32 on 8) x 16384 to
+    // 2048 x 64 backward: 949 us without an end, 975 us with 16; 4 take 84 us more.
+    static constexpr int GROUP = 16;
     static constexpr int OFF_T = STAGES * STAGE, OFF_S = OFF_T + 16384;
     static constexpr int OFF_OUT = (OFF_S + KB * SATOM + 1023) / 1024 * 1024;
     static constexpr int OFF_SMALL = OFF_OUT + TILE;
@@ -872,12 +889,13 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             // G of tile i and the sums of tile j <= i, whichever has its operands: a tile
             // that is still under way holds back no sums, which free a place for the next
             auto v = w;
-            int i = 0, j = 0, states = 0, ended = 0;
+            int i = 0, j = 0, states = 0, ended = 0, in = 0;
             long long deadline = 0;
             for (int polls = 0; j < steps;) {
                 if (j < i) {
                     const int st = j % L::STAGES;
-                    const bool first = j == 0 || v.tile == 0, last = v.last() || j == steps - 1;
+                    const bool first = in == 0;
+                    const bool last = v.last() || j == steps - 1 || in == L::GROUP - 1;
                     if (mbar_test_wait(&sm.psi[st], (j / L::STAGES) & 1) &&
                         (!first || mbar_test_wait(&sm.ds_empty, (ended & 1) ^ 1))) {
                         tc_fence_after();
@@ -894,9 +912,11 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                         }
                         mma_commit(&sm.empty[st]);
                         mma_commit(&sm.t_free);
+                        ++in;
                         if (last) {
                             mma_commit(&sm.ds_full);
                             ++ended;
+                            in = 0;
                         }
                         ++j;
                         v.next();
@@ -944,7 +964,11 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         constexpr int kCols = DK / kParts;
         const int f0 = me.part * kCols;  // this thread's features of its row
         int first_tile = w.tile, drained = 0;
-        auto drain = [&](long long state, int slot) {  // a state's sums are complete
+        // the chain of sums that has ended, if >= 0: its state, where it goes to, and whether
+        // one before it is there
+        int old_state = -1, old_slot = 0;
+        bool old_more = false;
+        auto drain = [&]() {
             wait_bar(&sm.ds_full, drained & 1, cx);
             ++drained;
             tc_fence_after();
@@ -954,10 +978,9 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             Sum::get(me, kDs, v, z);
             tc_fence_before();
             arrive_warp(&sm.ds_empty);
-            Sum::write(p, me, state, slot, v, z);
+            Sum::write(p, me, old_state, old_slot, v, z, old_more);
+            old_state = -1;
         };
-        long long old_state = -1;
-        int old_slot = 0;
         for (int j = 0; j < steps; ++j, w.next()) {
             const int st = j % L::STAGES;
             const long long state = (long long)w.b * p.Hk + w.seg;
@@ -1018,7 +1041,6 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 }
                 fence_async_shared();
                 arrive_warp(&sm.s_ready);
-                if (old_state >= 0) drain(old_state, old_slot);
                 first_tile = w.tile;
             }
             wait_bar(&sm.full[st], (j / L::STAGES) & 1, cx);
@@ -1036,6 +1058,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                     den = fmaf(f[i + q], sm.z[f0 + i + q], den);
                 }
             }
+            if (old_state >= 0) drain();  // of the tiles before: phi has given it time
             wait_bar(&sm.g_full[j & 1], (j >> 1) & 1, cx);
             tc_fence_after();
             const uint32_t gb = me.lane_base + kTmG + (j & 1) * kTmStep;
@@ -1063,20 +1086,9 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             }
             float r = 1.f, t = 0.f, t_all = 0.f;
             if (p.norm) {
-                r = den == 0.f ? 0.f : 1.f / den;
+                r = 1.f / den;
                 t = dot * r;
                 t_all = t + u2f(m0) + u2f(m1);
-            }
-            if (p.norm && den == 0.f) {
-                // the row's gradient is 0 and it adds nothing, whatever S and its dY are (G
-                // has been formed of that)
-                t = t_all = 0.f;
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) v[i] = 0;
-#pragma unroll
-                for (int i = 0; i < kCols; i += 8)
-                    *reinterpret_cast<uint4 *>(qt + L::TILE + tile_at(128, me.row, f0 + i)) =
-                        make_uint4(0, 0, 0, 0);
             }
             uint8_t *ot = smem + L::OFF_OUT;
 #pragma unroll
@@ -1092,24 +1104,38 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                 *reinterpret_cast<uint4 *>(ot + at) = shut8(g);
                 *reinterpret_cast<uint4 *>(qt + at) = shut8(s);
             }
+            if (p.norm && den == 0.f) {
+                // the row's gradient is 0 and it adds nothing, whatever S and its dY are (G
+                // has been formed of that); rare, and apart from the way of the others
+                t_all = 0.f;
+                for (int i = 0; i < kCols; i += 8) {
+                    const uint32_t at = tile_at(128, me.row, f0 + i);
+                    *reinterpret_cast<uint4 *>(ot + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(qt + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(qt + L::TILE + at) = make_uint4(0, 0, 0, 0);
+                }
+            }
             if (me.part == 0)
                 *reinterpret_cast<uint32_t *>(smem + L::OFF_T + sw128_offset(me.row, 0)) =
                     split(t_all);
             fence_async_shared();
             arrive_warp(&sm.psi[st]);
             if (lane == 0) mbar_arrive(&sm.out_full);
-            if (w.last() || j == steps - 1) {
-                const bool began = first_tile > 0, ends = w.last();
-                old_state = state;
+            const bool whole = w.last() || j == steps - 1;
+            const int at = w.tile - first_tile;
+            if (whole || at % L::GROUP == L::GROUP - 1) {
+                const bool began = first_tile > 0, ends = w.tiles - w.tile <= steps - j;
+                old_state = (int)state;
                 old_slot = began ? 0 : ends ? -1 : 1;
-                if (began && me.et == 0) {
+                old_more = at >= L::GROUP;
+                if (whole && began && me.et == 0) {
                     const long long s0 = x.x0 + j - w.tile;
                     p.info[blockIdx.x] =
                         make_int4((int)state, x.of(s0), x.of(s0 + w.tiles - 1), 0);
                 }
             }
         }
-        if (old_state >= 0) drain(old_state, old_slot);
+        if (old_state >= 0) drain();
     } else if (lane == 0) {
         for (int j = 0; j < steps; ++j, w.next()) {
             const int g = w.tile / tiles;
