@@ -768,6 +768,11 @@ unsigned long long la_kernel_launch_count(void);
  * as well, whichever comes first: there, the first block of every thread-block
  * cluster never fetches its rows of round `hold_segment` (0 or 1, of the
  * first rounds; -1: fetches all).
+ * So do la_decode_step_paged over pages of whole 16-key tiles (each warp never
+ * fetches tile `hold_segment` of its own), and, where they run on the tensor
+ * cores' tiles, la_forward_cross (its states), la_decode_step_cross and
+ * la_backward_cross (both kernels): each block fetches nothing from its tile
+ * `hold_segment` on.
  *
  * la_debug_fail_next_allocs -- the next `n` stream-ordered workspace
  * allocations of the forward kernels (tensor-core launches given no

@@ -60,7 +60,6 @@ constexpr int kWarpsC = kC / 32, kParts = kWarpsC / 4;  // warps that share rows
 constexpr int kG = kC / 2, kWarpsG = kG / 32;
 constexpr int BAR_C = 1;
 constexpr uint32_t kTmemCols = 512;
-constexpr long long kTimeout = 1LL << 32;
 
 struct Params {
     int B, Hk, G, L, d, phi, norm;  // L: tokens of a head
@@ -72,6 +71,8 @@ struct Params {
                                     // continues (-1: none), first and last block of it
     float zsign;
     int *status;
+    long long timeout;  // clock cycles per wait
+    int hold;           // test hook: a block fetches no tile from this one of its own on, or -1
 };
 
 __device__ __forceinline__ int tokens_of(const Params &p, int b) {
@@ -111,6 +112,14 @@ struct Walk {
 template <typename F>
 __device__ __forceinline__ Walk<F> walk(F f, const Params &p, const Piece &x) {
     return Walk<F>(f, p, x);
+}
+
+// Whether a block's tile j may be fetched into a stage, once `empty` says that it is free.
+// Where a wait has given up that may be untrue: it passes, and with it what follows, while
+// the stage's copy is under way, whose barrier must not be armed a second time.
+__device__ __forceinline__ bool may_fetch(const Params &p, uint64_t *empty, uint32_t parity, int j,
+                                          const Ctx &cx) {
+    return j != p.hold && wait_bar(empty, parity, cx) && !*cx.abort;
 }
 
 // ------------------------------------------------------------------ TMA, 4-D maps
@@ -409,7 +418,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         mbar_init(&sm.fin, 1);
     });
-    const Ctx cx{&sm.abort, p.status, kTimeout};
+    const Ctx cx{&sm.abort, p.status, p.timeout};
     auto count = [](int len) { return max(1, (len + L::TOK - 1) / L::TOK); };
     const Piece x = find_piece<kThreads>(
         p.B, p.Hk, 4, [&](int b) { return count(tokens_of(p, b)); }, sm.plan);
@@ -424,7 +433,7 @@ state_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             int j = 0;
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES;
-                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                if (!may_fetch(p, &sm.empty[st], ((j / L::STAGES) & 1) ^ 1, j, cx)) break;
                 uint8_t *at = smem + st * L::STAGE;
                 mbar_arrive_expect_tx(&sm.full[st], 2 * L::TILE);
                 for (int a = 0; a < L::KB; ++a) {
@@ -635,7 +644,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         }
         mbar_init(&sm.fin, 1);
     });
-    const Ctx cx{&sm.abort, p.status, kTimeout};
+    const Ctx cx{&sm.abort, p.status, p.timeout};
     auto count = [&](int) { return p.G * tiles; };
     const Piece x = even_piece(p.B, p.Hk, 1, p.G * tiles);
     const int steps = (int)(x.x1 - x.x0);
@@ -648,7 +657,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
             int j = 0;
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES, g = w.tile / tiles;
-                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                if (!may_fetch(p, &sm.empty[st], ((j / L::STAGES) & 1) ^ 1, j, cx)) break;
                 mbar_arrive_expect_tx(&sm.full[st], L::TILE);
                 for (int a = 0; a < L::KB; ++a)
                     load_tile(smem + st * L::TILE + a * 16384, &tq, &sm.full[st], 64 * a,
@@ -849,7 +858,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         mbar_init(&sm.out_empty, 1);
         mbar_init(&sm.fin, 1);
     });
-    const Ctx cx{&sm.abort, p.status, kTimeout};
+    const Ctx cx{&sm.abort, p.status, p.timeout};
     auto count = [&](int) { return p.G * tiles; };
     const Piece x = even_piece(p.B, p.Hk, 2, p.G * tiles);
     const int steps = (int)(x.x1 - x.x0);
@@ -863,7 +872,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             int j = 0;
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES, g = w.tile / tiles;
-                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                if (!may_fetch(p, &sm.empty[st], ((j / L::STAGES) & 1) ^ 1, j, cx)) break;
                 // the first product needs dY alone: it comes first and is waited for apart
                 mbar_arrive_expect_tx(&sm.y_full[st], L::TILE);
                 mbar_arrive_expect_tx(&sm.full[st], L::TILE);
@@ -1206,7 +1215,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         mbar_init(&sm.fin, 1);
     });
-    const Ctx cx{&sm.abort, p.status, kTimeout};
+    const Ctx cx{&sm.abort, p.status, p.timeout};
     auto count = [](int len) { return (len + 127) / 128; };
     const Piece x = find_piece<kThreads>(
         p.B, p.Hk, 1, [&](int b) { return count(tokens_of(p, b)); }, sm.plan);
@@ -1220,7 +1229,7 @@ kgrad_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             int j = 0;
             for (; j < steps; ++j, w.next()) {
                 const int st = j % L::STAGES;
-                if (!wait_bar(&sm.empty[st], ((j / L::STAGES) & 1) ^ 1, cx)) break;
+                if (!may_fetch(p, &sm.empty[st], ((j / L::STAGES) & 1) ^ 1, j, cx)) break;
                 // phi needs the keys alone: they come first and are waited for apart
                 mbar_arrive_expect_tx(&sm.full[st], L::TILE);
                 mbar_arrive_expect_tx(&sm.v_full[st], L::TILE);
@@ -1474,7 +1483,14 @@ bool rows_fit(const Rows &r, int B, int H, int L) {
     return true;
 }
 
-Params params_of(const Shape &sh, int L, int *status) {
+// How long a call's kernels wait, and the test hook's hold.
+struct Limits {
+    long long timeout = 1LL << 32;
+    int hold = -1;
+    Limits() { tc_debug_take_timeout(&timeout, &hold); }
+};
+
+Params params_of(const Shape &sh, int L, const Limits &lim, int *status) {
     Params p{};
     p.B = sh.B;
     p.Hk = sh.Hk;
@@ -1485,6 +1501,8 @@ Params params_of(const Shape &sh, int L, int *status) {
     p.norm = sh.norm;
     p.zsign = 1.f;
     p.status = status;
+    p.timeout = lim.timeout;
+    p.hold = lim.hold;
     return p;
 }
 
@@ -1539,7 +1557,7 @@ cudaError_t state(const Shape &sh, Rows k, Rows v, float *S, float *z, char *ws,
     cudaError_t e = make_map(&tk, k, sh.B, sh.Hk, sh.M, sh.d, L::TOK);
     if (e == cudaSuccess) e = make_map(&tv, v, sh.B, sh.Hk, sh.M, sh.d, L::TOK);
     if (e != cudaSuccess) return e;
-    Params p = params_of(sh, sh.M, status);
+    Params p = params_of(sh, sh.M, Limits(), status);
     p.lengths = sh.lengths;
     p.So = S;
     p.zo = z;
@@ -1558,7 +1576,7 @@ cudaError_t read(const Shape &sh, Rows q, Rows out, const float *S, const float 
     cudaError_t e = make_map(&tq, q, sh.B, sh.Hq, sh.N, sh.d, 128);
     if (e == cudaSuccess) e = make_map(&to, out, sh.B, sh.Hq, sh.N, sh.d, 128);
     if (e != cudaSuccess) return e;
-    Params p = params_of(sh, sh.N, status);
+    Params p = params_of(sh, sh.N, Limits(), status);
     p.S = S;
     p.z = z;
     const int blocks = blocks_of(sh, (long long)sh.G() * ((sh.N + 127) / 128), sms);
@@ -1576,7 +1594,8 @@ cudaError_t back(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, const float
         e = i < 3 ? make_map(&m[i], *r[i], sh.B, sh.Hq, sh.N, sh.d, 128)
                   : make_map(&m[i], *r[i], sh.B, sh.Hk, sh.M, sh.d, 128);
     if (e != cudaSuccess) return e;
-    Params p = params_of(sh, sh.N, status);
+    const Limits lim;  // of both kernels
+    Params p = params_of(sh, sh.N, lim, status);
     float *dS = reinterpret_cast<float *>(ws);
     float *dz = reinterpret_cast<float *>(ws + up(sizeof(float) * (size_t)(sh.heads() * sh.state())));
     char *rest = reinterpret_cast<char *>(dz) + up(sizeof(float) * (size_t)(sh.heads() * sh.d));
@@ -1592,7 +1611,7 @@ cudaError_t back(const Shape &sh, Rows dout, Rows q, Rows k, Rows v, const float
                m[1], m[2], p);
     if (e == cudaSuccess) e = join(p, blocks, s);
     if (e != cudaSuccess) return e;
-    Params c = params_of(sh, sh.M, status);
+    Params c = params_of(sh, sh.M, lim, status);
     c.lengths = sh.lengths;
     c.S = dS;
     c.z = dz;

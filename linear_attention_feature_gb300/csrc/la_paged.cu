@@ -53,6 +53,8 @@ struct Params {
     float scale2;             // scale log2(e)
     int4 *info;               // of each block: see Plan
     float *part;              // [blocks][2][row_tile][d + 2]
+    long long timeout;        // clock cycles per wait
+    int hold;                 // test hook: warps fetch no tile from this one of their own on, or -1
 };
 
 // Where a sequence's keys lie: [lo, hi) in tiles of kTile from the one of lo on.  One
@@ -319,7 +321,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
     unsigned *masks = reinterpret_cast<unsigned *>(smem + L::kOffMask) + warp * L::kStages;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * L::kStages;
     int *abort = reinterpret_cast<int *>(smem + L::kOffPlan + (kWarps + 2) * 8);
-    const tcc::Ctx cx{abort, p.status, 1LL << 32};
+    const tcc::Ctx cx{abort, p.status, p.timeout};
     const int segs = p.Hk * p.row_tiles;
 
     if (kUnit != 0)  // features from d on
@@ -368,7 +370,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
                 // the tile's keys are in one page
                 const int first = max(f.s.lo - ahead.key, 0), n = min(f.s.hi - ahead.key, kKeys);
                 mask = ahead.page >= 0 && n > first ? (0xffffu >> (kKeys - n)) >> first << first : 0;
-                if (lane == 0) {
+                if (lane == 0 && steps - f_left != p.hold) {
                     if (mask == 0) {
                         tc::mbar_arrive(bars + f_stage);
                     } else {
@@ -468,6 +470,14 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         float m[2] = {-INFINITY, -INFINITY};
+        // A wait has run out: nothing more is fetched, since a barrier must not be armed again
+        // while its copy is under way, and what is under way lands.
+        auto give_up = [&](int it) {
+            if (f_left < 0) return;  // all that has been fetched is there
+            for (int i = steps - left + it; i < steps - f_left; ++i)
+                if (i != p.hold) tcc::settle_wait(bars + i % L::kStages, i / L::kStages & 1);
+            f_left = -1;
+        };
         // the last key of this lane's two queries
         int last[2];
 #pragma unroll
@@ -478,8 +488,8 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             fetch();
             if constexpr (kUnit != 0)
                 asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
-            else
-                tcc::wait_bar(bars + stage, parity, cx);
+            else if (!tcc::wait_bar(bars + stage, parity, cx))
+                give_up(it);
             __syncwarp();
             const unsigned st = tc::smem_u32(ring + stage * L::kStage);
             T *values = reinterpret_cast<T *>(ring + stage * L::kStage + L::kSide);
@@ -660,14 +670,7 @@ paged_half_kernel(const __grid_constant__ Params p, const __grid_constant__ CUte
             __syncwarp();
         }
     }
-    if constexpr (kUnit != 0) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (*abort) {  // a wait gave up: what is under way lands before the block ends
-        for (int i = 0, q = 0, ph = 0; i < steps; ++i) {
-            if (i + L::kStages >= steps) tcc::settle_wait(bars + q, ph);
-            if (++q == L::kStages) q = 0, ph ^= 1;
-        }
-    }
+    if constexpr (kUnit != 0) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ fp32
@@ -1155,6 +1158,9 @@ la_status la_decode_step_paged(const void *q, void *out, const la_cache *cache,
         }
         ws = own;
     }
+    p.timeout = 1LL << 32;
+    p.hold = -1;
+    if (tiles_fit) tc_debug_take_timeout(&p.timeout, &p.hold);
     p.info = static_cast<int4 *>(ws);
     p.part = reinterpret_cast<float *>(p.info + blocks);
     e = cudaFuncSetAttribute(c.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);

@@ -63,9 +63,10 @@ cudaError_t tc_workspace_alloc(void **ws, size_t bytes, cudaStream_t stream);
 
 // Test hooks, per calling thread, each consumed by the next launch that
 // reads it (set through la_debug_inject_timeout / la_debug_fail_next_allocs):
-// the next d = 128 causal launch or scan of the recurrence bounds every wait by
-// `wait_cycles`, and segment `hold_segment` never publishes the state it holds, or
-// round `hold_segment` is never fetched (-1: all are);
+// the next d = 128 causal launch, scan of the recurrence, paged attention or cross call by
+// tiles bounds every wait by `wait_cycles`, and segment `hold_segment` never publishes the
+// state it holds, or round or tile `hold_segment` is never fetched (-1: all are), see
+// linattn.h;
 // the next `n` workspace allocations fail.
 void tc_debug_set_timeout(long long wait_cycles, int hold_segment);
 bool tc_debug_take_timeout(long long *wait_cycles, int *hold_segment);
