@@ -22,8 +22,9 @@ def phi(x):
     return torch.where(x > 0, x + 1, torch.exp(x.clamp(max=0)))
 
 
-def rows(g, B, H, L, d, pad=0):
-    return torch.randn(B, H, L, d + pad, generator=g, device="cuda")[..., pad:]
+def rows(g, H, L, d, pad, scale=1.0, shift=0.0):
+    x = torch.randn(1, H, L, d + pad, generator=g, device="cuda").mul_(scale).add_(shift)
+    return x.bfloat16()[..., pad:]
 
 
 def gradients(q, k, v, dout, S, z):
@@ -58,8 +59,8 @@ def test_queries_gradient_where_values_have_a_mean(d, pad):
     g = torch.Generator(device="cuda")
     g.manual_seed(d)
     M, c = 2048, 8.0
-    q, k, v, dout = (rows(g, 1, H, L, d, pad) for H, L in ((2, 200), (1, M), (1, M), (2, 200)))
-    q, k, v, dout = (x.bfloat16() for x in (0.7 * q, 0.7 * k, v + c, dout))
+    q, k = rows(g, 2, 200, d, pad, 0.7), rows(g, 1, M, d, pad, 0.7)
+    v, dout = rows(g, 1, M, d, pad, shift=c), rows(g, 2, 200, d, pad)
     _, S, z = la.forward_cross(q, k, v)
     dq, _, _ = la.backward_cross(dout, q, k, v, S, z)
     assert off(dq, gradients(q, k, v, dout, S, z)[0]) <= 2.0 ** -16 * c * M ** 0.5 + 3 * 2.0 ** -8
@@ -74,8 +75,8 @@ def test_keys_gradient_where_values_have_a_mean(d, pad):
     g = torch.Generator(device="cuda")
     g.manual_seed(d)
     c = 64.0
-    q, k, v, dout = (rows(g, 1, H, L, d, pad) for H, L in ((2, 256), (1, 64), (1, 64), (2, 256)))
-    q, k, v, dout = (x.bfloat16() for x in (0.7 * q, 0.7 * k, v + c, 0.5 * dout + 1))
+    q, k = rows(g, 2, 256, d, pad, 0.7), rows(g, 1, 64, d, pad, 0.7)
+    v, dout = rows(g, 1, 64, d, pad, shift=c), rows(g, 2, 256, d, pad, 0.5, 1.0)
     _, S, z = la.forward_cross(q, k, v)
     _, dk, dv = la.backward_cross(dout, q, k, v, S, z)
     ref = gradients(q, k, v, dout, S, z)
