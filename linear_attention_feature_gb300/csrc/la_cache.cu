@@ -84,7 +84,7 @@ struct Turn {
 // under way at a time.
 //
 // Bound by memory: 8 x 8192 tokens (fewer in some sequences) of 32 + 8 + 8 heads of 128
-// bf16 values: 247 us, 6.0 TB/s.  (Two heads under way 272 us; three or four blocks per SM
+// bf16 values: 240 us, 6.2 TB/s.  (Two heads under way 272 us; three or four blocks per SM
 // spill: 275 to 293 us.  Angles found for three heads at a time instead of twelve: 367 us.)
 template <typename T, int V, bool kInter>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ Params p) {

@@ -11,7 +11,8 @@
 // token's is kept from the forward: S and z are all that the backward needs.
 //
 // This file has the argument checks, the fp32 kernels on CUDA cores, which take any head
-// size and stride and are bound by the fp32 units, and the single tokens' kernel.
+// size and stride and reach a third of what the fp32 units could (23 to 25 TFLOP/s on 8 x 8
+// x 2048 to 2048 x 128), and the single tokens' kernel.
 #include <cuda_bf16.h>
 
 #include <algorithm>

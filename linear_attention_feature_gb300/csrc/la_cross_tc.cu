@@ -32,8 +32,8 @@
 // take phi, empty TMEM and compute what lies between, warp 18 stores tiles (TMA).  The
 // computing warps set the pace: with 8 of them, and phi with a branch, the kernels were
 // bound by latency and instructions at a third of the memory's rate.  They do not fill a
-// pipe now (0.36 to 0.60 instructions issued per cycle, tensor cores 9 to 22 %, memory
-// 49 to 55 %): what is left is the way of a tile through fetch, phi, product and emptying,
+// pipe now (0.36 to 0.62 instructions issued per cycle, tensor cores 9 to 21 %, memory
+// 48 to 54 %): what is left is the way of a tile through fetch, phi, product and emptying,
 // of which two to four are under way in shared memory, and some 8 us of start and end.
 #include <cuda_bf16.h>
 
@@ -59,7 +59,7 @@ constexpr int kWarpsC = kC / 32, kParts = kWarpsC / 4;  // warps that share rows
 // one works while the other waits.
 constexpr int kG = kC / 2, kWarpsG = kG / 32;
 constexpr int BAR_C = 1;
-constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemCols = 512;  // all: one block per SM (d <= 64 would do with half)
 
 struct Params {
     int B, Hk, G, L, d, phi, norm;  // L: tokens of a head
@@ -369,8 +369,8 @@ struct Loaded {
 // ------------------------------------------------------------------ state
 //
 // phi(K) as high and low, high in K's place, low in a ring of its own; both times [V | 1]
-// into TMEM, DK rows a, DK + 16 columns.  4 x 8 x 16384 x 128 (ragged, 198 MB read): 52 us,
-// 3.8 TB/s; without phi and products it is 42 us.  Tiles of 64 tokens, since four stages of
+// into TMEM, DK rows a, DK + 16 columns.  4 x 8 x 16384 x 128 (ragged, 198 MB read): 53 us,
+// 3.7 TB/s; without phi and products it is 42 us.  Tiles of 64 tokens, since four stages of
 // them fit with d = 128 (32 tokens: 63 us).  Fetching tiles into L2 ahead, 59 us.
 
 template <int DK>
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const Params p) {
 //
 // 128 tokens x d of queries stay in their place as phi(q), then as the outputs; two groups
 // of computing warps take tiles in turn, so that one works while the other waits.
-// 4 x 32 x 4096 x 128 (134 MB in, 134 MB out): 52 us, 5.2 TB/s.
+// 4 x 32 x 4096 x 128 (134 MB in, 134 MB out): 50 us, 5.4 TB/s.
 
 template <int DK>
 struct ReadLayout {
@@ -794,7 +794,7 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 // Two products depend on one another for each tile (psi needs the first's t), and the
 // second's sums stay in TMEM over up to 16 tiles of a state: then they are added to those
 // before in memory, by reductions that nothing waits for.  4 x 8 x 4096 x 128 (101 MB in and out):
-// 41 us, 2.4 TB/s: 7 tiles per block, each at the latency of fetch, product, psi, product
+// 42 us, 2.4 TB/s: 7 tiles per block, each at the latency of fetch, product, psi, product
 // and store.  Two groups of computing warps 48 us (a state's sums then meet at its end);
 // dq straight from registers 51 us.
 
@@ -1166,7 +1166,7 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 //
 // dphi(K) goes into K's place and dV into V's, after the products that read them; two
 // groups of computing warps take tiles in turn.  4 x 8 x 16384 x 128 (ragged; 198 MB in,
-// 268 MB out with the padding's zeros): 92 us, 5.1 TB/s.  Both gradients straight from
+// 268 MB out with the padding's zeros): 94 us, 5.0 TB/s.  Both gradients straight from
 // registers 144 us; staged in halves with phi in place 136 us.
 
 template <int DK>
