@@ -995,7 +995,9 @@ qgrad_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             const long long state = (long long)w.b * p.Hk + w.seg;
             if (j == 0 || w.tile == 0) {
                 Loaded<DK> S;
-                const float z_mine = me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
+                // (without the normaliser z is no part of the formulas, whatever it is)
+                const float z_mine =
+                    p.norm && me.et < p.d ? __ldcg(p.z + state * p.d + me.et) : 0.f;
                 S.load(p.S + state * p.d * p.d, p.d, me.et);
                 sync_compute();  // all are through with the state before
                 if (me.et < 128) sm.z[me.et] = z_mine;

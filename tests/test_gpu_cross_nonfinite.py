@@ -183,3 +183,21 @@ def test_a_denominator_of_zero_gives_zeros_whatever_the_rest_is(dtype, d, pad, b
     assert not bool(dq[at].ne(0).any())
     padding_is_zero(dk, dv)
     la.check_device_status()
+
+
+@pytest.mark.parametrize("fmap", ["identity", "elu1"])
+@pytest.mark.parametrize("dtype, d, pad", PATHS)
+def test_without_the_normaliser_z_is_not_used(dtype, d, pad, fmap):
+    # its sum may overflow where that of the products does not
+    q, dout, k, v = inputs(dtype, d, pad)
+    lens, form = ints(LENGTHS), {"feature_map": fmap, "normalise": False}
+    _, S, z = la.forward_cross(q, k, v, lens, **form)
+    want = la.backward_cross(dout, q, k, v, S, z, lens, **form)
+    steps = [la.decode_step_cross(S, z, q[:, :, :n], **form) for n in (1, 9, 40)]
+    for bad in (INF, NAN):
+        z.fill_(bad)
+        assert all(torch.equal(a, b) for a, b in
+                   zip(la.backward_cross(dout, q, k, v, S, z, lens, **form), want))
+        assert all(torch.equal(a, la.decode_step_cross(S, z, q[:, :, :n], **form))
+                   for a, n in zip(steps, (1, 9, 40)))
+    la.check_device_status()
