@@ -632,8 +632,8 @@ size_t la_decode_step_paged_workspace_bytes(int Hq, int Hk, int T, int d,
  *              that fails).
  * A denominator of exactly 0 (a sequence without keys) gives zeros.  Values that
  * are not finite act as in the formulas, but with bf16 a result may be NaN
- * where the formula has an infinity.  No output may alias another tensor.  The parts of a sum are joined in a fixed order:
- * repeated calls are bit-identical.
+ * where the formula has an infinity.  No output may alias another tensor.  The
+ * parts of a sum are joined in a fixed order: repeated calls are bit-identical.
  */
 la_status la_forward_cross(const void *q, const void *k, const void *v, void *out,
                            float *S, float *z, const int *lengths,

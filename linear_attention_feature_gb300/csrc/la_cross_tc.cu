@@ -793,9 +793,9 @@ read_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 //
 // Two products depend on one another for each tile (psi needs the first's t), and the
 // second's sums stay in TMEM over up to 16 tiles of a state: then they are added to those
-// before in memory, by reductions that nothing waits for.  4 x 8 x 4096 x 128 (101 MB in and out):
-// 42 us, 2.4 TB/s: 7 tiles per block, each at the latency of fetch, product, psi, product
-// and store.  Two groups of computing warps 48 us (a state's sums then meet at its end);
+// before in memory, by reductions that nothing waits for.  4 x 8 x 4096 x 128 (101 MB in and
+// out): 42 us, 2.4 TB/s: 7 tiles per block, each at the latency of fetch, product, psi,
+// product and store.  Two groups of computing warps 48 us (a state's sums then meet at its end);
 // dq straight from registers 51 us.
 
 template <int DK>
